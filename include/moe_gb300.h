@@ -108,7 +108,15 @@ enum { MOE_PATH_FLAG_WEIGHTS_EARLY = 0x100 };
 enum { MOE_PATH_FLAG_K_GATED = 0x200 };
 #define MOE_PATH_K_RANGE(lo, hi) (MOE_PATH_FLAG_K_GATED | ((lo) << 16) | ((hi) << 24))
 /* Device error word bits (moe_get_device_error). */
-enum { MOE_DEVERR_BAD_EXPERT = 1u, MOE_DEVERR_TIMEOUT = 2u, MOE_DEVERR_BAD_INDEX = 4u };
+enum {
+  MOE_DEVERR_BAD_EXPERT = 1u,
+  MOE_DEVERR_TIMEOUT = 2u,
+  MOE_DEVERR_BAD_INDEX = 4u,
+  MOE_DEVERR_BAD_SCORE = 8u,   /* moe_route_scored: a logit is NaN or +inf, or a bias is NaN */
+  MOE_DEVERR_BAD_ADAPTER = 16u /* moe_lora_apply: an adapter id past the adapters */
+};
+/* Score functions of moe_route_scored. */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
 /* inv_pos value of an assignment that its expert's capacity turned away
  * (moe_permute_capped); moe_combine skips it. */
 enum { MOE_DROPPED = -2 };
@@ -465,6 +473,176 @@ moe_status_t moe_get_device_error(uint32_t* flags, int clear, moe_stream_t strea
  * context stays usable.  Asynchronous on `stream`.
  * ---------------------------------------------------------------------- */
 moe_status_t moe_selftest_wait_timeout(uint32_t budget_cycles, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * moe_router_logits -- the router logits on their own.
+ *
+ * logits[t, e] of moe_router_topk (the same fp32 sums in the same order, then
+ * the bias, then the temperature), for selections that work on logits
+ * (moe_route_scored) and for the routing gradient.
+ *
+ * x bf16 [T, H]; w_router fp32 [E, H]; logit_bias fp32 [E] or NULL;
+ * inv_temperature finite and positive; logits out: fp32 [T, E].
+ * ---------------------------------------------------------------------- */
+moe_status_t moe_router_logits(const uint16_t* x, const float* w_router, const float* logit_bias,
+                               float inv_temperature, int T, int H, int E, float* logits,
+                               moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * moe_route_scored -- expert ids and weights from router logits, with a
+ * choice of score, a balance bias and group-limited selection.
+ *
+ * Page [B], section 3.3 (a per-expert balance term that steers the selection)
+ * and page [A], section 1.1 (experts in groups).  For each token, in fp32:
+ *   score   s_e = exp(l_e - max l) / sum exp(l - max l)   (MOE_SCORE_SOFTMAX)
+ *           s_e = 1 / (1 + exp(-l_e))                     (MOE_SCORE_SIGMOID)
+ *   choice  c_e = s_e + select_bias[e]  (the bias selects, it does not weigh)
+ *   groups  with n_groups > 1, groups of E / n_groups consecutive ids have the
+ *           value of their best choice (group_top 1) or of the sum of their
+ *           two best (group_top 2); only experts of the topk_groups best
+ *           groups remain (equal values: the lower group).
+ *   ids     the k largest choices, largest first (equal: the lower id).
+ *   weights w_j = s_j / sum_i s_i over the chosen (renormalize; 0 when the sum
+ *           is 0) or s_j, times `scale`.
+ * The softmax denominator adds neighbours pairwise (experts 2i and 2i + 1,
+ * then pairs of pairs, ..., zeros past E), so the ids are reproducible.
+ *
+ * Unavailable experts: a logit of -inf or a bias of -inf takes the expert out
+ * for that token; it has score 0 and is never chosen, its group ranks by the
+ * available ones (a group without any ranks last).  When fewer than k experts
+ * are left, the remaining slots hold id -1 and weight 0 (moe_permute_masked
+ * groups such rows; a row with no expert at all combines to zeros).  A NaN or
+ * +inf logit and a NaN bias count as unavailable and set MOE_DEVERR_BAD_SCORE.
+ *
+ * logits       fp32 or bf16 [T, E], rows `ld` elements apart (ld >= E),
+ *              aligned to their type; 16-byte aligned rows of E = a power of
+ *              two from 32 up load fastest.
+ * select_bias  fp32 [E], or NULL.
+ * n_groups     1 .. 32, dividing E; 1 <= topk_groups <= n_groups; group_top 1
+ *              or 2; 1 <= k <= min(kmax, topk_groups * E / n_groups); kmax <= 16.
+ * scale        finite, positive.
+ * topk_ids     out: int32 [T, kmax]; slots j >= k hold -1.
+ * topk_w       out: fp32 [T, kmax]; slots j >= k hold 0.
+ * k_dev        out: int32 scalar k, as the later calls read it.
+ * These three are aligned to 4 bytes.
+ * ---------------------------------------------------------------------- */
+moe_status_t moe_route_scored(const void* logits, int logits_dtype, int64_t ld,
+                              const float* select_bias, int T, int E, int score, int n_groups,
+                              int topk_groups, int group_top, int k, int kmax, int renormalize,
+                              float scale, int32_t* topk_ids, float* topk_w, int32_t* k_dev,
+                              moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * moe_route_scored_backward -- gradient of the routing weights with respect
+ * to the logits, with the balance and z losses, in one pass over the logits.
+ *
+ * Page [B], sections 2.2, 3.3 and 4.1 (load-balancing loss, router z-loss).  With s, w as in
+ * moe_route_scored, q_te = s_te / sum_e s_te, n_e = expert_counts[e] (held
+ * constant) and lse_t = ln sum_e exp(l_te) over the available experts,
+ *   losses[0] = balance_coef * E / (k T) * sum_e n_e * (1/T) sum_t q_te
+ *   losses[1] = z_coef * (1/T) sum_t lse_t^2
+ *   d_logits  = d/dl [ sum_tj d_topk_w[t, j] * w[t, j] + losses[0] + losses[1] ].
+ * The ids, the bias and the counts carry no gradient.  An unavailable expert
+ * has gradient 0; a token without any adds nothing to the losses' sums.
+ *
+ * logits, logits_dtype, ld, score, k, kmax, renormalize, scale: as in the
+ *                  forward call.
+ * topk_ids         int32 [T, kmax]: the chosen ids, -1 for an empty slot,
+ *                  different ids within a token.
+ * d_topk_w         fp32 [T, kmax] (moe_combine_backward), or NULL: the losses
+ *                  alone.
+ * expert_counts    int32 [E]; may be NULL when balance_coef is 0.
+ * d_logits         out: like logits, rows ld_out apart; not the same memory.
+ * losses           out: fp32 [2].
+ * workspace        device scratch of moe_route_backward_workspace_size(E)
+ *                  bytes, aligned to 4.  Sums run in a fixed order.
+ * An id >= E is skipped and sets MOE_DEVERR_BAD_EXPERT.
+ * ---------------------------------------------------------------------- */
+size_t moe_route_backward_workspace_size(int E);
+
+moe_status_t moe_route_scored_backward(const void* logits, int logits_dtype, int64_t ld,
+                                       const int32_t* topk_ids, const float* d_topk_w,
+                                       const int32_t* expert_counts, int T, int E, int score,
+                                       int k, int kmax, int renormalize, float scale,
+                                       float balance_coef, float z_coef, void* d_logits,
+                                       int64_t ld_out, float* losses, void* workspace,
+                                       size_t workspace_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * moe_permute_masked -- moe_permute for ids with empty slots.
+ *
+ * As moe_permute (or, with capacity >= 0, moe_permute_capped; -1: no limit),
+ * except that an id of -1 in a slot j < k is an empty slot (moe_route_scored):
+ * it gets inv_pos = MOE_DROPPED and sets no error.  sorted_assign entries past
+ * offsets[E] (up to T*k) hold 0, a valid assignment.
+ * ---------------------------------------------------------------------- */
+moe_status_t moe_permute_masked(const int32_t* topk_ids, const int32_t* k_dev, int T, int kmax,
+                                int E, int capacity, int32_t* expert_counts,
+                                int32_t* expert_offsets, int32_t* sorted_assign,
+                                int32_t* inv_pos, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * moe_combine_backward -- gradient of moe_combine.
+ *
+ * Page [A], section 4.2 (the weighted sum).  For a slot j < k with
+ * row = inv_pos[t*kmax + j] >= 0:
+ *   d_topk_w[t, j] = sum_m d_out[t, m] * y[row, m]      (fp32)
+ *   d_y[row, m]    = topk_w[t, j] * d_out[t, m]         (y's type, rounded once)
+ * Dropped and unused slots have d_topk_w = 0; rows of d_y that no slot points
+ * to are left untouched.
+ *
+ * d_out bf16 [T, H]; y, d_y [T*kmax, H] of y_dtype in sorted order (d_y may be
+ * NULL: the weights' gradient alone; not y's memory); the rest as moe_combine.
+ * ---------------------------------------------------------------------- */
+moe_status_t moe_combine_backward(const uint16_t* d_out, const void* y, int y_dtype,
+                                  const int32_t* inv_pos, const float* topk_w,
+                                  const int32_t* k_dev, int T, int kmax, int H, float* d_topk_w,
+                                  void* d_y, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * moe_lora_apply -- low-rank adapters of many requests at once, beside a
+ * projection that all requests share (or each expert's).
+ *
+ * Page [B], section 4.4 (expert-level LoRA).  Row r belongs to a token with
+ * adapter a = adapter_ids[token] (negative: none) and expert e (0 when there
+ * is one projection):
+ *   z[r]   = base[r] + scales[a] * (x[row] A[a, e]^T) B[a, e]^T
+ *   RAW:    out[r] = z[r] in base's type
+ *   SWIGLU: out[r, n] = SiLU(z[r, n]) * z[r, N/2 + n]   (base fp32)
+ * Rows of tokens without an adapter get their base through unchanged.
+ * Accumulation in fp32; x A^T is kept in fp32 between the two products.
+ *
+ * Two forms:
+ *   one projection: topk_ids, sorted_assign, expert_offsets NULL, kmax = E = 1;
+ *     rows are tokens.
+ *   expert rows: sorted_assign, expert_offsets (moe_permute and its variants)
+ *     and topk_ids given; row r is sorted row r, r < expert_offsets[E]; further
+ *     rows are not touched.
+ *
+ * x             bf16; x_by_token 1: [T, K] by token; 0: [T*kmax, K] in sorted order.
+ * adapter_ids   int32 [T].
+ * lora_a        bf16 [n_adapters, E, R, K];  lora_b  bf16 [n_adapters, E, N, R].
+ * scales        fp32 [n_adapters], or NULL (all 1).
+ * base          [T*kmax, N] of base_dtype; NULL (RAW only): zeros.
+ * out           [T*kmax, N] (RAW; may be base: in place) or [T*kmax, N/2]
+ *               (SWIGLU, of out_dtype fp32 or bf16; not base's memory).
+ * workspace     moe_lora_workspace_size(...) bytes of device scratch.
+ * Limits: K % 64 == 0, N % 64 == 0, R % 8 == 0, 8 <= R <= 128 (smaller ranks
+ * are padded with zero rows of A), n_adapters * E <= 2^20.
+ * RAW needs out_dtype == base_dtype, SWIGLU base_dtype fp32 (else
+ * MOE_ERR_UNSUPPORTED).  An adapter id >= n_adapters counts as none and sets
+ * MOE_DEVERR_BAD_ADAPTER; a bad expert id or sorted entry sets
+ * MOE_DEVERR_BAD_EXPERT / _BAD_INDEX and its row gets no adapter.
+ * ---------------------------------------------------------------------- */
+size_t moe_lora_workspace_size(int T, int kmax, int E, int n_adapters, int R);
+
+moe_status_t moe_lora_apply(const uint16_t* x, int x_by_token, const int32_t* adapter_ids,
+                            const int32_t* topk_ids, const int32_t* sorted_assign,
+                            const int32_t* expert_offsets, int T, int kmax, int E,
+                            int n_adapters, int K, int N, int R, const uint16_t* lora_a,
+                            const uint16_t* lora_b, const float* scales, const void* base,
+                            int base_dtype, int epilogue, int out_dtype, void* out,
+                            void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -21,6 +21,8 @@ def path_k_range(lo: int, hi: int) -> int:
     """Flags of a k-gated launch: the product runs only if lo <= k <= hi."""
     return PATH_FLAG_K_GATED | (lo << 16) | (hi << 24)
 DEVERR_BAD_EXPERT, DEVERR_TIMEOUT, DEVERR_BAD_INDEX = 1, 2, 4
+DEVERR_BAD_SCORE, DEVERR_BAD_ADAPTER = 8, 16
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 DROPPED = -2  # inv_pos of an assignment dropped by its expert's capacity
 QMODE_AFFINE = 0
 SCALE_F16, SCALE_BF16, SCALE_F32 = 0, 1, 2
@@ -31,6 +33,9 @@ EXPORTS = (
     "moe_router_topk", "moe_router_topk_noalloc", "moe_route", "moe_route_grouped", "moe_permute", "moe_permute_capped", "moe_permute_rows", "moe_gate_up_qmm", "moe_down_qmm", "moe_combine",
     "moe_swiglu", "moe_get_device_error", "moe_selftest_wait_timeout",
     "moe_expert_counts_accumulate", "moe_expert_health",
+    "moe_router_logits", "moe_route_scored", "moe_route_scored_backward",
+    "moe_route_backward_workspace_size", "moe_permute_masked", "moe_combine_backward",
+    "moe_lora_workspace_size", "moe_lora_apply",
 )
 
 
@@ -53,6 +58,7 @@ vp = ctypes.c_void_p
 i32 = ctypes.c_int
 f32 = ctypes.c_float
 sz = ctypes.c_size_t
+i64 = ctypes.c_int64
 
 
 def _declare(lib):
@@ -87,12 +93,27 @@ def _declare(lib):
     lib.moe_selftest_wait_timeout.argtypes = [ctypes.c_uint32, vp]
     lib.moe_expert_counts_accumulate.argtypes = [vp, i32, vp, vp]
     lib.moe_expert_health.argtypes = [vp, i32, vp, vp, vp]
+    lib.moe_router_logits.argtypes = [vp, vp, vp, f32, i32, i32, i32, vp, vp]
+    lib.moe_route_scored.argtypes = [vp, i32, i64, vp, i32, i32, i32, i32, i32, i32, i32, i32, i32,
+                                     f32, vp, vp, vp, vp]
+    lib.moe_route_backward_workspace_size.argtypes = [i32]
+    lib.moe_route_backward_workspace_size.restype = sz
+    lib.moe_route_scored_backward.argtypes = [vp, i32, i64, vp, vp, vp, i32, i32, i32, i32, i32,
+                                              i32, f32, f32, f32, vp, i64, vp, vp, sz, vp]
+    lib.moe_permute_masked.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp]
+    lib.moe_combine_backward.argtypes = [vp, vp, i32, vp, vp, vp, i32, i32, i32, vp, vp, vp]
+    lib.moe_lora_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+    lib.moe_lora_workspace_size.restype = sz
+    lib.moe_lora_apply.argtypes = [vp, i32, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, vp,
+                                   vp, vp, vp, i32, i32, i32, vp, vp, sz, vp]
     for name in ("moe_pack_gate_up", "moe_router_topk", "moe_router_topk_noalloc", "moe_route",
                  "moe_route_grouped", "moe_permute_capped",
                  "moe_permute", "moe_permute_rows", "moe_gate_up_qmm",
                  "moe_down_qmm", "moe_combine", "moe_swiglu", "moe_get_device_error",
                  "moe_selftest_wait_timeout", "moe_expert_counts_accumulate",
-                 "moe_expert_health"):
+                 "moe_expert_health", "moe_router_logits", "moe_route_scored",
+                 "moe_route_scored_backward", "moe_permute_masked", "moe_combine_backward",
+                 "moe_lora_apply"):
         getattr(lib, name).restype = i32
 
 

@@ -286,3 +286,303 @@ def moe_get_device_error(clear: bool = True, stream=None) -> int:
     st = lib().moe_get_device_error(ctypes.byref(v), int(clear), _stream(stream))
     check("moe_get_device_error", st)
     return int(v.value)
+
+
+# ---- score routing, its gradient, adapters ----------------------------------
+
+
+def _raw(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _cur(stream, dev) -> int:
+    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    return s.cuda_stream
+
+
+def _hold(stream, *tensors):
+    """Tell the allocator that ``stream`` uses these tensors, so that none of
+    their memory is handed out again before the enqueued work has run."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _rows2d(t: torch.Tensor, name: str) -> int:
+    """Row stride of a 2D CUDA tensor of fp32 or bf16 with dense rows."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _DT:
+        raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    T, E = t.shape
+    if E > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    ld = t.stride(0) if T > 1 else E
+    if ld < E:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return ld
+
+
+def _like(t: torch.Tensor, shape, dtype, dev, name: str):
+    _need(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+
+
+def moe_router_logits(x, w_router, logit_bias=None, inv_temperature: float = 1.0, logits=None,
+                      stream=None):
+    """-> logits fp32 [T, E], in the summation order of moe_router_topk."""
+    _need(x, torch.bfloat16, "x")
+    _need(w_router, torch.float32, "w_router")
+    T, H = x.shape
+    E = w_router.shape[0]
+    if w_router.shape[1] != H:
+        raise ValueError("w_router and x differ in their hidden size")
+    if logit_bias is not None:
+        _like(logit_bias, (E,), torch.float32, x.device, "logit_bias")
+    if logits is None:
+        logits = torch.empty((T, E), dtype=torch.float32, device=x.device)
+    else:
+        _like(logits, (T, E), torch.float32, x.device, "logits")
+    _hold(stream, x, w_router, logit_bias, logits)
+    check("moe_router_logits",
+          lib().moe_router_logits(_raw(x), _raw(w_router), _raw(logit_bias), inv_temperature, T, H,
+                                  E, _raw(logits), _cur(stream, x.device)))
+    return logits
+
+
+def moe_route_scored(logits, k: int, score: int = _lib.SCORE_SOFTMAX, select_bias=None,
+                     n_groups: int = 1, topk_groups: int = 1, group_top: int = 2,
+                     renormalize: bool = True, scale: float = 1.0, kmax: Optional[int] = None,
+                     topk_ids=None, topk_w=None, k_dev=None, stream=None):
+    """-> (topk_ids int32 [T, kmax], topk_w f32 [T, kmax], k_dev int32 [1]).
+
+    Scores (softmax or sigmoid) of fp32 or bf16 logits [T, E] (rows may be
+    strided); ``select_bias`` steers the selection only; with ``n_groups`` > 1
+    the experts of the ``topk_groups`` best groups compete.  Slots without an
+    available expert hold id -1 and weight 0."""
+    ld = _rows2d(logits, "logits")
+    T, E = logits.shape
+    if kmax is None:
+        kmax = k
+    dev = logits.device
+    if select_bias is not None:
+        _like(select_bias, (E,), torch.float32, dev, "select_bias")
+    if topk_ids is None:
+        topk_ids = torch.empty((T, kmax), dtype=torch.int32, device=dev)
+    else:
+        _like(topk_ids, (T, kmax), torch.int32, dev, "topk_ids")
+    if topk_w is None:
+        topk_w = torch.empty((T, kmax), dtype=torch.float32, device=dev)
+    else:
+        _like(topk_w, (T, kmax), torch.float32, dev, "topk_w")
+    if k_dev is None:
+        k_dev = torch.empty(1, dtype=torch.int32, device=dev)
+    else:
+        _like(k_dev, (1,), torch.int32, dev, "k_dev")
+    _hold(stream, logits, select_bias, topk_ids, topk_w, k_dev)
+    st = lib().moe_route_scored(_raw(logits), _DT[logits.dtype], ld, _raw(select_bias), T, E, score,
+                                n_groups, topk_groups, group_top, k, kmax, bool(renormalize),
+                                scale, _raw(topk_ids), _raw(topk_w), _raw(k_dev),
+                                _cur(stream, dev))
+    check("moe_route_scored", st)
+    return topk_ids, topk_w, k_dev
+
+
+def moe_route_backward_workspace_size(E: int) -> int:
+    return int(lib().moe_route_backward_workspace_size(E))
+
+
+def moe_route_scored_backward(logits, topk_ids, d_topk_w=None, expert_counts=None,
+                              score: int = _lib.SCORE_SOFTMAX, k: Optional[int] = None,
+                              renormalize: bool = True, scale: float = 1.0,
+                              balance_coef: float = 0.0, z_coef: float = 0.0, d_logits=None,
+                              losses=None, workspace=None, stream=None):
+    """-> (d_logits like logits, losses f32 [2]: the balance and the z loss).
+
+    Gradient of sum(d_topk_w * topk_w) + balance + z with respect to the
+    logits of moe_route_scored (same score, renormalize and scale)."""
+    ld = _rows2d(logits, "logits")
+    T, E = logits.shape
+    dev = logits.device
+    _need(topk_ids, torch.int32, "topk_ids")
+    if topk_ids.dim() != 2 or topk_ids.shape[0] != T:
+        raise ValueError("topk_ids must be [T, kmax]")
+    kmax = topk_ids.shape[1]
+    if k is None:
+        k = kmax
+    if d_topk_w is not None:
+        _like(d_topk_w, (T, kmax), torch.float32, dev, "d_topk_w")
+    if expert_counts is not None:
+        _like(expert_counts, (E,), torch.int32, dev, "expert_counts")
+    if d_logits is None:
+        d_logits = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    elif d_logits.dtype != logits.dtype or d_logits.shape != logits.shape:
+        raise ValueError("d_logits must have the type and shape of logits")
+    ld_out = _rows2d(d_logits, "d_logits")
+    if losses is None:
+        losses = torch.empty(2, dtype=torch.float32, device=dev)
+    else:
+        _like(losses, (2,), torch.float32, dev, "losses")
+    if workspace is None:
+        workspace = torch.empty(moe_route_backward_workspace_size(E), dtype=torch.uint8, device=dev)
+    _hold(stream, logits, topk_ids, d_topk_w, expert_counts, d_logits, losses, workspace)
+    st = lib().moe_route_scored_backward(
+        _raw(logits), _DT[logits.dtype], ld, _raw(topk_ids), _raw(d_topk_w), _raw(expert_counts),
+        T, E, score, k, kmax, bool(renormalize), scale, balance_coef, z_coef, _raw(d_logits),
+        ld_out, _raw(losses), _raw(workspace), workspace.numel(), _cur(stream, dev))
+    check("moe_route_scored_backward", st)
+    return d_logits, losses
+
+
+def moe_permute_masked(topk_ids, k_dev, E: int, capacity: Optional[int] = None,
+                       expert_counts=None, expert_offsets=None, sorted_assign=None, inv_pos=None,
+                       stream=None):
+    """moe_permute (with an optional capacity) for ids with empty slots (-1):
+    -> (expert_counts, expert_offsets, sorted_assign, inv_pos)."""
+    _need(topk_ids, torch.int32, "topk_ids")
+    T, kmax = topk_ids.shape
+    dev = topk_ids.device
+    if expert_counts is None:
+        expert_counts = torch.empty(E, dtype=torch.int32, device=dev)
+    if expert_offsets is None:
+        expert_offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    if sorted_assign is None:
+        sorted_assign = torch.empty(max(T * kmax, 1), dtype=torch.int32, device=dev)
+    if inv_pos is None:
+        inv_pos = torch.empty(max(T * kmax, 1), dtype=torch.int32, device=dev)
+    _hold(stream, topk_ids, k_dev, expert_counts, expert_offsets, sorted_assign, inv_pos)
+    check("moe_permute_masked",
+          lib().moe_permute_masked(_raw(topk_ids), _raw(k_dev), T, kmax, E,
+                                   -1 if capacity is None else int(capacity), _raw(expert_counts),
+                                   _raw(expert_offsets), _raw(sorted_assign), _raw(inv_pos),
+                                   _cur(stream, dev)))
+    return expert_counts, expert_offsets, sorted_assign, inv_pos
+
+
+def moe_combine_backward(d_out, y, inv_pos, topk_w, k_dev, d_topk_w=None, d_y=None,
+                         need_d_y: bool = True, stream=None):
+    """Gradient of moe_combine -> (d_topk_w f32 [T, kmax], d_y like y).
+
+    Rows of ``d_y`` that no kept slot points to keep what they held (zeros
+    when the buffer is allocated here).  need_d_y=False computes d_topk_w
+    alone (d_y is None)."""
+    _need(d_out, torch.bfloat16, "d_out")
+    if y.dtype not in _DT:
+        raise ValueError(f"y must be float32 or bfloat16, got {y.dtype}")
+    _need(y, y.dtype, "y")
+    T, H = d_out.shape
+    dev = d_out.device
+    if topk_w.dim() != 2:
+        raise ValueError("topk_w must be [T, kmax]")
+    kmax = topk_w.shape[1]
+    _like(topk_w, (T, kmax), torch.float32, dev, "topk_w")
+    _need(inv_pos, torch.int32, "inv_pos")
+    if inv_pos.numel() < T * kmax or y.dim() != 2 or y.shape[1] != H or y.shape[0] < T * kmax:
+        raise ValueError("y must be [T*kmax, H] and inv_pos [T*kmax]")
+    _like(k_dev, (1,), torch.int32, dev, "k_dev")
+    if d_topk_w is None:
+        d_topk_w = torch.empty((T, kmax), dtype=torch.float32, device=dev)
+    else:
+        _like(d_topk_w, (T, kmax), torch.float32, dev, "d_topk_w")
+    if d_y is not None:
+        _like(d_y, y.shape, y.dtype, dev, "d_y")
+    elif need_d_y:
+        d_y = torch.zeros_like(y)
+    _hold(stream, d_out, y, inv_pos, topk_w, k_dev, d_topk_w, d_y)
+    check("moe_combine_backward",
+          lib().moe_combine_backward(_raw(d_out), _raw(y), _DT[y.dtype], _raw(inv_pos),
+                                     _raw(topk_w), _raw(k_dev), T, kmax, H, _raw(d_topk_w),
+                                     _raw(d_y), _cur(stream, dev)))
+    return d_topk_w, d_y
+
+
+def moe_lora_workspace_size(T: int, kmax: int, E: int, n_adapters: int, R: int) -> int:
+    return int(lib().moe_lora_workspace_size(T, kmax, E, n_adapters, R))
+
+
+def moe_lora_apply(x, adapter_ids, lora_a, lora_b, scales=None, base=None, out=None,
+                   epilogue: int = EPILOGUE_RAW, out_dtype=None, topk_ids=None,
+                   sorted_assign=None, expert_offsets=None, k_dev=None, x_by_token: bool = True,
+                   workspace=None, stream=None):
+    """Adapters of many requests: out = base + scale (x A^T) B^T row by row.
+
+    adapter_ids int32 [T] (negative: no adapter).  lora_a bf16 [n, R, K] or
+    [n, E, R, K], lora_b bf16 [n, N, R] or [n, E, N, R].  With topk_ids,
+    sorted_assign and expert_offsets the rows are expert rows in sorted order;
+    x is by token, or (x_by_token False) in sorted order too.  ``out`` may be
+    ``base`` (RAW); base None stands for zeros (out_dtype then says the type).
+    EPILOGUE_SWIGLU takes an fp32 base [rows, N] and gives [rows, N/2], bf16
+    unless out_dtype says fp32.  k_dev is accepted beside the other routing
+    results and not needed (expert_offsets holds the row count)."""
+    _need(x, torch.bfloat16, "x")
+    _need(lora_a, torch.bfloat16, "lora_a")
+    _need(lora_b, torch.bfloat16, "lora_b")
+    dev = x.device
+    if lora_a.dim() == 3:
+        n, R, K = lora_a.shape
+        E = 1
+    elif lora_a.dim() == 4:
+        n, E, R, K = lora_a.shape
+    else:
+        raise ValueError("lora_a must be [n, R, K] or [n, E, R, K]")
+    N = lora_b.shape[-2]
+    if tuple(lora_b.shape) != ((n, N, R) if lora_a.dim() == 3 else (n, E, N, R)):
+        raise ValueError("lora_b does not match lora_a")
+    if x.dim() != 2 or x.shape[1] != K:
+        raise ValueError(f"x must be [rows, {K}]")
+    T = adapter_ids.shape[0]
+    _like(adapter_ids, (T,), torch.int32, dev, "adapter_ids")
+    kmax = 1
+    if sorted_assign is not None:
+        if topk_ids is None or expert_offsets is None:
+            raise ValueError("expert rows need topk_ids, sorted_assign and expert_offsets")
+        kmax = topk_ids.shape[1]
+        _like(topk_ids, (T, kmax), torch.int32, dev, "topk_ids")
+        _like(expert_offsets, (E + 1,), torch.int32, dev, "expert_offsets")
+        _need(sorted_assign, torch.int32, "sorted_assign")
+        if sorted_assign.numel() < T * kmax:
+            raise ValueError("sorted_assign must hold T*kmax entries")
+    elif topk_ids is not None or expert_offsets is not None:
+        raise ValueError("expert rows need topk_ids, sorted_assign and expert_offsets")
+    rows = T * kmax
+    if x.shape[0] < (T if x_by_token else rows):
+        raise ValueError("x has too few rows")
+    if scales is not None:
+        _like(scales, (n,), torch.float32, dev, "scales")
+    swiglu = epilogue == EPILOGUE_SWIGLU
+    cols = N // 2 if swiglu else N
+    if base is not None:
+        if base.dtype not in _DT:
+            raise ValueError(f"base must be float32 or bfloat16, got {base.dtype}")
+        _need(base, base.dtype, "base")
+        if base.dim() != 2 or base.shape[0] < rows or base.shape[1] != N:
+            raise ValueError(f"base must be [{rows}, {N}]")
+    if out is not None:
+        if out.dtype not in _DT:
+            raise ValueError(f"out must be float32 or bfloat16, got {out.dtype}")
+        _need(out, out.dtype, "out")
+        if out.dim() != 2 or out.shape[0] < rows or out.shape[1] != cols:
+            raise ValueError(f"out must be [{rows}, {cols}]")
+    else:
+        if out_dtype is None:
+            out_dtype = torch.bfloat16 if swiglu or base is None else base.dtype
+        out = torch.empty((rows, cols), dtype=out_dtype, device=dev)
+    base_dt = _DT[out.dtype] if base is None else _DT[base.dtype]
+    need = moe_lora_workspace_size(T, kmax, E, n, R)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _hold(stream, x, adapter_ids, lora_a, lora_b, scales, base, out, topk_ids, sorted_assign,
+          expert_offsets, workspace)
+    st = lib().moe_lora_apply(_raw(x), int(x_by_token), _raw(adapter_ids), _raw(topk_ids),
+                              _raw(sorted_assign), _raw(expert_offsets), T, kmax, E, n, K, N, R,
+                              _raw(lora_a), _raw(lora_b), _raw(scales), _raw(base), base_dt,
+                              epilogue, _DT[out.dtype], _raw(out), _raw(workspace),
+                              workspace.numel(), _cur(stream, dev))
+    check("moe_lora_apply", st)
+    return out

@@ -34,6 +34,7 @@ struct PermuteParams {
   int32_t* sorted;
   int32_t* inv_pos;
   int capacity;  // most assignments an expert keeps (INT32_MAX: no limit)
+  int empty_ok;  // an id of -1 is an empty slot (inv_pos = MOE_DROPPED), not an error
   unsigned int* err;
 };
 
@@ -64,7 +65,7 @@ __global__ void __launch_bounds__(kPermuteThreads) permute_kernel(PermuteParams 
     if (a >= slots || a % p.kmax >= k) return -1;
     const int v = __ldg(p.ids + a);
     if (v >= 0 && v < E) return v;
-    if (report) raise_device_error(p.err, MOE_DEVERR_BAD_EXPERT);
+    if (report && !(p.empty_ok && v == -1)) raise_device_error(p.err, MOE_DEVERR_BAD_EXPERT);
     return -1;
   };
 
@@ -136,7 +137,8 @@ __global__ void __launch_bounds__(kPermuteThreads) permute_kernel(PermuteParams 
   for (int base = lo; base < hi; base += kPermuteThreads) {
     const int a = base + tid;
     const int e = a < hi ? expert_of(a, false) : -1;
-    if (a < hi && e < 0) p.inv_pos[a] = -1;
+    if (a < hi && e < 0)
+      p.inv_pos[a] = p.empty_ok && a % p.kmax < k && __ldg(p.ids + a) == -1 ? MOE_DROPPED : -1;
     const unsigned peers = __match_any_sync(0xFFFFFFFFu, e);
     const int rank_in_warp = __popc(peers & lanemask_lt());
     const bool leader = (peers & lanemask_lt()) == 0u;
@@ -170,9 +172,9 @@ __global__ void __launch_bounds__(kPermuteThreads) permute_kernel(PermuteParams 
     }
     __syncthreads();
   }
-  // with a capacity, sorted rows past the kept total hold assignment 0 (a
-  // valid one), so consumers of T*k sorted rows stay in bounds
-  if (p.capacity != INT32_MAX && blockIdx.x == 0) {
+  // with a capacity or empty slots, sorted rows past the kept total hold
+  // assignment 0 (a valid one), so consumers of T*k sorted rows stay in bounds
+  if ((p.capacity != INT32_MAX || p.empty_ok) && blockIdx.x == 0) {
     int kept = 0;
     for (int x = 0; x < E; ++x) kept += min(cnt[x], p.capacity);
     for (int i = kept + tid; i < p.T * k; i += kPermuteThreads) p.sorted[i] = 0;
@@ -187,8 +189,9 @@ using namespace moe;
 namespace {
 
 moe_status_t permute_impl(const int32_t* topk_ids, const int32_t* k_dev, int T, int kmax, int E,
-                          int capacity, int32_t* expert_counts, int32_t* expert_offsets,
-                          int32_t* sorted_assign, int32_t* inv_pos, moe_stream_t stream) {
+                          int capacity, bool empty_ok, int32_t* expert_counts,
+                          int32_t* expert_offsets, int32_t* sorted_assign, int32_t* inv_pos,
+                          moe_stream_t stream) {
   using namespace moe_host;
   if (T < 0 || E < 1 || E > 1024 || kmax < 1 || kmax > 16) return MOE_ERR_INVALID_ARG;
   if ((int64_t)T * kmax > (1 << 24)) return MOE_ERR_INVALID_ARG;
@@ -205,6 +208,7 @@ moe_status_t permute_impl(const int32_t* topk_ids, const int32_t* k_dev, int T, 
   p.sorted = sorted_assign;
   p.inv_pos = inv_pos;
   p.capacity = capacity;
+  p.empty_ok = empty_ok;
   p.err = device_error_word();
   size_t smem = (size_t)(4 + kPermuteWarps) * E * sizeof(int);
   if (smem > 48 * 1024) {
@@ -229,8 +233,18 @@ extern "C" moe_status_t moe_permute(const int32_t* topk_ids, const int32_t* k_de
                                     int kmax, int E, int32_t* expert_counts,
                                     int32_t* expert_offsets, int32_t* sorted_assign,
                                     int32_t* inv_pos, moe_stream_t stream) {
-  return permute_impl(topk_ids, k_dev, T, kmax, E, INT32_MAX, expert_counts, expert_offsets,
-                      sorted_assign, inv_pos, stream);
+  return permute_impl(topk_ids, k_dev, T, kmax, E, INT32_MAX, false, expert_counts,
+                      expert_offsets, sorted_assign, inv_pos, stream);
+}
+
+extern "C" moe_status_t moe_permute_masked(const int32_t* topk_ids, const int32_t* k_dev, int T,
+                                           int kmax, int E, int capacity,
+                                           int32_t* expert_counts, int32_t* expert_offsets,
+                                           int32_t* sorted_assign, int32_t* inv_pos,
+                                           moe_stream_t stream) {
+  if (capacity < -1) return MOE_ERR_INVALID_ARG;
+  return permute_impl(topk_ids, k_dev, T, kmax, E, capacity < 0 ? INT32_MAX : capacity, true,
+                      expert_counts, expert_offsets, sorted_assign, inv_pos, stream);
 }
 
 extern "C" moe_status_t moe_permute_capped(const int32_t* topk_ids, const int32_t* k_dev, int T,
@@ -239,8 +253,8 @@ extern "C" moe_status_t moe_permute_capped(const int32_t* topk_ids, const int32_
                                            int32_t* sorted_assign, int32_t* inv_pos,
                                            moe_stream_t stream) {
   if (capacity < 0) return MOE_ERR_INVALID_ARG;
-  return permute_impl(topk_ids, k_dev, T, kmax, E, capacity, expert_counts, expert_offsets,
-                      sorted_assign, inv_pos, stream);
+  return permute_impl(topk_ids, k_dev, T, kmax, E, capacity, false, expert_counts,
+                      expert_offsets, sorted_assign, inv_pos, stream);
 }
 
 // ---- token rows in expert order ------------------------------------------

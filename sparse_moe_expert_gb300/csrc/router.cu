@@ -1339,3 +1339,72 @@ extern "C" moe_status_t moe_router_topk_noalloc(const uint16_t* x, const float* 
 
   return launch_router(p, st);
 }
+
+// ---- logits alone (for selections other than the kernels' own) --------------
+
+namespace moe {
+namespace {
+
+// Logits of a token group x an expert slice: phase A without a cluster (the
+// CTA is its own leader), then coalesced stores.  The same sums in the same
+// order as the routing kernels.
+__global__ void __launch_bounds__(kRouterThreads)
+    router_logits_kernel(RouterParams p, int slices, float* __restrict__ out) {
+  extern __shared__ __align__(16) float logits_s[];  // [tpc][E]
+  pdl_wait();
+  pdl_trigger();
+  const int t0 = blockIdx.x * p.tpc, nt = min(p.tpc, p.T - t0);
+  const int e_lo = (int)((int64_t)blockIdx.y * p.E / slices);
+  const int ne = (int)((int64_t)(blockIdx.y + 1) * p.E / slices) - e_lo;
+  if (ne <= 0) return;
+  const uint32_t lead = cluster_map(logits_s, 0);
+  if (nt >= 8 && ((nt + 7) / 8) * ((ne + 3) / 4) >= 4)
+    router_logit_tiles<8, 4, false>(p, t0, nt, e_lo, ne, lead, nullptr, nullptr);
+  else if (nt >= 8)
+    router_logit_tiles<8, 1, false>(p, t0, nt, e_lo, ne, lead, nullptr, nullptr);
+  else
+    router_logit_tiles<1, 1, false>(p, t0, nt, e_lo, ne, lead, nullptr, nullptr);
+  __syncthreads();
+  for (int i = threadIdx.x; i < nt * ne; i += kRouterThreads) {
+    const int tl = i / ne, e = e_lo + i % ne;
+    out[(int64_t)(t0 + tl) * p.E + e] = logits_s[tl * p.E + e];
+  }
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" moe_status_t moe_router_logits(const uint16_t* x, const float* w_router,
+                                          const float* logit_bias, float inv_temperature, int T,
+                                          int H, int E, float* logits, moe_stream_t stream) {
+  using namespace moe_host;
+  if (T < 0 || H <= 0 || H % 64 != 0 || E < 1 || E > moe::kMaxExperts) return MOE_ERR_INVALID_ARG;
+  if (!(inv_temperature > 0.0f) || isinf(inv_temperature)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (T > (1 << 24)) return MOE_ERR_INVALID_ARG;
+  const void* ptrs[] = {x, w_router, logits};
+  for (const void* q : ptrs)
+    if (!q || !aligned16(q)) return MOE_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(logit_bias) & 3u) return MOE_ERR_INVALID_ARG;
+  moe::RouterParams p = {};
+  p.x = x;
+  p.w = w_router;
+  p.bias = logit_bias;
+  p.inv_temp = inv_temperature;
+  p.T = T;
+  p.H = H;
+  p.E = E;
+  p.tpc = moe::router_group_tokens(E);
+  const int groups = (T + p.tpc - 1) / p.tpc;
+  // enough expert slices for every SM to have a CTA; at least 16 experts each
+  int slices = (sm_count() + groups - 1) / groups;
+  const int most = (E + moe::kRouterWarps - 1) / moe::kRouterWarps;
+  if (slices > most) slices = most;
+  const size_t smem = (size_t)p.tpc * E * sizeof(float);
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(moe::router_logits_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)smem) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  return launch(moe::router_logits_kernel, dim3(groups, slices), moe::kRouterThreads, smem,
+                reinterpret_cast<cudaStream_t>(stream), p, slices, logits);
+}

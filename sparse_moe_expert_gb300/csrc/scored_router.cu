@@ -1,0 +1,674 @@
+// Routing by scores: from router logits to expert ids and weights, and the
+// gradient back to the logits together with the balance and z losses.
+//
+// Page "Qwen3.5-MoE与Qwen3-MoE架构差异深度解析", section 3.3 (a per-expert
+// balance term added before the selection; the load-balancing loss), sections 2.2
+// and 4.1 (load balancing, router z-loss); page "Qwen3.5 Block在llama.cpp中的映射与优化原理",
+// section 1.1 (experts in groups).
+//
+// One warp per token.  Lane i holds the V = P / 32 consecutive experts
+// [i V, i V + V), P = E rounded up to a power of two (at least 32), so that
+//  - a lane's logits are one contiguous piece of the row (16 bytes for 256
+//    bf16 logits),
+//  - the pairwise sum over neighbours (the order the header fixes for the
+//    softmax denominator) is V - 1 adds in the lane and five xor shuffles,
+//  - equal values resolve to the lower expert id by taking the lowest lane.
+#include <math.h>
+
+#include "common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kScoredThreads = 256;
+constexpr int kScoredWarps = kScoredThreads / 32;
+constexpr unsigned kFull = 0xFFFFFFFFu;
+constexpr int kMaxGroups = 32;
+
+struct ScoredParams {
+  const void* logits;  // fp32 or bf16 [T, E], rows `ld` elements apart
+  int64_t ld;
+  const float* bias;  // [E] or null: added for the selection only
+  int T, E, k, kmax;
+  int n_groups, topk_groups, group_top;
+  int renorm;
+  float scale;
+  int32_t* ids;
+  float* w;
+  int32_t* k_dev;
+  unsigned int* err;
+};
+
+// Order-preserving map of fp32 values onto uint32; 0 stands for "unavailable"
+// and is below the key of every value above -inf.
+__device__ __forceinline__ uint32_t choice_key(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+template <bool BF16>
+__device__ __forceinline__ float load_logit(const void* row, int e) {
+  if constexpr (BF16) return bf16_bits_to_f32(__ldg(static_cast<const uint16_t*>(row) + e));
+  return __ldg(static_cast<const float*>(row) + e);
+}
+
+// The lane's V logits of one row: 16-byte (or narrower whole-lane) loads when
+// `vec` says that every lane's piece is aligned and inside the row, else one
+// load per expert.  Experts past E read as -inf.
+template <int V, bool BF16>
+__device__ __forceinline__ void load_logits(float (&l)[V], const void* row, int e0, int E,
+                                            bool vec) {
+  if constexpr (BF16) {
+    if (vec && V >= 2) {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(row) + e0);
+      if constexpr (V >= 8) {
+#pragma unroll
+        for (int i = 0; i < V / 8; ++i) {
+          const uint4 q = ldg_nc_v4(p + 4 * i);
+          const uint32_t w4[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = bf16x2_to_f32x2(w4[j]);
+            l[8 * i + 2 * j] = f.x;
+            l[8 * i + 2 * j + 1] = f.y;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) {
+          const float2 f = bf16x2_to_f32x2(__ldg(p + j));
+          l[2 * j] = f.x;
+          l[2 * j + 1] = f.y;
+        }
+      }
+      return;
+    }
+  } else {
+    if (vec && V >= 4) {
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(row) + e0);
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) {
+        const float4 q = __ldg(p + i);
+        l[4 * i] = q.x;
+        l[4 * i + 1] = q.y;
+        l[4 * i + 2] = q.z;
+        l[4 * i + 3] = q.w;
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    l[v] = e0 + v < E ? load_logit<BF16>(row, e0 + v) : -INFINITY;
+}
+
+__device__ __forceinline__ float sigmoid_f32(float l) {
+  return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-l)));
+}
+
+// Pairwise sum over neighbouring experts, the same bits in every lane.
+template <int V>
+__device__ __forceinline__ float neighbour_sum(const float (&x)[V]) {
+  float t[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) t[v] = x[v];
+#pragma unroll
+  for (int n = V; n > 1; n >>= 1)
+#pragma unroll
+    for (int v = 0; v < n / 2; ++v) t[v] = __fadd_rn(t[2 * v], t[2 * v + 1]);
+  float s = t[0];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) s = __fadd_rn(s, __shfl_xor_sync(kFull, s, o));
+  return s;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  return v;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+// The two largest of two pairs (a1 >= a2, b1 >= b2).
+__device__ __forceinline__ void merge_top2(float& a1, float& a2, float b1, float b2) {
+  const float lo = fminf(a1, b1);
+  a1 = fmaxf(a1, b1);
+  a2 = fmaxf(lo, fmaxf(a2, b2));
+}
+
+// Strikes the choices outside the best `topk_groups` groups (key = 0).  A
+// group's value is its best choice, or the sum of its two best (of the only
+// one, if it has one); a group without any available expert is never ahead of
+// one that has; equal values go to the lower group.
+template <int V>
+__device__ __forceinline__ void limit_groups(const ScoredParams& p, const float (&c)[V],
+                                             uint32_t (&key)[V], int e0) {
+  const int lane = threadIdx.x & 31;
+  const int G = p.n_groups, gsz = p.E / G;
+  uint32_t mine = 0u;  // lane g: key of group g's value
+  const int span = gsz / V;  // lanes of a group when groups are whole aligned lane runs
+  const bool aligned = gsz % V == 0 && (span & (span - 1)) == 0 && span <= 32;
+  if (aligned) {
+    float a1 = -INFINITY, a2 = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < V; ++v) merge_top2(a1, a2, key[v] ? c[v] : -INFINITY, -INFINITY);
+    for (int o = 1; o < span; o <<= 1) {
+      const float b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
+      merge_top2(a1, a2, b1, b2);
+    }
+    const float val = p.group_top == 2 && a2 > -INFINITY ? __fadd_rn(a1, a2) : a1;
+    const uint32_t kv = a1 > -INFINITY ? choice_key(val) : 0u;
+    mine = __shfl_sync(kFull, kv, lane < G ? lane * span : 0);
+  } else {
+    for (int g = 0; g < G; ++g) {
+      float a1 = -INFINITY, a2 = -INFINITY;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int e = e0 + v;
+        if (key[v] && e >= g * gsz && e < (g + 1) * gsz) merge_top2(a1, a2, c[v], -INFINITY);
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
+        merge_top2(a1, a2, b1, b2);
+      }
+      const float val = p.group_top == 2 && a2 > -INFINITY ? __fadd_rn(a1, a2) : a1;
+      if (lane == g) mine = a1 > -INFINITY ? choice_key(val) : 0u;
+    }
+  }
+  int rank = 0;
+  for (int g = 0; g < G; ++g) {
+    const uint32_t o = __shfl_sync(kFull, mine, g);
+    rank += o > mine || (o == mine && g < lane);
+  }
+  const unsigned chosen = __ballot_sync(kFull, lane < G && rank < p.topk_groups);
+  if (aligned) {
+    const int g = e0 / gsz;
+    if (g >= G || !((chosen >> g) & 1u)) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) key[v] = 0u;
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int g = (e0 + v) / gsz;
+      if (g >= G || !((chosen >> g) & 1u)) key[v] = 0u;
+    }
+  }
+}
+
+template <int V, bool BF16, bool SIGMOID>
+__global__ void __launch_bounds__(kScoredThreads) route_scored_kernel(ScoredParams p, int vec) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const int e0 = lane * V;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.k_dev = p.k;
+  float b[V];
+  bool bad_bias = false;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    b[v] = p.bias && e0 + v < p.E ? __ldg(p.bias + e0 + v) : 0.0f;
+    bad_bias |= b[v] != b[v];
+  }
+  bool bad = bad_bias;
+  for (int64_t t = (int64_t)blockIdx.x * kScoredWarps + (threadIdx.x >> 5); t < p.T;
+       t += (int64_t)gridDim.x * kScoredWarps) {
+    float s[V], c[V];
+    uint32_t key[V];
+    {
+      float l[V];
+      const char* row = static_cast<const char*>(p.logits) + t * p.ld * (BF16 ? 2 : 4);
+      load_logits<V, BF16>(l, row, e0, p.E, vec != 0);
+      // available: a finite logit; NaN and +inf are reported
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        bad |= !(l[v] < INFINITY);
+        key[v] = fabsf(l[v]) < INFINITY ? 1u : 0u;
+      }
+      if constexpr (SIGMOID) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[v] = key[v] ? sigmoid_f32(l[v]) : 0.0f;
+      } else {
+        float m = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < V; ++v) m = key[v] ? fmaxf(m, l[v]) : m;
+        m = warp_max(m);
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[v] = key[v] ? expf(__fsub_rn(l[v], m)) : 0.0f;
+        const float den = neighbour_sum(s);
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[v] = key[v] ? __fdiv_rn(s[v], den) : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      c[v] = p.bias ? __fadd_rn(s[v], b[v]) : s[v];
+      key[v] = key[v] && c[v] > -INFINITY ? choice_key(c[v]) : 0u;
+    }
+    if (p.n_groups > 1) limit_groups<V>(p, c, key, e0);
+
+    // k rounds of a warp argmax over the lanes' best remaining choices
+    int my_id = -1;
+    float my_s = 0.0f;
+    for (int r = 0; r < p.k; ++r) {
+      uint32_t bk = 0u;
+      int bv = 0;
+      float bs = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (key[v] > bk) {
+          bk = key[v];
+          bv = v;
+          bs = s[v];
+        }
+      const uint32_t top = __reduce_max_sync(kFull, bk);
+      if (top == 0u) break;  // no expert left: the remaining slots stay empty
+      const int win = __ffs(__ballot_sync(kFull, bk == top)) - 1;
+      const int id = __shfl_sync(kFull, e0 + bv, win);
+      const float sv = __shfl_sync(kFull, bs, win);
+      if (lane == r) {
+        my_id = id;
+        my_s = sv;
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (e0 + v == id) key[v] = 0u;
+    }
+    float w = my_s;
+    if (p.renorm) {
+      const float tot = warp_sum(my_s);
+      w = tot > 0.0f ? __fdiv_rn(my_s, tot) : 0.0f;
+    }
+    if (lane < p.kmax) {
+      p.ids[t * p.kmax + lane] = my_id;
+      p.w[t * p.kmax + lane] = __fmul_rn(w, p.scale);
+    }
+  }
+  if (bad) raise_device_error(p.err, MOE_DEVERR_BAD_SCORE);
+}
+
+// ---- gradient and losses ---------------------------------------------------
+
+struct ScoredGradParams {
+  const void* logits;
+  int64_t ld;
+  const int32_t* ids;     // [T, kmax]
+  const float* d_w;       // [T, kmax] or null (the losses' gradient only)
+  const int32_t* counts;  // [E] or null (no balance loss)
+  int T, E, k, kmax;
+  int renorm;
+  float scale, balance, z;
+  void* d_logits;  // like logits, rows ld_out elements apart
+  int64_t ld_out;
+  float* part;  // [grid][E + 1]: sums over the block's tokens of q_e and of lse^2
+  unsigned int* err;
+};
+
+template <int V, bool BF16, bool SIGMOID>
+__global__ void __launch_bounds__(kScoredThreads) route_scored_backward_kernel(ScoredGradParams p,
+                                                                               int vec) {
+  constexpr int P = 32 * V;
+  __shared__ __align__(16) float scatter[kScoredWarps][P];
+  __shared__ float lse_part[kScoredWarps];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int e0 = lane * V;
+  float* buf = scatter[warp];
+  float coef[V], qsum[V];  // d balance / d q_te, and the running sum of q_te
+  // coef = balance * E / (k T) * counts / T
+  const float unit = p.counts ? p.balance * ((float)p.E / ((float)p.k * (float)p.T)) / (float)p.T : 0.0f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    coef[v] = p.counts && e0 + v < p.E ? unit * (float)__ldg(p.counts + e0 + v) : 0.0f;
+    qsum[v] = 0.0f;
+    buf[e0 + v] = 0.0f;
+  }
+  float lse2 = 0.0f;
+  bool bad = false;
+  __syncwarp();
+  for (int64_t t = (int64_t)blockIdx.x * kScoredWarps + warp; t < p.T;
+       t += (int64_t)gridDim.x * kScoredWarps) {
+    float l[V], s[V];
+    const char* row = static_cast<const char*>(p.logits) + t * p.ld * (BF16 ? 2 : 4);
+    load_logits<V, BF16>(l, row, e0, p.E, vec != 0);
+    int id = -1;
+    float dw = 0.0f;
+    if (p.d_w && lane < p.kmax && lane < p.k) {
+      id = __ldg(p.ids + t * p.kmax + lane);
+      dw = __ldg(p.d_w + t * p.kmax + lane);
+      if (id >= p.E) {
+        bad = true;
+        id = -1;
+      }
+    }
+    bool on[V];
+    float m = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      on[v] = fabsf(l[v]) < INFINITY;
+      if (on[v]) m = fmaxf(m, l[v]);
+    }
+    // softmax terms: the scores themselves, or (sigmoid) only for the z loss
+    float esum = 0.0f, lse = 0.0f;
+    float ex[V];
+    const bool need_softmax = !SIGMOID || p.z != 0.0f;
+    if (need_softmax) {
+      m = warp_max(m);
+      float es = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        ex[v] = on[v] ? expf(l[v] - m) : 0.0f;
+        es += ex[v];
+      }
+      esum = warp_sum(es);
+      if (esum > 0.0f) lse = m + logf(esum);
+    }
+    const float einv = esum > 0.0f ? 1.0f / esum : 0.0f;
+    float total = 1.0f;
+    if constexpr (SIGMOID) {
+      float ss = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        s[v] = on[v] ? sigmoid_f32(l[v]) : 0.0f;
+        ss += s[v];
+      }
+      total = warp_sum(ss);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) s[v] = ex[v] * einv;
+    }
+    const float tinv = total > 0.0f ? 1.0f / total : 0.0f;
+    // the chosen slots: score of the slot's expert, then d score
+    float ps = 0.0f;
+    if (id >= 0) {
+      const float lj = load_logit<BF16>(row, id);
+      if (fabsf(lj) < INFINITY) ps = SIGMOID ? sigmoid_f32(lj) : expf(lj - m) * einv;
+    }
+    dw *= p.scale;
+    if (id < 0) dw = 0.0f;
+    float dp = dw;
+    if (p.renorm) {
+      const float tot = warp_sum(ps), dot = warp_sum(dw * ps);
+      dp = tot > 0.0f && id >= 0 ? (dw - dot / tot) / tot : 0.0f;
+    }
+    if (id >= 0) buf[id] = dp;
+    float dots = 0.0f;
+    if constexpr (!SIGMOID) dots = p.renorm ? 0.0f : warp_sum(dp * ps);
+    __syncwarp();
+    float dotq = 0.0f;
+    if (p.counts) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float q = SIGMOID ? s[v] * tinv : s[v];
+        dotq = fmaf(coef[v], q, dotq);
+        qsum[v] += q;
+      }
+      dotq = warp_sum(dotq);
+    }
+    const float zc = 2.0f * p.z / (float)p.T * lse * einv;
+    if (lane == 0) lse2 = fmaf(lse, lse, lse2);
+    float d[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float ds = buf[e0 + v] + (SIGMOID ? (coef[v] - dotq) * tinv : coef[v] - dotq);
+      d[v] = SIGMOID ? ds * s[v] * (1.0f - s[v]) : s[v] * (ds - dots);
+      if (need_softmax) d[v] = fmaf(zc, ex[v], d[v]);
+      d[v] = on[v] ? d[v] : 0.0f;
+    }
+    __syncwarp();
+    if (id >= 0) buf[id] = 0.0f;
+    __syncwarp();
+    char* out = static_cast<char*>(p.d_logits) + t * p.ld_out * (BF16 ? 2 : 4);
+    if constexpr (BF16) {
+      if (vec && V >= 2) {
+        uint32_t w2[V / 2 > 0 ? V / 2 : 1];
+#pragma unroll
+        for (int v = 0; v < V / 2; ++v)
+          w2[v] = (uint32_t)f32_to_bf16_rne(d[2 * v]) | ((uint32_t)f32_to_bf16_rne(d[2 * v + 1]) << 16);
+        uint32_t* o = reinterpret_cast<uint32_t*>(out) + e0 / 2;
+        if constexpr (V >= 8) {
+#pragma unroll
+          for (int i = 0; i < V / 8; ++i)
+            reinterpret_cast<uint4*>(o)[i] =
+                make_uint4(w2[4 * i], w2[4 * i + 1], w2[4 * i + 2], w2[4 * i + 3]);
+        } else {
+#pragma unroll
+          for (int v = 0; v < V / 2; ++v) o[v] = w2[v];
+        }
+        continue;
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (e0 + v < p.E) reinterpret_cast<uint16_t*>(out)[e0 + v] = f32_to_bf16_rne(d[v]);
+    } else {
+      if (vec && V >= 4) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i)
+          reinterpret_cast<float4*>(out)[e0 / 4 + i] =
+              make_float4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
+        continue;
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (e0 + v < p.E) reinterpret_cast<float*>(out)[e0 + v] = d[v];
+    }
+  }
+  if (bad) raise_device_error(p.err, MOE_DEVERR_BAD_EXPERT);
+  // the block's sums, warps in order
+  __syncwarp();
+#pragma unroll
+  for (int v = 0; v < V; ++v) buf[e0 + v] = qsum[v];
+  if (lane == 0) lse_part[warp] = lse2;
+  __syncthreads();
+  for (int e = threadIdx.x; e <= p.E; e += kScoredThreads) {
+    float a = 0.0f;
+    for (int w = 0; w < kScoredWarps; ++w) a += e < p.E ? scatter[w][e] : lse_part[w];
+    p.part[(int64_t)blockIdx.x * (p.E + 1) + e] = a;
+  }
+}
+
+// losses[0] = balance E / (k T) sum_e counts_e mean_t q_te, losses[1] = z mean lse^2:
+// the blocks' sums in block order, then a tree over the experts.
+constexpr int kLossThreads = 1024;
+__global__ void __launch_bounds__(kLossThreads) route_losses_kernel(ScoredGradParams p, int blocks,
+                                                                    float* losses) {
+  __shared__ float part[kLossThreads / 32];
+  __shared__ float zsum;
+  pdl_wait();
+  pdl_trigger();
+  const int e = threadIdx.x;
+  float term = 0.0f;
+  for (int x = e; x <= p.E; x += kLossThreads) {
+    float a = 0.0f;
+    for (int b = 0; b < blocks; ++b) a += p.part[(int64_t)b * (p.E + 1) + x];
+    if (x == p.E) zsum = a;
+    else if (p.counts) term += a * (float)p.counts[x];
+  }
+  term = warp_sum(term);
+  if ((e & 31) == 0) part[e >> 5] = term;
+  __syncthreads();
+  if (e < 32) {
+    const float s = warp_sum(part[e]);
+    if (e == 0) {
+      const float T = (float)p.T;
+      losses[0] = p.balance * ((float)p.E / ((float)p.k * T)) * (s / T);
+      losses[1] = p.z * (zsum / T);
+    }
+  }
+}
+
+constexpr int kGradMaxBlocks = 1024;
+
+int lane_values(int E) {
+  int v = 1;
+  while (32 * v < E) v <<= 1;
+  return v;
+}
+
+template <template <int, bool, bool> class F, typename... A>
+moe_status_t dispatch_scored(int V, bool bf16, bool sig, A&&... a) {
+#define MOE_SCORED_CASE(v)                                                             \
+  case v:                                                                              \
+    if (bf16) return sig ? F<v, true, true>::go(a...) : F<v, true, false>::go(a...);   \
+    return sig ? F<v, false, true>::go(a...) : F<v, false, false>::go(a...);
+  switch (V) {
+    MOE_SCORED_CASE(1)
+    MOE_SCORED_CASE(2)
+    MOE_SCORED_CASE(4)
+    MOE_SCORED_CASE(8)
+    MOE_SCORED_CASE(16)
+    MOE_SCORED_CASE(32)
+  }
+#undef MOE_SCORED_CASE
+  return MOE_ERR_UNSUPPORTED;
+}
+
+template <int V, bool BF16, bool SIG>
+struct ForwardLaunch {
+  static moe_status_t go(const ScoredParams& p, int grid, int vec, cudaStream_t st) {
+    return moe_host::launch(route_scored_kernel<V, BF16, SIG>, grid, kScoredThreads, 0, st, p, vec);
+  }
+};
+template <int V, bool BF16, bool SIG>
+struct BackwardLaunch {
+  static moe_status_t go(const ScoredGradParams& p, int grid, int vec, cudaStream_t st) {
+    return moe_host::launch(route_scored_backward_kernel<V, BF16, SIG>, grid, kScoredThreads, 0, st,
+                            p, vec);
+  }
+};
+
+// Whole-lane vector accesses: every lane's V values lie inside the row and on
+// a 16-byte (or whole-piece) boundary.
+bool can_vector(const void* base, int64_t ld, int E, int V, int size) {
+  const int piece = V * size < 16 ? V * size : 16;
+  return E == 32 * V && ld * size % piece == 0 &&
+         (reinterpret_cast<uintptr_t>(base) % piece) == 0;
+}
+
+bool scored_shape_ok(int T, int E, int k, int kmax, int dtype, int score, int64_t ld) {
+  return T >= 0 && E >= 1 && E <= 1024 && k >= 1 && k <= kmax && kmax <= 16 && k <= E && ld >= E &&
+         (int64_t)T * kmax <= (1 << 24) &&
+         (dtype == MOE_DTYPE_F32 || dtype == MOE_DTYPE_BF16) &&
+         (score == MOE_SCORE_SOFTMAX || score == MOE_SCORE_SIGMOID);
+}
+
+int scored_grid(int T) {
+  int64_t g = ((int64_t)T + kScoredWarps - 1) / kScoredWarps;
+  const int64_t cap = (int64_t)moe_host::sm_count() * 8;
+  if (g > cap) g = cap;
+  return (int)(g < 1 ? 1 : g);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status_t moe_route_scored(const void* logits, int logits_dtype, int64_t ld,
+                                         const float* select_bias, int T, int E, int score,
+                                         int n_groups, int topk_groups, int group_top, int k,
+                                         int kmax, int renormalize, float scale,
+                                         int32_t* topk_ids, float* topk_w, int32_t* k_dev,
+                                         moe_stream_t stream) {
+  using namespace moe_host;
+  if (!scored_shape_ok(T, E, k, kmax, logits_dtype, score, ld)) return MOE_ERR_INVALID_ARG;
+  if (n_groups < 1 || n_groups > kMaxGroups || E % n_groups || topk_groups < 1 ||
+      topk_groups > n_groups || (group_top != 1 && group_top != 2))
+    return MOE_ERR_INVALID_ARG;
+  if (k > topk_groups * (E / n_groups)) return MOE_ERR_INVALID_ARG;
+  if (!(scale > 0.0f) || isinf(scale)) return MOE_ERR_INVALID_ARG;
+  if (!k_dev) return MOE_ERR_INVALID_ARG;
+  const int size = logits_dtype == MOE_DTYPE_BF16 ? 2 : 4;
+  if (T > 0 && (!logits || !topk_ids || !topk_w)) return MOE_ERR_INVALID_ARG;
+  const void* ptrs[] = {select_bias, topk_ids, topk_w, k_dev};
+  for (const void* q : ptrs)
+    if (reinterpret_cast<uintptr_t>(q) & 3u) return MOE_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(logits) % size) return MOE_ERR_INVALID_ARG;
+  ScoredParams p;
+  p.logits = logits;
+  p.ld = ld;
+  p.bias = select_bias;
+  p.T = T;
+  p.E = E;
+  p.k = k;
+  p.kmax = kmax;
+  p.n_groups = n_groups;
+  p.topk_groups = topk_groups;
+  p.group_top = group_top;
+  p.renorm = renormalize != 0;
+  p.scale = scale;
+  p.ids = topk_ids;
+  p.w = topk_w;
+  p.k_dev = k_dev;
+  p.err = device_error_word();
+  const int V = lane_values(E);
+  return dispatch_scored<ForwardLaunch>(V, logits_dtype == MOE_DTYPE_BF16,
+                                        score == MOE_SCORE_SIGMOID, p, scored_grid(T),
+                                        (int)can_vector(logits, ld, E, V, size),
+                                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t moe_route_backward_workspace_size(int E) {
+  if (E < 1 || E > 1024) return 0;
+  return (size_t)kGradMaxBlocks * (E + 1) * sizeof(float);
+}
+
+extern "C" moe_status_t moe_route_scored_backward(
+    const void* logits, int logits_dtype, int64_t ld, const int32_t* topk_ids,
+    const float* d_topk_w, const int32_t* expert_counts, int T, int E, int score, int k, int kmax,
+    int renormalize, float scale, float balance_coef, float z_coef, void* d_logits, int64_t ld_out,
+    float* losses, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  using namespace moe_host;
+  if (!scored_shape_ok(T, E, k, kmax, logits_dtype, score, ld) || ld_out < E)
+    return MOE_ERR_INVALID_ARG;
+  if (!(scale > 0.0f) || isinf(scale) || !isfinite(balance_coef) || !isfinite(z_coef))
+    return MOE_ERR_INVALID_ARG;
+  if (balance_coef != 0.0f && !expert_counts) return MOE_ERR_INVALID_ARG;
+  if (!losses || !workspace || workspace_bytes < moe_route_backward_workspace_size(E))
+    return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!logits || !d_logits || d_logits == logits || (d_topk_w && !topk_ids)))
+    return MOE_ERR_INVALID_ARG;
+  const void* ptrs[] = {topk_ids, d_topk_w, expert_counts, losses, workspace};
+  for (const void* q : ptrs)
+    if (reinterpret_cast<uintptr_t>(q) & 3u) return MOE_ERR_INVALID_ARG;
+  const int size = logits_dtype == MOE_DTYPE_BF16 ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(logits) % size || reinterpret_cast<uintptr_t>(d_logits) % size)
+    return MOE_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0)
+    return cudaMemsetAsync(losses, 0, 2 * sizeof(float), st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  ScoredGradParams p;
+  p.logits = logits;
+  p.ld = ld;
+  p.ids = topk_ids;
+  p.d_w = d_topk_w;
+  p.counts = balance_coef != 0.0f ? expert_counts : nullptr;
+  p.T = T;
+  p.E = E;
+  p.k = k;
+  p.kmax = kmax;
+  p.renorm = renormalize != 0;
+  p.scale = scale;
+  p.balance = balance_coef;
+  p.z = z_coef;
+  p.d_logits = d_logits;
+  p.ld_out = ld_out;
+  p.part = static_cast<float*>(workspace);
+  p.err = device_error_word();
+  const int V = lane_values(E);
+  int grid = scored_grid(T);
+  if (grid > kGradMaxBlocks) grid = kGradMaxBlocks;
+  const bool vec = can_vector(logits, ld, E, V, size) && can_vector(d_logits, ld_out, E, V, size);
+  const moe_status_t s =
+      dispatch_scored<BackwardLaunch>(V, logits_dtype == MOE_DTYPE_BF16,
+                                      score == MOE_SCORE_SIGMOID, p, grid, (int)vec, st);
+  if (s != MOE_OK) return s;
+  return launch(route_losses_kernel, 1, kLossThreads, 0, st, p, grid, losses);
+}
