@@ -12,66 +12,13 @@
 // contraction index is free, so lane t of a quad takes contiguous elements
 // of its row (16 bytes of x and A, 8 bytes of B) and no shared-memory
 // staging is needed.
-#include "common.cuh"
+#include "lora.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kLoraThreads = 256;
 constexpr int kLoraWarps = kLoraThreads / 32;
-constexpr int kMaxRank = 128;
-
-struct LoraParams {
-  const uint16_t* x;
-  int x_by_token;
-  const int32_t* adapter_ids;  // [T]
-  const int32_t* topk_ids;     // [T, kmax], null: one projection (E = 1)
-  const int32_t* sorted;       // [T kmax], null: rows are tokens
-  const int32_t* offsets;      // [E + 1]
-  int T, kmax, E, n_adapters;
-  int K, N, R;
-  const uint16_t* a;  // [n_adapters, E, R, K]
-  const uint16_t* b;  // [n_adapters, E, N, R]
-  const float* scales;
-  const void* base;
-  void* out;
-  float* v;  // [rows, R]
-  unsigned int* err;
-};
-
-// Which matrices a row uses.
-struct LoraRow {
-  int slot;       // adapter * E + expert, or -1: no adapter
-  int64_t x_row;  // row of x
-};
-
-__device__ __forceinline__ int lora_rows(const LoraParams& p) {
-  if (!p.sorted) return p.T;
-  return min(max(__ldg(p.offsets + p.E), 0), p.T * p.kmax);
-}
-
-__device__ __forceinline__ LoraRow lora_row(const LoraParams& p, int r) {
-  int a = r, e = 0;
-  if (p.sorted) {
-    a = __ldg(p.sorted + r);
-    if (a < 0 || a >= p.T * p.kmax) {
-      raise_device_error(p.err, MOE_DEVERR_BAD_INDEX);
-      return {-1, 0};
-    }
-    e = __ldg(p.topk_ids + a);
-  }
-  const int token = a / p.kmax;
-  const int ad = __ldg(p.adapter_ids + token);
-  LoraRow row{-1, p.x_by_token ? token : r};
-  if (e < 0 || e >= p.E) {
-    raise_device_error(p.err, MOE_DEVERR_BAD_EXPERT);
-  } else if (ad >= p.n_adapters) {
-    raise_device_error(p.err, MOE_DEVERR_BAD_ADAPTER);
-  } else if (ad >= 0) {
-    row.slot = ad * p.E + e;
-  }
-  return row;
-}
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
@@ -262,10 +209,50 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(LoraParams p)
 
 using namespace moe;
 
+namespace {
+
+// From this many rows on they are grouped by adapter, if each adapter (and
+// expert) may expect two or more.
+constexpr int kLoraGroupRows = 192;
+
+bool lora_groups(int64_t rows, int E, int n_adapters) {
+  return rows >= kLoraGroupRows && rows >= 2 * (int64_t)n_adapters * E &&
+         n_adapters <= kLoraPlanAdapters;
+}
+
+// K ranges of the grouped shrink: enough (tile, range) units for two CTAs per
+// SM when the tiles alone are too few, at least four k-blocks of 64 each.
+int lora_splits(int64_t rows, int K) {
+  const int64_t tiles = (rows + kLoraTileRows - 1) / kLoraTileRows;
+  int64_t s = (2 * 148 + tiles - 1) / tiles;
+  if (s > K / 256) s = K / 256;
+  if (s > kLoraMaxSplit) s = kLoraMaxSplit;
+  return s < 1 ? 1 : (int)s;
+}
+
+struct LoraSpace {
+  size_t v, perm, tiles, total;
+};
+
+LoraSpace lora_space(int64_t rows, int E, int n_adapters, int R) {
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  LoraSpace s{};
+  const size_t one = (size_t)(rows ? rows : 1) * R * sizeof(float);
+  if (!lora_groups(rows, E, n_adapters)) {
+    s.total = one;
+    return s;
+  }
+  s.perm = up(one * lora_splits(rows, 1 << 20));
+  s.tiles = s.perm + up((size_t)rows * sizeof(int32_t));
+  s.total = s.tiles + (size_t)(1 + lora_tile_capacity(rows, E, n_adapters)) * sizeof(int4);
+  return s;
+}
+
+}  // namespace
+
 extern "C" size_t moe_lora_workspace_size(int T, int kmax, int E, int n_adapters, int R) {
   if (T < 0 || kmax < 1 || kmax > 16 || E < 1 || n_adapters < 1 || R < 1 || R > kMaxRank) return 0;
-  const size_t rows = (size_t)T * kmax;
-  return (rows ? rows : 1) * R * sizeof(float);
+  return lora_space((int64_t)T * kmax, E, n_adapters, R).total;
 }
 
 extern "C" moe_status_t moe_lora_apply(const uint16_t* x, int x_by_token,
@@ -324,6 +311,14 @@ extern "C" moe_status_t moe_lora_apply(const uint16_t* x, int x_by_token,
   p.err = device_error_word();
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int rows = T * kmax;
+  if (lora_groups(rows, E, n_adapters)) {
+    const LoraSpace sp = lora_space(rows, E, n_adapters, R);
+    char* ws = static_cast<char*>(workspace);
+    const LoraPlan plan{reinterpret_cast<int32_t*>(ws + sp.perm),
+                        reinterpret_cast<int4*>(ws + sp.tiles), lora_splits(rows, K),
+                        !swiglu && base == out, lora_tile_capacity(rows, E, n_adapters)};
+    return lora_grouped(p, plan, rows, swiglu, out_dtype == MOE_DTYPE_BF16, st);
+  }
   moe_status_t s;
   if (R <= 16) s = launch(lora_shrink_kernel<2>, rows, kLoraThreads, 0, st, p);
   else if (R <= 32) s = launch(lora_shrink_kernel<4>, rows, kLoraThreads, 0, st, p);

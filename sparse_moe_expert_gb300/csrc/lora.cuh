@@ -1,0 +1,87 @@
+// Parameters and row lookup shared by the adapter kernels.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+constexpr int kMaxRank = 128;
+
+struct LoraParams {
+  const uint16_t* x;
+  int x_by_token;
+  const int32_t* adapter_ids;  // [T]
+  const int32_t* topk_ids;     // [T, kmax], null: one projection (E = 1)
+  const int32_t* sorted;       // [T kmax], null: rows are tokens
+  const int32_t* offsets;      // [E + 1]
+  int T, kmax, E, n_adapters;
+  int K, N, R;
+  const uint16_t* a;  // [n_adapters, E, R, K]
+  const uint16_t* b;  // [n_adapters, E, N, R]
+  const float* scales;
+  const void* base;
+  void* out;
+  float* v;  // [rows, R]
+  unsigned int* err;
+};
+
+// Which matrices a row uses.
+struct LoraRow {
+  int slot;       // adapter * E + expert, or -1: no adapter
+  int64_t x_row;  // row of x
+};
+
+__device__ __forceinline__ int lora_rows(const LoraParams& p) {
+  if (!p.sorted) return p.T;
+  return min(max(__ldg(p.offsets + p.E), 0), p.T * p.kmax);
+}
+
+__device__ __forceinline__ LoraRow lora_row(const LoraParams& p, int r) {
+  int a = r, e = 0;
+  if (p.sorted) {
+    a = __ldg(p.sorted + r);
+    if (a < 0 || a >= p.T * p.kmax) {
+      raise_device_error(p.err, MOE_DEVERR_BAD_INDEX);
+      return {-1, 0};
+    }
+    e = __ldg(p.topk_ids + a);
+  }
+  const int token = a / p.kmax;
+  const int ad = __ldg(p.adapter_ids + token);
+  LoraRow row{-1, p.x_by_token ? token : r};
+  if (e < 0 || e >= p.E) {
+    raise_device_error(p.err, MOE_DEVERR_BAD_EXPERT);
+  } else if (ad >= p.n_adapters) {
+    raise_device_error(p.err, MOE_DEVERR_BAD_ADAPTER);
+  } else if (ad >= 0) {
+    row.slot = ad * p.E + e;
+  }
+  return row;
+}
+
+// Rows grouped by the matrices they use, made on the device for one call.
+// perm[pos] = row; a tile is up to kLoraTileRows consecutive positions of one
+// slot: tiles[1 + i] = (slot or -1, first position, rows, 0); tiles[0].x is
+// their count.
+constexpr int kLoraTileRows = 128;
+constexpr int kLoraMaxSplit = 8;  // K ranges of the grouped shrink
+struct LoraPlan {
+  int32_t* perm;
+  int4* tiles;
+  int splits;     // K ranges; v holds one [rows, R] partial sum per range
+  int skip_none;  // rows without an adapter need no work
+  int64_t capacity;  // tiles the list holds
+};
+
+// Most adapters the grouping's counters hold in shared memory.
+constexpr int kLoraPlanAdapters = 4096;
+
+inline int64_t lora_tile_capacity(int64_t rows, int E, int n_adapters) {
+  const int64_t most = rows / kLoraTileRows + (int64_t)E * (n_adapters + 1);
+  return rows < most ? rows : most;
+}
+
+moe_status_t lora_grouped(const LoraParams& p, const LoraPlan& plan, int64_t rows, bool swiglu,
+                          bool out_bf16, cudaStream_t st);
+
+}  // namespace moe
