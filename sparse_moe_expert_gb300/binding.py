@@ -8,6 +8,7 @@ of the layer is computed here.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -289,6 +290,10 @@ def moe_get_device_error(clear: bool = True, stream=None) -> int:
 
 
 # ---- score routing, its gradient, adapters ----------------------------------
+#
+# These calls are short (a few microseconds on the device), so the checks are
+# single comparisons that fall through to a message only when one fails, and
+# sizes that depend on a few integers are remembered.
 
 
 def _raw(t: Optional[torch.Tensor]):
@@ -296,17 +301,19 @@ def _raw(t: Optional[torch.Tensor]):
 
 
 def _cur(stream, dev) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    return s.cuda_stream
+    """The cudaStream_t of ``stream``, or of the device's current stream
+    (read without building a torch.cuda.Stream, which costs 3 us)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _hold(stream, *tensors):
     """Tell the allocator that ``stream`` uses these tensors, so that none of
     their memory is handed out again before the enqueued work has run."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
 
 
 def _rows2d(t: torch.Tensor, name: str) -> int:
@@ -318,41 +325,74 @@ def _rows2d(t: torch.Tensor, name: str) -> int:
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions")
     T, E = t.shape
-    if E > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if E > 1 and step != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    ld = t.stride(0) if T > 1 else E
+    if T <= 1:
+        return E
     if ld < E:
         raise ValueError(f"{name} must have rows that do not overlap")
     return ld
 
 
-def _like(t: torch.Tensor, shape, dtype, dev, name: str):
+def _like(t: torch.Tensor, shape: tuple, dtype, dev, name: str):
+    if t.dtype == dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return
     _need(t, dtype, name)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be on {dev}")
+
+
+def _flat(t: torch.Tensor, least: int, dev, name: str):
+    """A contiguous int32 tensor of at least ``least`` elements."""
+    if t.dtype == torch.int32 and t.device == dev and t.is_contiguous() and t.numel() >= least:
+        return
+    _need(t, torch.int32, name)
+    if t.numel() < least:
+        raise ValueError(f"{name} must hold {least} entries")
+    raise ValueError(f"{name} must be on {dev}")
+
+
+def _matrix(t: torch.Tensor, rows: int, cols: int, dev, name: str):
+    """A contiguous fp32 or bf16 matrix of at least ``rows`` rows of ``cols``."""
+    if t.dtype not in _DT:
+        raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if t.dim() == 2 and t.device == dev and t.is_contiguous():
+        n, c = t.shape
+        if n >= rows and c == cols:
+            return
+    _need(t, t.dtype, name)
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}")
+    raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
+
+
+def _scratch(t: Optional[torch.Tensor], dev) -> int:
+    if t.device != dev or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    return t.numel() * t.element_size()
 
 
 def moe_router_logits(x, w_router, logit_bias=None, inv_temperature: float = 1.0, logits=None,
                       stream=None):
     """-> logits fp32 [T, E], in the summation order of moe_router_topk."""
     _need(x, torch.bfloat16, "x")
-    _need(w_router, torch.float32, "w_router")
+    dev = x.device
     T, H = x.shape
     E = w_router.shape[0]
-    if w_router.shape[1] != H:
-        raise ValueError("w_router and x differ in their hidden size")
+    _like(w_router, (E, H), torch.float32, dev, "w_router")
     if logit_bias is not None:
-        _like(logit_bias, (E,), torch.float32, x.device, "logit_bias")
+        _like(logit_bias, (E,), torch.float32, dev, "logit_bias")
     if logits is None:
-        logits = torch.empty((T, E), dtype=torch.float32, device=x.device)
+        logits = torch.empty((T, E), dtype=torch.float32, device=dev)
     else:
-        _like(logits, (T, E), torch.float32, x.device, "logits")
-    _hold(stream, x, w_router, logit_bias, logits)
+        _like(logits, (T, E), torch.float32, dev, "logits")
+    if stream is not None:
+        _hold(stream, x, w_router, logit_bias, logits)
     check("moe_router_logits",
-          lib().moe_router_logits(_raw(x), _raw(w_router), _raw(logit_bias), inv_temperature, T, H,
-                                  E, _raw(logits), _cur(stream, x.device)))
+          lib().moe_router_logits(x.data_ptr(), w_router.data_ptr(), _raw(logit_bias),
+                                  inv_temperature, T, H, E, logits.data_ptr(), _cur(stream, dev)))
     return logits
 
 
@@ -385,15 +425,18 @@ def moe_route_scored(logits, k: int, score: int = _lib.SCORE_SOFTMAX, select_bia
         k_dev = torch.empty(1, dtype=torch.int32, device=dev)
     else:
         _like(k_dev, (1,), torch.int32, dev, "k_dev")
-    _hold(stream, logits, select_bias, topk_ids, topk_w, k_dev)
-    st = lib().moe_route_scored(_raw(logits), _DT[logits.dtype], ld, _raw(select_bias), T, E, score,
-                                n_groups, topk_groups, group_top, k, kmax, bool(renormalize),
-                                scale, _raw(topk_ids), _raw(topk_w), _raw(k_dev),
-                                _cur(stream, dev))
-    check("moe_route_scored", st)
+    if stream is not None:
+        _hold(stream, logits, select_bias, topk_ids, topk_w, k_dev)
+    st = lib().moe_route_scored(logits.data_ptr(), _DT[logits.dtype], ld, _raw(select_bias), T, E,
+                                score, n_groups, topk_groups, group_top, k, kmax,
+                                bool(renormalize), scale, topk_ids.data_ptr(), topk_w.data_ptr(),
+                                k_dev.data_ptr(), _cur(stream, dev))
+    if st:
+        check("moe_route_scored", st)
     return topk_ids, topk_w, k_dev
 
 
+@functools.lru_cache(maxsize=1024)
 def moe_route_backward_workspace_size(E: int) -> int:
     return int(lib().moe_route_backward_workspace_size(E))
 
@@ -410,10 +453,10 @@ def moe_route_scored_backward(logits, topk_ids, d_topk_w=None, expert_counts=Non
     ld = _rows2d(logits, "logits")
     T, E = logits.shape
     dev = logits.device
-    _need(topk_ids, torch.int32, "topk_ids")
     if topk_ids.dim() != 2 or topk_ids.shape[0] != T:
         raise ValueError("topk_ids must be [T, kmax]")
     kmax = topk_ids.shape[1]
+    _like(topk_ids, (T, kmax), torch.int32, dev, "topk_ids")
     if k is None:
         k = kmax
     if d_topk_w is not None:
@@ -422,21 +465,31 @@ def moe_route_scored_backward(logits, topk_ids, d_topk_w=None, expert_counts=Non
         _like(expert_counts, (E,), torch.int32, dev, "expert_counts")
     if d_logits is None:
         d_logits = torch.empty((T, E), dtype=logits.dtype, device=dev)
-    elif d_logits.dtype != logits.dtype or d_logits.shape != logits.shape:
-        raise ValueError("d_logits must have the type and shape of logits")
-    ld_out = _rows2d(d_logits, "d_logits")
+        ld_out = E
+    else:
+        if d_logits.dtype != logits.dtype or d_logits.shape != logits.shape:
+            raise ValueError("d_logits must have the type and shape of logits")
+        if d_logits.device != dev:
+            raise ValueError(f"d_logits must be on {dev}")
+        ld_out = _rows2d(d_logits, "d_logits")
     if losses is None:
         losses = torch.empty(2, dtype=torch.float32, device=dev)
     else:
         _like(losses, (2,), torch.float32, dev, "losses")
     if workspace is None:
-        workspace = torch.empty(moe_route_backward_workspace_size(E), dtype=torch.uint8, device=dev)
-    _hold(stream, logits, topk_ids, d_topk_w, expert_counts, d_logits, losses, workspace)
+        ws_bytes = moe_route_backward_workspace_size(E)
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    else:
+        ws_bytes = _scratch(workspace, dev)
+    if stream is not None:
+        _hold(stream, logits, topk_ids, d_topk_w, expert_counts, d_logits, losses, workspace)
     st = lib().moe_route_scored_backward(
-        _raw(logits), _DT[logits.dtype], ld, _raw(topk_ids), _raw(d_topk_w), _raw(expert_counts),
-        T, E, score, k, kmax, bool(renormalize), scale, balance_coef, z_coef, _raw(d_logits),
-        ld_out, _raw(losses), _raw(workspace), workspace.numel(), _cur(stream, dev))
-    check("moe_route_scored_backward", st)
+        logits.data_ptr(), _DT[logits.dtype], ld, topk_ids.data_ptr(), _raw(d_topk_w),
+        _raw(expert_counts), T, E, score, k, kmax, bool(renormalize), scale, balance_coef, z_coef,
+        d_logits.data_ptr(), ld_out, losses.data_ptr(), workspace.data_ptr(), ws_bytes,
+        _cur(stream, dev))
+    if st:
+        check("moe_route_scored_backward", st)
     return d_logits, losses
 
 
@@ -448,19 +501,31 @@ def moe_permute_masked(topk_ids, k_dev, E: int, capacity: Optional[int] = None,
     _need(topk_ids, torch.int32, "topk_ids")
     T, kmax = topk_ids.shape
     dev = topk_ids.device
+    A = max(T * kmax, 1)
+    _like(k_dev, (1,), torch.int32, dev, "k_dev")
     if expert_counts is None:
         expert_counts = torch.empty(E, dtype=torch.int32, device=dev)
+    else:
+        _like(expert_counts, (E,), torch.int32, dev, "expert_counts")
     if expert_offsets is None:
         expert_offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    else:
+        _like(expert_offsets, (E + 1,), torch.int32, dev, "expert_offsets")
     if sorted_assign is None:
-        sorted_assign = torch.empty(max(T * kmax, 1), dtype=torch.int32, device=dev)
+        sorted_assign = torch.empty(A, dtype=torch.int32, device=dev)
+    else:
+        _flat(sorted_assign, T * kmax, dev, "sorted_assign")
     if inv_pos is None:
-        inv_pos = torch.empty(max(T * kmax, 1), dtype=torch.int32, device=dev)
-    _hold(stream, topk_ids, k_dev, expert_counts, expert_offsets, sorted_assign, inv_pos)
+        inv_pos = torch.empty(A, dtype=torch.int32, device=dev)
+    else:
+        _flat(inv_pos, T * kmax, dev, "inv_pos")
+    if stream is not None:
+        _hold(stream, topk_ids, k_dev, expert_counts, expert_offsets, sorted_assign, inv_pos)
     check("moe_permute_masked",
-          lib().moe_permute_masked(_raw(topk_ids), _raw(k_dev), T, kmax, E,
-                                   -1 if capacity is None else int(capacity), _raw(expert_counts),
-                                   _raw(expert_offsets), _raw(sorted_assign), _raw(inv_pos),
+          lib().moe_permute_masked(topk_ids.data_ptr(), k_dev.data_ptr(), T, kmax, E,
+                                   -1 if capacity is None else int(capacity),
+                                   expert_counts.data_ptr(), expert_offsets.data_ptr(),
+                                   sorted_assign.data_ptr(), inv_pos.data_ptr(),
                                    _cur(stream, dev)))
     return expert_counts, expert_offsets, sorted_assign, inv_pos
 
@@ -473,35 +538,34 @@ def moe_combine_backward(d_out, y, inv_pos, topk_w, k_dev, d_topk_w=None, d_y=No
     when the buffer is allocated here).  need_d_y=False computes d_topk_w
     alone (d_y is None)."""
     _need(d_out, torch.bfloat16, "d_out")
-    if y.dtype not in _DT:
-        raise ValueError(f"y must be float32 or bfloat16, got {y.dtype}")
-    _need(y, y.dtype, "y")
     T, H = d_out.shape
     dev = d_out.device
     if topk_w.dim() != 2:
         raise ValueError("topk_w must be [T, kmax]")
     kmax = topk_w.shape[1]
     _like(topk_w, (T, kmax), torch.float32, dev, "topk_w")
-    _need(inv_pos, torch.int32, "inv_pos")
-    if inv_pos.numel() < T * kmax or y.dim() != 2 or y.shape[1] != H or y.shape[0] < T * kmax:
-        raise ValueError("y must be [T*kmax, H] and inv_pos [T*kmax]")
+    _flat(inv_pos, T * kmax, dev, "inv_pos")
+    _matrix(y, T * kmax, H, dev, "y")
     _like(k_dev, (1,), torch.int32, dev, "k_dev")
     if d_topk_w is None:
         d_topk_w = torch.empty((T, kmax), dtype=torch.float32, device=dev)
     else:
         _like(d_topk_w, (T, kmax), torch.float32, dev, "d_topk_w")
     if d_y is not None:
-        _like(d_y, y.shape, y.dtype, dev, "d_y")
+        _like(d_y, tuple(y.shape), y.dtype, dev, "d_y")
     elif need_d_y:
         d_y = torch.zeros_like(y)
-    _hold(stream, d_out, y, inv_pos, topk_w, k_dev, d_topk_w, d_y)
-    check("moe_combine_backward",
-          lib().moe_combine_backward(_raw(d_out), _raw(y), _DT[y.dtype], _raw(inv_pos),
-                                     _raw(topk_w), _raw(k_dev), T, kmax, H, _raw(d_topk_w),
-                                     _raw(d_y), _cur(stream, dev)))
+    if stream is not None:
+        _hold(stream, d_out, y, inv_pos, topk_w, k_dev, d_topk_w, d_y)
+    st = lib().moe_combine_backward(d_out.data_ptr(), y.data_ptr(), _DT[y.dtype],
+                                    inv_pos.data_ptr(), topk_w.data_ptr(), k_dev.data_ptr(), T,
+                                    kmax, H, d_topk_w.data_ptr(), _raw(d_y), _cur(stream, dev))
+    if st:
+        check("moe_combine_backward", st)
     return d_topk_w, d_y
 
 
+@functools.lru_cache(maxsize=1024)
 def moe_lora_workspace_size(T: int, kmax: int, E: int, n_adapters: int, R: int) -> int:
     return int(lib().moe_lora_workspace_size(T, kmax, E, n_adapters, R))
 
@@ -521,21 +585,18 @@ def moe_lora_apply(x, adapter_ids, lora_a, lora_b, scales=None, base=None, out=N
     unless out_dtype says fp32.  k_dev is accepted beside the other routing
     results and not needed (expert_offsets holds the row count)."""
     _need(x, torch.bfloat16, "x")
-    _need(lora_a, torch.bfloat16, "lora_a")
-    _need(lora_b, torch.bfloat16, "lora_b")
     dev = x.device
-    if lora_a.dim() == 3:
-        n, R, K = lora_a.shape
+    shape = lora_a.shape
+    if len(shape) == 3:
+        n, R, K = shape
         E = 1
-    elif lora_a.dim() == 4:
-        n, E, R, K = lora_a.shape
+    elif len(shape) == 4:
+        n, E, R, K = shape
     else:
         raise ValueError("lora_a must be [n, R, K] or [n, E, R, K]")
     N = lora_b.shape[-2]
-    if tuple(lora_b.shape) != ((n, N, R) if lora_a.dim() == 3 else (n, E, N, R)):
-        raise ValueError("lora_b does not match lora_a")
-    if x.dim() != 2 or x.shape[1] != K:
-        raise ValueError(f"x must be [rows, {K}]")
+    _like(lora_a, tuple(shape), torch.bfloat16, dev, "lora_a")
+    _like(lora_b, (n, N, R) if len(shape) == 3 else (n, E, N, R), torch.bfloat16, dev, "lora_b")
     T = adapter_ids.shape[0]
     _like(adapter_ids, (T,), torch.int32, dev, "adapter_ids")
     kmax = 1
@@ -545,12 +606,12 @@ def moe_lora_apply(x, adapter_ids, lora_a, lora_b, scales=None, base=None, out=N
         kmax = topk_ids.shape[1]
         _like(topk_ids, (T, kmax), torch.int32, dev, "topk_ids")
         _like(expert_offsets, (E + 1,), torch.int32, dev, "expert_offsets")
-        _need(sorted_assign, torch.int32, "sorted_assign")
-        if sorted_assign.numel() < T * kmax:
-            raise ValueError("sorted_assign must hold T*kmax entries")
+        _flat(sorted_assign, T * kmax, dev, "sorted_assign")
     elif topk_ids is not None or expert_offsets is not None:
         raise ValueError("expert rows need topk_ids, sorted_assign and expert_offsets")
     rows = T * kmax
+    if x.dim() != 2 or x.shape[1] != K:
+        raise ValueError(f"x must be [rows, {K}]")
     if x.shape[0] < (T if x_by_token else rows):
         raise ValueError("x has too few rows")
     if scales is not None:
@@ -558,31 +619,28 @@ def moe_lora_apply(x, adapter_ids, lora_a, lora_b, scales=None, base=None, out=N
     swiglu = epilogue == EPILOGUE_SWIGLU
     cols = N // 2 if swiglu else N
     if base is not None:
-        if base.dtype not in _DT:
-            raise ValueError(f"base must be float32 or bfloat16, got {base.dtype}")
-        _need(base, base.dtype, "base")
-        if base.dim() != 2 or base.shape[0] < rows or base.shape[1] != N:
-            raise ValueError(f"base must be [{rows}, {N}]")
+        _matrix(base, rows, N, dev, "base")
     if out is not None:
-        if out.dtype not in _DT:
-            raise ValueError(f"out must be float32 or bfloat16, got {out.dtype}")
-        _need(out, out.dtype, "out")
-        if out.dim() != 2 or out.shape[0] < rows or out.shape[1] != cols:
-            raise ValueError(f"out must be [{rows}, {cols}]")
+        _matrix(out, rows, cols, dev, "out")
     else:
         if out_dtype is None:
             out_dtype = torch.bfloat16 if swiglu or base is None else base.dtype
         out = torch.empty((rows, cols), dtype=out_dtype, device=dev)
-    base_dt = _DT[out.dtype] if base is None else _DT[base.dtype]
-    need = moe_lora_workspace_size(T, kmax, E, n, R)
+    out_dt = _DT[out.dtype]
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _hold(stream, x, adapter_ids, lora_a, lora_b, scales, base, out, topk_ids, sorted_assign,
-          expert_offsets, workspace)
-    st = lib().moe_lora_apply(_raw(x), int(x_by_token), _raw(adapter_ids), _raw(topk_ids),
-                              _raw(sorted_assign), _raw(expert_offsets), T, kmax, E, n, K, N, R,
-                              _raw(lora_a), _raw(lora_b), _raw(scales), _raw(base), base_dt,
-                              epilogue, _DT[out.dtype], _raw(out), _raw(workspace),
-                              workspace.numel(), _cur(stream, dev))
-    check("moe_lora_apply", st)
+        ws_bytes = moe_lora_workspace_size(T, kmax, E, n, R)
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    else:
+        ws_bytes = _scratch(workspace, dev)
+    if stream is not None:
+        _hold(stream, x, adapter_ids, lora_a, lora_b, scales, base, out, topk_ids, sorted_assign,
+              expert_offsets, workspace)
+    st = lib().moe_lora_apply(x.data_ptr(), bool(x_by_token), adapter_ids.data_ptr(),
+                              _raw(topk_ids), _raw(sorted_assign), _raw(expert_offsets), T, kmax,
+                              E, n, K, N, R, lora_a.data_ptr(), lora_b.data_ptr(), _raw(scales),
+                              _raw(base), out_dt if base is None else _DT[base.dtype], epilogue,
+                              out_dt, out.data_ptr(), workspace.data_ptr(), ws_bytes,
+                              _cur(stream, dev))
+    if st:
+        check("moe_lora_apply", st)
     return out
