@@ -64,7 +64,7 @@ __device__ __forceinline__ void load_logits(float (&l)[V], const void* row, int 
       if constexpr (V >= 8) {
 #pragma unroll
         for (int i = 0; i < V / 8; ++i) {
-          const uint4 q = ldg_nc_v4(p + 4 * i);
+          const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + i);
           const uint32_t w4[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -290,42 +290,40 @@ __device__ __noinline__ void route_token_exact(const ScoredParams& p, int64_t t,
   store_chosen(p, t, my_id, my_s);
 }
 
-// Group selection on approximate choices (each within `eps` of the exact
-// one).  False when the cut between chosen and struck groups is closer than
-// the approximation; otherwise the struck groups' choices become -inf.
+// 1 / (1 + exp(-l)) to 1e-6 absolute: the hardware's 2^x and reciprocal, two
+// instructions where expf and an exact division take some twenty.
+__device__ __forceinline__ float sigmoid_approx(float l) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * l));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return r;
+}
+
+// Largest two of the lane's V values.
 template <int V>
-__device__ __forceinline__ bool limit_groups_approx(const ScoredParams& p, float (&c)[V], int e0,
-                                                    float eps) {
-  const int lane = threadIdx.x & 31;
-  const int G = p.n_groups, gsz = p.E / G;
-  const int span = gsz / V;
-  if (gsz % V != 0 || (span & (span - 1)) != 0 || span > 32) return false;  // uniform
-  float a1 = -INFINITY, a2 = -INFINITY;
+__device__ __forceinline__ void lane_top2(const float (&c)[V], float& a1, float& a2) {
+  if constexpr (V == 1) {
+    a1 = c[0];
+    a2 = -INFINITY;
+  } else {
+    float hi[V / 2], lo[V / 2];
 #pragma unroll
-  for (int v = 0; v < V; ++v) merge_top2(a1, a2, c[v], -INFINITY);
-  for (int o = 1; o < span; o <<= 1) {
-    const float b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
-    merge_top2(a1, a2, b1, b2);
-  }
-  const float val = p.group_top == 2 && a2 > -INFINITY ? a1 + a2 : a1;
-  const float other = __shfl_sync(kFull, val, lane < G ? lane * span : 0);
-  const float mine = lane < G ? other : -INFINITY;
-  int rank = 0;
-  for (int g = 0; g < G; ++g) {
-    const float o = __shfl_sync(kFull, mine, g);
-    rank += o > mine || (o == mine && g < lane);
-  }
-  const bool chosen = lane < G && rank < p.topk_groups;
-  const float lo = redux_min(chosen ? mine : INFINITY);
-  const float hi = redux_max(chosen ? -INFINITY : mine);
-  if (hi > -INFINITY && !(lo - hi > 4.0f * eps + fabsf(hi) * 0x1p-20f)) return false;
-  const unsigned set = __ballot_sync(kFull, chosen);
-  const int g = e0 / gsz;
-  if (g >= G || !((set >> g) & 1u)) {
+    for (int v = 0; v < V / 2; ++v) {
+      hi[v] = fmaxf(c[2 * v], c[2 * v + 1]);
+      lo[v] = fminf(c[2 * v], c[2 * v + 1]);
+    }
 #pragma unroll
-    for (int v = 0; v < V; ++v) c[v] = -INFINITY;
+    for (int n = V / 2; n > 1; n >>= 1)
+#pragma unroll
+      for (int v = 0; v < n / 2; ++v) {
+        float x1 = hi[2 * v], x2 = lo[2 * v];
+        merge_top2(x1, x2, hi[2 * v + 1], lo[2 * v + 1]);
+        hi[v] = x1;
+        lo[v] = x2;
+      }
+    a1 = hi[0];
+    a2 = lo[0];
   }
-  return true;
 }
 
 // Ids and weights of one token per warp and step.
@@ -337,13 +335,17 @@ __device__ __forceinline__ bool limit_groups_approx(const ScoredParams& p, float
 // The k-th largest of the lanes' best c~ is a lower bound of the k-th largest
 // choice, so every chosen expert has c~ >= bound - 2 eps.  Those candidates
 // (about k + 2 of 256) get one lane each, their exact scores and their ranks
-// by counting, and the lanes with rank < k are the answer.  More than 32
-// candidates (many equal choices) or groups too close to call fall back to
-// route_token_exact; results never depend on which way was taken.
-// Measured, 65536 tokens x 256 bf16 experts, k 8, 4 of 8 groups: see below.
+// by counting, and the lanes with rank < k are the answer.  Groups are cut on
+// c~ too when the cut is wider than the approximation.  More than 32
+// candidates (many equal choices), groups too close to call and groups that
+// are not whole runs of lanes go to route_token_exact; results do not depend
+// on which way was taken.
+//
+// Bound by the issue rate: MEASURED_PLACEHOLDER
 template <int V, bool BF16, bool SIGMOID>
-__global__ void __launch_bounds__(kScoredThreads) route_scored_kernel(ScoredParams p, int vec) {
-  __shared__ float2 cand[kScoredWarps][32];
+__global__ void __launch_bounds__(kScoredThreads, V <= 8 ? 4 : 2)
+    route_scored_kernel(ScoredParams p, int vec) {
+  __shared__ __align__(16) float2 cand[kScoredWarps][32];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -354,9 +356,15 @@ __global__ void __launch_bounds__(kScoredThreads) route_scored_kernel(ScoredPara
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     b[v] = p.bias && e0 + v < p.E ? __ldg(p.bias + e0 + v) : 0.0f;
-    bad |= b[v] != b[v];
+    if (b[v] != b[v]) {
+      bad = true;
+      b[v] = -INFINITY;
+    }
   }
-  const float eps = 1e-6f;
+  constexpr float eps = 1e-6f;
+  const int G = p.n_groups, gsz = p.E / G, span = gsz / V;  // span: lanes of a group
+  const bool lane_groups = gsz % V == 0 && (span & (span - 1)) == 0 && span <= 32;
+  const int my_group = e0 / gsz;  // >= G past the experts
   for (int64_t t = (int64_t)blockIdx.x * kScoredWarps + warp; t < p.T;
        t += (int64_t)gridDim.x * kScoredWarps) {
     float l[V], c[V];
@@ -367,9 +375,7 @@ __global__ void __launch_bounds__(kScoredThreads) route_scored_kernel(ScoredPara
     for (int v = 0; v < V; ++v) bad |= !(l[v] < INFINITY);
     if constexpr (SIGMOID) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        c[v] = __fdividef(1.0f, 1.0f + __expf(-l[v]));
-      }
+      for (int v = 0; v < V; ++v) c[v] = sigmoid_approx(l[v]);
     } else {
       m = -INFINITY;
 #pragma unroll
@@ -383,33 +389,61 @@ __global__ void __launch_bounds__(kScoredThreads) route_scored_kernel(ScoredPara
 #pragma unroll
       for (int v = 0; v < V; ++v) c[v] = ex[v] * inv;
     }
-    float best = -INFINITY;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      c[v] += b[v];
-      if (!(fabsf(l[v]) < INFINITY) || c[v] != c[v]) c[v] = -INFINITY;
+    for (int v = 0; v < V; ++v) c[v] = fabsf(l[v]) < INFINITY ? c[v] + b[v] : -INFINITY;
+
+    float best, second;
+    lane_top2<V>(c, best, second);
+    bool live = true;  // the lane's group is among the chosen
+    if (G > 1) {
+      bool sure = lane_groups;
+      if (lane_groups) {
+        float a1 = best, a2 = second;
+        for (int o = 1; o < span; o <<= 1) {
+          const float b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
+          merge_top2(a1, a2, b1, b2);
+        }
+        // every lane of a group holds the group's value
+        const float val = p.group_top == 2 && a2 > -INFINITY ? a1 + a2 : a1;
+        const float mine = my_group < G ? val : -INFINITY;
+        float rest = mine, cut = -INFINITY;
+        for (int r = 0; r < p.topk_groups; ++r) {
+          cut = redux_max(rest);
+          if (rest == cut) rest = -INFINITY;
+        }
+        const float next = redux_max(rest);
+        live = mine >= cut && mine > -INFINITY;
+        // no tie among the chosen values or at the cut: as many groups as asked
+        // (or all that have an expert), the next one clearly below
+        const int groups = __popc(__ballot_sync(kFull, live && (lane & (span - 1)) == 0));
+        sure = next == -INFINITY ? groups <= p.topk_groups
+                                 : groups == p.topk_groups &&
+                                       cut - next > 4.0f * eps + fabsf(next) * 0x1p-20f;
+      }
+      if (!sure) {
+        route_token_exact<V, BF16, SIGMOID>(p, t, vec);
+        continue;
+      }
     }
-    bool sure = true;
-    if (p.n_groups > 1) sure = limit_groups_approx<V>(p, c, e0, eps);
-    if (!sure) {
-      route_token_exact<V, BF16, SIGMOID>(p, t, vec);
-      continue;
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) best = fmaxf(best, c[v]);
     float bound = -INFINITY;
+    float rest = live ? best : -INFINITY;
     for (int r = 0; r < p.k; ++r) {
-      bound = redux_max(best);
-      if (best == bound) best = -INFINITY;
+      bound = redux_max(rest);
+      if (rest == bound) rest = -INFINITY;
     }
-    const float cut = bound - (2.0f * eps + fabsf(bound) * 0x1p-20f);  // -inf stays -inf
-    int n = 0;
+    // -FLT_MAX when fewer than k lanes have an expert: all of them are candidates
+    float cut = fmaxf(bound - (2.0f * eps + fabsf(bound) * 0x1p-20f), -3.4028234e38f);
+    if (bound == -INFINITY) cut = -3.4028234e38f;
+    if (!live) cut = INFINITY;
+    unsigned mine = 0u;  // the lane's candidates, one bit each
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const bool in = c[v] > -INFINITY && c[v] >= cut;
-      const unsigned who = __ballot_sync(kFull, in);
+    for (int v = 0; v < V; ++v)
+      if (c[v] >= cut) mine |= 1u << v;
+    int n = 0;
+    for (unsigned who = __ballot_sync(kFull, mine != 0u); who; who = __ballot_sync(kFull, mine != 0u)) {
       const int at = n + __popc(who & lanemask_lt());
-      if (in && at < 32) cand[warp][at] = make_float2(l[v], __int_as_float(e0 + v));
+      if (mine != 0u && at < 32) cand[warp][at].y = __int_as_float(e0 + __ffs(mine) - 1);
+      mine &= mine - 1u;
       n += __popc(who);
     }
     if (n > 32) {
@@ -417,34 +451,36 @@ __global__ void __launch_bounds__(kScoredThreads) route_scored_kernel(ScoredPara
       continue;
     }
     __syncwarp();
-    int id = -1;
+    int id = 0x7FFFFFFF;
     float s = 0.0f, x = -INFINITY;
     if (lane < n) {
-      const float2 q = cand[warp][lane];
-      id = __float_as_int(q.y);
-      s = SIGMOID ? sigmoid_f32(q.x) : __fdiv_rn(expf(__fsub_rn(q.x, m)), den);
+      id = __float_as_int(cand[warp][lane].y);
+      const float q = load_logit<BF16>(row, id);
+      s = SIGMOID ? sigmoid_f32(q) : __fdiv_rn(expf(__fsub_rn(q, m)), den);
       x = p.bias ? __fadd_rn(s, __ldg(p.bias + id)) : s;
-      cand[warp][lane] = make_float2(x, q.y);
     }
+    cand[warp][lane] = make_float2(x, __int_as_float(id));
     __syncwarp();
     int rank = lane < n ? 0 : 32;
-    for (int j = 0; j < n; ++j) {
-      const float2 q = cand[warp][j];
+    for (int j = 0; j < n; j += 2) {  // past the candidates: -inf, never ahead
+      const float4 q = *reinterpret_cast<const float4*>(&cand[warp][j]);
       rank += q.x > x || (q.x == x && __float_as_int(q.y) < id);
+      rank += q.z > x || (q.z == x && __float_as_int(q.w) < id);
     }
-    const int found = min(n, p.k);
-    float w = rank < p.k ? s : 0.0f;
+    const bool chosen = rank < p.k;
+    float w = chosen ? s : 0.0f;
     if (p.renorm) {
       const float tot = warp_sum(w);
       w = tot > 0.0f ? __fdiv_rn(w, tot) : 0.0f;
     }
-    if (rank < p.k) {
-      p.ids[t * p.kmax + rank] = id;
-      p.w[t * p.kmax + rank] = __fmul_rn(w, p.scale);
+    const int64_t out = t * p.kmax;
+    if (chosen) {
+      p.ids[out + rank] = id;
+      p.w[out + rank] = __fmul_rn(w, p.scale);
     }
-    if (lane >= found && lane < p.kmax) {
-      p.ids[t * p.kmax + lane] = -1;
-      p.w[t * p.kmax + lane] = 0.0f;
+    if (lane >= min(n, p.k) && lane < p.kmax) {
+      p.ids[out + lane] = -1;
+      p.w[out + lane] = 0.0f;
     }
     __syncwarp();
   }
