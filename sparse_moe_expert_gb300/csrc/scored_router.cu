@@ -103,7 +103,7 @@ __device__ __forceinline__ void load_logits(float (&l)[V], const void* row, int 
 }
 
 __device__ __forceinline__ float sigmoid_f32(float l) {
-  return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-l)));
+  return __frcp_rn(__fadd_rn(1.0f, expf(-l)));
 }
 
 // Pairwise sum over neighbouring experts, the same bits in every lane.
@@ -345,7 +345,8 @@ __device__ __forceinline__ void lane_top2(const float (&c)[V], float& a1, float&
 template <int V, bool BF16, bool SIGMOID>
 __global__ void __launch_bounds__(kScoredThreads, V <= 8 ? 4 : 2)
     route_scored_kernel(ScoredParams p, int vec) {
-  __shared__ __align__(16) float2 cand[kScoredWarps][32];
+  __shared__ __align__(16) int cand_id[kScoredWarps][32];
+  __shared__ __align__(16) float cand_x[kScoredWarps][32];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -407,6 +408,7 @@ __global__ void __launch_bounds__(kScoredThreads, V <= 8 ? 4 : 2)
         const float val = p.group_top == 2 && a2 > -INFINITY ? a1 + a2 : a1;
         const float mine = my_group < G ? val : -INFINITY;
         float rest = mine, cut = -INFINITY;
+#pragma unroll 4
         for (int r = 0; r < p.topk_groups; ++r) {
           cut = redux_max(rest);
           if (rest == cut) rest = -INFINITY;
@@ -427,6 +429,7 @@ __global__ void __launch_bounds__(kScoredThreads, V <= 8 ? 4 : 2)
     }
     float bound = -INFINITY;
     float rest = live ? best : -INFINITY;
+#pragma unroll 4
     for (int r = 0; r < p.k; ++r) {
       bound = redux_max(rest);
       if (rest == bound) rest = -INFINITY;
@@ -442,7 +445,7 @@ __global__ void __launch_bounds__(kScoredThreads, V <= 8 ? 4 : 2)
     int n = 0;
     for (unsigned who = __ballot_sync(kFull, mine != 0u); who; who = __ballot_sync(kFull, mine != 0u)) {
       const int at = n + __popc(who & lanemask_lt());
-      if (mine != 0u && at < 32) cand[warp][at].y = __int_as_float(e0 + __ffs(mine) - 1);
+      if (mine != 0u && at < 32) cand_id[warp][at] = e0 + __ffs(mine) - 1;
       mine &= mine - 1u;
       n += __popc(who);
     }
@@ -454,18 +457,27 @@ __global__ void __launch_bounds__(kScoredThreads, V <= 8 ? 4 : 2)
     int id = 0x7FFFFFFF;
     float s = 0.0f, x = -INFINITY;
     if (lane < n) {
-      id = __float_as_int(cand[warp][lane].y);
+      id = cand_id[warp][lane];
       const float q = load_logit<BF16>(row, id);
       s = SIGMOID ? sigmoid_f32(q) : __fdiv_rn(expf(__fsub_rn(q, m)), den);
       x = p.bias ? __fadd_rn(s, __ldg(p.bias + id)) : s;
     }
-    cand[warp][lane] = make_float2(x, __int_as_float(id));
+    cand_x[warp][lane] = x;
     __syncwarp();
-    int rank = lane < n ? 0 : 32;
-    for (int j = 0; j < n; j += 2) {  // past the candidates: -inf, never ahead
-      const float4 q = *reinterpret_cast<const float4*>(&cand[warp][j]);
-      rank += q.x > x || (q.x == x && __float_as_int(q.y) < id);
-      rank += q.z > x || (q.z == x && __float_as_int(q.w) < id);
+    int rank = 0;
+    for (int j = 0; j < n; j += 4) {  // past the candidates: -inf, never ahead
+      const float4 q = *reinterpret_cast<const float4*>(&cand_x[warp][j]);
+      rank += q.x > x;
+      rank += q.y > x;
+      rank += q.z > x;
+      rank += q.w > x;
+    }
+    if (lane >= n) rank = 32;
+    // distinct choices have the ranks 0 .. n - 1; equal ones go by id
+    const unsigned seen = __reduce_or_sync(kFull, lane < n ? 1u << rank : 0u);
+    if (__popc(seen) != n) {
+      for (int j = 0; j < n; ++j)
+        rank += cand_x[warp][j] == x && cand_id[warp][j] < id;
     }
     const bool chosen = rank < p.k;
     float w = chosen ? s : 0.0f;
