@@ -516,6 +516,42 @@ struct ScoredGradParams {
   unsigned int* err;
 };
 
+// Four sums over the warp at once, every lane with all four: at the first two
+// steps a lane keeps half of the values that it holds and sends the rest, so
+// nine shuffles instead of twenty.
+__device__ __forceinline__ void warp_sum4(float& a, float& b, float& c, float& d) {
+  const int lane = threadIdx.x & 31;
+  const bool h16 = (lane & 16) != 0, h8 = (lane & 8) != 0;
+  float x = h16 ? c : a, y = h16 ? d : b;
+  x += __shfl_xor_sync(kFull, h16 ? a : c, 16);
+  y += __shfl_xor_sync(kFull, h16 ? b : d, 16);
+  float z = h8 ? y : x;
+  z += __shfl_xor_sync(kFull, h8 ? x : y, 8);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
+  a = __shfl_sync(kFull, z, 0);
+  b = __shfl_sync(kFull, z, 8);
+  c = __shfl_sync(kFull, z, 16);
+  d = __shfl_sync(kFull, z, 24);
+}
+
+__device__ __forceinline__ float exp_approx(float x) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(1.4426950408889634f * x));
+  return e;
+}
+
+// One token per warp and step, its V experts per lane in registers.  With
+// u_e = exp(l_e - max) or the sigmoid, U its sum, c_e = d balance / d q_e:
+//   slots    r = sum dw u / sum u over the chosen, d u_j = (dw_j - r) U / sum u
+//            (renormalized; scale-free, so the softmax needs no division), or dw_j
+//   softmax  d l = s (d u + c - sum c s - [sum dw s when not renormalized])
+//   sigmoid  d l = s (1 - s) (d u + (c - sum c s / U) / U)
+//   z        d l += 2 z / T lse softmax(l)
+// so one joint reduction of four sums (and the z loss's fifth) serves all of
+// it.  The hardware exponential and reciprocal are good to a few 1e-7 here,
+// far inside the rounding of the differences they enter.  The chosen slots'
+// d u meets its expert's lane through a row of shared memory per warp.
 template <int V, bool BF16, bool SIGMOID>
 __global__ void __launch_bounds__(kScoredThreads) route_scored_backward_kernel(ScoredGradParams p,
                                                                                int vec) {
@@ -536,101 +572,97 @@ __global__ void __launch_bounds__(kScoredThreads) route_scored_backward_kernel(S
     qsum[v] = 0.0f;
     buf[e0 + v] = 0.0f;
   }
+  const bool need_z = p.z != 0.0f;
+  const float zt = 2.0f * p.z / (float)p.T;
   float lse2 = 0.0f;
   bool bad = false;
   __syncwarp();
   for (int64_t t = (int64_t)blockIdx.x * kScoredWarps + warp; t < p.T;
        t += (int64_t)gridDim.x * kScoredWarps) {
-    float l[V], s[V];
     const char* row = static_cast<const char*>(p.logits) + t * p.ld * (BF16 ? 2 : 4);
-    load_logits<V, BF16>(l, row, e0, p.E, vec != 0);
     int id = -1;
     float dw = 0.0f;
-    if (p.d_w && lane < p.kmax && lane < p.k) {
+    if (p.d_w && lane < p.k) {
       id = __ldg(p.ids + t * p.kmax + lane);
-      dw = __ldg(p.d_w + t * p.kmax + lane);
-      if (id >= p.E) {
-        bad = true;
-        id = -1;
-      }
+      dw = __ldg(p.d_w + t * p.kmax + lane) * p.scale;
     }
-    bool on[V];
+    float l[V];
+    load_logits<V, BF16>(l, row, e0, p.E, vec != 0);
+    if (id >= p.E) {
+      bad = true;
+      id = -1;
+    }
+    float lj = id >= 0 ? load_logit<BF16>(row, id) : -INFINITY;
+    if (!(lj < INFINITY)) lj = -INFINITY;
+    if (id < 0) dw = 0.0f;
     float m = -INFINITY;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      on[v] = fabsf(l[v]) < INFINITY;
-      if (on[v]) m = fmaxf(m, l[v]);
+      l[v] = l[v] < INFINITY ? l[v] : -INFINITY;  // NaN and +inf: unavailable
+      m = fmaxf(m, l[v]);
     }
-    // softmax terms: the scores themselves, or (sigmoid) only for the z loss
-    float esum = 0.0f, lse = 0.0f;
-    float ex[V];
-    const bool need_softmax = !SIGMOID || p.z != 0.0f;
-    if (need_softmax) {
-      m = warp_max(m);
-      float es = 0.0f;
+    m = redux_max(m);
+    const bool some = m > -INFINITY;
+    if (!some) m = 0.0f;  // every exponential is 0
+    float u[V], ex[SIGMOID ? V : 1];
+    float su = 0.0f, sc = 0.0f, ez = 0.0f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        ex[v] = on[v] ? expf(l[v] - m) : 0.0f;
-        es += ex[v];
-      }
-      esum = warp_sum(es);
-      if (esum > 0.0f) lse = m + logf(esum);
+    for (int v = 0; v < V; ++v) {
+      u[v] = SIGMOID ? sigmoid_approx(l[v]) : exp_approx(l[v] - m);
+      su += u[v];
+      sc = fmaf(coef[v], u[v], sc);
     }
-    const float einv = esum > 0.0f ? 1.0f / esum : 0.0f;
-    float total = 1.0f;
     if constexpr (SIGMOID) {
-      float ss = 0.0f;
+      if (need_z) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        s[v] = on[v] ? sigmoid_f32(l[v]) : 0.0f;
-        ss += s[v];
+        for (int v = 0; v < V; ++v) {
+          ex[v] = exp_approx(l[v] - m);
+          ez += ex[v];
+        }
+        ez = warp_sum(ez);
       }
-      total = warp_sum(ss);
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v) s[v] = ex[v] * einv;
     }
-    const float tinv = total > 0.0f ? 1.0f / total : 0.0f;
-    // the chosen slots: score of the slot's expert, then d score
-    float ps = 0.0f;
-    if (id >= 0) {
-      const float lj = load_logit<BF16>(row, id);
-      if (fabsf(lj) < INFINITY) ps = SIGMOID ? sigmoid_f32(lj) : expf(lj - m) * einv;
-    }
-    dw *= p.scale;
-    if (id < 0) dw = 0.0f;
-    float dp = dw;
+    const float uj = SIGMOID ? sigmoid_approx(lj) : exp_approx(lj - m);  // 0 without a slot
+    float st = uj, sd = dw * uj;
+    warp_sum4(su, sc, st, sd);
+    if constexpr (!SIGMOID) ez = su;
+    const float uinv = su > 0.0f ? __fdividef(1.0f, su) : 0.0f;
+    // q = u uinv for both scores (the softmax's U makes u its unnormalised s)
+    float dp;
     if (p.renorm) {
-      const float tot = warp_sum(ps), dot = warp_sum(dw * ps);
-      dp = tot > 0.0f && id >= 0 ? (dw - dot / tot) / tot : 0.0f;
+      const float r = __fdividef(sd, st);
+      dp = st > 0.0f && id >= 0 ? __fdividef((dw - r) * (SIGMOID ? 1.0f : su), st) : 0.0f;
+    } else {
+      dp = dw;
     }
     if (id >= 0) buf[id] = dp;
-    float dots = 0.0f;
-    if constexpr (!SIGMOID) dots = p.renorm ? 0.0f : warp_sum(dp * ps);
-    __syncwarp();
-    float dotq = 0.0f;
-    if (p.counts) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float q = SIGMOID ? s[v] * tinv : s[v];
-        dotq = fmaf(coef[v], q, dotq);
-        qsum[v] += q;
-      }
-      dotq = warp_sum(dotq);
+    const float zc = need_z && some ? zt * (m + __logf(ez)) * __fdividef(1.0f, ez) : 0.0f;
+    if (need_z && some) {
+      const float lse = m + __logf(ez);
+      lse2 = fmaf(lse, lse, lse2);
     }
-    const float zc = 2.0f * p.z / (float)p.T * lse * einv;
-    if (lane == 0) lse2 = fmaf(lse, lse, lse2);
+    // what is the same for all of the token's experts: sum c q, and the
+    // softmax's sum of d u s when the weights are not renormalized
+    const float dotq = sc * uinv;
+    const float off = SIGMOID || p.renorm ? dotq : fmaf(sd, uinv, dotq);
+    __syncwarp();
     float d[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float ds = buf[e0 + v] + (SIGMOID ? (coef[v] - dotq) * tinv : coef[v] - dotq);
-      d[v] = SIGMOID ? ds * s[v] * (1.0f - s[v]) : s[v] * (ds - dots);
-      if (need_softmax) d[v] = fmaf(zc, ex[v], d[v]);
-      d[v] = on[v] ? d[v] : 0.0f;
+      const float s = SIGMOID ? u[v] : u[v] * uinv;
+      const float own = buf[e0 + v];
+      if constexpr (SIGMOID) {
+        const float ds = fmaf(coef[v] - off, uinv, own);
+        d[v] = ds * (s - s * s);
+        if (need_z) d[v] = fmaf(zc, ex[v], d[v]);
+        qsum[v] = fmaf(u[v], uinv, qsum[v]);
+      } else {
+        d[v] = fmaf(zc, u[v], s * (own + (coef[v] - off)));
+        qsum[v] += s;
+      }
     }
     __syncwarp();
     if (id >= 0) buf[id] = 0.0f;
-    __syncwarp();
     char* out = static_cast<char*>(p.d_logits) + t * p.ld_out * (BF16 ? 2 : 4);
     if constexpr (BF16) {
       if (vec && V >= 2) {
@@ -648,23 +680,24 @@ __global__ void __launch_bounds__(kScoredThreads) route_scored_backward_kernel(S
 #pragma unroll
           for (int v = 0; v < V / 2; ++v) o[v] = w2[v];
         }
-        continue;
-      }
+      } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (e0 + v < p.E) reinterpret_cast<uint16_t*>(out)[e0 + v] = f32_to_bf16_rne(d[v]);
+        for (int v = 0; v < V; ++v)
+          if (e0 + v < p.E) reinterpret_cast<uint16_t*>(out)[e0 + v] = f32_to_bf16_rne(d[v]);
+      }
     } else {
       if (vec && V >= 4) {
 #pragma unroll
         for (int i = 0; i < V / 4; ++i)
           reinterpret_cast<float4*>(out)[e0 / 4 + i] =
               make_float4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
-        continue;
-      }
+      } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (e0 + v < p.E) reinterpret_cast<float*>(out)[e0 + v] = d[v];
+        for (int v = 0; v < V; ++v)
+          if (e0 + v < p.E) reinterpret_cast<float*>(out)[e0 + v] = d[v];
+      }
     }
+    __syncwarp();
   }
   if (bad) raise_device_error(p.err, MOE_DEVERR_BAD_EXPERT);
   // the block's sums, warps in order
@@ -680,37 +713,67 @@ __global__ void __launch_bounds__(kScoredThreads) route_scored_backward_kernel(S
   }
 }
 
-// losses[0] = balance E / (k T) sum_e counts_e mean_t q_te, losses[1] = z mean lse^2:
-// the blocks' sums in block order, then a tree over the experts.
+// losses[0] = balance E / (k T) sum_e counts_e mean_t q_te, losses[1] = z mean lse^2.
+// A cluster of 8 CTAs shares the columns of the partial sums: lane = column,
+// the warps take the blocks in turn, and the leader adds the CTAs' parts in
+// rank order, so the sums always run in one order.
 constexpr int kLossThreads = 1024;
-__global__ void __launch_bounds__(kLossThreads) route_losses_kernel(ScoredGradParams p, int blocks,
-                                                                    float* losses) {
-  __shared__ float part[kLossThreads / 32];
-  __shared__ float zsum;
+constexpr int kLossCluster = 8;
+__global__ void __cluster_dims__(kLossCluster, 1, 1) __launch_bounds__(kLossThreads)
+    route_losses_kernel(ScoredGradParams p, int blocks, float* losses) {
+  __shared__ float part[kLossThreads / 32][33];
+  __shared__ float joined[kLossCluster][2];
   pdl_wait();
   pdl_trigger();
-  const int e = threadIdx.x;
-  float term = 0.0f;
-  for (int x = e; x <= p.E; x += kLossThreads) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float bal = 0.0f, zsum = 0.0f;  // warp 0
+  for (int x0 = blockIdx.x * 32; x0 <= p.E; x0 += kLossCluster * 32) {
+    const int x = x0 + lane;
     float a = 0.0f;
-    for (int b = 0; b < blocks; ++b) a += p.part[(int64_t)b * (p.E + 1) + x];
-    if (x == p.E) zsum = a;
-    else if (p.counts) term += a * (float)p.counts[x];
-  }
-  term = warp_sum(term);
-  if ((e & 31) == 0) part[e >> 5] = term;
-  __syncthreads();
-  if (e < 32) {
-    const float s = warp_sum(part[e]);
-    if (e == 0) {
-      const float T = (float)p.T;
-      losses[0] = p.balance * ((float)p.E / ((float)p.k * T)) * (s / T);
-      losses[1] = p.z * (zsum / T);
+    if (x <= p.E) {
+#pragma unroll 4
+      for (int b = warp; b < blocks; b += kLossThreads / 32)
+        a += p.part[(int64_t)b * (p.E + 1) + x];
     }
+    part[warp][lane] = a;
+    __syncthreads();
+    if (warp == 0) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kLossThreads / 32; ++w) s += part[w][lane];
+      if (x < p.E && p.counts) bal += s * (float)__ldg(p.counts + x);
+      if (x == p.E) zsum = s;
+    }
+    __syncthreads();
+  }
+  if (warp == 0) {
+    bal = warp_sum(bal);
+    zsum = warp_sum(zsum);
+    if (lane == 0) {
+      // into the leader's shared memory
+      uint32_t at;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, 0;"
+                   : "=r"(at)
+                   : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(&joined[blockIdx.x][0]))));
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(bal) : "memory");
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 4), "f"(zsum) : "memory");
+    }
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    float s = 0.0f, z = 0.0f;
+    for (int r = 0; r < kLossCluster; ++r) {
+      s += joined[r][0];
+      z += joined[r][1];
+    }
+    const float T = (float)p.T;
+    losses[0] = p.balance * ((float)p.E / ((float)p.k * T)) * (s / T);
+    losses[1] = p.z * (z / T);
   }
 }
 
-constexpr int kGradMaxBlocks = 1024;
+constexpr int kGradMaxBlocks = 1024;  // rows of partial sums the workspace holds
 
 int lane_values(int E) {
   int v = 1;
@@ -870,11 +933,13 @@ extern "C" moe_status_t moe_route_scored_backward(
   p.err = device_error_word();
   const int V = lane_values(E);
   int grid = scored_grid(T);
+  // few enough blocks that joining their sums stays short
+  if (grid > 4 * sm_count()) grid = 4 * sm_count();
   if (grid > kGradMaxBlocks) grid = kGradMaxBlocks;
   const bool vec = can_vector(logits, ld, E, V, size) && can_vector(d_logits, ld_out, E, V, size);
   const moe_status_t s =
       dispatch_scored<BackwardLaunch>(V, logits_dtype == MOE_DTYPE_BF16,
                                       score == MOE_SCORE_SIGMOID, p, grid, (int)vec, st);
   if (s != MOE_OK) return s;
-  return launch(route_losses_kernel, 1, kLossThreads, 0, st, p, grid, losses);
+  return launch(route_losses_kernel, kLossCluster, kLossThreads, 0, st, p, grid, losses);
 }
