@@ -18,7 +18,7 @@ constexpr int kCgThreads = 256;
 constexpr int kCgWarps = kCgThreads / 32;
 constexpr int kCgSlots = 8;  // slots in flight; kmax > 8 takes two passes over d_out
 constexpr int kCgMaxSlots = 16;
-constexpr int kCgCtas = 4;  // resident per SM
+constexpr int kCgCtas = 3;  // resident per SM
 
 struct CombineGradParams {
   const uint16_t* d_out;

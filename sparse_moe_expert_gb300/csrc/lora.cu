@@ -220,18 +220,17 @@ bool lora_groups(int64_t rows, int E, int n_adapters) {
          n_adapters <= kLoraPlanAdapters;
 }
 
-// K ranges of the grouped shrink: enough (tile, range) units for two CTAs per
-// SM when the tiles alone are too few, at least four k-blocks of 64 each.
+// CTAs per tile in the grouped shrink: enough for two per SM when the tiles
+// alone are too few, with at least four k-blocks of 64 each.
 int lora_splits(int64_t rows, int K) {
   const int64_t tiles = (rows + kLoraTileRows - 1) / kLoraTileRows;
-  int64_t s = (2 * 148 + tiles - 1) / tiles;
-  if (s > K / 256) s = K / 256;
-  if (s > kLoraMaxSplit) s = kLoraMaxSplit;
-  return s < 1 ? 1 : (int)s;
+  int s = 1;
+  while (s < kLoraMaxSplit && 2 * s * tiles <= 2 * moe_host::sm_count() && 2 * s * 256 <= K) s *= 2;
+  return s;
 }
 
 struct LoraSpace {
-  size_t v, perm, tiles, total;
+  size_t rows, tiles, total;  // v comes first
 };
 
 LoraSpace lora_space(int64_t rows, int E, int n_adapters, int R) {
@@ -242,8 +241,8 @@ LoraSpace lora_space(int64_t rows, int E, int n_adapters, int R) {
     s.total = one;
     return s;
   }
-  s.perm = up(one * lora_splits(rows, 1 << 20));
-  s.tiles = s.perm + up((size_t)rows * sizeof(int32_t));
+  s.rows = up((size_t)rows * kLoraMaxTerms * rank_pad(R) * sizeof(uint16_t));
+  s.tiles = s.rows + up((size_t)rows * sizeof(int2));
   s.total = s.tiles + (size_t)(1 + lora_tile_capacity(rows, E, n_adapters)) * sizeof(int4);
   return s;
 }
@@ -314,9 +313,14 @@ extern "C" moe_status_t moe_lora_apply(const uint16_t* x, int x_by_token,
   if (lora_groups(rows, E, n_adapters)) {
     const LoraSpace sp = lora_space(rows, E, n_adapters, R);
     char* ws = static_cast<char*>(workspace);
-    const LoraPlan plan{reinterpret_cast<int32_t*>(ws + sp.perm),
-                        reinterpret_cast<int4*>(ws + sp.tiles), lora_splits(rows, K),
-                        !swiglu && base == out, lora_tile_capacity(rows, E, n_adapters)};
+    int4* tiles = reinterpret_cast<int4*>(ws + sp.tiles);
+    const LoraPlan plan{reinterpret_cast<int2*>(ws + sp.rows),
+                        tiles,
+                        tiles + 1,
+                        lora_tile_capacity(rows, E, n_adapters),
+                        lora_splits(rows, K),
+                        static_cast<uint16_t*>(workspace),
+                        !swiglu && base == out};
     return lora_grouped(p, plan, rows, swiglu, out_dtype == MOE_DTYPE_BF16, st);
   }
   moe_status_t s;

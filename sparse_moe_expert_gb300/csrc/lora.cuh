@@ -6,6 +6,8 @@
 namespace moe {
 
 constexpr int kMaxRank = 128;
+__host__ __device__ constexpr int rank_pad(int R) { return (R + 15) / 16 * 16; }
+constexpr int kLoraMaxTerms = 3;
 
 struct LoraParams {
   const uint16_t* x;
@@ -59,25 +61,36 @@ __device__ __forceinline__ LoraRow lora_row(const LoraParams& p, int r) {
   return row;
 }
 
+// Which row of x a row uses (the row's slot is known).
+__device__ __forceinline__ int lora_x_row(const LoraParams& p, int r) {
+  return p.sorted && p.x_by_token ? __ldg(p.sorted + r) / p.kmax : r;
+}
+
 // Rows grouped by the matrices they use, made on the device for one call.
-// perm[pos] = row; a tile is up to kLoraTileRows consecutive positions of one
-// slot: tiles[1 + i] = (slot or -1, first position, rows, 0); tiles[0].x is
-// their count.
+// rows[pos] = (row, row of x).  A tile is a run of positions of one slot:
+// (slot or -1, first position, rows, 0).  Large tiles (up to 128 rows) fill
+// the list from the front, small ones (up to 16) from the back; counts[0] =
+// (large, small, 0, 0).
 constexpr int kLoraTileRows = 128;
-constexpr int kLoraMaxSplit = 8;  // K ranges of the grouped shrink
+constexpr int kLoraSmallRows = 16;
+constexpr int kLoraSmallMost = 48;  // a rest of at most this many rows takes small tiles
+constexpr int kLoraMaxSplit = 8;    // CTAs that share a tile's K in the grouped shrink
 struct LoraPlan {
-  int32_t* perm;
+  int2* rows;
+  int4* counts;
   int4* tiles;
-  int splits;     // K ranges; v holds one [rows, R] partial sum per range
-  int skip_none;  // rows without an adapter need no work
   int64_t capacity;  // tiles the list holds
+  int splits;        // CTAs (a cluster) that share a tile's K: 1, 2, 4 or 8
+  uint16_t* terms;   // v as bf16 terms side by side: [rows][terms * padded rank]
+  int skip_none;     // rows without an adapter need no work
 };
 
 // Most adapters the grouping's counters hold in shared memory.
 constexpr int kLoraPlanAdapters = 4096;
 
 inline int64_t lora_tile_capacity(int64_t rows, int E, int n_adapters) {
-  const int64_t most = rows / kLoraTileRows + (int64_t)E * (n_adapters + 1);
+  const int64_t most =
+      rows / kLoraTileRows + (int64_t)(kLoraSmallMost / kLoraSmallRows) * E * (n_adapters + 1);
   return rows < most ? rows : most;
 }
 

@@ -1,19 +1,23 @@
 // Adapters of many rows: the grouped form of moe_lora_apply (lora.cu has the
 // formula and the form for few rows).
 //
-// Rows are grouped by the matrices they use (lora_plan_kernel), so that a
-// tile of up to 128 rows meets one pair A, B on the tensor cores (tcgen05,
-// accumulators in TMEM):
-//   shrink: D[row, j]  = sum_k x[row, k] A[j, k]; M = 128 rows, N = the rank,
-//           a unit is one tile and one range of K (partial sums, added in
-//           range order by the expand, keep the result reproducible);
-//   expand: D[row, n]  = sum_j v[row, j] B[n, j]; 128 rows x 128 columns, v as
+// Rows are grouped by the matrices they use (lora_plan_kernel).  A tile of up
+// to 128 rows meets one pair A, B on the tensor cores (tcgen05, accumulators
+// in TMEM):
+//   shrink: D[row, j]  = sum_k x[row, k] A[j, k]; M = 128 rows, N = the rank;
+//           when tiles are few, a cluster of 2 to 8 CTAs shares a tile's K and
+//           joins the sums through distributed shared memory in rank order;
+//   expand: D[row, n]  = sum_j v[row, j] B[n, j]; 128 rows x 64 columns, v as
 //           two or three bf16 terms side by side along the contraction, so
 //           that the fp32 value enters to 2^-17 (bf16 base) or 2^-26 (fp32 base,
 //           whose bf16 and fp32 activations are then the same numbers).
 // Both stream x, base and out once; the tensor cores take the operands from
 // shared memory, so the load/store path carries little else (with mma.sync
 // the fragments of v and B would cost it more than base and out together).
+// What is left of an adapter's rows after whole tiles, 48 at most, goes in
+// tiles of up to 16 rows through mma.sync with operands straight from global
+// memory: there A and B are the bulk of the bytes, each read once per tile,
+// and a 128-row accumulator would leave three of four warps without rows.
 #include "async.cuh"
 #include "lora.cuh"
 #include "tc.cuh"
@@ -23,77 +27,108 @@ namespace {
 
 // ---- grouping --------------------------------------------------------------
 
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanUnroll = 4;
+constexpr int kPlanThreads = 256;
+constexpr int kPlanUnroll = 8;
 
-// CTA (e, c): counts the rows of expert e per adapter (the last bin: none),
-// the ones before its range c separately, and places its range; range 0 also
-// lists the expert's tiles.  The order of rows within an
-// adapter is left open (shared-memory atomics): a row's result does not
-// depend on its place in a tile.
+// Tiles of an adapter's n rows.
+__device__ __forceinline__ int2 tiles_of(int n) {
+  const int rest = n % kLoraTileRows;
+  const bool small = rest <= kLoraSmallMost;
+  return make_int2(n / kLoraTileRows + (small ? 0 : 1),
+                   small ? (rest + kLoraSmallRows - 1) / kLoraSmallRows : 0);
+}
+
+__device__ __forceinline__ int warp_scan_incl(int v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += y;
+  }
+  return v;
+}
+
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
+// A cluster per expert e: CTA c of it counts its range of the expert's rows
+// per adapter (the last bin: none), learns the other ranges' counts through
+// distributed shared memory and places its rows; the first CTA also lists the
+// expert's tiles.  Rows of an adapter stay in order, so that every row meets
+// the same tile, and the same sums, each time; the order of the experts'
+// tiles is left open.
 __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(LoraParams p, LoraPlan pl) {
   extern __shared__ int plan_s[];
   pdl_wait();
   pdl_trigger();
   const int bins = p.n_adapters + 1;
-  int* cnt = plan_s;
+  int* own = plan_s;
+  int* cnt = own + bins;
   int* cursor = cnt + bins;
   int* start = cursor + bins;
-  __shared__ int tile_base;
   const int tid = threadIdx.x, lane = tid & 31;
   const int e = blockIdx.x, rows = lora_rows(p);
+  const int ranges = gridDim.y, range = blockIdx.y;  // the cluster's size, the rank in it
   const int lo = p.sorted ? min(max(__ldg(p.offsets + e), 0), rows) : 0;
   const int n = (p.sorted ? min(max(__ldg(p.offsets + e + 1), lo), rows) : rows) - lo;
-  // ranges of whole kPlanThreads rows
-  const int64_t step = (int64_t)gridDim.y * kPlanThreads;
-  const int64_t per = (n + step - 1) / step * kPlanThreads;
-  if (per * blockIdx.y >= n) return;
-  const int c0 = (int)(per * blockIdx.y), c1 = (int)(c0 + per < n ? c0 + per : n);
-  for (int i = tid; i < bins; i += kPlanThreads) cnt[i] = cursor[i] = 0;
+  if (n <= 0) {  // for the whole cluster alike
+    if (p.E == 1 && range == 0 && tid == 0) *pl.counts = make_int4(0, 0, 0, 0);
+    return;
+  }
+  const int64_t per = ((int64_t)n + ranges - 1) / ranges;
+  const int c0 = (int)(per * range < n ? per * range : n);
+  const int c1 = (int)(c0 + per < n ? c0 + per : n);
+  for (int i = tid; i < bins; i += kPlanThreads) own[i] = 0;
   __syncthreads();
   auto bin_of = [&](int i) {
     const int s = lora_row(p, lo + i).slot;
-    return s < 0 ? p.n_adapters : s / p.E;
+    return s < 0 ? p.n_adapters : p.E == 1 ? s : s / p.E;
   };
-  for (int i0 = 0; i0 < n; i0 += kPlanThreads * kPlanUnroll) {
+  for (int i0 = c0; i0 < c1; i0 += kPlanThreads * kPlanUnroll) {
     int b[kPlanUnroll];
 #pragma unroll
     for (int u = 0; u < kPlanUnroll; ++u) {
       const int i = i0 + u * kPlanThreads + tid;
-      b[u] = i < n ? bin_of(i) : -1;
+      b[u] = i < c1 ? bin_of(i) : -1;
     }
 #pragma unroll
-    for (int u = 0; u < kPlanUnroll; ++u) {
-      const int i = i0 + u * kPlanThreads + tid;
-      const unsigned same = __match_any_sync(0xFFFFFFFFu, b[u]);
-      if (b[u] >= 0 && (same & lanemask_lt()) == 0u) {
-        atomicAdd(&cnt[b[u]], __popc(same));
-        if (i < c0) atomicAdd(&cursor[b[u]], __popc(same));  // c0 is a multiple of 32
-      }
-    }
+    for (int u = 0; u < kPlanUnroll; ++u)
+      if (b[u] >= 0) atomicAdd(&own[b[u]], 1);
   }
   __syncthreads();
+  if (ranges > 1) cluster_barrier();
+  for (int x = tid; x < bins; x += kPlanThreads) {
+    int total = 0, before = 0;
+    for (int r = 0; r < ranges; ++r) {
+      int v = own[x];
+      if (r != range)
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(own + x, r)));
+      total += v;
+      if (r < range) before += v;
+    }
+    cnt[x] = total;
+    cursor[x] = before;
+  }
+  __syncthreads();
+  if (ranges > 1) cluster_barrier();  // nobody's counts are needed any more
   if (tid < 32) {
-    int carry = 0, tiles = 0;
+    int carry = 0;
     for (int x0 = 0; x0 < bins; x0 += 32) {
       const int x = x0 + lane;
       const int v = x < bins ? cnt[x] : 0;
-      int incl = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o) incl += y;
-      }
+      const int incl = warp_scan_incl(v);
       if (x < bins) {
         start[x] = carry + incl - v;
         cursor[x] += carry + incl - v;
-        if (x < p.n_adapters || !pl.skip_none) tiles += (v + kLoraTileRows - 1) / kLoraTileRows;
       }
       carry += __shfl_sync(0xFFFFFFFFu, incl, 31);
-    }
-    if (c0 == 0) {
-      tiles = __reduce_add_sync(0xFFFFFFFFu, tiles);
-      if (lane == 0) tile_base = atomicAdd(&pl.tiles[0].x, tiles);
     }
   }
   __syncthreads();
@@ -101,40 +136,70 @@ __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(LoraParams p, L
     const int i = i0 + tid;
     const int b = i < c1 ? bin_of(i) : -1;
     const unsigned same = __match_any_sync(0xFFFFFFFFu, b);
+    const int before = __popc(same & lanemask_lt());
     int at = 0;
-    if (b >= 0 && (same & lanemask_lt()) == 0u) at = atomicAdd(&cursor[b], __popc(same));
-    at = __shfl_sync(0xFFFFFFFFu, at, __ffs(same) - 1);
-    if (b >= 0) pl.perm[lo + at + __popc(same & lanemask_lt())] = lo + i;
-  }
-  if (c0 == 0 && tid < 32) {
-    int carry = tile_base;
-    for (int x0 = 0; x0 < bins; x0 += 32) {
-      const int x = x0 + lane;
-      const int v = x < bins && (x < p.n_adapters || !pl.skip_none) ? cnt[x] : 0;
-      const int tiles = (v + kLoraTileRows - 1) / kLoraTileRows;
-      int incl = tiles;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o) incl += y;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {  // the warps in turn
+      if (tid >> 5 == w && b >= 0 && before == 0) {
+        at = cursor[b];
+        cursor[b] = at + __popc(same);
       }
-      const int slot = x < p.n_adapters ? x * p.E + e : -1;
-      for (int j = 0; j < tiles; ++j) {
-        const int64_t at = (int64_t)carry + incl - tiles + j;
-        if (at < pl.capacity)  // always, when the offsets are a prefix sum
-          pl.tiles[1 + at] = make_int4(slot, lo + start[x] + j * kLoraTileRows,
-                                       min(kLoraTileRows, v - j * kLoraTileRows), 0);
-        else
-          raise_device_error(p.err, MOE_DEVERR_BAD_INDEX);
-      }
-      carry += __shfl_sync(0xFFFFFFFFu, incl, 31);
+      __syncthreads();
     }
+    at = __shfl_sync(0xFFFFFFFFu, at, __ffs(same) - 1) + before;
+    if (b >= 0) pl.rows[lo + at] = make_int2(lo + i, lora_x_row(p, lo + i));
+  }
+  if (range != 0 || tid >= 32) return;
+  // the tiles, one warp: their number first, then a scan over the adapters
+  auto tiles_in = [&](int x) {
+    if (x >= bins || (x == p.n_adapters && pl.skip_none)) return make_int2(0, 0);
+    // rows without an adapter are copied, which large tiles do as well
+    if (x == p.n_adapters) return make_int2((cnt[x] + kLoraTileRows - 1) / kLoraTileRows, 0);
+    return tiles_of(cnt[x]);
+  };
+  int2 total = make_int2(0, 0), base = make_int2(0, 0);
+  for (int x0 = 0; x0 < bins; x0 += 32) {
+    const int2 k = tiles_in(x0 + lane);
+    total.x += __reduce_add_sync(0xFFFFFFFFu, k.x);
+    total.y += __reduce_add_sync(0xFFFFFFFFu, k.y);
+  }
+  if (lane == 0) {
+    if (p.E == 1) {
+      *pl.counts = make_int4(total.x, total.y, 0, 0);
+    } else {
+      base.x = atomicAdd(&pl.counts->x, total.x);
+      base.y = atomicAdd(&pl.counts->y, total.y);
+    }
+  }
+  base.x = __shfl_sync(0xFFFFFFFFu, base.x, 0);
+  base.y = __shfl_sync(0xFFFFFFFFu, base.y, 0);
+  auto put = [&](int64_t at, int slot, int first, int num) {
+    if (at >= 0 && at < pl.capacity)  // always, when the offsets are a prefix sum
+      pl.tiles[at] = make_int4(slot, first, num, 0);
+    else
+      raise_device_error(p.err, MOE_DEVERR_BAD_INDEX);
+  };
+  for (int x0 = 0; x0 < bins; x0 += 32) {
+    const int x = x0 + lane;
+    const int2 k = tiles_in(x);
+    const int ix = warp_scan_incl(k.x), iy = warp_scan_incl(k.y);
+    if (x < bins) {
+      const int slot = x < p.n_adapters ? x * p.E + e : -1;
+      const int first = lo + start[x], v = cnt[x];
+      for (int j = 0; j < k.x; ++j)
+        put((int64_t)base.x + ix - k.x + j, slot, first + j * kLoraTileRows,
+            min(kLoraTileRows, v - j * kLoraTileRows));
+      const int done = k.x * kLoraTileRows;
+      for (int j = 0; j < k.y; ++j)
+        put(pl.capacity - 1 - ((int64_t)base.y + iy - k.y + j), slot,
+            first + done + j * kLoraSmallRows, min(kLoraSmallRows, v - done - j * kLoraSmallRows));
+    }
+    base.x += __shfl_sync(0xFFFFFFFFu, ix, 31);
+    base.y += __shfl_sync(0xFFFFFFFFu, iy, 31);
   }
 }
 
 // ---- shared by the two products ---------------------------------------------
 
-constexpr int kTcThreads = 256;
 constexpr int kBlockBytes = 16384;  // 128 rows x 128 bytes, 128-byte swizzled
 
 // 16 bytes global -> shared; `on` false writes zeros.
@@ -169,25 +234,90 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
 // their loop together.
 __device__ __forceinline__ void wait_or_flag(uint64_t* bar, uint32_t parity, int& bad,
                                              unsigned int* err) {
-  if (!mbar_wait_sleep(bar, parity, kWaitBudgetCycles)) {
+  if (!bad && !mbar_wait_sleep(bar, parity, kWaitBudgetCycles)) {
     bad = 1;
     raise_device_error(err, MOE_DEVERR_TIMEOUT);
   }
 }
 
-__device__ __forceinline__ int lora_tiles(const LoraPlan& pl) {
-  return (int)min((int64_t)pl.tiles[0].x, pl.capacity);
+// (large, small) tiles; never more than the list holds.
+__device__ __forceinline__ int2 lora_tiles(const LoraPlan& pl) {
+  const int4 c = *pl.counts;
+  const int large = (int)min((int64_t)max(c.x, 0), pl.capacity);
+  return make_int2(large, (int)min((int64_t)max(c.y, 0), pl.capacity - large));
 }
 
-__host__ __device__ constexpr int rank_pad(int R) { return (R + 15) / 16 * 16; }
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 
 // ---- shrink ----------------------------------------------------------------
 
+constexpr int kShrinkThreads = 256;
+constexpr int kShrinkWarps = kShrinkThreads / 32;
 constexpr int kShrinkStages = 4;
 
-__global__ void __launch_bounds__(kTcThreads) lora_shrink_tc_kernel(LoraParams p, LoraPlan pl,
-                                                                   int64_t rows_cap,
-                                                                   uint32_t tmem_cols) {
+// A tile of up to 16 rows, k in [k0, k1): the warps take blocks of 32 k in
+// turn, fragments straight from global memory (lane t of a quad holds 8
+// consecutive k of its row), their sums added in warp order.  NT: eights of
+// the rank (rounded up).
+template <int NT>
+__device__ __forceinline__ void shrink_small(const LoraParams& p, const LoraPlan& pl, int4 tile,
+                                             int k0, int k1, float* part, int pitch, float* red) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int nt = p.R >> 3;
+  const bool on0 = g < tile.z, on1 = g + 8 < tile.z;
+  const uint4* x0 = reinterpret_cast<const uint4*>(
+      p.x + (int64_t)(on0 ? pl.rows[tile.y + g].y : 0) * p.K + k0) + t;
+  const uint4* x1 = reinterpret_cast<const uint4*>(
+      p.x + (int64_t)(on1 ? pl.rows[tile.y + g + 8].y : 0) * p.K + k0) + t;
+  const uint4* ar = reinterpret_cast<const uint4*>(p.a + ((int64_t)tile.x * p.R + g) * p.K + k0) + t;
+  float acc[NT][4];
+#pragma unroll
+  for (int q = 0; q < NT; ++q)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[q][i] = 0.0f;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 2
+  for (int kb = warp; kb < (k1 - k0) >> 5; kb += kShrinkWarps) {
+    const uint4 a = on0 ? __ldg(x0 + kb * 4) : zero, b = on1 ? __ldg(x1 + kb * 4) : zero;
+    uint4 w[NT];
+#pragma unroll
+    for (int q = 0; q < NT; ++q)
+      if (q < nt) w[q] = ldg_nc_v4(ar + (int64_t)q * p.K + kb * 4);
+#pragma unroll
+    for (int q = 0; q < NT; ++q)
+      if (q < nt) {
+        mma_bf16(acc[q], a.x, b.x, a.y, b.y, w[q].x, w[q].y);
+        mma_bf16(acc[q], a.z, b.z, a.w, b.w, w[q].z, w[q].w);
+      }
+  }
+  constexpr int RW = NT * 8;
+#pragma unroll
+  for (int q = 0; q < NT; ++q) {
+    float* at = red + (warp * kLoraSmallRows + g) * RW + q * 8 + 2 * t;
+    *reinterpret_cast<float2*>(at) = make_float2(acc[q][0], acc[q][1]);
+    *reinterpret_cast<float2*>(at + 8 * RW) = make_float2(acc[q][2], acc[q][3]);
+  }
+  __syncthreads();
+  for (int i = tid; i < kLoraSmallRows * RW; i += kShrinkThreads) {
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kShrinkWarps; ++w) s += red[w * kLoraSmallRows * RW + i];
+    if (i % RW < p.R) part[(i / RW) * pitch + i % RW] = s;
+  }
+}
+
+// A cluster walks over the tiles, its CTAs each over their range of K; the
+// joined sums are scaled and stored as bf16 terms, ready for the expand.
+template <int NT>
+__global__ void __launch_bounds__(kShrinkThreads, NT <= 8 ? 2 : 1) lora_shrink_tc_kernel(
+    LoraParams p, LoraPlan pl, int terms, uint32_t tmem_cols) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t done[kShrinkStages];
   __shared__ uint32_t tmem_sh;
@@ -196,6 +326,11 @@ __global__ void __launch_bounds__(kTcThreads) lora_shrink_tc_kernel(LoraParams p
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int RP = rank_pad(p.R);
   const int stage_bytes = kBlockBytes + RP * 128;
+  // sums of a tile, over the stages once their products are done; the small
+  // tiles' per-warp sums lie behind them
+  float* part = reinterpret_cast<float*>(smem);
+  const int pitch = RP + 4;
+  float* red = part + kLoraSmallRows * pitch;
   if (tid == 0) {
     for (int s = 0; s < kShrinkStages; ++s) mbar_init(&done[s], 1);
     fence_barrier_init();
@@ -212,94 +347,138 @@ __global__ void __launch_bounds__(kTcThreads) lora_shrink_tc_kernel(LoraParams p
   const uint32_t tmem = tmem_sh;
   const uint32_t idesc = idesc_bf16(128, RP);
   int bad = 0;
-  const int ntiles = lora_tiles(pl), splits = pl.splits;
+  const int2 ntiles = lora_tiles(pl);
+  const int splits = pl.splits, rank = blockIdx.x % splits;
   const int nkb = p.K / 64;
-  uint32_t phase[kShrinkStages] = {};  // parity of each stage's next completion
+  const int kb0 = rank * nkb / splits, nb = (rank + 1) * nkb / splits - kb0;
+  uint32_t phases = 0;  // bit s: parity of stage s's next completion
   const int c = tid & 7, r0 = tid >> 3;  // this thread's 16-byte column and first row
-  for (int u = blockIdx.x; u < ntiles * splits; u += gridDim.x) {
-    const int4 tile = pl.tiles[1 + u / splits];
-    const int ks = u % splits;
-    if (tile.x < 0) continue;
-    const int kb0 = ks * nkb / splits, nb = (ks + 1) * nkb / splits - kb0;
-    const uint16_t* xr[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = r0 + 32 * i;
-      xr[i] = r < tile.z ? p.x + lora_row(p, pl.perm[tile.y + r]).x_row * p.K + kb0 * 64 + c * 8
-                         : nullptr;
-    }
-    const uint16_t* ar = p.a + ((int64_t)tile.x * p.R + r0) * p.K + kb0 * 64 + c * 8;
-    auto load = [&](int kb) {
-      unsigned char* xs = smem + (kb % kShrinkStages) * stage_bytes;
-      unsigned char* as = xs + kBlockBytes;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (xr[i]) cp_async16(xs + sw128_offset(r0 + 32 * i, c), xr[i] + kb * 64, true);
+  for (int ti = blockIdx.x / splits; ti < ntiles.x + ntiles.y; ti += gridDim.x / splits) {
+    const bool is_small = ti >= ntiles.x;
+    const int4 tile = pl.tiles[is_small ? pl.capacity - 1 - (ti - ntiles.x) : ti];
+    if (tile.x < 0) continue;  // the whole cluster alike
+    if (is_small) {
+      shrink_small<NT>(p, pl, tile, kb0 * 64, (kb0 + nb) * 64, part, pitch, red);
+    } else {
+      const uint16_t* xr[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = r0 + 32 * i;
-        if (r < RP)
-          cp_async16(as + sw128_offset(r, c), r < p.R ? ar + (int64_t)32 * i * p.K + kb * 64 : p.a,
-                     r < p.R);
+        xr[i] = r < tile.z ? p.x + (int64_t)pl.rows[tile.y + r].y * p.K + kb0 * 64 + c * 8 : nullptr;
       }
-    };
-    for (int kb = 0; kb < kShrinkStages - 1; ++kb) {
-      if (kb < nb) load(kb);
-      cp_async_commit();
-    }
-    bool ok = true;
-    for (int kb = 0; kb < nb; ++kb) {
-      cp_async_wait<kShrinkStages - 2>();
-      fence_proxy_async_smem();
-      ok = !__syncthreads_or(bad);
-      if (!ok) break;
-      const int s = kb % kShrinkStages;
-      if (warp == 0) {
-        const uint64_t xd = smem_desc_sw128(smem + s * stage_bytes);
-        const uint64_t ad = smem_desc_sw128(smem + s * stage_bytes + kBlockBytes);
+      const uint16_t* ar = p.a + ((int64_t)tile.x * p.R + r0) * p.K + kb0 * 64 + c * 8;
+      auto load = [&](int kb) {
+        unsigned char* xs = smem + (kb % kShrinkStages) * stage_bytes;
+        unsigned char* as = xs + kBlockBytes;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) umma_bf16(tmem, xd + 2 * k, ad + 2 * k, idesc, kb > 0 || k > 0);
-        umma_commit(&done[s]);
-      }
-      // the stage that k-block kb + 3 takes was read by the MMAs of kb - 1
-      const int nx = kb + kShrinkStages - 1;
-      if (kb > 0) {
-        const int sp = (kb - 1) % kShrinkStages;
-        wait_or_flag(&done[sp], phase[sp], bad, p.err);
-        phase[sp] ^= 1u;
-      }
-      if (nx < nb) load(nx);
-      cp_async_commit();
-    }
-    if (ok) {
-      const int sp = (nb - 1) % kShrinkStages;
-      wait_or_flag(&done[sp], phase[sp], bad, p.err);
-      phase[sp] ^= 1u;
-    }
-    cp_async_wait<0>();
-    if (__syncthreads_or(bad)) break;
-    tc_fence_after();
-    if (warp < 4) {
-      const int row = warp * 32 + lane;
-      const float sc = p.scales ? __ldg(p.scales + tile.x / p.E) : 1.0f;
-      float* out = p.v + ((int64_t)ks * rows_cap + tile.y + row) * p.R;
-      for (int j = 0; j < RP; j += 16) {
-        uint32_t r[16];
-        tmem_ld16(tmem + ((uint32_t)(warp * 32) << 16) + j, r);
-        tmem_ld_wait();
-        if (row < tile.z) {
+        for (int i = 0; i < 4; ++i)
+          if (xr[i]) cp_async16(xs + sw128_offset(r0 + 32 * i, c), xr[i] + kb * 64, true);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (j + 4 * q < p.R)
-              *reinterpret_cast<float4*>(out + j + 4 * q) =
-                  make_float4(sc * __uint_as_float(r[4 * q]), sc * __uint_as_float(r[4 * q + 1]),
-                              sc * __uint_as_float(r[4 * q + 2]), sc * __uint_as_float(r[4 * q + 3]));
+        for (int i = 0; i < (NT * 8 + 31) / 32; ++i) {
+          const int r = r0 + 32 * i;
+          if (r < RP)
+            cp_async16(as + sw128_offset(r, c),
+                       r < p.R ? ar + (int64_t)32 * i * p.K + kb * 64 : p.a, r < p.R);
         }
+      };
+      for (int kb = 0; kb < kShrinkStages - 1; ++kb) {
+        if (kb < nb) load(kb);
+        cp_async_commit();
+      }
+      for (int kb = 0; kb < nb; ++kb) {
+        cp_async_wait<kShrinkStages - 2>();
+        fence_proxy_async_smem();
+        if (__syncthreads_or(bad)) {
+          bad = 1;
+          break;
+        }
+        const int s = kb % kShrinkStages;
+        if (warp == 0) {
+          const uint64_t xd = smem_desc_sw128(smem + s * stage_bytes);
+          const uint64_t ad = smem_desc_sw128(smem + s * stage_bytes + kBlockBytes);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_bf16(tmem, xd + 2 * k, ad + 2 * k, idesc, kb > 0 || k > 0);
+          umma_commit(&done[s]);
+        }
+        // the stage that k-block kb + 3 takes was read by the MMAs of kb - 1
+        const int nx = kb + kShrinkStages - 1;
+        if (kb > 0) {
+          const int sp = (kb - 1) % kShrinkStages;
+          wait_or_flag(&done[sp], (phases >> sp) & 1u, bad, p.err);
+          phases ^= 1u << sp;
+        }
+        if (nx < nb) load(nx);
+        cp_async_commit();
+      }
+      const int sp = (nb - 1) % kShrinkStages;
+      wait_or_flag(&done[sp], (phases >> sp) & 1u, bad, p.err);
+      phases ^= 1u << sp;
+      cp_async_wait<0>();
+      __syncthreads();
+      tc_fence_after();
+      // rows of the tile in warps 0-3, half of the columns in each warp of a pair
+      const int row = (warp & 3) * 32 + lane;
+      for (int j = (warp >> 2) * 16; j < RP; j += 32) {
+        uint32_t r[16];
+        tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + j, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<float4*>(part + row * pitch + j + 4 * q) =
+              make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
+                          __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+      }
+      tc_fence_before();
+    }
+    __syncthreads();
+    if (splits > 1) cluster_barrier();
+    tc_fence_after();
+    // join in rank order, each CTA its share of the values
+    const float sc = p.scales ? __ldg(p.scales + tile.x / p.E) : 1.0f;
+    const int quads = RP / 4;
+    for (int i = rank * kShrinkThreads + tid; i < tile.z * quads; i += splits * kShrinkThreads) {
+      const int r = i / quads, j = (i - r * quads) * 4;
+      float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (j < p.R) {
+        const float* at = part + r * pitch + j;
+        float4 q[kLoraMaxSplit];
+#pragma unroll
+        for (int s = 0; s < kLoraMaxSplit; ++s)
+          if (s < splits) {
+            if (s == rank)
+              q[s] = *reinterpret_cast<const float4*>(at);
+            else
+              asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                           : "=f"(q[s].x), "=f"(q[s].y), "=f"(q[s].z), "=f"(q[s].w)
+                           : "r"(cluster_addr(at, s)));
+          }
+#pragma unroll
+        for (int s = 0; s < kLoraMaxSplit; ++s)
+          if (s < splits) {
+            f.x += q[s].x;
+            f.y += q[s].y;
+            f.z += q[s].z;
+            f.w += q[s].w;
+          }
+        f.x *= sc;
+        f.y *= sc;
+        f.z *= sc;
+        f.w *= sc;
+      }
+      uint16_t* out = pl.terms + (int64_t)(tile.y + r) * terms * RP + j;
+      for (int x = 0; x < terms; ++x) {
+        const uint32_t a = pack_bf16x2(f.x, f.y), b = pack_bf16x2(f.z, f.w);
+        *reinterpret_cast<uint2*>(out + x * RP) = make_uint2(a, b);
+        const float2 fa = bf16x2_to_f32x2(a), fb = bf16x2_to_f32x2(b);
+        f.x -= fa.x;
+        f.y -= fa.y;
+        f.z -= fb.x;
+        f.w -= fb.y;
       }
     }
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
+    if (splits > 1) cluster_barrier();
   }
   __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, tmem_cols);
@@ -359,29 +538,107 @@ __device__ __forceinline__ void put8(void* out, int64_t at, const float (&f)[8])
   }
 }
 
-constexpr int kExpandCols = 128;  // accumulator columns of a unit
+constexpr int kExpandThreads = 128;
+constexpr int kExpandCols = 64;        // accumulator columns of a large unit
+constexpr int kExpandSmallCols = 128;  // output columns of a small unit, 32 per warp
 
-// Accumulator columns [32 b, 32 b + 32), b = 0..3, are 32 consecutive output
-// columns each (SWIGLU: b 0, 1 the gate's, b 2, 3 the same columns of up), in
-// an order that leaves lane t of a quad with eight consecutive ones: column
-// 8 q + 2 t + i of a block is its column 8 t + 2 q + i.
+// v's terms of the `n` rows from position `first` -> shared memory, 128-byte
+// swizzled; rows n .. up to `fill` become zeros.  Asynchronous copies.
+template <int TERMS>
+__device__ __forceinline__ void stage_v(const LoraPlan& pl, int RP, int first, int n, int fill,
+                                        unsigned char* vs) {
+  const int pieces = TERMS * RP / 8, c0 = threadIdx.x & 3;
+  for (int r = threadIdx.x >> 2; r < fill; r += kExpandThreads / 4) {
+    const uint16_t* src = pl.terms + (int64_t)(first + (r < n ? r : 0)) * (TERMS * RP);
+    for (int c = c0; c < pieces; c += 4)
+      cp_async16(vs + (c >> 3) * kBlockBytes + sw128_offset(r, c & 7), src + c * 8, r < n);
+  }
+}
+
+// One 32-column block (columns col .. of B's rows) of a small tile: acc[q]
+// holds, for rows g and g + 8, the lane's columns 8 t + 2 q + {0, 1}.
+template <int TERMS>
+__device__ __forceinline__ void small_block(float (&acc)[4][4], const LoraParams& p, int slot,
+                                            int col, const unsigned char* vs) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int RP = rank_pad(p.R);
+  const uint16_t* b0 = p.b + ((int64_t)slot * p.N + col + 8 * (g >> 1) + (g & 1)) * p.R + 4 * t;
+#pragma unroll 2
+  for (int s = 0; s < p.R; s += 16) {
+    const bool in = s + 4 * t < p.R;
+    uint2 bq[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      bq[q] = in ? __ldg(reinterpret_cast<const uint2*>(b0 + (int64_t)(2 * q) * p.R + s))
+                 : make_uint2(0u, 0u);
+#pragma unroll
+    for (int x = TERMS - 1; x >= 0; --x) {  // the small terms first
+      const int c = x * RP + s + 4 * t;
+      const unsigned char* at = vs + (c >> 6) * kBlockBytes + (c & 4) * 2;
+      const uint2 lo = *reinterpret_cast<const uint2*>(at + sw128_offset(g, (c & 63) >> 3));
+      const uint2 hi = *reinterpret_cast<const uint2*>(at + sw128_offset(g + 8, (c & 63) >> 3));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) mma_bf16(acc[q], lo.x, hi.x, lo.y, hi.y, bq[q].x, bq[q].y);
+    }
+  }
+}
+
+// Large units: accumulator columns [32 h, 32 h + 32), h = 0, 1, are 32
+// consecutive output columns each (SWIGLU: the gate's, then the same ones of
+// up), in an order that leaves lane t of a quad with eight consecutive ones:
+// column 8 q + 2 t + i of a block is its column 8 t + 2 q + i.  A lane's
+// pieces of base are requested one unit ahead, as soon as the registers of
+// the unit before are consumed, so loads are in flight through the waits.
 template <int TERMS, bool BASE_BF16, bool OUT_BF16, bool SWIGLU>
-__global__ void __launch_bounds__(kTcThreads, 2) lora_expand_tc_kernel(LoraParams p, LoraPlan pl,
-                                                                    int64_t rows_cap) {
+__global__ void __launch_bounds__(kExpandThreads, BASE_BF16 ? 4 : 3) lora_expand_tc_kernel(
+    LoraParams p, LoraPlan pl) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t done;
   __shared__ uint32_t tmem_sh;
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int RP = rank_pad(p.R);
   const int vblocks = (TERMS * RP + 63) / 64, bblocks = (RP + 63) / 64;
+  constexpr int kBBytes = kExpandCols * 128;  // 64 rows x 128 bytes
   unsigned char* vs = smem;
-  unsigned char* bs = smem + vblocks * kBlockBytes;  // two slots of bblocks blocks
+  unsigned char* bs = smem + vblocks * kBlockBytes;  // two slots of bblocks
   if (tid == 0) {
     mbar_init(&done, 1);
     fence_barrier_init();
   }
+  const uint32_t idesc = idesc_bf16(128, kExpandCols);
+  const int cols = SWIGLU ? p.N / 2 : p.N;                       // output columns
+  constexpr int span = SWIGLU ? kExpandCols / 2 : kExpandCols;   // of them in a large unit
+  constexpr int sspan = kExpandSmallCols;
+  const int chunks = cols / span, schunks = (cols + sspan - 1) / sspan;
+
+  // B rows of a large unit -> slot `s`: a thread takes every second 16-byte
+  // piece of one row
+  auto load_b = [&](int64_t u, int s) {
+    const int4 tile = pl.tiles[u / chunks];
+    if (tile.x < 0) return;
+    const int col0 = (int)(u % chunks) * span;
+    const int row = tid >> 1, h = row >> 5, w = row & 31;
+    const int n = SWIGLU ? h * cols + col0 + w : col0 + row;
+    const int drow = h * 32 + 8 * ((w & 7) >> 1) + 2 * (w >> 3) + (w & 1);
+    unsigned char* dst = bs + s * bblocks * kBBytes;
+    const uint16_t* src = p.b + ((int64_t)tile.x * p.N + n) * p.R;
+    for (int ch = tid & 1; ch < RP / 8; ch += 2) {
+      const bool on = ch * 8 < p.R;
+      cp_async16(dst + (ch >> 3) * kBBytes + sw128_offset(drow, ch & 7), on ? src + ch * 8 : p.b, on);
+    }
+  };
+
+  // The plan and base were complete before the kernel just before this one
+  // (the shrink) let it start: only v has to be waited for.
+  const int2 ntiles = lora_tiles(pl);
+  // every CTA gets its share of the large units and of the small ones, which
+  // take about as long for a fraction of the bytes
+  const int64_t large = (int64_t)ntiles.x * chunks, small = (int64_t)ntiles.y * schunks;
+  const int64_t u0 = large * blockIdx.x / gridDim.x, lend = large * (blockIdx.x + 1) / gridDim.x;
+  if (u0 < lend) load_b(u0, 0);
+  cp_async_commit();
   pdl_wait();
   if (warp == 0) {
     tmem_alloc(&tmem_sh, kExpandCols);
@@ -392,118 +649,49 @@ __global__ void __launch_bounds__(kTcThreads, 2) lora_expand_tc_kernel(LoraParam
   tc_fence_after();
   pdl_trigger();
   const uint32_t tmem = tmem_sh;
-  const uint32_t idesc = idesc_bf16(128, kExpandCols);
-  int bad = 0;
-  const int ntiles = lora_tiles(pl);
-  const int cols = SWIGLU ? p.N / 2 : p.N;                      // output columns
-  const int span = SWIGLU ? kExpandCols / 2 : kExpandCols;      // of them in a unit
-  const int chunks = (cols + span - 1) / span;
-  const int64_t units = (int64_t)ntiles * chunks;
-  const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
 
-  // B rows of a unit -> slot `s`
-  auto load_b = [&](int64_t u, int s) {
-    const int4 tile = pl.tiles[1 + u / chunks];
-    if (tile.x < 0) return;
-    const int col0 = (int)(u % chunks) * span;
-    const int nc = RP / 8;
-    unsigned char* dst = bs + s * bblocks * kBlockBytes;
-    const uint16_t* src = p.b + (int64_t)tile.x * p.N * p.R;
-    for (int i = tid; i < kExpandCols * nc; i += kTcThreads) {
-      const int row = i / nc, ch = i % nc;
-      const int b = row >> 5, w = row & 31;
-      int n = col0 + row;
-      if (SWIGLU) n = (b >> 1) * cols + col0 + (b & 1) * 32 + w;
-      // beyond the matrix: only columns that are never stored
-      const bool in = (SWIGLU ? col0 + (b & 1) * 32 : col0 + b * 32) < cols;
-      const int drow = b * 32 + 8 * ((w & 7) >> 1) + 2 * (w >> 3) + (w & 1);
-      const bool on = in && ch * 8 < p.R;
-      cp_async16(dst + (ch >> 3) * kBlockBytes + sw128_offset(drow, ch & 7),
-                 on ? src + (int64_t)n * p.R + ch * 8 : p.b, on);
-    }
-  };
-
-  const int g = lane >> 2, t = lane & 3;
-  const int lq = (warp & 3) * 32;  // this warp's accumulator rows
-  const int half = warp >> 2;      // and its two 32-column blocks: half (+ 2 or + 1)
-  int cur_tile = -1, slot = 0;
+  int bad = 0, cur_tile = -1, slot = 0;
   int4 tile = make_int4(-1, 0, 0, 0);
   int64_t row_at[4] = {};  // this lane's four rows (-1: none)
+  Base8<BASE_BF16> bq[2][4];
   uint32_t parity = 0;
-  if (u0 < u1) load_b(u0, 0);
-  cp_async_commit();
-  for (int64_t u = u0; u < u1; ++u) {
-    const int ti = (int)(u / chunks);
-    if (ti != cur_tile) {
-      cur_tile = ti;
-      tile = pl.tiles[1 + ti];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = lq + g + 8 * i;
-        row_at[i] = r < tile.z ? (int64_t)pl.perm[tile.y + r] : -1;
-      }
-      if (tile.x >= 0) {
-        // v (the K ranges' sums) -> bf16 terms; rows past the tile's are never stored
-        const int quads = RP / 4;
-        for (int i = tid; i < tile.z * quads; i += kTcThreads) {
-          const int r = i / quads, j = (i % quads) * 4;
-          float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (j < p.R) {
-            const float* src = p.v + (int64_t)(tile.y + r) * p.R + j;
-            for (int s = 0; s < pl.splits; ++s) {
-              const float4 q = __ldcg(reinterpret_cast<const float4*>(src + s * rows_cap * p.R));
-              f.x += q.x;
-              f.y += q.y;
-              f.z += q.z;
-              f.w += q.w;
-            }
-          }
-#pragma unroll
-          for (int x = 0; x < TERMS; ++x) {
-            const uint32_t a = pack_bf16x2(f.x, f.y), b = pack_bf16x2(f.z, f.w);
-            const int col = x * RP + j;
-            *reinterpret_cast<uint2*>(vs + (col >> 6) * kBlockBytes +
-                                      sw128_offset(r, (col & 63) >> 3) + (col & 4) * 2) =
-                make_uint2(a, b);
-            const float2 fa = bf16x2_to_f32x2(a), fb = bf16x2_to_f32x2(b);
-            f.x -= fa.x;
-            f.y -= fa.y;
-            f.z -= fb.x;
-            f.w -= fb.y;
-          }
-        }
-      }
-    }
-    if (u + 1 < u1) load_b(u + 1, slot ^ 1);
-    cp_async_commit();
-    // base of the unit, in flight while B lands and the MMAs run
-    const int col0 = (int)(u % chunks) * span;
-    Base8<BASE_BF16> bq[2][4];
-    int colb[2];  // first output column of the two blocks in base
-    bool in[2];
+  auto load_base = [&](int i, int col0) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int o = SWIGLU ? col0 + half * 32 : col0 + (half + 2 * h) * 32;
-      in[h] = o < cols;
-      colb[h] = (SWIGLU ? h * cols : 0) + o + 8 * t;
+      const int col = (SWIGLU ? h * cols + col0 : col0 + h * 32) + 8 * t;
+      if (p.base && row_at[i] >= 0) bq[h][i].load(p.base, row_at[i] * p.N + col);
+      else bq[h][i].zero();
+    }
+  };
+  for (int64_t u = u0; u < lend; ++u) {
+    const int ti = (int)(u / chunks), col0 = (int)(u % chunks) * span;
+    if (ti != cur_tile) {
+      cur_tile = ti;
+      tile = pl.tiles[ti];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (p.base && in[h] && row_at[i] >= 0) bq[h][i].load(p.base, row_at[i] * p.N + colb[h]);
-        else bq[h][i].zero();
+        const int r = warp * 32 + g + 8 * i;
+        row_at[i] = r < tile.z ? (int64_t)pl.rows[tile.y + r].x : -1;
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) load_base(i, col0);
+      if (tile.x >= 0) stage_v<TERMS>(pl, RP, tile.y, tile.z, tile.z, vs);
+      cp_async_commit();
     }
+    if (u + 1 < lend) load_b(u + 1, slot ^ 1);
+    cp_async_commit();
     cp_async_wait<1>();
     fence_proxy_async_smem();
     if (__syncthreads_or(bad)) break;
     if (tile.x >= 0) {
       if (warp == 0) {
-        for (int x = 0; x < TERMS; ++x)
+        for (int x = TERMS - 1; x >= 0; --x)  // the small terms first
           for (int j = 0; j < RP; j += 16) {
             const int col = x * RP + j;
             const uint64_t ad = smem_desc_sw128(vs + (col >> 6) * kBlockBytes) + ((col & 63) >> 3);
             const uint64_t bd =
-                smem_desc_sw128(bs + (slot * bblocks + (j >> 6)) * kBlockBytes) + ((j & 63) >> 3);
-            umma_bf16(tmem, ad, bd, idesc, x > 0 || j > 0);
+                smem_desc_sw128(bs + (slot * bblocks + (j >> 6)) * kBBytes) + ((j & 63) >> 3);
+            umma_bf16(tmem, ad, bd, idesc, x < TERMS - 1 || j > 0);
           }
         umma_commit(&done);
       }
@@ -511,14 +699,15 @@ __global__ void __launch_bounds__(kTcThreads, 2) lora_expand_tc_kernel(LoraParam
       parity ^= 1u;
       tc_fence_after();
     }
+    const bool more = u + 1 < lend && (int)((u + 1) / chunks) == ti;
 #pragma unroll
-    for (int hr = 0; hr < 2; ++hr) {  // accumulator rows lq + 16 hr ..
+    for (int hr = 0; hr < 2; ++hr) {  // accumulator rows 32 warp + 16 hr ..
       float z[2][2][8];               // [block][row g, g + 8]
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t r[16];
         if (tile.x >= 0) {
-          tmem_ld_16x256b_x4(tmem + ((uint32_t)(lq + 16 * hr) << 16) + (half + 2 * h) * 32, r);
+          tmem_ld_16x256b_x4(tmem + ((uint32_t)(warp * 32 + 16 * hr) << 16) + h * 32, r);
           tmem_ld_wait();
         }
 #pragma unroll
@@ -533,19 +722,22 @@ __global__ void __launch_bounds__(kTcThreads, 2) lora_expand_tc_kernel(LoraParam
           }
         }
       }
+      if (more) {
+        load_base(2 * hr, col0 + span);
+        load_base(2 * hr + 1, col0 + span);
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int64_t row = row_at[2 * hr + i];
         if (row < 0) continue;
         if constexpr (SWIGLU) {
-          if (!in[0]) continue;
 #pragma unroll
           for (int x = 0; x < 8; ++x) z[0][i][x] = swiglu_f32(z[0][i][x], z[1][i][x]);
-          put8<OUT_BF16>(p.out, row * cols + colb[0], z[0][i]);
+          put8<OUT_BF16>(p.out, row * cols + col0 + 8 * t, z[0][i]);
         } else {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            if (in[h]) put8<OUT_BF16>(p.out, row * cols + colb[h], z[h][i]);
+            put8<OUT_BF16>(p.out, row * cols + col0 + h * 32 + 8 * t, z[h][i]);
         }
       }
     }
@@ -555,17 +747,70 @@ __global__ void __launch_bounds__(kTcThreads, 2) lora_expand_tc_kernel(LoraParam
     tc_fence_after();
   }
   cp_async_wait<0>();
+  const bool stop = __syncthreads_or(bad) != 0;
+
+  cur_tile = -1;
+  const int64_t s1 = small * (blockIdx.x + 1) / gridDim.x;
+  for (int64_t u = small * blockIdx.x / gridDim.x; u < s1 && !stop; ++u) {
+    const int ti = (int)(u / schunks), c0 = (int)(u % schunks) * sspan;
+    if (ti != cur_tile) {
+      cur_tile = ti;
+      tile = pl.tiles[pl.capacity - 1 - ti];
+      row_at[0] = g < tile.z ? (int64_t)pl.rows[tile.y + g].x : -1;
+      row_at[1] = g + 8 < tile.z ? (int64_t)pl.rows[tile.y + g + 8].x : -1;
+      __syncthreads();  // no warp still reads the tile before
+      stage_v<TERMS>(pl, RP, tile.y, tile.z, kLoraSmallRows, vs);
+      cp_async_commit();
+      cp_async_wait<0>();
+      __syncthreads();
+    }
+    for (int col = c0 + warp * 32; col < min(c0 + sspan, cols); col += kExpandThreads) {
+      float z[SWIGLU ? 2 : 1][2][8];
+#pragma unroll
+      for (int h = 0; h < (SWIGLU ? 2 : 1); ++h) {
+        float acc[4][4];
+        Base8<BASE_BF16> b[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (p.base && row_at[i] >= 0) b[i].load(p.base, row_at[i] * p.N + h * cols + col + 8 * t);
+          else b[i].zero();
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[q][i] = 0.0f;
+        small_block<TERMS>(acc, p, tile.x, h * cols + col, vs);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          b[i].get(z[h][i]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            z[h][i][2 * q] += acc[q][2 * i];
+            z[h][i][2 * q + 1] += acc[q][2 * i + 1];
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (row_at[i] < 0) continue;
+        if constexpr (SWIGLU) {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) z[0][i][x] = swiglu_f32(z[0][i][x], z[1][i][x]);
+        }
+        put8<OUT_BF16>(p.out, row_at[i] * cols + col + 8 * t, z[0][i]);
+      }
+    }
+  }
   __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, kExpandCols);
 }
 
 template <int TERMS, bool BASE_BF16, bool OUT_BF16, bool SWIGLU>
-moe_status_t launch_expand(const LoraParams& p, const LoraPlan& plan, int64_t rows,
-                           int64_t capacity, cudaStream_t st) {
+moe_status_t launch_expand(const LoraParams& p, const LoraPlan& plan, cudaStream_t st) {
   using namespace moe_host;
   const int RP = rank_pad(p.R);
-  const size_t smem =
-      ((TERMS * RP + 63) / 64 + 2 * ((RP + 63) / 64)) * (size_t)kBlockBytes + 1024;
+  const size_t smem = ((TERMS * RP + 63) / 64) * (size_t)kBlockBytes +
+                      2 * ((RP + 63) / 64) * (size_t)(kExpandCols * 128) + 1024;
   auto kern = lora_expand_tc_kernel<TERMS, BASE_BF16, OUT_BF16, SWIGLU>;
   static size_t set_max[kMaxCachedDevices] = {};
   const int dev = device_index();
@@ -575,12 +820,67 @@ moe_status_t launch_expand(const LoraParams& p, const LoraPlan& plan, int64_t ro
       return MOE_ERR_CUDA;
     set_max[dev] = smem;
   }
-  const int per_sm = smem <= 110 * 1024 ? 2 : 1;
-  const int span = SWIGLU ? kExpandCols / 2 : kExpandCols;
+  int per_sm = (int)(224 * 1024 / (smem + 1024));
+  if (per_sm > (BASE_BF16 ? 4 : 3)) per_sm = BASE_BF16 ? 4 : 3;
+  if (per_sm < 1) per_sm = 1;
   const int cols = SWIGLU ? p.N / 2 : p.N;
-  int64_t grid = capacity * ((cols + span - 1) / span);
+  const int span = SWIGLU ? kExpandCols / 2 : kExpandCols;
+  int64_t grid = plan.capacity * (cols / span);
   if (grid > (int64_t)sm_count() * per_sm) grid = (int64_t)sm_count() * per_sm;
-  return launch(kern, (int)grid, kTcThreads, smem, st, p, plan, rows);
+  return launch(kern, (int)grid, kExpandThreads, smem, st, p, plan);
+}
+
+// moe_host::launch with thread-block clusters.
+template <typename... KArgs, typename... Args>
+moe_status_t launch_clusters(void (*kern)(KArgs...), dim3 grid, int block, size_t smem,
+                             dim3 cluster, cudaStream_t st, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster.x;
+  attr[0].val.clusterDim.y = cluster.y;
+  attr[0].val.clusterDim.z = cluster.z;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = moe_host::pdl_enabled() ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...) != cudaSuccess) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
+}
+
+template <int NT>
+moe_status_t launch_shrink(const LoraParams& p, const LoraPlan& plan, int terms, cudaStream_t st) {
+  using namespace moe_host;
+  const int RP = rank_pad(p.R);
+  const size_t smem = (size_t)kShrinkStages * (kBlockBytes + RP * 128) + 1024;
+  // the least padded rank of this instantiation, and what lies over its stages
+  constexpr int least = NT == 2 ? 16 : rank_pad(NT * 4 + 8);
+  static_assert(kLoraSmallRows * (NT * 8 + 4) * 4 + kShrinkWarps * kLoraSmallRows * NT * 8 * 4 <=
+                    kShrinkStages * (kBlockBytes + least * 128), "the small tiles' sums fit");
+  static_assert(kLoraTileRows * (NT * 8 + 4) * 4 <= kShrinkStages * (kBlockBytes + least * 128),
+                "a tile's sums fit");
+  static size_t set_max[kMaxCachedDevices] = {};
+  const int dev = device_index();
+  if (smem > set_max[dev]) {
+    if (cudaFuncSetAttribute(lora_shrink_tc_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)smem) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    set_max[dev] = smem;
+  }
+  uint32_t tmem_cols = 32;
+  while ((int)tmem_cols < RP) tmem_cols <<= 1;
+  const int per_sm = NT <= 8 ? 2 : 1;
+  int64_t clusters = (int64_t)sm_count() * per_sm / plan.splits;
+  if (clusters > plan.capacity) clusters = plan.capacity;
+  return launch_clusters(lora_shrink_tc_kernel<NT>, dim3((unsigned)(clusters * plan.splits)),
+                         kShrinkThreads, smem, dim3(plan.splits), st, p, plan, terms, tmem_cols);
 }
 
 }  // namespace
@@ -588,41 +888,31 @@ moe_status_t launch_expand(const LoraParams& p, const LoraPlan& plan, int64_t ro
 moe_status_t lora_grouped(const LoraParams& p, const LoraPlan& plan, int64_t rows, bool swiglu,
                           bool out_bf16, cudaStream_t st) {
   using namespace moe_host;
-  const int64_t capacity = plan.capacity;
-  if (cudaMemsetAsync(plan.tiles, 0, sizeof(int4), st) != cudaSuccess) return MOE_ERR_CUDA;
-  const size_t plan_smem = (size_t)3 * (p.n_adapters + 1) * sizeof(int);
+  // with several experts their CTAs add to the counts
+  if (p.E > 1 && cudaMemsetAsync(plan.counts, 0, sizeof(int4), st) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  const size_t plan_smem = (size_t)4 * (p.n_adapters + 1) * sizeof(int);
   if (plan_smem > 48 * 1024 &&
       cudaFuncSetAttribute(lora_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)plan_smem) != cudaSuccess)
     return MOE_ERR_CUDA;
-  // an expert has about T rows at most; longer ones only make the ranges longer
-  int64_t chunks = ((int64_t)p.T + kPlanThreads - 1) / kPlanThreads;
-  if (chunks > 64) chunks = 64;
-  moe_status_t s = launch(lora_plan_kernel, dim3(p.E, (unsigned)chunks), kPlanThreads, plan_smem, st,
-                          p, plan);
+  // CTAs per expert: one per 1024 of the rows that an expert has on average
+  int ranges = 1;
+  while (ranges < 8 && (int64_t)ranges * 1024 * p.E < rows) ranges *= 2;
+  moe_status_t s = launch_clusters(lora_plan_kernel, dim3(p.E, ranges), kPlanThreads, plan_smem,
+                                   dim3(1, ranges), st, p, plan);
   if (s != MOE_OK) return s;
-  const int RP = rank_pad(p.R);
-  const size_t smem = (size_t)kShrinkStages * (kBlockBytes + RP * 128) + 1024;
-  static size_t set_max[kMaxCachedDevices] = {};
-  const int dev = device_index();
-  if (smem > set_max[dev]) {
-    if (cudaFuncSetAttribute(lora_shrink_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem) != cudaSuccess)
-      return MOE_ERR_CUDA;
-    set_max[dev] = smem;
-  }
-  uint32_t tmem_cols = 32;
-  while ((int)tmem_cols < RP) tmem_cols <<= 1;
-  const int per_sm = smem <= 110 * 1024 ? 2 : 1;
-  int64_t grid = capacity * plan.splits;
-  if (grid > (int64_t)sm_count() * per_sm) grid = (int64_t)sm_count() * per_sm;
-  s = launch(lora_shrink_tc_kernel, (int)grid, kTcThreads, smem, st, p, plan, rows, tmem_cols);
+  const int terms = out_bf16 && !swiglu ? 2 : 3;
+  if (p.R <= 16) s = launch_shrink<2>(p, plan, terms, st);
+  else if (p.R <= 32) s = launch_shrink<4>(p, plan, terms, st);
+  else if (p.R <= 64) s = launch_shrink<8>(p, plan, terms, st);
+  else s = launch_shrink<16>(p, plan, terms, st);
   if (s != MOE_OK) return s;
   if (swiglu)
-    return out_bf16 ? launch_expand<3, false, true, true>(p, plan, rows, capacity, st)
-                    : launch_expand<3, false, false, true>(p, plan, rows, capacity, st);
-  return out_bf16 ? launch_expand<2, true, true, false>(p, plan, rows, capacity, st)
-                  : launch_expand<3, false, false, false>(p, plan, rows, capacity, st);
+    return out_bf16 ? launch_expand<3, false, true, true>(p, plan, st)
+                    : launch_expand<3, false, false, true>(p, plan, st);
+  return out_bf16 ? launch_expand<2, true, true, false>(p, plan, st)
+                  : launch_expand<3, false, false, false>(p, plan, st);
 }
 
 }  // namespace moe
