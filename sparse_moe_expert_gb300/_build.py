@@ -1,8 +1,10 @@
-"""Build libmoe_gb300.so in-tree with nvcc for sm_103a.
+"""Build libmoe_gb300.so in-tree with nvcc for sm_103a, and _native.so, the
+CPython entry points of the short calls, with g++ against the installed torch.
 
 Each .cu file is compiled to an object in parallel, then linked into one
-shared library next to this file.  Objects are cached by source and header
-modification times.
+shared library next to this file; _native.so links to it.  Objects are cached
+by source and header modification times (the extension's also by torch's
+version).
 """
 from __future__ import annotations
 
@@ -11,12 +13,14 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_gb300.so")
+NATIVE = os.path.join(HERE, "_native.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-warn-spills"]
@@ -48,6 +52,41 @@ def _compile(nvcc: str, src: str, extra) -> str:
     return obj
 
 
+def _native_object() -> str:
+    import torch
+    src = os.path.join(CSRC, "native.cpp")
+    obj = os.path.join(BUILD, f"native-{torch.__version__}.o")
+    newest = max(os.path.getmtime(src), _headers_mtime())
+    if os.path.exists(obj) and os.path.getmtime(obj) >= newest:
+        return obj
+    root = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    incs = [root, os.path.join(root, "torch", "csrc", "api", "include"), cuda,
+            sysconfig.get_paths()["include"]]
+    tmp = obj + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+    for i in incs:
+        cmd += ["-isystem", i]
+    r = subprocess.run([*cmd, "-c", src, "-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on native.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, obj)
+    return obj
+
+
+def _link_native(obj: str) -> None:
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = NATIVE + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, LIB, f"-L{libs}",
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of _native.so failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, NATIVE)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -55,16 +94,22 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         for o in glob.glob(os.path.join(BUILD, "*.o")):
             os.remove(o)
     nvcc = _nvcc()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        native = ex.submit(_native_object)
         objs = list(ex.map(lambda s: _compile(nvcc, s, list(extra_flags)), srcs))
+        native_obj = native.result()
     newest = max(os.path.getmtime(o) for o in objs)
     if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < newest:
         tmp = LIB + f".tmp{os.getpid()}"
-        cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"]
+        cmd = [nvcc, *ARCH, "-shared", "-Xlinker", "-soname=libmoe_gb300.so", "-o", tmp, *objs,
+               "-lcudart"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    if (force or not os.path.exists(NATIVE)
+            or os.path.getmtime(NATIVE) < max(os.path.getmtime(native_obj), os.path.getmtime(LIB))):
+        _link_native(native_obj)
     if verbose:
         print(f"built {LIB}")
     return LIB

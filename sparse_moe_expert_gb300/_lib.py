@@ -2,6 +2,8 @@
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 from . import _build
@@ -135,6 +137,28 @@ def lib():
         _declare(handle)
         _LIB = handle
     return _LIB
+
+
+_NATIVE = None
+
+
+def native():
+    """The CPython entry points of the short calls (csrc/native.cpp); raises if
+    they have not been built."""
+    global _NATIVE
+    if _NATIVE is None:
+        import torch  # noqa: F401  (its libraries must be loaded first)
+        lib()
+        path = _build.NATIVE
+        if not os.path.exists(path):
+            raise RuntimeError(
+                f"{path} is missing: build it with sparse_moe_expert_gb300._build.build()")
+        loader = importlib.machinery.ExtensionFileLoader("_native", path)
+        spec = importlib.util.spec_from_file_location("_native", path, loader=loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        _NATIVE = module
+    return _NATIVE
 
 
 def check(name: str, status: int) -> None:

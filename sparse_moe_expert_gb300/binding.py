@@ -8,14 +8,13 @@ of the layer is computed here.
 from __future__ import annotations
 
 import ctypes
-import functools
 from typing import Optional
 
 import torch
 
 from . import _lib
 from ._lib import (DTYPE_BF16, DTYPE_F32, EPILOGUE_RAW, EPILOGUE_SWIGLU, PATH_AUTO, QDesc,
-                   check, lib)
+                   check, lib, native)
 
 _DT = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 
@@ -291,21 +290,8 @@ def moe_get_device_error(clear: bool = True, stream=None) -> int:
 
 # ---- score routing, its gradient, adapters ----------------------------------
 #
-# These calls are short (a few microseconds on the device), so the checks are
-# single comparisons that fall through to a message only when one fails, and
-# sizes that depend on a few integers are remembered.
-
-
-def _raw(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _cur(stream, dev) -> int:
-    """The cudaStream_t of ``stream``, or of the device's current stream
-    (read without building a torch.cuda.Stream, which costs 3 us)."""
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(dev.index)
+# The short ones (a few microseconds on the device) check their tensors,
+# allocate missing outputs and make the C call in csrc/native.cpp.
 
 
 def _hold(stream, *tensors):
@@ -316,62 +302,20 @@ def _hold(stream, *tensors):
             t.record_stream(stream)
 
 
-def _rows2d(t: torch.Tensor, name: str) -> int:
-    """Row stride of a 2D CUDA tensor of fp32 or bf16 with dense rows."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _DT:
-        raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions")
-    T, E = t.shape
-    ld, step = t.stride()
-    if E > 1 and step != 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    if T <= 1:
-        return E
-    if ld < E:
-        raise ValueError(f"{name} must have rows that do not overlap")
-    return ld
-
-
 def _like(t: torch.Tensor, shape: tuple, dtype, dev, name: str):
-    if t.dtype == dtype and t.shape == shape and t.device == dev and t.is_contiguous():
-        return
     _need(t, dtype, name)
     if tuple(t.shape) != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    raise ValueError(f"{name} must be on {dev}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
 
 
 def _flat(t: torch.Tensor, least: int, dev, name: str):
-    """A contiguous int32 tensor of at least ``least`` elements."""
-    if t.dtype == torch.int32 and t.device == dev and t.is_contiguous() and t.numel() >= least:
-        return
     _need(t, torch.int32, name)
     if t.numel() < least:
         raise ValueError(f"{name} must hold {least} entries")
-    raise ValueError(f"{name} must be on {dev}")
-
-
-def _matrix(t: torch.Tensor, rows: int, cols: int, dev, name: str):
-    """A contiguous fp32 or bf16 matrix of at least ``rows`` rows of ``cols``."""
-    if t.dtype not in _DT:
-        raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-    if t.dim() == 2 and t.device == dev and t.is_contiguous():
-        n, c = t.shape
-        if n >= rows and c == cols:
-            return
-    _need(t, t.dtype, name)
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}")
-    raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
-
-
-def _scratch(t: Optional[torch.Tensor], dev) -> int:
-    if t.device != dev or not t.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    return t.numel() * t.element_size()
 
 
 def moe_router_logits(x, w_router, logit_bias=None, inv_temperature: float = 1.0, logits=None,
@@ -391,8 +335,8 @@ def moe_router_logits(x, w_router, logit_bias=None, inv_temperature: float = 1.0
     if stream is not None:
         _hold(stream, x, w_router, logit_bias, logits)
     check("moe_router_logits",
-          lib().moe_router_logits(x.data_ptr(), w_router.data_ptr(), _raw(logit_bias),
-                                  inv_temperature, T, H, E, logits.data_ptr(), _cur(stream, dev)))
+          lib().moe_router_logits(_p(x), _p(w_router), _p(logit_bias), inv_temperature, T, H, E,
+                                  _p(logits), _stream(stream)))
     return logits
 
 
@@ -406,37 +350,16 @@ def moe_route_scored(logits, k: int, score: int = _lib.SCORE_SOFTMAX, select_bia
     strided); ``select_bias`` steers the selection only; with ``n_groups`` > 1
     the experts of the ``topk_groups`` best groups compete.  Slots without an
     available expert hold id -1 and weight 0."""
-    ld = _rows2d(logits, "logits")
-    T, E = logits.shape
-    if kmax is None:
-        kmax = k
-    dev = logits.device
-    if select_bias is not None:
-        _like(select_bias, (E,), torch.float32, dev, "select_bias")
-    if topk_ids is None:
-        topk_ids = torch.empty((T, kmax), dtype=torch.int32, device=dev)
-    else:
-        _like(topk_ids, (T, kmax), torch.int32, dev, "topk_ids")
-    if topk_w is None:
-        topk_w = torch.empty((T, kmax), dtype=torch.float32, device=dev)
-    else:
-        _like(topk_w, (T, kmax), torch.float32, dev, "topk_w")
-    if k_dev is None:
-        k_dev = torch.empty(1, dtype=torch.int32, device=dev)
-    else:
-        _like(k_dev, (1,), torch.int32, dev, "k_dev")
+    r = native().route_scored(logits, k, score, select_bias, n_groups, topk_groups, group_top,
+                              renormalize, scale, kmax, topk_ids, topk_w, k_dev,
+                              None if stream is None else stream.cuda_stream)
+    if r.__class__ is int:
+        check("moe_route_scored", r)
     if stream is not None:
-        _hold(stream, logits, select_bias, topk_ids, topk_w, k_dev)
-    st = lib().moe_route_scored(logits.data_ptr(), _DT[logits.dtype], ld, _raw(select_bias), T, E,
-                                score, n_groups, topk_groups, group_top, k, kmax,
-                                bool(renormalize), scale, topk_ids.data_ptr(), topk_w.data_ptr(),
-                                k_dev.data_ptr(), _cur(stream, dev))
-    if st:
-        check("moe_route_scored", st)
-    return topk_ids, topk_w, k_dev
+        _hold(stream, logits, select_bias, *r)
+    return r
 
 
-@functools.lru_cache(maxsize=1024)
 def moe_route_backward_workspace_size(E: int) -> int:
     return int(lib().moe_route_backward_workspace_size(E))
 
@@ -450,47 +373,14 @@ def moe_route_scored_backward(logits, topk_ids, d_topk_w=None, expert_counts=Non
 
     Gradient of sum(d_topk_w * topk_w) + balance + z with respect to the
     logits of moe_route_scored (same score, renormalize and scale)."""
-    ld = _rows2d(logits, "logits")
-    T, E = logits.shape
-    dev = logits.device
-    if topk_ids.dim() != 2 or topk_ids.shape[0] != T:
-        raise ValueError("topk_ids must be [T, kmax]")
-    kmax = topk_ids.shape[1]
-    _like(topk_ids, (T, kmax), torch.int32, dev, "topk_ids")
-    if k is None:
-        k = kmax
-    if d_topk_w is not None:
-        _like(d_topk_w, (T, kmax), torch.float32, dev, "d_topk_w")
-    if expert_counts is not None:
-        _like(expert_counts, (E,), torch.int32, dev, "expert_counts")
-    if d_logits is None:
-        d_logits = torch.empty((T, E), dtype=logits.dtype, device=dev)
-        ld_out = E
-    else:
-        if d_logits.dtype != logits.dtype or d_logits.shape != logits.shape:
-            raise ValueError("d_logits must have the type and shape of logits")
-        if d_logits.device != dev:
-            raise ValueError(f"d_logits must be on {dev}")
-        ld_out = _rows2d(d_logits, "d_logits")
-    if losses is None:
-        losses = torch.empty(2, dtype=torch.float32, device=dev)
-    else:
-        _like(losses, (2,), torch.float32, dev, "losses")
-    if workspace is None:
-        ws_bytes = moe_route_backward_workspace_size(E)
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-    else:
-        ws_bytes = _scratch(workspace, dev)
+    r = native().route_scored_backward(logits, topk_ids, d_topk_w, expert_counts, score, k,
+                                       renormalize, scale, balance_coef, z_coef, d_logits, losses,
+                                       workspace, None if stream is None else stream.cuda_stream)
+    if r.__class__ is int:
+        check("moe_route_scored_backward", r)
     if stream is not None:
-        _hold(stream, logits, topk_ids, d_topk_w, expert_counts, d_logits, losses, workspace)
-    st = lib().moe_route_scored_backward(
-        logits.data_ptr(), _DT[logits.dtype], ld, topk_ids.data_ptr(), _raw(d_topk_w),
-        _raw(expert_counts), T, E, score, k, kmax, bool(renormalize), scale, balance_coef, z_coef,
-        d_logits.data_ptr(), ld_out, losses.data_ptr(), workspace.data_ptr(), ws_bytes,
-        _cur(stream, dev))
-    if st:
-        check("moe_route_scored_backward", st)
-    return d_logits, losses
+        _hold(stream, logits, topk_ids, d_topk_w, expert_counts, *r)
+    return r[:2]
 
 
 def moe_permute_masked(topk_ids, k_dev, E: int, capacity: Optional[int] = None,
@@ -522,11 +412,10 @@ def moe_permute_masked(topk_ids, k_dev, E: int, capacity: Optional[int] = None,
     if stream is not None:
         _hold(stream, topk_ids, k_dev, expert_counts, expert_offsets, sorted_assign, inv_pos)
     check("moe_permute_masked",
-          lib().moe_permute_masked(topk_ids.data_ptr(), k_dev.data_ptr(), T, kmax, E,
-                                   -1 if capacity is None else int(capacity),
-                                   expert_counts.data_ptr(), expert_offsets.data_ptr(),
-                                   sorted_assign.data_ptr(), inv_pos.data_ptr(),
-                                   _cur(stream, dev)))
+          lib().moe_permute_masked(_p(topk_ids), _p(k_dev), T, kmax, E,
+                                   -1 if capacity is None else int(capacity), _p(expert_counts),
+                                   _p(expert_offsets), _p(sorted_assign), _p(inv_pos),
+                                   _stream(stream)))
     return expert_counts, expert_offsets, sorted_assign, inv_pos
 
 
@@ -537,35 +426,18 @@ def moe_combine_backward(d_out, y, inv_pos, topk_w, k_dev, d_topk_w=None, d_y=No
     Rows of ``d_y`` that no kept slot points to keep what they held (zeros
     when the buffer is allocated here).  need_d_y=False computes d_topk_w
     alone (d_y is None)."""
-    _need(d_out, torch.bfloat16, "d_out")
-    T, H = d_out.shape
-    dev = d_out.device
-    if topk_w.dim() != 2:
-        raise ValueError("topk_w must be [T, kmax]")
-    kmax = topk_w.shape[1]
-    _like(topk_w, (T, kmax), torch.float32, dev, "topk_w")
-    _flat(inv_pos, T * kmax, dev, "inv_pos")
-    _matrix(y, T * kmax, H, dev, "y")
-    _like(k_dev, (1,), torch.int32, dev, "k_dev")
-    if d_topk_w is None:
-        d_topk_w = torch.empty((T, kmax), dtype=torch.float32, device=dev)
-    else:
-        _like(d_topk_w, (T, kmax), torch.float32, dev, "d_topk_w")
-    if d_y is not None:
-        _like(d_y, tuple(y.shape), y.dtype, dev, "d_y")
-    elif need_d_y:
-        d_y = torch.zeros_like(y)
+    if d_y is None and need_d_y and stream is not None:
+        with torch.cuda.stream(stream):  # the zeros belong to the call
+            d_y = torch.zeros_like(y)
+    r = native().combine_backward(d_out, y, inv_pos, topk_w, k_dev, d_topk_w, d_y, need_d_y,
+                                  None if stream is None else stream.cuda_stream)
+    if r.__class__ is int:
+        check("moe_combine_backward", r)
     if stream is not None:
-        _hold(stream, d_out, y, inv_pos, topk_w, k_dev, d_topk_w, d_y)
-    st = lib().moe_combine_backward(d_out.data_ptr(), y.data_ptr(), _DT[y.dtype],
-                                    inv_pos.data_ptr(), topk_w.data_ptr(), k_dev.data_ptr(), T,
-                                    kmax, H, d_topk_w.data_ptr(), _raw(d_y), _cur(stream, dev))
-    if st:
-        check("moe_combine_backward", st)
-    return d_topk_w, d_y
+        _hold(stream, d_out, y, inv_pos, topk_w, k_dev, *r)
+    return r
 
 
-@functools.lru_cache(maxsize=1024)
 def moe_lora_workspace_size(T: int, kmax: int, E: int, n_adapters: int, R: int) -> int:
     return int(lib().moe_lora_workspace_size(T, kmax, E, n_adapters, R))
 
@@ -584,63 +456,16 @@ def moe_lora_apply(x, adapter_ids, lora_a, lora_b, scales=None, base=None, out=N
     EPILOGUE_SWIGLU takes an fp32 base [rows, N] and gives [rows, N/2], bf16
     unless out_dtype says fp32.  k_dev is accepted beside the other routing
     results and not needed (expert_offsets holds the row count)."""
-    _need(x, torch.bfloat16, "x")
-    dev = x.device
-    shape = lora_a.shape
-    if len(shape) == 3:
-        n, R, K = shape
-        E = 1
-    elif len(shape) == 4:
-        n, E, R, K = shape
-    else:
-        raise ValueError("lora_a must be [n, R, K] or [n, E, R, K]")
-    N = lora_b.shape[-2]
-    _like(lora_a, tuple(shape), torch.bfloat16, dev, "lora_a")
-    _like(lora_b, (n, N, R) if len(shape) == 3 else (n, E, N, R), torch.bfloat16, dev, "lora_b")
-    T = adapter_ids.shape[0]
-    _like(adapter_ids, (T,), torch.int32, dev, "adapter_ids")
-    kmax = 1
-    if sorted_assign is not None:
-        if topk_ids is None or expert_offsets is None:
-            raise ValueError("expert rows need topk_ids, sorted_assign and expert_offsets")
-        kmax = topk_ids.shape[1]
-        _like(topk_ids, (T, kmax), torch.int32, dev, "topk_ids")
-        _like(expert_offsets, (E + 1,), torch.int32, dev, "expert_offsets")
-        _flat(sorted_assign, T * kmax, dev, "sorted_assign")
-    elif topk_ids is not None or expert_offsets is not None:
-        raise ValueError("expert rows need topk_ids, sorted_assign and expert_offsets")
-    rows = T * kmax
-    if x.dim() != 2 or x.shape[1] != K:
-        raise ValueError(f"x must be [rows, {K}]")
-    if x.shape[0] < (T if x_by_token else rows):
-        raise ValueError("x has too few rows")
-    if scales is not None:
-        _like(scales, (n,), torch.float32, dev, "scales")
-    swiglu = epilogue == EPILOGUE_SWIGLU
-    cols = N // 2 if swiglu else N
-    if base is not None:
-        _matrix(base, rows, N, dev, "base")
-    if out is not None:
-        _matrix(out, rows, cols, dev, "out")
-    else:
-        if out_dtype is None:
-            out_dtype = torch.bfloat16 if swiglu or base is None else base.dtype
-        out = torch.empty((rows, cols), dtype=out_dtype, device=dev)
-    out_dt = _DT[out.dtype]
-    if workspace is None:
-        ws_bytes = moe_lora_workspace_size(T, kmax, E, n, R)
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-    else:
-        ws_bytes = _scratch(workspace, dev)
+    if out_dtype is not None:
+        if out_dtype not in _DT:
+            raise ValueError(f"out_dtype must be float32 or bfloat16, got {out_dtype}")
+        out_dtype = out_dtype is torch.bfloat16
+    r = native().lora_apply(x, adapter_ids, lora_a, lora_b, scales, base, out, epilogue, out_dtype,
+                            topk_ids, sorted_assign, expert_offsets, x_by_token, workspace,
+                            None if stream is None else stream.cuda_stream)
+    if r.__class__ is int:
+        check("moe_lora_apply", r)
     if stream is not None:
-        _hold(stream, x, adapter_ids, lora_a, lora_b, scales, base, out, topk_ids, sorted_assign,
-              expert_offsets, workspace)
-    st = lib().moe_lora_apply(x.data_ptr(), bool(x_by_token), adapter_ids.data_ptr(),
-                              _raw(topk_ids), _raw(sorted_assign), _raw(expert_offsets), T, kmax,
-                              E, n, K, N, R, lora_a.data_ptr(), lora_b.data_ptr(), _raw(scales),
-                              _raw(base), out_dt if base is None else _DT[base.dtype], epilogue,
-                              out_dt, out.data_ptr(), workspace.data_ptr(), ws_bytes,
-                              _cur(stream, dev))
-    if st:
-        check("moe_lora_apply", st)
-    return out
+        _hold(stream, x, adapter_ids, lora_a, lora_b, scales, base, topk_ids, sorted_assign,
+              expert_offsets, *r)
+    return r[0]

@@ -147,3 +147,73 @@ def test_header_constants_match_the_binding(tmp_path):
     assert vals == [moe.PATH_GEMV, moe.PATH_TC, moe.PATH_FLAG_WEIGHTS_EARLY,
                     moe.PATH_FLAG_K_GATED, moe.path_k_range(2, 3), moe.DROPPED,
                     moe.PATH_AUTO]
+
+
+def test_native_entry_points_load_and_refuse_host_tensors(L):
+    """The CPython entry points of the short calls load next to the library
+    and refuse wrong arguments with ValueError before any C call."""
+    import torch
+    import sparse_moe_expert_gb300 as moe
+    from sparse_moe_expert_gb300 import _lib
+    assert _lib.native() is _lib.native()
+    i32 = torch.int32
+    with pytest.raises(ValueError, match="logits must be a CUDA tensor"):
+        moe.moe_route_scored(torch.zeros(2, 8), 2)
+    with pytest.raises(ValueError, match="must be a tensor"):
+        moe.moe_route_scored([1.0], 2)
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.moe_route_scored_backward(torch.zeros(2, 8), torch.zeros((2, 2), dtype=i32))
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.moe_combine_backward(torch.zeros((2, 64), dtype=torch.bfloat16), torch.zeros(4, 64),
+                                 torch.zeros(4, dtype=i32), torch.zeros(2, 2),
+                                 torch.zeros(1, dtype=i32))
+    with pytest.raises(ValueError, match="CUDA"):
+        b = torch.zeros((1, 64, 8), dtype=torch.bfloat16)
+        moe.moe_lora_apply(torch.zeros((2, 64), dtype=torch.bfloat16), torch.zeros(2, dtype=i32),
+                           b.view(1, 8, 64), b)
+    with pytest.raises(TypeError):
+        moe.moe_route_scored(torch.zeros(2, 8), "two")
+
+
+def test_operator_calls_reject_bad_shapes_before_launch(L):
+    f = L.moe_route_scored
+    base = dict(l=GOOD, dt=0, ld=64, b=None, T=4, E=64, s=0, g=1, tg=1, gt=1, k=4, km=4, rn=1,
+                sc=1.0, ids=GOOD, w=GOOD, kd=GOOD)
+
+    def route(**over):
+        a = dict(base, **over)
+        return f(vp(a["l"]), a["dt"], a["ld"], a["b"], a["T"], a["E"], a["s"], a["g"], a["tg"],
+                 a["gt"], a["k"], a["km"], a["rn"], ctypes.c_float(a["sc"]), vp(a["ids"]),
+                 vp(a["w"]), vp(a["kd"]), None)
+    for bad in (dict(E=0), dict(E=1025), dict(ld=63), dict(k=5), dict(km=17), dict(g=3),
+                dict(g=4, tg=5), dict(gt=0), dict(s=2), dict(dt=2), dict(sc=0.0), dict(kd=0),
+                dict(ids=0), dict(w=GOOD + 2), dict(l=GOOD + 2), dict(T=-1), dict(b=vp(GOOD + 1))):
+        assert route(**bad) == 1, bad
+    b = L.moe_route_scored_backward
+
+    def back(T=4, E=64, ws=GOOD, wsb=1 << 30, d=GOOD * 2, bal=0.0, counts=None, losses=GOOD):
+        return b(vp(GOOD), 0, 64, vp(GOOD), vp(GOOD), counts, T, E, 0, 2, 2, 1, ctypes.c_float(1),
+                 ctypes.c_float(bal), ctypes.c_float(0), vp(d), 64, vp(losses), vp(ws), wsb, None)
+    assert back(wsb=16) == 1 and back(d=GOOD) == 1 and back(bal=0.1) == 1
+    assert back(E=2000) == 1 and back(losses=0) == 1 and back(ws=0) == 1 and back(T=-1) == 1
+    c = L.moe_combine_backward
+    args = [vp(GOOD), vp(GOOD), 0, vp(GOOD), vp(GOOD), vp(GOOD), 4, 2, 128, vp(GOOD), None, None]
+    for i, v in ((2, 5), (7, 0), (7, 17), (8, 100), (0, vp(GOOD + 4)), (5, None), (10, vp(GOOD))):
+        bad = list(args)
+        bad[i] = v
+        assert c(*bad) == 1, i
+    a = L.moe_lora_apply
+    good = [vp(GOOD), 1, vp(GOOD), None, None, None, 4, 1, 1, 3, 128, 128, 16, vp(GOOD), vp(GOOD),
+            None, vp(GOOD), 0, 0, 0, vp(GOOD), vp(GOOD), 1 << 30, None]
+    for i, v, st in ((6, -1, 1), (7, 2, 1), (8, 4, 1), (9, 0, 1), (10, 96, 1), (11, 100, 1),
+                     (12, 12, 1), (12, 136, 1), (13, None, 1), (16, vp(GOOD + 8), 1), (17, 1, 2),
+                     (18, 2, 1), (19, 7, 1), (20, None, 1), (22, 8, 1), (3, vp(GOOD), 1)):
+        bad = list(good)
+        bad[i] = v
+        assert a(*bad) == st, i
+    assert L.moe_permute_masked(vp(GOOD), vp(GOOD), 4, 2, 8, -2, vp(GOOD), vp(GOOD), vp(GOOD),
+                                vp(GOOD), None) == 1
+    assert L.moe_router_logits(vp(GOOD), vp(GOOD), None, ctypes.c_float(0), 4, 256, 8, vp(GOOD),
+                               None) == 1
+    assert L.moe_router_logits(vp(GOOD), vp(GOOD), None, ctypes.c_float(1), 4, 100, 8, vp(GOOD),
+                               None) == 1
