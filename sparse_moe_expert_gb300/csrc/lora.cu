@@ -4,14 +4,14 @@
 // in an expert layer, to expert e.  Page "Qwen3.5-MoE与Qwen3-MoE架构差异深度
 // 解析", section 4.4 (expert-level LoRA).
 //
-// Two kernels: the shrink v[r] = scale x[r] A^T (contraction over K, rank R
-// wide) and the expand out[r] = base[r] + v[r] B^T (contraction over R).
-// Both are bound by memory: a matrix of one adapter is read for a handful of
-// rows, or x, base and out are streamed past a small matrix.  Operands go
-// from global memory straight into mma.sync fragments: the order of the
-// contraction index is free, so lane t of a quad takes contiguous elements
-// of its row (16 bytes of x and A, 8 bytes of B) and no shared-memory
-// staging is needed.
+// Bound by memory: one adapter's matrices are read for a handful of rows, or
+// x, base and out are streamed past small matrices (lora_tc.cu).
+//
+// Few rows (this file): a cluster of CTAs per row, one launch.  The CTAs share
+// K, join their parts of v = scale x A^T through distributed shared memory,
+// and share the columns of v B^T; the first columns of B and base are
+// requested before the join, so both matrices are on their way at once.
+// MEASURED_PLACEHOLDER
 #include "lora.cuh"
 
 namespace moe {
@@ -29,179 +29,175 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// v[r, j] = scale * sum_k x[r, k] A[j, k].  One CTA per row; the warps take
-// blocks of 32 k in turn and their sums are added in warp order.  NT: eights
-// of the rank (rounded up).
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(r)
+               : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
+template <bool BF16>
+__device__ __forceinline__ float load_value(const void* base, int64_t at) {
+  if constexpr (BF16) return bf16_bits_to_f32(static_cast<const uint16_t*>(base)[at]);
+  return static_cast<const float*>(base)[at];
+}
+
+// sum_j v[j] B[n, j] for the R values of one row of B, four partial sums.
 template <int NT>
-__global__ void __launch_bounds__(kLoraThreads) lora_shrink_kernel(LoraParams p) {
-  __shared__ float red[kLoraWarps][NT * 8];
-  pdl_wait();
-  pdl_trigger();
-  const int r = blockIdx.x;
-  if (r >= lora_rows(p)) return;
-  const LoraRow row = lora_row(p, r);
-  if (row.slot < 0) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int nt = p.R >> 3;
-  const uint4* xr = reinterpret_cast<const uint4*>(p.x + row.x_row * p.K) + t;
-  const uint4* ar = reinterpret_cast<const uint4*>(p.a + ((int64_t)row.slot * p.R + g) * p.K) + t;
-  const int64_t astep = (int64_t)p.K;  // 8 rows of A in uint4
-  float acc[NT][4];
+__device__ __forceinline__ float dot_row(const uint4 (&b)[NT], const float* v, int nt) {
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int q = 0; q < NT; ++q)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[q][i] = 0.0f;
-  const int blocks = p.K >> 5;
-#pragma unroll 2
-  for (int kb = warp; kb < blocks; kb += kLoraWarps) {
-    uint4 xv = make_uint4(0u, 0u, 0u, 0u);
-    if (g == 0) xv = __ldg(xr + kb * 4);
-    uint4 av[NT];
-#pragma unroll
-    for (int q = 0; q < NT; ++q)
-      if (q < nt) av[q] = ldg_nc_v4(ar + q * astep + kb * 4);
-    const uint32_t f0[4] = {xv.x, 0u, xv.y, 0u}, f1[4] = {xv.z, 0u, xv.w, 0u};
-#pragma unroll
-    for (int q = 0; q < NT; ++q)
-      if (q < nt) {
-        mma_bf16(acc[q], f0, av[q].x, av[q].y);
-        mma_bf16(acc[q], f1, av[q].z, av[q].w);
-      }
-  }
-  if (g == 0) {
-#pragma unroll
-    for (int q = 0; q < NT; ++q) {
-      red[warp][q * 8 + 2 * t] = acc[q][0];
-      red[warp][q * 8 + 2 * t + 1] = acc[q][1];
+    if (q < nt) {
+      const float4 lo = *reinterpret_cast<const float4*>(v + 8 * q);
+      const float4 hi = *reinterpret_cast<const float4*>(v + 8 * q + 4);
+      const float2 a = bf16x2_to_f32x2(b[q].x), c = bf16x2_to_f32x2(b[q].y),
+                   d = bf16x2_to_f32x2(b[q].z), e = bf16x2_to_f32x2(b[q].w);
+      acc[0] = fmaf(lo.x, a.x, acc[0]);
+      acc[1] = fmaf(lo.y, a.y, acc[1]);
+      acc[2] = fmaf(lo.z, c.x, acc[2]);
+      acc[3] = fmaf(lo.w, c.y, acc[3]);
+      acc[0] = fmaf(hi.x, d.x, acc[0]);
+      acc[1] = fmaf(hi.y, d.y, acc[1]);
+      acc[2] = fmaf(hi.z, e.x, acc[2]);
+      acc[3] = fmaf(hi.w, e.y, acc[3]);
     }
-  }
-  __syncthreads();
-  if (threadIdx.x < p.R) {
-    float s = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kLoraWarps; ++w) s += red[w][threadIdx.x];
-    const float sc = p.scales ? __ldg(p.scales + row.slot / p.E) : 1.0f;
-    p.v[(int64_t)r * p.R + threadIdx.x] = s * sc;
-  }
+  return (acc[0] + acc[1]) + (acc[2] + acc[3]);
 }
 
-// Eight consecutive values of a row of base (fp32 or bf16).
-template <bool BF16>
-__device__ __forceinline__ void load8(float (&f)[8], const void* base, int64_t at) {
-  if constexpr (BF16) {
-    const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
-    const uint32_t w4[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 v = bf16x2_to_f32x2(w4[i]);
-      f[2 * i] = v.x;
-      f[2 * i + 1] = v.y;
-    }
-  } else {
-    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-    const float4 a = q[0], b = q[1];
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-  }
-}
-
-template <bool BF16>
-__device__ __forceinline__ void store8(void* out, int64_t at, const float (&f)[8]) {
-  if constexpr (BF16) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = (uint32_t)f32_to_bf16_rne(f[2 * i]) | ((uint32_t)f32_to_bf16_rne(f[2 * i + 1]) << 16);
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-    float4* q = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-    q[0] = make_float4(f[0], f[1], f[2], f[3]);
-    q[1] = make_float4(f[4], f[5], f[6], f[7]);
-  }
-}
-
-// Three bf16 terms whose sum is the fp32 value to 2^-26 of it (two values packed per word).
-__device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-  const uint32_t ah = f32_to_bf16_rne(a), bh = f32_to_bf16_rne(b);
-  const float ar = a - bf16_bits_to_f32(ah), br = b - bf16_bits_to_f32(bh);
-  const uint32_t am = f32_to_bf16_rne(ar), bm = f32_to_bf16_rne(br);
-  const uint32_t al = f32_to_bf16_rne(ar - bf16_bits_to_f32(am));
-  const uint32_t bl = f32_to_bf16_rne(br - bf16_bits_to_f32(bm));
-  hi = ah | (bh << 16);
-  mid = am | (bm << 16);
-  lo = al | (bl << 16);
-}
-
-// acc[q] += v (one row, lanes with g = 0) B^T for the lane's 32-column block at
-// `col`: column 2t + i of eight q is column 8t + 2q + i of the block, so a
-// lane ends with eight consecutive columns.
-__device__ __forceinline__ void expand_block(float (&acc)[4][4], const LoraParams& p, int64_t slot,
-                                             const float* v, bool live, int col) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const uint16_t* b0 = p.b + (slot * p.N + col + 8 * (g >> 1) + (g & 1)) * p.R + 4 * t;
-  for (int s = 0; s < p.R; s += 16) {
-    const bool in = s + 4 * t < p.R;
-    uint2 bq[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      bq[q] = in ? __ldg(reinterpret_cast<const uint2*>(b0 + (int64_t)(2 * q) * p.R + s))
-                 : make_uint2(0u, 0u);
-    float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (in && live) f = *reinterpret_cast<const float4*>(v + s + 4 * t);
-    uint32_t h0, m0, l0, h1, m1, l1;
-    split3(f.x, f.y, h0, m0, l0);
-    split3(f.z, f.w, h1, m1, l1);
-    const uint32_t fh[4] = {h0, 0u, h1, 0u}, fm[4] = {m0, 0u, m1, 0u}, fl[4] = {l0, 0u, l1, 0u};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      mma_bf16(acc[q], fl, bq[q].x, bq[q].y);
-      mma_bf16(acc[q], fm, bq[q].x, bq[q].y);
-      mma_bf16(acc[q], fh, bq[q].x, bq[q].y);
-    }
-  }
-}
-
-// out[r, n] = base[r, n] + sum_j v[r, j] B[n, j], or SiLU(gate) * up of it.
-template <bool BASE_BF16, bool OUT_BF16, bool SWIGLU>
-__global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(LoraParams p) {
+// One row per cluster.  x A^T: the warps take blocks of 32 k in turn; lane
+// (g, t) holds 8 consecutive k (t) of row g of each eight of A as an
+// mma.sync fragment (the order of the contraction index is free), so that
+// the tensor core also adds over the lanes; the row of x is row 0 of the
+// tile.  v B^T: one column per lane, fp32.  NT: eights of the rank (rounded
+// up).
+template <int NT, bool BASE_BF16, bool OUT_BF16, bool SWIGLU>
+__global__ void __launch_bounds__(kLoraThreads) lora_row_kernel(LoraParams p, int ctas) {
+  __shared__ __align__(16) float red[kLoraWarps][NT * 8];
+  __shared__ __align__(16) float part[NT * 8];
+  __shared__ __align__(16) float v[NT * 8];
   pdl_wait();
   pdl_trigger();
-  const int r = blockIdx.x;
-  if (r >= lora_rows(p)) return;
+  const int r = blockIdx.x / ctas, rank = blockIdx.x % ctas;
+  if (r >= lora_rows(p)) return;  // the whole cluster alike
   const LoraRow row = lora_row(p, r);
-  if (row.slot < 0 && !SWIGLU && p.base == p.out) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int nt = p.R >> 3;
   const int cols = SWIGLU ? p.N / 2 : p.N;
-  for (int col = (blockIdx.y * kLoraWarps + warp) * 32; col < cols;
-       col += gridDim.y * kLoraWarps * 32) {
-    float f[SWIGLU ? 2 : 1][8];
+  constexpr int H = SWIGLU ? 2 : 1;
+  const int first = (rank * kLoraWarps + warp) * 32 + lane;  // this lane's first column
+  const int64_t base_row = (int64_t)r * p.N;
+  const uint16_t* bm = p.b + (int64_t)max(row.slot, 0) * p.N * p.R;
+  uint4 b[H][NT];
+  float z[H];
+  auto fetch = [&](int c) {
 #pragma unroll
-    for (int h = 0; h < (SWIGLU ? 2 : 1); ++h) {
-      float acc[4][4];
-      float b8[8];
+    for (int h = 0; h < H; ++h) {
+      z[h] = p.base ? load_value<BASE_BF16>(p.base, base_row + h * cols + c) : 0.0f;
+      if (row.slot >= 0) {
+        const uint4* src = reinterpret_cast<const uint4*>(bm + ((int64_t)h * cols + c) * p.R);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) b8[i] = 0.0f;
-      if (g == 0 && p.base) load8<BASE_BF16>(b8, p.base, (int64_t)r * p.N + h * cols + col + 8 * t);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        acc[q][0] = b8[2 * q];
-        acc[q][1] = b8[2 * q + 1];
-        acc[q][2] = acc[q][3] = 0.0f;
-      }
-      if (row.slot >= 0)
-        expand_block(acc, p, row.slot, p.v + (int64_t)r * p.R, g == 0, h * cols + col);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        f[h][2 * q] = acc[q][0];
-        f[h][2 * q + 1] = acc[q][1];
+        for (int q = 0; q < NT; ++q)
+          if (q < nt) b[h][q] = __ldg(src + q);
       }
     }
-    if constexpr (SWIGLU) {
+  };
+  if (row.slot >= 0) {
+    const uint4* xr = reinterpret_cast<const uint4*>(p.x + row.x_row * p.K) + t;
+    const uint4* ar = reinterpret_cast<const uint4*>(p.a + ((int64_t)row.slot * p.R + g) * p.K) + t;
+    float acc[NT][4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[0][i] = swiglu_f32(f[0][i], f[1][i]);
+    for (int q = 0; q < NT; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[q][i] = 0.0f;
+    const int blocks = p.K >> 5;
+#pragma unroll 2
+    for (int kb = rank * kLoraWarps + warp; kb < blocks; kb += ctas * kLoraWarps) {
+      uint4 xv = make_uint4(0u, 0u, 0u, 0u);
+      if (g == 0) xv = __ldg(xr + kb * 4);
+      uint4 av[NT];
+#pragma unroll
+      for (int q = 0; q < NT; ++q)
+        if (q < nt) av[q] = ldg_nc_v4(ar + (int64_t)q * p.K + kb * 4);
+      const uint32_t f0[4] = {xv.x, 0u, xv.y, 0u}, f1[4] = {xv.z, 0u, xv.w, 0u};
+#pragma unroll
+      for (int q = 0; q < NT; ++q)
+        if (q < nt) {
+          mma_bf16(acc[q], f0, av[q].x, av[q].y);
+          mma_bf16(acc[q], f1, av[q].z, av[q].w);
+        }
     }
-    if (g == 0) store8<OUT_BF16>(p.out, (int64_t)r * cols + col + 8 * t, f[0]);
+    if (NT <= 8 && first < cols) fetch(first);
+    if (g == 0) {
+#pragma unroll
+      for (int q = 0; q < NT; ++q) {
+        red[warp][q * 8 + 2 * t] = acc[q][0];
+        red[warp][q * 8 + 2 * t + 1] = acc[q][1];
+      }
+    }
+    __syncthreads();
+    if (tid < p.R) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kLoraWarps; ++w) s += red[w][tid];
+      part[tid] = s;
+    }
+    cluster_barrier();
+    if (tid < p.R) {
+      float s = 0.0f;
+      for (int c = 0; c < ctas; ++c) {  // rank order
+        float q;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q) : "r"(cluster_addr(part + tid, c)));
+        s += q;
+      }
+      v[tid] = s * (p.scales ? __ldg(p.scales + row.slot / p.E) : 1.0f);
+    }
+    __syncthreads();
+    // no CTA may leave while another reads its part: arrive now, wait at the end
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   }
+  if (row.slot >= 0 || SWIGLU || p.base != p.out) {
+    for (int c = first; c < cols; c += ctas * kLoraThreads) {
+      if (row.slot < 0 || NT > 8 || c != first) fetch(c);
+      if (row.slot >= 0) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) z[h] += dot_row<NT>(b[h], v, nt);
+      }
+      float o = z[0];
+      if constexpr (SWIGLU) o = swiglu_f32(z[0], z[H - 1]);
+      const int64_t at = (int64_t)r * cols + c;
+      if constexpr (OUT_BF16) static_cast<uint16_t*>(p.out)[at] = f32_to_bf16_rne(o);
+      else static_cast<float*>(p.out)[at] = o;
+    }
+  }
+  if (row.slot >= 0) {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+}
+
+template <int NT, bool BASE_BF16, bool OUT_BF16, bool SWIGLU>
+moe_status_t launch_rows(const LoraParams& p, int rows, int ctas, cudaStream_t st) {
+  return moe_host::launch_clusters(lora_row_kernel<NT, BASE_BF16, OUT_BF16, SWIGLU>,
+                                   dim3((unsigned)rows * ctas), kLoraThreads, 0, dim3(ctas), st, p,
+                                   ctas);
+}
+
+template <bool BASE_BF16, bool OUT_BF16, bool SWIGLU>
+moe_status_t lora_few(const LoraParams& p, int rows, cudaStream_t st) {
+  // CTAs per row: the whole of K and N in one or two steps of each for a
+  // single request; fewer when the rows alone fill the SMs
+  int ctas = 8;
+  while (ctas > 1 && (int64_t)rows * ctas > 8 * moe_host::sm_count()) ctas >>= 1;
+  if (p.R <= 16) return launch_rows<2, BASE_BF16, OUT_BF16, SWIGLU>(p, rows, ctas, st);
+  if (p.R <= 32) return launch_rows<4, BASE_BF16, OUT_BF16, SWIGLU>(p, rows, ctas, st);
+  if (p.R <= 64) return launch_rows<8, BASE_BF16, OUT_BF16, SWIGLU>(p, rows, ctas, st);
+  return launch_rows<16, BASE_BF16, OUT_BF16, SWIGLU>(p, rows, ctas, st);
 }
 
 }  // namespace
@@ -236,9 +232,8 @@ struct LoraSpace {
 LoraSpace lora_space(int64_t rows, int E, int n_adapters, int R) {
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   LoraSpace s{};
-  const size_t one = (size_t)(rows ? rows : 1) * R * sizeof(float);
   if (!lora_groups(rows, E, n_adapters)) {
-    s.total = one;
+    s.total = 256;  // the rows' form needs none; a size of 0 means bad arguments
     return s;
   }
   s.rows = up((size_t)rows * kLoraMaxTerms * rank_pad(R) * sizeof(uint16_t));
@@ -323,18 +318,8 @@ extern "C" moe_status_t moe_lora_apply(const uint16_t* x, int x_by_token,
                         !swiglu && base == out};
     return lora_grouped(p, plan, rows, swiglu, out_dtype == MOE_DTYPE_BF16, st);
   }
-  moe_status_t s;
-  if (R <= 16) s = launch(lora_shrink_kernel<2>, rows, kLoraThreads, 0, st, p);
-  else if (R <= 32) s = launch(lora_shrink_kernel<4>, rows, kLoraThreads, 0, st, p);
-  else if (R <= 64) s = launch(lora_shrink_kernel<8>, rows, kLoraThreads, 0, st, p);
-  else s = launch(lora_shrink_kernel<16>, rows, kLoraThreads, 0, st, p);
-  if (s != MOE_OK) return s;
-  const int cols = swiglu ? N / 2 : N;
-  const dim3 grid(rows, (cols + kLoraWarps * 32 - 1) / (kLoraWarps * 32));
   const bool bf = out_dtype == MOE_DTYPE_BF16;
   if (swiglu)
-    return bf ? launch(lora_expand_kernel<false, true, true>, grid, kLoraThreads, 0, st, p)
-              : launch(lora_expand_kernel<false, false, true>, grid, kLoraThreads, 0, st, p);
-  return bf ? launch(lora_expand_kernel<true, true, false>, grid, kLoraThreads, 0, st, p)
-            : launch(lora_expand_kernel<false, false, false>, grid, kLoraThreads, 0, st, p);
+    return bf ? lora_few<false, true, true>(p, rows, st) : lora_few<false, false, true>(p, rows, st);
+  return bf ? lora_few<true, true, false>(p, rows, st) : lora_few<false, false, false>(p, rows, st);
 }

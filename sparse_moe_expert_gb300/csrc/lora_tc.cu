@@ -830,31 +830,6 @@ moe_status_t launch_expand(const LoraParams& p, const LoraPlan& plan, cudaStream
   return launch(kern, (int)grid, kExpandThreads, smem, st, p, plan);
 }
 
-// moe_host::launch with thread-block clusters.
-template <typename... KArgs, typename... Args>
-moe_status_t launch_clusters(void (*kern)(KArgs...), dim3 grid, int block, size_t smem,
-                             dim3 cluster, cudaStream_t st, Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster.x;
-  attr[0].val.clusterDim.y = cluster.y;
-  attr[0].val.clusterDim.z = cluster.z;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = moe_host::pdl_enabled() ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...) != cudaSuccess) {
-    cudaGetLastError();
-    return MOE_ERR_CUDA;
-  }
-  return MOE_OK;
-}
-
 template <int NT>
 moe_status_t launch_shrink(const LoraParams& p, const LoraPlan& plan, int terms, cudaStream_t st) {
   using namespace moe_host;
@@ -879,7 +854,7 @@ moe_status_t launch_shrink(const LoraParams& p, const LoraPlan& plan, int terms,
   const int per_sm = NT <= 8 ? 2 : 1;
   int64_t clusters = (int64_t)sm_count() * per_sm / plan.splits;
   if (clusters > plan.capacity) clusters = plan.capacity;
-  return launch_clusters(lora_shrink_tc_kernel<NT>, dim3((unsigned)(clusters * plan.splits)),
+  return moe_host::launch_clusters(lora_shrink_tc_kernel<NT>, dim3((unsigned)(clusters * plan.splits)),
                          kShrinkThreads, smem, dim3(plan.splits), st, p, plan, terms, tmem_cols);
 }
 
@@ -899,7 +874,7 @@ moe_status_t lora_grouped(const LoraParams& p, const LoraPlan& plan, int64_t row
   // CTAs per expert: one per 1024 of the rows that an expert has on average
   int ranges = 1;
   while (ranges < 8 && (int64_t)ranges * 1024 * p.E < rows) ranges *= 2;
-  moe_status_t s = launch_clusters(lora_plan_kernel, dim3(p.E, ranges), kPlanThreads, plan_smem,
+  moe_status_t s = moe_host::launch_clusters(lora_plan_kernel, dim3(p.E, ranges), kPlanThreads, plan_smem,
                                    dim3(1, ranges), st, p, plan);
   if (s != MOE_OK) return s;
   const int terms = out_bf16 && !swiglu ? 2 : 3;
