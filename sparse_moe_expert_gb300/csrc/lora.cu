@@ -47,37 +47,54 @@ __device__ __forceinline__ float load_value(const void* base, int64_t at) {
   return static_cast<const float*>(base)[at];
 }
 
-// sum_j v[j] B[n, j] for the R values of one row of B, four partial sums.
-template <int NT>
-__device__ __forceinline__ float dot_row(const uint4 (&b)[NT], const float* v, int nt) {
+// Sum of 16 products, four partial sums: two 16-byte pieces of a row of B with
+// the same entries of v.
+__device__ __forceinline__ float dot16(const uint4 (&b)[2], const float (&v)[16]) {
   float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int q = 0; q < NT; ++q)
-    if (q < nt) {
-      const float4 lo = *reinterpret_cast<const float4*>(v + 8 * q);
-      const float4 hi = *reinterpret_cast<const float4*>(v + 8 * q + 4);
-      const float2 a = bf16x2_to_f32x2(b[q].x), c = bf16x2_to_f32x2(b[q].y),
-                   d = bf16x2_to_f32x2(b[q].z), e = bf16x2_to_f32x2(b[q].w);
-      acc[0] = fmaf(lo.x, a.x, acc[0]);
-      acc[1] = fmaf(lo.y, a.y, acc[1]);
-      acc[2] = fmaf(lo.z, c.x, acc[2]);
-      acc[3] = fmaf(lo.w, c.y, acc[3]);
-      acc[0] = fmaf(hi.x, d.x, acc[0]);
-      acc[1] = fmaf(hi.y, d.y, acc[1]);
-      acc[2] = fmaf(hi.z, e.x, acc[2]);
-      acc[3] = fmaf(hi.w, e.y, acc[3]);
+  for (int q = 0; q < 2; ++q) {
+    const uint32_t w[4] = {b[q].x, b[q].y, b[q].z, b[q].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = bf16x2_to_f32x2(w[i]);
+      acc[i] = fmaf(v[8 * q + 2 * i], f.x, acc[i]);
+      acc[i] = fmaf(v[8 * q + 2 * i + 1], f.y, acc[i]);
     }
+  }
   return (acc[0] + acc[1]) + (acc[2] + acc[3]);
+}
+
+// L values per lane, L lanes (neighbours) per column: lane s of the L gets the
+// sum over them of value s.
+template <int L>
+__device__ __forceinline__ float reduce_lanes(float (&a)[L]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int off = L / 2; off >= 1; off >>= 1) {
+    const bool hi = (lane & off) != 0;
+#pragma unroll
+    for (int j = 0; j < off; ++j) {
+      const float keep = hi ? a[j + off] : a[j];
+      const float send = hi ? a[j] : a[j + off];
+      a[j] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, off);
+    }
+  }
+  return a[0];
 }
 
 // One row per cluster.  x A^T: the warps take blocks of 32 k in turn; lane
 // (g, t) holds 8 consecutive k (t) of row g of each eight of A as an
 // mma.sync fragment (the order of the contraction index is free), so that
 // the tensor core also adds over the lanes; the row of x is row 0 of the
-// tile.  v B^T: one column per lane, fp32.  NT: eights of the rank (rounded
-// up).
+// tile.  v B^T in fp32: a warp takes 32 columns, L = NT / 2 lanes to a row of
+// B (neighbouring 16-byte pieces, so that a load covers whole sectors of few
+// rows), and a reduce-scatter leaves every lane with one column.  NT: eights
+// of the rank (rounded up).
+// CTAs of the row kernel that an SM holds at once, by registers.
+constexpr int row_ctas_per_sm(int NT) { return NT <= 4 ? 4 : NT <= 8 ? 2 : 1; }
+
 template <int NT, bool BASE_BF16, bool OUT_BF16, bool SWIGLU>
-__global__ void __launch_bounds__(kLoraThreads) lora_row_kernel(LoraParams p, int ctas) {
+__global__ void __launch_bounds__(kLoraThreads, row_ctas_per_sm(NT)) lora_row_kernel(LoraParams p, int ctas) {
   __shared__ __align__(16) float red[kLoraWarps][NT * 8];
   __shared__ __align__(16) float part[NT * 8];
   __shared__ __align__(16) float v[NT * 8];
@@ -90,20 +107,36 @@ __global__ void __launch_bounds__(kLoraThreads) lora_row_kernel(LoraParams p, in
   const int nt = p.R >> 3;
   const int cols = SWIGLU ? p.N / 2 : p.N;
   constexpr int H = SWIGLU ? 2 : 1;
-  const int first = (rank * kLoraWarps + warp) * 32 + lane;  // this lane's first column
+  // columns a lane takes at once (more cost registers, and with them CTAs)
+  constexpr int U = NT * H <= 2 ? 2 : 1;
+  constexpr int L = NT / 2;  // lanes of a row of B
+  const int stride = ctas * kLoraThreads;
+  const int first = (rank * kLoraWarps + warp) * 32;         // this warp's first columns
+  const int own = (lane % L) * (32 / L) + lane / L;          // the lane's among 32
   const int64_t base_row = (int64_t)r * p.N;
   const uint16_t* bm = p.b + (int64_t)max(row.slot, 0) * p.N * p.R;
-  uint4 b[H][NT];
-  float z[H];
-  auto fetch = [&](int c) {
+  uint4 b[U][H][L][2];
+  float z[U][H];
+  auto fetch = [&](int c0) {
 #pragma unroll
-    for (int h = 0; h < H; ++h) {
-      z[h] = p.base ? load_value<BASE_BF16>(p.base, base_row + h * cols + c) : 0.0f;
-      if (row.slot >= 0) {
-        const uint4* src = reinterpret_cast<const uint4*>(bm + ((int64_t)h * cols + c) * p.R);
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u * stride;
+      if (c < cols) {
 #pragma unroll
-        for (int q = 0; q < NT; ++q)
-          if (q < nt) b[h][q] = __ldg(src + q);
+        for (int h = 0; h < H; ++h) {
+          z[u][h] = p.base ? load_value<BASE_BF16>(p.base, base_row + h * cols + c + own) : 0.0f;
+          if (row.slot >= 0) {
+            const uint4* src = reinterpret_cast<const uint4*>(
+                bm + ((int64_t)h * cols + c + lane / L) * p.R) + lane % L;
+            const int64_t step = (int64_t)(32 / L) * p.R / 8;
+#pragma unroll
+            for (int i = 0; i < L; ++i)
+#pragma unroll
+              for (int q = 0; q < 2; ++q)
+                if (lane % L + L * q < nt) b[u][h][i][q] = __ldg(src + i * step + L * q);
+                else b[u][h][i][q] = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
       }
     }
   };
@@ -116,7 +149,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_row_kernel(LoraParams p, in
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[q][i] = 0.0f;
     const int blocks = p.K >> 5;
-#pragma unroll 2
+#pragma unroll(NT <= 4 ? 4 : 2)
     for (int kb = rank * kLoraWarps + warp; kb < blocks; kb += ctas * kLoraWarps) {
       uint4 xv = make_uint4(0u, 0u, 0u, 0u);
       if (g == 0) xv = __ldg(xr + kb * 4);
@@ -132,7 +165,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_row_kernel(LoraParams p, in
           mma_bf16(acc[q], f1, av[q].z, av[q].w);
         }
     }
-    if (NT <= 8 && first < cols) fetch(first);
+    if (first < cols) fetch(first);
     if (g == 0) {
 #pragma unroll
       for (int q = 0; q < NT; ++q) {
@@ -162,17 +195,35 @@ __global__ void __launch_bounds__(kLoraThreads) lora_row_kernel(LoraParams p, in
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   }
   if (row.slot >= 0 || SWIGLU || p.base != p.out) {
-    for (int c = first; c < cols; c += ctas * kLoraThreads) {
-      if (row.slot < 0 || NT > 8 || c != first) fetch(c);
-      if (row.slot >= 0) {
+    float vr[16];
+    if (row.slot >= 0) {
 #pragma unroll
-        for (int h = 0; h < H; ++h) z[h] += dot_row<NT>(b[h], v, nt);
+      for (int i = 0; i < 16; ++i) {
+        const int j = (lane % L + L * (i / 8)) * 8 + i % 8;
+        vr[i] = j < p.R ? v[j] : 0.0f;
       }
-      float o = z[0];
-      if constexpr (SWIGLU) o = swiglu_f32(z[0], z[H - 1]);
-      const int64_t at = (int64_t)r * cols + c;
-      if constexpr (OUT_BF16) static_cast<uint16_t*>(p.out)[at] = f32_to_bf16_rne(o);
-      else static_cast<float*>(p.out)[at] = o;
+    }
+    for (int c0 = first; c0 < cols; c0 += U * stride) {
+      if (row.slot < 0 || c0 != first) fetch(c0);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + u * stride;
+        if (c >= cols) break;
+        if (row.slot >= 0) {
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            float a[L];
+#pragma unroll
+            for (int i = 0; i < L; ++i) a[i] = dot16(b[u][h][i], vr);
+            z[u][h] += reduce_lanes<L>(a);
+          }
+        }
+        float o = z[u][0];
+        if constexpr (SWIGLU) o = swiglu_f32(z[u][0], z[u][H - 1]);
+        const int64_t at = (int64_t)r * cols + c + own;
+        if constexpr (OUT_BF16) static_cast<uint16_t*>(p.out)[at] = f32_to_bf16_rne(o);
+        else static_cast<float*>(p.out)[at] = o;
+      }
     }
   }
   if (row.slot >= 0) {
@@ -182,7 +233,10 @@ __global__ void __launch_bounds__(kLoraThreads) lora_row_kernel(LoraParams p, in
 }
 
 template <int NT, bool BASE_BF16, bool OUT_BF16, bool SWIGLU>
-moe_status_t launch_rows(const LoraParams& p, int rows, int ctas, cudaStream_t st) {
+moe_status_t launch_rows(const LoraParams& p, int rows, cudaStream_t st) {
+  // CTAs per row: as many as run at once without queueing, 8 at most
+  int ctas = row_ctas_per_sm(NT) * moe_host::sm_count() / rows;
+  ctas = ctas < 1 ? 1 : ctas > 8 ? 8 : ctas;
   return moe_host::launch_clusters(lora_row_kernel<NT, BASE_BF16, OUT_BF16, SWIGLU>,
                                    dim3((unsigned)rows * ctas), kLoraThreads, 0, dim3(ctas), st, p,
                                    ctas);
@@ -190,14 +244,10 @@ moe_status_t launch_rows(const LoraParams& p, int rows, int ctas, cudaStream_t s
 
 template <bool BASE_BF16, bool OUT_BF16, bool SWIGLU>
 moe_status_t lora_few(const LoraParams& p, int rows, cudaStream_t st) {
-  // CTAs per row: the whole of K and N in one or two steps of each for a
-  // single request; fewer when the rows alone fill the SMs
-  int ctas = 8;
-  while (ctas > 1 && (int64_t)rows * ctas > 8 * moe_host::sm_count()) ctas >>= 1;
-  if (p.R <= 16) return launch_rows<2, BASE_BF16, OUT_BF16, SWIGLU>(p, rows, ctas, st);
-  if (p.R <= 32) return launch_rows<4, BASE_BF16, OUT_BF16, SWIGLU>(p, rows, ctas, st);
-  if (p.R <= 64) return launch_rows<8, BASE_BF16, OUT_BF16, SWIGLU>(p, rows, ctas, st);
-  return launch_rows<16, BASE_BF16, OUT_BF16, SWIGLU>(p, rows, ctas, st);
+  if (p.R <= 16) return launch_rows<2, BASE_BF16, OUT_BF16, SWIGLU>(p, rows, st);
+  if (p.R <= 32) return launch_rows<4, BASE_BF16, OUT_BF16, SWIGLU>(p, rows, st);
+  if (p.R <= 64) return launch_rows<8, BASE_BF16, OUT_BF16, SWIGLU>(p, rows, st);
+  return launch_rows<16, BASE_BF16, OUT_BF16, SWIGLU>(p, rows, st);
 }
 
 }  // namespace

@@ -28,7 +28,8 @@ namespace {
 // ---- grouping --------------------------------------------------------------
 
 constexpr int kPlanThreads = 256;
-constexpr int kPlanUnroll = 8;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanUnroll = 4;
 
 // Tiles of an adapter's n rows.
 __device__ __forceinline__ int2 tiles_of(int n) {
@@ -59,21 +60,22 @@ __device__ __forceinline__ void cluster_barrier() {
 }
 
 // A cluster per expert e: CTA c of it counts its range of the expert's rows
-// per adapter (the last bin: none), learns the other ranges' counts through
-// distributed shared memory and places its rows; the first CTA also lists the
-// expert's tiles.  Rows of an adapter stay in order, so that every row meets
-// the same tile, and the same sums, each time; the order of the experts'
-// tiles is left open.
+// per adapter (the last bin: none), each warp its part of the range in
+// counters of its own, learns the other CTAs' counts through distributed
+// shared memory, and places its rows, the warps independently.  The first CTA
+// also lists the expert's tiles.  Rows of an adapter stay in order, so that
+// every row meets the same tile, and the same sums, each time; the order of
+// the experts' tiles is left open.
 __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(LoraParams p, LoraPlan pl) {
   extern __shared__ int plan_s[];
   pdl_wait();
   pdl_trigger();
   const int bins = p.n_adapters + 1;
-  int* own = plan_s;
-  int* cnt = own + bins;
-  int* cursor = cnt + bins;
-  int* start = cursor + bins;
-  const int tid = threadIdx.x, lane = tid & 31;
+  int* own = plan_s;                 // this CTA's counts
+  int* cnt = own + bins;             // the expert's
+  int* start = cnt + bins;           // first position of each adapter
+  int* cursor = start + bins;        // [warp][bins]: counts, then next positions
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int e = blockIdx.x, rows = lora_rows(p);
   const int ranges = gridDim.y, range = blockIdx.y;  // the cluster's size, the rank in it
   const int lo = p.sorted ? min(max(__ldg(p.offsets + e), 0), rows) : 0;
@@ -82,73 +84,83 @@ __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(LoraParams p, L
     if (p.E == 1 && range == 0 && tid == 0) *pl.counts = make_int4(0, 0, 0, 0);
     return;
   }
-  const int64_t per = ((int64_t)n + ranges - 1) / ranges;
-  const int c0 = (int)(per * range < n ? per * range : n);
-  const int c1 = (int)(c0 + per < n ? c0 + per : n);
-  for (int i = tid; i < bins; i += kPlanThreads) own[i] = 0;
+  // this warp's rows, whole groups of 32
+  const int64_t per = (((int64_t)n + ranges * kPlanWarps - 1) / (ranges * kPlanWarps) + 31) / 32 * 32;
+  const int64_t w0 = per * (range * kPlanWarps + warp);
+  const int c0 = (int)(w0 < n ? w0 : n), c1 = (int)(w0 + per < n ? w0 + per : n);
+  for (int i = tid; i < kPlanWarps * bins; i += kPlanThreads) cursor[i] = 0;
   __syncthreads();
   auto bin_of = [&](int i) {
     const int s = lora_row(p, lo + i).slot;
     return s < 0 ? p.n_adapters : p.E == 1 ? s : s / p.E;
   };
-  for (int i0 = c0; i0 < c1; i0 += kPlanThreads * kPlanUnroll) {
-    int b[kPlanUnroll];
+  int* mine = cursor + warp * bins;
+  int kept[kPlanUnroll];  // the bins of the warp's first rows
 #pragma unroll
-    for (int u = 0; u < kPlanUnroll; ++u) {
-      const int i = i0 + u * kPlanThreads + tid;
-      b[u] = i < c1 ? bin_of(i) : -1;
-    }
-#pragma unroll
-    for (int u = 0; u < kPlanUnroll; ++u)
-      if (b[u] >= 0) atomicAdd(&own[b[u]], 1);
+  for (int u = 0; u < kPlanUnroll; ++u) {
+    const int i = c0 + u * 32 + lane;
+    kept[u] = i < c1 ? bin_of(i) : -1;
   }
+#pragma unroll
+  for (int u = 0; u < kPlanUnroll; ++u)
+    if (kept[u] >= 0) atomicAdd(&mine[kept[u]], 1);
+  for (int i = c0 + kPlanUnroll * 32 + lane; i < c1; i += 32) atomicAdd(&mine[bin_of(i)], 1);
   __syncthreads();
-  if (ranges > 1) cluster_barrier();
+  // counts of the CTA, and where in it each warp's rows begin
   for (int x = tid; x < bins; x += kPlanThreads) {
-    int total = 0, before = 0;
-    for (int r = 0; r < ranges; ++r) {
-      int v = own[x];
-      if (r != range)
-        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(own + x, r)));
-      total += v;
-      if (r < range) before += v;
+    int sum = 0;
+    for (int w = 0; w < kPlanWarps; ++w) {
+      const int v = cursor[w * bins + x];
+      cursor[w * bins + x] = sum;
+      sum += v;
     }
-    cnt[x] = total;
-    cursor[x] = before;
+    own[x] = sum;
+    cnt[x] = sum;
   }
   __syncthreads();
-  if (ranges > 1) cluster_barrier();  // nobody's counts are needed any more
-  if (tid < 32) {
+  if (ranges > 1) {
+    cluster_barrier();
+    for (int x = tid; x < bins; x += kPlanThreads) {
+      int total = 0, before = 0;
+      for (int r = 0; r < ranges; ++r) {
+        int v;
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(own + x, r)));
+        total += v;
+        if (r < range) before += v;
+      }
+      cnt[x] = total;
+      for (int w = 0; w < kPlanWarps; ++w) cursor[w * bins + x] += before;
+    }
+    __syncthreads();
+    cluster_barrier();  // nobody's counts are needed any more
+  }
+  if (warp == 0) {
     int carry = 0;
     for (int x0 = 0; x0 < bins; x0 += 32) {
       const int x = x0 + lane;
       const int v = x < bins ? cnt[x] : 0;
       const int incl = warp_scan_incl(v);
-      if (x < bins) {
-        start[x] = carry + incl - v;
-        cursor[x] += carry + incl - v;
-      }
+      if (x < bins) start[x] = carry + incl - v;
       carry += __shfl_sync(0xFFFFFFFFu, incl, 31);
     }
   }
   __syncthreads();
-  for (int i0 = c0; i0 < c1; i0 += kPlanThreads) {
-    const int i = i0 + tid;
-    const int b = i < c1 ? bin_of(i) : -1;
+  auto place = [&](int i, int b) {  // the warp together
     const unsigned same = __match_any_sync(0xFFFFFFFFu, b);
     const int before = __popc(same & lanemask_lt());
     int at = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) {  // the warps in turn
-      if (tid >> 5 == w && b >= 0 && before == 0) {
-        at = cursor[b];
-        cursor[b] = at + __popc(same);
-      }
-      __syncthreads();
-    }
-    at = __shfl_sync(0xFFFFFFFFu, at, __ffs(same) - 1) + before;
-    if (b >= 0) pl.rows[lo + at] = make_int2(lo + i, lora_x_row(p, lo + i));
-  }
-  if (range != 0 || tid >= 32) return;
+    if (b >= 0) at = mine[b];
+    __syncwarp();
+    if (b >= 0 && before == 0) mine[b] = at + __popc(same);
+    __syncwarp();
+    if (b >= 0) pl.rows[lo + start[b] + at + before] = make_int2(lo + i, lora_x_row(p, lo + i));
+  };
+#pragma unroll
+  for (int u = 0; u < kPlanUnroll; ++u)
+    if (c0 + u * 32 < c1) place(c0 + u * 32 + lane, kept[u]);
+  for (int i0 = c0 + kPlanUnroll * 32; i0 < c1; i0 += 32)
+    place(i0 + lane, i0 + lane < c1 ? bin_of(i0 + lane) : -1);
+  if (range != 0 || warp != 0) return;
   // the tiles, one warp: their number first, then a scan over the adapters
   auto tiles_in = [&](int x) {
     if (x >= bins || (x == p.n_adapters && pl.skip_none)) return make_int2(0, 0);
@@ -866,7 +878,7 @@ moe_status_t lora_grouped(const LoraParams& p, const LoraPlan& plan, int64_t row
   // with several experts their CTAs add to the counts
   if (p.E > 1 && cudaMemsetAsync(plan.counts, 0, sizeof(int4), st) != cudaSuccess)
     return MOE_ERR_CUDA;
-  const size_t plan_smem = (size_t)4 * (p.n_adapters + 1) * sizeof(int);
+  const size_t plan_smem = (size_t)(3 + kPlanWarps) * (p.n_adapters + 1) * sizeof(int);
   if (plan_smem > 48 * 1024 &&
       cudaFuncSetAttribute(lora_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)plan_smem) != cudaSuccess)
