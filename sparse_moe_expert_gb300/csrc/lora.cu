@@ -257,19 +257,26 @@ using namespace moe;
 
 namespace {
 
-// From this many rows on they are grouped by adapter, if each adapter (and
-// expert) may expect two or more.
-constexpr int kLoraGroupRows = 192;
-
-bool lora_groups(int64_t rows, int E, int n_adapters) {
-  return rows >= kLoraGroupRows && rows >= 2 * (int64_t)n_adapters * E &&
-         n_adapters <= kLoraPlanAdapters;
+// Whether the rows are grouped by adapter (lora_tc.cu) or each gets its own
+// cluster.  A cluster costs its row's A and B from L2, so rows x rank; the
+// grouping costs two more launches and gains when rows share matrices.
+// Measured, K = N = 4096 bf16, us (own cluster / grouped): rank 16, 256 rows
+// 11.1 / 15.6 over 8 adapters, 13.2 / 25.1 over 64; rank 64, 64 rows 10.3 /
+// 18.1 over 8, 14.5 / 35.7 over 64; 96 rows 22.3 / 18.3 over 8, 31.9 / 39.3
+// over 64; 256 rows 30.6 / 21.5 over 8, 45.3 / 46.5 over 64.  Far more rows
+// are grouped even if every adapter could have few of them: which of the
+// adapters a batch uses is known on the device only.
+bool lora_groups(int64_t rows, int E, int n_adapters, int R) {
+  const int64_t cost = rows * R;
+  return n_adapters <= kLoraPlanAdapters &&
+         ((cost >= 6144 && rows >= 4 * (int64_t)n_adapters * E) || cost >= 32768);
 }
 
-// CTAs per tile in the grouped shrink: enough for two per SM when the tiles
-// alone are too few, with at least four k-blocks of 64 each.
-int lora_splits(int64_t rows, int K) {
-  const int64_t tiles = (rows + kLoraTileRows - 1) / kLoraTileRows;
+// CTAs per tile in the grouped shrink: as many as two per SM hold, with the
+// tiles that full ones and one rest per adapter make, and at least four
+// k-blocks of 64 each.
+int lora_splits(int64_t rows, int64_t slots, int K) {
+  const int64_t tiles = (rows + kLoraTileRows - 1) / kLoraTileRows + (slots < rows ? slots : rows);
   int s = 1;
   while (s < kLoraMaxSplit && 2 * s * tiles <= 2 * moe_host::sm_count() && 2 * s * 256 <= K) s *= 2;
   return s;
@@ -282,7 +289,7 @@ struct LoraSpace {
 LoraSpace lora_space(int64_t rows, int E, int n_adapters, int R) {
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   LoraSpace s{};
-  if (!lora_groups(rows, E, n_adapters)) {
+  if (!lora_groups(rows, E, n_adapters, R)) {
     s.total = 256;  // the rows' form needs none; a size of 0 means bad arguments
     return s;
   }
@@ -355,7 +362,7 @@ extern "C" moe_status_t moe_lora_apply(const uint16_t* x, int x_by_token,
   p.err = device_error_word();
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int rows = T * kmax;
-  if (lora_groups(rows, E, n_adapters)) {
+  if (lora_groups(rows, E, n_adapters, R)) {
     const LoraSpace sp = lora_space(rows, E, n_adapters, R);
     char* ws = static_cast<char*>(workspace);
     int4* tiles = reinterpret_cast<int4*>(ws + sp.tiles);
@@ -363,7 +370,7 @@ extern "C" moe_status_t moe_lora_apply(const uint16_t* x, int x_by_token,
                         tiles,
                         tiles + 1,
                         lora_tile_capacity(rows, E, n_adapters),
-                        lora_splits(rows, K),
+                        lora_splits(rows, (int64_t)E * n_adapters, K),
                         static_cast<uint16_t*>(workspace),
                         !swiglu && base == out};
     return lora_grouped(p, plan, rows, swiglu, out_dtype == MOE_DTYPE_BF16, st);

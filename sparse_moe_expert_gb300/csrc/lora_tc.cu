@@ -567,31 +567,52 @@ __device__ __forceinline__ void stage_v(const LoraPlan& pl, int RP, int first, i
   }
 }
 
-// One 32-column block (columns col .. of B's rows) of a small tile: acc[q]
-// holds, for rows g and g + 8, the lane's columns 8 t + 2 q + {0, 1}.
+// Operands of a small tile's 32-column block that do not wait for v: the
+// lane's pieces of B for the first 64 of the rank (columns col .. of B's rows,
+// in the order of the large units), requested before v has landed.
+struct SmallB {
+  uint2 q[4][4];  // [16 of the rank][eight columns]
+  __device__ __forceinline__ static uint2 piece(const uint16_t* b0, int R, int s, int i) {
+    const int t = threadIdx.x & 3;
+    return s + 4 * t < R ? __ldg(reinterpret_cast<const uint2*>(b0 + (int64_t)(2 * i) * R + s))
+                         : make_uint2(0u, 0u);
+  }
+  __device__ __forceinline__ void load(const uint16_t* b0, int R) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[s][i] = 16 * s < R ? piece(b0, R, 16 * s, i) : make_uint2(0u, 0u);
+  }
+};
+
+// acc[q] += v B^T for rows g and g + 8: the lane's columns 8 t + 2 q + {0, 1}.
 template <int TERMS>
-__device__ __forceinline__ void small_block(float (&acc)[4][4], const LoraParams& p, int slot,
-                                            int col, const unsigned char* vs) {
+__device__ __forceinline__ void small_step(float (&acc)[4][4], const uint2 (&bq)[4], int RP, int s,
+                                           const unsigned char* vs) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int RP = rank_pad(p.R);
-  const uint16_t* b0 = p.b + ((int64_t)slot * p.N + col + 8 * (g >> 1) + (g & 1)) * p.R + 4 * t;
-#pragma unroll 2
-  for (int s = 0; s < p.R; s += 16) {
-    const bool in = s + 4 * t < p.R;
+#pragma unroll
+  for (int x = TERMS - 1; x >= 0; --x) {  // the small terms first
+    const int c = x * RP + s + 4 * t;
+    const unsigned char* at = vs + (c >> 6) * kBlockBytes + (c & 4) * 2;
+    const uint2 lo = *reinterpret_cast<const uint2*>(at + sw128_offset(g, (c & 63) >> 3));
+    const uint2 hi = *reinterpret_cast<const uint2*>(at + sw128_offset(g + 8, (c & 63) >> 3));
+#pragma unroll
+    for (int q = 0; q < 4; ++q) mma_bf16(acc[q], lo.x, hi.x, lo.y, hi.y, bq[q].x, bq[q].y);
+  }
+}
+
+template <int TERMS>
+__device__ __forceinline__ void small_block(float (&acc)[4][4], const SmallB& b,
+                                            const uint16_t* b0, int R, const unsigned char* vs) {
+  const int RP = rank_pad(R);
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+    if (16 * s < R) small_step<TERMS>(acc, b.q[s], RP, 16 * s, vs);
+  for (int s = 64; s < R; s += 16) {
     uint2 bq[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      bq[q] = in ? __ldg(reinterpret_cast<const uint2*>(b0 + (int64_t)(2 * q) * p.R + s))
-                 : make_uint2(0u, 0u);
-#pragma unroll
-    for (int x = TERMS - 1; x >= 0; --x) {  // the small terms first
-      const int c = x * RP + s + 4 * t;
-      const unsigned char* at = vs + (c >> 6) * kBlockBytes + (c & 4) * 2;
-      const uint2 lo = *reinterpret_cast<const uint2*>(at + sw128_offset(g, (c & 63) >> 3));
-      const uint2 hi = *reinterpret_cast<const uint2*>(at + sw128_offset(g + 8, (c & 63) >> 3));
-#pragma unroll
-      for (int q = 0; q < 4; ++q) mma_bf16(acc[q], lo.x, hi.x, lo.y, hi.y, bq[q].x, bq[q].y);
-    }
+    for (int i = 0; i < 4; ++i) bq[i] = SmallB::piece(b0, R, s, i);
+    small_step<TERMS>(acc, bq, RP, s, vs);
   }
 }
 
@@ -762,55 +783,70 @@ __global__ void __launch_bounds__(kExpandThreads, BASE_BF16 ? 4 : 3) lora_expand
   const bool stop = __syncthreads_or(bad) != 0;
 
   cur_tile = -1;
+  constexpr int H = SWIGLU ? 2 : 1;
   const int64_t s1 = small * (blockIdx.x + 1) / gridDim.x;
   for (int64_t u = small * blockIdx.x / gridDim.x; u < s1 && !stop; ++u) {
-    const int ti = (int)(u / schunks), c0 = (int)(u % schunks) * sspan;
-    if (ti != cur_tile) {
+    const int ti = (int)(u / schunks), col = (int)(u % schunks) * sspan + warp * 32;
+    const bool fresh = ti != cur_tile;
+    if (fresh) {
       cur_tile = ti;
       tile = pl.tiles[pl.capacity - 1 - ti];
-      row_at[0] = g < tile.z ? (int64_t)pl.rows[tile.y + g].x : -1;
-      row_at[1] = g + 8 < tile.z ? (int64_t)pl.rows[tile.y + g + 8].x : -1;
       __syncthreads();  // no warp still reads the tile before
       stage_v<TERMS>(pl, RP, tile.y, tile.z, kLoraSmallRows, vs);
       cp_async_commit();
+      row_at[0] = g < tile.z ? (int64_t)pl.rows[tile.y + g].x : -1;
+      row_at[1] = g + 8 < tile.z ? (int64_t)pl.rows[tile.y + g + 8].x : -1;
+    }
+    const bool on = col < cols;  // the warp's 32 columns exist
+    SmallB sb[H];
+    Base8<BASE_BF16> b[H][2];
+    const uint16_t* b0[H];
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      b0[h] = p.b + ((int64_t)tile.x * p.N + h * cols + col + 8 * (g >> 1) + (g & 1)) * p.R + 4 * t;
+      if (on) {
+        sb[h].load(b0[h], p.R);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (p.base && row_at[i] >= 0)
+            b[h][i].load(p.base, row_at[i] * p.N + h * cols + col + 8 * t);
+          else
+            b[h][i].zero();
+        }
+      }
+    }
+    if (fresh) {
       cp_async_wait<0>();
       __syncthreads();
     }
-    for (int col = c0 + warp * 32; col < min(c0 + sspan, cols); col += kExpandThreads) {
-      float z[SWIGLU ? 2 : 1][2][8];
+    if (!on) continue;
+    float z[H][2][8];
 #pragma unroll
-      for (int h = 0; h < (SWIGLU ? 2 : 1); ++h) {
-        float acc[4][4];
-        Base8<BASE_BF16> b[2];
+    for (int h = 0; h < H; ++h) {
+      float acc[4][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (p.base && row_at[i] >= 0) b[i].load(p.base, row_at[i] * p.N + h * cols + col + 8 * t);
-          else b[i].zero();
-        }
+      for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[q][i] = 0.0f;
-        small_block<TERMS>(acc, p, tile.x, h * cols + col, vs);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          b[i].get(z[h][i]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            z[h][i][2 * q] += acc[q][2 * i];
-            z[h][i][2 * q + 1] += acc[q][2 * i + 1];
-          }
-        }
-      }
+        for (int i = 0; i < 4; ++i) acc[q][i] = 0.0f;
+      small_block<TERMS>(acc, sb[h], b0[h], p.R, vs);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        if (row_at[i] < 0) continue;
-        if constexpr (SWIGLU) {
+        b[h][i].get(z[h][i]);
 #pragma unroll
-          for (int x = 0; x < 8; ++x) z[0][i][x] = swiglu_f32(z[0][i][x], z[1][i][x]);
+        for (int q = 0; q < 4; ++q) {
+          z[h][i][2 * q] += acc[q][2 * i];
+          z[h][i][2 * q + 1] += acc[q][2 * i + 1];
         }
-        put8<OUT_BF16>(p.out, row_at[i] * cols + col + 8 * t, z[0][i]);
       }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (row_at[i] < 0) continue;
+      if constexpr (SWIGLU) {
+#pragma unroll
+        for (int x = 0; x < 8; ++x) z[0][i][x] = swiglu_f32(z[0][i][x], z[H - 1][i][x]);
+      }
+      put8<OUT_BF16>(p.out, row_at[i] * cols + col + 8 * t, z[0][i]);
     }
   }
   __syncthreads();
