@@ -646,20 +646,18 @@ __global__ void __launch_bounds__(kExpandThreads, BASE_BF16 ? 4 : 3) lora_expand
   constexpr int sspan = kExpandSmallCols;
   const int chunks = cols / span, schunks = (cols + sspan - 1) / sspan;
 
-  // B rows of a large unit -> slot `s`: a thread takes every second 16-byte
-  // piece of one row
-  auto load_b = [&](int64_t u, int s) {
-    const int4 tile = pl.tiles[u / chunks];
-    if (tile.x < 0) return;
-    const int col0 = (int)(u % chunks) * span;
-    const int row = tid >> 1, h = row >> 5, w = row & 31;
-    const int n = SWIGLU ? h * cols + col0 + w : col0 + row;
-    const int drow = h * 32 + 8 * ((w & 7) >> 1) + 2 * (w >> 3) + (w & 1);
+  // B rows of the unit at (tile slot, col0) -> slot `s` of shared memory: a
+  // thread takes every second 16-byte piece of one row
+  const int brow = tid >> 1, bh = brow >> 5, bw = brow & 31;
+  const int bdst = bh * 32 + 8 * ((bw & 7) >> 1) + 2 * (bw >> 3) + (bw & 1);
+  auto load_b = [&](int slot_id, int col0, int s) {
+    if (slot_id < 0) return;
+    const int n = SWIGLU ? bh * cols + col0 + bw : col0 + brow;
     unsigned char* dst = bs + s * bblocks * kBBytes;
-    const uint16_t* src = p.b + ((int64_t)tile.x * p.N + n) * p.R;
+    const uint16_t* src = p.b + ((int64_t)slot_id * p.N + n) * p.R;
     for (int ch = tid & 1; ch < RP / 8; ch += 2) {
       const bool on = ch * 8 < p.R;
-      cp_async16(dst + (ch >> 3) * kBBytes + sw128_offset(drow, ch & 7), on ? src + ch * 8 : p.b, on);
+      cp_async16(dst + (ch >> 3) * kBBytes + sw128_offset(bdst, ch & 7), on ? src + ch * 8 : p.b, on);
     }
   };
 
@@ -670,7 +668,12 @@ __global__ void __launch_bounds__(kExpandThreads, BASE_BF16 ? 4 : 3) lora_expand
   // take about as long for a fraction of the bytes
   const int64_t large = (int64_t)ntiles.x * chunks, small = (int64_t)ntiles.y * schunks;
   const int64_t u0 = large * blockIdx.x / gridDim.x, lend = large * (blockIdx.x + 1) / gridDim.x;
-  if (u0 < lend) load_b(u0, 0);
+  int ti = (int)(u0 / chunks), col0 = (int)(u0 % chunks) * span;  // the unit, step by step
+  int4 tile = make_int4(-1, 0, 0, 0);
+  if (u0 < lend) {
+    tile = pl.tiles[ti];
+    load_b(tile.x, col0, 0);
+  }
   cp_async_commit();
   pdl_wait();
   if (warp == 0) {
@@ -683,8 +686,8 @@ __global__ void __launch_bounds__(kExpandThreads, BASE_BF16 ? 4 : 3) lora_expand
   pdl_trigger();
   const uint32_t tmem = tmem_sh;
 
-  int bad = 0, cur_tile = -1, slot = 0;
-  int4 tile = make_int4(-1, 0, 0, 0);
+  int bad = 0, slot = 0;
+  bool fresh = true;  // the unit is the first of its tile here
   int64_t row_at[4] = {};  // this lane's four rows (-1: none)
   Base8<BASE_BF16> bq[2][4];
   uint32_t parity = 0;
@@ -697,10 +700,7 @@ __global__ void __launch_bounds__(kExpandThreads, BASE_BF16 ? 4 : 3) lora_expand
     }
   };
   for (int64_t u = u0; u < lend; ++u) {
-    const int ti = (int)(u / chunks), col0 = (int)(u % chunks) * span;
-    if (ti != cur_tile) {
-      cur_tile = ti;
-      tile = pl.tiles[ti];
+    if (fresh) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = warp * 32 + g + 8 * i;
@@ -711,7 +711,12 @@ __global__ void __launch_bounds__(kExpandThreads, BASE_BF16 ? 4 : 3) lora_expand
       if (tile.x >= 0) stage_v<TERMS>(pl, RP, tile.y, tile.z, tile.z, vs);
       cp_async_commit();
     }
-    if (u + 1 < lend) load_b(u + 1, slot ^ 1);
+    const bool last = u + 1 >= lend, more = !last && col0 + span < cols;  // more: of this tile
+    int4 next = tile;
+    if (!last) {
+      if (!more) next = pl.tiles[ti + 1];
+      load_b(next.x, more ? col0 + span : 0, slot ^ 1);
+    }
     cp_async_commit();
     cp_async_wait<1>();
     fence_proxy_async_smem();
@@ -732,7 +737,6 @@ __global__ void __launch_bounds__(kExpandThreads, BASE_BF16 ? 4 : 3) lora_expand
       parity ^= 1u;
       tc_fence_after();
     }
-    const bool more = u + 1 < lend && (int)((u + 1) / chunks) == ti;
 #pragma unroll
     for (int hr = 0; hr < 2; ++hr) {  // accumulator rows 32 warp + 16 hr ..
       float z[2][2][8];               // [block][row g, g + 8]
@@ -775,6 +779,10 @@ __global__ void __launch_bounds__(kExpandThreads, BASE_BF16 ? 4 : 3) lora_expand
       }
     }
     slot ^= 1;
+    fresh = !more;
+    col0 = more ? col0 + span : 0;
+    ti += more ? 0 : 1;
+    tile = next;
     tc_fence_before();
     __syncthreads();  // the accumulator, v and the old slot of B are free again
     tc_fence_after();
@@ -782,14 +790,21 @@ __global__ void __launch_bounds__(kExpandThreads, BASE_BF16 ? 4 : 3) lora_expand
   cp_async_wait<0>();
   const bool stop = __syncthreads_or(bad) != 0;
 
-  cur_tile = -1;
   constexpr int H = SWIGLU ? 2 : 1;
-  const int64_t s1 = small * (blockIdx.x + 1) / gridDim.x;
-  for (int64_t u = small * blockIdx.x / gridDim.x; u < s1 && !stop; ++u) {
-    const int ti = (int)(u / schunks), col = (int)(u % schunks) * sspan + warp * 32;
-    const bool fresh = ti != cur_tile;
-    if (fresh) {
-      cur_tile = ti;
+  const int64_t s0 = small * blockIdx.x / gridDim.x, s1 = small * (blockIdx.x + 1) / gridDim.x;
+  ti = (int)(s0 / schunks);
+  int chunk = (int)(s0 % schunks);
+  fresh = true;
+  for (int64_t u = s0; u < s1 && !stop; ++u, ++chunk) {
+    if (chunk == schunks) {
+      chunk = 0;
+      ++ti;
+      fresh = true;
+    }
+    const int col = chunk * sspan + warp * 32;
+    const bool stage = fresh;
+    fresh = false;
+    if (stage) {
       tile = pl.tiles[pl.capacity - 1 - ti];
       __syncthreads();  // no warp still reads the tile before
       stage_v<TERMS>(pl, RP, tile.y, tile.z, kLoraSmallRows, vs);
@@ -815,7 +830,7 @@ __global__ void __launch_bounds__(kExpandThreads, BASE_BF16 ? 4 : 3) lora_expand
         }
       }
     }
-    if (fresh) {
+    if (stage) {
       cp_async_wait<0>();
       __syncthreads();
     }
