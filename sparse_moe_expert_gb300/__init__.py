@@ -21,10 +21,11 @@ from .binding import (moe_abi_version, moe_combine, moe_combine_backward, moe_do
                       moe_set_launch_overlap,
                       moe_router_workspace_size, moe_status_string, moe_swiglu, qdesc)
 from .health import ExpertHealthMonitor, WindowHealth
-from .layer import MoELayer, QTensor, bf16_from_bits, qtensor_from_numpy
+from .layer import (ExpertAdapters, MoELayer, QTensor, ScoredRouting, bf16_from_bits,
+                    qtensor_from_numpy)
 
 __all__ = [
-    "MoELayer", "QTensor", "MoEError", "ExpertHealthMonitor", "WindowHealth",
+    "MoELayer", "ScoredRouting", "ExpertAdapters", "QTensor", "MoEError", "ExpertHealthMonitor", "WindowHealth",
     "moe_expert_counts_accumulate", "moe_expert_health", "qtensor_from_numpy", "bf16_from_bits", "lib", "lib_path",
     "moe_abi_version", "moe_set_launch_overlap", "moe_status_string", "moe_pack_gate_up", "moe_router_workspace_size",
     "moe_router_topk", "moe_route", "moe_route_grouped", "moe_permute", "moe_permute_capped", "moe_permute_rows", "moe_gate_up_qmm", "moe_down_qmm", "moe_combine",

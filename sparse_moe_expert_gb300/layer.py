@@ -16,7 +16,7 @@ import torch
 
 from . import binding as B
 from ._lib import (EPILOGUE_RAW, EPILOGUE_SWIGLU, PATH_AUTO, PATH_FLAG_WEIGHTS_EARLY, PATH_GEMV,
-                   PATH_TC, MoEError, path_k_range)
+                   PATH_TC, SCORE_SIGMOID, SCORE_SOFTMAX, MoEError, path_k_range)
 
 FUSE_ENV = "MOE_GB300_FUSE_GATE_UP"
 TC_MIN_TOKENS_PER_EXPERT = 24  # mirrors the library's automatic path choice
@@ -55,6 +55,45 @@ def bf16_from_bits(x_bits: np.ndarray, device=None, pin: bool = False) -> torch.
     return t.to(device) if device is not None else t
 
 
+@dataclasses.dataclass
+class ScoredRouting:
+    """How a layer turns router logits into experts (moe_route_scored).
+
+    ``select_bias`` (fp32 [E], on the device) steers the selection and does
+    not weigh; with ``n_groups`` > 1 the experts of the ``topk_groups`` best
+    groups compete, a group ranking by the sum of its ``group_top`` best."""
+    score: int = SCORE_SOFTMAX
+    select_bias: Optional[torch.Tensor] = None
+    n_groups: int = 1
+    topk_groups: int = 1
+    group_top: int = 2
+    scale: float = 1.0
+
+
+@dataclasses.dataclass
+class ExpertAdapters:
+    """Low-rank adapters of many requests on every expert (moe_lora_apply).
+
+    gate_up_a bf16 [n, E, R, H], gate_up_b bf16 [n, E, 2*I, R] and down_a bf16
+    [n, E, R', I], down_b bf16 [n, E, H, R'] (either pair may be None); scales
+    fp32 [n] or None."""
+    gate_up_a: Optional[torch.Tensor] = None
+    gate_up_b: Optional[torch.Tensor] = None
+    down_a: Optional[torch.Tensor] = None
+    down_b: Optional[torch.Tensor] = None
+    scales: Optional[torch.Tensor] = None
+
+    @staticmethod
+    def join_gate_up(gate_a, gate_b, up_a, up_b):
+        """(gate_up_a, gate_up_b) of separate gate and up adapters: the two
+        ranks side by side, each half of B reading its own (rank doubled)."""
+        a = torch.cat([gate_a, up_a], dim=-2).contiguous()
+        r, r2 = gate_b.shape[-1], up_b.shape[-1]
+        top = torch.nn.functional.pad(gate_b, (0, r2))
+        low = torch.nn.functional.pad(up_b, (r, 0))
+        return a, torch.cat([top, low], dim=-2).contiguous()
+
+
 class MoELayer:
     """Forward of one quantized sparse-MoE SwitchGLU layer on one GPU.
 
@@ -70,15 +109,22 @@ class MoELayer:
     the down product's rows between the down and combine kernels: None
     stores bf16 when a call's products run on the tensor cores (large
     batches, where y is hundreds of MB written and read again) and fp32
-    otherwise.
+    otherwise.  ``scoring`` routes by scores (ScoredRouting) instead of the
+    plain softmax top-k; it needs a fixed k and takes the place of ``groups``.
+    ``adapters`` (ExpertAdapters) serve calls that name each token's adapter;
+    they need the fused gate_up matrix.
     """
+    scoring: Optional[ScoredRouting] = None
+    adapters: Optional[ExpertAdapters] = None
 
     def __init__(self, router_w: torch.Tensor, logit_bias: Optional[torch.Tensor], gate: QTensor,
                  up: QTensor, down: QTensor, k_fixed: int, kmax: Optional[int] = None,
                  inv_temperature: float = 1.0, renormalize: bool = True,
                  thresholds=(1.2, 2.5), fuse_gate_up: Optional[bool] = None,
                  path: int = PATH_AUTO, free_sources: bool = False, groups: int = 0,
-                 capacity: Optional[int] = None, y_dtype: Optional[torch.dtype] = None):
+                 capacity: Optional[int] = None, y_dtype: Optional[torch.dtype] = None,
+                 scoring: Optional[ScoredRouting] = None,
+                 adapters: Optional[ExpertAdapters] = None):
         self.device = router_w.device
         self.router_w = router_w.contiguous()
         self.logit_bias = None if logit_bias is None else logit_bias.contiguous()
@@ -98,6 +144,9 @@ class MoELayer:
         self.y_dtype = y_dtype
         if self.groups > 0 and (self.E % self.groups or k_fixed != self.groups):
             raise ValueError("group-limited routing needs k_fixed == groups dividing E")
+        self.scoring = scoring
+        if scoring is not None and (k_fixed < 1 or self.groups > 0):
+            raise ValueError("scoring needs a fixed k and takes the place of groups")
         self.down = down
         if fuse_gate_up is None:
             fuse_gate_up = os.environ.get(FUSE_ENV, "1") != "0"
@@ -115,7 +164,11 @@ class MoELayer:
             except MoEError as err:
                 if err.status != 3:  # MOE_ERR_INCOMPATIBLE keeps the unfused path
                     raise
+        self.adapters = adapters
+        if adapters is not None and not self.fused:
+            raise ValueError("adapters need the fused gate_up matrix")
         self._bufs = {}
+        self._last = None  # tokens of the last forward, for router_grad
 
     @classmethod
     def from_workload(cls, layer_inputs, device, batch: int = 0, **kw) -> "MoELayer":
@@ -173,7 +226,12 @@ class MoELayer:
         activation when unfused), down and combine.  With a capacity the
         capped grouping is a kernel of its own.  When k_split is set both
         kernel families of each product are launched (one of them returns at
-        once)."""
+        once).  With scoring the logits, the scores and the grouping are a
+        kernel each.  Calls with adapters add theirs."""
+        if self.scoring is not None:
+            # logits, scores, grouping, [row permute], products, combine
+            n = 3 + (1 if self.resolved_path(T) == PATH_TC else 0)
+            return n + (1 if self.fused else 3) + 2
         group = 32 if self.E <= 256 else 16
         one_group = (T + group - 1) // group == 1
         n = 1 + (0 if one_group else 1)
@@ -211,26 +269,56 @@ class MoELayer:
                 y=torch.empty((A, self.H), dtype=self.y_storage(T), device=dev),
                 out=torch.empty((T, self.H), dtype=torch.bfloat16, device=dev),
             )
+            if self.scoring is not None:
+                bufs["logits"] = torch.empty((T, self.E), dtype=torch.float32, device=dev)
             if not self.fused:
                 bufs["g_raw"] = torch.empty((A, self.I), dtype=torch.float32, device=dev)
                 bufs["u_raw"] = torch.empty((A, self.I), dtype=torch.float32, device=dev)
             self._bufs[key] = bufs
         return self._bufs[key]
 
+    def _adapter_buffers(self, b: dict, T: int) -> None:
+        ad, dev = self.adapters, self.device
+        if ad.gate_up_a is not None and "gu_raw" not in b:
+            b["gu_raw"] = torch.empty((max(T * self.kmax, 1), 2 * self.I), dtype=torch.float32,
+                                      device=dev)
+        if "lora_ws" not in b:
+            need = [B.moe_lora_workspace_size(T, self.kmax, self.E, a.shape[0], a.shape[2])
+                    for a in (ad.gate_up_a, ad.down_a) if a is not None]
+            b["lora_ws"] = torch.empty(max(need, default=1), dtype=torch.uint8, device=dev)
+
+    def _route_scored(self, x, b, it):
+        """Logits, scored selection and the grouping (empty slots allowed)."""
+        s = self.scoring
+        B.moe_router_logits(x, self.router_w, self.logit_bias, it, b["logits"])
+        B.moe_route_scored(b["logits"], self.k_fixed, s.score, s.select_bias, s.n_groups,
+                           s.topk_groups, s.group_top, self.renormalize, s.scale, self.kmax,
+                           b["topk_ids"], b["topk_w"], b["k_dev"])
+        B.moe_permute_masked(b["topk_ids"], b["k_dev"], self.E, self.capacity, b["counts"],
+                             b["offsets"], b["sorted"], b["inv_pos"])
+
     def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None,
-                inv_temperature: Optional[float] = None, events: Optional[dict] = None
-                ) -> torch.Tensor:
+                inv_temperature: Optional[float] = None, events: Optional[dict] = None,
+                adapter_ids: Optional[torch.Tensor] = None) -> torch.Tensor:
         """x: bf16 [T, H] on the device.  Returns bf16 [T, H] (a reused buffer
         unless ``out`` is given).  ``events``, if given, receives per kernel
         ("router", "permute", "permute_rows", "gate_up", "down", "combine") a
-        list of (start, end) CUDA events around its launches."""
+        list of (start, end) CUDA events around its launches.  ``adapter_ids``
+        (int32 [T], negative: none) names each token's adapter."""
         T = x.shape[0]
         b = self.buffers(T)
         path = self.resolved_path(T)
+        if adapter_ids is not None:
+            if self.adapters is None:
+                raise ValueError("adapter_ids given to a layer without adapters")
+            self._adapter_buffers(b, T)
+        self._last = T
         it = self.inv_temperature if inv_temperature is None else float(inv_temperature)
         # router, top-k and the expert grouping (one launch for small batches)
         ev = _Timer(events, "route")
-        if self.capacity is not None:
+        if self.scoring is not None:
+            self._route_scored(x, b, it)
+        elif self.capacity is not None:
             # router (group-limited or top-k), then the grouping with each
             # expert's capacity (it replaces the uncapped grouping that the
             # group-limited route also writes)
@@ -256,7 +344,7 @@ class MoELayer:
                         b["k_dev"], b["mean_entropy"], b["ws"], b["counts"], b["offsets"],
                         b["sorted"], b["inv_pos"])
         ev.stop()
-        ks = self.k_split(T)
+        ks = self.k_split(T) if adapter_ids is None else 0
         if ks:
             return self._forward_k_split(x, b, ks, T, out, events)
         # tensor cores: token rows copied once into expert order, so every
@@ -269,7 +357,17 @@ class MoELayer:
         else:
             xs, srt = x, b["sorted"]
         ev = _Timer(events, "gate_up")
-        if self.fused:
+        ad = self.adapters if adapter_ids is not None else None
+        route = dict(topk_ids=b["topk_ids"], sorted_assign=b["sorted"],
+                     expert_offsets=b["offsets"])
+        if ad is not None and ad.gate_up_a is not None:
+            # the raw halves, then adapters and activation in one kernel
+            g = self.gate_up
+            B.moe_gate_up_qmm(xs, srt, b["offsets"], b["k_dev"], self.kmax, g.q, g.s, g.b,
+                              self.bits, EPILOGUE_RAW, torch.float32, b["gu_raw"], path, T=T)
+            B.moe_lora_apply(x, adapter_ids, ad.gate_up_a, ad.gate_up_b, ad.scales, b["gu_raw"],
+                             b["h"], EPILOGUE_SWIGLU, workspace=b["lora_ws"], **route)
+        elif self.fused:
             g = self.gate_up
             B.moe_gate_up_qmm(xs, srt, b["offsets"], b["k_dev"], self.kmax, g.q, g.s, g.b,
                               self.bits, EPILOGUE_SWIGLU, b["h"].dtype, b["h"], path, T=T)
@@ -285,12 +383,39 @@ class MoELayer:
         # only h: the down weights may stream while it finishes
         B.moe_down_qmm(b["h"], b["offsets"], b["k_dev"], T, self.kmax, d.q, d.s, d.b, self.bits,
                        b["y"], path | PATH_FLAG_WEIGHTS_EARLY)
+        if ad is not None and ad.down_a is not None:
+            B.moe_lora_apply(b["h"], adapter_ids, ad.down_a, ad.down_b, ad.scales, b["y"], b["y"],
+                             workspace=b["lora_ws"], x_by_token=False, **route)
         ev.stop()
         res = out if out is not None else b["out"]
         ev = _Timer(events, "combine")
         B.moe_combine(b["y"], b["inv_pos"], b["topk_w"], b["k_dev"], T, self.kmax, res)
         ev.stop()
         return res
+
+    def router_grad(self, d_out: torch.Tensor, balance_coef: float = 0.0, z_coef: float = 0.0):
+        """Gradient of the last forward with respect to the router logits, the
+        experts held fixed: -> (d_logits fp32 [T, E], losses fp32 [2]).
+
+        d_out bf16 [T, H]: the gradient of the layer's output.  Adds the
+        balance and z losses (their values are returned).  Only for layers
+        with ``scoring``; the router weight's gradient is
+        inv_temperature * d_logits^T x."""
+        if self.scoring is None or self._last is None:
+            raise ValueError("router_grad needs a layer with scoring, after a forward")
+        T = self._last
+        b = self.buffers(T)
+        if tuple(d_out.shape) != (T, self.H):
+            raise ValueError(f"d_out must be {(T, self.H)}, got {tuple(d_out.shape)}")
+        if T == 0:
+            return (torch.zeros((0, self.E), device=self.device),
+                    torch.zeros(2, device=self.device))
+        d_w, _ = B.moe_combine_backward(d_out, b["y"], b["inv_pos"], b["topk_w"], b["k_dev"],
+                                        need_d_y=False)
+        s = self.scoring
+        return B.moe_route_scored_backward(
+            b["logits"], b["topk_ids"], d_w, b["counts"], s.score, self.k_fixed, self.renormalize,
+            s.scale, balance_coef, z_coef)
 
     def _forward_k_split(self, x, b, ks, T, out, events):
         """The products after routing when k < ks takes the streamed GEMV and
