@@ -298,6 +298,44 @@ def test_route_scored_strides_kmax_and_empty(cuda_lib):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("E,G,tg,gt,k", [(256, 8, 4, 2, 8), (128, 1, 1, 1, 8), (60, 1, 1, 1, 5),
+                                         (64, 4, 2, 1, 4), (33, 1, 1, 1, 16), (512, 32, 9, 2, 12),
+                                         (8, 1, 1, 1, 8), (1000, 1, 1, 1, 3), (60, 4, 2, 2, 6)])
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_route_scored_many_tokens_as_few(cuda_lib, E, G, tg, gt, k, score, dtype):
+    """A call of many tokens gives each token what a call of few gives it, bit
+    for bit, with masks, ties, empty rows and odd strides among them."""
+    T = 16384 + 37
+    g = torch.Generator(device=dev())
+    g.manual_seed(E + G)
+    wide = torch.randn((T, E + 5), generator=g, device=dev()) * 1.5
+    wide[::7] = torch.round(wide[::7])                    # ties
+    wide[torch.rand((T, E + 5), generator=g, device=dev()) < 0.05] = -math.inf
+    wide[100] = -math.inf
+    wide[101] = 0.0
+    wide[102, 1:] = -math.inf
+    wide = wide.to(dtype)
+    bias = torch.round(torch.randn(E, generator=g, device=dev()) * 20) * 0.001
+    for l, b in ((wide[:, :E].contiguous(), bias), (wide[:, :E].contiguous(), None),
+                 (wide[:, 3:3 + E], bias)):
+        kw = dict(k=k, score=score, select_bias=b, n_groups=G, topk_groups=tg, group_top=gt,
+                  scale=2.5, kmax=k + 1 if k < 16 else k)
+        ids, w, kd = cuda_lib.moe_route_scored(l, **kw)
+        assert int(kd.item()) == k
+        few = [cuda_lib.moe_route_scored(l[i:i + 4000], **kw) for i in range(0, T, 4000)]
+        assert torch.equal(ids, torch.cat([f[0] for f in few]))
+        fw = torch.cat([f[1] for f in few])
+        # the weights' sum runs in another order: two roundings of <= 16 terms
+        assert torch.allclose(w, fw, rtol=W_TOL, atol=0)
+    cuda_lib.moe_get_device_error(clear=True)
+    l = wide[:, :E].contiguous()
+    l[T - 1, E - 1] = math.nan
+    ids, _, _ = cuda_lib.moe_route_scored(l, k, score=score)
+    assert cuda_lib.moe_get_device_error(clear=True) == cuda_lib.DEVERR_BAD_SCORE
+    assert not (ids[T - 1] == E - 1).any()
+
+
 def test_route_scored_refusals(cuda_lib):
     d = dev()
     l = torch.zeros((4, 64), device=d)
