@@ -332,8 +332,8 @@ __device__ __forceinline__ void lane_top2(const float (&c)[V], float& a1, float&
 // c~ from the hardware exponential and reciprocal are within eps of the exact
 // fp32 ones (scores are at most 1: the sigmoid's error is below 1e-6, the
 // softmax's below 1e-6 of the score; a choice adds one rounding of itself).
-// The k-th largest of the lanes' best c~ is a lower bound of the k-th largest
-// choice, so every chosen expert has c~ >= bound - 2 eps.  Those candidates
+// The k-th largest of the lanes' two best c~ is a lower bound of the k-th
+// largest choice, so every chosen expert has c~ >= bound - 2 eps.  Those candidates
 // (about k + 2 of 256) get one lane each, their exact scores and their ranks
 // by counting, and the lanes with rank < k are the answer.  Groups are cut on
 // c~ too when the cut is wider than the approximation.  More than 32
@@ -342,11 +342,14 @@ __device__ __forceinline__ void lane_top2(const float (&c)[V], float& a1, float&
 // on which way was taken.
 //
 // Bound by the issue rate: MEASURED_PLACEHOLDER
+// Two tokens share the last part of the work: the candidates of one on lanes
+// 0-15, those of the other on lanes 16-31.
 template <int V, bool BF16, bool SIGMOID>
 __global__ void __launch_bounds__(kScoredThreads, V <= 8 ? 4 : 2)
-    route_scored_kernel(ScoredParams p, int vec) {
-  __shared__ __align__(16) int cand_id[kScoredWarps][32];
-  __shared__ __align__(16) float cand_x[kScoredWarps][32];
+    route_scored_kernel(ScoredParams p, int vec, int per) {
+  constexpr int C = 16;  // candidates of a token
+  __shared__ __align__(16) int cand_id[kScoredWarps][2 * C];
+  __shared__ __align__(16) float cand_x[kScoredWarps][2 * C];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -366,12 +369,13 @@ __global__ void __launch_bounds__(kScoredThreads, V <= 8 ? 4 : 2)
   const int G = p.n_groups, gsz = p.E / G, span = gsz / V;  // span: lanes of a group
   const bool lane_groups = gsz % V == 0 && (span & (span - 1)) == 0 && span <= 32;
   const int my_group = e0 / gsz;  // >= G past the experts
-  for (int64_t t = (int64_t)blockIdx.x * kScoredWarps + warp; t < p.T;
-       t += (int64_t)gridDim.x * kScoredWarps) {
+
+  // The candidates of the token whose logits lie at `row` into ids[]; their
+  // number, or -1 when they are not certain or too many.  m, den: the
+  // softmax's largest logit and denominator.
+  auto candidates = [&](const char* row, int* ids, float& m, float& den) -> int {
     float l[V], c[V];
-    const char* row = static_cast<const char*>(p.logits) + t * p.ld * (BF16 ? 2 : 4);
     load_logits<V, BF16>(l, row, e0, p.E, vec != 0);
-    float m = 0.0f, den = 1.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) bad |= !(l[v] < INFINITY);
     if constexpr (SIGMOID) {
@@ -392,47 +396,44 @@ __global__ void __launch_bounds__(kScoredThreads, V <= 8 ? 4 : 2)
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) c[v] = fabsf(l[v]) < INFINITY ? c[v] + b[v] : -INFINITY;
-
     float best, second;
     lane_top2<V>(c, best, second);
     bool live = true;  // the lane's group is among the chosen
     if (G > 1) {
-      bool sure = lane_groups;
-      if (lane_groups) {
-        float a1 = best, a2 = second;
-        for (int o = 1; o < span; o <<= 1) {
-          const float b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
-          merge_top2(a1, a2, b1, b2);
-        }
-        // every lane of a group holds the group's value
-        const float val = p.group_top == 2 && a2 > -INFINITY ? a1 + a2 : a1;
-        const float mine = my_group < G ? val : -INFINITY;
-        float rest = mine, cut = -INFINITY;
+      if (!lane_groups) return -1;
+      float a1 = best, a2 = second;
+      for (int o = 1; o < span; o <<= 1) {
+        const float b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
+        merge_top2(a1, a2, b1, b2);
+      }
+      // every lane of a group holds the group's value
+      const float val = p.group_top == 2 && a2 > -INFINITY ? a1 + a2 : a1;
+      const float mine = my_group < G ? val : -INFINITY;
+      float rest = mine, cut = -INFINITY;
 #pragma unroll 4
-        for (int r = 0; r < p.topk_groups; ++r) {
-          cut = redux_max(rest);
-          if (rest == cut) rest = -INFINITY;
-        }
-        const float next = redux_max(rest);
-        live = mine >= cut && mine > -INFINITY;
-        // no tie among the chosen values or at the cut: as many groups as asked
-        // (or all that have an expert), the next one clearly below
-        const int groups = __popc(__ballot_sync(kFull, live && (lane & (span - 1)) == 0));
-        sure = next == -INFINITY ? groups <= p.topk_groups
-                                 : groups == p.topk_groups &&
-                                       cut - next > 4.0f * eps + fabsf(next) * 0x1p-20f;
+      for (int r = 0; r < p.topk_groups; ++r) {
+        cut = redux_max(rest);
+        if (rest == cut) rest = -INFINITY;
       }
-      if (!sure) {
-        route_token_exact<V, BF16, SIGMOID>(p, t, vec);
-        continue;
-      }
+      const float next = redux_max(rest);
+      live = mine >= cut && mine > -INFINITY;
+      // no tie among the chosen values or at the cut: as many groups as asked
+      // (or all that have an expert), the next one clearly below
+      const int groups = __popc(__ballot_sync(kFull, live && (lane & (span - 1)) == 0));
+      const bool sure = next == -INFINITY ? groups <= p.topk_groups
+                                          : groups == p.topk_groups &&
+                                                cut - next > 4.0f * eps + fabsf(next) * 0x1p-20f;
+      if (!sure) return -1;
     }
     float bound = -INFINITY;
-    float rest = live ? best : -INFINITY;
+    float rest = live ? best : -INFINITY, after = live ? second : -INFINITY;
 #pragma unroll 4
     for (int r = 0; r < p.k; ++r) {
       bound = redux_max(rest);
-      if (rest == bound) rest = -INFINITY;
+      if (rest == bound) {
+        rest = after;
+        after = -INFINITY;
+      }
     }
     // -FLT_MAX when fewer than k lanes have an expert: all of them are candidates
     float cut = fmaxf(bound - (2.0f * eps + fabsf(bound) * 0x1p-20f), -3.4028234e38f);
@@ -445,55 +446,71 @@ __global__ void __launch_bounds__(kScoredThreads, V <= 8 ? 4 : 2)
     int n = 0;
     for (unsigned who = __ballot_sync(kFull, mine != 0u); who; who = __ballot_sync(kFull, mine != 0u)) {
       const int at = n + __popc(who & lanemask_lt());
-      if (mine != 0u && at < 32) cand_id[warp][at] = e0 + __ffs(mine) - 1;
+      if (mine != 0u && at < C) ids[at] = e0 + __ffs(mine) - 1;
       mine &= mine - 1u;
       n += __popc(who);
     }
-    if (n > 32) {
-      route_token_exact<V, BF16, SIGMOID>(p, t, vec);
-      continue;
-    }
+    return n <= C ? n : -1;
+  };
+
+  // a warp takes two neighbouring tokens per step, or (few tokens) one
+  const int64_t step = (int64_t)gridDim.x * kScoredWarps * per;
+  const int half = lane >> 4, i = lane & 15;
+  for (int64_t t = ((int64_t)blockIdx.x * kScoredWarps + warp) * per; t < p.T; t += step) {
+    const char* row = static_cast<const char*>(p.logits) + t * p.ld * (BF16 ? 2 : 4);
+    const char* row1 = row + p.ld * (BF16 ? 2 : 4);
+    const bool two = per == 2 && t + 1 < p.T;
+    float m0 = 0.0f, den0 = 1.0f, m1 = 0.0f, den1 = 1.0f;
+    const int n0 = candidates(row, cand_id[warp], m0, den0);
+    const int n1 = two ? candidates(row1, cand_id[warp] + C, m1, den1) : 0;
     __syncwarp();
+    const int n = half ? n1 : n0;
+    const float m = half ? m1 : m0, den = half ? den1 : den0;
     int id = 0x7FFFFFFF;
     float s = 0.0f, x = -INFINITY;
-    if (lane < n) {
+    if (i < n) {
       id = cand_id[warp][lane];
-      const float q = load_logit<BF16>(row, id);
+      const float q = load_logit<BF16>(half ? row1 : row, id);
       s = SIGMOID ? sigmoid_f32(q) : __fdiv_rn(expf(__fsub_rn(q, m)), den);
       x = p.bias ? __fadd_rn(s, __ldg(p.bias + id)) : s;
     }
     cand_x[warp][lane] = x;
     __syncwarp();
     int rank = 0;
-    for (int j = 0; j < n; j += 4) {  // past the candidates: -inf, never ahead
-      const float4 q = *reinterpret_cast<const float4*>(&cand_x[warp][j]);
+    const float* xs = &cand_x[warp][half * C];
+    for (int j = 0; j < max(n0, n1); j += 4) {  // past the candidates: -inf, never ahead
+      const float4 q = *reinterpret_cast<const float4*>(xs + j);
       rank += q.x > x;
       rank += q.y > x;
       rank += q.z > x;
       rank += q.w > x;
     }
-    if (lane >= n) rank = 32;
+    if (i >= n) rank = 32;
     // distinct choices have the ranks 0 .. n - 1; equal ones go by id
-    const unsigned seen = __reduce_or_sync(kFull, lane < n ? 1u << rank : 0u);
-    if (__popc(seen) != n) {
+    const unsigned seen = __reduce_or_sync(kFull, i < n ? 1u << (rank + 16 * half) : 0u);
+    if (__popc(seen) != max(n0, 0) + max(n1, 0)) {
       for (int j = 0; j < n; ++j)
-        rank += cand_x[warp][j] == x && cand_id[warp][j] < id;
+        rank += xs[j] == x && cand_id[warp][half * C + j] < id;
     }
     const bool chosen = rank < p.k;
     float w = chosen ? s : 0.0f;
     if (p.renorm) {
-      const float tot = warp_sum(w);
+      float tot = w;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) tot += __shfl_xor_sync(kFull, tot, o);
       w = tot > 0.0f ? __fdiv_rn(w, tot) : 0.0f;
     }
-    const int64_t out = t * p.kmax;
+    const int64_t out = (t + half) * p.kmax;
     if (chosen) {
       p.ids[out + rank] = id;
       p.w[out + rank] = __fmul_rn(w, p.scale);
     }
-    if (lane >= min(n, p.k) && lane < p.kmax) {
-      p.ids[out + lane] = -1;
-      p.w[out + lane] = 0.0f;
+    if (n >= 0 && i >= min(n, p.k) && i < p.kmax && (half == 0 || two)) {
+      p.ids[out + i] = -1;
+      p.w[out + i] = 0.0f;
     }
+    if (n0 < 0) route_token_exact<V, BF16, SIGMOID>(p, t, vec);
+    if (n1 < 0) route_token_exact<V, BF16, SIGMOID>(p, t + 1, vec);
     __syncwarp();
   }
   if (bad) raise_device_error(p.err, MOE_DEVERR_BAD_SCORE);
@@ -799,10 +816,21 @@ moe_status_t dispatch_scored(int V, bool bf16, bool sig, A&&... a) {
   return MOE_ERR_UNSUPPORTED;
 }
 
+int scored_grid(int T) {
+  int64_t g = ((int64_t)T + kScoredWarps - 1) / kScoredWarps;
+  const int64_t cap = (int64_t)moe_host::sm_count() * 8;
+  if (g > cap) g = cap;
+  return (int)(g < 1 ? 1 : g);
+}
+
 template <int V, bool BF16, bool SIG>
 struct ForwardLaunch {
-  static moe_status_t go(const ScoredParams& p, int grid, int vec, cudaStream_t st) {
-    return moe_host::launch(route_scored_kernel<V, BF16, SIG>, grid, kScoredThreads, 0, st, p, vec);
+  static moe_status_t go(const ScoredParams& p, int vec, cudaStream_t st) {
+    // two tokens per warp once every SM has some warps (measured: 64 tokens
+    // 2.7 us with one, 3.3 with two; 4096 tokens 5.4 and 4.7)
+    const int per = p.T > moe_host::sm_count() * kScoredWarps ? 2 : 1;
+    return moe_host::launch(route_scored_kernel<V, BF16, SIG>, scored_grid((p.T + per - 1) / per),
+                            kScoredThreads, 0, st, p, vec, per);
   }
 };
 template <int V, bool BF16, bool SIG>
@@ -826,13 +854,6 @@ bool scored_shape_ok(int T, int E, int k, int kmax, int dtype, int score, int64_
          (int64_t)T * kmax <= (1 << 24) &&
          (dtype == MOE_DTYPE_F32 || dtype == MOE_DTYPE_BF16) &&
          (score == MOE_SCORE_SOFTMAX || score == MOE_SCORE_SIGMOID);
-}
-
-int scored_grid(int T) {
-  int64_t g = ((int64_t)T + kScoredWarps - 1) / kScoredWarps;
-  const int64_t cap = (int64_t)moe_host::sm_count() * 8;
-  if (g > cap) g = cap;
-  return (int)(g < 1 ? 1 : g);
 }
 
 }  // namespace
@@ -879,7 +900,7 @@ extern "C" moe_status_t moe_route_scored(const void* logits, int logits_dtype, i
   p.err = device_error_word();
   const int V = lane_values(E);
   return dispatch_scored<ForwardLaunch>(V, logits_dtype == MOE_DTYPE_BF16,
-                                        score == MOE_SCORE_SIGMOID, p, scored_grid(T),
+                                        score == MOE_SCORE_SIGMOID, p,
                                         (int)can_vector(logits, ld, E, V, size),
                                         reinterpret_cast<cudaStream_t>(stream));
 }
