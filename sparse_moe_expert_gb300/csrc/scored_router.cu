@@ -57,7 +57,12 @@ __device__ __forceinline__ float load_logit(const void* row, int e) {
 // load per expert.  Experts past E read as -inf.
 template <int V, bool BF16>
 __device__ __forceinline__ void load_logits(float (&l)[V], const void* row, int e0, int E,
-                                            bool vec) {
+                                            int vec) {
+  if (vec == 1 && e0 >= E) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) l[v] = -INFINITY;
+    return;
+  }
   if constexpr (BF16) {
     if (vec && V >= 2) {
       const uint32_t* p = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(row) + e0);
@@ -237,7 +242,7 @@ __device__ __noinline__ void route_token_exact(const ScoredParams& p, int64_t t,
   {
     float l[V];
     const char* row = static_cast<const char*>(p.logits) + t * p.ld * (BF16 ? 2 : 4);
-    load_logits<V, BF16>(l, row, e0, p.E, vec != 0);
+    load_logits<V, BF16>(l, row, e0, p.E, vec);
 #pragma unroll
     for (int v = 0; v < V; ++v) key[v] = fabsf(l[v]) < INFINITY ? 1u : 0u;
     if constexpr (SIGMOID) {
@@ -375,7 +380,7 @@ __global__ void __launch_bounds__(kScoredThreads, V <= 8 ? 4 : 2)
   // softmax's largest logit and denominator.
   auto candidates = [&](const char* row, int* ids, float& m, float& den) -> int {
     float l[V], c[V];
-    load_logits<V, BF16>(l, row, e0, p.E, vec != 0);
+    load_logits<V, BF16>(l, row, e0, p.E, vec);
 #pragma unroll
     for (int v = 0; v < V; ++v) bad |= !(l[v] < INFINITY);
     if constexpr (SIGMOID) {
@@ -569,8 +574,10 @@ __device__ __forceinline__ float exp_approx(float x) {
 // it.  The hardware exponential and reciprocal are good to a few 1e-7 here,
 // far inside the rounding of the differences they enter.  The chosen slots'
 // d u meets its expert's lane through a row of shared memory per warp.
+constexpr int grad_ctas_per_sm(int V) { return V <= 4 ? 4 : V <= 8 ? 3 : V <= 16 ? 2 : 1; }
+
 template <int V, bool BF16, bool SIGMOID>
-__global__ void __launch_bounds__(kScoredThreads) route_scored_backward_kernel(ScoredGradParams p,
+__global__ void __launch_bounds__(kScoredThreads, grad_ctas_per_sm(V)) route_scored_backward_kernel(ScoredGradParams p,
                                                                                int vec) {
   constexpr int P = 32 * V;
   __shared__ __align__(16) float scatter[kScoredWarps][P];
@@ -604,7 +611,7 @@ __global__ void __launch_bounds__(kScoredThreads) route_scored_backward_kernel(S
       dw = __ldg(p.d_w + t * p.kmax + lane) * p.scale;
     }
     float l[V];
-    load_logits<V, BF16>(l, row, e0, p.E, vec != 0);
+    load_logits<V, BF16>(l, row, e0, p.E, vec);
     if (id >= p.E) {
       bad = true;
       id = -1;
@@ -681,37 +688,39 @@ __global__ void __launch_bounds__(kScoredThreads) route_scored_backward_kernel(S
     __syncwarp();
     if (id >= 0) buf[id] = 0.0f;
     char* out = static_cast<char*>(p.d_logits) + t * p.ld_out * (BF16 ? 2 : 4);
-    if constexpr (BF16) {
-      if (vec && V >= 2) {
-        uint32_t w2[V / 2 > 0 ? V / 2 : 1];
+    if (e0 < p.E) {  // some lanes may lie past the experts
+      if constexpr (BF16) {
+        if (vec && V >= 2) {
+          uint32_t w2[V / 2 > 0 ? V / 2 : 1];
 #pragma unroll
-        for (int v = 0; v < V / 2; ++v)
-          w2[v] = (uint32_t)f32_to_bf16_rne(d[2 * v]) | ((uint32_t)f32_to_bf16_rne(d[2 * v + 1]) << 16);
-        uint32_t* o = reinterpret_cast<uint32_t*>(out) + e0 / 2;
-        if constexpr (V >= 8) {
+          for (int v = 0; v < V / 2; ++v)
+            w2[v] = (uint32_t)f32_to_bf16_rne(d[2 * v]) | ((uint32_t)f32_to_bf16_rne(d[2 * v + 1]) << 16);
+          uint32_t* o = reinterpret_cast<uint32_t*>(out) + e0 / 2;
+          if constexpr (V >= 8) {
 #pragma unroll
-          for (int i = 0; i < V / 8; ++i)
-            reinterpret_cast<uint4*>(o)[i] =
-                make_uint4(w2[4 * i], w2[4 * i + 1], w2[4 * i + 2], w2[4 * i + 3]);
+            for (int i = 0; i < V / 8; ++i)
+              reinterpret_cast<uint4*>(o)[i] =
+                  make_uint4(w2[4 * i], w2[4 * i + 1], w2[4 * i + 2], w2[4 * i + 3]);
+          } else {
+#pragma unroll
+            for (int v = 0; v < V / 2; ++v) o[v] = w2[v];
+          }
         } else {
 #pragma unroll
-          for (int v = 0; v < V / 2; ++v) o[v] = w2[v];
+          for (int v = 0; v < V; ++v)
+            if (e0 + v < p.E) reinterpret_cast<uint16_t*>(out)[e0 + v] = f32_to_bf16_rne(d[v]);
         }
       } else {
+        if (vec && V >= 4) {
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-          if (e0 + v < p.E) reinterpret_cast<uint16_t*>(out)[e0 + v] = f32_to_bf16_rne(d[v]);
-      }
-    } else {
-      if (vec && V >= 4) {
+          for (int i = 0; i < V / 4; ++i)
+            reinterpret_cast<float4*>(out)[e0 / 4 + i] =
+                make_float4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < V / 4; ++i)
-          reinterpret_cast<float4*>(out)[e0 / 4 + i] =
-              make_float4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
-      } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-          if (e0 + v < p.E) reinterpret_cast<float*>(out)[e0 + v] = d[v];
+          for (int v = 0; v < V; ++v)
+            if (e0 + v < p.E) reinterpret_cast<float*>(out)[e0 + v] = d[v];
+        }
       }
     }
     __syncwarp();
@@ -841,12 +850,15 @@ struct BackwardLaunch {
   }
 };
 
-// Whole-lane vector accesses: every lane's V values lie inside the row and on
-// a 16-byte (or whole-piece) boundary.
-bool can_vector(const void* base, int64_t ld, int E, int V, int size) {
+// Whole-lane vector accesses: every lane's V values lie inside the row, or all
+// past it (2: no lane lies past it), and on a 16-byte (or whole-piece)
+// boundary.
+int can_vector(const void* base, int64_t ld, int E, int V, int size) {
   const int piece = V * size < 16 ? V * size : 16;
-  return E == 32 * V && ld * size % piece == 0 &&
-         (reinterpret_cast<uintptr_t>(base) % piece) == 0;
+  return E % V == 0 && ld * size % piece == 0 &&
+                 (reinterpret_cast<uintptr_t>(base) % piece) == 0
+             ? (E == 32 * V ? 2 : 1)
+             : 0;
 }
 
 bool scored_shape_ok(int T, int E, int k, int kmax, int dtype, int score, int64_t ld) {
@@ -901,7 +913,7 @@ extern "C" moe_status_t moe_route_scored(const void* logits, int logits_dtype, i
   const int V = lane_values(E);
   return dispatch_scored<ForwardLaunch>(V, logits_dtype == MOE_DTYPE_BF16,
                                         score == MOE_SCORE_SIGMOID, p,
-                                        (int)can_vector(logits, ld, E, V, size),
+                                        can_vector(logits, ld, E, V, size),
                                         reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -953,14 +965,16 @@ extern "C" moe_status_t moe_route_scored_backward(
   p.part = static_cast<float*>(workspace);
   p.err = device_error_word();
   const int V = lane_values(E);
-  int grid = scored_grid(T);
-  // few enough blocks that joining their sums stays short
-  if (grid > 4 * sm_count()) grid = 4 * sm_count();
+  // as many blocks as run at once: none queues, and joining their sums is short
+  // (and at least two tokens per warp, once there are some)
+  int grid = scored_grid(T > 512 ? (T + 1) / 2 : T);
+  const int most = grad_ctas_per_sm(V) * sm_count();
+  if (grid > most) grid = most;
   if (grid > kGradMaxBlocks) grid = kGradMaxBlocks;
-  const bool vec = can_vector(logits, ld, E, V, size) && can_vector(d_logits, ld_out, E, V, size);
+  const int vec = can_vector(d_logits, ld_out, E, V, size) ? can_vector(logits, ld, E, V, size) : 0;
   const moe_status_t s =
       dispatch_scored<BackwardLaunch>(V, logits_dtype == MOE_DTYPE_BF16,
-                                      score == MOE_SCORE_SIGMOID, p, grid, (int)vec, st);
+                                      score == MOE_SCORE_SIGMOID, p, grid, vec, st);
   if (s != MOE_OK) return s;
   return launch(route_losses_kernel, kLossCluster, kLossThreads, 0, st, p, grid, losses);
 }
