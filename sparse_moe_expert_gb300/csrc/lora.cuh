@@ -86,7 +86,7 @@ struct LoraPlan {
 };
 
 // Most adapters the grouping's counters hold in shared memory.
-constexpr int kLoraPlanAdapters = 4096;
+constexpr int kLoraPlanAdapters = 2048;
 
 inline int64_t lora_tile_capacity(int64_t rows, int E, int n_adapters) {
   const int64_t most =

@@ -27,7 +27,7 @@ namespace {
 
 // ---- grouping --------------------------------------------------------------
 
-constexpr int kPlanThreads = 256;
+constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanUnroll = 4;
 
@@ -272,7 +272,7 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
 
 constexpr int kShrinkThreads = 256;
 constexpr int kShrinkWarps = kShrinkThreads / 32;
-constexpr int kShrinkStages = 4;
+constexpr int kShrinkStages = 3;
 
 // A tile of up to 16 rows, k in [k0, k1): the warps take blocks of 32 k in
 // turn, fragments straight from global memory (lane t of a quad holds 8
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kShrinkThreads, NT <= 8 ? 2 : 1) lora_shrink_t
             umma_bf16(tmem, xd + 2 * k, ad + 2 * k, idesc, kb > 0 || k > 0);
           umma_commit(&done[s]);
         }
-        // the stage that k-block kb + 3 takes was read by the MMAs of kb - 1
+        // the stage that k-block kb + 2 takes was read by the MMAs of kb - 1
         const int nx = kb + kShrinkStages - 1;
         if (kb > 0) {
           const int sp = (kb - 1) % kShrinkStages;
