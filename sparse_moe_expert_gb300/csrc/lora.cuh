@@ -23,7 +23,6 @@ struct LoraParams {
   const float* scales;
   const void* base;
   void* out;
-  float* v;  // [rows, R]
   unsigned int* err;
 };
 
@@ -64,6 +63,20 @@ __device__ __forceinline__ LoraRow lora_row(const LoraParams& p, int r) {
 // Which row of x a row uses (the row's slot is known).
 __device__ __forceinline__ int lora_x_row(const LoraParams& p, int r) {
   return p.sorted && p.x_by_token ? __ldg(p.sorted + r) / p.kmax : r;
+}
+
+// A shared-memory address of this CTA as CTA `rank` of the cluster has it, and
+// the barrier of the cluster's CTAs.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(r)
+               : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
 }
 
 // Rows grouped by the matrices they use, made on the device for one call.

