@@ -52,59 +52,68 @@ __device__ __forceinline__ float load_logit(const void* row, int e) {
   return __ldg(static_cast<const float*>(row) + e);
 }
 
-// The lane's V logits of one row: 16-byte (or narrower whole-lane) loads when
-// `vec` says that every lane's piece is aligned and inside the row, else one
-// load per expert.  Experts past E read as -inf.
+// The lane's V logits of one row as they lie in memory, so that a row can be
+// on its way while another is worked on: 16-byte (or narrower whole-lane)
+// loads when `vec` says that every lane's piece is aligned and inside the row
+// (2) or inside or wholly past it (1), else one load per expert.  Experts past
+// E read as -inf.
 template <int V, bool BF16>
-__device__ __forceinline__ void load_logits(float (&l)[V], const void* row, int e0, int E,
-                                            int vec) {
-  if (vec == 1 && e0 >= E) {
+struct RawLogits {
+  static constexpr int W = BF16 ? (V + 1) / 2 : V;
+  static constexpr uint32_t kNone = BF16 ? 0xFF80FF80u : 0xFF800000u;
+  uint32_t w[W];
+
+  __device__ __forceinline__ void load(const void* row, int e0, int E, int vec) {
+    if (vec == 1 && e0 >= E) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) l[v] = -INFINITY;
-    return;
-  }
-  if constexpr (BF16) {
-    if (vec && V >= 2) {
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(row) + e0);
-      if constexpr (V >= 8) {
+      for (int i = 0; i < W; ++i) w[i] = kNone;
+    } else if (vec && V >= (BF16 ? 2 : 4)) {
+      const uint32_t* p = static_cast<const uint32_t*>(row) + (BF16 ? e0 / 2 : e0);
+      if constexpr (W >= 4) {
 #pragma unroll
-        for (int i = 0; i < V / 8; ++i) {
+        for (int i = 0; i < W / 4; ++i) {
           const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + i);
-          const uint32_t w4[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = bf16x2_to_f32x2(w4[j]);
-            l[8 * i + 2 * j] = f.x;
-            l[8 * i + 2 * j + 1] = f.y;
-          }
+          w[4 * i] = q.x;
+          w[4 * i + 1] = q.y;
+          w[4 * i + 2] = q.z;
+          w[4 * i + 3] = q.w;
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < V / 2; ++j) {
-          const float2 f = bf16x2_to_f32x2(__ldg(p + j));
-          l[2 * j] = f.x;
-          l[2 * j + 1] = f.y;
-        }
+        for (int i = 0; i < W; ++i) w[i] = __ldg(p + i);
       }
-      return;
-    }
-  } else {
-    if (vec && V >= 4) {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(row) + e0);
+    } else if constexpr (BF16) {
+      const uint16_t* p = static_cast<const uint16_t*>(row);
 #pragma unroll
-      for (int i = 0; i < V / 4; ++i) {
-        const float4 q = __ldg(p + i);
-        l[4 * i] = q.x;
-        l[4 * i + 1] = q.y;
-        l[4 * i + 2] = q.z;
-        l[4 * i + 3] = q.w;
+      for (int i = 0; i < W; ++i) {
+        const int e = e0 + 2 * i;
+        const uint32_t lo = e < E ? __ldg(p + e) : 0xFF80u;
+        const uint32_t hi = V > 1 && e + 1 < E ? __ldg(p + e + 1) : 0xFF80u;
+        w[i] = lo | (hi << 16);
       }
-      return;
+    } else {
+      const uint32_t* p = static_cast<const uint32_t*>(row);
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = e0 + i < E ? __ldg(p + e0 + i) : kNone;
     }
   }
+  __device__ __forceinline__ void get(float (&l)[V]) const {
 #pragma unroll
-  for (int v = 0; v < V; ++v)
-    l[v] = e0 + v < E ? load_logit<BF16>(row, e0 + v) : -INFINITY;
+    for (int v = 0; v < V; ++v) {
+      if constexpr (BF16)
+        l[v] = __uint_as_float((v & 1) ? w[v / 2] & 0xFFFF0000u : w[v / 2] << 16);
+      else
+        l[v] = __uint_as_float(w[v]);
+    }
+  }
+};
+
+template <int V, bool BF16>
+__device__ __forceinline__ void load_logits(float (&l)[V], const void* row, int e0, int E,
+                                            int vec) {
+  RawLogits<V, BF16> raw;
+  raw.load(row, e0, E, vec);
+  raw.get(l);
 }
 
 __device__ __forceinline__ float sigmoid_f32(float l) {
@@ -574,7 +583,7 @@ __device__ __forceinline__ float exp_approx(float x) {
 // it.  The hardware exponential and reciprocal are good to a few 1e-7 here,
 // far inside the rounding of the differences they enter.  The chosen slots'
 // d u meets its expert's lane through a row of shared memory per warp.
-constexpr int grad_ctas_per_sm(int V) { return V <= 4 ? 4 : V <= 8 ? 3 : V <= 16 ? 2 : 1; }
+constexpr int grad_ctas_per_sm(int V) { return V <= 4 ? 4 : V <= 16 ? 2 : 1; }
 
 template <int V, bool BF16, bool SIGMOID>
 __global__ void __launch_bounds__(kScoredThreads, grad_ctas_per_sm(V)) route_scored_backward_kernel(ScoredGradParams p,
@@ -601,17 +610,27 @@ __global__ void __launch_bounds__(kScoredThreads, grad_ctas_per_sm(V)) route_sco
   float lse2 = 0.0f;
   bool bad = false;
   __syncwarp();
-  for (int64_t t = (int64_t)blockIdx.x * kScoredWarps + warp; t < p.T;
-       t += (int64_t)gridDim.x * kScoredWarps) {
-    const char* row = static_cast<const char*>(p.logits) + t * p.ld * (BF16 ? 2 : 4);
-    int id = -1;
-    float dw = 0.0f;
-    if (p.d_w && lane < p.k) {
-      id = __ldg(p.ids + t * p.kmax + lane);
-      dw = __ldg(p.d_w + t * p.kmax + lane) * p.scale;
+  const int64_t step = (int64_t)gridDim.x * kScoredWarps;
+  const bool slot = p.d_w && lane < p.k;
+  int64_t t = (int64_t)blockIdx.x * kScoredWarps + warp;
+  RawLogits<V, BF16> raw;
+  int next_id = -1;
+  float next_dw = 0.0f;
+  auto fetch = [&](int64_t to) {
+    raw.load(static_cast<const char*>(p.logits) + to * p.ld * (BF16 ? 2 : 4), e0, p.E, vec);
+    if (slot) {
+      next_id = __ldg(p.ids + to * p.kmax + lane);
+      next_dw = __ldg(p.d_w + to * p.kmax + lane);
     }
+  };
+  if (t < p.T) fetch(t);
+  for (; t < p.T; t += step) {
+    const char* row = static_cast<const char*>(p.logits) + t * p.ld * (BF16 ? 2 : 4);
     float l[V];
-    load_logits<V, BF16>(l, row, e0, p.E, vec);
+    raw.get(l);
+    int id = next_id;
+    float dw = next_dw * p.scale;
+    if (t + step < p.T) fetch(t + step);  // the next token's, while this one is worked on
     if (id >= p.E) {
       bad = true;
       id = -1;
