@@ -543,7 +543,7 @@ struct ScoredGradParams {
   float scale, balance, z;
   void* d_logits;  // like logits, rows ld_out elements apart
   int64_t ld_out;
-  float* part;  // [grid][E + 1]: sums over the block's tokens of q_e and of lse^2
+  float* part;  // [grid][2]: the block's parts of sum_te c_e q_te (the balance loss) and of sum_t lse^2
   unsigned int* err;
 };
 
@@ -590,24 +590,23 @@ __global__ void __launch_bounds__(kScoredThreads, grad_ctas_per_sm(V)) route_sco
                                                                                int vec) {
   constexpr int P = 32 * V;
   __shared__ __align__(16) float scatter[kScoredWarps][P];
-  __shared__ float lse_part[kScoredWarps];
+  __shared__ float loss_part[kScoredWarps][2];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int e0 = lane * V;
   float* buf = scatter[warp];
-  float coef[V], qsum[V];  // d balance / d q_te, and the running sum of q_te
+  float coef[V];  // c_e = d balance / d q_te; the loss itself is sum_te c_e q_te
   // coef = balance * E / (k T) * counts / T
   const float unit = p.counts ? p.balance * ((float)p.E / ((float)p.k * (float)p.T)) / (float)p.T : 0.0f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     coef[v] = p.counts && e0 + v < p.E ? unit * (float)__ldg(p.counts + e0 + v) : 0.0f;
-    qsum[v] = 0.0f;
     buf[e0 + v] = 0.0f;
   }
   const bool need_z = p.z != 0.0f;
   const float zt = 2.0f * p.z / (float)p.T;
-  float lse2 = 0.0f;
+  float lse2 = 0.0f, bal = 0.0f;
   bool bad = false;
   __syncwarp();
   const int64_t step = (int64_t)gridDim.x * kScoredWarps;
@@ -687,6 +686,7 @@ __global__ void __launch_bounds__(kScoredThreads, grad_ctas_per_sm(V)) route_sco
     // what is the same for all of the token's experts: sum c q, and the
     // softmax's sum of d u s when the weights are not renormalized
     const float dotq = sc * uinv;
+    bal += dotq;
     const float off = SIGMOID || p.renorm ? dotq : fmaf(sd, uinv, dotq);
     __syncwarp();
     float d[V];
@@ -698,10 +698,8 @@ __global__ void __launch_bounds__(kScoredThreads, grad_ctas_per_sm(V)) route_sco
         const float ds = fmaf(coef[v] - off, uinv, own);
         d[v] = ds * (s - s * s);
         if (need_z) d[v] = fmaf(zc, ex[v], d[v]);
-        qsum[v] = fmaf(u[v], uinv, qsum[v]);
       } else {
         d[v] = fmaf(zc, u[v], s * (own + (coef[v] - off)));
-        qsum[v] += s;
       }
     }
     __syncwarp();
@@ -746,79 +744,33 @@ __global__ void __launch_bounds__(kScoredThreads, grad_ctas_per_sm(V)) route_sco
   }
   if (bad) raise_device_error(p.err, MOE_DEVERR_BAD_EXPERT);
   // the block's sums, warps in order
-  __syncwarp();
-#pragma unroll
-  for (int v = 0; v < V; ++v) buf[e0 + v] = qsum[v];
-  if (lane == 0) lse_part[warp] = lse2;
+  if (lane == 0) {
+    loss_part[warp][0] = bal;
+    loss_part[warp][1] = lse2;
+  }
   __syncthreads();
-  for (int e = threadIdx.x; e <= p.E; e += kScoredThreads) {
+  if (threadIdx.x < 2) {
     float a = 0.0f;
-    for (int w = 0; w < kScoredWarps; ++w) a += e < p.E ? scatter[w][e] : lse_part[w];
-    p.part[(int64_t)blockIdx.x * (p.E + 1) + e] = a;
+    for (int w = 0; w < kScoredWarps; ++w) a += loss_part[w][threadIdx.x];
+    p.part[2 * blockIdx.x + threadIdx.x] = a;
   }
 }
 
-// losses[0] = balance E / (k T) sum_e counts_e mean_t q_te, losses[1] = z mean lse^2.
-// A cluster of 8 CTAs shares the columns of the partial sums: lane = column,
-// the warps take the blocks in turn, and the leader adds the CTAs' parts in
-// rank order, so the sums always run in one order.
-constexpr int kLossThreads = 1024;
-constexpr int kLossCluster = 8;
-__global__ void __cluster_dims__(kLossCluster, 1, 1) __launch_bounds__(kLossThreads)
-    route_losses_kernel(ScoredGradParams p, int blocks, float* losses) {
-  __shared__ float part[kLossThreads / 32][33];
-  __shared__ float joined[kLossCluster][2];
+// losses[0] = sum_te c_e q_te, losses[1] = z mean lse^2: the blocks' parts in
+// one order (per lane, then a butterfly), a warp for each loss.
+__global__ void __launch_bounds__(64) route_losses_kernel(ScoredGradParams p, int blocks,
+                                                          float* losses) {
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float bal = 0.0f, zsum = 0.0f;  // warp 0
-  for (int x0 = blockIdx.x * 32; x0 <= p.E; x0 += kLossCluster * 32) {
-    const int x = x0 + lane;
-    float a = 0.0f;
-    if (x <= p.E) {
-#pragma unroll 4
-      for (int b = warp; b < blocks; b += kLossThreads / 32)
-        a += p.part[(int64_t)b * (p.E + 1) + x];
-    }
-    part[warp][lane] = a;
-    __syncthreads();
-    if (warp == 0) {
-      float s = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kLossThreads / 32; ++w) s += part[w][lane];
-      if (x < p.E && p.counts) bal += s * (float)__ldg(p.counts + x);
-      if (x == p.E) zsum = s;
-    }
-    __syncthreads();
-  }
-  if (warp == 0) {
-    bal = warp_sum(bal);
-    zsum = warp_sum(zsum);
-    if (lane == 0) {
-      // into the leader's shared memory
-      uint32_t at;
-      asm volatile("mapa.shared::cluster.u32 %0, %1, 0;"
-                   : "=r"(at)
-                   : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(&joined[blockIdx.x][0]))));
-      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(bal) : "memory");
-      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 4), "f"(zsum) : "memory");
-    }
-  }
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    float s = 0.0f, z = 0.0f;
-    for (int r = 0; r < kLossCluster; ++r) {
-      s += joined[r][0];
-      z += joined[r][1];
-    }
-    const float T = (float)p.T;
-    losses[0] = p.balance * ((float)p.E / ((float)p.k * T)) * (s / T);
-    losses[1] = p.z * (z / T);
-  }
+  const int lane = threadIdx.x & 31, which = threadIdx.x >> 5;
+  float a = 0.0f;
+#pragma unroll 8
+  for (int b = lane; b < blocks; b += 32) a += p.part[2 * b + which];
+  a = warp_sum(a);
+  if (lane == 0) losses[which] = which ? p.z * (a / (float)p.T) : a;
 }
 
-constexpr int kGradMaxBlocks = 1024;  // rows of partial sums the workspace holds
+constexpr int kGradMaxBlocks = 1024;  // blocks whose sums the workspace holds
 
 int lane_values(int E) {
   int v = 1;
@@ -938,7 +890,7 @@ extern "C" moe_status_t moe_route_scored(const void* logits, int logits_dtype, i
 
 extern "C" size_t moe_route_backward_workspace_size(int E) {
   if (E < 1 || E > 1024) return 0;
-  return (size_t)kGradMaxBlocks * (E + 1) * sizeof(float);
+  return (size_t)kGradMaxBlocks * 2 * sizeof(float);
 }
 
 extern "C" moe_status_t moe_route_scored_backward(
@@ -984,7 +936,7 @@ extern "C" moe_status_t moe_route_scored_backward(
   p.part = static_cast<float*>(workspace);
   p.err = device_error_word();
   const int V = lane_values(E);
-  // as many blocks as run at once: none queues, and joining their sums is short
+  // as many blocks as run at once: none queues
   // (and at least two tokens per warp, once there are some)
   int grid = scored_grid(T > 512 ? (T + 1) / 2 : T);
   const int most = grad_ctas_per_sm(V) * sm_count();
@@ -995,5 +947,5 @@ extern "C" moe_status_t moe_route_scored_backward(
       dispatch_scored<BackwardLaunch>(V, logits_dtype == MOE_DTYPE_BF16,
                                       score == MOE_SCORE_SIGMOID, p, grid, vec, st);
   if (s != MOE_OK) return s;
-  return launch(route_losses_kernel, kLossCluster, kLossThreads, 0, st, p, grid, losses);
+  return launch(route_losses_kernel, 1, 64, 0, st, p, grid, losses);
 }
