@@ -17,6 +17,9 @@
  *   [B] "Qwen3.5-MoE与Qwen3-MoE架构差异深度解析" (jsqmd.com/news/1062166)
  *   [C] "oMLX MoE gate/up 融合优化：qwen35_moe_gate_up 实现剖析" (xdnf.cn/news/169715)
  *
+ * Beside these steps: routing by scores with its gradient, the combine's
+ * gradient, and low-rank adapters of many requests (the last declarations).
+ *
  * Conventions shared by every call
  * --------------------------------
  * - All tensor pointers are DEVICE pointers owned by the caller; the library
@@ -610,7 +613,10 @@ moe_status_t moe_combine_backward(const uint16_t* d_out, const void* y, int y_dt
  *   RAW:    out[r] = z[r] in base's type
  *   SWIGLU: out[r, n] = SiLU(z[r, n]) * z[r, N/2 + n]   (base fp32)
  * Rows of tokens without an adapter get their base through unchanged.
- * Accumulation in fp32; x A^T is kept in fp32 between the two products.
+ * Accumulation in fp32; scale * x A^T enters the second product in fp32 (few
+ * rows) or as bf16 terms that hold it to 2^-17 (bf16 base) or 2^-26 (fp32 base)
+ * of itself (many rows, grouped by adapter on the device).  The same call
+ * gives the same bits.
  *
  * Two forms:
  *   one projection: topk_ids, sorted_assign, expert_offsets NULL, kmax = E = 1;
@@ -626,6 +632,7 @@ moe_status_t moe_combine_backward(const uint16_t* d_out, const void* y, int y_dt
  * base          [T*kmax, N] of base_dtype; NULL (RAW only): zeros.
  * out           [T*kmax, N] (RAW; may be base: in place) or [T*kmax, N/2]
  *               (SWIGLU, of out_dtype fp32 or bf16; not base's memory).
+ *               x must not overlap out.
  * workspace     moe_lora_workspace_size(...) bytes of device scratch.
  * Limits: K % 64 == 0, N % 64 == 0, R % 8 == 0, 8 <= R <= 128 (smaller ranks
  * are padded with zero rows of A), n_adapters * E <= 2^20.
