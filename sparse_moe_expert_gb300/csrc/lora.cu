@@ -92,8 +92,9 @@ __global__ void __launch_bounds__(kLoraThreads, row_ctas_per_sm(NT)) lora_row_ke
   pdl_wait();
   pdl_trigger();
   const int r = blockIdx.x / ctas, rank = blockIdx.x % ctas;
-  if (r >= lora_rows(p)) return;  // the whole cluster alike
-  const LoraRow row = lora_row(p, r);
+  const int entry = p.sorted ? __ldg(p.sorted + r) : r;  // beside the row count, not after it
+  if (r >= lora_rows(p)) return;                         // the whole cluster alike
+  const LoraRow row = lora_row(p, r, entry);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int nt = p.R >> 3;
   const int cols = SWIGLU ? p.N / 2 : p.N;

@@ -37,10 +37,10 @@ __device__ __forceinline__ int lora_rows(const LoraParams& p) {
   return min(max(__ldg(p.offsets + p.E), 0), p.T * p.kmax);
 }
 
-__device__ __forceinline__ LoraRow lora_row(const LoraParams& p, int r) {
-  int a = r, e = 0;
+// `a`: the row's entry of sorted (r itself without one).
+__device__ __forceinline__ LoraRow lora_row(const LoraParams& p, int r, int a) {
+  int e = 0;
   if (p.sorted) {
-    a = __ldg(p.sorted + r);
     if (a < 0 || a >= p.T * p.kmax) {
       raise_device_error(p.err, MOE_DEVERR_BAD_INDEX);
       return {-1, 0};
@@ -58,6 +58,10 @@ __device__ __forceinline__ LoraRow lora_row(const LoraParams& p, int r) {
     row.slot = ad * p.E + e;
   }
   return row;
+}
+
+__device__ __forceinline__ LoraRow lora_row(const LoraParams& p, int r) {
+  return lora_row(p, r, p.sorted ? __ldg(p.sorted + r) : r);
 }
 
 // Which row of x a row uses (the row's slot is known).

@@ -673,7 +673,11 @@ __global__ void __launch_bounds__(kScoredThreads, grad_ctas_per_sm(V)) route_sco
     float dp;
     if (p.renorm) {
       const float r = __fdividef(sd, st);
-      dp = st > 0.0f && id >= 0 ? __fdividef((dw - r) * (SIGMOID ? 1.0f : su), st) : 0.0f;
+      // one chosen expert has the constant weight `scale`: no gradient, not
+      // the rounding of dw - dw
+      const unsigned with = __ballot_sync(kFull, uj > 0.0f);
+      const bool several = (with & (with - 1u)) != 0u;
+      dp = several && id >= 0 ? __fdividef((dw - r) * (SIGMOID ? 1.0f : su), st) : 0.0f;
     } else {
       dp = dw;
     }

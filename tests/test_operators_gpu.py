@@ -490,6 +490,12 @@ def test_route_backward_parts_strides_and_empty(cuda_lib):
                                             torch.tensor(bw, device=d), torch.tensor(bc, device=d),
                                             balance_coef=0.1, z_coef=0.1) for _ in range(2)]
     assert torch.equal(a[0][0], a[1][0]) and torch.equal(a[0][1], a[1][1])
+    # one chosen expert has a constant weight: exactly no gradient
+    for score in (0, 1):
+        one = ids_t.clone()
+        one[:, 1:] = -1
+        dl, _ = cuda_lib.moe_route_scored_backward(l, one, dw_t, score=score, scale=2.5)
+        assert not to_np(dl).any()
     # a bad id is reported and skipped
     cuda_lib.moe_get_device_error(clear=True)
     ids_t[5, 0] = 64
