@@ -12,6 +12,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -146,7 +147,7 @@ int64_t rows2d(const Tensor& t, const char* name) {
 }
 
 Tensor make(c10::IntArrayRef shape, at::ScalarType type, c10::Device dev) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+  return at::detail::empty_cuda(shape, type, dev, std::nullopt);
 }
 
 int as_int(int64_t v, const char* what) {
