@@ -344,10 +344,9 @@ __device__ __forceinline__ void lane_top2(const float (&c)[V], float& a1, float&
 // largest choice, so every chosen expert has c~ >= bound - 2 eps.  Those candidates
 // (about k + 2 of 256) get one lane each, their exact scores and their ranks
 // by counting, and the lanes with rank < k are the answer.  Groups are cut on
-// c~ too when the cut is wider than the approximation.  More than 32
-// candidates (many equal choices), groups too close to call and groups that
-// are not whole runs of lanes go to route_token_exact; results do not depend
-// on which way was taken.
+// c~ too when the cut is wider than the approximation.  More than 16
+// candidates (many equal choices) and groups too close to call go to
+// route_token_exact; results do not depend on which way was taken.
 //
 // Bound by the issue rate: some 550 instructions per token of 256 experts
 // (issue slots 69 % used, ALU 58 %).  Measured, k 8 of 256 bf16 experts in 8
@@ -364,6 +363,7 @@ __global__ void __launch_bounds__(kScoredThreads, V <= 8 ? 4 : 2)
   constexpr int C = 16;  // candidates of a token
   __shared__ __align__(16) int cand_id[kScoredWarps][2 * C];
   __shared__ __align__(16) float cand_x[kScoredWarps][2 * C];
+  __shared__ __align__(16) float group_x[kScoredWarps][32 * V];  // groups that straddle lanes
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -382,7 +382,13 @@ __global__ void __launch_bounds__(kScoredThreads, V <= 8 ? 4 : 2)
   constexpr float eps = 1e-6f;
   const int G = p.n_groups, gsz = p.E / G, span = gsz / V;  // span: lanes of a group
   const bool lane_groups = gsz % V == 0 && (span & (span - 1)) == 0 && span <= 32;
-  const int my_group = e0 / gsz;  // >= G past the experts
+  // lanes that work on a group: its own when groups are whole aligned runs of
+  // lanes, else as many as fit (a power of two), over shared memory
+  int width = 1;
+  if (lane_groups) width = span;
+  else
+    while (2 * width * G <= 32) width *= 2;
+  const int my_group = lane_groups ? e0 / gsz : lane / width;  // >= G: none
 
   // The candidates of the token whose logits lie at `row` into ids[]; their
   // number, or -1 when they are not certain or too many.  m, den: the
@@ -414,30 +420,59 @@ __global__ void __launch_bounds__(kScoredThreads, V <= 8 ? 4 : 2)
     lane_top2<V>(c, best, second);
     bool live = true;  // the lane's group is among the chosen
     if (G > 1) {
-      if (!lane_groups) return -1;
       float a1 = best, a2 = second;
-      for (int o = 1; o < span; o <<= 1) {
+      float* xs = group_x[warp];
+      const int from = my_group * gsz + (lane & (width - 1));
+      const int to = my_group < G ? (my_group + 1) * gsz : 0;
+      if (!lane_groups) {
+        __syncwarp();
+#pragma unroll
+        for (int v = 0; v < V; ++v) xs[e0 + v] = c[v];
+        __syncwarp();
+        a1 = a2 = -INFINITY;
+        for (int e = from; e < to; e += width) merge_top2(a1, a2, xs[e], -INFINITY);
+      }
+      for (int o = 1; o < width; o <<= 1) {
         const float b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
         merge_top2(a1, a2, b1, b2);
       }
       // every lane of a group holds the group's value
       const float val = p.group_top == 2 && a2 > -INFINITY ? a1 + a2 : a1;
       const float mine = my_group < G ? val : -INFINITY;
+      const bool first = (lane & (width - 1)) == 0;  // one lane of each group
       float rest = mine, cut = -INFINITY;
 #pragma unroll 4
       for (int r = 0; r < p.topk_groups; ++r) {
         cut = redux_max(rest);
         if (rest == cut) rest = -INFINITY;
       }
+      int groups = __popc(__ballot_sync(kFull, first && mine >= cut && mine > -INFINITY));
+      if (groups > p.topk_groups) {  // equal values left together: count them
+        rest = mine;
+        groups = 0;
+        while (groups < p.topk_groups) {
+          cut = redux_max(rest);
+          groups += __popc(__ballot_sync(kFull, first && rest == cut));
+          if (rest == cut) rest = -INFINITY;
+        }
+      }
       const float next = redux_max(rest);
       live = mine >= cut && mine > -INFINITY;
-      // no tie among the chosen values or at the cut: as many groups as asked
-      // (or all that have an expert), the next one clearly below
-      const int groups = __popc(__ballot_sync(kFull, live && (lane & (span - 1)) == 0));
+      // as many groups as asked (or all that have an expert), and the next one
+      // clearly below
       const bool sure = next == -INFINITY ? groups <= p.topk_groups
                                           : groups == p.topk_groups &&
                                                 cut - next > 4.0f * eps + fabsf(next) * 0x1p-20f;
       if (!sure) return -1;
+      if (!lane_groups) {  // strike the other groups' choices
+        if (!live)
+          for (int e = from; e < to; e += width) xs[e] = -INFINITY;
+        __syncwarp();
+#pragma unroll
+        for (int v = 0; v < V; ++v) c[v] = xs[e0 + v];
+        lane_top2<V>(c, best, second);
+        live = true;
+      }
     }
     float bound = -INFINITY;
     float rest = live ? best : -INFINITY, after = live ? second : -INFINITY;
