@@ -149,65 +149,44 @@ __device__ __forceinline__ void merge_top2(float& a1, float& a2, float b1, float
   a2 = fmaxf(lo, fmaxf(a2, b2));
 }
 
-// Strikes the choices outside the best `topk_groups` groups (key = 0).  A
+// Strikes the choices outside the best `topk_groups` groups (c = -inf).  A
 // group's value is its best choice, or the sum of its two best (of the only
 // one, if it has one); a group without any available expert is never ahead of
-// one that has; equal values go to the lower group.
+// one that has; equal values go to the lower group.  xs: 32 V floats of shared
+// memory; the lanes share the groups' experts there, a power of two of them
+// to a group, because a group need not be a run of whole lanes.
 template <int V>
-__device__ __forceinline__ void limit_groups(const ScoredParams& p, const float (&c)[V],
-                                             uint32_t (&key)[V], int e0) {
+__device__ __forceinline__ void limit_groups(const ScoredParams& p, float (&c)[V], int e0,
+                                             float* xs) {
   const int lane = threadIdx.x & 31;
   const int G = p.n_groups, gsz = p.E / G;
-  uint32_t mine = 0u;  // lane g: key of group g's value
-  const int span = gsz / V;  // lanes of a group when groups are whole aligned lane runs
-  const bool aligned = gsz % V == 0 && (span & (span - 1)) == 0 && span <= 32;
-  if (aligned) {
-    float a1 = -INFINITY, a2 = -INFINITY;
+  int width = 1;
+  while (2 * width * G <= 32) width *= 2;
+  const int g = lane / width, from = g * gsz + (lane & (width - 1)), to = g < G ? (g + 1) * gsz : 0;
+  __syncwarp();
 #pragma unroll
-    for (int v = 0; v < V; ++v) merge_top2(a1, a2, key[v] ? c[v] : -INFINITY, -INFINITY);
-    for (int o = 1; o < span; o <<= 1) {
-      const float b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
-      merge_top2(a1, a2, b1, b2);
-    }
-    const float val = p.group_top == 2 && a2 > -INFINITY ? __fadd_rn(a1, a2) : a1;
-    const uint32_t kv = a1 > -INFINITY ? choice_key(val) : 0u;
-    mine = __shfl_sync(kFull, kv, lane < G ? lane * span : 0);
-  } else {
-    for (int g = 0; g < G; ++g) {
-      float a1 = -INFINITY, a2 = -INFINITY;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int e = e0 + v;
-        if (key[v] && e >= g * gsz && e < (g + 1) * gsz) merge_top2(a1, a2, c[v], -INFINITY);
-      }
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
-        merge_top2(a1, a2, b1, b2);
-      }
-      const float val = p.group_top == 2 && a2 > -INFINITY ? __fadd_rn(a1, a2) : a1;
-      if (lane == g) mine = a1 > -INFINITY ? choice_key(val) : 0u;
-    }
+  for (int v = 0; v < V; ++v) xs[e0 + v] = c[v];
+  __syncwarp();
+  float a1 = -INFINITY, a2 = -INFINITY;
+  for (int e = from; e < to; e += width) merge_top2(a1, a2, xs[e], -INFINITY);
+  for (int o = 1; o < width; o <<= 1) {
+    const float b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
+    merge_top2(a1, a2, b1, b2);
   }
+  const float val = p.group_top == 2 && a2 > -INFINITY ? __fadd_rn(a1, a2) : a1;
+  const uint32_t kv = a1 > -INFINITY ? choice_key(val) : 0u;
+  const uint32_t mine = __shfl_sync(kFull, kv, lane < G ? lane * width : 0);  // lane h: group h
   int rank = 0;
-  for (int g = 0; g < G; ++g) {
-    const uint32_t o = __shfl_sync(kFull, mine, g);
-    rank += o > mine || (o == mine && g < lane);
+  for (int h = 0; h < G; ++h) {
+    const uint32_t o = __shfl_sync(kFull, mine, h);
+    rank += o > mine || (o == mine && h < lane);
   }
   const unsigned chosen = __ballot_sync(kFull, lane < G && rank < p.topk_groups);
-  if (aligned) {
-    const int g = e0 / gsz;
-    if (g >= G || !((chosen >> g) & 1u)) {
+  if (g < G && !((chosen >> g) & 1u))
+    for (int e = from; e < to; e += width) xs[e] = -INFINITY;
+  __syncwarp();
 #pragma unroll
-      for (int v = 0; v < V; ++v) key[v] = 0u;
-    }
-  } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int g = (e0 + v) / gsz;
-      if (g >= G || !((chosen >> g) & 1u)) key[v] = 0u;
-    }
-  }
+  for (int v = 0; v < V; ++v) c[v] = xs[e0 + v];
 }
 
 __device__ __forceinline__ float redux_max(float v) {
@@ -238,7 +217,8 @@ __device__ __forceinline__ void store_chosen(const ScoredParams& p, int64_t t, i
 // The definition as it stands: exact scores of every expert, then k rounds of
 // a warp argmax.  For the tokens whose fast selection is not certain.
 template <int V, bool BF16, bool SIGMOID>
-__device__ __noinline__ void route_token_exact(const ScoredParams& p, int64_t t, int vec) {
+__device__ __noinline__ void route_token_exact(const ScoredParams& p, int64_t t, int vec,
+                                              float* xs) {
   const int lane = threadIdx.x & 31, e0 = lane * V;
   float s[V], c[V];
   uint32_t key[V];
@@ -266,9 +246,11 @@ __device__ __noinline__ void route_token_exact(const ScoredParams& p, int64_t t,
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     c[v] = p.bias && e0 + v < p.E ? __fadd_rn(s[v], __ldg(p.bias + e0 + v)) : s[v];
-    key[v] = key[v] && c[v] > -INFINITY ? choice_key(c[v]) : 0u;
+    if (!key[v] || !(c[v] > -INFINITY)) c[v] = -INFINITY;
   }
-  if (p.n_groups > 1) limit_groups<V>(p, c, key, e0);
+  if (p.n_groups > 1) limit_groups<V>(p, c, e0, xs);
+#pragma unroll
+  for (int v = 0; v < V; ++v) key[v] = c[v] > -INFINITY ? choice_key(c[v]) : 0u;
   int my_id = -1;
   float my_s = 0.0f;
   for (int r = 0; r < p.k; ++r) {
@@ -350,7 +332,7 @@ __device__ __forceinline__ void lane_top2(const float (&c)[V], float& a1, float&
 //
 // Bound by the issue rate: some 550 instructions per token of 256 experts
 // (issue slots 69 % used, ALU 58 %).  Measured, k 8 of 256 bf16 experts in 8
-// groups, 65536 tokens: 45 us (37.7 MB: 6 us at the copy rate); with exact
+// groups, 65536 tokens: 46 us (37.7 MB: 6 us at the copy rate); with exact
 // scores for every expert and k rounds of argmax 93 us; 64 experts 23 us.  A
 // lane per token (rows in shared memory) was no faster: 47 us, 83 us for fp32
 // rows, whose 32 rows per warp leave few warps.
@@ -558,8 +540,8 @@ __global__ void __launch_bounds__(kScoredThreads, V <= 8 ? 4 : 2)
       p.ids[out + i] = -1;
       p.w[out + i] = 0.0f;
     }
-    if (n0 < 0) route_token_exact<V, BF16, SIGMOID>(p, t, vec);
-    if (n1 < 0) route_token_exact<V, BF16, SIGMOID>(p, t + 1, vec);
+    if (n0 < 0) route_token_exact<V, BF16, SIGMOID>(p, t, vec, group_x[warp]);
+    if (n1 < 0) route_token_exact<V, BF16, SIGMOID>(p, t + 1, vec, group_x[warp]);
     __syncwarp();
   }
   if (bad) raise_device_error(p.err, MOE_DEVERR_BAD_SCORE);
