@@ -279,32 +279,36 @@ __device__ __forceinline__ void shrink_small(const LoraParams& p, const LoraPlan
   const uint4* x1 = reinterpret_cast<const uint4*>(
       p.x + (int64_t)(on1 ? pl.rows[tile.y + g + 8].y : 0) * p.K + k0) + t;
   const uint4* ar = reinterpret_cast<const uint4*>(p.a + ((int64_t)tile.x * p.R + g) * p.K + k0) + t;
-  float acc[NT][4];
-#pragma unroll
-  for (int q = 0; q < NT; ++q)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[q][i] = 0.0f;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll 2
-  for (int kb = warp; kb < (k1 - k0) >> 5; kb += kShrinkWarps) {
-    const uint4 a = on0 ? __ldg(x0 + kb * 4) : zero, b = on1 ? __ldg(x1 + kb * 4) : zero;
-    uint4 w[NT];
-#pragma unroll
-    for (int q = 0; q < NT; ++q)
-      if (q < nt) w[q] = ldg_nc_v4(ar + (int64_t)q * p.K + kb * 4);
-#pragma unroll
-    for (int q = 0; q < NT; ++q)
-      if (q < nt) {
-        mma_bf16(acc[q], a.x, b.x, a.y, b.y, w[q].x, w[q].y);
-        mma_bf16(acc[q], a.z, b.z, a.w, b.w, w[q].z, w[q].w);
-      }
-  }
   constexpr int RW = NT * 8;
+  constexpr int Q = NT < 8 ? NT : 8;  // eights of the rank at a time, for the registers
+#pragma unroll 1
+  for (int q0 = 0; q0 < NT; q0 += Q) {
+    float acc[Q][4];
 #pragma unroll
-  for (int q = 0; q < NT; ++q) {
-    float* at = red + (warp * kLoraSmallRows + g) * RW + q * 8 + 2 * t;
-    *reinterpret_cast<float2*>(at) = make_float2(acc[q][0], acc[q][1]);
-    *reinterpret_cast<float2*>(at + 8 * RW) = make_float2(acc[q][2], acc[q][3]);
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[q][i] = 0.0f;
+#pragma unroll(NT <= 2 ? 4 : 2)
+    for (int kb = warp; kb < (k1 - k0) >> 5; kb += kShrinkWarps) {
+      const uint4 a = on0 ? __ldg(x0 + kb * 4) : zero, b = on1 ? __ldg(x1 + kb * 4) : zero;
+      uint4 w[Q];
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+        if (q0 + q < nt) w[q] = ldg_nc_v4(ar + (int64_t)(q0 + q) * p.K + kb * 4);
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+        if (q0 + q < nt) {
+          mma_bf16(acc[q], a.x, b.x, a.y, b.y, w[q].x, w[q].y);
+          mma_bf16(acc[q], a.z, b.z, a.w, b.w, w[q].z, w[q].w);
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      float* at = red + (warp * kLoraSmallRows + g) * RW + (q0 + q) * 8 + 2 * t;
+      *reinterpret_cast<float2*>(at) = make_float2(acc[q][0], acc[q][1]);
+      *reinterpret_cast<float2*>(at + 8 * RW) = make_float2(acc[q][2], acc[q][3]);
+    }
   }
   __syncthreads();
   for (int i = tid; i < kLoraSmallRows * RW; i += kShrinkThreads) {
@@ -318,7 +322,7 @@ __device__ __forceinline__ void shrink_small(const LoraParams& p, const LoraPlan
 // A cluster walks over the tiles, its CTAs each over their range of K; the
 // joined sums are scaled and stored as bf16 terms, ready for the expand.
 template <int NT>
-__global__ void __launch_bounds__(kShrinkThreads, NT <= 8 ? 2 : 1) lora_shrink_tc_kernel(
+__global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_tc_kernel(
     LoraParams p, LoraPlan pl, int terms, uint32_t tmem_cols) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t done[kShrinkStages];
@@ -904,7 +908,7 @@ moe_status_t launch_shrink(const LoraParams& p, const LoraPlan& plan, int terms,
   }
   uint32_t tmem_cols = 32;
   while ((int)tmem_cols < RP) tmem_cols <<= 1;
-  const int per_sm = NT <= 8 ? 2 : 1;
+  constexpr int per_sm = 2;
   int64_t clusters = (int64_t)sm_count() * per_sm / plan.splits;
   if (clusters > plan.capacity) clusters = plan.capacity;
   return moe_host::launch_clusters(lora_shrink_tc_kernel<NT>, dim3((unsigned)(clusters * plan.splits)),
