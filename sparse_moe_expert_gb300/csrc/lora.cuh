@@ -90,7 +90,7 @@ __device__ __forceinline__ void cluster_barrier() {
 // (large, small, 0, 0).
 constexpr int kLoraTileRows = 128;
 constexpr int kLoraSmallRows = 16;
-constexpr int kLoraSmallMost = 48;  // a rest of at most this many rows takes small tiles
+constexpr int kLoraSmallMost = 32;  // a rest of at most this many rows takes small tiles
 constexpr int kLoraMaxSplit = 8;    // CTAs that share a tile's K in the grouped shrink
 struct LoraPlan {
   int2* rows;
