@@ -159,8 +159,9 @@ __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(LoraParams p, L
     if (c0 + u * 32 < c1) place(c0 + u * 32 + lane, kept[u]);
   for (int i0 = c0 + kPlanUnroll * 32; i0 < c1; i0 += 32)
     place(i0 + lane, i0 + lane < c1 ? bin_of(i0 + lane) : -1);
-  if (range != 0 || warp != 0) return;
-  // the tiles, one warp: their number first, then a scan over the adapters
+  if (range != 0 || warp != kPlanWarps - 1) return;
+  // the tiles, the last warp (the first to have no rows): their number first,
+  // then a scan over the adapters
   auto tiles_in = [&](int x) {
     if (x >= bins || (x == p.n_adapters && pl.skip_none)) return make_int2(0, 0);
     // rows without an adapter are copied, which large tiles do as well
