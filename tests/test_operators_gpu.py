@@ -830,6 +830,55 @@ def test_lora_deterministic_and_streams(cuda_lib):
     assert torch.equal(out, a)
 
 
+@pytest.mark.parametrize("T,NA", [(4200, 2100), (5000, 2048), (700, 60)])
+def test_lora_many_adapters(cuda_lib, T, NA):
+    """More adapters than the grouping counts (each row on its own), as many as
+    it counts, and a batch that meets most of its adapters a few times."""
+    o = make_lora(T, 64, 64, 8 if NA > 60 else 16, NA, NA)
+    out = cuda_lib.moe_lora_apply(*dense_args(o), base=o["base"])
+    assert rel(to_np(out), lora_ref(o)) <= LORA_TOL
+
+
+def test_lora_expert_rows_in_a_graph_and_on_two_streams(cuda_lib):
+    """The grouped form of expert rows replays, and calls on two streams at
+    once (each with its own workspace) give what they give alone."""
+    d = dev()
+    cases = []
+    for seed, T, E, n, K, N, R in ((1, 1200, 8, 3, 256, 256, 64), (2, 900, 6, 2, 512, 192, 128)):
+        o = make_lora(T, K, N, R, n, seed, E=E, k=2)
+        args = (o["x"], torch.tensor(o["ad"], device=d), o["a"], o["b"],
+                torch.tensor(o["sc"], device=d), o["base"])
+        kw = dict(topk_ids=torch.tensor(o["ids"], device=d),
+                  sorted_assign=torch.tensor(o["sorted"], device=d),
+                  expert_offsets=torch.tensor(o["off"], device=d),
+                  workspace=torch.empty(cuda_lib.moe_lora_workspace_size(T, 2, E, n, R),
+                                        dtype=torch.uint8, device=d))
+        ref = cuda_lib.moe_lora_apply(*args, **kw)
+        assert rel(to_np(ref), lora_ref(o)) <= LORA_TOL
+        cases.append((args, kw, ref))
+    args, kw, ref = cases[0]
+    out = torch.zeros_like(ref)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cuda_lib.moe_lora_apply(*args, out=out, **kw)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, ref)
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [[torch.empty_like(c[2]) for _ in range(20)] for c in cases]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for (args, kw, _), s, o in zip(cases, streams, outs):
+            with torch.cuda.stream(s):
+                cuda_lib.moe_lora_apply(*args, out=o[i], **kw)
+    torch.cuda.synchronize()
+    for (_, _, ref), o in zip(cases, outs):
+        assert all(torch.equal(x, ref) for x in o)
+    assert cuda_lib.moe_get_device_error(clear=True) == 0
+
+
 def test_lora_refusals(cuda_lib):
     d = dev()
     o = make_lora(4, 128, 128, 16, 3, 8)
