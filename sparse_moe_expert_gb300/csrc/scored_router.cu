@@ -332,14 +332,17 @@ __device__ __forceinline__ void lane_top2(const float (&c)[V], float& a1, float&
 //
 // Bound by the issue rate: some 550 instructions per token of 256 experts
 // (issue slots 69 % used, ALU 58 %).  Measured, k 8 of 256 bf16 experts in 8
-// groups, 65536 tokens: 46 us (37.7 MB: 6 us at the copy rate); with exact
-// scores for every expert and k rounds of argmax 93 us; 64 experts 23 us.  A
+// groups, 65536 tokens: 44 us (37.7 MB: 6 us at the copy rate); with exact
+// scores for every expert and k rounds of argmax 93 us; 64 experts 21 us.  A
 // lane per token (rows in shared memory) was no faster: 47 us, 83 us for fp32
 // rows, whose 32 rows per warp leave few warps.
 //
 // Two tokens share the last part of the work: the candidates of one on lanes
 // 0-15, those of the other on lanes 16-31.
-template <int V, bool BF16, bool SIGMOID>
+// LANES: groups, if any, are whole aligned runs of lanes (a power of two of
+// them), so that their values are joined by shuffles alone; 3 us of 46 as a
+// constant.
+template <int V, bool BF16, bool SIGMOID, bool LANES>
 __global__ void __launch_bounds__(kScoredThreads, V <= 8 ? 4 : 2)
     route_scored_kernel(ScoredParams p, int vec, int per) {
   constexpr int C = 16;  // candidates of a token
@@ -363,14 +366,13 @@ __global__ void __launch_bounds__(kScoredThreads, V <= 8 ? 4 : 2)
   }
   constexpr float eps = 1e-6f;
   const int G = p.n_groups, gsz = p.E / G, span = gsz / V;  // span: lanes of a group
-  const bool lane_groups = gsz % V == 0 && (span & (span - 1)) == 0 && span <= 32;
   // lanes that work on a group: its own when groups are whole aligned runs of
   // lanes, else as many as fit (a power of two), over shared memory
   int width = 1;
-  if (lane_groups) width = span;
+  if (LANES) width = span;
   else
     while (2 * width * G <= 32) width *= 2;
-  const int my_group = lane_groups ? e0 / gsz : lane / width;  // >= G: none
+  const int my_group = LANES ? e0 / gsz : lane / width;  // >= G: none
 
   // The candidates of the token whose logits lie at `row` into ids[]; their
   // number, or -1 when they are not certain or too many.  m, den: the
@@ -406,7 +408,7 @@ __global__ void __launch_bounds__(kScoredThreads, V <= 8 ? 4 : 2)
       float* xs = group_x[warp];
       const int from = my_group * gsz + (lane & (width - 1));
       const int to = my_group < G ? (my_group + 1) * gsz : 0;
-      if (!lane_groups) {
+      if constexpr (!LANES) {
         __syncwarp();
 #pragma unroll
         for (int v = 0; v < V; ++v) xs[e0 + v] = c[v];
@@ -446,7 +448,7 @@ __global__ void __launch_bounds__(kScoredThreads, V <= 8 ? 4 : 2)
                                           : groups == p.topk_groups &&
                                                 cut - next > 4.0f * eps + fabsf(next) * 0x1p-20f;
       if (!sure) return -1;
-      if (!lane_groups) {  // strike the other groups' choices
+      if constexpr (!LANES) {  // strike the other groups' choices
         if (!live)
           for (int e = from; e < to; e += width) xs[e] = -INFINITY;
         __syncwarp();
@@ -458,7 +460,7 @@ __global__ void __launch_bounds__(kScoredThreads, V <= 8 ? 4 : 2)
     }
     float bound = -INFINITY;
     float rest = live ? best : -INFINITY, after = live ? second : -INFINITY;
-#pragma unroll 4
+#pragma unroll 8
     for (int r = 0; r < p.k; ++r) {
       bound = redux_max(rest);
       if (rest == bound) {
@@ -830,8 +832,11 @@ struct ForwardLaunch {
     // two tokens per warp once every SM has some warps (measured: 64 tokens
     // 2.7 us with one, 3.3 with two; 4096 tokens 5.4 and 4.7)
     const int per = p.T > moe_host::sm_count() * kScoredWarps ? 2 : 1;
-    return moe_host::launch(route_scored_kernel<V, BF16, SIG>, scored_grid((p.T + per - 1) / per),
-                            kScoredThreads, 0, st, p, vec, per);
+    const int span = p.E / p.n_groups / V;
+    const bool lanes = p.n_groups == 1 || (p.E / p.n_groups % V == 0 && (span & (span - 1)) == 0);
+    return moe_host::launch(lanes ? route_scored_kernel<V, BF16, SIG, true>
+                                  : route_scored_kernel<V, BF16, SIG, false>,
+                            scored_grid((p.T + per - 1) / per), kScoredThreads, 0, st, p, vec, per);
   }
 };
 template <int V, bool BF16, bool SIG>
