@@ -340,8 +340,8 @@ __device__ __forceinline__ void lane_top2(const float (&c)[V], float& a1, float&
 // Two tokens share the last part of the work: the candidates of one on lanes
 // 0-15, those of the other on lanes 16-31.
 // LANES: groups, if any, are whole aligned runs of lanes (a power of two of
-// them), so that their values are joined by shuffles alone; 3 us of 46 as a
-// constant.
+// them), so that their values are joined by shuffles alone; decided at run
+// time the size above takes 46 us.
 template <int V, bool BF16, bool SIGMOID, bool LANES>
 __global__ void __launch_bounds__(kScoredThreads, V <= 8 ? 4 : 2)
     route_scored_kernel(ScoredParams p, int vec, int per) {
