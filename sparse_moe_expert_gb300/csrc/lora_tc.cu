@@ -335,7 +335,7 @@ template <int NT>
 __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_tc_kernel(
     LoraParams p, LoraPlan pl, int terms, uint32_t tmem_cols) {
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t done[kShrinkStages];
+  __shared__ __align__(8) uint64_t done;
   __shared__ uint32_t tmem_sh;
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_tc_kernel(
   const int pitch = RP + 4;
   float* red = part + kLoraSmallRows * pitch;
   if (tid == 0) {
-    for (int s = 0; s < kShrinkStages; ++s) mbar_init(&done[s], 1);
+    mbar_init(&done, 1);
     fence_barrier_init();
   }
   pdl_wait();
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_tc_kernel(
   const int splits = pl.splits, rank = blockIdx.x % splits;
   const int nkb = p.K / 64;
   const int kb0 = rank * nkb / splits, nb = (rank + 1) * nkb / splits - kb0;
-  uint32_t phases = 0;  // bit s: parity of stage s's next completion
+  uint32_t parity = 0;  // of the next completion (warp 0)
   const int c = tid & 7, r0 = tid >> 3;  // this thread's 16-byte column and first row
   for (int ti = blockIdx.x / splits; ti < ntiles.x + ntiles.y; ti += gridDim.x / splits) {
     const bool is_small = ti >= ntiles.x;
@@ -383,53 +383,58 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_tc_kernel(
         xr[i] = r < tile.z ? p.x + (int64_t)pl.rows[tile.y + r].y * p.K + kb0 * 64 + c * 8 : nullptr;
       }
       const uint16_t* ar = p.a + ((int64_t)tile.x * p.R + r0) * p.K + kb0 * 64 + c * 8;
-      auto load = [&](int kb) {
-        unsigned char* xs = smem + (kb % kShrinkStages) * stage_bytes;
-        unsigned char* as = xs + kBlockBytes;
+      const int a_step = 32 * p.K;
+      // the next k-block -> stage s
+      auto load = [&](int s) {
+        unsigned char* at = smem + s * stage_bytes + sw128_offset(r0, c);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (xr[i]) cp_async16(xs + sw128_offset(r0 + 32 * i, c), xr[i] + kb * 64, true);
+          if (xr[i]) {
+            cp_async16(at + i * 4096, xr[i], true);
+            xr[i] += 64;
+          }
 #pragma unroll
         for (int i = 0; i < (NT * 8 + 31) / 32; ++i) {
           const int r = r0 + 32 * i;
           if (r < RP)
-            cp_async16(as + sw128_offset(r, c),
-                       r < p.R ? ar + (int64_t)32 * i * p.K + kb * 64 : p.a, r < p.R);
+            cp_async16(at + kBlockBytes + i * 4096, r < p.R ? ar + (int64_t)i * a_step : p.a, r < p.R);
         }
+        ar += 64;
       };
       for (int kb = 0; kb < kShrinkStages - 1; ++kb) {
         if (kb < nb) load(kb);
         cp_async_commit();
       }
+      int s = 0, before = kShrinkStages - 1;  // stages of this k-block and of the one before
       for (int kb = 0; kb < nb; ++kb) {
         cp_async_wait<kShrinkStages - 2>();
         fence_proxy_async_smem();
+        // the products of the k-block before have had this one's wait to end
+        if (warp == 0 && kb > 0) {
+          wait_or_flag(&done, parity, bad, p.err);
+          parity ^= 1u;
+        }
         if (__syncthreads_or(bad)) {
           bad = 1;
           break;
         }
-        const int s = kb % kShrinkStages;
         if (warp == 0) {
           const uint64_t xd = smem_desc_sw128(smem + s * stage_bytes);
           const uint64_t ad = smem_desc_sw128(smem + s * stage_bytes + kBlockBytes);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             umma_bf16(tmem, xd + 2 * k, ad + 2 * k, idesc, kb > 0 || k > 0);
-          umma_commit(&done[s]);
+          umma_commit(&done);
         }
-        // the stage that k-block kb + 2 takes was read by the MMAs of kb - 1
-        const int nx = kb + kShrinkStages - 1;
-        if (kb > 0) {
-          const int sp = (kb - 1) % kShrinkStages;
-          wait_or_flag(&done[sp], (phases >> sp) & 1u, bad, p.err);
-          phases ^= 1u << sp;
-        }
-        if (nx < nb) load(nx);
+        if (kb + kShrinkStages - 1 < nb) load(before);
         cp_async_commit();
+        before = s;
+        s = s == kShrinkStages - 1 ? 0 : s + 1;
       }
-      const int sp = (nb - 1) % kShrinkStages;
-      wait_or_flag(&done[sp], (phases >> sp) & 1u, bad, p.err);
-      phases ^= 1u << sp;
+      if (warp == 0) {
+        wait_or_flag(&done, parity, bad, p.err);
+        parity ^= 1u;
+      }
       cp_async_wait<0>();
       __syncthreads();
       tc_fence_after();
