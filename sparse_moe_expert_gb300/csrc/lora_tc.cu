@@ -507,17 +507,29 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_tc_kernel(
 
 // ---- expand ----------------------------------------------------------------
 
+// 16 bytes of a row of base.  A unit reads 128 (bf16) or 256 bytes of each of
+// its rows; asking L2 for 256 at a time makes DRAM's pieces longer: 8192 x 11008
+// bf16 over both directions 114.7 us for the call, 118.5 without.
+__device__ __forceinline__ uint4 load_ahead(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
 // Eight consecutive values of base held as loaded (16 bytes bf16, 32 fp32).
 template <bool BF16>
 struct Base8 {
   uint4 q[BF16 ? 1 : 2];
   __device__ __forceinline__ void load(const void* base, int64_t at) {
     if constexpr (BF16) {
-      q[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
+      q[0] = load_ahead(static_cast<const uint16_t*>(base) + at);
     } else {
-      const uint4* b = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + at);
-      q[0] = b[0];
-      q[1] = b[1];
+      const float* b = static_cast<const float*>(base) + at;
+      q[0] = load_ahead(b);
+      q[1] = load_ahead(b + 4);
     }
   }
   __device__ __forceinline__ void zero() {
