@@ -571,17 +571,16 @@ __device__ __forceinline__ void put8(void* out, int64_t at, const float (&f)[8])
   }
 }
 
-constexpr int kExpandThreads = 128;
-constexpr int kExpandCols = 64;        // accumulator columns of a large unit
-constexpr int kExpandSmallCols = 128;  // output columns of a small unit, 32 per warp
+constexpr int kExpandThreads = 128;  // of a group of warps
+constexpr int kExpandCols = 64;      // accumulator columns of a group in a large unit
 
 // v's terms of the `n` rows from position `first` -> shared memory, 128-byte
 // swizzled; rows n .. up to `fill` become zeros.  Asynchronous copies.
-template <int TERMS>
+template <int TERMS, int THREADS>
 __device__ __forceinline__ void stage_v(const LoraPlan& pl, int RP, int first, int n, int fill,
                                         unsigned char* vs) {
   const int pieces = TERMS * RP / 8, c0 = threadIdx.x & 3;
-  for (int r = threadIdx.x >> 2; r < fill; r += kExpandThreads / 4) {
+  for (int r = threadIdx.x >> 2; r < fill; r += THREADS / 4) {
     const uint16_t* src = pl.terms + (int64_t)(first + (r < n ? r : 0)) * (TERMS * RP);
     for (int c = c0; c < pieces; c += 4)
       cp_async16(vs + (c >> 3) * kBlockBytes + sw128_offset(r, c & 7), src + c * 8, r < n);
@@ -643,9 +642,10 @@ __device__ __forceinline__ void small_block(float (&acc)[4][4], const SmallB& b,
 // column 8 q + 2 t + i of a block is its column 8 t + 2 q + i.  A lane's
 // pieces of base are requested one unit ahead, as soon as the registers of
 // the unit before are consumed, so loads are in flight through the waits.
-template <int TERMS, bool BASE_BF16, bool OUT_BF16, bool SWIGLU>
-__global__ void __launch_bounds__(kExpandThreads, BASE_BF16 ? 4 : 3) lora_expand_tc_kernel(
-    LoraParams p, LoraPlan pl) {
+// GROUPS of four warps have columns of their own and share v.
+template <int TERMS, bool BASE_BF16, bool OUT_BF16, bool SWIGLU, int GROUPS>
+__global__ void __launch_bounds__(kExpandThreads* GROUPS, GROUPS > 1 ? 1 : BASE_BF16 ? 4 : 3)
+    lora_expand_tc_kernel(LoraParams p, LoraPlan pl) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t done;
   __shared__ uint32_t tmem_sh;
@@ -654,25 +654,29 @@ __global__ void __launch_bounds__(kExpandThreads, BASE_BF16 ? 4 : 3) lora_expand
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int RP = rank_pad(p.R);
   const int vblocks = (TERMS * RP + 63) / 64, bblocks = (RP + 63) / 64;
-  constexpr int kBBytes = kExpandCols * 128;  // 64 rows x 128 bytes
+  constexpr int kThreads = kExpandThreads * GROUPS;
+  constexpr int kBBytes = GROUPS * kExpandCols * 128;  // the unit's rows of B x 128 bytes
   unsigned char* vs = smem;
   unsigned char* bs = smem + vblocks * kBlockBytes;  // two slots of bblocks
   if (tid == 0) {
     mbar_init(&done, 1);
     fence_barrier_init();
   }
-  const uint32_t idesc = idesc_bf16(128, kExpandCols);
+  const uint32_t idesc = idesc_bf16(128, GROUPS * kExpandCols);
   const int cols = SWIGLU ? p.N / 2 : p.N;                       // output columns
-  constexpr int span = SWIGLU ? kExpandCols / 2 : kExpandCols;   // of them in a large unit
-  constexpr int sspan = kExpandSmallCols;
-  const int chunks = cols / span, schunks = (cols + sspan - 1) / sspan;
+  constexpr int gspan = SWIGLU ? kExpandCols / 2 : kExpandCols;  // of them a group's in a large unit
+  constexpr int span = GROUPS * gspan;                           // and the unit's
+  constexpr int sspan = kThreads;                                // a small unit's, 32 per warp
+  const int group = warp / 4;
+  const int chunks = (cols + span - 1) / span, schunks = (cols + sspan - 1) / sspan;
 
   // B rows of the unit at (tile slot, col0) -> slot `s` of shared memory: a
   // thread takes every second 16-byte piece of one row
-  const int brow = tid >> 1, bh = brow >> 5, bw = brow & 31;
-  const int bdst = bh * 32 + 8 * ((bw & 7) >> 1) + 2 * (bw >> 3) + (bw & 1);
+  const int brow = (tid >> 1) & 63, bh = brow >> 5, bw = brow & 31;
+  const int bdst = group * 64 + bh * 32 + 8 * ((bw & 7) >> 1) + 2 * (bw >> 3) + (bw & 1);
   auto load_b = [&](int slot_id, int col0, int s) {
-    if (slot_id < 0) return;
+    col0 += group * gspan;
+    if (slot_id < 0 || (GROUPS > 1 && col0 >= cols)) return;
     const int n = SWIGLU ? bh * cols + col0 + bw : col0 + brow;
     unsigned char* dst = bs + s * bblocks * kBBytes;
     const uint16_t* src = p.b + ((int64_t)slot_id * p.N + n) * p.R;
@@ -698,7 +702,7 @@ __global__ void __launch_bounds__(kExpandThreads, BASE_BF16 ? 4 : 3) lora_expand
   cp_async_commit();
   pdl_wait();
   if (warp == 0) {
-    tmem_alloc(&tmem_sh, kExpandCols);
+    tmem_alloc(&tmem_sh, GROUPS * kExpandCols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -713,23 +717,26 @@ __global__ void __launch_bounds__(kExpandThreads, BASE_BF16 ? 4 : 3) lora_expand
   Base8<BASE_BF16> bq[2][4];
   uint32_t parity = 0;
   auto load_base = [&](int i, int col0) {
+    col0 += group * gspan;
+    const bool on = p.base && row_at[i] >= 0 && (GROUPS == 1 || col0 < cols);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int col = (SWIGLU ? h * cols + col0 : col0 + h * 32) + 8 * t;
-      if (p.base && row_at[i] >= 0) bq[h][i].load(p.base, row_at[i] * p.N + col);
+      if (on) bq[h][i].load(p.base, row_at[i] * p.N + col);
       else bq[h][i].zero();
     }
   };
   for (int64_t u = u0; u < lend; ++u) {
+    const int gcol = col0 + group * gspan;
     if (fresh) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int r = warp * 32 + g + 8 * i;
+        const int r = (warp & 3) * 32 + g + 8 * i;
         row_at[i] = r < tile.z ? (int64_t)pl.rows[tile.y + r].x : -1;
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) load_base(i, col0);
-      if (tile.x >= 0) stage_v<TERMS>(pl, RP, tile.y, tile.z, tile.z, vs);
+      if (tile.x >= 0) stage_v<TERMS, kThreads>(pl, RP, tile.y, tile.z, tile.z, vs);
       cp_async_commit();
     }
     const bool last = u + 1 >= lend, more = !last && col0 + span < cols;  // more: of this tile
@@ -759,13 +766,14 @@ __global__ void __launch_bounds__(kExpandThreads, BASE_BF16 ? 4 : 3) lora_expand
       tc_fence_after();
     }
 #pragma unroll
-    for (int hr = 0; hr < 2; ++hr) {  // accumulator rows 32 warp + 16 hr ..
+    for (int hr = 0; hr < 2; ++hr) {  // accumulator rows 32 (warp % 4) + 16 hr ..
       float z[2][2][8];               // [block][row g, g + 8]
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t r[16];
         if (tile.x >= 0) {
-          tmem_ld_16x256b_x4(tmem + ((uint32_t)(warp * 32 + 16 * hr) << 16) + h * 32, r);
+          tmem_ld_16x256b_x4(
+              tmem + ((uint32_t)((warp & 3) * 32 + 16 * hr) << 16) + group * kExpandCols + h * 32, r);
           tmem_ld_wait();
         }
 #pragma unroll
@@ -787,15 +795,15 @@ __global__ void __launch_bounds__(kExpandThreads, BASE_BF16 ? 4 : 3) lora_expand
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int64_t row = row_at[2 * hr + i];
-        if (row < 0) continue;
+        if (row < 0 || (GROUPS > 1 && gcol >= cols)) continue;
         if constexpr (SWIGLU) {
 #pragma unroll
           for (int x = 0; x < 8; ++x) z[0][i][x] = swiglu_f32(z[0][i][x], z[1][i][x]);
-          put8<OUT_BF16>(p.out, row * cols + col0 + 8 * t, z[0][i]);
+          put8<OUT_BF16>(p.out, row * cols + gcol + 8 * t, z[0][i]);
         } else {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            put8<OUT_BF16>(p.out, row * cols + col0 + h * 32 + 8 * t, z[h][i]);
+            put8<OUT_BF16>(p.out, row * cols + gcol + h * 32 + 8 * t, z[h][i]);
         }
       }
     }
@@ -828,7 +836,7 @@ __global__ void __launch_bounds__(kExpandThreads, BASE_BF16 ? 4 : 3) lora_expand
     if (stage) {
       tile = pl.tiles[pl.capacity - 1 - ti];
       __syncthreads();  // no warp still reads the tile before
-      stage_v<TERMS>(pl, RP, tile.y, tile.z, kLoraSmallRows, vs);
+      stage_v<TERMS, kThreads>(pl, RP, tile.y, tile.z, kLoraSmallRows, vs);
       cp_async_commit();
       row_at[0] = g < tile.z ? (int64_t)pl.rows[tile.y + g].x : -1;
       row_at[1] = g + 8 < tile.z ? (int64_t)pl.rows[tile.y + g + 8].x : -1;
@@ -886,16 +894,24 @@ __global__ void __launch_bounds__(kExpandThreads, BASE_BF16 ? 4 : 3) lora_expand
     }
   }
   __syncthreads();
-  if (warp == 0) tmem_dealloc(tmem, kExpandCols);
+  if (warp == 0) tmem_dealloc(tmem, GROUPS * kExpandCols);
 }
 
-template <int TERMS, bool BASE_BF16, bool OUT_BF16, bool SWIGLU>
-moe_status_t launch_expand(const LoraParams& p, const LoraPlan& plan, cudaStream_t st) {
+// Shared memory of a CTA, and how many of them an SM holds.
+size_t expand_smem(int terms, int RP, int groups) {
+  return ((terms * RP + 63) / 64) * (size_t)kBlockBytes +
+         2 * ((RP + 63) / 64) * (size_t)(groups * kExpandCols * 128) + 1024;
+}
+int expand_per_sm(size_t smem, int most) {
+  const int n = (int)(224 * 1024 / (smem + 1024));
+  return n < 1 ? 1 : n > most ? most : n;
+}
+
+template <int TERMS, bool BASE_BF16, bool OUT_BF16, bool SWIGLU, int GROUPS>
+moe_status_t launch_expand_groups(const LoraParams& p, const LoraPlan& plan, cudaStream_t st) {
   using namespace moe_host;
-  const int RP = rank_pad(p.R);
-  const size_t smem = ((TERMS * RP + 63) / 64) * (size_t)kBlockBytes +
-                      2 * ((RP + 63) / 64) * (size_t)(kExpandCols * 128) + 1024;
-  auto kern = lora_expand_tc_kernel<TERMS, BASE_BF16, OUT_BF16, SWIGLU>;
+  const size_t smem = expand_smem(TERMS, rank_pad(p.R), GROUPS);
+  auto kern = lora_expand_tc_kernel<TERMS, BASE_BF16, OUT_BF16, SWIGLU, GROUPS>;
   static size_t set_max[kMaxCachedDevices] = {};
   const int dev = device_index();
   if (smem > set_max[dev]) {
@@ -904,14 +920,23 @@ moe_status_t launch_expand(const LoraParams& p, const LoraPlan& plan, cudaStream
       return MOE_ERR_CUDA;
     set_max[dev] = smem;
   }
-  int per_sm = (int)(224 * 1024 / (smem + 1024));
-  if (per_sm > (BASE_BF16 ? 4 : 3)) per_sm = BASE_BF16 ? 4 : 3;
-  if (per_sm < 1) per_sm = 1;
+  const int per_sm = expand_per_sm(smem, GROUPS > 1 ? 1 : BASE_BF16 ? 4 : 3);
   const int cols = SWIGLU ? p.N / 2 : p.N;
-  const int span = SWIGLU ? kExpandCols / 2 : kExpandCols;
-  int64_t grid = plan.capacity * (cols / span);
+  const int span = GROUPS * (SWIGLU ? kExpandCols / 2 : kExpandCols);
+  int64_t grid = plan.capacity * ((cols + span - 1) / span);
   if (grid > (int64_t)sm_count() * per_sm) grid = (int64_t)sm_count() * per_sm;
-  return launch(kern, (int)grid, kExpandThreads, smem, st, p, plan);
+  return launch(kern, (int)grid, kExpandThreads * GROUPS, smem, st, p, plan);
+}
+
+// v of a wide rank leaves room for one CTA per SM; two groups of warps then
+// share it.  4096 rows, rank 128, 4096 -> 4096, fp32: 78 us for the call, 86
+// with one group.
+template <int TERMS, bool BASE_BF16, bool OUT_BF16, bool SWIGLU>
+moe_status_t launch_expand(const LoraParams& p, const LoraPlan& plan, cudaStream_t st) {
+  if constexpr (TERMS > 2)
+    if (expand_per_sm(expand_smem(TERMS, rank_pad(p.R), 1), 2) == 1)
+      return launch_expand_groups<TERMS, BASE_BF16, OUT_BF16, SWIGLU, 2>(p, plan, st);
+  return launch_expand_groups<TERMS, BASE_BF16, OUT_BF16, SWIGLU, 1>(p, plan, st);
 }
 
 template <int NT>

@@ -929,3 +929,18 @@ def test_router_logits_match_the_fixed_order(cuda_lib, T, H, E):
                                      torch.tensor(bias, device=dev()), 0.75)
     ref = oracle.router_logits(bits, w, bias, 0.75)
     assert np.array_equal(to_np(got), ref)
+
+
+# Ranks of 96 and more, whose CTAs take 128 columns at a time (64 with SwiGLU):
+# column counts that are whole, and that leave half of the last unit.
+@pytest.mark.parametrize("T,K,N,R,NA", [(700, 320, 192, 128, 2), (400, 128, 576, 96, 3),
+                                        (1300, 64, 256, 120, 5), (350, 64, 64, 104, 1)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_lora_wide_rank(cuda_lib, T, K, N, R, NA, dtype):
+    test_lora_one_projection(cuda_lib, T, K, N, R, NA, dtype)
+
+
+@pytest.mark.parametrize("T,k,E,NA,K,N,R", [(600, 2, 3, 2, 128, 192, 128), (500, 1, 2, 1, 64, 256, 96)])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_lora_wide_rank_expert_rows(cuda_lib, T, k, E, NA, K, N, R, swiglu):
+    test_lora_expert_rows(cuda_lib, T, k, E, NA, K, N, R, swiglu)
