@@ -39,6 +39,7 @@ namespace {
 constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanUnroll = 4;
+constexpr int kPlanRanges = 8;  // CTAs that share an expert's rows, at most
 
 // Tiles of an adapter's n rows.
 __device__ __forceinline__ int2 tiles_of(int n) {
@@ -48,11 +49,12 @@ __device__ __forceinline__ int2 tiles_of(int n) {
                    small ? (rest + kLoraSmallRows - 1) / kLoraSmallRows : 0);
 }
 
-__device__ __forceinline__ int warp_scan_incl(int v) {
+template <typename T>
+__device__ __forceinline__ T warp_scan_incl(T v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    const T y = __shfl_up_sync(0xFFFFFFFFu, v, o);
     if (lane >= o) v += y;
   }
   return v;
@@ -67,13 +69,16 @@ __device__ __forceinline__ int warp_scan_incl(int v) {
 // the experts' tiles is left open.
 __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(LoraParams p, LoraPlan pl) {
   extern __shared__ int plan_s[];
+  __shared__ unsigned tile_total;  // as first_tile
+  __shared__ int2 tile_base;       // the expert's first tiles in the list
   pdl_wait();
   pdl_trigger();
   const int bins = p.n_adapters + 1;
   int* own = plan_s;                 // this CTA's counts
   int* cnt = own + bins;             // the expert's
   int* start = cnt + bins;           // first position of each adapter
-  int* cursor = start + bins;        // [warp][bins]: counts, then next positions
+  unsigned* first_tile = reinterpret_cast<unsigned*>(start + bins);  // and tile: large, small
+  int* cursor = start + 2 * bins;    // [warp][bins]: counts, then next positions
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int e = blockIdx.x, rows = lora_rows(p);
   const int ranges = gridDim.y, range = blockIdx.y;  // the cluster's size, the rank in it
@@ -120,30 +125,63 @@ __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(LoraParams p, L
   if (ranges > 1) {
     cluster_barrier();
     for (int x = tid; x < bins; x += kPlanThreads) {
+      int v[kPlanRanges];
+#pragma unroll
+      for (int r = 0; r < kPlanRanges; ++r)
+        if (r < ranges)
+          asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v[r]) : "r"(cluster_addr(own + x, r)));
       int total = 0, before = 0;
-      for (int r = 0; r < ranges; ++r) {
-        int v;
-        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(own + x, r)));
-        total += v;
-        if (r < range) before += v;
-      }
+#pragma unroll
+      for (int r = 0; r < kPlanRanges; ++r)
+        if (r < ranges) {
+          total += v[r];
+          if (r < range) before += v[r];
+        }
       cnt[x] = total;
       for (int w = 0; w < kPlanWarps; ++w) cursor[w * bins + x] += before;
     }
     __syncthreads();
-    cluster_barrier();  // nobody's counts are needed any more
+    cluster_arrive();  // the other CTAs' counts have been read
   }
+  // rows without an adapter are copied, which large tiles do as well
+  auto tiles_in = [&](int x) {
+    if (x >= bins || (x == p.n_adapters && pl.skip_none)) return make_int2(0, 0);
+    if (x == p.n_adapters) return make_int2((cnt[x] + kLoraTileRows - 1) / kLoraTileRows, 0);
+    return tiles_of(cnt[x]);
+  };
+  // large tiles above, small ones (two per adapter at most) below
+  constexpr int kSmallBits = 13;
+  constexpr unsigned kSmallMask = (1u << kSmallBits) - 1;
+  static_assert(kLoraSmallMost / kLoraSmallRows * kLoraPlanAdapters <= kSmallMask, "small tiles fit");
   if (warp == 0) {
     int carry = 0;
+    unsigned tcarry = 0;
     for (int x0 = 0; x0 < bins; x0 += 32) {
       const int x = x0 + lane;
       const int v = x < bins ? cnt[x] : 0;
+      const int2 k = tiles_in(x);
+      const unsigned kk = ((unsigned)k.x << kSmallBits) + k.y;
       const int incl = warp_scan_incl(v);
-      if (x < bins) start[x] = carry + incl - v;
+      const unsigned tincl = warp_scan_incl(kk);
+      if (x < bins) {
+        start[x] = carry + incl - v;
+        first_tile[x] = tcarry + tincl - kk;
+      }
       carry += __shfl_sync(0xFFFFFFFFu, incl, 31);
+      tcarry += __shfl_sync(0xFFFFFFFFu, tincl, 31);
     }
+    if (lane == 0) tile_total = tcarry;
   }
   __syncthreads();
+  if (range == 0 && tid == kPlanThreads - 1) {
+    const int large = tile_total >> kSmallBits, small = tile_total & kSmallMask;
+    if (p.E == 1) {
+      *pl.counts = make_int4(large, small, 0, 0);
+      tile_base = make_int2(0, 0);
+    } else {
+      tile_base = make_int2(atomicAdd(&pl.counts->x, large), atomicAdd(&pl.counts->y, small));
+    }
+  }
   auto place = [&](int i, int b) {  // the warp together
     const unsigned same = __match_any_sync(0xFFFFFFFFu, b);
     const int before = __popc(same & lanemask_lt());
@@ -159,54 +197,27 @@ __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(LoraParams p, L
     if (c0 + u * 32 < c1) place(c0 + u * 32 + lane, kept[u]);
   for (int i0 = c0 + kPlanUnroll * 32; i0 < c1; i0 += 32)
     place(i0 + lane, i0 + lane < c1 ? bin_of(i0 + lane) : -1);
-  if (range != 0 || warp != kPlanWarps - 1) return;
-  // the tiles, the last warp (the first to have no rows): their number first,
-  // then a scan over the adapters
-  auto tiles_in = [&](int x) {
-    if (x >= bins || (x == p.n_adapters && pl.skip_none)) return make_int2(0, 0);
-    // rows without an adapter are copied, which large tiles do as well
-    if (x == p.n_adapters) return make_int2((cnt[x] + kLoraTileRows - 1) / kLoraTileRows, 0);
-    return tiles_of(cnt[x]);
-  };
-  int2 total = make_int2(0, 0), base = make_int2(0, 0);
-  for (int x0 = 0; x0 < bins; x0 += 32) {
-    const int2 k = tiles_in(x0 + lane);
-    total.x += __reduce_add_sync(0xFFFFFFFFu, k.x);
-    total.y += __reduce_add_sync(0xFFFFFFFFu, k.y);
-  }
-  if (lane == 0) {
-    if (p.E == 1) {
-      *pl.counts = make_int4(total.x, total.y, 0, 0);
-    } else {
-      base.x = atomicAdd(&pl.counts->x, total.x);
-      base.y = atomicAdd(&pl.counts->y, total.y);
-    }
-  }
-  base.x = __shfl_sync(0xFFFFFFFFu, base.x, 0);
-  base.y = __shfl_sync(0xFFFFFFFFu, base.y, 0);
+  if (ranges > 1) cluster_wait();
+  if (range != 0) return;
+  __syncthreads();
+  // the tiles, eight threads per adapter
   auto put = [&](int64_t at, int slot, int first, int num) {
     if (at >= 0 && at < pl.capacity)  // always, when the offsets are a prefix sum
       pl.tiles[at] = make_int4(slot, first, num, 0);
     else
       raise_device_error(p.err, MOE_DEVERR_BAD_INDEX);
   };
-  for (int x0 = 0; x0 < bins; x0 += 32) {
-    const int x = x0 + lane;
+  const int2 base = tile_base;
+  for (int x = tid >> 3; x < bins; x += kPlanThreads / 8) {
     const int2 k = tiles_in(x);
-    const int ix = warp_scan_incl(k.x), iy = warp_scan_incl(k.y);
-    if (x < bins) {
-      const int slot = x < p.n_adapters ? x * p.E + e : -1;
-      const int first = lo + start[x], v = cnt[x];
-      for (int j = 0; j < k.x; ++j)
-        put((int64_t)base.x + ix - k.x + j, slot, first + j * kLoraTileRows,
-            min(kLoraTileRows, v - j * kLoraTileRows));
-      const int done = k.x * kLoraTileRows;
-      for (int j = 0; j < k.y; ++j)
-        put(pl.capacity - 1 - ((int64_t)base.y + iy - k.y + j), slot,
-            first + done + j * kLoraSmallRows, min(kLoraSmallRows, v - done - j * kLoraSmallRows));
-    }
-    base.x += __shfl_sync(0xFFFFFFFFu, ix, 31);
-    base.y += __shfl_sync(0xFFFFFFFFu, iy, 31);
+    const int64_t x0 = (int64_t)base.x + (first_tile[x] >> kSmallBits);
+    const int64_t y0 = pl.capacity - 1 - ((int64_t)base.y + (first_tile[x] & kSmallMask));
+    const int slot = x < p.n_adapters ? x * p.E + e : -1;
+    const int first = lo + start[x], v = cnt[x], done = k.x * kLoraTileRows;
+    for (int j = tid & 7; j < k.x; j += 8)
+      put(x0 + j, slot, first + j * kLoraTileRows, min(kLoraTileRows, v - j * kLoraTileRows));
+    for (int j = tid & 7; j < k.y; j += 8)
+      put(y0 - j, slot, first + done + j * kLoraSmallRows, min(kLoraSmallRows, v - done - j * kLoraSmallRows));
   }
 }
 
@@ -975,14 +986,14 @@ moe_status_t lora_grouped(const LoraParams& p, const LoraPlan& plan, int64_t row
   // with several experts their CTAs add to the counts
   if (p.E > 1 && cudaMemsetAsync(plan.counts, 0, sizeof(int4), st) != cudaSuccess)
     return MOE_ERR_CUDA;
-  const size_t plan_smem = (size_t)(3 + kPlanWarps) * (p.n_adapters + 1) * sizeof(int);
+  const size_t plan_smem = (size_t)(4 + kPlanWarps) * (p.n_adapters + 1) * sizeof(int);
   if (plan_smem > 48 * 1024 &&
       cudaFuncSetAttribute(lora_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)plan_smem) != cudaSuccess)
     return MOE_ERR_CUDA;
   // CTAs per expert: one per 1024 of the rows that an expert has on average
   int ranges = 1;
-  while (ranges < 8 && (int64_t)ranges * 1024 * p.E < rows) ranges *= 2;
+  while (ranges < kPlanRanges && (int64_t)ranges * 1024 * p.E < rows) ranges *= 2;
   moe_status_t s = moe_host::launch_clusters(lora_plan_kernel, dim3(p.E, ranges), kPlanThreads, plan_smem,
                                    dim3(1, ranges), st, p, plan);
   if (s != MOE_OK) return s;
