@@ -264,13 +264,26 @@ bool lora_groups(int64_t rows, int E, int n_adapters, int R) {
          ((cost >= 6144 && rows >= 4 * (int64_t)n_adapters * E) || cost >= 32768);
 }
 
-// CTAs per tile in the grouped shrink: as many as two per SM hold, with the
-// tiles that full ones and one rest per adapter make, and at least four
-// k-blocks of 64 each.
+// CTAs per tile in the grouped shrink, with the tiles that full ones and one
+// rest per adapter make and at least four k-blocks of 64 each: as many as two
+// per SM hold at once, or somewhat more where each keeps a long range of K,
+// since a tile's time goes with its range and whole tiles share out badly.
+// Measured, us for s = 1, 2, 4, 8 (rounds of CTAs at s = 1): 4096 rows, 64
+// adapters, K 4096 (0.3) 68, 53, 48, 57; 16384 rows, 32 adapters, K 4096 (0.5)
+// 103, 92, 97, 120; 8000 rows, 300 adapters, K 4096 (1.2) 117, 106, 130, 168;
+// 2048 tokens on 4 of 32 experts, 4 adapters, K 2048 (0.6) 51, 45, 49, 67; on 8
+// of 128 (2.1) 91, 103, 153, 223; 777 rows, 40 adapters, K 4096 (0.15) 54, 38,
+// 31, 32.
 int lora_splits(int64_t rows, int64_t slots, int K) {
   const int64_t tiles = (rows + kLoraTileRows - 1) / kLoraTileRows + (slots < rows ? slots : rows);
+  const int64_t held = 2 * moe_host::sm_count();
   int s = 1;
-  while (s < kLoraMaxSplit && 2 * s * tiles <= 2 * moe_host::sm_count() && 2 * s * 256 <= K) s *= 2;
+  while (s < kLoraMaxSplit && 2 * s * 256 <= K) {
+    const int64_t ctas = 2 * s * tiles;
+    // at most a round, or 1.3 of them per 1024 of K
+    if (ctas > held && ctas * 10240 > held * 13 * (K / (2 * s))) break;
+    s *= 2;
+  }
   return s;
 }
 
