@@ -253,9 +253,10 @@ namespace {
 // cluster.  A cluster costs its row's A and B from L2, so rows x rank; the
 // grouping costs two more launches and gains when rows share matrices.
 // Measured, K = N = 4096 bf16, us (own cluster / grouped): rank 16, 256 rows
-// 11.1 / 15.6 over 8 adapters, 13.2 / 25.1 over 64; rank 64, 64 rows 10.3 /
-// 18.1 over 8, 14.5 / 35.7 over 64; 96 rows 22.3 / 18.3 over 8, 31.9 / 39.3
-// over 64; 256 rows 30.6 / 21.5 over 8, 45.3 / 46.5 over 64.  Far more rows
+// 11.2 / 18.0 over 8 adapters, 13.4 / 18.8 over 64; 384 rows 18.3 / 17.5 and
+// 21.8 / 19.1; rank 64, 64 rows 10.5 / 16.2 over 8, 15.0 / 24.1 over 64; 96 rows
+// 22.5 / 16.3 and 32.9 / 26.9; 128 rows 16.7 / 16.6 and 25.8 / 27.5; 256 rows
+// 28.0 / 20.3 and 46.0 / 31.1.  Far more rows
 // are grouped even if every adapter could have few of them: which of the
 // adapters a batch uses is known on the device only.
 bool lora_groups(int64_t rows, int E, int n_adapters, int R) {
