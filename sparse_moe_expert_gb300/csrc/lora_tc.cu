@@ -26,7 +26,7 @@
 // it plan 6, shrink 22 (67 MB of x: 10 at the copy rate; 1 us per k-block of 64,
 // the latency of its loads), expand 80 (360 MB: 53 at the copy rate, 58 to 84
 // for a bare copy with its access pattern).  777 tokens, 40 adapters, rank 32,
-// fp32: 30.5 us, of it plan 5, shrink 13, expand 12, each bound by its chain of
+// fp32: 29.7 us, of it plan 5, shrink 12, expand 12, each bound by its chain of
 // dependent loads.  Gathering the shrink's rows with TMA (four rows of 128 bytes
 // per request) was slower, 128 and 43 us: the requests follow one another at
 // some 40 ns.
@@ -286,7 +286,11 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
 
 constexpr int kShrinkThreads = 256;
 constexpr int kShrinkWarps = kShrinkThreads / 32;
-constexpr int kShrinkStages = 3;
+// k-blocks in shared memory.  Four for ranks up to 32; with more the expand's
+// CTAs find less room to start beside the shrink's.  us with 3 / 4 / 5: 777
+// rows, rank 32 30.5 / 29.7 / -; 4096 rows, rank 16 37.9 / 36.3 / 36.5; 8192
+// rows, rank 64, N 11008 111.3 / 114.5 / -.
+__host__ __device__ constexpr int shrink_stages(int NT) { return NT > 4 ? 3 : 4; }
 
 // A tile of up to 16 rows, k in [k0, k1): the warps take blocks of 32 k in
 // turn, fragments straight from global memory (lane t of a quad holds 8
@@ -348,6 +352,7 @@ __device__ __forceinline__ void shrink_small(const LoraParams& p, const LoraPlan
 template <int NT>
 __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_tc_kernel(
     LoraParams p, LoraPlan pl, int terms, uint32_t tmem_cols) {
+  constexpr int kStages = shrink_stages(NT);
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t done;
   __shared__ uint32_t tmem_sh;
@@ -415,13 +420,13 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_tc_kernel(
         }
         ar += 64;
       };
-      for (int kb = 0; kb < kShrinkStages - 1; ++kb) {
+      for (int kb = 0; kb < kStages - 1; ++kb) {
         if (kb < nb) load(kb);
         cp_async_commit();
       }
-      int s = 0, before = kShrinkStages - 1;  // stages of this k-block and of the one before
+      int s = 0, before = kStages - 1;  // stages of this k-block and of the one before
       for (int kb = 0; kb < nb; ++kb) {
-        cp_async_wait<kShrinkStages - 2>();
+        cp_async_wait<kStages - 2>();
         fence_proxy_async_smem();
         // the products of the k-block before have had this one's wait to end
         if (warp == 0 && kb > 0) {
@@ -440,10 +445,10 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_tc_kernel(
             umma_bf16(tmem, xd + 2 * k, ad + 2 * k, idesc, kb > 0 || k > 0);
           umma_commit(&done);
         }
-        if (kb + kShrinkStages - 1 < nb) load(before);
+        if (kb + kStages - 1 < nb) load(before);
         cp_async_commit();
         before = s;
-        s = s == kShrinkStages - 1 ? 0 : s + 1;
+        s = s == kStages - 1 ? 0 : s + 1;
       }
       if (warp == 0) {
         wait_or_flag(&done, parity, bad, p.err);
@@ -956,13 +961,14 @@ moe_status_t launch_expand(const LoraParams& p, const LoraPlan& plan, cudaStream
 template <int NT>
 moe_status_t launch_shrink(const LoraParams& p, const LoraPlan& plan, int terms, cudaStream_t st) {
   using namespace moe_host;
+  constexpr int kStages = shrink_stages(NT);
   const int RP = rank_pad(p.R);
-  const size_t smem = (size_t)kShrinkStages * (kBlockBytes + RP * 128) + 1024;
+  const size_t smem = (size_t)kStages * (kBlockBytes + RP * 128) + 1024;
   // the least padded rank of this instantiation, and what lies over its stages
   constexpr int least = NT == 2 ? 16 : rank_pad(NT * 4 + 8);
   static_assert(kLoraSmallRows * (NT * 8 + 4) * 4 + kShrinkWarps * kLoraSmallRows * NT * 8 * 4 <=
-                    kShrinkStages * (kBlockBytes + least * 128), "the small tiles' sums fit");
-  static_assert(kLoraTileRows * (NT * 8 + 4) * 4 <= kShrinkStages * (kBlockBytes + least * 128),
+                    kStages * (kBlockBytes + least * 128), "the small tiles' sums fit");
+  static_assert(kLoraTileRows * (NT * 8 + 4) * 4 <= kStages * (kBlockBytes + least * 128),
                 "a tile's sums fit");
   static size_t set_max[kMaxCachedDevices] = {};
   const int dev = device_index();
