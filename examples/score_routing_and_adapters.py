@@ -54,7 +54,7 @@ def finetune_router(layer, x, adapter_ids, target, steps, lr=0.3):
         history.append((float(diff.square().mean()), float(aux[0]), float(aux[1])))
         layer.router_w -= lr * layer.inv_temperature * (d_logits.t() @ x.float())
         # the balance bias moves against the load, one step per batch
-        load = layer.buffers(x.shape[0])["counts"].float()
+        load = layer.chosen_counts().float()
         layer.scoring.select_bias += 0.001 * torch.sign(load.mean() - load)
     return history
 

@@ -554,7 +554,9 @@ moe_status_t moe_route_scored(const void* logits, int logits_dtype, int64_t ld,
  *                  different ids within a token.
  * d_topk_w         fp32 [T, kmax] (moe_combine_backward), or NULL: the losses
  *                  alone.
- * expert_counts    int32 [E]; may be NULL when balance_coef is 0.
+ * expert_counts    int32 [E]: how often topk_ids choose each expert (of a
+ *                  grouping with a capacity the kept ones alone would be too
+ *                  few); may be NULL when balance_coef is 0.
  * d_logits         out: like logits, rows ld_out apart; not the same memory.
  * losses           out: fp32 [2].
  * workspace        device scratch of moe_route_backward_workspace_size(E)

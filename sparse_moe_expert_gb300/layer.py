@@ -393,12 +393,25 @@ class MoELayer:
         ev.stop()
         return res
 
+    def chosen_counts(self) -> torch.Tensor:
+        """int32 [E]: how often the last forward's routing chose each expert,
+        the assignments that a capacity turned away included (the grouping's
+        own counts hold the kept ones).  May be a buffer that the next forward
+        writes again."""
+        if self._last is None:
+            raise ValueError("chosen_counts needs a forward first")
+        b = self.buffers(self._last)
+        if self.capacity is None:
+            return b["counts"]
+        return B.moe_permute_masked(b["topk_ids"], b["k_dev"], self.E)[0]
+
     def router_grad(self, d_out: torch.Tensor, balance_coef: float = 0.0, z_coef: float = 0.0):
         """Gradient of the last forward with respect to the router logits, the
         experts held fixed: -> (d_logits fp32 [T, E], losses fp32 [2]).
 
         d_out bf16 [T, H]: the gradient of the layer's output.  Adds the
-        balance and z losses (their values are returned).  Only for layers
+        balance and z losses (their values are returned); the balance loss
+        counts the router's choices, whatever a capacity kept.  Only for layers
         with ``scoring``; the router weight's gradient is
         inv_temperature * d_logits^T x."""
         if self.scoring is None or self._last is None:
@@ -413,8 +426,9 @@ class MoELayer:
         d_w, _ = B.moe_combine_backward(d_out, b["y"], b["inv_pos"], b["topk_w"], b["k_dev"],
                                         need_d_y=False)
         s = self.scoring
+        counts = self.chosen_counts() if balance_coef else None
         return B.moe_route_scored_backward(
-            b["logits"], b["topk_ids"], d_w, b["counts"], s.score, self.k_fixed, self.renormalize,
+            b["logits"], b["topk_ids"], d_w, counts, s.score, self.k_fixed, self.renormalize,
             s.scale, balance_coef, z_coef)
 
     def _forward_k_split(self, x, b, ks, T, out, events):

@@ -176,3 +176,46 @@ def test_example_runs_and_learns(cuda_lib):
     assert not torch.equal(adapted[~none], plain[~none])
     assert history[-1][0] < history[0][0]
     assert all(np.isfinite(h).all() for h in history)
+
+
+@pytest.mark.parametrize("capacity", [0, 3, 9])
+def test_router_grad_with_a_capacity_balances_what_was_chosen(cuda_lib, capacity):
+    """An expert's capacity turns rows away from the products; the balance loss
+    still counts every choice of the router.  Against the objective in 64 bits
+    with counts taken from the ids, and its differences."""
+    T, E, k, H = 40, 16, 4, 256
+    cfg, layer_np, layer, lora, x_bits, ids = make(cuda_lib, T, E, k, H, 128, 3, 8,
+                                                   cuda_lib.PATH_AUTO, capacity=capacity)
+    x = cuda_lib.bf16_from_bits(x_bits, dev())
+    layer(x, adapter_ids=torch.tensor(ids, device=dev()))
+    g = np.random.default_rng(5)
+    d_out = torch.tensor(g.normal(size=(T, H)), dtype=torch.float32, device=dev()).bfloat16()
+    d_logits, losses = layer.router_grad(d_out, balance_coef=0.5, z_coef=0.01)
+    b = layer.buffers(T)
+    y, topk, inv = b["y"].double().cpu().numpy(), to_np(b["topk_ids"]), to_np(b["inv_pos"])
+    counts = np.bincount(topk[topk >= 0], minlength=E).astype(np.float64)
+    assert (counts > capacity).any() and (inv == -2).any()  # the capacity binds
+    D, l0 = d_out.double().cpu().numpy(), b["logits"].double().cpu().numpy()
+    proj = np.array([[D[t] @ y[inv[t * k + j]] if inv[t * k + j] >= 0 else 0.0
+                      for j in range(k)] for t in range(T)])
+
+    def objective(l):
+        s = 1 / (1 + np.exp(-l))
+        w = np.take_along_axis(s, topk, 1)
+        w = 2.5 * w / w.sum(1, keepdims=True)
+        q = s / s.sum(1, keepdims=True)
+        m = l.max(1, keepdims=True)
+        lse = (m + np.log(np.exp(l - m).sum(1, keepdims=True)))[:, 0]
+        return ((w * proj).sum(), 0.5 * E / (k * T) * (counts * q.mean(0)).sum(),
+                0.01 * (lse ** 2).mean())
+
+    assert np.allclose(to_np(losses), objective(l0)[1:], rtol=1e-5)
+    num = np.zeros_like(l0)
+    for t in range(T):
+        for e in range(E):
+            hi, lo = l0.copy(), l0.copy()
+            hi[t, e] += 1e-5
+            lo[t, e] -= 1e-5
+            num[t, e] = (sum(objective(hi)) - sum(objective(lo))) / 2e-5
+    # fp32 sums over H = 256 in d_w, then the gradient's own 1e-5
+    assert rel_l2(to_np(d_logits), num) <= 2e-5
