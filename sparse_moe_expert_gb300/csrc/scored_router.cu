@@ -421,7 +421,12 @@ __global__ void __launch_bounds__(kScoredThreads, V <= 8 ? 4 : 2)
         merge_top2(a1, a2, b1, b2);
       }
       // every lane of a group holds the group's value
-      const float val = p.group_top == 2 && a2 > -INFINITY ? a1 + a2 : a1;
+      const bool pair = p.group_top == 2 && a2 > -INFINITY;
+      const float val = pair ? a1 + a2 : a1;
+      // how far val may be from the exact value: the choices' errors, each
+      // relative to its choice, which do not cancel as the choices may
+      const float mag = pair ? fabsf(a1) + fabsf(a2) : fabsf(a1);
+      const float err = mag < INFINITY ? fmaf(mag, 0x1p-21f, 2.0f * eps) : 0.0f;
       const float mine = my_group < G ? val : -INFINITY;
       const bool first = (lane & (width - 1)) == 0;  // one lane of each group
       float rest = mine, cut = -INFINITY;
@@ -440,13 +445,13 @@ __global__ void __launch_bounds__(kScoredThreads, V <= 8 ? 4 : 2)
           if (rest == cut) rest = -INFINITY;
         }
       }
-      const float next = redux_max(rest);
       live = mine >= cut && mine > -INFINITY;
-      // as many groups as asked (or all that have an expert), and the next one
+      const float least = redux_min(live ? mine - err : INFINITY);  // a chosen group's value
+      const float next = redux_max(live ? -INFINITY : mine + err);  // another's
+      // as many groups as asked (or all that have an expert), and the others
       // clearly below
       const bool sure = next == -INFINITY ? groups <= p.topk_groups
-                                          : groups == p.topk_groups &&
-                                                cut - next > 4.0f * eps + fabsf(next) * 0x1p-20f;
+                                          : groups == p.topk_groups && least > next;
       if (!sure) return -1;
       if constexpr (!LANES) {  // strike the other groups' choices
         if (!live)

@@ -944,3 +944,41 @@ def test_lora_wide_rank(cuda_lib, T, K, N, R, NA, dtype):
 @pytest.mark.parametrize("swiglu", [False, True])
 def test_lora_wide_rank_expert_rows(cuda_lib, T, k, E, NA, K, N, R, swiglu):
     test_lora_expert_rows(cuda_lib, T, k, E, NA, K, N, R, swiglu)
+
+
+@pytest.mark.parametrize("pad", [0, 1])
+def test_route_scored_groups_of_cancelling_biases(cuda_lib, pad):
+    """Groups whose two best choices are large and of opposite sign: their sum
+    is small, its rounding is the summands'.  The scores are taken from the
+    call itself (every expert, no bias; checked in 64 bits), the choices and
+    the group values from the definition in fp32.  One group's score runs over
+    the floats around the points where score + 4096 rounds up, the other's
+    stays inside the interval below."""
+    step = 2.0 ** -11                        # an ulp of 4096 + s
+    q = np.arange(80, 1960, dtype=np.float64)
+    edge, inside = (q + 0.5) * step, q * step
+    at = np.log(edge / (1 - edge)).astype(np.float32)
+    near = np.stack([(at.view(np.int32) + d).view(np.float32) for d in range(-32, 33)], 1)
+    other = np.log(inside / (1 - inside)).astype(np.float32)
+    n = 2 + pad                              # experts of a group; the third one is masked
+    l = np.full(near.shape + (2 * n,), -np.inf, np.float32)
+    l[..., 0] = other[:, None]
+    l[..., n] = near
+    l[..., 1] = l[..., n + 1] = -0.3
+    l = l.reshape(-1, 2 * n)
+    bias = np.zeros(2 * n, np.float32)
+    bias[[0, n]], bias[[1, n + 1]] = 4096.0, -4096.0
+    l_t, d = torch.tensor(l, device=dev()), dev()
+    on = np.isfinite(l)
+    ids, w, _ = cuda_lib.moe_route_scored(l_t, 4, score=1, renormalize=False)
+    s = np.zeros_like(l)
+    np.put_along_axis(s, to_np(ids).astype(np.int64), to_np(w).astype(np.float32), 1)
+    s64, _ = scores64(l.astype(np.float64), 1)
+    assert np.allclose(s[on], s64[on], rtol=W_TOL, atol=0)
+    c = (s + bias).astype(np.float32)
+    value = np.stack([c[:, 0] + c[:, 1], c[:, n] + c[:, n + 1]], 1)
+    assert (value[:, 0] == value[:, 1]).any() and (value[:, 0] < value[:, 1]).any()
+    want = np.where(value[:, 1] > value[:, 0], n, 0)   # equal groups: the lower one
+    ids, _, _ = cuda_lib.moe_route_scored(l_t, 2, score=1, select_bias=torch.tensor(bias, device=d),
+                                          n_groups=2, topk_groups=1, group_top=2)
+    assert np.array_equal(to_np(ids), np.stack([want, want + 1], 1))
