@@ -294,12 +294,26 @@ def moe_get_device_error(clear: bool = True, stream=None) -> int:
 # allocate missing outputs and make the C call in csrc/native.cpp.
 
 
-def _hold(stream, *tensors):
-    """Tell the allocator that ``stream`` uses these tensors, so that none of
-    their memory is handed out again before the enqueued work has run."""
-    for t in tensors:
+def _new(stream, shape, dtype, dev) -> torch.Tensor:
+    """Uninitialized memory that belongs to ``stream`` (None: the current one),
+    so that it is none that another stream gave up and may still read."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _hold(stream, inputs, results):
+    """Tell the allocator that ``stream`` uses these tensors, and the caller's
+    current stream the results, so that none of their memory is handed out
+    again before the enqueued work has run."""
+    here = torch.cuda.current_stream(stream.device)
+    for t in (*inputs, *results):
         if t is not None:
             t.record_stream(stream)
+    for t in results:
+        if t is not None:
+            t.record_stream(here)
 
 
 def _like(t: torch.Tensor, shape: tuple, dtype, dev, name: str):
@@ -329,11 +343,11 @@ def moe_router_logits(x, w_router, logit_bias=None, inv_temperature: float = 1.0
     if logit_bias is not None:
         _like(logit_bias, (E,), torch.float32, dev, "logit_bias")
     if logits is None:
-        logits = torch.empty((T, E), dtype=torch.float32, device=dev)
+        logits = _new(stream, (T, E), torch.float32, dev)
     else:
         _like(logits, (T, E), torch.float32, dev, "logits")
     if stream is not None:
-        _hold(stream, x, w_router, logit_bias, logits)
+        _hold(stream, (x, w_router, logit_bias), (logits,))
     check("moe_router_logits",
           lib().moe_router_logits(_p(x), _p(w_router), _p(logit_bias), inv_temperature, T, H, E,
                                   _p(logits), _stream(stream)))
@@ -356,7 +370,7 @@ def moe_route_scored(logits, k: int, score: int = _lib.SCORE_SOFTMAX, select_bia
     if r.__class__ is int:
         check("moe_route_scored", r)
     if stream is not None:
-        _hold(stream, logits, select_bias, *r)
+        _hold(stream, (logits, select_bias), r)
     return r
 
 
@@ -379,7 +393,7 @@ def moe_route_scored_backward(logits, topk_ids, d_topk_w=None, expert_counts=Non
     if r.__class__ is int:
         check("moe_route_scored_backward", r)
     if stream is not None:
-        _hold(stream, logits, topk_ids, d_topk_w, expert_counts, *r)
+        _hold(stream, (logits, topk_ids, d_topk_w, expert_counts), r)
     return r[:2]
 
 
@@ -394,23 +408,23 @@ def moe_permute_masked(topk_ids, k_dev, E: int, capacity: Optional[int] = None,
     A = max(T * kmax, 1)
     _like(k_dev, (1,), torch.int32, dev, "k_dev")
     if expert_counts is None:
-        expert_counts = torch.empty(E, dtype=torch.int32, device=dev)
+        expert_counts = _new(stream, E, torch.int32, dev)
     else:
         _like(expert_counts, (E,), torch.int32, dev, "expert_counts")
     if expert_offsets is None:
-        expert_offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        expert_offsets = _new(stream, E + 1, torch.int32, dev)
     else:
         _like(expert_offsets, (E + 1,), torch.int32, dev, "expert_offsets")
     if sorted_assign is None:
-        sorted_assign = torch.empty(A, dtype=torch.int32, device=dev)
+        sorted_assign = _new(stream, A, torch.int32, dev)
     else:
         _flat(sorted_assign, T * kmax, dev, "sorted_assign")
     if inv_pos is None:
-        inv_pos = torch.empty(A, dtype=torch.int32, device=dev)
+        inv_pos = _new(stream, A, torch.int32, dev)
     else:
         _flat(inv_pos, T * kmax, dev, "inv_pos")
     if stream is not None:
-        _hold(stream, topk_ids, k_dev, expert_counts, expert_offsets, sorted_assign, inv_pos)
+        _hold(stream, (topk_ids, k_dev), (expert_counts, expert_offsets, sorted_assign, inv_pos))
     check("moe_permute_masked",
           lib().moe_permute_masked(_p(topk_ids), _p(k_dev), T, kmax, E,
                                    -1 if capacity is None else int(capacity), _p(expert_counts),
@@ -426,15 +440,12 @@ def moe_combine_backward(d_out, y, inv_pos, topk_w, k_dev, d_topk_w=None, d_y=No
     Rows of ``d_y`` that no kept slot points to keep what they held (zeros
     when the buffer is allocated here).  need_d_y=False computes d_topk_w
     alone (d_y is None)."""
-    if d_y is None and need_d_y and stream is not None:
-        with torch.cuda.stream(stream):  # the zeros belong to the call
-            d_y = torch.zeros_like(y)
     r = native().combine_backward(d_out, y, inv_pos, topk_w, k_dev, d_topk_w, d_y, need_d_y,
                                   None if stream is None else stream.cuda_stream)
     if r.__class__ is int:
         check("moe_combine_backward", r)
     if stream is not None:
-        _hold(stream, d_out, y, inv_pos, topk_w, k_dev, *r)
+        _hold(stream, (d_out, y, inv_pos, topk_w, k_dev), r)
     return r
 
 
@@ -466,6 +477,6 @@ def moe_lora_apply(x, adapter_ids, lora_a, lora_b, scales=None, base=None, out=N
     if r.__class__ is int:
         check("moe_lora_apply", r)
     if stream is not None:
-        _hold(stream, x, adapter_ids, lora_a, lora_b, scales, base, topk_ids, sorted_assign,
-              expert_offsets, *r)
+        _hold(stream, (x, adapter_ids, lora_a, lora_b, scales, base, topk_ids, sorted_assign,
+                       expert_offsets), r)
     return r[0]

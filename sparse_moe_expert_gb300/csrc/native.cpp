@@ -166,16 +166,26 @@ size_t scratch_bytes(const Tensor& t, c10::Device dev) {
   return (size_t)t.nbytes();
 }
 
-// The stream a call runs on: the handle that Python passed, or the device's
-// current stream.
-moe_stream_t stream_of(PyObject* o, c10::Device dev) {
-  if (o != Py_None) {
-    void* s = PyLong_AsVoidPtr(o);
-    if (!s && PyErr_Occurred()) throw Raised();
-    return s;
+// The device and stream a call runs on: the handle that Python passed, or the
+// device's current stream.  While it lives they are torch's current ones, so
+// that what the call allocates belongs to its stream: a block that another
+// stream gave up, and may still read, is not handed out to it.
+struct OnStream {
+  c10::cuda::CUDAGuard device;
+  c10::cuda::OptionalCUDAStreamGuard guard;
+  moe_stream_t handle;
+
+  OnStream(PyObject* o, c10::Device dev) : device(dev) {
+    if (o == Py_None) {
+      handle = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+      return;
+    }
+    handle = PyLong_AsVoidPtr(o);
+    if (!handle && PyErr_Occurred()) throw Raised();
+    guard.reset_stream(
+        c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle), dev.index()));
   }
-  return c10::cuda::getCurrentCUDAStream(dev.index()).stream();
-}
+};
 
 PyObject* result(std::initializer_list<Tensor> ts) {
   PyObject* t = PyTuple_New((Py_ssize_t)ts.size());
@@ -222,7 +232,7 @@ PyObject* route_scored(Args a) {
   }
   if (kmax < 0) return status(MOE_ERR_INVALID_ARG);
   const c10::Device dev = logits.device();
-  const c10::cuda::CUDAGuard guard(dev);
+  const OnStream on(stream, dev);
   if (bias.defined()) like(bias, {E}, at::kFloat, dev, "select_bias");
   if (ids.defined()) like(ids, {T, kmax}, at::kInt, dev, "topk_ids");
   else ids = make({T, kmax}, at::kInt, dev);
@@ -233,7 +243,7 @@ PyObject* route_scored(Args a) {
   const moe_status_t s = moe_route_scored(
       logits.data_ptr(), dtype_code(logits, "logits"), ld, ptr<float>(bias), T, E, score, n_groups,
       topk_groups, group_top, k, kmax, renorm, (float)scale, ptr<int32_t>(ids), ptr<float>(w),
-      ptr<int32_t>(k_dev), stream_of(stream, dev));
+      ptr<int32_t>(k_dev), on.handle);
   return s ? status(s) : result({ids, w, k_dev});
 }
 
@@ -260,7 +270,7 @@ PyObject* route_scored_backward(Args a) {
     Args one{&k_o, 1};
     k = one.i32();
   }
-  const c10::cuda::CUDAGuard guard(dev);
+  const OnStream on(stream, dev);
   if (d_w.defined()) like(d_w, {T, kmax}, at::kFloat, dev, "d_topk_w");
   if (counts.defined()) like(counts, {E}, at::kInt, dev, "expert_counts");
   int64_t ld_out = E;
@@ -280,7 +290,7 @@ PyObject* route_scored_backward(Args a) {
       logits.data_ptr(), dtype_code(logits, "logits"), ld, ptr<int32_t>(ids), ptr<float>(d_w),
       ptr<int32_t>(counts), T, E, score, k, kmax, renorm, (float)scale, (float)balance, (float)z,
       d_logits.data_ptr(), ld_out, ptr<float>(losses), ws.data_ptr(), scratch_bytes(ws, dev),
-      stream_of(stream, dev));
+      on.handle);
   return s ? status(s) : result({d_logits, losses, ws});
 }
 
@@ -295,7 +305,7 @@ PyObject* combine_backward(Args a) {
   if (d_out.dim() != 2) throw Refused("d_out must be [T, H]");
   const int T = as_int(d_out.size(0), "T"), H = as_int(d_out.size(1), "H");
   const c10::Device dev = d_out.device();
-  const c10::cuda::CUDAGuard guard(dev);
+  const OnStream on(stream, dev);
   if (w.dim() != 2) throw Refused("topk_w must be [T, kmax]");
   const int kmax = as_int(w.size(1), "kmax");
   like(w, {T, kmax}, at::kFloat, dev, "topk_w");
@@ -308,7 +318,7 @@ PyObject* combine_backward(Args a) {
   else if (need_d_y) d_y = at::zeros_like(y);
   const moe_status_t s = moe_combine_backward(
       ptr<uint16_t>(d_out), y.data_ptr(), dtype_code(y, "y"), ptr<int32_t>(inv_pos), ptr<float>(w),
-      ptr<int32_t>(k_dev), T, kmax, H, ptr<float>(d_w), ptr<void>(d_y), stream_of(stream, dev));
+      ptr<int32_t>(k_dev), T, kmax, H, ptr<float>(d_w), ptr<void>(d_y), on.handle);
   return s ? status(s) : result({d_w, d_y});
 }
 
@@ -330,7 +340,7 @@ PyObject* lora_apply(Args a) {
 
   need(x, at::kBFloat16, "x");
   const c10::Device dev = x.device();
-  const c10::cuda::CUDAGuard guard(dev);
+  const OnStream on(stream, dev);
   if (la.dim() != 3 && la.dim() != 4) throw Refused("lora_a must be [n, R, K] or [n, E, R, K]");
   if (lb.dim() != la.dim()) throw Refused("lora_b does not match lora_a");
   const bool experts = la.dim() == 4;
@@ -376,7 +386,7 @@ PyObject* lora_apply(Args a) {
       ptr<int32_t>(offsets), T, kmax, E, n, K, N, R, ptr<uint16_t>(la), ptr<uint16_t>(lb),
       ptr<float>(scales), ptr<void>(base), base.defined() ? dtype_code(base, "base") : out_dt,
       epilogue, out_dt, out.data_ptr(), ws.data_ptr(), scratch_bytes(ws, dev),
-      stream_of(stream, dev));
+      on.handle);
   return s ? status(s) : result({out, ws});
 }
 
