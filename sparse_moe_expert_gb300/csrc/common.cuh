@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/moe_gb300.h"
 
 namespace moe {
@@ -120,6 +122,25 @@ int sm_count();
 // (kernel attributes are set per device); 0 .. kMaxCachedDevices - 1.
 constexpr int kMaxCachedDevices = 64;
 int device_index();
+
+// Lets a kernel take up to `most` bytes of dynamic shared memory on the current
+// device, once.  `most` is the largest size that any call asks of the kernel,
+// never one call's own: a host thread with a smaller one could lower the limit
+// between another thread's setting and its launch.
+template <auto Kernel>
+inline moe_status_t allow_smem(size_t most) {
+  static std::atomic<bool> set[kMaxCachedDevices] = {};
+  std::atomic<bool>& mine = set[device_index()];
+  if (!mine.load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return MOE_ERR_CUDA;
+    }
+    mine.store(true, std::memory_order_release);
+  }
+  return MOE_OK;
+}
 
 // Device address of the current device's error word (nullptr on failure).
 unsigned int* device_error_word();

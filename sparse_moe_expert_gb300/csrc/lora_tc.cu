@@ -930,15 +930,9 @@ template <int TERMS, bool BASE_BF16, bool OUT_BF16, bool SWIGLU, int GROUPS>
 moe_status_t launch_expand_groups(const LoraParams& p, const LoraPlan& plan, cudaStream_t st) {
   using namespace moe_host;
   const size_t smem = expand_smem(TERMS, rank_pad(p.R), GROUPS);
-  auto kern = lora_expand_tc_kernel<TERMS, BASE_BF16, OUT_BF16, SWIGLU, GROUPS>;
-  static size_t set_max[kMaxCachedDevices] = {};
-  const int dev = device_index();
-  if (smem > set_max[dev]) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-        cudaSuccess)
-      return MOE_ERR_CUDA;
-    set_max[dev] = smem;
-  }
+  constexpr auto kern = lora_expand_tc_kernel<TERMS, BASE_BF16, OUT_BF16, SWIGLU, GROUPS>;
+  const moe_status_t s = allow_smem<kern>(expand_smem(TERMS, kMaxRank, GROUPS));
+  if (s != MOE_OK) return s;
   const int per_sm = expand_per_sm(smem, GROUPS > 1 ? 1 : BASE_BF16 ? 4 : 3);
   const int cols = SWIGLU ? p.N / 2 : p.N;
   const int span = GROUPS * (SWIGLU ? kExpandCols / 2 : kExpandCols);
@@ -970,14 +964,9 @@ moe_status_t launch_shrink(const LoraParams& p, const LoraPlan& plan, int terms,
                     kStages * (kBlockBytes + least * 128), "the small tiles' sums fit");
   static_assert(kLoraTileRows * (NT * 8 + 4) * 4 <= kStages * (kBlockBytes + least * 128),
                 "a tile's sums fit");
-  static size_t set_max[kMaxCachedDevices] = {};
-  const int dev = device_index();
-  if (smem > set_max[dev]) {
-    if (cudaFuncSetAttribute(lora_shrink_tc_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem) != cudaSuccess)
-      return MOE_ERR_CUDA;
-    set_max[dev] = smem;
-  }
+  const moe_status_t s = allow_smem<lora_shrink_tc_kernel<NT>>(
+      (size_t)kStages * (kBlockBytes + NT * 8 * 128) + 1024);
+  if (s != MOE_OK) return s;
   uint32_t tmem_cols = 32;
   while ((int)tmem_cols < RP) tmem_cols <<= 1;
   constexpr int per_sm = 2;
@@ -995,16 +984,16 @@ moe_status_t lora_grouped(const LoraParams& p, const LoraPlan& plan, int64_t row
   // with several experts their CTAs add to the counts
   if (p.E > 1 && cudaMemsetAsync(plan.counts, 0, sizeof(int4), st) != cudaSuccess)
     return MOE_ERR_CUDA;
-  const size_t plan_smem = (size_t)(4 + kPlanWarps) * (p.n_adapters + 1) * sizeof(int);
-  if (plan_smem > 48 * 1024 &&
-      cudaFuncSetAttribute(lora_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)plan_smem) != cudaSuccess)
-    return MOE_ERR_CUDA;
+  auto plan_bytes = [](int adapters) {
+    return (size_t)(4 + kPlanWarps) * (adapters + 1) * sizeof(int);
+  };
+  moe_status_t s = allow_smem<lora_plan_kernel>(plan_bytes(kLoraPlanAdapters));
+  if (s != MOE_OK) return s;
   // CTAs per expert: one per 1024 of the rows that an expert has on average
   int ranges = 1;
   while (ranges < kPlanRanges && (int64_t)ranges * 1024 * p.E < rows) ranges *= 2;
-  moe_status_t s = moe_host::launch_clusters(lora_plan_kernel, dim3(p.E, ranges), kPlanThreads, plan_smem,
-                                   dim3(1, ranges), st, p, plan);
+  s = moe_host::launch_clusters(lora_plan_kernel, dim3(p.E, ranges), kPlanThreads,
+                                plan_bytes(p.n_adapters), dim3(1, ranges), st, p, plan);
   if (s != MOE_OK) return s;
   const int terms = out_bf16 && !swiglu ? 2 : 3;
   if (p.R <= 16) s = launch_shrink<2>(p, plan, terms, st);

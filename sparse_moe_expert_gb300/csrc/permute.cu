@@ -24,6 +24,7 @@ namespace {
 
 constexpr int kPermuteThreads = 1024;
 constexpr int kPermuteWarps = kPermuteThreads / 32;
+constexpr int kPermuteExperts = 1024;  // at most
 
 struct PermuteParams {
   const int32_t* ids;
@@ -193,7 +194,7 @@ moe_status_t permute_impl(const int32_t* topk_ids, const int32_t* k_dev, int T, 
                           int32_t* expert_offsets, int32_t* sorted_assign, int32_t* inv_pos,
                           moe_stream_t stream) {
   using namespace moe_host;
-  if (T < 0 || E < 1 || E > 1024 || kmax < 1 || kmax > 16) return MOE_ERR_INVALID_ARG;
+  if (T < 0 || E < 1 || E > kPermuteExperts || kmax < 1 || kmax > 16) return MOE_ERR_INVALID_ARG;
   if ((int64_t)T * kmax > (1 << 24)) return MOE_ERR_INVALID_ARG;
   if (!k_dev || !expert_counts || !expert_offsets) return MOE_ERR_INVALID_ARG;
   if (T > 0 && (!topk_ids || !sorted_assign || !inv_pos)) return MOE_ERR_INVALID_ARG;
@@ -210,12 +211,10 @@ moe_status_t permute_impl(const int32_t* topk_ids, const int32_t* k_dev, int T, 
   p.capacity = capacity;
   p.empty_ok = empty_ok;
   p.err = device_error_word();
-  size_t smem = (size_t)(4 + kPermuteWarps) * E * sizeof(int);
-  if (smem > 48 * 1024) {
-    if (cudaFuncSetAttribute(permute_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem) != cudaSuccess)
-      return MOE_ERR_CUDA;
-  }
+  const size_t smem = (size_t)(4 + kPermuteWarps) * E * sizeof(int);
+  const moe_status_t allowed =
+      allow_smem<permute_kernel>((size_t)(4 + kPermuteWarps) * kPermuteExperts * sizeof(int));
+  if (allowed != MOE_OK) return allowed;
   // ranges of whole 1024-assignment chunks; every CTA also reads all ids
   // once to count, so the CTA count stays moderate
   const int slots = T * kmax;

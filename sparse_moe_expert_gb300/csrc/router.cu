@@ -1401,10 +1401,9 @@ extern "C" moe_status_t moe_router_logits(const uint16_t* x, const float* w_rout
   const int most = (E + moe::kRouterWarps - 1) / moe::kRouterWarps;
   if (slices > most) slices = most;
   const size_t smem = (size_t)p.tpc * E * sizeof(float);
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(moe::router_logits_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem) != cudaSuccess)
-    return MOE_ERR_CUDA;
+  const moe_status_t s = allow_smem<moe::router_logits_kernel>(
+      (size_t)moe::router_group_tokens(moe::kMaxExperts) * moe::kMaxExperts * sizeof(float));
+  if (s != MOE_OK) return s;
   return launch(moe::router_logits_kernel, dim3(groups, slices), moe::kRouterThreads, smem,
                 reinterpret_cast<cudaStream_t>(stream), p, slices, logits);
 }
