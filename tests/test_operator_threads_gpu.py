@@ -6,6 +6,8 @@ import ctypes
 import os
 import shutil
 import subprocess
+import threading
+import time
 
 import pytest
 import torch
@@ -74,7 +76,7 @@ class Job(ctypes.Structure):
 
 
 @pytest.fixture(scope="module")
-def threads(tmp_path_factory, cuda_lib):
+def hammer(tmp_path_factory, cuda_lib):
     cxx = shutil.which("g++") or shutil.which("c++")
     if cxx is None:
         pytest.skip("no C++ compiler")
@@ -111,26 +113,26 @@ def threads(tmp_path_factory, cuda_lib):
     return together
 
 
-def test_router_logits_of_several_widths(threads):
+def test_router_logits_of_several_widths(hammer):
     def job(E, T=4, K=64):
         x = torch.randn((T, K), device=dev()).bfloat16()
         w = torch.randn((E, K), device=dev())
         out = torch.empty((T, E), device=dev())
         return dict(kind=0, T=T, K=K, E=E), dict(x=x, a=w, out=out), [out]
-    threads([job(1024), job(800), job(1000), job(64)])
+    hammer([job(1024), job(800), job(1000), job(64)])
 
 
-def test_grouping_of_several_widths(threads):
+def test_grouping_of_several_widths(hammer):
     def job(E, T=16, k=4):
         ids = torch.randint(-1, E, (T, k), dtype=torch.int32, device=dev())
         kd = torch.full((1,), k, dtype=torch.int32, device=dev())
         outs = [torch.zeros(m, dtype=torch.int32, device=dev()) for m in (E, E + 1, T * k, T * k)]
         names = dict(zip(("out", "out2", "out3", "out4"), outs))
         return dict(kind=1, T=T, k=k, E=E), dict(x=kd, ids=ids, **names), outs
-    threads([job(1024), job(400), job(700), job(8)])
+    hammer([job(1024), job(400), job(700), job(8)])
 
 
-def test_grouped_adapters_of_several_counts_and_ranks(threads, cuda_lib):
+def test_grouped_adapters_of_several_counts_and_ranks(hammer, cuda_lib):
     def job(n, R, dtype, T=1024, K=256, N=128):
         g = torch.Generator(device=dev())
         g.manual_seed(n)
@@ -145,6 +147,36 @@ def test_grouped_adapters_of_several_counts_and_ranks(threads, cuda_lib):
         dt = cuda_lib.DTYPE_BF16 if dtype == torch.bfloat16 else cuda_lib.DTYPE_F32
         return (dict(kind=2, T=T, n=n, K=K, N=N, R=R, dtype=dt, ws_bytes=size),
                 dict(x=x, a=a, b=b, base=base, ids=ids, out=out, ws=ws), [out])
-    threads([job(2000, 32, torch.float32), job(700, 32, torch.float32),
+    hammer([job(2000, 32, torch.float32), job(700, 32, torch.float32),
              job(40, 72, torch.float32), job(1200, 128, torch.float32),
              job(30, 128, torch.bfloat16), job(31, 72, torch.bfloat16)])
+
+
+def test_a_call_that_waits_for_its_queue_leaves_the_interpreter_free(cuda_lib):
+    """A stream is kept busy for some half a second while one thread fills its
+    queue; this thread goes on meanwhile."""
+    l = torch.randn((8, 64), device=dev())
+    outs = [t.clone() for t in cuda_lib.moe_route_scored(l, 4)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    spent = []
+
+    def fill():
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(1_000_000_000)
+            t0 = time.perf_counter()
+            for _ in range(6000):  # several times what a queue takes
+                cuda_lib.moe_route_scored(l, 4, topk_ids=outs[0], topk_w=outs[1], k_dev=outs[2])
+            spent.append(time.perf_counter() - t0)
+
+    worker = threading.Thread(target=fill)
+    longest, last = 0.0, time.perf_counter()
+    worker.start()
+    while worker.is_alive():
+        time.sleep(0.001)
+        now = time.perf_counter()
+        longest, last = max(longest, now - last), now
+    worker.join()
+    torch.cuda.synchronize()
+    assert spent[0] > 0.2      # the queue was full and the thread waited
+    assert longest < spent[0] / 2
