@@ -7,6 +7,7 @@ of the layer is computed here.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional
 
@@ -294,6 +295,15 @@ def moe_get_device_error(clear: bool = True, stream=None) -> int:
 # allocate missing outputs and make the C call in csrc/native.cpp.
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _on(dev):
+    """A context in which ``dev`` is the current device, and with it the
+    device that the C call and its default stream belong to."""
+    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
 def _new(stream, shape, dtype, dev) -> torch.Tensor:
     """Uninitialized memory that belongs to ``stream`` (None: the current one),
     so that it is none that another stream gave up and may still read."""
@@ -348,9 +358,10 @@ def moe_router_logits(x, w_router, logit_bias=None, inv_temperature: float = 1.0
         _like(logits, (T, E), torch.float32, dev, "logits")
     if stream is not None:
         _hold(stream, (x, w_router, logit_bias), (logits,))
-    check("moe_router_logits",
-          lib().moe_router_logits(_p(x), _p(w_router), _p(logit_bias), inv_temperature, T, H, E,
-                                  _p(logits), _stream(stream)))
+    with _on(dev):
+        st = lib().moe_router_logits(_p(x), _p(w_router), _p(logit_bias), inv_temperature, T, H, E,
+                                     _p(logits), _stream(stream))
+    check("moe_router_logits", st)
     return logits
 
 
@@ -425,11 +436,12 @@ def moe_permute_masked(topk_ids, k_dev, E: int, capacity: Optional[int] = None,
         _flat(inv_pos, T * kmax, dev, "inv_pos")
     if stream is not None:
         _hold(stream, (topk_ids, k_dev), (expert_counts, expert_offsets, sorted_assign, inv_pos))
-    check("moe_permute_masked",
-          lib().moe_permute_masked(_p(topk_ids), _p(k_dev), T, kmax, E,
-                                   -1 if capacity is None else int(capacity), _p(expert_counts),
-                                   _p(expert_offsets), _p(sorted_assign), _p(inv_pos),
-                                   _stream(stream)))
+    with _on(dev):
+        st = lib().moe_permute_masked(_p(topk_ids), _p(k_dev), T, kmax, E,
+                                      -1 if capacity is None else int(capacity),
+                                      _p(expert_counts), _p(expert_offsets), _p(sorted_assign),
+                                      _p(inv_pos), _stream(stream))
+    check("moe_permute_masked", st)
     return expert_counts, expert_offsets, sorted_assign, inv_pos
 
 
