@@ -97,7 +97,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
         native = ex.submit(_native_object)
         objs = list(ex.map(lambda s: _compile(nvcc, s, list(extra_flags)), srcs))
-        native_obj = native.result()
     newest = max(os.path.getmtime(o) for o in objs)
     if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < newest:
         tmp = LIB + f".tmp{os.getpid()}"
@@ -107,6 +106,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    native_obj = native.result()  # raises only now: the C library needs no torch
     if (force or not os.path.exists(NATIVE)
             or os.path.getmtime(NATIVE) < max(os.path.getmtime(native_obj), os.path.getmtime(LIB))):
         _link_native(native_obj)

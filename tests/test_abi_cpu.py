@@ -217,3 +217,21 @@ def test_operator_calls_reject_bad_shapes_before_launch(L):
                                None) == 1
     assert L.moe_router_logits(vp(GOOD), vp(GOOD), None, ctypes.c_float(1), 4, 100, 8, vp(GOOD),
                                None) == 1
+
+
+def test_the_c_library_is_built_without_torch(monkeypatch, tmp_path):
+    """Users of the C ABI need no torch: libmoe_gb300.so is linked before the
+    CPython entry points are asked for, whose failure is still raised."""
+    import sys
+    from sparse_moe_expert_gb300 import _build
+    src = tmp_path / "csrc"
+    src.mkdir()
+    (src / "one.cu").write_text('extern "C" int moe_one(void) { return 1; }\n')
+    monkeypatch.setattr(_build, "CSRC", str(src))
+    monkeypatch.setattr(_build, "BUILD", str(tmp_path / "_build"))
+    monkeypatch.setattr(_build, "LIB", str(tmp_path / "lib.so"))
+    monkeypatch.setattr(_build, "NATIVE", str(tmp_path / "_native.so"))
+    monkeypatch.setitem(sys.modules, "torch", None)
+    with pytest.raises(ImportError):
+        _build.build()
+    assert ctypes.CDLL(str(tmp_path / "lib.so")).moe_one() == 1
