@@ -282,10 +282,17 @@ class MoELayer:
         if ad.gate_up_a is not None and "gu_raw" not in b:
             b["gu_raw"] = torch.empty((max(T * self.kmax, 1), 2 * self.I), dtype=torch.float32,
                                       device=dev)
-        if "lora_ws" not in b:
-            need = [B.moe_lora_workspace_size(T, self.kmax, self.E, a.shape[0], a.shape[2])
-                    for a in (ad.gate_up_a, ad.down_a) if a is not None]
-            b["lora_ws"] = torch.empty(max(need, default=1), dtype=torch.uint8, device=dev)
+        # the adapters of a served layer may change, and the need with them
+        sizes = tuple((a.shape[0], a.shape[2]) for a in (ad.gate_up_a, ad.down_a)
+                      if a is not None)
+        if b.get("lora_sizes") != sizes:
+            need = max((B.moe_lora_workspace_size(T, self.kmax, self.E, n, r) for n, r in sizes),
+                       default=1)
+            if "lora_ws" not in b or b["lora_ws"].numel() < need:
+                # a captured graph may go on using the one outgrown
+                b.setdefault("lora_ws_outgrown", []).append(b.get("lora_ws"))
+                b["lora_ws"] = torch.empty(need, dtype=torch.uint8, device=dev)
+            b["lora_sizes"] = sizes
 
     def _route_scored(self, x, b, it):
         """Logits, scored selection and the grouping (empty slots allowed)."""

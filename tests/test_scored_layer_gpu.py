@@ -219,3 +219,31 @@ def test_router_grad_with_a_capacity_balances_what_was_chosen(cuda_lib, capacity
             num[t, e] = (sum(objective(hi)) - sum(objective(lo))) / 2e-5
     # fp32 sums over H = 256 in d_w, then the gradient's own 1e-5
     assert rel_l2(to_np(d_logits), num) <= 2e-5
+
+
+def test_adapters_of_a_served_layer_may_change(cuda_lib):
+    """Another set of adapters (more of them, a rank whose rows are grouped, a
+    pair that was missing) at a batch size already served: the same bits as a
+    layer made with them."""
+    T, E, k = 100, 8, 2
+    moe = cuda_lib
+
+    def layer_with(n, rank):
+        return make(moe, T, E, k, 256, 128, n, rank, moe.PATH_AUTO)
+
+    _, _, layer, small, x_bits, _ = layer_with(2, 8)
+    large_layer = layer_with(3, 64)[2]
+    large = large_layer.adapters
+    assert moe.moe_lora_workspace_size(T, k, E, 3, 64) > moe.moe_lora_workspace_size(T, k, E, 2, 8)
+    x = moe.bf16_from_bits(x_bits, dev())
+    ids = torch.arange(-1, T - 1, device=dev(), dtype=torch.int32) % 3
+    layer.adapters = moe.ExpertAdapters(down_a=small.down_a, down_b=small.down_b,
+                                        scales=small.scales)
+    layer(x, adapter_ids=ids % 2)
+    layer.adapters = small
+    layer(x, adapter_ids=ids % 2)
+    layer.adapters = large
+    assert torch.equal(layer(x, adapter_ids=ids), large_layer(x, adapter_ids=ids))
+    layer.adapters = small                      # and back
+    want = layer_with(2, 8)[2]
+    assert torch.equal(layer(x, adapter_ids=ids % 2), want(x, adapter_ids=ids % 2))
