@@ -168,7 +168,8 @@ class MoELayer:
         if adapters is not None and not self.fused:
             raise ValueError("adapters need the fused gate_up matrix")
         self._bufs = {}
-        self._last = None  # tokens of the last forward, for router_grad
+        # tokens of the last forward and whether it routed by scores, for router_grad
+        self._last, self._scored = None, False
 
     @classmethod
     def from_workload(cls, layer_inputs, device, batch: int = 0, **kw) -> "MoELayer":
@@ -269,13 +270,14 @@ class MoELayer:
                 y=torch.empty((A, self.H), dtype=self.y_storage(T), device=dev),
                 out=torch.empty((T, self.H), dtype=torch.bfloat16, device=dev),
             )
-            if self.scoring is not None:
-                bufs["logits"] = torch.empty((T, self.E), dtype=torch.float32, device=dev)
             if not self.fused:
                 bufs["g_raw"] = torch.empty((A, self.I), dtype=torch.float32, device=dev)
                 bufs["u_raw"] = torch.empty((A, self.I), dtype=torch.float32, device=dev)
             self._bufs[key] = bufs
-        return self._bufs[key]
+        bufs = self._bufs[key]
+        if self.scoring is not None and "logits" not in bufs:
+            bufs["logits"] = torch.empty((T, self.E), dtype=torch.float32, device=self.device)
+        return bufs
 
     def _adapter_buffers(self, b: dict, T: int) -> None:
         ad, dev = self.adapters, self.device
@@ -319,7 +321,7 @@ class MoELayer:
             if self.adapters is None:
                 raise ValueError("adapter_ids given to a layer without adapters")
             self._adapter_buffers(b, T)
-        self._last = T
+        self._last, self._scored = T, self.scoring is not None
         it = self.inv_temperature if inv_temperature is None else float(inv_temperature)
         # router, top-k and the expert grouping (one launch for small batches)
         ev = _Timer(events, "route")
@@ -425,6 +427,8 @@ class MoELayer:
             raise ValueError("router_grad needs a layer with scoring, after a forward")
         T = self._last
         b = self.buffers(T)
+        if not self._scored:
+            raise ValueError("router_grad needs a forward with the layer's scoring")
         if tuple(d_out.shape) != (T, self.H):
             raise ValueError(f"d_out must be {(T, self.H)}, got {tuple(d_out.shape)}")
         if T == 0:

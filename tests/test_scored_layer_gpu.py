@@ -247,3 +247,18 @@ def test_adapters_of_a_served_layer_may_change(cuda_lib):
     layer.adapters = small                      # and back
     want = layer_with(2, 8)[2]
     assert torch.equal(layer(x, adapter_ids=ids % 2), want(x, adapter_ids=ids % 2))
+
+
+def test_scoring_may_be_given_to_a_served_layer(cuda_lib):
+    _, layer_np, want, _, x_bits, _ = make(cuda_lib, 100, 8, 2, 256, 128, 2, 8,
+                                           cuda_lib.PATH_AUTO)
+    x = cuda_lib.bf16_from_bits(x_bits, dev())
+    plain = cuda_lib.MoELayer.from_workload(layer_np, dev())
+    plain(x)
+    with pytest.raises(ValueError):
+        plain.router_grad(x)
+    plain.scoring = want.scoring
+    with pytest.raises(ValueError):
+        plain.router_grad(x)                    # the last forward had no scores
+    assert torch.equal(plain(x), want(x))
+    plain.router_grad(x)
