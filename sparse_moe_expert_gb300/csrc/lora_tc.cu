@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_tc_kernel(
         xr[i] = r < tile.z ? p.x + (int64_t)pl.rows[tile.y + r].y * p.K + kb0 * 64 + c * 8 : nullptr;
       }
       const uint16_t* ar = p.a + ((int64_t)tile.x * p.R + r0) * p.K + kb0 * 64 + c * 8;
-      const int a_step = 32 * p.K;
+      const int64_t a_step = (int64_t)32 * p.K;
       // the next k-block -> stage s
       auto load = [&](int s) {
         unsigned char* at = smem + s * stage_bytes + sw128_offset(r0, c);
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_tc_kernel(
         for (int i = 0; i < (NT * 8 + 31) / 32; ++i) {
           const int r = r0 + 32 * i;
           if (r < RP)
-            cp_async16(at + kBlockBytes + i * 4096, r < p.R ? ar + (int64_t)i * a_step : p.a, r < p.R);
+            cp_async16(at + kBlockBytes + i * 4096, r < p.R ? ar + i * a_step : p.a, r < p.R);
         }
         ar += 64;
       };

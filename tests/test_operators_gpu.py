@@ -982,3 +982,24 @@ def test_route_scored_groups_of_cancelling_biases(cuda_lib, pad):
     ids, _, _ = cuda_lib.moe_route_scored(l_t, 2, score=1, select_bias=torch.tensor(bias, device=d),
                                           n_groups=2, topk_groups=1, group_top=2)
     assert np.array_equal(to_np(ids), np.stack([want, want + 1], 1))
+
+
+def test_lora_rows_of_a_that_pass_32_bits(cuda_lib):
+    """32 rows of A are 2^31 elements long: exact sums of single products at
+    both ends of K, ranks past 32 among them."""
+    T, K, N, R = 160, 1 << 26, 64, 40
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 30 GB")
+    d = dev()
+    x = torch.zeros((T, K), dtype=torch.bfloat16, device=d)
+    a = torch.zeros((1, R, K), dtype=torch.bfloat16, device=d)
+    rank = torch.arange(R, device=d)
+    at = torch.where(rank % 2 == 0, rank * 7, K - 1 - rank * 3)  # different columns
+    value = torch.randint(-8, 9, (T, R), device=d).bfloat16()
+    x[:, at] = value
+    a[0, rank, at] = 1.0
+    b = torch.randint(-2, 3, (1, N, R), device=d).bfloat16()
+    ids = torch.zeros(T, dtype=torch.int32, device=d)
+    base = torch.randint(-4, 5, (T, N), device=d).float()
+    got = cuda_lib.moe_lora_apply(x, ids, a, b, None, base)
+    assert torch.equal(got.double(), base.double() + value.double() @ b[0].double().t())
