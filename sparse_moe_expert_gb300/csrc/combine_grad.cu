@@ -178,7 +178,7 @@ extern "C" moe_status_t moe_combine_backward(const uint16_t* d_out, const void* 
   if (T < 0 || H <= 0 || H % 64 != 0 || kmax < 1 || kmax > 16) return MOE_ERR_INVALID_ARG;
   if ((int64_t)T * kmax > (1 << 24)) return MOE_ERR_INVALID_ARG;
   if (y_dtype != MOE_DTYPE_F32 && y_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
-  if (!k_dev) return MOE_ERR_INVALID_ARG;
+  if (!k_dev || !aligned4(k_dev)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   const void* ptrs[] = {d_out, y, inv_pos, topk_w, d_topk_w};
   for (const void* q : ptrs)

@@ -115,6 +115,7 @@ __device__ __forceinline__ unsigned lanemask_lt() {
 namespace moe_host {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Streaming multiprocessor count of the current device (cached per device).
 int sm_count();

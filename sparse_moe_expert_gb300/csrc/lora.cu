@@ -342,6 +342,9 @@ extern "C" moe_status_t moe_lora_apply(const uint16_t* x, int x_by_token,
   for (const void* q : ptrs)
     if (!q || !aligned16(q)) return MOE_ERR_INVALID_ARG;
   if (!adapter_ids || !aligned16(base)) return MOE_ERR_INVALID_ARG;
+  for (const void* q : {(const void*)adapter_ids, (const void*)topk_ids, (const void*)sorted_assign,
+                        (const void*)expert_offsets, (const void*)scales})
+    if (!aligned4(q)) return MOE_ERR_INVALID_ARG;
   if (swiglu && base == out) return MOE_ERR_INVALID_ARG;
   if (workspace_bytes < moe_lora_workspace_size(T, kmax, E, n_adapters, R))
     return MOE_ERR_INVALID_ARG;

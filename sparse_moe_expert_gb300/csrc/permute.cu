@@ -198,6 +198,11 @@ moe_status_t permute_impl(const int32_t* topk_ids, const int32_t* k_dev, int T, 
   if ((int64_t)T * kmax > (1 << 24)) return MOE_ERR_INVALID_ARG;
   if (!k_dev || !expert_counts || !expert_offsets) return MOE_ERR_INVALID_ARG;
   if (T > 0 && (!topk_ids || !sorted_assign || !inv_pos)) return MOE_ERR_INVALID_ARG;
+  for (const int32_t* q : {topk_ids, k_dev, static_cast<const int32_t*>(expert_counts),
+                           static_cast<const int32_t*>(expert_offsets),
+                           static_cast<const int32_t*>(sorted_assign),
+                           static_cast<const int32_t*>(inv_pos)})
+    if (!aligned4(q)) return MOE_ERR_INVALID_ARG;
   PermuteParams p;
   p.ids = topk_ids;
   p.k_dev = k_dev;

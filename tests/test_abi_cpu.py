@@ -235,3 +235,26 @@ def test_the_c_library_is_built_without_torch(monkeypatch, tmp_path):
     with pytest.raises(ImportError):
         _build.build()
     assert ctypes.CDLL(str(tmp_path / "lib.so")).moe_one() == 1
+
+
+def test_misaligned_integers_and_scales_are_refused(L):
+    """Arrays of 4-byte entries off their boundary, which the kernels could
+    only fault on."""
+    a = L.moe_lora_apply
+    good = [vp(GOOD), 1, vp(GOOD), vp(GOOD), vp(GOOD), vp(GOOD), 4, 2, 8, 3, 128, 128, 16,
+            vp(GOOD), vp(GOOD), vp(GOOD), vp(GOOD), 0, 0, 0, vp(GOOD), vp(GOOD), 1 << 30, None]
+    for i in (2, 3, 4, 5, 15):
+        for off in (1, 2, 3):
+            bad = list(good)
+            bad[i] = vp(GOOD + off)
+            assert a(*bad) == 1, i
+    c = L.moe_combine_backward
+    args = [vp(GOOD), vp(GOOD), 0, vp(GOOD), vp(GOOD), vp(GOOD + 2), 4, 2, 128, vp(GOOD), None,
+            None]
+    assert c(*args) == 1
+    m = L.moe_permute_masked
+    good = [vp(GOOD), vp(GOOD), 4, 2, 8, -1, vp(GOOD), vp(GOOD), vp(GOOD), vp(GOOD), None]
+    for i in (0, 1, 6, 7, 8, 9):
+        bad = list(good)
+        bad[i] = vp(GOOD + 2)
+        assert m(*bad) == 1, i
