@@ -266,9 +266,10 @@ __device__ __forceinline__ void wait_or_flag(uint64_t* bar, uint32_t parity, int
   }
 }
 
-// (large, small) tiles; never more than the list holds.
+// (large, small) tiles; never more than the list holds.  Past L1, which may
+// hold an earlier call's numbers where a kernel reads them before its wait.
 __device__ __forceinline__ int2 lora_tiles(const LoraPlan& pl) {
-  const int4 c = *pl.counts;
+  const int4 c = __ldcg(pl.counts);
   const int large = (int)min((int64_t)max(c.x, 0), pl.capacity);
   return make_int2(large, (int)min((int64_t)max(c.y, 0), pl.capacity - large));
 }
@@ -705,8 +706,8 @@ __global__ void __launch_bounds__(kExpandThreads* GROUPS, GROUPS > 1 ? 1 : BASE_
     }
   };
 
-  // The plan and base were complete before the kernel just before this one
-  // (the shrink) let it start: only v has to be waited for.
+  // The plan was complete before the kernel just before this one (the shrink)
+  // let it start: its first tile and that tile's rows of B need no wait.
   const int2 ntiles = lora_tiles(pl);
   // every CTA gets its share of the large units and of the small ones, which
   // take about as long for a fraction of the bytes
@@ -715,7 +716,7 @@ __global__ void __launch_bounds__(kExpandThreads* GROUPS, GROUPS > 1 ? 1 : BASE_
   int ti = (int)(u0 / chunks), col0 = (int)(u0 % chunks) * span;  // the unit, step by step
   int4 tile = make_int4(-1, 0, 0, 0);
   if (u0 < lend) {
-    tile = pl.tiles[ti];
+    tile = __ldcg(pl.tiles + ti);
     load_b(tile.x, col0, 0);
   }
   cp_async_commit();

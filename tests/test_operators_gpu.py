@@ -1003,3 +1003,61 @@ def test_lora_rows_of_a_that_pass_32_bits(cuda_lib):
     base = torch.randint(-4, 5, (T, N), device=d).float()
     got = cuda_lib.moe_lora_apply(x, ids, a, b, None, base)
     assert torch.equal(got.double(), base.double() + value.double() @ b[0].double().t())
+
+
+@pytest.mark.parametrize("E,k", [(1, 1), (16, 4)])
+def test_lora_calls_that_share_a_workspace(cuda_lib, E, k):
+    """Calls one behind the other on one workspace, their adapters and tile
+    lists different each time, eager and as a graph: each as when alone."""
+    T, K, N, R, n = 1500, 512, 384, 32, 6
+    d = dev()
+    g = torch.Generator(device=d)
+    g.manual_seed(E)
+    a = (torch.randn((n, E, R, K), generator=g, device=d) * K ** -0.5).bfloat16()
+    b = torch.randn((n, E, N, R), generator=g, device=d).bfloat16()
+    if E == 1:
+        a, b = a[:, 0], b[:, 0]
+    x = torch.randn((T, K), generator=g, device=d).bfloat16()
+    base = torch.randn((T * k, N), generator=g, device=d)
+    ws = torch.empty(cuda_lib.moe_lora_workspace_size(T, k, E, n, R), dtype=torch.uint8, device=d)
+    assert ws.numel() > 256                      # the grouped form
+    calls = []
+    for i in range(12):
+        # none, one, few or all adapters, more or fewer tiles each time
+        ids = torch.randint(-1, 1 + i % n, (T,), generator=g, device=d, dtype=torch.int32)
+        ids[: (i * 331) % T] = -1
+        kw = {}
+        if E > 1:
+            topk = torch.stack([torch.randperm(1 + (i % 4) * 5 if i % 4 else E, generator=g,
+                                               device=d)[:k] for _ in range(T)]) \
+                if i % 4 == 0 else torch.randint(0, 1 + (i % 4) * 5, (T, k), generator=g, device=d)
+            topk = topk.int().contiguous()
+            _, off, order, _ = cuda_lib.moe_permute_masked(
+                topk, torch.full((1,), k, dtype=torch.int32, device=d), E)
+            kw = dict(topk_ids=topk, sorted_assign=order, expert_offsets=off)
+        out = torch.empty_like(base)
+        calls.append((lambda ids=ids, kw=kw, out=out: cuda_lib.moe_lora_apply(
+            x, ids, a, b, None, base, out, workspace=ws, **kw), out))
+    want = []
+    for call, out in calls:
+        call()
+        torch.cuda.synchronize()
+        want.append(out.clone())
+
+    def check():
+        torch.cuda.synchronize()
+        assert all(torch.equal(out, ref) for (_, out), ref in zip(calls, want))
+
+    for _ in range(20):
+        for call, out in calls:
+            call()
+    check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for call, out in calls:
+            call()
+    for _, out in calls:
+        out.zero_()
+    for _ in range(20):
+        graph.replay()
+    check()
