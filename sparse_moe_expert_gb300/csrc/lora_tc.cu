@@ -348,6 +348,21 @@ __device__ __forceinline__ void shrink_small(const LoraParams& p, const LoraPlan
   }
 }
 
+// The values' next bf16 terms, which are taken off them.  A finite value past
+// bf16's largest number gives that one and leaves the rest; an infinity or a
+// NaN is its first term alone (what is left of it would be a NaN, and so would
+// the sum of its terms' products).
+__device__ __forceinline__ uint32_t take_term(float& lo, float& hi) {
+  constexpr float top = 0x1.FEp127f;
+  const bool l = fabsf(lo) < INFINITY, h = fabsf(hi) < INFINITY;
+  const uint32_t w = pack_bf16x2(l ? fminf(fmaxf(lo, -top), top) : lo,
+                                 h ? fminf(fmaxf(hi, -top), top) : hi);
+  const float2 f = bf16x2_to_f32x2(w);
+  lo = l ? lo - f.x : 0.0f;
+  hi = h ? hi - f.y : 0.0f;
+  return w;
+}
+
 // A cluster walks over the tiles, its CTAs each over their range of K; the
 // joined sums are scaled and stored as bf16 terms, ready for the expand.
 template <int NT>
@@ -509,13 +524,8 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_tc_kernel(
       }
       uint16_t* out = pl.terms + (int64_t)(tile.y + r) * terms * RP + j;
       for (int x = 0; x < terms; ++x) {
-        const uint32_t a = pack_bf16x2(f.x, f.y), b = pack_bf16x2(f.z, f.w);
+        const uint32_t a = take_term(f.x, f.y), b = take_term(f.z, f.w);
         *reinterpret_cast<uint2*>(out + x * RP) = make_uint2(a, b);
-        const float2 fa = bf16x2_to_f32x2(a), fb = bf16x2_to_f32x2(b);
-        f.x -= fa.x;
-        f.y -= fa.y;
-        f.z -= fb.x;
-        f.w -= fb.y;
       }
     }
     __syncthreads();

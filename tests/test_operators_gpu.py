@@ -1061,3 +1061,47 @@ def test_lora_calls_that_share_a_workspace(cuda_lib, E, k):
     for _ in range(20):
         graph.replay()
     check()
+
+
+@pytest.mark.parametrize("T,few", [(3, False), (20, False), (700, False), (110, True)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_lora_values_past_bf16_and_infinities(cuda_lib, T, few, dtype):
+    """One entry of x A^T overflows to an infinity, is a NaN, or is finite and
+    past bf16's largest number; the others are 0.  In every form (own rows,
+    small and large tiles): infinities of B's signs, NaN, and the product; the
+    other rows are as without them."""
+    K, N, R, n = 256, 128, 64, 2
+    d = dev()
+    g = torch.Generator(device=d)
+    g.manual_seed(T)
+    top = 2.0 ** 127
+    x = torch.zeros((T, K), device=d)
+    a = torch.zeros((n, R, K), device=d)
+    a[:, 0, :4] = 1.0
+    a[:, 1, 4] = 255.0 / 128
+    a[:, 1, 5] = 1.0
+    x[0, :4] = top                         # 4 x 2^127: +inf
+    x[1, :4] = -top                        # -inf
+    x[2, 4], x[2, 5] = top, 2.0 ** 119     # finite, past 255 x 2^120
+    if T > 3:
+        x[5, 0] = math.nan
+        x[4, 2] = 1.0
+    b = torch.randint(1, 4, (n, N, R), generator=g, device=d) * 1.0
+    b[:, ::3] *= -1.0
+    b[:, :, 1] = 2.0 ** -126
+    ids = torch.zeros(T, dtype=torch.int32, device=d)
+    ids[6::1 if few else 2] = 1            # few: these rows are a small tile
+    base = torch.randint(-3, 4, (T, N), generator=g, device=d).to(dtype)
+    got = cuda_lib.moe_lora_apply(x.bfloat16(), ids, a.bfloat16(), b.bfloat16(), None,
+                                  base).double()
+    sign = torch.where(b[0, :, 0] > 0, 1.0, -1.0).double()
+    assert torch.equal(got[0], sign * math.inf) and torch.equal(got[1], -sign * math.inf)
+    want = base.double()
+    want[2] += 255.0 / 64 + 2.0 ** -7
+    if T > 3:
+        assert got[5].isnan().all()
+        want[4] += b[0, :, 0].double()
+    rest = [i for i in range(T) if i not in (0, 1, 5)]
+    want = want[rest].to(dtype).double()
+    # exact sums of a few bits, but for the second product's own 2^-17 (bf16 base)
+    assert torch.allclose(got[rest], want, rtol=0 if dtype == torch.float32 else 2.0 ** -8, atol=0)
