@@ -1105,3 +1105,44 @@ def test_lora_values_past_bf16_and_infinities(cuda_lib, T, few, dtype):
     want = want[rest].to(dtype).double()
     # exact sums of a few bits, but for the second product's own 2^-17 (bf16 base)
     assert torch.allclose(got[rest], want, rtol=0 if dtype == torch.float32 else 2.0 ** -8, atol=0)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("E", [32, 96, 256])
+def test_route_backward_of_saturated_scores(cuda_lib, dtype, renorm, E):
+    """Every chosen expert's derivative to its own relative accuracy, logits
+    from -20 to 20.  Relative error of s (1 - s): e^-|l| has the roundings of
+    the exponent (two of |l| log2 e <= 29, times ln 2: 2.4e-6) and of the
+    hardware's exponential and reciprocal (2^-22 + 2^-23), then a few
+    roundings: 4e-6; renormalized, sums and a difference of terms of one size
+    on top: 1e-5.  bf16 logits: the fp32 result of the same numbers, rounded."""
+    T, k, scale = 9, 16, 2.5
+    g = np.random.default_rng(E)
+    l = np.stack([g.permutation(np.linspace(-20, 20, E)) for _ in range(T)])
+    l_t = torch.tensor(l, dtype=torch.float32, device=dev()).to(dtype).float()
+    l = l_t.double().cpu().numpy()
+    ids = np.stack([g.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    dw = np.float32(np.where(np.arange(k) % 2 == 0, 1.0, -1.0) * (1 + g.random((T, k))))
+
+    def grad(logits):
+        return cuda_lib.moe_route_scored_backward(
+            logits, torch.tensor(ids, device=dev()), torch.tensor(dw, device=dev()), score=1,
+            renormalize=renorm, scale=scale)[0]
+
+    got = grad(l_t)
+    if dtype == torch.bfloat16:
+        assert torch.equal(grad(l_t.to(dtype)), got.to(dtype))
+    s = 1 / (1 + np.exp(-l))
+    ds = scale * dw.astype(np.float64)
+    if renorm:
+        p = np.take_along_axis(s, ids, 1)
+        ds = (ds - (ds * p).sum(1, keepdims=True) / p.sum(1, keepdims=True)) / p.sum(1, keepdims=True)
+        ds[np.abs(ds) < 0.1 * np.abs(ds).max(1, keepdims=True)] = np.nan  # differences near 0
+    want = np.zeros_like(l)
+    np.put_along_axis(want, ids, ds, 1)
+    want *= s / (1 + np.exp(l))            # 1 - s without a difference
+    got = got.double().cpu().numpy()
+    on = ~np.isnan(want)
+    assert on.mean() > 0.8 and (np.abs(want[on & (l > 17)]) > 0).any()
+    assert np.allclose(got[on], want[on], rtol=1e-5 if renorm else 4e-6, atol=0)
