@@ -1146,3 +1146,22 @@ def test_route_backward_of_saturated_scores(cuda_lib, dtype, renorm, E):
     on = ~np.isnan(want)
     assert on.mean() > 0.8 and (np.abs(want[on & (l > 17)]) > 0).any()
     assert np.allclose(got[on], want[on], rtol=1e-5 if renorm else 4e-6, atol=0)
+
+
+@pytest.mark.parametrize("E,G,tg,k", [(256, 8, 4, 8), (60, 4, 2, 6), (33, 1, 1, 16)])
+@pytest.mark.parametrize("score", [0, 1])
+def test_route_scored_bits_do_not_depend_on_the_batch(cuda_lib, E, G, tg, k, score):
+    """Ids and weights of one token per warp step (few tokens) and of two
+    (many), bit for bit: a call of 8000 tokens against calls of 301."""
+    g = torch.Generator(device=dev())
+    g.manual_seed(E + score)
+    l = torch.randn((8000, E), generator=g, device=dev()) * 1.5
+    l[::7] = torch.round(l[::7])                              # ties
+    l[torch.rand(l.shape, generator=g, device=dev()) < 0.05] = -math.inf
+    l[100] = -math.inf
+    bias = torch.round(torch.randn(E, generator=g, device=dev()) * 20) * 0.001
+    kw = dict(k=k, score=score, select_bias=bias, n_groups=G, topk_groups=tg, scale=2.5)
+    ids, w, _ = cuda_lib.moe_route_scored(l, **kw)
+    few = [cuda_lib.moe_route_scored(l[i:i + 301], **kw) for i in range(0, 8000, 301)]
+    assert torch.equal(ids, torch.cat([f[0] for f in few]))
+    assert torch.equal(w, torch.cat([f[1] for f in few]))
