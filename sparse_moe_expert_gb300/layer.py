@@ -476,16 +476,25 @@ class MoELayer:
     __call__ = forward
 
     def forward_host(self, x_host: torch.Tensor, out_host: torch.Tensor,
-                     inv_temperature: Optional[float] = None) -> torch.Tensor:
+                     inv_temperature: Optional[float] = None,
+                     adapter_ids: Optional[torch.Tensor] = None) -> torch.Tensor:
         """End-to-end call with host buffers: copies x (pinned host, bf16
-        [T, H]) to the device, runs the layer and copies the result back into
-        out_host, all enqueued on the current stream (no synchronization)."""
+        [T, H]) and, if given, adapter_ids (pinned host, int32 [T]) to the
+        device, runs the layer and copies the result back into out_host, all
+        enqueued on the current stream (no synchronization)."""
         T = x_host.shape[0]
         b = self.buffers(T)
         if "x_dev" not in b:
             b["x_dev"] = torch.empty((T, self.H), dtype=torch.bfloat16, device=self.device)
         b["x_dev"].copy_(x_host, non_blocking=True)
-        res = self.forward(b["x_dev"], inv_temperature=inv_temperature)
+        if adapter_ids is not None:
+            if adapter_ids.dtype != torch.int32 or tuple(adapter_ids.shape) != (T,):
+                raise ValueError(f"adapter_ids must be int32 {(T,)}")
+            if "adapters_dev" not in b:
+                b["adapters_dev"] = torch.empty(T, dtype=torch.int32, device=self.device)
+            b["adapters_dev"].copy_(adapter_ids, non_blocking=True)
+            adapter_ids = b["adapters_dev"]
+        res = self.forward(b["x_dev"], inv_temperature=inv_temperature, adapter_ids=adapter_ids)
         out_host.copy_(res, non_blocking=True)
         return out_host
 

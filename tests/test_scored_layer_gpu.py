@@ -262,3 +262,23 @@ def test_scoring_may_be_given_to_a_served_layer(cuda_lib):
         plain.router_grad(x)                    # the last forward had no scores
     assert torch.equal(plain(x), want(x))
     plain.router_grad(x)
+
+
+def test_host_buffers_with_adapters(cuda_lib):
+    """forward_host with each token's adapter: the bits of forward; wrong ids
+    are refused."""
+    T = 37
+    _, _, layer, _, x_bits, ids = make(cuda_lib, T, 16, 4, 512, 192, 5, 16, cuda_lib.PATH_AUTO)
+    x_host = cuda_lib.bf16_from_bits(x_bits, pin=True)
+    ids_host = torch.tensor(ids).pin_memory()
+    out = torch.empty((T, 512), dtype=torch.bfloat16).pin_memory()
+    plain = torch.empty_like(out).pin_memory()
+    layer.forward_host(x_host, out, adapter_ids=ids_host)
+    layer.forward_host(x_host, plain)
+    torch.cuda.synchronize()
+    x = x_host.to(dev())
+    assert torch.equal(out, layer(x, adapter_ids=ids_host.to(dev())).cpu())
+    assert torch.equal(plain, layer(x).cpu()) and not torch.equal(out, plain)
+    for bad in (ids_host.long(), ids_host[:5]):
+        with pytest.raises(ValueError):
+            layer.forward_host(x_host, out, adapter_ids=bad)
