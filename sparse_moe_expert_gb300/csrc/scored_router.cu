@@ -328,12 +328,16 @@ __device__ __forceinline__ void lane_top2(const float (&c)[V], float& a1, float&
 // by counting, and the lanes with rank < k are the answer.  Groups are cut on
 // c~ too when the cut is wider than the approximation.  More than 16
 // candidates (many equal choices) and groups too close to call go to
-// route_token_exact; results do not depend on which way was taken.
+// route_token_exact.  The ids do not depend on which way was taken; the sum that
+// renormalizes the weights runs over the candidates here and in rank order
+// there, so their last bit may.
 //
-// Bound by the issue rate: some 550 instructions per token of 256 experts
-// (issue slots 69 % used, ALU 58 %).  Measured, k 8 of 256 bf16 experts in 8
-// groups, 65536 tokens: 44 us (37.7 MB: 6 us at the copy rate); with exact
-// scores for every expert and k rounds of argmax 93 us; 64 experts 21 us.  A
+// Bound by the issue rate: some 560 instructions per token of 256 experts
+// (issue slots 70 % used, ALU 61 %).  Measured, k 8 of 256 bf16 experts in 8
+// groups, 65536 tokens: 45 us (37.7 MB: 6 us at the copy rate); with exact
+// scores for every expert and k rounds of argmax 93 us; 64 experts 21 us.  For
+// the CTAs per SM, V = 32 (more than 512 experts) spills 130-160 bytes a
+// thread, V = 8 without LANES 40, the other V 4 or none.  A
 // lane per token (rows in shared memory) was no faster: 47 us, 83 us for fp32
 // rows, whose 32 rows per warp leave few warps.
 //
@@ -618,6 +622,12 @@ __device__ __forceinline__ float sigmoid_slope(float l, float& slope) {
 // it.  The hardware exponential and reciprocal are good to a few 1e-7 here,
 // far inside the rounding of the differences they enter.  The chosen slots'
 // d u meets its expert's lane through a row of shared memory per warp.
+//
+// Bound by the issue rate and the shuffles' latency: some 370 instructions per
+// token of 256 experts, issue slots 61 % used.  Measured, 32768 x 256 bf16,
+// sigmoid: 18.4 us (35.7 MB: 5.3 at the copy rate; with s - s^2 for the
+// sigmoid's slope 17.8), softmax 16.1; 4096 x 128 fp32, softmax 4.0 with the
+// losses' kernel.
 constexpr int grad_ctas_per_sm(int V) { return V <= 4 ? 4 : V <= 16 ? 2 : 1; }
 
 template <int V, bool BF16, bool SIGMOID>
