@@ -655,6 +655,165 @@ moe_status_t moe_lora_apply(const uint16_t* x, int x_by_token, const int32_t* ad
                             int base_dtype, int epilogue, int out_dtype, void* out,
                             void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * moe_layer_norm -- layer norm or RMS norm of rows, after an optional sum.
+ *
+ * Page [B], section 3 (the norms of a block and of its experts).  For row t:
+ *   s    = x[t] (+ residual[t]; the sum is rounded to x's type, stored in
+ *          `summed`, and normed as stored)
+ *   mu   = mean of s (MOE_NORM_RMS: 0)
+ *   rstd = 1 / sqrt(mean of (s - mu)^2 + eps)
+ *   out  = (s - mu) * rstd * weight + bias
+ * in fp32, sums in an order that T and H fix.
+ *
+ * x, residual  [T, H] of x_dtype, rows ld_x and ld_residual elements apart
+ *              (>= H); residual may be NULL.
+ * weight, bias [H] of weight_dtype; either may be NULL (1 and 0).
+ * out          [T, H] of out_dtype; summed [T, H] of x_dtype, needed with a
+ *              residual and untouched without.  Dense rows.  out may be x, and
+ *              summed x or residual, where type and rows are the same.
+ * mean, rstd   fp32 [T] out, or NULL: what the gradient needs (RMS: mean 0).
+ * 1 <= H <= 8192; eps finite and not negative.  Tensors are aligned to their
+ * type; rows of whole 16-byte pieces at 16-byte aligned addresses are fastest.
+ * ---------------------------------------------------------------------- */
+enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 };
+moe_status_t moe_layer_norm(const void* x, int x_dtype, int64_t ld_x, const void* residual,
+                            int64_t ld_residual, const void* weight, const void* bias,
+                            int weight_dtype, int T, int H, int kind, float eps, int out_dtype,
+                            void* out, void* summed, float* mean, float* rstd,
+                            moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * moe_layer_norm_backward -- gradient of moe_layer_norm.
+ *
+ * With xh = (x - mean) * rstd and c = d_out * weight, per row
+ *   d_x      = rstd * (c - mean(c) - xh * mean(c * xh)) + d_sum
+ *   d_weight = sum_t d_out * xh,   d_bias = sum_t d_out      (fp32)
+ * where x is the normed sum (`summed` of the forward call, x without a
+ * residual) and d_x is the gradient of both x and residual.  mean NULL: RMS
+ * (no mean(c) term).
+ *
+ * d_out  [T, H] of d_dtype, rows ld_d apart; x [T, H] of x_dtype, rows ld_x
+ *        apart; d_sum [T, H] of x_dtype, rows ld_sum apart, or NULL: gradient
+ *        that reaches the sum elsewhere (the residual stream).
+ * mean, rstd  fp32 [T] of the forward call.
+ * d_x    [T, H] of x_dtype, dense; may be d_out, x or d_sum where type and rows
+ *        are the same.
+ * d_weight, d_bias  fp32 [H], or NULL.  Written, not added to (zeros for T = 0).
+ * workspace   moe_layer_norm_workspace_size(T, H) bytes of device scratch,
+ *        16-byte aligned, for d_weight or d_bias.
+ * ---------------------------------------------------------------------- */
+size_t moe_layer_norm_workspace_size(int T, int H);
+
+moe_status_t moe_layer_norm_backward(const void* d_out, int d_dtype, int64_t ld_d, const void* x,
+                                     int x_dtype, int64_t ld_x, const float* mean,
+                                     const float* rstd, const void* weight, int weight_dtype,
+                                     const void* d_sum, int64_t ld_sum, int T, int H, void* d_x,
+                                     float* d_weight, float* d_bias, void* workspace,
+                                     size_t workspace_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * moe_adamw_step -- one AdamW step over many tensors, states in 32 or 8 bits.
+ *
+ * For each tensor, element by element in fp32, t = step[0] + 1:
+ *   g = grad * grad_scale
+ *   m = beta1 m + (1 - beta1) g;   v = beta2 v + (1 - beta2) g^2
+ *   w = w (1 - lr wd) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * w is `master` where given and param then w rounded to bf16; else param.
+ * With state_bits 8, blocks of 256 consecutive elements share a scale:
+ *   exp_avg    int8 c:  m = scale * sign(c) * (c / 127)^2
+ *   exp_avg_sq uint8 c: sqrt(v) = scale * (c / 255)^2, c >= 1 where v > 0
+ * coded after the step has used m and v; scales are fp32 [ceil(n / 256)].  A
+ * value that is not finite makes its block's states NaN.
+ *
+ * tensors     host array (read before the call returns).  The tensors are
+ *             different memory and do not overlap; the same param twice is refused.
+ * param_dtype, grad_dtype  fp32 or bf16, for all tensors; masters for all
+ *             tensors or none, and only beside bf16 params.
+ * lr_dev      device scalar that takes lr's place, or NULL (a captured graph
+ *             then follows a schedule).
+ * grad_scale  device scalar, or NULL (1).  One that is not finite skips the
+ *             step: nothing is written, the step is not counted.
+ * step        int32 [2] on the device: steps done, and 0 (scratch of a running
+ *             call).  The call adds 1 to the first.
+ * Tensors are aligned to their type; 16-byte aligned ones are fastest.
+ *
+ * moe_adamw_values -- the fp32 values that eight-bit states stand for (m and
+ * v), the tensors one after the other in `exp_avg` and `exp_avg_sq`; of the
+ * table it reads exp_avg, exp_avg_sq, their scales and n.
+ * ---------------------------------------------------------------------- */
+typedef struct moe_adamw_tensor {
+  void* param;
+  const void* grad;
+  float* master;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* exp_avg_scale;
+  float* exp_avg_sq_scale;
+  int64_t n;
+  float weight_decay;
+} moe_adamw_tensor_t;
+
+moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int count, int param_dtype,
+                            int grad_dtype, int state_bits, double lr, const float* lr_dev,
+                            double beta1, double beta2, double eps, const float* grad_scale,
+                            int32_t* step, moe_stream_t stream);
+moe_status_t moe_adamw_values(const moe_adamw_tensor_t* tensors, int count, float* exp_avg,
+                              float* exp_avg_sq, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * moe_linear -- a dense product with bias, activation and residual: the expert
+ * that every token passes beside the routed ones, or any projection.
+ *
+ * Page [B], section 4 (shared experts; prose).  With z = x W^T + bias:
+ *   MOE_ACT_NONE    out = z
+ *   MOE_ACT_SILU    out = z / (1 + e^-z)
+ *   MOE_ACT_GELU    out = z Phi(z), Phi the normal distribution function
+ *   MOE_ACT_SWIGLU  out[t, n] = SiLU(z[t, n]) * z[t, N/2 + n]  (gate rows first)
+ * plus residual.  bf16 factors, fp32 sums (on the tensor cores: in an order and
+ * with the rounding of their accumulators), one rounding at the end.
+ *
+ * x         bf16 [T, K], rows ld_x elements apart (a multiple of 8, >= K).
+ * w         bf16 [N, K] dense; x and w 16-byte aligned.
+ * bias      fp32 [N], or NULL.
+ * residual  [T, cols] of out_dtype, or NULL; may be out (in place).
+ * out       [T, cols] of out_dtype; cols = N, with SWIGLU N / 2.
+ * preact    out: bf16 [T, N], z rounded, for the gradient; or NULL.
+ * K % 8 == 0, K >= 8; N >= 1, even with SWIGLU.  Outputs are aligned to their
+ * type; cols a multiple of 8 and 16-byte aligned outputs are fastest.
+ * ---------------------------------------------------------------------- */
+enum { MOE_ACT_NONE = 0, MOE_ACT_SILU = 1, MOE_ACT_GELU = 2, MOE_ACT_SWIGLU = 3 };
+moe_status_t moe_linear(const uint16_t* x, int64_t ld_x, const uint16_t* w, const float* bias,
+                        const void* residual, int T, int K, int N, int activation, int out_dtype,
+                        void* out, uint16_t* preact, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * moe_linear_backward -- gradient of moe_linear (the residual's is d_out).
+ *
+ *   d_z    = d_out * act'(z)   (SWIGLU: both halves), held in bf16 like z
+ *   d_bias = sum_t d_z         (of the values before that rounding)
+ *   d_x    = d_z W,   d_w = d_z^T x (+ d_w with accumulate)
+ *
+ * d_out     [T, cols] of d_dtype, rows ld_d apart.
+ * preact    bf16 [T, N] of the forward call; not needed for MOE_ACT_NONE.
+ * d_preact  out: bf16 [T, N], rows ld_dp apart (a multiple of 8, >= N), 16-byte
+ *           aligned.  Not written, and may be NULL, where d_out is d_z as it
+ *           stands: MOE_ACT_NONE, bf16, 16-byte aligned, ld_d a multiple of 8.
+ * d_x       bf16 [T, K], d_w [N, K] of d_w_dtype, d_bias fp32 [N]: out, each
+ *           NULL if not wanted.  Zeros for T = 0 (d_w with accumulate: as it was).
+ * workspace moe_linear_backward_workspace_size(T, N, activation) bytes of
+ *           device scratch, 16-byte aligned, for d_bias.
+ * No output may overlap an input.  x, w, K, N as in moe_linear.
+ * ---------------------------------------------------------------------- */
+size_t moe_linear_backward_workspace_size(int T, int N, int activation);
+
+moe_status_t moe_linear_backward(const void* d_out, int d_dtype, int64_t ld_d, const uint16_t* x,
+                                 int64_t ld_x, const uint16_t* w, const uint16_t* preact, int T,
+                                 int K, int N, int activation, uint16_t* d_preact, int64_t ld_dp,
+                                 uint16_t* d_x, void* d_w, int d_w_dtype, int accumulate,
+                                 float* d_bias, void* workspace, size_t workspace_bytes,
+                                 moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -25,6 +25,9 @@ def path_k_range(lo: int, hi: int) -> int:
 DEVERR_BAD_EXPERT, DEVERR_TIMEOUT, DEVERR_BAD_INDEX = 1, 2, 4
 DEVERR_BAD_SCORE, DEVERR_BAD_ADAPTER = 8, 16
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+NORM_LAYER, NORM_RMS = 0, 1
+ACT_NONE, ACT_SILU, ACT_GELU, ACT_SWIGLU = 0, 1, 2, 3
+ADAMW_BLOCK = 256  # consecutive elements that share a scale of the 8-bit states
 DROPPED = -2  # inv_pos of an assignment dropped by its expert's capacity
 QMODE_AFFINE = 0
 SCALE_F16, SCALE_BF16, SCALE_F32 = 0, 1, 2
@@ -38,6 +41,9 @@ EXPORTS = (
     "moe_router_logits", "moe_route_scored", "moe_route_scored_backward",
     "moe_route_backward_workspace_size", "moe_permute_masked", "moe_combine_backward",
     "moe_lora_workspace_size", "moe_lora_apply",
+    "moe_layer_norm", "moe_layer_norm_workspace_size", "moe_layer_norm_backward",
+    "moe_adamw_step", "moe_adamw_values",
+    "moe_linear", "moe_linear_backward", "moe_linear_backward_workspace_size",
 )
 
 
@@ -54,6 +60,14 @@ class QDesc(ctypes.Structure):
                 ("cols", ctypes.c_int32), ("scale_dtype", ctypes.c_int32)]
 
 
+class AdamWTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("master", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p),
+                ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p),
+                ("exp_avg_sq_scale", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("weight_decay", ctypes.c_float)]
+
+
 _LIB = None
 
 vp = ctypes.c_void_p
@@ -61,6 +75,7 @@ i32 = ctypes.c_int
 f32 = ctypes.c_float
 sz = ctypes.c_size_t
 i64 = ctypes.c_int64
+f64 = ctypes.c_double
 
 
 def _declare(lib):
@@ -108,6 +123,20 @@ def _declare(lib):
     lib.moe_lora_workspace_size.restype = sz
     lib.moe_lora_apply.argtypes = [vp, i32, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, vp,
                                    vp, vp, vp, i32, i32, i32, vp, vp, sz, vp]
+    lib.moe_layer_norm.argtypes = [vp, i32, i64, vp, i64, vp, vp, i32, i32, i32, i32, f32, i32, vp,
+                                   vp, vp, vp, vp]
+    lib.moe_layer_norm_workspace_size.argtypes = [i32, i32]
+    lib.moe_layer_norm_workspace_size.restype = sz
+    lib.moe_layer_norm_backward.argtypes = [vp, i32, i64, vp, i32, i64, vp, vp, vp, i32, vp, i64,
+                                            i32, i32, vp, vp, vp, vp, sz, vp]
+    lib.moe_adamw_step.argtypes = [ctypes.POINTER(AdamWTensor), i32, i32, i32, i32, f64, vp, f64,
+                                   f64, f64, vp, vp, vp]
+    lib.moe_adamw_values.argtypes = [ctypes.POINTER(AdamWTensor), i32, vp, vp, vp]
+    lib.moe_linear.argtypes = [vp, i64, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp]
+    lib.moe_linear_backward_workspace_size.argtypes = [i32, i32, i32]
+    lib.moe_linear_backward_workspace_size.restype = sz
+    lib.moe_linear_backward.argtypes = [vp, i32, i64, vp, i64, vp, vp, i32, i32, i32, i32, vp, i64,
+                                        vp, vp, i32, i32, vp, vp, sz, vp]
     for name in ("moe_pack_gate_up", "moe_router_topk", "moe_router_topk_noalloc", "moe_route",
                  "moe_route_grouped", "moe_permute_capped",
                  "moe_permute", "moe_permute_rows", "moe_gate_up_qmm",
@@ -115,7 +144,8 @@ def _declare(lib):
                  "moe_selftest_wait_timeout", "moe_expert_counts_accumulate",
                  "moe_expert_health", "moe_router_logits", "moe_route_scored",
                  "moe_route_scored_backward", "moe_permute_masked", "moe_combine_backward",
-                 "moe_lora_apply"):
+                 "moe_lora_apply", "moe_layer_norm", "moe_layer_norm_backward", "moe_adamw_step",
+                 "moe_adamw_values", "moe_linear", "moe_linear_backward"):
         getattr(lib, name).restype = i32
 
 

@@ -492,3 +492,142 @@ def moe_lora_apply(x, adapter_ids, lora_a, lora_b, scales=None, base=None, out=N
         _hold(stream, (x, adapter_ids, lora_a, lora_b, scales, base, topk_ids, sorted_assign,
                        expert_offsets), r)
     return r[0]
+
+
+# ---- norms and the optimizer -------------------------------------------------
+
+
+def _raw(stream):
+    return None if stream is None else stream.cuda_stream
+
+
+def moe_layer_norm(x, weight=None, bias=None, residual=None, eps: float = 1e-6,
+                   kind: int = _lib.NORM_LAYER, need_stats: bool = False, out_dtype=None, out=None,
+                   summed=None, mean=None, rstd=None, stream=None):
+    """Layer norm (NORM_LAYER) or RMS norm (NORM_RMS) of the rows of x [T, H]
+    (fp32 or bf16, rows may be strided) -> (out, summed, mean, rstd).
+
+    With ``residual`` the sum x + residual, rounded to x's type, is normed and
+    returned as ``summed`` (else None).  weight and bias [H] are fp32 or bf16.
+    need_stats (or buffers for them) gives mean and rstd fp32 [T] for the
+    gradient; RMS has no mean unless a buffer is given (zeros).  ``out`` may be
+    x, ``summed`` x or residual: in place."""
+    if out_dtype is not None:
+        if out_dtype not in _DT:
+            raise ValueError(f"out_dtype must be float32 or bfloat16, got {out_dtype}")
+        out_dtype = out_dtype is torch.bfloat16
+    r = native().layer_norm(x, weight, bias, residual, eps, kind, out_dtype, need_stats, out, summed,
+                            mean, rstd, _raw(stream))
+    if r.__class__ is int:
+        check("moe_layer_norm", r)
+    if stream is not None:
+        _hold(stream, (x, weight, bias, residual), r)
+    return r
+
+
+def moe_layer_norm_workspace_size(T: int, H: int) -> int:
+    return int(lib().moe_layer_norm_workspace_size(T, H))
+
+
+def moe_layer_norm_backward(d_out, x, rstd, mean=None, weight=None, d_sum=None,
+                            kind: int = _lib.NORM_LAYER, need_d_weight: bool = True,
+                            need_d_bias: bool = True, d_x=None, d_weight=None, d_bias=None,
+                            workspace=None, stream=None):
+    """Gradient of moe_layer_norm -> (d_x like x, d_weight, d_bias f32 [H] or None).
+
+    ``x`` is what was normed (``summed`` where there was a residual), ``d_sum``
+    a gradient that reaches it elsewhere; d_x is the gradient of x and of the
+    residual.  ``mean`` belongs to NORM_LAYER and is None for NORM_RMS."""
+    r = native().layer_norm_backward(d_out, x, rstd, mean, weight, d_sum, kind, need_d_weight,
+                                     need_d_bias, d_x, d_weight, d_bias, workspace, _raw(stream))
+    if r.__class__ is int:
+        check("moe_layer_norm_backward", r)
+    if stream is not None:
+        _hold(stream, (d_out, x, rstd, mean, weight, d_sum), r)
+    return r[:3]
+
+
+def moe_linear(x, w, bias=None, residual=None, activation: int = _lib.ACT_NONE, out=None,
+               out_dtype=None, need_preact: bool = False, preact=None, stream=None):
+    """out = activation(x w^T + bias) + residual -> (out, preact or None).
+
+    x bf16 [T, K] (rows may be strided, 16-byte aligned), w bf16 [N, K], bias
+    fp32 [N], residual and out [T, cols] of one type (bf16 unless residual, out or
+    out_dtype says fp32); cols is N, with ACT_SWIGLU N / 2 (gate rows first).
+    ``out`` may be residual.  need_preact (or a buffer) gives x w^T + bias in
+    bf16 [T, N], which the gradient of an activation needs."""
+    if out_dtype is not None:
+        if out_dtype not in _DT:
+            raise ValueError(f"out_dtype must be float32 or bfloat16, got {out_dtype}")
+        out_dtype = out_dtype is torch.bfloat16
+    r = native().linear(x, w, bias, residual, activation, out, out_dtype, need_preact, preact,
+                        _raw(stream))
+    if r.__class__ is int:
+        check("moe_linear", r)
+    if stream is not None:
+        _hold(stream, (x, w, bias, residual), r)
+    return r
+
+
+def moe_linear_backward_workspace_size(T: int, N: int, activation: int = _lib.ACT_NONE) -> int:
+    return int(lib().moe_linear_backward_workspace_size(T, N, activation))
+
+
+def moe_linear_backward(d_out, x, w, preact=None, activation: int = _lib.ACT_NONE,
+                        need_d_x: bool = True, need_d_w: bool = True, need_d_bias: bool = True,
+                        d_x=None, d_w=None, d_w_dtype=None, accumulate: bool = False, d_bias=None,
+                        workspace=None, stream=None):
+    """Gradient of moe_linear -> (d_x bf16 [T, K], d_w [N, K], d_bias f32 [N],
+    d_preact bf16 [T, N]); what is not wanted is None.
+
+    d_out is the residual's gradient as it stands.  d_w is fp32 unless d_w or
+    d_w_dtype says bf16; with accumulate d_w is added to.  d_preact is d_out itself
+    where there is no activation and d_out is bf16 with 16-byte aligned rows."""
+    if d_w_dtype is not None:
+        if d_w_dtype not in _DT:
+            raise ValueError(f"d_w_dtype must be float32 or bfloat16, got {d_w_dtype}")
+        d_w_dtype = d_w_dtype is torch.bfloat16
+    r = native().linear_backward(d_out, x, w, preact, activation, need_d_x, need_d_w, need_d_bias, d_x,
+                                 d_w, d_w_dtype, accumulate, d_bias, workspace, _raw(stream))
+    if r.__class__ is int:
+        check("moe_linear_backward", r)
+    if stream is not None:
+        _hold(stream, (d_out, x, w, preact), r)
+    return r[:4]
+
+
+def moe_adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, beta1: float = 0.9,
+                   beta2: float = 0.999, eps: float = 1e-8, weight_decay=0.0, masters=None,
+                   exp_avg_scales=None, exp_avg_sq_scales=None, grad_scale=None, stream=None):
+    """One AdamW step over lists of dense tensors, in place.
+
+    params: all fp32, or all bf16 (with fp32 ``masters``, of which they are the
+    rounding, or without); grads all fp32 or all bf16.  States are fp32, or
+    int8 ``exp_avg`` and uint8 ``exp_avg_sq`` with fp32 scales, one per
+    ADAMW_BLOCK elements.  ``step`` int32 [2] on the device holds the steps
+    done and 0; the call counts one.  ``lr`` is a number or an fp32 tensor of one
+    element on the device, ``weight_decay`` a number or one for each tensor.
+    ``grad_scale`` (fp32, one element) multiplies the gradients; one that is
+    not finite skips the step."""
+    lr_dev = None
+    if isinstance(lr, torch.Tensor):
+        lr, lr_dev = 0.0, lr
+    r = native().adamw_step(params, grads, exp_avg, exp_avg_sq, exp_avg_scales, exp_avg_sq_scales,
+                            masters, step, lr, lr_dev, beta1, beta2, eps, weight_decay, grad_scale,
+                            _raw(stream))
+    if r is not None:
+        check("moe_adamw_step", r)
+    if stream is not None:
+        lists = (params, grads, exp_avg, exp_avg_sq, exp_avg_scales, exp_avg_sq_scales, masters)
+        _hold(stream, [t for ts in lists if ts for t in ts] + [step, lr_dev, grad_scale], ())
+
+
+def moe_adamw_values(exp_avg, exp_avg_sq, exp_avg_scales, exp_avg_sq_scales, stream=None):
+    """-> (m, v): the fp32 values that 8-bit states stand for, the tensors of
+    the lists one after the other."""
+    r = native().adamw_values(exp_avg, exp_avg_sq, exp_avg_scales, exp_avg_sq_scales, _raw(stream))
+    if r.__class__ is int:
+        check("moe_adamw_values", r)
+    if stream is not None:
+        _hold(stream, (*exp_avg, *exp_avg_sq, *exp_avg_scales, *exp_avg_sq_scales), r)
+    return r

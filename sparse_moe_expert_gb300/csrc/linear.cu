@@ -1,0 +1,275 @@
+// The dense product out = act(x W^T + bias) + residual on the tensor cores, and
+// the products of its gradient, which are the same sums over other axes:
+//   forward  D[t, n] = sum_k x[t, k] W[n, k]       both operands in rows of k
+//   d_x      D[t, k] = sum_n d_z[t, n] W[n, k]     W by columns
+//   d_w      D[n, k] = sum_t d_z[t, n] x[t, k]     both by columns
+// tcgen05 takes either order from shared memory (the descriptors say which), so
+// nothing is transposed.
+#include "linear.cuh"
+
+#include "lora.cuh"
+
+namespace moe {
+
+bool make_tensor_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner,
+                        uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
+                        CUtensorMapSwizzle sw);
+
+bool linear_map(CUtensorMap* m, const LinearOp& op, int rows, int K, int box_rows) {
+  const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  return op.row_major
+             ? make_tensor_map_2d(m, bf16, op.p, K, rows, (uint64_t)op.ld * 2, kLinBK, box_rows, sw)
+             : make_tensor_map_2d(m, bf16, op.p, rows, K, (uint64_t)op.ld * 2, 64, kLinBK, sw);
+}
+
+namespace {
+
+// ---- one tile per CTA, K shared by a cluster -----------------------------------
+//
+// 128 x BN tiles.  A cluster of `splits` CTAs takes a tile, each CTA a run of K;
+// the sums meet in shared memory and are added in rank order, each CTA a share
+// of the rows.
+
+constexpr int kTileThreads = 256;
+constexpr int kTileM = 128;
+constexpr int kTileMaxSplit = 8;
+__host__ __device__ constexpr int tile_stages(int BN) { return BN == 64 ? 4 : 3; }
+__host__ __device__ constexpr int tile_stage_bytes(int BN) { return (kTileM + BN) * 128; }
+constexpr size_t tile_smem(int BN) {
+  const size_t ring = (size_t)tile_stages(BN) * tile_stage_bytes(BN);
+  const size_t sums = (size_t)kTileM * (BN + 4) * 4;
+  return (ring > sums ? ring : sums) + 1024;
+}
+
+template <int BN, bool A_ROW, bool B_ROW, bool SWIGLU>
+__global__ void __launch_bounds__(kTileThreads, 2)
+    linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                       LinearEpi e, int K, int splits, int m_tiles, unsigned int* err) {
+  constexpr int kStages = tile_stages(BN);
+  constexpr int kStageBytes = tile_stage_bytes(BN);
+  constexpr int kOut = SWIGLU ? BN / 2 : BN;  // output columns of the tile
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t full[kStages], empty[kStages], done;
+  __shared__ uint32_t tmem_sh;
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = blockIdx.x % splits, tile = blockIdx.x / splits;
+  const int row0 = tile % m_tiles * kTileM, col0 = tile / m_tiles * kOut;
+  const int nkb = (K + kLinBK - 1) / kLinBK;
+  const int kb0 = (int)((int64_t)rank * nkb / splits);
+  const int nb = (int)((int64_t)(rank + 1) * nkb / splits) - kb0;
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&done, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_sh, BN);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_wait();
+  pdl_trigger();  // after the allocation: a later kernel may not take TMEM from a CTA still to come
+  const uint32_t tmem = tmem_sh;
+  int bad = 0;
+  if (warp == 0) {
+    int issued = 0;
+    for (int kb = 0; kb < nb; ++kb) {
+      const int s = kb % kStages;
+      if (kb >= kStages) {
+        bad |= !mbar_wait_sleep(&empty[s], (uint32_t)(kb / kStages - 1) & 1u, kWaitBudgetCycles);
+        if (__any_sync(0xFFFFFFFFu, bad)) {
+          bad = 1;
+          break;
+        }
+      }
+      if (lane == 0) {
+        unsigned char* a = smem + s * kStageBytes;
+        unsigned char* b = a + kTileM * 128;
+        const int k = (kb0 + kb) * kLinBK;
+        mbar_arrive_expect_tx(&full[s], kStageBytes);
+        if constexpr (A_ROW) {
+          linear_tma_2d(a, &tm_a, k, row0, &full[s]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kTileM / 64; ++j) linear_tma_2d(a + j * 8192, &tm_a, row0 + j * 64, k, &full[s]);
+        }
+        if constexpr (SWIGLU) {
+          linear_tma_2d(b, &tm_b, k, col0, &full[s]);
+          linear_tma_2d(b + kOut * 128, &tm_b, k, e.cols + col0, &full[s]);
+        } else if constexpr (B_ROW) {
+          linear_tma_2d(b, &tm_b, k, col0, &full[s]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < BN / 64; ++j) linear_tma_2d(b + j * 8192, &tm_b, col0 + j * 64, k, &full[s]);
+        }
+      }
+      issued = kb + 1;
+    }
+    if (bad)  // copies in flight end before the CTA may
+      for (int kb = issued > kStages ? issued - kStages : 0; kb < issued; ++kb)
+        mbar_wait_sleep(&full[kb % kStages], (uint32_t)(kb / kStages) & 1u, kWaitBudgetCycles);
+  } else if (warp == 1) {
+    const uint32_t idesc = idesc_linear<A_ROW, B_ROW>(kTileM, BN);
+    for (int kb = 0; kb < nb; ++kb) {
+      const int s = kb % kStages;
+      bad |= !mbar_wait_sleep(&full[s], (uint32_t)(kb / kStages) & 1u, kWaitBudgetCycles);
+      if (__any_sync(0xFFFFFFFFu, bad)) {
+        bad = 1;
+        break;
+      }
+      tc_fence_after();
+      const uint64_t ad = operand_desc<A_ROW>(smem + s * kStageBytes);
+      const uint64_t bd = operand_desc<B_ROW>(smem + s * kStageBytes + kTileM * 128);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        umma_bf16(tmem, ad + k * operand_step<A_ROW>(), bd + k * operand_step<B_ROW>(), idesc,
+                  kb > 0 || k > 0);
+      umma_commit(&empty[s]);
+    }
+    umma_commit(&done);
+    bad |= !mbar_wait_sleep(&done, 0u, kWaitBudgetCycles);
+  }
+  __syncwarp();
+  bad = __syncthreads_or(bad);
+  if (bad && tid == 0) raise_device_error(err, MOE_DEVERR_TIMEOUT);
+  tc_fence_after();
+  // the ring is free: the sums take its place, [row][BN + 4] fp32
+  float* part = reinterpret_cast<float*>(smem);
+  constexpr int kPitch = BN + 4;
+  const int row = (warp & 3) * 32 + lane;
+#pragma unroll 1
+  for (int j = (warp >> 2) * 16; j < BN; j += 32) {
+    uint32_t r[16];
+    tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + j, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<float4*>(part + row * kPitch + j + 4 * q) =
+          make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
+                      __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (splits > 1) cluster_barrier();
+  if (warp == 1) tmem_dealloc(tmem, BN);
+  if (!bad) {
+    constexpr int kGroups = kOut / 8;
+    const int rows = min(kTileM, e.M - row0);
+    for (int i = rank * kTileThreads + tid; i < rows * kGroups; i += splits * kTileThreads) {
+      const int r = i / kGroups, c = i % kGroups * 8;
+      float z[2][8];
+#pragma unroll
+      for (int h = 0; h < (SWIGLU ? 2 : 1); ++h) {
+        const float* at = part + r * kPitch + h * kOut + c;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) z[h][x] = 0.0f;
+        for (int q = 0; q < splits; ++q) {
+          float4 f[2];
+          if (q == rank) {
+            f[0] = *reinterpret_cast<const float4*>(at);
+            f[1] = *reinterpret_cast<const float4*>(at + 4);
+          } else {
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+              asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                           : "=f"(f[y].x), "=f"(f[y].y), "=f"(f[y].z), "=f"(f[y].w)
+                           : "r"(cluster_addr(at + 4 * y, q)));
+          }
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            z[h][4 * y] += f[y].x;
+            z[h][4 * y + 1] += f[y].y;
+            z[h][4 * y + 2] += f[y].z;
+            z[h][4 * y + 3] += f[y].w;
+          }
+        }
+      }
+      finish8<SWIGLU>(e, row0 + r, col0 + c, z[0], z[1]);
+    }
+  }
+  if (splits > 1) cluster_barrier();
+}
+
+template <int BN, bool A_ROW, bool B_ROW, bool SWIGLU>
+moe_status_t launch_tiles(const LinearOp& a, const LinearOp& b, int K, const LinearEpi& e,
+                          cudaStream_t st) {
+  constexpr int kOut = SWIGLU ? BN / 2 : BN;
+  constexpr auto kern = linear_tile_kernel<BN, A_ROW, B_ROW, SWIGLU>;
+  const int m_tiles = (e.M + kTileM - 1) / kTileM;
+  const int64_t tiles = (int64_t)m_tiles * ((e.cols + kOut - 1) / kOut);
+  if (tiles > (INT32_MAX / kTileMaxSplit)) return MOE_ERR_INVALID_ARG;
+  // CTAs that share a tile's K: while the GPU holds twice as many and each
+  // still gets four blocks of 64
+  const int nkb = (K + kLinBK - 1) / kLinBK;
+  int splits = 1;
+  while (splits < kTileMaxSplit && tiles * splits * 2 <= 2 * moe_host::sm_count() &&
+         nkb >= splits * 2 * 4)
+    splits *= 2;
+  CUtensorMap ta, tb;
+  if (!linear_map(&ta, a, e.M, K, kTileM) || !linear_map(&tb, b, e.N, K, SWIGLU ? kOut : BN))
+    return MOE_ERR_CUDA;
+  if (const moe_status_t s = moe_host::allow_smem<kern>(tile_smem(BN))) return s;
+  return moe_host::launch_clusters(kern, dim3((unsigned)(tiles * splits)), kTileThreads, tile_smem(BN),
+                                   dim3(splits, 1, 1), st, ta, tb, e, K, splits, m_tiles,
+                                   moe_host::device_error_word());
+}
+
+template <int BN>
+moe_status_t tiles_as(const LinearOp& a, const LinearOp& b, int K, const LinearEpi& e, cudaStream_t st) {
+  if (e.act == MOE_ACT_SWIGLU) return launch_tiles<BN, true, true, true>(a, b, K, e, st);
+  if (a.row_major)
+    return b.row_major ? launch_tiles<BN, true, true, false>(a, b, K, e, st)
+                       : launch_tiles<BN, true, false, false>(a, b, K, e, st);
+  return launch_tiles<BN, false, false, false>(a, b, K, e, st);
+}
+
+}  // namespace
+
+moe_status_t linear_tiles(const LinearOp& a, const LinearOp& b, int K, const LinearEpi& e,
+                          cudaStream_t st) {
+  const int64_t m_tiles = (e.M + kTileM - 1) / kTileM;
+  // narrow tiles while there are fewer wide ones than SMs
+  if (m_tiles * ((e.N + 127) / 128) < moe_host::sm_count()) return tiles_as<64>(a, b, K, e, st);
+  return tiles_as<128>(a, b, K, e, st);
+}
+
+moe_status_t linear_product(const LinearOp& a, const LinearOp& b, int K, LinearEpi e, cudaStream_t st) {
+  using moe_host::aligned16;
+  e.vec = e.cols % 8 == 0 && aligned16(e.out) && aligned16(e.residual) && aligned16(e.preact) &&
+          aligned16(e.bias);
+  if (a.row_major && b.row_major && e.M <= kLinearRowsMost) return linear_rows(a.p, a.ld, b.p, K, e, st);
+  return linear_tiles(a, b, K, e, st);
+}
+
+}  // namespace moe
+
+extern "C" moe_status_t moe_linear(const uint16_t* x, int64_t ld_x, const uint16_t* w,
+                                   const float* bias, const void* residual, int T, int K, int N,
+                                   int activation, int out_dtype, void* out, uint16_t* preact,
+                                   moe_stream_t stream) {
+  using namespace moe;
+  using moe_host::aligned16;
+  using moe_host::aligned4;
+  if (T < 0 || K < 8 || K % 8 != 0 || N < 1) return MOE_ERR_INVALID_ARG;
+  if (activation < MOE_ACT_NONE || activation > MOE_ACT_SWIGLU) return MOE_ERR_INVALID_ARG;
+  if (activation == MOE_ACT_SWIGLU && N % 2 != 0) return MOE_ERR_INVALID_ARG;
+  if (out_dtype != MOE_DTYPE_F32 && out_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!x || !w || !out || !aligned16(x) || !aligned16(w) || ld_x < K || ld_x % 8 != 0)
+    return MOE_ERR_INVALID_ARG;
+  const uintptr_t odd = out_dtype == MOE_DTYPE_BF16 ? 1u : 3u;
+  if ((reinterpret_cast<uintptr_t>(out) & odd) || (reinterpret_cast<uintptr_t>(residual) & odd) ||
+      (reinterpret_cast<uintptr_t>(preact) & 1u) || !aligned4(bias))
+    return MOE_ERR_INVALID_ARG;
+  const int cols = activation == MOE_ACT_SWIGLU ? N / 2 : N;
+  const LinearEpi e{bias, residual, out, preact, T, N, cols, activation, out_dtype == MOE_DTYPE_BF16, 0};
+  return linear_product({x, ld_x, true}, {w, K, true}, K, e, reinterpret_cast<cudaStream_t>(stream));
+}

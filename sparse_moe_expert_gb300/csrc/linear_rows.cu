@@ -1,0 +1,116 @@
+// The dense product for a few rows of x (a decode step): out = act(x W^T + bias)
+// + residual, bound by reading W once.
+//
+// A CTA takes 16 rows of W (SwiGLU: 8 of the gate, 8 of up) and its warps take
+// blocks of 32 k in turn.  A lane holds eight consecutive k of its row of W and
+// of its token, which serve as two k-halves of mma.sync m16n8k16 in the same
+// order on both sides; W goes from global memory straight into the operand, and
+// x comes through L1, where the CTA's warps find it again.  The warps' sums meet
+// in shared memory in warp order.
+#include "linear.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kRowsThreads = 256;
+constexpr int kRowsWarps = kRowsThreads / 32;
+
+__device__ __forceinline__ void rows_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// NT: eights of tokens.
+template <int NT, bool SWIGLU>
+__global__ void __launch_bounds__(kRowsThreads)
+    linear_rows_kernel(const uint16_t* x, int64_t ldx, const uint16_t* w, int K, LinearEpi e) {
+  constexpr int kTokens = NT * 8;
+  __shared__ float sums[kRowsWarps][16][kTokens + 1];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int span = SWIGLU ? 8 : 16;  // output columns
+  const int col0 = blockIdx.x * span;
+  // this lane's two rows of W; a row past the end reads the last one and is not stored
+  const int n0 = min(col0 + g, e.cols - 1);
+  const int n1 = SWIGLU ? e.cols + n0 : min(col0 + 8 + g, e.cols - 1);
+  const uint16_t* w0 = w + (int64_t)n0 * K + 8 * t;
+  const uint16_t* w1 = w + (int64_t)n1 * K + 8 * t;
+  const uint16_t* xr[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) xr[i] = x + (int64_t)min(i * 8 + g, e.M - 1) * ldx + 8 * t;
+  float acc[NT][4];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+  constexpr int kDeep = NT > 2 ? 2 : 4;  // blocks of k in flight
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  const int blocks = (K + 31) / 32;
+#pragma unroll 1
+  for (int kb = warp; kb < blocks; kb += kRowsWarps * kDeep) {
+    uint4 a[kDeep], b[kDeep], q[kDeep][NT];
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      const int k = (kb + d * kRowsWarps) * 32;
+      const bool on = k + 8 * t < K;
+      a[d] = on ? ldg_nc_v4(w0 + k) : zero;
+      b[d] = on ? ldg_nc_v4(w1 + k) : zero;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) q[d][i] = on ? __ldg(reinterpret_cast<const uint4*>(xr[i] + k)) : zero;
+    }
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        rows_mma(acc[i], a[d].x, b[d].x, a[d].y, b[d].y, q[d][i].x, q[d][i].y);
+        rows_mma(acc[i], a[d].z, b[d].z, a[d].w, b[d].w, q[d][i].z, q[d][i].w);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sums[warp][g + (j >> 1) * 8][i * 8 + 2 * t + (j & 1)] = acc[i][j];
+  __syncthreads();
+  // a thread takes eight columns of a token
+  const int groups = SWIGLU ? 1 : 2;
+  for (int i = tid; i < e.M * groups; i += kRowsThreads) {
+    const int r = i / groups, c = i % groups * 8;
+    float z[2][8];
+#pragma unroll
+    for (int h = 0; h < (SWIGLU ? 2 : 1); ++h)
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        float s = 0.0f;
+#pragma unroll
+        for (int v = 0; v < kRowsWarps; ++v) s += sums[v][h * 8 + c + y][r];
+        z[h][y] = s;
+      }
+    finish8<SWIGLU>(e, r, col0 + c, z[0], z[1]);
+  }
+}
+
+template <bool SWIGLU>
+moe_status_t launch_rows(const uint16_t* x, int64_t ldx, const uint16_t* w, int K, const LinearEpi& e,
+                         cudaStream_t st) {
+  const int span = SWIGLU ? 8 : 16;
+  const dim3 grid((e.cols + span - 1) / span), block(kRowsThreads);
+  using moe_host::launch;
+  if (e.M <= 8) return launch(linear_rows_kernel<1, SWIGLU>, grid, block, 0, st, x, ldx, w, K, e);
+  if (e.M <= 16) return launch(linear_rows_kernel<2, SWIGLU>, grid, block, 0, st, x, ldx, w, K, e);
+  return launch(linear_rows_kernel<4, SWIGLU>, grid, block, 0, st, x, ldx, w, K, e);
+}
+
+}  // namespace
+
+moe_status_t linear_rows(const uint16_t* x, int64_t ldx, const uint16_t* w, int K, const LinearEpi& e,
+                         cudaStream_t st) {
+  return e.act == MOE_ACT_SWIGLU ? launch_rows<true>(x, ldx, w, K, e, st)
+                                 : launch_rows<false>(x, ldx, w, K, e, st);
+}
+
+}  // namespace moe

@@ -22,6 +22,7 @@
 #include <optional>
 #include <stdexcept>
 #include <string>
+#include <vector>
 
 #include "../../include/moe_gb300.h"
 
@@ -49,6 +50,7 @@ const char* type_name(at::ScalarType t) {
     case at::kBFloat16: return "torch.bfloat16";
     case at::kInt: return "torch.int32";
     case at::kByte: return "torch.uint8";
+    case at::kChar: return "torch.int8";
     default: return c10::toString(t);
   }
 }
@@ -223,6 +225,7 @@ moe_status_t unlocked(F&& f) {
 }
 
 PyObject* result(std::initializer_list<Tensor> ts) {
+  if (ts.size() == 0) Py_RETURN_NONE;
   PyObject* t = PyTuple_New((Py_ssize_t)ts.size());
   if (!t) throw Raised();
   Py_ssize_t i = 0;
@@ -422,6 +425,426 @@ PyObject* lora_apply(Args a) {
   return s ? status(s) : result({out, ws});
 }
 
+// A result that may be an input itself (same type and rows) and otherwise may
+// not share memory with it: kernels read a row whole before they write it.
+void same_or_apart(const Tensor& out, const char* name, const Tensor& in, const char* other) {
+  if (!out.defined() || !in.defined() || out.numel() == 0 || in.numel() == 0) return;
+  const auto lo = [](const Tensor& t) { return reinterpret_cast<uintptr_t>(t.data_ptr()); };
+  const auto hi = [&](const Tensor& t) {
+    int64_t last = 0;
+    for (int64_t i = 0; i < t.dim(); ++i) last += (t.size(i) - 1) * t.stride(i);
+    return lo(t) + (uintptr_t)(last + 1) * t.element_size();
+  };
+  if (lo(out) >= hi(in) || lo(in) >= hi(out)) return;
+  bool same = lo(out) == lo(in) && out.scalar_type() == in.scalar_type() && out.sizes() == in.sizes();
+  for (int64_t i = 0; same && i < out.dim(); ++i)
+    same = out.size(i) == 1 || out.stride(i) == in.stride(i);
+  if (!same) throw Refused(std::string(name) + " overlaps " + other);
+}
+
+void apart(const Tensor& out, const char* name, const Tensor& in, const char* other) {
+  if (!out.defined() || !in.defined() || out.numel() == 0 || in.numel() == 0) return;
+  if (out.data_ptr() == in.data_ptr()) throw Refused(std::string(name) + " overlaps " + other);
+  same_or_apart(out, name, in, other);
+}
+
+// x's rows [T, H], of `type` if given; the row stride.
+int64_t rows_like(const Tensor& t, int64_t T, int64_t H, c10::Device dev, const char* name) {
+  const int64_t ld = rows2d(t, name);
+  if (t.size(0) != T || t.size(1) != H)
+    throw Refused(std::string(name) + " must be [" + std::to_string(T) + ", " + std::to_string(H) +
+                  "], got " + shape_text(t.sizes()));
+  on_device(t, dev, name);
+  return ld;
+}
+
+void same_type(const Tensor& t, at::ScalarType type, const char* name) {
+  if (t.scalar_type() != type)
+    throw Refused(std::string(name) + " must be " + type_name(type) + ", got " +
+                  type_name(t.scalar_type()));
+}
+
+// A weight or bias [n], fp32 or bf16; both of one type.
+int vector_pair(const Tensor& w, const char* wn, const Tensor& b, const char* bn, int64_t n,
+                c10::Device dev) {
+  const Tensor& first = w.defined() ? w : b;
+  if (!first.defined()) return MOE_DTYPE_F32;
+  const int code = dtype_code(first, w.defined() ? wn : bn);
+  if (w.defined()) like(w, {n}, first.scalar_type(), dev, wn);
+  if (b.defined()) like(b, {n}, first.scalar_type(), dev, bn);
+  return code;
+}
+
+// x, weight, bias, residual, eps, kind, out_bf16 (None: as x), need_stats, out,
+// summed, mean, rstd, stream
+PyObject* layer_norm(Args a) {
+  const Tensor &x = a.tensor("x"), &w = a.tensor("weight", true), &bias = a.tensor("bias", true),
+               &residual = a.tensor("residual", true);
+  const double eps = a.real();
+  const int kind = a.i32();
+  const std::optional<bool> out_bf16 = a.optional_flag();
+  const bool need_stats = a.flag();
+  Tensor out = a.tensor("out", true), summed = a.tensor("summed", true),
+         mean = a.tensor("mean", true), rstd = a.tensor("rstd", true);
+  const StreamArg stream(a.next());
+  const moe_status_t s = unlocked([&] {
+    const int64_t ld = rows2d(x, "x");
+    const int T = as_int(x.size(0), "T"), H = as_int(x.size(1), "H");
+    const c10::Device dev = x.device();
+    const OnStream on(stream, dev);
+    int64_t ld_r = 0;
+    const at::ScalarType xt = x.scalar_type();
+    if (residual.defined()) {
+      ld_r = rows_like(residual, T, H, dev, "residual");
+      same_type(residual, xt, "residual");
+      if (summed.defined()) like(summed, {T, H}, xt, dev, "summed");
+      else summed = make({T, H}, xt, dev);
+    } else if (summed.defined()) {
+      throw Refused("summed needs a residual");
+    }
+    const int wt = vector_pair(w, "weight", bias, "bias", H, dev);
+    at::ScalarType ot = out.defined() ? out.scalar_type() : xt;
+    if (out_bf16) ot = *out_bf16 ? at::kBFloat16 : at::kFloat;
+    if (out.defined()) like(out, {T, H}, ot, dev, "out");
+    else out = make({T, H}, ot, dev);
+    const int out_code = dtype_code(out, "out");
+    const bool layer = kind == MOE_NORM_LAYER;
+    if (mean.defined()) like(mean, {T}, at::kFloat, dev, "mean");
+    else if (need_stats && layer) mean = make({T}, at::kFloat, dev);
+    if (rstd.defined()) like(rstd, {T}, at::kFloat, dev, "rstd");
+    else if (need_stats) rstd = make({T}, at::kFloat, dev);
+    same_or_apart(out, "out", x, "x");
+    same_or_apart(out, "out", residual, "residual");
+    same_or_apart(summed, "summed", x, "x");
+    same_or_apart(summed, "summed", residual, "residual");
+    apart(out, "out", summed, "summed");
+    return moe_layer_norm(x.data_ptr(), dtype_code(x, "x"), ld, ptr<void>(residual), ld_r,
+                          ptr<void>(w), ptr<void>(bias), wt, T, H, kind, (float)eps, out_code,
+                          out.data_ptr(), ptr<void>(summed), ptr<float>(mean), ptr<float>(rstd),
+                          on.handle);
+  });
+  return s ? status(s) : result({out, summed, mean, rstd});
+}
+
+// d_out, x, rstd, mean, weight, d_sum, kind, need_d_weight, need_d_bias, d_x,
+// d_weight, d_bias, workspace, stream
+PyObject* layer_norm_backward(Args a) {
+  const Tensor &d = a.tensor("d_out"), &x = a.tensor("x"), &rstd = a.tensor("rstd"),
+               &mean = a.tensor("mean", true), &w = a.tensor("weight", true),
+               &d_sum = a.tensor("d_sum", true);
+  const int kind = a.i32();
+  const bool need_w = a.flag(), need_b = a.flag();
+  Tensor d_x = a.tensor("d_x", true), d_w = a.tensor("d_weight", true),
+         d_b = a.tensor("d_bias", true), ws = a.tensor("workspace", true);
+  const StreamArg stream(a.next());
+  const moe_status_t s = unlocked([&] {
+    const int64_t ld_x = rows2d(x, "x");
+    const int T = as_int(x.size(0), "T"), H = as_int(x.size(1), "H");
+    const c10::Device dev = x.device();
+    const OnStream on(stream, dev);
+    const at::ScalarType xt = x.scalar_type();
+    const int64_t ld_d = rows_like(d, T, H, dev, "d_out");
+    if (kind != MOE_NORM_LAYER && kind != MOE_NORM_RMS) return MOE_ERR_INVALID_ARG;
+    if ((kind == MOE_NORM_LAYER) != mean.defined())
+      throw Refused("mean belongs to the layer norm, and to it alone");
+    if (mean.defined()) like(mean, {T}, at::kFloat, dev, "mean");
+    like(rstd, {T}, at::kFloat, dev, "rstd");
+    const int wt = vector_pair(w, "weight", Tensor(), "", H, dev);
+    int64_t ld_s = 0;
+    if (d_sum.defined()) {
+      ld_s = rows_like(d_sum, T, H, dev, "d_sum");
+      same_type(d_sum, xt, "d_sum");
+    }
+    if (d_x.defined()) like(d_x, {T, H}, xt, dev, "d_x");
+    else d_x = make({T, H}, xt, dev);
+    if (d_w.defined()) like(d_w, {H}, at::kFloat, dev, "d_weight");
+    else if (need_w) d_w = make({H}, at::kFloat, dev);
+    if (d_b.defined()) like(d_b, {H}, at::kFloat, dev, "d_bias");
+    else if (need_b) d_b = make({H}, at::kFloat, dev);
+    same_or_apart(d_x, "d_x", d, "d_out");
+    same_or_apart(d_x, "d_x", x, "x");
+    same_or_apart(d_x, "d_x", d_sum, "d_sum");
+    if (!ws.defined() && (d_w.defined() || d_b.defined()))
+      ws = make({(int64_t)moe_layer_norm_workspace_size(T, H)}, at::kByte, dev);
+    return moe_layer_norm_backward(
+        d.data_ptr(), dtype_code(d, "d_out"), ld_d, x.data_ptr(), dtype_code(x, "x"), ld_x,
+        ptr<float>(mean), ptr<float>(rstd), ptr<void>(w), wt, ptr<void>(d_sum), ld_s, T, H,
+        d_x.data_ptr(), ptr<float>(d_w), ptr<float>(d_b), ptr<void>(ws),
+        ws.defined() ? scratch_bytes(ws, dev) : 0, on.handle);
+  });
+  return s ? status(s) : result({d_x, d_w, d_b, ws});
+}
+
+// The tensors of a list or tuple; none at all for None.
+std::vector<Tensor> tensors(PyObject* o, const char* name, bool optional = false) {
+  std::vector<Tensor> out;
+  if (o == Py_None && optional) return out;
+  PyObject* seq = PyList_Check(o) || PyTuple_Check(o) ? o : nullptr;
+  if (!seq) throw Refused(std::string(name) + " must be a list of tensors");
+  const Py_ssize_t n = PySequence_Fast_GET_SIZE(seq);
+  out.reserve(n);
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    PyObject* t = PySequence_Fast_GET_ITEM(seq, i);
+    if (!THPVariable_Check(t)) throw Refused(std::string(name) + " must hold tensors");
+    out.push_back(THPVariable_Unpack(t));
+  }
+  return out;
+}
+
+void entries(const std::vector<Tensor>& ts, size_t n, const char* name) {
+  if (ts.size() != n)
+    throw Refused(std::string(name) + " must have " + std::to_string(n) + " entries, got " +
+                  std::to_string(ts.size()));
+}
+
+// One of a list's tensors: dense, of this type, with n elements.
+void item(const Tensor& t, int64_t n, at::ScalarType type, c10::Device dev, const char* name) {
+  need(t, type, name);
+  if (t.numel() != n)
+    throw Refused(std::string(name) + " must hold " + std::to_string(n) + " elements, got " +
+                  std::to_string(t.numel()));
+  on_device(t, dev, name);
+}
+
+constexpr int64_t kStateBlock = 256;  // elements that share a scale of the 8-bit states
+
+void eight_bit_states(moe_adamw_tensor_t& e, const Tensor& m, const Tensor& v, const Tensor& ms,
+                      const Tensor& vs, int64_t n, c10::Device dev) {
+  const int64_t blocks = (n + kStateBlock - 1) / kStateBlock;
+  item(m, n, at::kChar, dev, "exp_avg");
+  item(v, n, at::kByte, dev, "exp_avg_sq");
+  item(ms, blocks, at::kFloat, dev, "exp_avg_scales");
+  item(vs, blocks, at::kFloat, dev, "exp_avg_sq_scales");
+  e.exp_avg_scale = ptr<float>(ms);
+  e.exp_avg_sq_scale = ptr<float>(vs);
+}
+
+// params, grads, exp_avg, exp_avg_sq, exp_avg_scales, exp_avg_sq_scales, masters,
+// step, lr, lr_dev, beta1, beta2, eps, weight_decay (a float or a list),
+// grad_scale, stream
+PyObject* adamw_step(Args a) {
+  const std::vector<Tensor> params = tensors(a.next(), "params"), grads = tensors(a.next(), "grads"),
+                            m = tensors(a.next(), "exp_avg"), v = tensors(a.next(), "exp_avg_sq"),
+                            ms = tensors(a.next(), "exp_avg_scales", true),
+                            vs = tensors(a.next(), "exp_avg_sq_scales", true),
+                            masters = tensors(a.next(), "masters", true);
+  const Tensor& step = a.tensor("step");
+  const double lr = a.real();
+  const Tensor& lr_dev = a.tensor("lr", true);
+  const double beta1 = a.real(), beta2 = a.real(), eps = a.real();
+  const size_t n = params.size();
+  std::vector<float> decay(n);
+  PyObject* wd = a.next();
+  if (PyList_Check(wd) || PyTuple_Check(wd)) {
+    if ((size_t)PySequence_Fast_GET_SIZE(wd) != n)
+      throw Refused("weight_decay must be a number or have " + std::to_string(n) + " entries");
+    for (size_t i = 0; i < n; ++i) {
+      decay[i] = (float)PyFloat_AsDouble(PySequence_Fast_GET_ITEM(wd, i));
+      if (PyErr_Occurred()) throw Raised();
+    }
+  } else {
+    const double one = PyFloat_AsDouble(wd);
+    if (PyErr_Occurred()) throw Raised();
+    decay.assign(n, (float)one);
+  }
+  const Tensor& scale = a.tensor("grad_scale", true);
+  const StreamArg stream(a.next());
+  const moe_status_t s = unlocked([&] {
+    const c10::Device dev = step.device();
+    like(step, {2}, at::kInt, dev, "step");
+    const OnStream on(stream, dev);
+    if (scale.defined()) item(scale, 1, at::kFloat, dev, "grad_scale");
+    if (lr_dev.defined()) item(lr_dev, 1, at::kFloat, dev, "lr");
+    const bool eight = !ms.empty() || !vs.empty() || (n > 0 && !m.empty() && m[0].scalar_type() == at::kChar);
+    entries(grads, n, "grads");
+    entries(m, n, "exp_avg");
+    entries(v, n, "exp_avg_sq");
+    if (eight) {
+      entries(ms, n, "exp_avg_scales");
+      entries(vs, n, "exp_avg_sq_scales");
+    }
+    if (!masters.empty()) entries(masters, n, "masters");
+    std::vector<moe_adamw_tensor_t> table(n);
+    for (size_t i = 0; i < n; ++i) {
+      moe_adamw_tensor_t& e = table[i];
+      const int64_t size = params[i].numel();
+      dtype_code(params[i], "params");
+      dtype_code(grads[i], "grads");
+      item(params[i], size, params[0].scalar_type(), dev, "params");
+      item(grads[i], size, grads[0].scalar_type(), dev, "grads");
+      e = {params[i].data_ptr(), grads[i].data_ptr(), nullptr, m[i].data_ptr(), v[i].data_ptr(),
+           nullptr, nullptr, size, decay[i]};
+      if (!masters.empty()) {
+        item(masters[i], size, at::kFloat, dev, "masters");
+        e.master = ptr<float>(masters[i]);
+      }
+      if (eight) {
+        eight_bit_states(e, m[i], v[i], ms[i], vs[i], size, dev);
+      } else {
+        item(m[i], size, at::kFloat, dev, "exp_avg");
+        item(v[i], size, at::kFloat, dev, "exp_avg_sq");
+      }
+    }
+    return moe_adamw_step(table.data(), (int)n, n ? dtype_code(params[0], "params") : MOE_DTYPE_F32,
+                          n ? dtype_code(grads[0], "grads") : MOE_DTYPE_F32, eight ? 8 : 32, lr,
+                          ptr<float>(lr_dev), beta1, beta2, eps, ptr<float>(scale),
+                          ptr<int32_t>(step), on.handle);
+  });
+  return s ? status(s) : result({});
+}
+
+// exp_avg, exp_avg_sq, exp_avg_scales, exp_avg_sq_scales, stream
+PyObject* adamw_values(Args a) {
+  const std::vector<Tensor> m = tensors(a.next(), "exp_avg"), v = tensors(a.next(), "exp_avg_sq"),
+                            ms = tensors(a.next(), "exp_avg_scales"),
+                            vs = tensors(a.next(), "exp_avg_sq_scales");
+  const StreamArg stream(a.next());
+  Tensor out_m, out_v;
+  if (m.empty()) throw Refused("exp_avg must not be empty");
+  const moe_status_t s = unlocked([&] {
+    const size_t n = m.size();
+    entries(v, n, "exp_avg_sq");
+    entries(ms, n, "exp_avg_scales");
+    entries(vs, n, "exp_avg_sq_scales");
+    const c10::Device dev = m[0].device();
+    std::vector<moe_adamw_tensor_t> table(n);
+    int64_t total = 0;
+    for (size_t i = 0; i < n; ++i) {
+      const int64_t size = m[i].numel();
+      table[i] = {nullptr, nullptr, nullptr, m[i].data_ptr(), v[i].data_ptr(), nullptr, nullptr, size,
+                  0.0f};
+      eight_bit_states(table[i], m[i], v[i], ms[i], vs[i], size, dev);
+      total += size;
+    }
+    const OnStream on(stream, dev);
+    out_m = make({total}, at::kFloat, dev);
+    out_v = make({total}, at::kFloat, dev);
+    return moe_adamw_values(table.data(), (int)n, ptr<float>(out_m), ptr<float>(out_v), on.handle);
+  });
+  return s ? status(s) : result({out_m, out_v});
+}
+
+// Rows of a bf16 matrix that a tensor map can describe: 16-byte aligned rows.
+int64_t mapped_rows(const Tensor& t, const char* name) {
+  const int64_t ld = rows2d(t, name);
+  same_type(t, at::kBFloat16, name);
+  if (ld % 8 != 0 || reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 != 0)
+    throw Refused(std::string(name) + " must have 16-byte aligned rows");
+  return ld;
+}
+
+// x, w, bias, residual, activation, out, out_bf16 (None: bf16, or as residual),
+// need_preact, preact, stream
+PyObject* linear(Args a) {
+  const Tensor &x = a.tensor("x"), &w = a.tensor("w"), &bias = a.tensor("bias", true),
+               &residual = a.tensor("residual", true);
+  const int act = a.i32();
+  Tensor out = a.tensor("out", true);
+  const std::optional<bool> out_bf16 = a.optional_flag();
+  const bool need_preact = a.flag();
+  Tensor preact = a.tensor("preact", true);
+  const StreamArg stream(a.next());
+  const moe_status_t s = unlocked([&] {
+    const int64_t ld = mapped_rows(x, "x");
+    const c10::Device dev = x.device();
+    const OnStream on(stream, dev);
+    const int T = as_int(x.size(0), "T"), K = as_int(x.size(1), "K");
+    if (w.dim() != 2 || w.size(1) != K) throw Refused("w must be [N, " + std::to_string(K) + "]");
+    const int N = as_int(w.size(0), "N");
+    like(w, {N, K}, at::kBFloat16, dev, "w");
+    if (bias.defined()) like(bias, {N}, at::kFloat, dev, "bias");
+    if (act < MOE_ACT_NONE || act > MOE_ACT_SWIGLU) return MOE_ERR_INVALID_ARG;
+    const int64_t cols = act == MOE_ACT_SWIGLU ? N / 2 : N;
+    at::ScalarType ot = out.defined() ? out.scalar_type()
+                        : residual.defined() ? residual.scalar_type() : at::kBFloat16;
+    if (out_bf16) ot = *out_bf16 ? at::kBFloat16 : at::kFloat;
+    if (residual.defined()) like(residual, {T, cols}, ot, dev, "residual");
+    if (out.defined()) like(out, {T, cols}, ot, dev, "out");
+    else out = make({T, cols}, ot, dev);
+    const int out_code = dtype_code(out, "out");
+    if (preact.defined()) like(preact, {T, N}, at::kBFloat16, dev, "preact");
+    else if (need_preact) preact = make({T, N}, at::kBFloat16, dev);
+    same_or_apart(out, "out", residual, "residual");
+    for (const Tensor* o : {&out, &preact}) {
+      const char* name = o == &out ? "out" : "preact";
+      apart(*o, name, x, "x");
+      apart(*o, name, w, "w");
+      apart(*o, name, bias, "bias");
+    }
+    apart(preact, "preact", out, "out");
+    apart(preact, "preact", residual, "residual");
+    return moe_linear(ptr<uint16_t>(x), ld, ptr<uint16_t>(w), ptr<float>(bias), ptr<void>(residual), T,
+                      K, N, act, out_code, out.data_ptr(), ptr<uint16_t>(preact), on.handle);
+  });
+  return s ? status(s) : result({out, preact});
+}
+
+// d_out, x, w, preact, activation, need_d_x, need_d_w, need_d_bias, d_x, d_w,
+// d_w_bf16 (None: fp32), accumulate, d_bias, workspace, stream
+PyObject* linear_backward(Args a) {
+  const Tensor &d = a.tensor("d_out"), &x = a.tensor("x"), &w = a.tensor("w"),
+               &preact = a.tensor("preact", true);
+  const int act = a.i32();
+  const bool need_x = a.flag(), need_w = a.flag(), need_b = a.flag();
+  Tensor d_x = a.tensor("d_x", true), d_w = a.tensor("d_w", true);
+  const std::optional<bool> w_bf16 = a.optional_flag();
+  const bool accumulate = a.flag();
+  Tensor d_b = a.tensor("d_bias", true), ws = a.tensor("workspace", true), d_z;
+  const StreamArg stream(a.next());
+  const moe_status_t s = unlocked([&] {
+    const int64_t ld_x = mapped_rows(x, "x");
+    const c10::Device dev = x.device();
+    const OnStream on(stream, dev);
+    const int T = as_int(x.size(0), "T"), K = as_int(x.size(1), "K");
+    if (w.dim() != 2 || w.size(1) != K) throw Refused("w must be [N, " + std::to_string(K) + "]");
+    const int N = as_int(w.size(0), "N");
+    like(w, {N, K}, at::kBFloat16, dev, "w");
+    if (act < MOE_ACT_NONE || act > MOE_ACT_SWIGLU) return MOE_ERR_INVALID_ARG;
+    const int64_t cols = act == MOE_ACT_SWIGLU ? N / 2 : N;
+    const int64_t ld_d = rows_like(d, T, cols, dev, "d_out");
+    if (preact.defined()) like(preact, {T, N}, at::kBFloat16, dev, "preact");
+    else if (act != MOE_ACT_NONE) throw Refused("preact is needed for the activation's gradient");
+    if (d_x.defined()) like(d_x, {T, K}, at::kBFloat16, dev, "d_x");
+    else if (need_x) d_x = make({T, K}, at::kBFloat16, dev);
+    if (accumulate && !d_w.defined()) throw Refused("accumulate needs d_w");
+    at::ScalarType wt = d_w.defined() ? d_w.scalar_type() : at::kFloat;
+    if (w_bf16) wt = *w_bf16 ? at::kBFloat16 : at::kFloat;
+    if (d_w.defined()) like(d_w, {N, K}, wt, dev, "d_w");
+    else if (need_w) d_w = make({N, K}, wt, dev);
+    const int w_code = d_w.defined() ? dtype_code(d_w, "d_w") : MOE_DTYPE_F32;
+    if (d_b.defined()) like(d_b, {N}, at::kFloat, dev, "d_bias");
+    else if (need_b) d_b = make({N}, at::kFloat, dev);
+    for (const Tensor* o : {&d_x, &d_w, &d_b}) {
+      const char* name = o == &d_x ? "d_x" : o == &d_w ? "d_w" : "d_bias";
+      apart(*o, name, d, "d_out");
+      apart(*o, name, x, "x");
+      apart(*o, name, w, "w");
+      apart(*o, name, preact, "preact");
+    }
+    apart(d_x, "d_x", d_w, "d_w");
+    // d_out is d_preact where it is bf16 with aligned rows and nothing was activated
+    const bool direct = act == MOE_ACT_NONE && d.scalar_type() == at::kBFloat16 && ld_d % 8 == 0 &&
+                        reinterpret_cast<uintptr_t>(d.data_ptr()) % 16 == 0;
+    int64_t ld_z = 0;
+    if (direct) {
+      d_z = d;
+    } else {
+      ld_z = ((int64_t)N + 7) / 8 * 8;
+      d_z = make({T, ld_z}, at::kBFloat16, dev);
+    }
+    if (!ws.defined() && d_b.defined())
+      ws = make({(int64_t)moe_linear_backward_workspace_size(T, N, act)}, at::kByte, dev);
+    return moe_linear_backward(d.data_ptr(), dtype_code(d, "d_out"), ld_d, ptr<uint16_t>(x), ld_x,
+                               ptr<uint16_t>(w), ptr<uint16_t>(preact), T, K, N, act,
+                               direct ? nullptr : ptr<uint16_t>(d_z), ld_z, ptr<uint16_t>(d_x),
+                               ptr<void>(d_w), w_code, accumulate, ptr<float>(d_b), ptr<void>(ws),
+                               ws.defined() ? scratch_bytes(ws, dev) : 0, on.handle);
+  });
+  if (s) return status(s);
+  if (d_z.size(1) != w.size(0)) d_z = d_z.narrow(1, 0, w.size(0));
+  return result({d_x, d_w, d_b, d_z, ws});
+}
+
 // C++ exceptions end here: refusals and torch's own errors become Python
 // exceptions.
 template <PyObject* (*F)(Args)>
@@ -456,6 +879,12 @@ PyMethodDef methods[] = {
     {"route_scored_backward", method<route_scored_backward>(), METH_FASTCALL, nullptr},
     {"combine_backward", method<combine_backward>(), METH_FASTCALL, nullptr},
     {"lora_apply", method<lora_apply>(), METH_FASTCALL, nullptr},
+    {"layer_norm", method<layer_norm>(), METH_FASTCALL, nullptr},
+    {"layer_norm_backward", method<layer_norm_backward>(), METH_FASTCALL, nullptr},
+    {"linear", method<linear>(), METH_FASTCALL, nullptr},
+    {"linear_backward", method<linear_backward>(), METH_FASTCALL, nullptr},
+    {"adamw_step", method<adamw_step>(), METH_FASTCALL, nullptr},
+    {"adamw_values", method<adamw_values>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 

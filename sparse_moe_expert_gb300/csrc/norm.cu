@@ -1,0 +1,486 @@
+// Layer and RMS norm of rows, and their gradient.
+//
+// With s = x (+ residual, rounded to x's type and stored), over a row of H:
+//   mu   = mean s (RMS: 0),  rstd = (mean (s - mu)^2 + eps)^-1/2
+//   out  = (s - mu) rstd w + b
+// and backwards, with xh = (s - mu) rstd and c = d w:
+//   d_s  = rstd (c - mean c - xh mean(c xh)) (+ d_sum)      (RMS: no mean c)
+//   d_w  = sum_t d xh,   d_b = sum_t d
+// The row stays in registers between its sums, so each value is read once; the
+// variance is summed from the centred values.  All sums are fp32 in an order
+// that the sizes fix.  A thread owns columns, and in the gradient it keeps
+// their d_w and d_b over all rows of its CTA; the CTAs' sums are joined by a
+// second kernel in the CTAs' order.
+#include "dense.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kNormMaxWidth = 8192;  // 512 threads with two vectors of eight each
+constexpr int kNormWarpWidth = 512;  // up to this width a warp takes a row
+
+struct NormParams {
+  const void* x;
+  int64_t ldx;
+  const void* residual;
+  int64_t ldr;
+  const void* weight;
+  const void* bias;
+  int w_bf16;
+  int T, H;
+  float eps;
+  int rms;
+  void* out;
+  void* summed;
+  float* mean;
+  float* rstd;
+};
+
+// Column of value e of a thread's vector j.  VEC: eight consecutive ones;
+// else neighbours lie in neighbouring threads.
+template <bool VEC>
+__device__ __forceinline__ int column(int j, int e) {
+  return VEC ? (j * (int)blockDim.x + (int)threadIdx.x) * 8 + e
+             : (j * 8 + e) * (int)blockDim.x + (int)threadIdx.x;
+}
+
+template <bool BF16, bool VEC>
+struct RowVec {
+  Vec8<BF16> v;
+  // columns of vector j of the row at p; zeros past H
+  __device__ __forceinline__ void load(const void* p, int64_t row, int j, int H) {
+    if constexpr (VEC) {
+      const int c = column<true>(j, 0);
+      if (c < H) v.load(p, row + c);
+      else v.zero();
+    } else {
+      uint32_t w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = column<false>(j, e);
+        if constexpr (BF16) w[e] = c < H ? static_cast<const uint16_t*>(p)[row + c] : 0u;
+        else w[e] = c < H ? static_cast<const uint32_t*>(p)[row + c] : 0u;
+      }
+      if constexpr (BF16) {
+        v.q[0] = make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16),
+                            w[6] | (w[7] << 16));
+      } else {
+        v.q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        v.q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(void* p, int64_t row, int j, int H) const {
+    if constexpr (VEC) {
+      const int c = column<true>(j, 0);
+      if (c < H) v.store(p, row + c);
+    } else if constexpr (BF16) {
+      const uint32_t w[4] = {v.q[0].x, v.q[0].y, v.q[0].z, v.q[0].w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = column<false>(j, e);
+        if (c < H) static_cast<uint16_t*>(p)[row + c] = (uint16_t)(e & 1 ? w[e >> 1] >> 16 : w[e >> 1]);
+      }
+    } else {
+      float f[8];
+      v.get(f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = column<false>(j, e);
+        if (c < H) static_cast<float*>(p)[row + c] = f[e];
+      }
+    }
+  }
+};
+
+// Weight or bias at a thread's vector j.
+template <bool VEC>
+__device__ __forceinline__ void load_param(float (&f)[8], const void* p, int bf16, int j, int H) {
+  if (bf16) {
+    RowVec<true, VEC> v;
+    v.load(p, 0, j, H);
+    v.v.get(f);
+  } else {
+    RowVec<false, VEC> v;
+    v.load(p, 0, j, H);
+    v.v.get(f);
+  }
+}
+
+// blockDim.x threads take a row; blockDim.y rows per CTA when those are a warp.
+template <bool X_BF16, bool OUT_BF16, int NV, bool VEC>
+__global__ void __launch_bounds__(512) layer_norm_kernel(NormParams p) {
+  __shared__ float part[2][32];
+  pdl_wait();
+  pdl_trigger();
+  const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (t >= p.T) return;  // whole warps, which are on their own where there is more than one row
+  float f[NV][8];
+  RowVec<X_BF16, VEC> x[NV], r[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) x[j].load(p.x, t * p.ldx, j, p.H);
+  if (p.residual) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) r[j].load(p.residual, t * p.ldr, j, p.H);
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    x[j].v.get(f[j]);
+    if (p.residual) {
+      float g[8];
+      r[j].v.get(g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[j][e] += g[e];
+      x[j].v.set(f[j]);
+      x[j].store(p.summed, t * p.H, j, p.H);
+      x[j].v.get(f[j]);  // the sum as stored
+    }
+  }
+  const float inv_h = 1.0f / (float)p.H;
+  float mu = 0.0f;
+  if (!p.rms) {
+    float s[1] = {0.0f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[0] += f[j][e];
+    block_sum(s, part[0]);
+    mu = s[0] * inv_h;
+  }
+  float q[1] = {0.0f};
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (column<VEC>(j, e) < p.H) f[j][e] -= mu;
+      q[0] = fmaf(f[j][e], f[j][e], q[0]);
+    }
+  block_sum(q, part[1]);
+  const float rstd = 1.0f / sqrtf(q[0] * inv_h + p.eps);
+  if (threadIdx.x == 0) {
+    if (p.mean) p.mean[t] = mu;
+    if (p.rstd) p.rstd[t] = rstd;
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = f[j][e] * rstd;
+    if (p.weight) {
+      float w[8];
+      load_param<VEC>(w, p.weight, p.w_bf16, j, p.H);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] *= w[e];
+    }
+    if (p.bias) {
+      float b[8];
+      load_param<VEC>(b, p.bias, p.w_bf16, j, p.H);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] += b[e];
+    }
+    RowVec<OUT_BF16, VEC> o;
+    o.v.set(y);
+    o.store(p.out, t * p.H, j, p.H);
+  }
+}
+
+// ---- gradient ----------------------------------------------------------------
+
+struct NormGradParams {
+  const void* d_out;
+  int64_t ldd;
+  const void* x;
+  int64_t ldx;
+  const void* d_sum;
+  int64_t lds;
+  const float* mean;  // null: RMS
+  const float* rstd;
+  const void* weight;
+  int w_bf16;
+  int T, H;
+  void* d_x;
+  float* part;  // [CTAs][2][H], or null: no weight or bias gradient
+};
+
+// CTAs walk over rows; the next row's values are on their way while the
+// present one is summed.
+template <bool D_BF16, bool X_BF16, int NV, bool VEC>
+__global__ void __launch_bounds__(512) layer_norm_backward_kernel(NormGradParams p) {
+  extern __shared__ float join[];  // [2][H], where a CTA takes several rows
+  __shared__ float part[2][2][32];
+  pdl_wait();
+  pdl_trigger();
+  float dw[NV][8], db[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[j][e] = db[j][e] = 0.0f;
+  const float inv_h = 1.0f / (float)p.H;
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  RowVec<D_BF16, VEC> d[NV];
+  RowVec<X_BF16, VEC> x[NV], s[NV];
+  float mu = 0.0f, rstd = 0.0f;
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      d[j].load(p.d_out, row * p.ldd, j, p.H);
+      x[j].load(p.x, row * p.ldx, j, p.H);
+      if (p.d_sum) s[j].load(p.d_sum, row * p.lds, j, p.H);
+    }
+    mu = p.mean ? p.mean[row] : 0.0f;
+    rstd = p.rstd[row];
+  };
+  if (t < p.T) fetch(t);
+  int buf = 0;
+  for (; t < p.T; t += step, buf ^= 1) {
+    const float r = rstd;
+    float c[NV][8], xh[NV][8], ds[NV][8];
+    float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float w[8];
+      d[j].v.get(c[j]);
+      x[j].v.get(xh[j]);
+      if (p.d_sum) s[j].v.get(ds[j]);
+      if (p.weight) load_param<VEC>(w, p.weight, p.w_bf16, j, p.H);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        xh[j][e] = column<VEC>(j, e) < p.H ? (xh[j][e] - mu) * r : 0.0f;
+        db[j][e] += c[j][e];
+        dw[j][e] = fmaf(c[j][e], xh[j][e], dw[j][e]);
+        if (p.weight) c[j][e] *= w[e];
+        sum[0] += c[j][e];
+        sum[1] = fmaf(c[j][e], xh[j][e], sum[1]);
+      }
+    }
+    if (t + step < p.T) fetch(t + step);
+    block_sum(sum, part[buf][0]);
+    const float m0 = p.mean ? sum[0] * inv_h : 0.0f, m1 = sum[1] * inv_h;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        y[e] = r * (c[j][e] - m0 - xh[j][e] * m1);
+        if (p.d_sum) y[e] += ds[j][e];
+      }
+      RowVec<X_BF16, VEC> o;
+      o.v.set(y);
+      o.store(p.d_x, t * p.H, j, p.H);
+    }
+  }
+  if (!p.part) return;
+  float* out = p.part + (int64_t)blockIdx.x * 2 * p.H;
+  if (blockDim.y > 1) {  // the warps' sums, one warp after the other
+    for (int w = 0; w < (int)blockDim.y; ++w) {
+      if ((int)threadIdx.y == w) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int col = column<VEC>(j, e);
+            if (col >= p.H) continue;
+            join[col] = w ? join[col] + dw[j][e] : dw[j][e];
+            join[p.H + col] = w ? join[p.H + col] + db[j][e] : db[j][e];
+          }
+      }
+      __syncthreads();
+    }
+    for (int i = threadIdx.y * 32 + threadIdx.x; i < 2 * p.H; i += 32 * blockDim.y) out[i] = join[i];
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    RowVec<false, VEC> o;
+    o.v.set(dw[j]);
+    o.store(out, 0, j, p.H);
+    o.v.set(db[j]);
+    o.store(out, p.H, j, p.H);
+  }
+}
+
+// ---- column sums ---------------------------------------------------------------
+
+constexpr int kColThreads = 512;
+constexpr int kColLanes = kColThreads / 32;
+
+// 32 columns per CTA; a warp sums a run of the rows, the runs are added in order.
+__global__ void __launch_bounds__(kColThreads) column_sums_kernel(const float* part, int rows,
+                                                                  int64_t ld, int cols, float* out) {
+  __shared__ float sum[kColLanes][32];
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31), lane = threadIdx.x >> 5;
+  const int per = (rows + kColLanes - 1) / kColLanes;
+  const int r0 = lane * per, r1 = min(r0 + per, rows);
+  float s = 0.0f;
+  if (c < cols) {
+#pragma unroll 8
+    for (int r = r0; r < r1; ++r) s += part[r * ld + c];
+  }
+  sum[lane][threadIdx.x & 31] = s;
+  __syncthreads();
+  if (lane == 0 && c < cols) {
+    s = sum[0][threadIdx.x];
+#pragma unroll
+    for (int i = 1; i < kColLanes; ++i) s += sum[i][threadIdx.x];
+    out[c] = s;
+  }
+}
+
+// How a row is shared out: vectors per thread, threads, rows per CTA.
+struct Shape {
+  int nv, threads, rows;
+};
+
+bool type_ok(int t) { return t == MOE_DTYPE_F32 || t == MOE_DTYPE_BF16; }
+
+// Whether rows of this tensor can be read eight values at a time.
+bool vec_ok(const void* p, int dtype, int64_t ld) {
+  return p == nullptr || (moe_host::aligned16(p) && (dtype == MOE_DTYPE_BF16 ? ld % 8 : ld % 4) == 0);
+}
+
+bool element_aligned(const void* p, int dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & (dtype == MOE_DTYPE_BF16 ? 1u : 3u)) == 0;
+}
+
+Shape norm_shape(int H, int want) {
+  const int vecs = (H + 7) / 8;
+  if (H <= kNormWarpWidth) return {vecs <= 32 ? 1 : 2, 32, 8};
+  int nv = want;
+  if (vecs > 512) nv = 2;
+  return {nv, ((vecs + nv - 1) / nv + 31) / 32 * 32, 1};
+}
+
+template <bool X_BF16, bool OUT_BF16, bool VEC>
+moe_status_t launch_norm(const NormParams& p, const Shape& s, cudaStream_t st) {
+  const dim3 grid((unsigned)(((int64_t)p.T + s.rows - 1) / s.rows)), block(s.threads, s.rows);
+  using moe_host::launch;
+  if (s.nv == 1) return launch(layer_norm_kernel<X_BF16, OUT_BF16, 1, VEC>, grid, block, 0, st, p);
+  return launch(layer_norm_kernel<X_BF16, OUT_BF16, 2, VEC>, grid, block, 0, st, p);
+}
+
+template <bool D_BF16, bool X_BF16, bool VEC>
+moe_status_t launch_norm_grad(const NormGradParams& p, const Shape& s, int grid, cudaStream_t st) {
+  const dim3 block(s.threads, s.rows);
+  const size_t smem = s.rows > 1 ? (size_t)p.H * 8 : 0;
+  using moe_host::launch;
+  if (s.nv == 1)
+    return launch(layer_norm_backward_kernel<D_BF16, X_BF16, 1, VEC>, grid, block, smem, st, p);
+  return launch(layer_norm_backward_kernel<D_BF16, X_BF16, 2, VEC>, grid, block, smem, st, p);
+}
+
+// CTAs of the gradient for rows of this shape.
+int norm_grad_ctas(int64_t T, const Shape& s) {
+  const int64_t most = (int64_t)moe_host::sm_count() * 2;
+  const int64_t need = (T + s.rows - 1) / s.rows;
+  return (int)(need < most ? need : most);
+}
+
+}  // namespace
+}  // namespace moe
+
+namespace moe_host {
+
+moe_status_t column_sums(const float* part, int rows, int64_t ld, int cols, float* out,
+                         cudaStream_t st) {
+  if (cols == 0) return MOE_OK;
+  return launch(moe::column_sums_kernel, dim3((cols + 31) / 32), dim3(moe::kColThreads), 0, st, part,
+                rows, ld, cols, out);
+}
+
+}  // namespace moe_host
+
+extern "C" moe_status_t moe_layer_norm(const void* x, int x_dtype, int64_t ld_x,
+                                       const void* residual, int64_t ld_residual,
+                                       const void* weight, const void* bias, int weight_dtype,
+                                       int T, int H, int kind, float eps, int out_dtype, void* out,
+                                       void* summed, float* mean, float* rstd,
+                                       moe_stream_t stream) {
+  using namespace moe;
+  if (T < 0 || H < 1 || H > kNormMaxWidth) return MOE_ERR_INVALID_ARG;
+  if (kind != MOE_NORM_LAYER && kind != MOE_NORM_RMS) return MOE_ERR_INVALID_ARG;
+  if (!type_ok(x_dtype) || !type_ok(out_dtype) || !type_ok(weight_dtype)) return MOE_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f) || !(eps < INFINITY)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!x || !out || ld_x < H || (residual && (!summed || ld_residual < H))) return MOE_ERR_INVALID_ARG;
+  if (!element_aligned(x, x_dtype) || !element_aligned(residual, x_dtype) ||
+      !element_aligned(summed, x_dtype) || !element_aligned(weight, weight_dtype) ||
+      !element_aligned(bias, weight_dtype) || !element_aligned(out, out_dtype) ||
+      !moe_host::aligned4(mean) || !moe_host::aligned4(rstd))
+    return MOE_ERR_INVALID_ARG;
+  NormParams p{x,   ld_x, residual, ld_residual, weight, bias, weight_dtype == MOE_DTYPE_BF16,
+               T,   H,    eps,      kind == MOE_NORM_RMS, out, summed, mean, rstd};
+  const bool vec = H % 8 == 0 && vec_ok(x, x_dtype, ld_x) && vec_ok(residual, x_dtype, ld_residual) &&
+                   vec_ok(residual ? summed : nullptr, x_dtype, H) && vec_ok(weight, weight_dtype, H) &&
+                   vec_ok(bias, weight_dtype, H) && vec_ok(out, out_dtype, H);
+  const Shape s = norm_shape(H, vec && T > moe_host::sm_count() ? 2 : 1);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool xb = x_dtype == MOE_DTYPE_BF16, ob = out_dtype == MOE_DTYPE_BF16;
+  if (vec)
+    return xb ? (ob ? launch_norm<true, true, true>(p, s, st) : launch_norm<true, false, true>(p, s, st))
+              : (ob ? launch_norm<false, true, true>(p, s, st) : launch_norm<false, false, true>(p, s, st));
+  return xb ? (ob ? launch_norm<true, true, false>(p, s, st) : launch_norm<true, false, false>(p, s, st))
+            : (ob ? launch_norm<false, true, false>(p, s, st) : launch_norm<false, false, false>(p, s, st));
+}
+
+extern "C" size_t moe_layer_norm_workspace_size(int T, int H) {
+  using namespace moe;
+  if (T < 1 || H < 1 || H > kNormMaxWidth) return 16;
+  return (size_t)norm_grad_ctas(T, norm_shape(H, 2)) * 2 * H * sizeof(float);
+}
+
+extern "C" moe_status_t moe_layer_norm_backward(
+    const void* d_out, int d_dtype, int64_t ld_d, const void* x, int x_dtype, int64_t ld_x,
+    const float* mean, const float* rstd, const void* weight, int weight_dtype, const void* d_sum,
+    int64_t ld_sum, int T, int H, void* d_x, float* d_weight, float* d_bias, void* workspace,
+    size_t workspace_bytes, moe_stream_t stream) {
+  using namespace moe;
+  if (T < 0 || H < 1 || H > kNormMaxWidth) return MOE_ERR_INVALID_ARG;
+  if (!type_ok(x_dtype) || !type_ok(d_dtype) || !type_ok(weight_dtype)) return MOE_ERR_INVALID_ARG;
+  if (!moe_host::aligned4(d_weight) || !moe_host::aligned4(d_bias)) return MOE_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool sums = d_weight || d_bias;
+  const Shape s = norm_shape(H, 2);
+  const int grid = norm_grad_ctas(T, s);
+  if (T > 0) {
+    if (!d_out || !x || !rstd || !d_x || ld_d < H || ld_x < H || (d_sum && ld_sum < H))
+      return MOE_ERR_INVALID_ARG;
+    if (!element_aligned(d_out, d_dtype) || !element_aligned(x, x_dtype) ||
+        !element_aligned(d_sum, x_dtype) || !element_aligned(d_x, x_dtype) ||
+        !element_aligned(weight, weight_dtype) || !moe_host::aligned4(mean) ||
+        !moe_host::aligned4(rstd))
+      return MOE_ERR_INVALID_ARG;
+    if (sums && (!workspace || !moe_host::aligned16(workspace) ||
+                 workspace_bytes < moe_layer_norm_workspace_size(T, H)))
+      return MOE_ERR_INVALID_ARG;
+    NormGradParams p{d_out, ld_d, x, ld_x, d_sum, ld_sum, mean, rstd, weight,
+                     weight_dtype == MOE_DTYPE_BF16, T, H, d_x,
+                     sums ? static_cast<float*>(workspace) : nullptr};
+    const bool vec = H % 8 == 0 && vec_ok(d_out, d_dtype, ld_d) && vec_ok(x, x_dtype, ld_x) &&
+                     vec_ok(d_sum, x_dtype, ld_sum) && vec_ok(d_x, x_dtype, H) &&
+                     vec_ok(weight, weight_dtype, H);
+    const bool db = d_dtype == MOE_DTYPE_BF16, xb = x_dtype == MOE_DTYPE_BF16;
+    const Shape run = norm_shape(H, vec ? 2 : 1);  // as many rows per CTA as s
+    moe_status_t r;
+    if (vec)
+      r = db ? (xb ? launch_norm_grad<true, true, true>(p, run, grid, st)
+                   : launch_norm_grad<true, false, true>(p, run, grid, st))
+             : (xb ? launch_norm_grad<false, true, true>(p, run, grid, st)
+                   : launch_norm_grad<false, false, true>(p, run, grid, st));
+    else
+      r = db ? (xb ? launch_norm_grad<true, true, false>(p, run, grid, st)
+                   : launch_norm_grad<true, false, false>(p, run, grid, st))
+             : (xb ? launch_norm_grad<false, true, false>(p, run, grid, st)
+                   : launch_norm_grad<false, false, false>(p, run, grid, st));
+    if (r) return r;
+  }
+  const float* part = static_cast<const float*>(workspace);
+  if (d_weight) {
+    const moe_status_t r = moe_host::column_sums(part, T ? grid : 0, 2 * (int64_t)H, H, d_weight, st);
+    if (r) return r;
+  }
+  if (d_bias) return moe_host::column_sums(part + H, T ? grid : 0, 2 * (int64_t)H, H, d_bias, st);
+  return MOE_OK;
+}
