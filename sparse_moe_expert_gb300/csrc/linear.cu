@@ -34,23 +34,41 @@ namespace {
 constexpr int kTileThreads = 256;
 constexpr int kTileM = 128;
 constexpr int kTileMaxSplit = 8;
-__host__ __device__ constexpr int tile_stages(int BN) { return BN == 64 ? 4 : 3; }
+constexpr int kTileMaxStages = 8;
 __host__ __device__ constexpr int tile_stage_bytes(int BN) { return (kTileM + BN) * 128; }
-constexpr size_t tile_smem(int BN) {
-  const size_t ring = (size_t)tile_stages(BN) * tile_stage_bytes(BN);
+// Stages that leave room for two CTAs per SM, and those that take all of it.
+constexpr int tile_stages(int BN, bool alone) { return (alone ? 196608 : 98304) / tile_stage_bytes(BN); }
+constexpr size_t tile_smem(int BN, bool alone) {
+  const size_t ring = (size_t)tile_stages(BN, alone) * tile_stage_bytes(BN);
   const size_t sums = (size_t)kTileM * (BN + 4) * 4;
   return (ring > sums ? ring : sums) + 1024;
+}
+
+// By one thread.
+__device__ __forceinline__ void tile_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                         uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on `bar` once the products this thread issued are done.
+__device__ __forceinline__ void tile_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+      : "memory");
 }
 
 template <int BN, bool A_ROW, bool B_ROW, bool SWIGLU>
 __global__ void __launch_bounds__(kTileThreads, 2)
     linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                       LinearEpi e, int K, int splits, int m_tiles, unsigned int* err) {
-  constexpr int kStages = tile_stages(BN);
+                       LinearEpi e, int K, int splits, int stages, int m_tiles, unsigned int* err) {
   constexpr int kStageBytes = tile_stage_bytes(BN);
   constexpr int kOut = SWIGLU ? BN / 2 : BN;  // output columns of the tile
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t full[kStages], empty[kStages], done;
+  __shared__ __align__(8) uint64_t full[kTileMaxStages], empty[kTileMaxStages], done;
   __shared__ uint32_t tmem_sh;
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -61,7 +79,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
   const int kb0 = (int)((int64_t)rank * nkb / splits);
   const int nb = (int)((int64_t)(rank + 1) * nkb / splits) - kb0;
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -79,18 +97,16 @@ __global__ void __launch_bounds__(kTileThreads, 2)
   pdl_trigger();  // after the allocation: a later kernel may not take TMEM from a CTA still to come
   const uint32_t tmem = tmem_sh;
   int bad = 0;
+  // one lane of a warp loads, one of another issues the products
   if (warp == 0) {
-    int issued = 0;
-    for (int kb = 0; kb < nb; ++kb) {
-      const int s = kb % kStages;
-      if (kb >= kStages) {
-        bad |= !mbar_wait_sleep(&empty[s], (uint32_t)(kb / kStages - 1) & 1u, kWaitBudgetCycles);
-        if (__any_sync(0xFFFFFFFFu, bad)) {
+    if (elected()) {
+      int issued = 0;
+      uint32_t phase = 0;
+      for (int kb = 0, s = 0; kb < nb; ++kb) {
+        if (kb >= stages && !mbar_wait(&empty[s], phase ^ 1u, kWaitBudgetCycles)) {
           bad = 1;
           break;
         }
-      }
-      if (lane == 0) {
         unsigned char* a = smem + s * kStageBytes;
         unsigned char* b = a + kTileM * 128;
         const int k = (kb0 + kb) * kLinBK;
@@ -110,32 +126,41 @@ __global__ void __launch_bounds__(kTileThreads, 2)
 #pragma unroll
           for (int j = 0; j < BN / 64; ++j) linear_tma_2d(b + j * 8192, &tm_b, col0 + j * 64, k, &full[s]);
         }
+        issued = kb + 1;
+        if (++s == stages) {
+          s = 0;
+          phase ^= 1u;
+        }
       }
-      issued = kb + 1;
+      if (bad)  // copies in flight end before the CTA may
+        for (int kb = issued > stages ? issued - stages : 0; kb < issued; ++kb)
+          mbar_wait(&full[kb % stages], (uint32_t)(kb / stages) & 1u, kWaitBudgetCycles);
     }
-    if (bad)  // copies in flight end before the CTA may
-      for (int kb = issued > kStages ? issued - kStages : 0; kb < issued; ++kb)
-        mbar_wait_sleep(&full[kb % kStages], (uint32_t)(kb / kStages) & 1u, kWaitBudgetCycles);
   } else if (warp == 1) {
-    const uint32_t idesc = idesc_linear<A_ROW, B_ROW>(kTileM, BN);
-    for (int kb = 0; kb < nb; ++kb) {
-      const int s = kb % kStages;
-      bad |= !mbar_wait_sleep(&full[s], (uint32_t)(kb / kStages) & 1u, kWaitBudgetCycles);
-      if (__any_sync(0xFFFFFFFFu, bad)) {
-        bad = 1;
-        break;
-      }
-      tc_fence_after();
-      const uint64_t ad = operand_desc<A_ROW>(smem + s * kStageBytes);
-      const uint64_t bd = operand_desc<B_ROW>(smem + s * kStageBytes + kTileM * 128);
+    if (elected()) {
+      const uint32_t idesc = idesc_linear<A_ROW, B_ROW>(kTileM, BN);
+      const uint64_t a_desc = operand_desc<A_ROW>(smem), b_desc = operand_desc<B_ROW>(smem + kTileM * 128);
+      uint32_t phase = 0;
+      for (int kb = 0, s = 0; kb < nb; ++kb) {
+        if (!mbar_wait(&full[s], phase, kWaitBudgetCycles)) {
+          bad = 1;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t ad = a_desc + s * (kStageBytes >> 4), bd = b_desc + s * (kStageBytes >> 4);
+        tile_mma(tmem, ad, bd, idesc, kb > 0);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        umma_bf16(tmem, ad + k * operand_step<A_ROW>(), bd + k * operand_step<B_ROW>(), idesc,
-                  kb > 0 || k > 0);
-      umma_commit(&empty[s]);
+        for (int k = 1; k < 4; ++k)
+          tile_mma(tmem, ad + k * operand_step<A_ROW>(), bd + k * operand_step<B_ROW>(), idesc, 1);
+        tile_commit(&empty[s]);
+        if (++s == stages) {
+          s = 0;
+          phase ^= 1u;
+        }
+      }
+      tile_commit(&done);
+      if (!mbar_wait(&done, 0u, kWaitBudgetCycles)) bad = 1;
     }
-    umma_commit(&done);
-    bad |= !mbar_wait_sleep(&done, 0u, kWaitBudgetCycles);
   }
   __syncwarp();
   bad = __syncthreads_or(bad);
@@ -199,54 +224,76 @@ __global__ void __launch_bounds__(kTileThreads, 2)
 }
 
 template <int BN, bool A_ROW, bool B_ROW, bool SWIGLU>
-moe_status_t launch_tiles(const LinearOp& a, const LinearOp& b, int K, const LinearEpi& e,
+moe_status_t launch_tiles(const LinearOp& a, const LinearOp& b, int K, const LinearEpi& e, int splits,
                           cudaStream_t st) {
   constexpr int kOut = SWIGLU ? BN / 2 : BN;
   constexpr auto kern = linear_tile_kernel<BN, A_ROW, B_ROW, SWIGLU>;
   const int m_tiles = (e.M + kTileM - 1) / kTileM;
   const int64_t tiles = (int64_t)m_tiles * ((e.cols + kOut - 1) / kOut);
   if (tiles > (INT32_MAX / kTileMaxSplit)) return MOE_ERR_INVALID_ARG;
-  // CTAs that share a tile's K: while the GPU holds twice as many and each
-  // still gets four blocks of 64
-  const int nkb = (K + kLinBK - 1) / kLinBK;
-  int splits = 1;
-  while (splits < kTileMaxSplit && tiles * splits * 2 <= 2 * moe_host::sm_count() &&
-         nkb >= splits * 2 * 4)
-    splits *= 2;
   CUtensorMap ta, tb;
   if (!linear_map(&ta, a, e.M, K, kTileM) || !linear_map(&tb, b, e.N, K, SWIGLU ? kOut : BN))
     return MOE_ERR_CUDA;
-  if (const moe_status_t s = moe_host::allow_smem<kern>(tile_smem(BN))) return s;
-  return moe_host::launch_clusters(kern, dim3((unsigned)(tiles * splits)), kTileThreads, tile_smem(BN),
-                                   dim3(splits, 1, 1), st, ta, tb, e, K, splits, m_tiles,
+  if (const moe_status_t s = moe_host::allow_smem<kern>(tile_smem(BN, true))) return s;
+  const bool alone = tiles * splits <= moe_host::sm_count();
+  return moe_host::launch_clusters(kern, dim3((unsigned)(tiles * splits)), kTileThreads,
+                                   tile_smem(BN, alone), dim3(splits, 1, 1), st, ta, tb, e, K, splits,
+                                   tile_stages(BN, alone), m_tiles,
                                    moe_host::device_error_word());
 }
 
 template <int BN>
-moe_status_t tiles_as(const LinearOp& a, const LinearOp& b, int K, const LinearEpi& e, cudaStream_t st) {
-  if (e.act == MOE_ACT_SWIGLU) return launch_tiles<BN, true, true, true>(a, b, K, e, st);
+moe_status_t tiles_as(const LinearOp& a, const LinearOp& b, int K, const LinearEpi& e, int splits,
+                      cudaStream_t st) {
+  if (e.act == MOE_ACT_SWIGLU) return launch_tiles<BN, true, true, true>(a, b, K, e, splits, st);
   if (a.row_major)
-    return b.row_major ? launch_tiles<BN, true, true, false>(a, b, K, e, st)
-                       : launch_tiles<BN, true, false, false>(a, b, K, e, st);
-  return launch_tiles<BN, false, false, false>(a, b, K, e, st);
+    return b.row_major ? launch_tiles<BN, true, true, false>(a, b, K, e, splits, st)
+                       : launch_tiles<BN, true, false, false>(a, b, K, e, splits, st);
+  return launch_tiles<BN, false, false, false>(a, b, K, e, splits, st);
+}
+
+// Width and splits of the small tiles by an estimate in us, fitted to
+// measurements over M 40 .. 512, N and K 256 .. 11008 (every width with every
+// split): a block of 64 k takes .14 us (64 columns) or .215 (128) with a CTA per
+// SM and twice as long with two; joining splits costs more the more CTAs there
+// are.  What it takes is 2 % slower than the best of them in the mean, 22 % at
+// worst (128 x 256 x 11008: 5.8 us for 4.8).
+struct TileChoice {
+  int bn, splits;
+  float us;
+};
+TileChoice choose_tiles(const LinearEpi& e, int K) {
+  const int sms = moe_host::sm_count(), nkb = (K + kLinBK - 1) / kLinBK;
+  const int64_t m_tiles = (e.M + kTileM - 1) / kTileM;
+  TileChoice best{64, 1, 1e30f};
+  for (int bn = 64; bn <= 128; bn += 64)
+    for (int splits = 1; splits <= kTileMaxSplit; splits *= 2) {
+      const int span = e.act == MOE_ACT_SWIGLU ? bn / 2 : bn;
+      const int64_t ctas = m_tiles * ((e.cols + span - 1) / span) * splits;
+      if (splits > 1 && (nkb < splits * 4 || ctas > 2 * sms)) break;
+      const int per = (nkb + splits - 1) / splits;
+      const float join = splits == 1 ? 0.0f : splits == 2 ? 0.4f : splits == 4 ? 1.2f : 4.0f;
+      const float crowd = ctas <= sms / 2 ? 1.0f : ctas <= sms ? 1.5f : 6.0f;
+      const int64_t rounds = (ctas + 2 * sms - 1) / (2 * sms);
+      const float us = (bn == 64 ? 3.4f : 4.6f) + join * crowd +
+                       (ctas <= sms ? per * (bn == 64 ? 0.14f : 0.215f)
+                                    : rounds * (per * (bn == 64 ? 0.29f : 0.40f) + 1.5f));
+      if (us < best.us) best = {bn, splits, us};
+    }
+  return best;
 }
 
 }  // namespace
-
-moe_status_t linear_tiles(const LinearOp& a, const LinearOp& b, int K, const LinearEpi& e,
-                          cudaStream_t st) {
-  const int64_t m_tiles = (e.M + kTileM - 1) / kTileM;
-  // narrow tiles while there are fewer wide ones than SMs
-  if (m_tiles * ((e.N + 127) / 128) < moe_host::sm_count()) return tiles_as<64>(a, b, K, e, st);
-  return tiles_as<128>(a, b, K, e, st);
-}
 
 moe_status_t linear_product(const LinearOp& a, const LinearOp& b, int K, LinearEpi e, cudaStream_t st) {
   using moe_host::aligned16;
   e.vec = e.cols % 8 == 0 && aligned16(e.out) && aligned16(e.residual) && aligned16(e.preact) &&
           aligned16(e.bias);
   if (a.row_major && b.row_major && e.M <= kLinearRowsMost) return linear_rows(a.p, a.ld, b.p, K, e, st);
-  return linear_tiles(a, b, K, e, st);
+  const TileChoice t = choose_tiles(e, K);
+  // a pair's tile has 256 rows: with 128 or fewer half of it would be empty
+  if (e.M > 128 && linear_pairs_us(e, K, b.row_major) < t.us) return linear_pairs(a, b, K, e, st);
+  return t.bn == 64 ? tiles_as<64>(a, b, K, e, t.splits, st) : tiles_as<128>(a, b, K, e, t.splits, st);
 }
 
 }  // namespace moe

@@ -143,6 +143,13 @@ __host__ __device__ constexpr uint32_t idesc_linear(int M, int N) {
   return idesc_bf16(M, N) | (A_ROW ? 0u : 1u << 15) | (B_ROW ? 0u : 1u << 16);
 }
 
+// True in the one lane that issues for its warp, the same one every time.
+__device__ __forceinline__ bool elected() {
+  uint32_t on;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(on));
+  return on != 0;
+}
+
 __device__ __forceinline__ void linear_tma_2d(void* dst, const CUtensorMap* tm, int c0, int c1,
                                               uint64_t* bar) {
   asm volatile(
@@ -155,9 +162,11 @@ __device__ __forceinline__ void linear_tma_2d(void* dst, const CUtensorMap* tm, 
 // Map of an operand: boxes of 64 k x `box_rows` rows, or of 64 rows x 64 k.
 bool linear_map(CUtensorMap* m, const LinearOp& op, int rows, int K, int box_rows);
 
-// D = A B^T for M rows of A and e.N rows of B; more than a few rows of A.
-moe_status_t linear_tiles(const LinearOp& a, const LinearOp& b, int K, const LinearEpi& e,
+// D = A B^T for M rows of A and e.N rows of B, by pairs of CTAs, and the time this
+// takes, estimated in us.
+moe_status_t linear_pairs(const LinearOp& a, const LinearOp& b, int K, const LinearEpi& e,
                           cudaStream_t st);
+float linear_pairs_us(const LinearEpi& e, int K, bool b_rows);
 // The same for up to kLinearRowsMost rows of A, both operands in rows.
 constexpr int kLinearRowsMost = 32;
 moe_status_t linear_rows(const uint16_t* x, int64_t ldx, const uint16_t* w, int K,

@@ -1,0 +1,330 @@
+// The dense product for many rows: pairs of CTAs on 256 x BN tiles.
+//
+// Two SMs of a cluster share one tile (tcgen05 cta_group::2): each holds 128 rows
+// of A, half of B's rows and the sums of its own rows, and the even CTA issues
+// the products for both, so a byte of B read from L2 serves 256 rows.  With one
+// CTA per 128 x 128 tile (linear.cu) each SM would have to take in 32 KB per 64 k
+// and 256 cycles; the pair takes 32 KB per 512 cycles.  Persistent: one warp
+// loads (TMA, a ring of k-blocks of 64), one issues the products (a single lane
+// each), eight take the
+// sums of the tile before out of the second half of TMEM meanwhile.  Tiles run
+// through A's rows eight tiles at a time, so that a wave of pairs meets in L2.
+#include "linear.cuh"
+
+#include "lora.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kPairThreads = 320;
+constexpr int kPairEpiWarps = 8;
+constexpr int kPairM = 256;
+constexpr int kPairGroup = 8;  // row tiles that are walked together
+constexpr int kPairTmem = 512;
+
+constexpr int kPairN = 256;    // widest tile
+constexpr int kPairStages = 6;
+constexpr int kPairStageBytes = (128 + kPairN / 2) * 128;
+constexpr size_t kPairSmem = (size_t)kPairStages * kPairStageBytes + 1024;
+
+// As linear_tma_2d, on a barrier of either CTA of the pair (`bar` as the
+// cluster has it).
+__device__ __forceinline__ void pair_tma_2d(void* dst, const CUtensorMap* tm, int c0, int c1,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+
+// By one thread of the even CTA, for the pair.
+__device__ __forceinline__ void pair_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                         uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Arrive on this barrier of both CTAs once the products this thread issued are done.
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+__device__ __forceinline__ void remote_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Tile t of m_tiles x n_tiles.
+__device__ __forceinline__ int2 pair_tile(int t, int m_tiles, int n_tiles) {
+  const int per = kPairGroup * n_tiles, g = t / per, r = t - g * per;
+  const int rows = min(kPairGroup, m_tiles - g * kPairGroup);
+  return make_int2(g * kPairGroup + r % rows, r / rows);
+}
+
+template <bool A_ROW, bool B_ROW, bool SWIGLU>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                       LinearEpi e, int K, int bn, int m_tiles, int n_tiles, unsigned int* err) {
+  constexpr int kStages = kPairStages, kStageBytes = kPairStageBytes;
+  const int span = SWIGLU ? bn / 2 : bn;  // output columns of a tile
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t full[kStages], empty[kStages], sums_full[2], sums_empty[2], drain;
+  __shared__ uint32_t tmem_sh;
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int cta = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int nkb = (K + kLinBK - 1) / kLinBK, tiles = m_tiles * n_tiles;
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sums_full[b], 1);
+      mbar_init(&sums_empty[b], 2 * kPairEpiWarps);
+    }
+    mbar_init(&drain, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&tmem_sh)),
+                 "r"(kPairTmem)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_barrier();  // the other CTA's barriers are there as well
+  tc_fence_after();
+  pdl_wait();
+  pdl_trigger();
+  const uint32_t tmem = tmem_sh;
+  // One lane of a warp runs each of the first two roles: with all lanes at the
+  // barriers the loops took some 600 cycles per block of k, more than its products.
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (mbar_wait(bar, parity, kWaitBudgetCycles)) return true;
+    raise_device_error(err, MOE_DEVERR_TIMEOUT);
+    return false;
+  };
+  if (warp == 0) {
+    if (elected()) {
+      int s = 0;
+      uint32_t phase = 0;
+      int64_t issued = 0;
+      bool ok = true;
+      const uint32_t bar0 = cluster_addr(full, 0);  // the even CTA's
+      for (int t = pair; ok && t < tiles; t += pairs) {
+        const int2 at = pair_tile(t, m_tiles, n_tiles);
+        const int row0 = at.x * kPairM + cta * 128;
+        const int col0 = SWIGLU ? cta * e.cols + at.y * span : at.y * span + cta * (bn / 2);
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (issued >= kStages && !(ok = wait(&empty[s], phase ^ 1u))) break;
+          unsigned char* a = smem + s * kStageBytes;
+          unsigned char* b = a + 128 * 128;
+          const uint32_t bar = bar0 + s * 8;
+          const int k = kb * kLinBK;
+          if (cta == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(256 + bn) * 128);
+          if constexpr (A_ROW) {
+            pair_tma_2d(a, &tm_a, k, row0, bar);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) pair_tma_2d(a + j * 8192, &tm_a, row0 + j * 64, k, bar);
+          }
+          if constexpr (B_ROW) {
+            pair_tma_2d(b, &tm_b, k, col0, bar);
+          } else {
+            for (int j = 0; j < bn / 128; ++j) pair_tma_2d(b + j * 8192, &tm_b, col0 + j * 64, k, bar);
+          }
+          ++issued;
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok && cta == 0) {  // copies in flight end before the pair may
+        const int64_t first = issued > kStages ? issued - kStages : 0;
+        for (int64_t i = first; i < issued; ++i)
+          mbar_wait(&full[i % kStages], (uint32_t)(i / kStages) & 1u, kWaitBudgetCycles);
+      }
+    }
+  } else if (warp == 1) {
+    if (cta == 0 && elected()) {
+      const uint32_t idesc = idesc_linear<A_ROW, B_ROW>(kPairM, bn);
+      const uint64_t a_desc = operand_desc<A_ROW>(smem);
+      const uint64_t b_desc = operand_desc<B_ROW>(smem + 128 * 128);
+      int s = 0;
+      uint32_t phase = 0;
+      int i = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < tiles; t += pairs, ++i) {
+        const int buf = i & 1;
+        if (i >= 2 && !(ok = wait(&sums_empty[buf], (uint32_t)((i >> 1) - 1) & 1u))) break;
+        const uint32_t d = tmem + buf * kPairN;
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!(ok = wait(&full[s], phase))) break;
+          tc_fence_after();
+          const uint64_t ad = a_desc + s * (kStageBytes >> 4), bd = b_desc + s * (kStageBytes >> 4);
+          pair_mma(d, ad, bd, idesc, kb > 0);
+#pragma unroll
+          for (int k = 1; k < 4; ++k)
+            pair_mma(d, ad + k * operand_step<A_ROW>(), bd + k * operand_step<B_ROW>(), idesc, 1);
+          pair_commit(&empty[s]);
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+        if (ok) pair_commit(&sums_full[buf]);
+      }
+      if (!ok) {  // products in flight end before the pair may
+        pair_commit(&drain);
+        mbar_wait(&drain, 0u, kWaitBudgetCycles);
+      }
+    }
+  } else {
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    int i = 0;
+    for (int t = pair; t < tiles; t += pairs, ++i) {
+      const int buf = i & 1;
+      int ok = mbar_wait_sleep(&sums_full[buf], (uint32_t)(i >> 1) & 1u, kWaitBudgetCycles);
+      if (!__all_sync(0xFFFFFFFFu, ok)) {
+        raise_device_error(err, MOE_DEVERR_TIMEOUT);
+        break;
+      }
+      tc_fence_after();
+      const int2 at = pair_tile(t, m_tiles, n_tiles);
+      const int64_t row = (int64_t)at.x * kPairM + cta * 128 + quad * 32 + lane;
+      const uint32_t base = tmem + buf * kPairN + ((uint32_t)(quad * 32) << 16);
+#pragma unroll 1
+      for (int c = half * 16; c < span; c += 32) {
+        uint32_t r[2][16];
+        tmem_ld16(base + c, r[0]);
+        if constexpr (SWIGLU) tmem_ld16(base + span + c, r[1]);
+        tmem_ld_wait();
+        if (c + 32 >= span) {  // the sums are in registers
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) remote_arrive(cluster_addr(&sums_empty[buf], 0));
+        }
+        if (row < e.M) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            float z[8], u[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              z[x] = __uint_as_float(r[0][q * 8 + x]);
+              if constexpr (SWIGLU) u[x] = __uint_as_float(r[1][q * 8 + x]);
+            }
+            finish8<SWIGLU>(e, row, at.y * span + c + q * 8, z, u);
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_barrier();  // neither CTA leaves while the other may still signal it
+  tc_fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kPairTmem)
+                 : "memory");
+}
+
+// Pairs that the current device holds at once.
+template <auto Kernel>
+int pairs_resident(size_t smem) {
+  static std::atomic<int> known[moe_host::kMaxCachedDevices] = {};
+  std::atomic<int>& mine = known[moe_host::device_index()];
+  int n = mine.load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (moe_host::sm_count() / 2));
+    cfg.blockDim = dim3(kPairThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, Kernel, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = moe_host::sm_count() / 2;
+    }
+    mine.store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+// Columns of a tile: the width whose waves cost least.  A block of 64 k takes a
+// time like bn + 217 (8192^3, ns per block at 256, 224, 192, 160, 128, 96: 322,
+// 288, 266, 249, 228, 208), so a narrower tile pays where it fills the last wave:
+// us at 256 and at the width taken, 3001 x 11008 x 4096 179, 163 (224), 4096 x 2048
+// x 1536 SwiGLU 28.4, 23.6 (192), 4096^3 91, 83 (224).  A B by columns comes in
+// blocks of 64 rows for each CTA, and SwiGLU's halves are whole chunks of the
+// epilogue.
+struct PairChoice {
+  int bn;
+  int64_t waves;
+};
+PairChoice choose_pairs(const LinearEpi& e, int pairs, bool b_rows) {
+  const int64_t m_tiles = (e.M + kPairM - 1) / kPairM;
+  const int unit = e.act == MOE_ACT_SWIGLU ? 32 : b_rows ? 16 : 128;
+  PairChoice best{0, 0};
+  for (int bn = kPairN; bn >= 96; bn -= unit) {
+    const int span = e.act == MOE_ACT_SWIGLU ? bn / 2 : bn;
+    const int64_t waves = (m_tiles * ((e.cols + span - 1) / span) + pairs - 1) / pairs;
+    if (!best.bn || waves * (bn + 217) < best.waves * (best.bn + 217)) best = {bn, waves};
+  }
+  return best;
+}
+
+template <bool A_ROW, bool B_ROW, bool SWIGLU>
+moe_status_t launch_pairs(const LinearOp& a, const LinearOp& b, int K, const LinearEpi& e,
+                          cudaStream_t st) {
+  constexpr auto kern = linear_pair_kernel<A_ROW, B_ROW, SWIGLU>;
+  if (const moe_status_t s = moe_host::allow_smem<kern>(kPairSmem)) return s;
+  const int most = pairs_resident<kern>(kPairSmem);
+  const int m_tiles = (e.M + kPairM - 1) / kPairM;
+  const int bn = choose_pairs(e, most, B_ROW).bn;
+  const int span = SWIGLU ? bn / 2 : bn, n_tiles = (e.cols + span - 1) / span;
+  if ((int64_t)m_tiles * n_tiles > INT32_MAX / 2) return MOE_ERR_INVALID_ARG;
+  CUtensorMap ta, tb;
+  if (!linear_map(&ta, a, e.M, K, 128) || !linear_map(&tb, b, e.N, K, bn / 2)) return MOE_ERR_CUDA;
+  const int tiles = m_tiles * n_tiles;
+  return moe_host::launch_clusters(kern, dim3(2 * (tiles < most ? tiles : most)), kPairThreads,
+                                   kPairSmem, dim3(2, 1, 1), st, ta, tb, e, K, bn, m_tiles, n_tiles,
+                                   moe_host::device_error_word());
+}
+
+}  // namespace
+
+// Fitted to the same measurements as the small tiles' estimate (linear.cu).
+float linear_pairs_us(const LinearEpi& e, int K, bool b_rows) {
+  const PairChoice c = choose_pairs(e, moe_host::sm_count() < 2 ? 1 : moe_host::sm_count() / 2, b_rows);
+  const float waves = (float)c.waves;
+  return 4.9f + waves * ((K + kLinBK - 1) / kLinBK) * (c.bn + 217) * 0.5e-3f + (waves - 1.0f);
+}
+
+moe_status_t linear_pairs(const LinearOp& a, const LinearOp& b, int K, const LinearEpi& e,
+                          cudaStream_t st) {
+  if (e.act == MOE_ACT_SWIGLU) return launch_pairs<true, true, true>(a, b, K, e, st);
+  if (a.row_major)
+    return b.row_major ? launch_pairs<true, true, false>(a, b, K, e, st)
+                       : launch_pairs<true, false, false>(a, b, K, e, st);
+  return launch_pairs<false, false, false>(a, b, K, e, st);
+}
+
+}  // namespace moe

@@ -66,7 +66,8 @@ def inputs(T, K, N, act, residual, out_dtype, seed=0):
 SIZES = [(1, 8, 1), (1, 64, 16), (1, 4096, 40), (2, 136, 17), (3, 2000, 300), (8, 512, 129),
          (9, 256, 64), (16, 1024, 33), (17, 320, 200), (31, 72, 515), (32, 4096, 128),
          (33, 64, 64), (40, 1000, 77), (64, 1536, 512), (127, 128, 130), (128, 2048, 96),
-         (129, 520, 384), (300, 4096, 1000), (777, 264, 1234), (1000, 96, 2050)]
+         (129, 520, 384), (300, 4096, 1000), (777, 264, 1234), (1000, 96, 2050),
+         (1300, 1032, 2052)]
 
 
 @pytest.mark.parametrize("T,K,N", SIZES)
@@ -96,7 +97,7 @@ def test_selected_entries_are_exact():
     """Whole numbers: every sum is exact, so every entry has to be equal."""
     m = moe()
     g = torch.Generator().manual_seed(0)
-    for T, K, N in ((5, 136, 33), (40, 200, 100), (200, 1032, 333), (513, 4104, 700)):
+    for T, K, N in ((5, 136, 33), (40, 200, 100), (200, 1032, 333), (513, 4104, 700), (1500, 1032, 2104)):
         x = torch.randint(-3, 4, (T, K), generator=g).to(B16).to(dev())
         w = torch.randint(-3, 4, (N, K), generator=g).to(B16).to(dev())
         want = (x.double() @ w.double().t()).float()
@@ -155,7 +156,8 @@ def test_infinities_and_nan_stay_in_their_rows():
 
 
 GRAD_SIZES = [(1, 64, 40), (1, 4096, 17), (3, 136, 300), (7, 8, 8), (33, 256, 129), (64, 1536, 200),
-              (129, 72, 515), (300, 520, 1000), (777, 1024, 130)]
+              (129, 72, 515), (300, 520, 1000), (777, 1024, 130),
+              (1300, 1032, 2052)]
 
 
 @pytest.mark.parametrize("T,K,N", GRAD_SIZES)
