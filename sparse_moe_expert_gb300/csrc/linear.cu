@@ -289,7 +289,12 @@ moe_status_t linear_product(const LinearOp& a, const LinearOp& b, int K, LinearE
   using moe_host::aligned16;
   e.vec = e.cols % 8 == 0 && aligned16(e.out) && aligned16(e.residual) && aligned16(e.preact) &&
           aligned16(e.bias);
-  if (a.row_major && b.row_major && e.M <= kLinearRowsMost) return linear_rows(a.p, a.ld, b.p, K, e, st);
+  // The form for few rows reads x for every 16 rows of W: past 16 rows of x that
+  // shows where W is large (us for 32 rows, this form and tiles: 4096 x 22016 48,
+  // 34; 4096 x 4096 11.4, 10.4; 1536 x 4096 6.4, 9.0; 2048 x 1536 6.1, 7.1).
+  if (a.row_major && b.row_major && e.M <= kLinearRowsMost &&
+      (e.M <= 16 || (int64_t)e.N * K < (1 << 24)))
+    return linear_rows(a.p, a.ld, b.p, K, e, st);
   const TileChoice t = choose_tiles(e, K);
   // a pair's tile has 256 rows: with 128 or fewer half of it would be empty
   if (e.M > 128 && linear_pairs_us(e, K, b.row_major) < t.us) return linear_pairs(a, b, K, e, st);

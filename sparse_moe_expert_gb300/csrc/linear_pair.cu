@@ -197,14 +197,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     int i = 0;
     for (int t = pair; t < tiles; t += pairs, ++i) {
       const int buf = i & 1;
+      const int2 at = pair_tile(t, m_tiles, n_tiles);
+      const int64_t row = (int64_t)at.x * kPairM + cta * 128 + quad * 32 + lane;
+      // the residual's part of the tile comes into L2 during the products
+      if (e.residual && row < e.M) {
+        const int size = e.out_bf16 ? 2 : 4;
+        const int c1 = min(span, e.cols - at.y * span) * size;
+        const char* p = static_cast<const char*>(e.residual) + (row * e.cols + (int64_t)at.y * span) * size;
+        for (int c = half * 128; c < c1; c += 256) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + c));
+      }
       int ok = mbar_wait_sleep(&sums_full[buf], (uint32_t)(i >> 1) & 1u, kWaitBudgetCycles);
       if (!__all_sync(0xFFFFFFFFu, ok)) {
         raise_device_error(err, MOE_DEVERR_TIMEOUT);
         break;
       }
       tc_fence_after();
-      const int2 at = pair_tile(t, m_tiles, n_tiles);
-      const int64_t row = (int64_t)at.x * kPairM + cta * 128 + quad * 32 + lane;
       const uint32_t base = tmem + buf * kPairN + ((uint32_t)(quad * 32) << 16);
 #pragma unroll 1
       for (int c = half * 16; c < span; c += 32) {
