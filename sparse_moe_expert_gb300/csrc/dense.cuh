@@ -130,9 +130,10 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float* part) {
 
 namespace moe_host {
 
-// out[c] (+)= sum over p of part[p, c], in the order of p by parts; part fp32
-// [rows, ld] with columns c < cols, 4-byte aligned.
-moe_status_t column_sums(const float* part, int rows, int64_t ld, int cols, float* out,
+// out[c] = sum over r of part[r, c] for c < cols, then more[c] = the same of the
+// next cols columns (either may be null); part fp32 [rows, ld].  The rows are added
+// in runs, the runs in order.
+moe_status_t column_sums(const float* part, int rows, int64_t ld, int cols, float* out, float* more,
                          cudaStream_t st);
 
 }  // namespace moe_host

@@ -165,7 +165,7 @@ extern "C" moe_status_t moe_linear_backward(const void* d_out, int d_dtype, int6
       cudaGetLastError();
       return MOE_ERR_CUDA;
     }
-    return d_bias ? moe_host::column_sums(nullptr, 0, N, N, d_bias, st) : MOE_OK;
+    return d_bias ? moe_host::column_sums(nullptr, 0, N, N, d_bias, nullptr, st) : MOE_OK;
   }
   const int cols = swiglu ? N / 2 : N;
   if (!d_out || ld_d < cols || (reinterpret_cast<uintptr_t>(d_out) & (d_dtype == MOE_DTYPE_BF16 ? 1u : 3u)))
@@ -197,7 +197,7 @@ extern "C" moe_status_t moe_linear_backward(const void* d_out, int d_dtype, int6
                                         : launch(linear_dz_kernel<false, false>, grid, block, 0, st, p));
     if (r) return r;
     if (d_bias)
-      if (const moe_status_t s = moe_host::column_sums(p.part, (int)dz_runs(T, run), N, N, d_bias, st))
+      if (const moe_status_t s = moe_host::column_sums(p.part, (int)dz_runs(T, run), N, N, d_bias, nullptr, st))
         return s;
   }
   const uint16_t* dz = direct ? static_cast<const uint16_t*>(d_out) : d_preact;

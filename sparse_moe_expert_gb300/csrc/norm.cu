@@ -11,12 +11,14 @@
 // that the sizes fix.  A thread owns columns, and in the gradient it keeps
 // their d_w and d_b over all rows of its CTA; the CTAs' sums are joined by a
 // second kernel in the CTAs' order.
+#include "async.cuh"
 #include "dense.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kNormMaxWidth = 8192;  // 512 threads with two vectors of eight each
+constexpr int kNormWarpRows = 1024;
 constexpr int kNormWarpWidth = 512;  // up to this width a warp takes a row
 
 struct NormParams {
@@ -300,23 +302,339 @@ __global__ void __launch_bounds__(512) layer_norm_backward_kernel(NormGradParams
   }
 }
 
+// ---- many rows of whole vectors ---------------------------------------------------
+
+// Pairs of fp32 values (one instruction for both).
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return ffma2(a, make_float2(1.0f, 1.0f), b); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return ffma2(a, b, make_float2(0.0f, 0.0f)); }
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
+template <bool BF16>
+__device__ __forceinline__ void get2(float2 (&f)[4], const Vec8<BF16>& v) {
+  if constexpr (BF16) {
+    const uint32_t w[4] = {v.q[0].x, v.q[0].y, v.q[0].z, v.q[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = bf16x2_to_f32x2(w[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f[2 * i] = make_float2(__uint_as_float(v.q[i].x), __uint_as_float(v.q[i].y));
+      f[2 * i + 1] = make_float2(__uint_as_float(v.q[i].z), __uint_as_float(v.q[i].w));
+    }
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ void set2(Vec8<BF16>& v, const float2 (&f)[4]) {
+  const float g[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
+  v.set(g);
+}
+__device__ __forceinline__ void load2(float2 (&f)[4], const void* p, int bf16, int col) {
+  if (bf16) {
+    Vec8<true> v;
+    v.load(p, col);
+    get2(f, v);
+  } else {
+    Vec8<false> v;
+    v.load(p, col);
+    get2(f, v);
+  }
+}
+
+// A warp takes a row, which it holds as loaded (packed) between its sums, so no
+// warp waits for another; a bulk copy brings its next row into shared memory
+// meanwhile.  Weight and bias lie there as fp32, [H] each, in front of the rows: from
+// global memory they would not stay in the L1 that is left.  One CTA per SM, its
+// warps as many as registers and shared memory allow.
+constexpr size_t kNormRoom = 200 * 1024;
+// Warps whose rows (4 or 8 registers per vector and lane) the registers hold.
+constexpr int warp_rows_most(bool bf16, int nv) { return nv * (bf16 ? 4 : 8) <= 64 ? 16 : 12; }
+
+template <bool X_BF16, bool OUT_BF16, int NV>
+__global__ void __launch_bounds__(warp_rows_most(X_BF16, NV) * 32, 1)
+    layer_norm_warp_kernel(NormParams p, int stage_bytes, unsigned int* err) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ __align__(8) uint64_t bars[16];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int params = (p.weight ? 1 : 0) + (p.bias ? 1 : 0);
+  float* w_s = reinterpret_cast<float*>(smem);
+  float* b_s = w_s + (p.weight ? p.H : 0);
+  unsigned char* at = smem + (size_t)params * p.H * 4 + (size_t)warp * stage_bytes;
+  uint64_t* bar = bars + warp;
+  const uint32_t x_bytes = p.H * (X_BF16 ? 2 : 4);
+  if (lane == 0) {
+    mbar_init(bar, 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  pdl_wait();
+  pdl_trigger();
+  auto fetch = [&](int64_t t) {  // by lane 0
+    mbar_arrive_expect_tx(bar, p.residual ? 2 * x_bytes : x_bytes);
+    bulk_g2s(at, static_cast<const unsigned char*>(p.x) + t * p.ldx * (X_BF16 ? 2 : 4), x_bytes, bar);
+    if (p.residual)
+      bulk_g2s(at + x_bytes, static_cast<const unsigned char*>(p.residual) + t * p.ldr * (X_BF16 ? 2 : 4),
+               x_bytes, bar);
+  };
+  // neighbouring rows go to different SMs, so that the last turn is shared out
+  const int64_t step = (int64_t)gridDim.x * warps;
+  int64_t t = (int64_t)warp * gridDim.x + blockIdx.x;
+  if (t < p.T && lane == 0) fetch(t);
+  for (int c = threadIdx.x * 8; c < p.H; c += blockDim.x * 8) {
+    float2 f[4];
+    Vec8<false> v;
+    if (p.weight) {
+      load2(f, p.weight, p.w_bf16, c);
+      set2(v, f);
+      v.store(w_s, c);
+    }
+    if (p.bias) {
+      load2(f, p.bias, p.w_bf16, c);
+      set2(v, f);
+      v.store(b_s, c);
+    }
+  }
+  __syncthreads();
+  const float inv_h = 1.0f / (float)p.H;
+  uint32_t phase = 0;
+  for (; t < p.T; t += step, phase ^= 1u) {
+    const bool ok = mbar_wait(bar, phase, kWaitBudgetCycles);
+    if (!__all_sync(0xFFFFFFFFu, ok)) {  // its copy has not ended in a second: nothing else to wait for
+      if (lane == 0) raise_device_error(err, MOE_DEVERR_TIMEOUT);
+      return;
+    }
+    Vec8<X_BF16> x[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * 32 + lane) * 8;
+      if (c < p.H) x[j].load(at, c);
+      else x[j].zero();
+    }
+    if (p.residual) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * 32 + lane) * 8;
+        if (c >= p.H) continue;
+        Vec8<X_BF16> r;
+        float2 f[4], g[4];
+        r.load(at + x_bytes, c);
+        get2(f, x[j]);
+        get2(g, r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = add2(f[i], g[i]);
+        set2(x[j], f);
+        x[j].store(p.summed, t * p.H + c);
+      }
+    }
+    __syncwarp();
+    if (lane == 0 && t + step < p.T) fetch(t + step);
+    float mu = 0.0f;
+    if (!p.rms) {
+      float2 s2[2] = {};
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        float2 f[4];
+        get2(f, x[j]);
+        s2[j & 1] = add2(s2[j & 1], add2(add2(f[0], f[1]), add2(f[2], f[3])));
+      }
+      float s[1] = {(s2[0].x + s2[0].y) + (s2[1].x + s2[1].y)};
+      warp_sum(s);
+      mu = s[0] * inv_h;
+    }
+    float2 q2[2] = {};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if ((j * 32 + lane) * 8 >= p.H) continue;
+      float2 f[4];
+      get2(f, x[j]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 d = add2(f[i], both(-mu));
+        q2[i & 1] = ffma2(d, d, q2[i & 1]);
+      }
+    }
+    float q[1] = {(q2[0].x + q2[0].y) + (q2[1].x + q2[1].y)};
+    warp_sum(q);
+    const float rstd = 1.0f / sqrtf(q[0] * inv_h + p.eps);
+    if (lane == 0) {
+      if (p.mean) p.mean[t] = mu;
+      if (p.rstd) p.rstd[t] = rstd;
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * 32 + lane) * 8;
+      if (c >= p.H) continue;
+      float2 f[4], w[4];
+      get2(f, x[j]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = mul2(add2(f[i], both(-mu)), both(rstd));
+      if (p.weight) {
+        load2(w, w_s, 0, c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], w[i]);
+      }
+      if (p.bias) {
+        load2(w, b_s, 0, c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = add2(f[i], w[i]);
+      }
+      Vec8<OUT_BF16> o;
+      set2(o, f);
+      o.store(p.out, t * p.H + c);
+    }
+  }
+}
+
+// The gradient: bulk copies bring the rows of a CTA's next turns into shared memory
+// while it works on one.  A thread takes eight columns and keeps their weights.
+constexpr int kRingMost = 8;
+struct RingPlan {
+  int threads, per_sm, stages;
+  int stage_bytes;
+};
+
+template <bool D_BF16, bool X_BF16>
+__global__ void __launch_bounds__(1024)
+    layer_norm_backward_ring_kernel(NormGradParams p, int stages, int stage_bytes, unsigned int* err) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ __align__(8) uint64_t full[kRingMost];
+  __shared__ float2 part[2][32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  const int col = tid * 8;
+  const bool on = col < p.H;
+  const uint32_t d_bytes = p.H * (D_BF16 ? 2 : 4), x_bytes = p.H * (X_BF16 ? 2 : 4);
+  if (tid == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+  const int64_t step = gridDim.x;
+  const uint32_t row_bytes = d_bytes + x_bytes + (p.d_sum ? x_bytes : 0);
+  auto fetch = [&](int64_t t, int s) {  // by thread 0
+    unsigned char* at = smem + (size_t)s * stage_bytes;
+    mbar_arrive_expect_tx(&full[s], row_bytes);
+    bulk_g2s(at, static_cast<const unsigned char*>(p.d_out) + t * p.ldd * (D_BF16 ? 2 : 4), d_bytes, &full[s]);
+    bulk_g2s(at + d_bytes, static_cast<const unsigned char*>(p.x) + t * p.ldx * (X_BF16 ? 2 : 4), x_bytes,
+             &full[s]);
+    if (p.d_sum)
+      bulk_g2s(at + d_bytes + x_bytes, static_cast<const unsigned char*>(p.d_sum) + t * p.lds * (X_BF16 ? 2 : 4),
+               x_bytes, &full[s]);
+  };
+  if (tid == 0)
+    for (int s = 0; s < stages; ++s)
+      if (blockIdx.x + s * step < p.T) fetch(blockIdx.x + s * step, s);
+  const float2 zero = make_float2(0.0f, 0.0f);
+  float2 dw[4], db[4], w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    dw[i] = db[i] = zero;
+    w[i] = both(1.0f);
+  }
+  if (on && p.weight) load2(w, p.weight, p.w_bf16, col);
+  const float inv_h = 1.0f / (float)p.H;
+  // the next row's statistics are on their way during this one
+  float mu = 0.0f, rstd = 0.0f;
+  if (blockIdx.x < p.T) {
+    if (p.mean) mu = p.mean[blockIdx.x];
+    rstd = p.rstd[blockIdx.x];
+  }
+  int s = 0, buf = 0, bad = 0;
+  uint32_t phase = 0;
+  for (int64_t t = blockIdx.x; t < p.T; t += step, buf ^= 1) {
+    const float r = rstd, shift = -mu * rstd;
+    if (t + step < p.T) {
+      if (p.mean) mu = p.mean[t + step];
+      rstd = p.rstd[t + step];
+    }
+    if (!mbar_wait(&full[s], phase, kWaitBudgetCycles)) bad = 1;
+    const unsigned char* at = smem + (size_t)s * stage_bytes;
+    float2 c[4], xh[4], s0 = zero, s1 = zero;
+    Vec8<X_BF16> ds;
+    if (on) {
+      Vec8<D_BF16> dv;
+      Vec8<X_BF16> xv;
+      dv.load(at, col);
+      xv.load(at + d_bytes, col);
+      if (p.d_sum) ds.load(at + d_bytes + x_bytes, col);
+      get2(c, dv);
+      get2(xh, xv);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        xh[i] = ffma2(xh[i], both(r), both(shift));
+        db[i] = add2(db[i], c[i]);
+        dw[i] = ffma2(c[i], xh[i], dw[i]);
+        c[i] = mul2(c[i], w[i]);
+        s0 = add2(s0, c[i]);
+        s1 = ffma2(c[i], xh[i], s1);
+      }
+    }
+    float sum[2] = {s0.x + s0.y, s1.x + s1.y};
+    warp_sum(sum);
+    if (lane == 0) part[buf][warp] = make_float2(sum[0], sum[1]);
+    bad = __syncthreads_or(bad);  // and the stage has been read
+    if (bad) break;
+    if (tid == 0 && t + stages * step < p.T) fetch(t + stages * step, s);
+    const float2 mine = lane < warps ? part[buf][lane] : zero;
+    sum[0] = mine.x;
+    sum[1] = mine.y;
+    warp_sum(sum);
+    if (on) {
+      const float2 m0 = both(p.mean ? -r * (sum[0] * inv_h) : 0.0f), m1 = both(-r * (sum[1] * inv_h));
+      float2 g[4];
+      if (p.d_sum) get2(g, ds);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c[i] = ffma2(c[i], both(r), ffma2(xh[i], m1, m0));
+        if (p.d_sum) c[i] = add2(c[i], g[i]);
+      }
+      Vec8<X_BF16> o;
+      set2(o, c);
+      o.store(p.d_x, t * p.H + col);
+    }
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1u;
+    }
+  }
+  if (bad) {  // copies in flight end before the CTA may
+    if (tid == 0) {
+      raise_device_error(err, MOE_DEVERR_TIMEOUT);
+      for (int i = 0; i < stages; ++i) mbar_wait(&full[i], i < s ? phase ^ 1u : phase, kWaitBudgetCycles);
+    }
+    return;
+  }
+  if (!p.part || !on) return;
+  float* out = p.part + (int64_t)blockIdx.x * 2 * p.H;
+  Vec8<false> o;
+  set2(o, dw);
+  o.store(out, col);
+  set2(o, db);
+  o.store(out, p.H + col);
+}
+
 // ---- column sums ---------------------------------------------------------------
 
-constexpr int kColThreads = 512;
+constexpr int kColThreads = 1024;
 constexpr int kColLanes = kColThreads / 32;
 
 // 32 columns per CTA; a warp sums a run of the rows, the runs are added in order.
-__global__ void __launch_bounds__(kColThreads) column_sums_kernel(const float* part, int rows,
-                                                                  int64_t ld, int cols, float* out) {
+__global__ void __launch_bounds__(kColThreads)
+    column_sums_kernel(const float* part, int rows, int64_t ld, int cols, float* out, float* more) {
   __shared__ float sum[kColLanes][32];
   pdl_wait();
   pdl_trigger();
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), lane = threadIdx.x >> 5;
+  if (blockIdx.y) {
+    part += cols;
+    out = more;
+  }
+  if (!out) return;
   const int per = (rows + kColLanes - 1) / kColLanes;
   const int r0 = lane * per, r1 = min(r0 + per, rows);
   float s = 0.0f;
   if (c < cols) {
-#pragma unroll 8
+#pragma unroll 16
     for (int r = r0; r < r1; ++r) s += part[r * ld + c];
   }
   sum[lane][threadIdx.x & 31] = s;
@@ -353,6 +671,19 @@ Shape norm_shape(int H, int want) {
   return {nv, ((vecs + nv - 1) / nv + 31) / 32 * 32, 1};
 }
 
+// A thread for each vector; as many CTAs as make 1024 threads per SM, of narrow
+// rows up to eight; then as many stages as the shared memory holds.
+RingPlan ring_plan(int H, int row_bytes) {
+  RingPlan r;
+  r.threads = (H / 8 + 31) / 32 * 32;
+  r.per_sm = 1024 / r.threads < 8 ? 1024 / r.threads : 8;
+  r.stage_bytes = row_bytes;
+  while (r.per_sm > 1 && (int)kNormRoom / r.per_sm / row_bytes < 2) --r.per_sm;
+  r.stages = (int)kNormRoom / r.per_sm / row_bytes;
+  if (r.stages > kRingMost) r.stages = kRingMost;
+  return r;
+}
+
 template <bool X_BF16, bool OUT_BF16, bool VEC>
 moe_status_t launch_norm(const NormParams& p, const Shape& s, cudaStream_t st) {
   const dim3 grid((unsigned)(((int64_t)p.T + s.rows - 1) / s.rows)), block(s.threads, s.rows);
@@ -371,11 +702,45 @@ moe_status_t launch_norm_grad(const NormGradParams& p, const Shape& s, int grid,
   return launch(layer_norm_backward_kernel<D_BF16, X_BF16, 2, VEC>, grid, block, smem, st, p);
 }
 
-// CTAs of the gradient for rows of this shape.
-int norm_grad_ctas(int64_t T, const Shape& s) {
-  const int64_t most = (int64_t)moe_host::sm_count() * 2;
+// CTAs of the gradient, at most: as many as the workspace has room for.
+int norm_grad_ctas(int64_t T, int H) {
+  const Shape s = norm_shape(H, 2);
+  const int per_sm = s.rows > 1 ? 4 : ring_plan((H + 7) / 8 * 8, 1).per_sm;
+  const int64_t most = (int64_t)moe_host::sm_count() * per_sm;
   const int64_t need = (T + s.rows - 1) / s.rows;
   return (int)(need < most ? need : most);
+}
+
+template <bool D_BF16, bool X_BF16>
+moe_status_t norm_grad_ring(const NormGradParams& p, int& grid, cudaStream_t st) {
+  constexpr auto kern = layer_norm_backward_ring_kernel<D_BF16, X_BF16>;
+  const RingPlan r = ring_plan(p.H, p.H * ((D_BF16 ? 2 : 4) + (X_BF16 ? 2 : 4) * (p.d_sum ? 2 : 1)));
+  const int most = moe_host::sm_count() * r.per_sm;
+  if (grid > most) grid = most;
+  if (const moe_status_t s = moe_host::allow_smem<kern>(kNormRoom)) return s;
+  return moe_host::launch(kern, dim3(grid), dim3(r.threads), (size_t)r.stages * r.stage_bytes, st, p,
+                          r.stages, r.stage_bytes, moe_host::device_error_word());
+}
+
+template <bool X_BF16, bool OUT_BF16, int NV>
+moe_status_t launch_norm_warps(const NormParams& p, cudaStream_t st) {
+  constexpr auto kern = layer_norm_warp_kernel<X_BF16, OUT_BF16, NV>;
+  const int row_bytes = p.H * (X_BF16 ? 2 : 4) * (p.residual ? 2 : 1);
+  const int params = ((p.weight ? 1 : 0) + (p.bias ? 1 : 0)) * p.H * 4;
+  const int room = ((int)kNormRoom - params) / row_bytes, most = warp_rows_most(X_BF16, NV);
+  const int warps = room < most ? room : most;
+  if (const moe_status_t s = moe_host::allow_smem<kern>(kNormRoom)) return s;
+  return moe_host::launch(kern, dim3(moe_host::sm_count()), dim3(warps * 32),
+                          (size_t)params + (size_t)warps * row_bytes, st, p, row_bytes, moe_host::device_error_word());
+}
+
+template <bool X_BF16, bool OUT_BF16>
+moe_status_t norm_warps(const NormParams& p, cudaStream_t st) {
+  if (p.H <= 1024) return launch_norm_warps<X_BF16, OUT_BF16, 4>(p, st);
+  if (p.H <= 2048) return launch_norm_warps<X_BF16, OUT_BF16, 8>(p, st);
+  if constexpr (X_BF16)
+    if (p.H > 4096) return launch_norm_warps<X_BF16, OUT_BF16, 32>(p, st);
+  return launch_norm_warps<X_BF16, OUT_BF16, 16>(p, st);
 }
 
 }  // namespace
@@ -383,11 +748,11 @@ int norm_grad_ctas(int64_t T, const Shape& s) {
 
 namespace moe_host {
 
-moe_status_t column_sums(const float* part, int rows, int64_t ld, int cols, float* out,
+moe_status_t column_sums(const float* part, int rows, int64_t ld, int cols, float* out, float* more,
                          cudaStream_t st) {
   if (cols == 0) return MOE_OK;
-  return launch(moe::column_sums_kernel, dim3((cols + 31) / 32), dim3(moe::kColThreads), 0, st, part,
-                rows, ld, cols, out);
+  return launch(moe::column_sums_kernel, dim3((cols + 31) / 32, more ? 2 : 1), dim3(moe::kColThreads), 0,
+                st, part, rows, ld, cols, out, more);
 }
 
 }  // namespace moe_host
@@ -418,6 +783,9 @@ extern "C" moe_status_t moe_layer_norm(const void* x, int x_dtype, int64_t ld_x,
   const Shape s = norm_shape(H, vec && T > moe_host::sm_count() ? 2 : 1);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool xb = x_dtype == MOE_DTYPE_BF16, ob = out_dtype == MOE_DTYPE_BF16;
+  if (vec && H > kNormWarpWidth && (xb || H <= 4096) && T >= kNormWarpRows)
+    return xb ? (ob ? norm_warps<true, true>(p, st) : norm_warps<true, false>(p, st))
+              : (ob ? norm_warps<false, true>(p, st) : norm_warps<false, false>(p, st));
   if (vec)
     return xb ? (ob ? launch_norm<true, true, true>(p, s, st) : launch_norm<true, false, true>(p, s, st))
               : (ob ? launch_norm<false, true, true>(p, s, st) : launch_norm<false, false, true>(p, s, st));
@@ -428,7 +796,7 @@ extern "C" moe_status_t moe_layer_norm(const void* x, int x_dtype, int64_t ld_x,
 extern "C" size_t moe_layer_norm_workspace_size(int T, int H) {
   using namespace moe;
   if (T < 1 || H < 1 || H > kNormMaxWidth) return 16;
-  return (size_t)norm_grad_ctas(T, norm_shape(H, 2)) * 2 * H * sizeof(float);
+  return (size_t)norm_grad_ctas(T, H) * 2 * H * sizeof(float);
 }
 
 extern "C" moe_status_t moe_layer_norm_backward(
@@ -442,8 +810,7 @@ extern "C" moe_status_t moe_layer_norm_backward(
   if (!moe_host::aligned4(d_weight) || !moe_host::aligned4(d_bias)) return MOE_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool sums = d_weight || d_bias;
-  const Shape s = norm_shape(H, 2);
-  const int grid = norm_grad_ctas(T, s);
+  int grid = norm_grad_ctas(T, H);
   if (T > 0) {
     if (!d_out || !x || !rstd || !d_x || ld_d < H || ld_x < H || (d_sum && ld_sum < H))
       return MOE_ERR_INVALID_ARG;
@@ -462,9 +829,12 @@ extern "C" moe_status_t moe_layer_norm_backward(
                      vec_ok(d_sum, x_dtype, ld_sum) && vec_ok(d_x, x_dtype, H) &&
                      vec_ok(weight, weight_dtype, H);
     const bool db = d_dtype == MOE_DTYPE_BF16, xb = x_dtype == MOE_DTYPE_BF16;
-    const Shape run = norm_shape(H, vec ? 2 : 1);  // as many rows per CTA as s
+    const Shape run = norm_shape(H, vec ? 2 : 1);
     moe_status_t r;
-    if (vec)
+    if (vec && run.rows == 1)
+      r = db ? (xb ? norm_grad_ring<true, true>(p, grid, st) : norm_grad_ring<true, false>(p, grid, st))
+             : (xb ? norm_grad_ring<false, true>(p, grid, st) : norm_grad_ring<false, false>(p, grid, st));
+    else if (vec)
       r = db ? (xb ? launch_norm_grad<true, true, true>(p, run, grid, st)
                    : launch_norm_grad<true, false, true>(p, run, grid, st))
              : (xb ? launch_norm_grad<false, true, true>(p, run, grid, st)
@@ -476,11 +846,7 @@ extern "C" moe_status_t moe_layer_norm_backward(
                    : launch_norm_grad<false, false, false>(p, run, grid, st));
     if (r) return r;
   }
-  const float* part = static_cast<const float*>(workspace);
-  if (d_weight) {
-    const moe_status_t r = moe_host::column_sums(part, T ? grid : 0, 2 * (int64_t)H, H, d_weight, st);
-    if (r) return r;
-  }
-  if (d_bias) return moe_host::column_sums(part + H, T ? grid : 0, 2 * (int64_t)H, H, d_bias, st);
-  return MOE_OK;
+  if (!sums) return MOE_OK;
+  return moe_host::column_sums(static_cast<const float*>(workspace), T ? grid : 0, 2 * (int64_t)H, H,
+                               d_weight, d_bias, st);
 }
