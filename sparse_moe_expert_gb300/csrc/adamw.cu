@@ -8,9 +8,12 @@
 //   sqrt v = s (c / 255)^2,           s = max sqrt v,  c >= 1 where v > 0
 // so that small values keep a relative step (1 / c) and a second moment never
 // becomes zero, which would let its update grow without bound.  The step itself
-// uses m and v before they are coded again.  Each operation is rounded to fp32
-// on its own (no contraction), so the codes are those of the formulas as
-// written, whatever surrounds them.
+// uses m and v before they are coded again.  The operations that lead to m, v and
+// the codes are rounded to fp32 one by one (no contraction), so the codes are
+// those of the formulas as written, whatever surrounds them: they come from the
+// hardware's approximate roots, and where one is so near a border between two
+// codes that its error could matter, from the rounded ones.  The step itself has
+// an approximate root and quotient (2 ulp each).
 //
 // The table of tensors travels as a kernel parameter, so a captured graph
 // holds its own and nothing is kept between calls.  CTAs walk over runs of
@@ -46,7 +49,7 @@ struct AdamTensor {
 
 // Kernel parameters hold at most 32764 bytes; few tensors take a small table,
 // whose launch is cheaper for the host.
-constexpr int kFewTensors = 16, kMostTensors = 384;
+constexpr int kFewTensors = 16, kMostTensors = 424;
 
 template <int CAP>
 struct AdamTable {
@@ -63,6 +66,7 @@ struct AdamParams {
   const float* grad_scale;
   int32_t* step;  // steps done, CTAs that have read it
   int count_step;
+  int tiny_eps;   // below 1e-15
 };
 
 enum { kParamF32, kParamMaster, kParamBf16 };
@@ -90,24 +94,56 @@ __device__ __forceinline__ int tensor_of(const AdamTable<CAP>& tab, int u) {
   return lo;
 }
 
-__device__ __forceinline__ float decode_m(int c, float s) {
-  const float a = __fmul_rn((float)c, (float)(1.0 / 127.0));
+// Byte e (0 .. 3) of w as a float, without a conversion: the byte becomes the end
+// of 2^23's mantissa.
+__device__ __forceinline__ float byte_float(uint32_t w, int e) {
+  return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u | (uint32_t)e)) - 8388608.0f;
+}
+__device__ __forceinline__ float signed_byte_float(uint32_t w, int e) {
+  return __uint_as_float(__byte_perm(w ^ 0x80808080u, 0x4B000000u, 0x7440u | (uint32_t)e)) - 8388736.0f;
+}
+__device__ __forceinline__ float decode_m(float c, float s) {
+  const float a = __fmul_rn(c, (float)(1.0 / 127.0));
   return __fmul_rn(__fmul_rn(a, fabsf(a)), s);
 }
-__device__ __forceinline__ float decode_r(int c, float s) {
-  const float a = __fmul_rn((float)c, (float)(1.0 / 255.0));
+__device__ __forceinline__ float decode_r(float c, float s) {
+  const float a = __fmul_rn(c, (float)(1.0 / 255.0));
   return __fmul_rn(__fmul_rn(a, a), s);
 }
+// One instruction each; inputs below 2^-126 count as zero.
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Rounding to an integer by the addition of 1.5 2^23: the sum's lowest byte is the
+// integer's.  `off` becomes the largest distance from one.
+constexpr float kRound = 12582912.0f;
+__device__ __forceinline__ uint32_t round_code(float t, float& off) {
+  const float q = __fadd_rn(t, kRound);
+  off = fmaxf(off, fabsf(__fsub_rn(t, __fsub_rn(q, kRound))));
+  return __float_as_uint(q);
+}
+// The lowest bytes of four words.
+__device__ __forceinline__ uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040u), __byte_perm(c, d, 0x0040u), 0x5410u);
+}
 
-// The block's largest value (values are not negative; a NaN counts as largest)
-// and its reciprocal.  A block whose reciprocal is not finite holds zeros, one
-// with a value that is not finite NaN.
-__device__ __forceinline__ float block_scale(const float (&x)[8], float& inv) {
+// The block's largest value; values are not negative, and a NaN counts as largest.
+__device__ __forceinline__ float block_max(const float (&x)[8]) {
   unsigned top = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]));
-  top = __reduce_max_sync(0xFFFFFFFFu, top);
-  float s = __uint_as_float(top);
+  return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, top));
+}
+// A block's scale and its reciprocal, from the largest value.  A block whose
+// reciprocal is not finite holds zeros, one with a value that is not finite NaN.
+__device__ __forceinline__ float block_scale(float s, float& inv) {
   inv = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
   if (inv == INFINITY) s = inv = 0.0f;
   if (s == INFINITY) s = NAN;
@@ -184,7 +220,7 @@ __global__ void __launch_bounds__(kAdamThreads)
     const int64_t left = t.n - at;
     const int n = left >= 8 ? 8 : left > 0 ? (int)left : 0;
     const bool vec = at16(t.param) && at16(t.grad) && at16(t.master) && at16(t.m) && at16(t.v);
-    float w[8], g[8], m[8], v[8], r[8];
+    float w[8], g[8], m[8], v[8];
     load8<G_BF16>(g, t.grad, at, n, vec);
     if constexpr (PARAM == kParamBf16) load8<true>(w, t.param, at, n, vec);
     else load8<false>(w, PARAM == kParamMaster ? t.master : t.param, at, n, vec);
@@ -195,10 +231,9 @@ __global__ void __launch_bounds__(kAdamThreads)
       const uint2 cm = load_codes(t.m, at, n, vec), cv = load_codes(t.v, at, n, vec);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int sh = (e & 3) * 8;
-        m[e] = decode_m((int8_t)((e < 4 ? cm.x : cm.y) >> sh), sm);
-        r[e] = decode_r((uint8_t)((e < 4 ? cv.x : cv.y) >> sh), sr);
-        v[e] = __fmul_rn(r[e], r[e]);
+        m[e] = decode_m(signed_byte_float(e < 4 ? cm.x : cm.y, e & 3), sm);
+        const float r = decode_r(byte_float(e < 4 ? cv.x : cv.y, e & 3), sr);
+        v[e] = __fmul_rn(r, r);
       }
     } else {
       load8<false>(m, t.m, at, n, vec);
@@ -210,9 +245,10 @@ __global__ void __launch_bounds__(kAdamThreads)
       if (p.grad_scale) g[e] = __fmul_rn(g[e], scale);
       m[e] = __fadd_rn(__fmul_rn(m[e], p.b1), __fmul_rn(g[e], p.a1));
       v[e] = __fadd_rn(__fmul_rn(v[e], p.b2), __fmul_rn(__fmul_rn(g[e], g[e]), p.a2));
-      r[e] = __fsqrt_rn(v[e]);
-      const float step = __fdiv_rn(__fmul_rn(m[e], c1), __fadd_rn(__fmul_rn(r[e], c2), p.eps));
-      w[e] = __fsub_rn(__fmul_rn(w[e], keep), __fmul_rn(step, lr));
+      // with an eps that small, second moments below 2^-126 matter
+      const float step = p.tiny_eps ? __fdiv_rn(m[e] * c1, fmaf(__fsqrt_rn(v[e]), c2, p.eps))
+                                    : m[e] * c1 * rcp_approx(fmaf(sqrt_approx(v[e]), c2, p.eps));
+      w[e] = fmaf(step, -lr, w[e] * keep);
     }
     if constexpr (PARAM != kParamF32) store8<true>(w, t.param, at, n, vec);
     if constexpr (PARAM != kParamBf16)
@@ -221,21 +257,33 @@ __global__ void __launch_bounds__(kAdamThreads)
       float x[8], im, ir;
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = e < n ? fabsf(m[e]) : 0.0f;
-      const float sm = block_scale(x, im);
+      const float sm = block_scale(block_max(x), im);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) r[e] = e < n ? r[e] : 0.0f;
-      const float sr = block_scale(r, ir);
-      uint32_t cm[2] = {0u, 0u}, cv[2] = {0u, 0u};
+      for (int e = 0; e < 8; ++e) v[e] = e < n ? v[e] : 0.0f;
+      const float top = block_max(v), sr = block_scale(__fsqrt_rn(top), ir);  // the root keeps the order
+      uint32_t cm[8], cv[8];
+      // an approximate root is 2^-22 of itself off, two of them 255 2^-21 = 1.2e-4 of a code
+      float off = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int sh = (e & 3) * 8;
-        const int a = (int)rintf(__fmul_rn(__fsqrt_rn(__fmul_rn(x[e], im)), 127.0f));
-        const int b = (int)rintf(__fmul_rn(__fsqrt_rn(__fmul_rn(r[e], ir)), 255.0f));
-        cm[e >> 2] |= (uint32_t)((m[e] < 0.0f ? -a : a) & 0xFF) << sh;
-        cv[e >> 2] |= (uint32_t)((v[e] > 0.0f && b < 1 ? 1 : b) & 0xFF) << sh;
+        const float a = 127.0f * sqrt_approx(__fmul_rn(x[e], im));
+        const float b = 255.0f * sqrt_approx(sqrt_approx(v[e]) * ir);
+        cm[e] = round_code(copysignf(a, m[e]), off);
+        cv[e] = round_code(v[e] > 0.0f ? fmaxf(b, 1.0f) : b, off);
       }
-      store_codes(t.m, at, n, vec, make_uint2(cm[0], cm[1]));
-      store_codes(t.v, at, n, vec, make_uint2(cv[0], cv[1]));
+      if (off > 0.4995f || top < 0x1p-100f) {  // or so small that the hardware's roots lose it
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float a = __fmul_rn(__fsqrt_rn(__fmul_rn(x[e], im)), 127.0f);
+          const float b = __fmul_rn(__fsqrt_rn(__fmul_rn(__fsqrt_rn(v[e]), ir)), 255.0f);
+          cm[e] = round_code(copysignf(a, m[e]), off);
+          cv[e] = round_code(v[e] > 0.0f ? fmaxf(b, 1.0f) : b, off);
+        }
+      }
+      store_codes(t.m, at, n, vec, make_uint2(pack_bytes(cm[0], cm[1], cm[2], cm[3]),
+                                               pack_bytes(cm[4], cm[5], cm[6], cm[7])));
+      store_codes(t.v, at, n, vec, make_uint2(pack_bytes(cv[0], cv[1], cv[2], cv[3]),
+                                               pack_bytes(cv[4], cv[5], cv[6], cv[7])));
       if (lane == 0 && n > 0) {
         t.m_scale[at / kAdamBlock] = sm;
         t.v_scale[at / kAdamBlock] = sr;
@@ -255,7 +303,9 @@ __global__ void __launch_bounds__(kAdamThreads)
   __threadfence();
 }
 
-// The values that eight-bit states stand for, the tensors one after the other.
+// The values that eight-bit states stand for, the tensors one after the other.  A
+// tensor's place in the output has any alignment: a warp writes its block in
+// 16-byte pieces from the first boundary on, the codes shifted to fit.
 template <int CAP>
 __global__ void __launch_bounds__(kAdamThreads)
     adamw_values_kernel(const __grid_constant__ AdamTable<CAP> tab) {
@@ -271,26 +321,39 @@ __global__ void __launch_bounds__(kAdamThreads)
     const AdamTensor& t = tab.t[ti];
     const int64_t b = (int64_t)(u - tab.first[ti]) * (kAdamUnit / kAdamBlock) + warp;
     if (b * kAdamBlock >= t.n) continue;
-    const float sm = t.m_scale[b], sr = t.v_scale[b];
-    const int8_t* cm = static_cast<const int8_t*>(t.m) + b * kAdamBlock;
-    const uint8_t* cv = static_cast<const uint8_t*>(t.v) + b * kAdamBlock;
-    float* m = static_cast<float*>(t.param) + b * kAdamBlock;
-    float* v = t.master + b * kAdamBlock;
-    const int64_t left = t.n - b * kAdamBlock;
-    int a[8], c[8];
+    const float scale[2] = {t.m_scale[b], t.v_scale[b]};
+    const int n = (int)min((int64_t)kAdamBlock, t.n - b * kAdamBlock);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = i * 32 + lane;
-      a[i] = e < left ? cm[e] : 0;
-      c[i] = e < left ? cv[e] : 0;
-    }
+    for (int h = 0; h < 2; ++h) {
+      const uint8_t* c = static_cast<const uint8_t*>(h ? t.v : t.m) + b * kAdamBlock;
+      float* out = (h ? t.master : static_cast<float*>(t.param)) + b * kAdamBlock;
+      auto value = [&](uint32_t w, int e) {
+        if (h == 0) return decode_m(signed_byte_float(w, e), scale[0]);
+        const float r = decode_r(byte_float(w, e), scale[1]);
+        return __fmul_rn(r, r);
+      };
+      const bool words = (reinterpret_cast<uintptr_t>(c) & 3u) == 0;
+      const int head = (int)((16u - (reinterpret_cast<uintptr_t>(out) & 15u)) & 15u) / 4;
+      const int quads = words && n > head ? (n - head) / 4 : 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = i * 32 + lane;
-      if (e >= left) continue;
-      const float r = decode_r(c[i], sr);
-      m[e] = decode_m(a[i], sm);
-      v[e] = __fmul_rn(r, r);
+      for (int i = 0; i < 2; ++i) {
+        const int q = i * 32 + lane;
+        if (q >= quads) continue;
+        const int e = head + 4 * q;
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(c + (e & ~3));
+        // the last word is read only where its bytes are needed
+        const uint32_t lo = w[0], hi = head ? w[1] : 0u;
+        const uint32_t four = __funnelshift_r(lo, hi, head * 8);
+        *reinterpret_cast<float4*>(out + e) =
+            make_float4(value(four, 0), value(four, 1), value(four, 2), value(four, 3));
+      }
+      if (words) {  // what lies before the first boundary and behind the last piece
+        if (lane < head && lane < n) out[lane] = value(c[lane], 0);
+        const int e = head + 4 * quads + lane;
+        if (lane < 4 && e < n) out[e] = value(c[e], 0);
+      } else {
+        for (int e = lane; e < n; e += 32) out[e] = value(c[e], 0);
+      }
     }
   }
 }
@@ -324,12 +387,14 @@ moe_status_t launch_step(const AdamTable<CAP>& tab, const AdamParams& p, int par
 template <typename F>
 moe_status_t over_tables(const std::vector<AdamTensor>& all, F&& each) {
   size_t i = 0;
+  // tables of about the same number of tensors
+  const size_t tables = (all.size() + kMostTensors - 1) / kMostTensors;
+  const int most = tables ? (int)((all.size() + tables - 1) / tables) : 0;
   do {
     auto fill = [&](auto& tab) {
       tab.count = 0;
       tab.first[0] = 0;
-      const int cap = (int)(sizeof(tab.t) / sizeof(tab.t[0]));
-      for (; i < all.size() && tab.count < cap; ++i) {
+      for (; i < all.size() && tab.count < most; ++i) {
         const int64_t next = tab.first[tab.count] + units_of(all[i].n);
         if (next > INT32_MAX) break;  // never with the first: n has a limit
         tab.t[tab.count] = all[i];
@@ -407,7 +472,8 @@ extern "C" moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int co
   std::sort(seen.begin(), seen.end());
   if (std::adjacent_find(seen.begin(), seen.end()) != seen.end()) return MOE_ERR_INVALID_ARG;
   AdamParams p{beta1, beta2, (float)beta1, (float)beta2, (float)(1.0 - beta1), (float)(1.0 - beta2),
-               (float)eps, (float)lr, lr_dev, grad_scale, step, 0};
+               (float)eps, (float)lr, lr_dev, grad_scale, step, 0,
+               eps < 1e-15};
   const int param = param_dtype == MOE_DTYPE_F32 ? kParamF32 : masters ? kParamMaster : kParamBf16;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return over_tables(all, [&](const auto& tab, bool last) {
