@@ -23,8 +23,9 @@ from .binding import (moe_abi_version, moe_adamw_step, moe_adamw_values, moe_lay
                       moe_set_launch_overlap,
                       moe_router_workspace_size, moe_status_string, moe_swiglu, qdesc)
 from .health import ExpertHealthMonitor, WindowHealth
-from .layer import (ExpertAdapters, MoELayer, QTensor, ScoredRouting, bf16_from_bits,
-                    qtensor_from_numpy)
+from .layer import (ExpertAdapters, MoELayer, Norm, QTensor, ScoredRouting, SharedExpert,
+                    bf16_from_bits, qtensor_from_numpy)
+from .optim import AdamW
 
 __all__ = [
     "MoELayer", "ScoredRouting", "ExpertAdapters", "QTensor", "MoEError", "ExpertHealthMonitor", "WindowHealth",
@@ -40,6 +41,6 @@ __all__ = [
     "moe_lora_apply", "moe_lora_workspace_size",
     "NORM_LAYER", "NORM_RMS", "ADAMW_BLOCK", "moe_layer_norm", "moe_layer_norm_backward",
     "moe_layer_norm_workspace_size", "moe_adamw_step", "moe_adamw_values",
-    "ACT_NONE", "ACT_SILU", "ACT_GELU", "ACT_SWIGLU", "moe_linear", "moe_linear_backward",
+    "AdamW", "Norm", "SharedExpert", "ACT_NONE", "ACT_SILU", "ACT_GELU", "ACT_SWIGLU", "moe_linear", "moe_linear_backward",
     "moe_linear_backward_workspace_size",
 ]

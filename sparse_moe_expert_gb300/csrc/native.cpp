@@ -782,7 +782,7 @@ PyObject* linear(Args a) {
 // d_out, x, w, preact, activation, need_d_x, need_d_w, need_d_bias, d_x, d_w,
 // d_w_bf16 (None: fp32), accumulate, d_bias, workspace, stream
 PyObject* linear_backward(Args a) {
-  const Tensor &d = a.tensor("d_out"), &x = a.tensor("x"), &w = a.tensor("w"),
+  const Tensor &d = a.tensor("d_out"), &x = a.tensor("x"), &w = a.tensor("w", true),
                &preact = a.tensor("preact", true);
   const int act = a.i32();
   const bool need_x = a.flag(), need_w = a.flag(), need_b = a.flag();
@@ -791,16 +791,22 @@ PyObject* linear_backward(Args a) {
   const bool accumulate = a.flag();
   Tensor d_b = a.tensor("d_bias", true), ws = a.tensor("workspace", true), d_z;
   const StreamArg stream(a.next());
+  int64_t features = 0;
   const moe_status_t s = unlocked([&] {
     const int64_t ld_x = mapped_rows(x, "x");
     const c10::Device dev = x.device();
     const OnStream on(stream, dev);
     const int T = as_int(x.size(0), "T"), K = as_int(x.size(1), "K");
-    if (w.dim() != 2 || w.size(1) != K) throw Refused("w must be [N, " + std::to_string(K) + "]");
-    const int N = as_int(w.size(0), "N");
-    like(w, {N, K}, at::kBFloat16, dev, "w");
     if (act < MOE_ACT_NONE || act > MOE_ACT_SWIGLU) return MOE_ERR_INVALID_ARG;
+    if (d.dim() != 2) throw Refused("d_out must have two dimensions");
+    // without w (no d_x) the gradient's width says how many features there are
+    if (!w.defined() && (need_x || d_x.defined())) throw Refused("d_x needs w");
+    if (w.defined() && (w.dim() != 2 || w.size(1) != K))
+      throw Refused("w must be [N, " + std::to_string(K) + "]");
+    const int N = as_int(w.defined() ? w.size(0) : d.size(1) * (act == MOE_ACT_SWIGLU ? 2 : 1), "N");
+    if (w.defined()) like(w, {N, K}, at::kBFloat16, dev, "w");
     const int64_t cols = act == MOE_ACT_SWIGLU ? N / 2 : N;
+    features = N;
     const int64_t ld_d = rows_like(d, T, cols, dev, "d_out");
     if (preact.defined()) like(preact, {T, N}, at::kBFloat16, dev, "preact");
     else if (act != MOE_ACT_NONE) throw Refused("preact is needed for the activation's gradient");
@@ -841,7 +847,7 @@ PyObject* linear_backward(Args a) {
                                ws.defined() ? scratch_bytes(ws, dev) : 0, on.handle);
   });
   if (s) return status(s);
-  if (d_z.size(1) != w.size(0)) d_z = d_z.narrow(1, 0, w.size(0));
+  if (d_z.size(1) != features) d_z = d_z.narrow(1, 0, features);
   return result({d_x, d_w, d_b, d_z, ws});
 }
 

@@ -15,7 +15,7 @@ import numpy as np
 import torch
 
 from . import binding as B
-from ._lib import (EPILOGUE_RAW, EPILOGUE_SWIGLU, PATH_AUTO, PATH_FLAG_WEIGHTS_EARLY, PATH_GEMV,
+from ._lib import (ACT_SWIGLU, NORM_LAYER, NORM_RMS, EPILOGUE_RAW, EPILOGUE_SWIGLU, PATH_AUTO, PATH_FLAG_WEIGHTS_EARLY, PATH_GEMV,
                    PATH_TC, SCORE_SIGMOID, SCORE_SOFTMAX, MoEError, path_k_range)
 
 FUSE_ENV = "MOE_GB300_FUSE_GATE_UP"
@@ -94,6 +94,24 @@ class ExpertAdapters:
         return a, torch.cat([top, low], dim=-2).contiguous()
 
 
+@dataclasses.dataclass
+class Norm:
+    """A norm of the block around the layer (moe_layer_norm): weight and bias
+    [H], fp32 or bf16, either may be None; kind NORM_RMS or NORM_LAYER."""
+    weight: Optional[torch.Tensor] = None
+    bias: Optional[torch.Tensor] = None
+    kind: int = NORM_RMS
+    eps: float = 1e-6
+
+
+@dataclasses.dataclass
+class SharedExpert:
+    """A dense SwiGLU expert that every token passes beside the routed ones
+    (moe_linear): gate_up bf16 [2*I', H] (gate rows first), down bf16 [H, I']."""
+    gate_up: torch.Tensor
+    down: torch.Tensor
+
+
 class MoELayer:
     """Forward of one quantized sparse-MoE SwitchGLU layer on one GPU.
 
@@ -112,10 +130,18 @@ class MoELayer:
     otherwise.  ``scoring`` routes by scores (ScoredRouting) instead of the
     plain softmax top-k; it needs a fixed k and takes the place of ``groups``.
     ``adapters`` (ExpertAdapters) serve calls that name each token's adapter;
-    they need the fused gate_up matrix.
+    they need the fused gate_up matrix.  ``shared`` (SharedExpert) is added to
+    the routed experts' sum.  ``norm`` and ``out_norm`` (Norm) stand in front of
+    and behind the layer in block().  With ``keep_for_grad`` a forward keeps what
+    grads() needs (the input, which must not change until then, and the shared
+    expert's pre-activations).
     """
     scoring: Optional[ScoredRouting] = None
     adapters: Optional[ExpertAdapters] = None
+    shared: Optional[SharedExpert] = None
+    norm: Optional[Norm] = None
+    out_norm: Optional[Norm] = None
+    keep_for_grad = False
 
     def __init__(self, router_w: torch.Tensor, logit_bias: Optional[torch.Tensor], gate: QTensor,
                  up: QTensor, down: QTensor, k_fixed: int, kmax: Optional[int] = None,
@@ -124,7 +150,9 @@ class MoELayer:
                  path: int = PATH_AUTO, free_sources: bool = False, groups: int = 0,
                  capacity: Optional[int] = None, y_dtype: Optional[torch.dtype] = None,
                  scoring: Optional[ScoredRouting] = None,
-                 adapters: Optional[ExpertAdapters] = None):
+                 adapters: Optional[ExpertAdapters] = None,
+                 shared: Optional[SharedExpert] = None, norm: Optional[Norm] = None,
+                 out_norm: Optional[Norm] = None):
         self.device = router_w.device
         self.router_w = router_w.contiguous()
         self.logit_bias = None if logit_bias is None else logit_bias.contiguous()
@@ -167,6 +195,12 @@ class MoELayer:
         self.adapters = adapters
         if adapters is not None and not self.fused:
             raise ValueError("adapters need the fused gate_up matrix")
+        if shared is not None:
+            two_i, h = shared.gate_up.shape
+            if h != self.H or two_i % 16 or tuple(shared.down.shape) != (self.H, two_i // 2):
+                raise ValueError("shared needs gate_up [2*I', H] and down [H, I'] with I' a multiple of 8")
+        self.shared, self.norm, self.out_norm = shared, norm, out_norm
+        self._kept = None
         self._bufs = {}
         # tokens of the last forward and whether it routed by scores, for router_grad
         self._last, self._scored = None, False
@@ -228,7 +262,11 @@ class MoELayer:
         capped grouping is a kernel of its own.  When k_split is set both
         kernel families of each product are launched (one of them returns at
         once).  With scoring the logits, the scores and the grouping are a
-        kernel each.  Calls with adapters add theirs."""
+        kernel each.  Calls with adapters add theirs, a shared expert its two
+        products, block() one for each norm."""
+        return self._routed_launches(T) + (2 if self.shared is not None else 0)
+
+    def _routed_launches(self, T: int) -> int:
         if self.scoring is not None:
             # logits, scores, grouping, [row permute], products, combine
             n = 3 + (1 if self.resolved_path(T) == PATH_TC else 0)
@@ -277,6 +315,21 @@ class MoELayer:
         bufs = self._bufs[key]
         if self.scoring is not None and "logits" not in bufs:
             bufs["logits"] = torch.empty((T, self.E), dtype=torch.float32, device=self.device)
+
+        def rows(name, width):
+            if name not in bufs or bufs[name].shape[1] != width:
+                if name in bufs:  # a captured graph may go on using the one outgrown
+                    bufs.setdefault("outgrown", []).append(bufs[name])
+                bufs[name] = torch.empty((T, width), dtype=torch.bfloat16, device=self.device)
+        if self.shared is not None:
+            rows("shared_h", self.shared.down.shape[1])
+            if self.keep_for_grad:
+                rows("shared_z", self.shared.gate_up.shape[0])
+        if self.norm is not None:
+            rows("normed", self.H)
+            rows("summed", self.H)
+        if self.out_norm is not None:
+            rows("block_out", self.H)
         return bufs
 
     def _adapter_buffers(self, b: dict, T: int) -> None:
@@ -312,8 +365,52 @@ class MoELayer:
         """x: bf16 [T, H] on the device.  Returns bf16 [T, H] (a reused buffer
         unless ``out`` is given).  ``events``, if given, receives per kernel
         ("router", "permute", "permute_rows", "gate_up", "down", "combine") a
-        list of (start, end) CUDA events around its launches.  ``adapter_ids``
-        (int32 [T], negative: none) names each token's adapter."""
+        list of (start, end) CUDA events around its launches ("shared" with a
+        shared expert).  ``adapter_ids`` (int32 [T], negative: none) names each
+        token's adapter."""
+        self._kept = dict(x=x) if self.keep_for_grad else None
+        res = self._routed(x, out, inv_temperature, events, adapter_ids)
+        if self._kept is not None:
+            self._kept["inv_temperature"] = (self.inv_temperature if inv_temperature is None
+                                             else float(inv_temperature))
+        if self.shared is not None and x.shape[0] > 0:
+            ev = _Timer(events, "shared")
+            b = self.buffers(x.shape[0])
+            B.moe_linear(x, self.shared.gate_up, activation=ACT_SWIGLU, out=b["shared_h"],
+                         preact=b["shared_z"] if self.keep_for_grad else None)
+            B.moe_linear(b["shared_h"], self.shared.down, residual=res, out=res)
+            ev.stop()
+        return res
+
+    def block(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
+              out: Optional[torch.Tensor] = None, **forward_args):
+        """The layer with its norms, as a block of a model: with s = x + residual
+        (x without one), out_norm(layer(norm(s))) -> (out, s), both bf16 [T, H] and
+        buffers that the next call of T tokens writes again unless ``out`` is
+        given (s is x itself without a residual).  The next block takes them as x and
+        residual, so the sum is part of its norm's kernel; out + s ends the last."""
+        if residual is not None and self.norm is None:
+            raise ValueError("a residual needs a layer with a norm, whose kernel adds it")
+        T = x.shape[0]
+        b, s, h = self.buffers(T), x, x
+        if self.norm is not None:
+            n = self.norm
+            h, s, _, _ = B.moe_layer_norm(
+                x, n.weight, n.bias, residual=residual, eps=n.eps, kind=n.kind, out=b["normed"],
+                summed=None if residual is None else b["summed"])
+            s = x if residual is None else s
+        y = self.forward(h, out=out if self.out_norm is None else None, **forward_args)
+        if self.out_norm is None:
+            return y, s
+        n = self.out_norm
+        res, _, mean, rstd = B.moe_layer_norm(
+            y, n.weight, n.bias, eps=n.eps, kind=n.kind, need_stats=self.keep_for_grad,
+            out=out if out is not None else b["block_out"])
+        if self._kept is not None:
+            self._kept.update(y=y, mean=mean, rstd=rstd)
+        return res, s
+
+    def _routed(self, x, out, inv_temperature, events, adapter_ids):
         T = x.shape[0]
         b = self.buffers(T)
         path = self.resolved_path(T)
@@ -441,6 +538,64 @@ class MoELayer:
         return B.moe_route_scored_backward(
             b["logits"], b["topk_ids"], d_w, counts, s.score, self.k_fixed, self.renormalize,
             s.scale, balance_coef, z_coef)
+
+    def trainable(self) -> dict:
+        """The tensors that grads() gives gradients of, by name: ``router_w`` (with
+        scoring), the shared expert's and out_norm's.  The quantized experts stay as
+        they are, and with them whatever reaches the loss through their input:
+        ``norm`` is not among them."""
+        t = {}
+        if self.scoring is not None:
+            t["router_w"] = self.router_w
+        if self.shared is not None:
+            t["shared.gate_up"], t["shared.down"] = self.shared.gate_up, self.shared.down
+        if self.out_norm is not None:
+            for name in ("weight", "bias"):
+                if getattr(self.out_norm, name) is not None:
+                    t["out_norm." + name] = getattr(self.out_norm, name)
+        return t
+
+    def grads(self, d_out: torch.Tensor, balance_coef: float = 0.0, z_coef: float = 0.0):
+        """Gradients of the last block() or forward() with keep_for_grad, for the
+        gradient ``d_out`` (bf16 [T, H]) of its output and the balance and z losses
+        (see router_grad) -> (gradients by the names of trainable(), fp32, losses
+        fp32 [2] or None without scoring)."""
+        k = self._kept
+        if k is None:
+            raise ValueError("grads needs a forward with keep_for_grad")
+        x, g, losses = k["x"], {}, None
+        T = x.shape[0]
+        if tuple(d_out.shape) != (T, self.H) or d_out.dtype != torch.bfloat16:
+            raise ValueError(f"d_out must be bfloat16 {(T, self.H)}")
+        if T == 0:
+            zeros = {n: torch.zeros(t.shape, device=t.device) for n, t in self.trainable().items()}
+            return zeros, None if self.scoring is None else torch.zeros(2, device=self.device)
+        if "rstd" in k:
+            n = self.out_norm
+            d_out, d_w, d_b = B.moe_layer_norm_backward(
+                d_out, k["y"], k["rstd"], k["mean"], n.weight, kind=n.kind,
+                need_d_weight=n.weight is not None, need_d_bias=n.bias is not None)
+            for name, t in (("weight", d_w), ("bias", d_b)):
+                if t is not None:
+                    g["out_norm." + name] = t
+        if self.scoring is not None:
+            d_logits, losses = self.router_grad(d_out, balance_coef, z_coef)
+            # inv_temperature d_logits^T x with the gradient as two bf16 terms, 2^-17 of it
+            d = d_logits * k["inv_temperature"]
+            hi = d.to(torch.bfloat16)
+            lo = (d - hi.float()).to(torch.bfloat16)
+            only = dict(need_d_x=False, need_d_bias=False)
+            w = B.moe_linear_backward(hi, x, None, **only)[1]
+            B.moe_linear_backward(lo, x, None, d_w=w, accumulate=True, **only)
+            g["router_w"] = w
+        if self.shared is not None:
+            b, s = self.buffers(T), self.shared
+            d_h, g["shared.down"], _, _ = B.moe_linear_backward(d_out, b["shared_h"], s.down,
+                                                                need_d_bias=False)
+            g["shared.gate_up"] = B.moe_linear_backward(
+                d_h, x, s.gate_up, b["shared_z"], activation=ACT_SWIGLU, need_d_x=False,
+                need_d_bias=False)[1]
+        return g, losses
 
     def _forward_k_split(self, x, b, ks, T, out, events):
         """The products after routing when k < ks takes the streamed GEMV and
