@@ -285,10 +285,14 @@ TileChoice choose_tiles(const LinearEpi& e, int K) {
 
 }  // namespace
 
-moe_status_t linear_product(const LinearOp& a, const LinearOp& b, int K, LinearEpi e, cudaStream_t st) {
+static void set_vec(LinearEpi& e) {
   using moe_host::aligned16;
   e.vec = e.cols % 8 == 0 && aligned16(e.out) && aligned16(e.residual) && aligned16(e.preact) &&
           aligned16(e.bias);
+}
+
+moe_status_t linear_product(const LinearOp& a, const LinearOp& b, int K, LinearEpi e, cudaStream_t st) {
+  set_vec(e);
   // The form for few rows reads x for every 16 rows of W: past 16 rows of x that
   // shows where W is large (us for 32 rows, this form and tiles: 4096 x 22016 48,
   // 34; 4096 x 4096 11.4, 10.4; 1536 x 4096 6.4, 9.0; 2048 x 1536 6.1, 7.1).
@@ -299,6 +303,28 @@ moe_status_t linear_product(const LinearOp& a, const LinearOp& b, int K, LinearE
   // a pair's tile has 256 rows: with 128 or fewer half of it would be empty
   if (e.M > 128 && linear_pairs_us(e, K, b.row_major) < t.us) return linear_pairs(a, b, K, e, st);
   return t.bn == 64 ? tiles_as<64>(a, b, K, e, t.splits, st) : tiles_as<128>(a, b, K, e, t.splits, st);
+}
+
+// The product with the longer tiles first.
+moe_status_t linear_products(const LinearOp (&a)[2], const LinearOp (&b)[2], const int (&K)[2],
+                             LinearEpi (&e)[2], cudaStream_t st) {
+  const int f = K[0] >= K[1] ? 0 : 1, g = 1 - f;
+  float apart = 0.0f;
+  for (int i = 0; i < 2; ++i) {
+    set_vec(e[i]);
+    const float tiles = choose_tiles(e[i], K[i]).us, pairs = linear_pairs_us(e[i], K[i], false);
+    apart += e[i].M > 128 && pairs < tiles ? pairs : tiles;
+  }
+  if (e[0].M > 128 && e[1].M > 128) {
+    const LinearEpi ee[2] = {e[f], e[g]};
+    const int kk[2] = {K[f], K[g]};
+    if (linear_pairs_both_us(ee, kk) < apart) {
+      const LinearOp aa[2] = {a[f], a[g]}, bb[2] = {b[f], b[g]};
+      return linear_pairs_both(aa, bb, kk, ee, st);
+    }
+  }
+  if (const moe_status_t s = linear_product(a[0], b[0], K[0], e[0], st)) return s;
+  return linear_product(a[1], b[1], K[1], e[1], st);
 }
 
 }  // namespace moe

@@ -167,11 +167,18 @@ bool linear_map(CUtensorMap* m, const LinearOp& op, int rows, int K, int box_row
 moe_status_t linear_pairs(const LinearOp& a, const LinearOp& b, int K, const LinearEpi& e,
                           cudaStream_t st);
 float linear_pairs_us(const LinearEpi& e, int K, bool b_rows);
+// Two products, B by columns, in one launch; the first one's tiles come first.
+moe_status_t linear_pairs_both(const LinearOp (&a)[2], const LinearOp (&b)[2], const int (&K)[2],
+                               const LinearEpi (&e)[2], cudaStream_t st);
+float linear_pairs_both_us(const LinearEpi (&e)[2], const int (&K)[2]);
 // The same for up to kLinearRowsMost rows of A, both operands in rows.
 constexpr int kLinearRowsMost = 32;
 moe_status_t linear_rows(const uint16_t* x, int64_t ldx, const uint16_t* w, int K,
                          const LinearEpi& e, cudaStream_t st);
 // Which of the forms serves the call.
 moe_status_t linear_product(const LinearOp& a, const LinearOp& b, int K, LinearEpi e, cudaStream_t st);
+// The same for two products with B by columns.
+moe_status_t linear_products(const LinearOp (&a)[2], const LinearOp (&b)[2], const int (&K)[2],
+                             LinearEpi (&e)[2], cudaStream_t st);
 
 }  // namespace moe

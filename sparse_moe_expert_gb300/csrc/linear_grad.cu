@@ -202,14 +202,17 @@ extern "C" moe_status_t moe_linear_backward(const void* d_out, int d_dtype, int6
   }
   const uint16_t* dz = direct ? static_cast<const uint16_t*>(d_out) : d_preact;
   const int64_t ld = direct ? ld_d : ld_dp;
-  if (d_x) {
-    const LinearEpi e{nullptr, nullptr, d_x, nullptr, T, K, K, MOE_ACT_NONE, 1, 0};
-    if (const moe_status_t s = linear_product({dz, ld, true}, {w, K, false}, N, e, st)) return s;
+  const LinearEpi ex{nullptr, nullptr, d_x, nullptr, T, K, K, MOE_ACT_NONE, 1, 0};
+  const LinearEpi ew{nullptr, accumulate ? d_w : nullptr, d_w, nullptr, N, K, K, MOE_ACT_NONE,
+                     d_w_dtype == MOE_DTYPE_BF16, 0};
+  const LinearOp z_rows{dz, ld, true}, z_cols{dz, ld, false}, w_cols{w, K, false}, x_cols{x, ld_x, false};
+  if (d_x && d_w) {
+    const LinearOp a[2] = {z_rows, z_cols}, b[2] = {w_cols, x_cols};
+    const int sums[2] = {N, T};
+    LinearEpi e[2] = {ex, ew};
+    return linear_products(a, b, sums, e, st);
   }
-  if (d_w) {
-    const LinearEpi e{nullptr, accumulate ? d_w : nullptr, d_w, nullptr, N, K, K, MOE_ACT_NONE,
-                      d_w_dtype == MOE_DTYPE_BF16, 0};
-    return linear_product({dz, ld, false}, {x, ld_x, false}, T, e, st);
-  }
+  if (d_x) return linear_product(z_rows, w_cols, N, ex, st);
+  if (d_w) return linear_product(z_cols, x_cols, T, ew, st);
   return MOE_OK;
 }

@@ -9,8 +9,13 @@
 // each), eight take the
 // sums of the tile before out of the second half of TMEM meanwhile.  Tiles run
 // through A's rows eight tiles at a time, so that a wave of pairs meets in L2.
-#include "linear.cuh"
+//
+// A launch takes one product or two, one after the other: of the gradient's two,
+// neither fills its last wave (256 and 688 tiles on 76 pairs: 4 and 10 turns for 3.4
+// and 9.1), and the pairs that the first leaves early begin with the second.
+#include <cstring>
 
+#include "linear.cuh"
 #include "lora.cuh"
 
 namespace moe {
@@ -62,19 +67,57 @@ __device__ __forceinline__ void remote_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Tile t of m_tiles x n_tiles.
-__device__ __forceinline__ int2 pair_tile(int t, int m_tiles, int n_tiles) {
-  const int per = kPairGroup * n_tiles, g = t / per, r = t - g * per;
-  const int rows = min(kPairGroup, m_tiles - g * kPairGroup);
-  return make_int2(g * kPairGroup + r % rows, r / rows);
+// One product of a launch.
+struct PairProduct {
+  CUtensorMap a, b;
+  LinearEpi e;
+  int K, bn;
+  int m_tiles, n_tiles;
+  int tiles;   // 0: no such product
+};
+// The tiles are dealt to the pairs in turns.  Of the first product the `heavy` first
+// pairs have one tile more; the others begin the second with `extra` turns of
+// their own, then it is dealt to all.
+struct PairWork {
+  PairProduct product[2];
+  int heavy, extra;
+  int rows_first;  // which of two has its A in rows
+};
+struct PairTile {
+  int which;  // -1: none left
+  int m, n;
+};
+
+template <bool TWO>
+__device__ __forceinline__ PairTile pair_tile(const PairWork& w, int pair, int pairs, int i) {
+  int t = pair + i * pairs, which = 0;
+  if (TWO && t >= w.product[0].tiles) {
+    const int first = w.product[0].tiles;
+    i -= pair < first ? (first - pair + pairs - 1) / pairs : 0;
+    const int light = pairs - w.heavy;
+    if (pair >= w.heavy && i < w.extra) {
+      t = pair - w.heavy + i * light;
+    } else {
+      if (pair >= w.heavy) i -= w.extra;
+      t = w.extra * light + pair + i * pairs;
+    }
+    which = 1;
+  }
+  const PairProduct& q = w.product[which];
+  if (t >= q.tiles) return {-1, 0, 0};
+  const int per = kPairGroup * q.n_tiles, g = t / per, r = t - g * per;
+  const int rows = min(kPairGroup, q.m_tiles - g * kPairGroup);
+  return {which, g * kPairGroup + r % rows, r / rows};
 }
 
-template <bool A_ROW, bool B_ROW, bool SWIGLU>
+// A's order.  Of two products one has it in rows of k, the other by columns.
+enum { kACols, kARows, kABoth };
+
+template <int A_ORDER, bool B_ROW, bool SWIGLU>
 __global__ void __launch_bounds__(kPairThreads, 1)
-    linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                       LinearEpi e, int K, int bn, int m_tiles, int n_tiles, unsigned int* err) {
+    linear_pair_kernel(const __grid_constant__ PairWork work, unsigned int* err) {
   constexpr int kStages = kPairStages, kStageBytes = kPairStageBytes;
-  const int span = SWIGLU ? bn / 2 : bn;  // output columns of a tile
+  constexpr bool kTwo = A_ORDER == kABoth;
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t full[kStages], empty[kStages], sums_full[2], sums_empty[2], drain;
   __shared__ uint32_t tmem_sh;
@@ -82,7 +125,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cta = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int nkb = (K + kLinBK - 1) / kLinBK, tiles = m_tiles * n_tiles;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -123,27 +165,33 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       int64_t issued = 0;
       bool ok = true;
       const uint32_t bar0 = cluster_addr(full, 0);  // the even CTA's
-      for (int t = pair; ok && t < tiles; t += pairs) {
-        const int2 at = pair_tile(t, m_tiles, n_tiles);
-        const int row0 = at.x * kPairM + cta * 128;
-        const int col0 = SWIGLU ? cta * e.cols + at.y * span : at.y * span + cta * (bn / 2);
+      for (int i = 0; ok; ++i) {
+        const PairTile at = pair_tile<kTwo>(work, pair, pairs, i);
+        if (at.which < 0) break;
+        const PairProduct& q = work.product[kTwo ? at.which : 0];
+        const int bn = q.bn, nkb = (q.K + kLinBK - 1) / kLinBK;
+        const bool a_rows = kTwo ? at.which == work.rows_first : A_ORDER == kARows;
+        const CUtensorMap *tm_a = &q.a, *tm_b = &q.b;
+        const uint32_t bytes = (uint32_t)(256 + bn) * 128;
+        const int row0 = at.m * kPairM + cta * 128;
+        const int col0 = SWIGLU ? cta * q.e.cols + at.n * (bn / 2) : at.n * bn + cta * (bn / 2);
         for (int kb = 0; kb < nkb; ++kb) {
           if (issued >= kStages && !(ok = wait(&empty[s], phase ^ 1u))) break;
           unsigned char* a = smem + s * kStageBytes;
           unsigned char* b = a + 128 * 128;
           const uint32_t bar = bar0 + s * 8;
           const int k = kb * kLinBK;
-          if (cta == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(256 + bn) * 128);
-          if constexpr (A_ROW) {
-            pair_tma_2d(a, &tm_a, k, row0, bar);
+          if (cta == 0) mbar_arrive_expect_tx(&full[s], bytes);
+          if (a_rows) {
+            pair_tma_2d(a, tm_a, k, row0, bar);
           } else {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) pair_tma_2d(a + j * 8192, &tm_a, row0 + j * 64, k, bar);
+            for (int j = 0; j < 2; ++j) pair_tma_2d(a + j * 8192, tm_a, row0 + j * 64, k, bar);
           }
           if constexpr (B_ROW) {
-            pair_tma_2d(b, &tm_b, k, col0, bar);
+            pair_tma_2d(b, tm_b, k, col0, bar);
           } else {
-            for (int j = 0; j < bn / 128; ++j) pair_tma_2d(b + j * 8192, &tm_b, col0 + j * 64, k, bar);
+            for (int j = 0; j < bn / 128; ++j) pair_tma_2d(b + j * 8192, tm_b, col0 + j * 64, k, bar);
           }
           ++issued;
           if (++s == kStages) {
@@ -160,25 +208,32 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
   } else if (warp == 1) {
     if (cta == 0 && elected()) {
-      const uint32_t idesc = idesc_linear<A_ROW, B_ROW>(kPairM, bn);
-      const uint64_t a_desc = operand_desc<A_ROW>(smem);
+      const uint64_t a_rows = operand_desc<true>(smem), a_cols = operand_desc<false>(smem);
       const uint64_t b_desc = operand_desc<B_ROW>(smem + 128 * 128);
       int s = 0;
       uint32_t phase = 0;
-      int i = 0;
       bool ok = true;
-      for (int t = pair; ok && t < tiles; t += pairs, ++i) {
-        const int buf = i & 1;
+      for (int i = 0; ok; ++i) {
+        const PairTile at = pair_tile<kTwo>(work, pair, pairs, i);
+        if (at.which < 0) break;
+        const PairProduct& q = work.product[kTwo ? at.which : 0];
+        const int nkb = (q.K + kLinBK - 1) / kLinBK, buf = i & 1;
+        const bool rows = kTwo ? at.which == work.rows_first : A_ORDER == kARows;
+        const uint32_t idesc = (rows ? idesc_linear<true, B_ROW>(kPairM, 0)
+                                     : idesc_linear<false, B_ROW>(kPairM, 0)) |
+                               ((uint32_t)(q.bn >> 3) << 17);
+        const uint64_t a0 = rows ? a_rows : a_cols;
+        const uint64_t a_step = rows ? operand_step<true>() : operand_step<false>();
         if (i >= 2 && !(ok = wait(&sums_empty[buf], (uint32_t)((i >> 1) - 1) & 1u))) break;
         const uint32_t d = tmem + buf * kPairN;
         for (int kb = 0; kb < nkb; ++kb) {
           if (!(ok = wait(&full[s], phase))) break;
           tc_fence_after();
-          const uint64_t ad = a_desc + s * (kStageBytes >> 4), bd = b_desc + s * (kStageBytes >> 4);
+          const uint64_t ad = a0 + s * (kStageBytes >> 4), bd = b_desc + s * (kStageBytes >> 4);
           pair_mma(d, ad, bd, idesc, kb > 0);
 #pragma unroll
           for (int k = 1; k < 4; ++k)
-            pair_mma(d, ad + k * operand_step<A_ROW>(), bd + k * operand_step<B_ROW>(), idesc, 1);
+            pair_mma(d, ad + k * a_step, bd + k * operand_step<B_ROW>(), idesc, 1);
           pair_commit(&empty[s]);
           if (++s == kStages) {
             s = 0;
@@ -194,16 +249,18 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
   } else {
     const int quad = warp & 3, half = (warp - 2) >> 2;
-    int i = 0;
-    for (int t = pair; t < tiles; t += pairs, ++i) {
-      const int buf = i & 1;
-      const int2 at = pair_tile(t, m_tiles, n_tiles);
-      const int64_t row = (int64_t)at.x * kPairM + cta * 128 + quad * 32 + lane;
+    for (int i = 0;; ++i) {
+      const PairTile at = pair_tile<kTwo>(work, pair, pairs, i);
+      if (at.which < 0) break;
+      const LinearEpi e = work.product[kTwo ? at.which : 0].e;  // in registers
+      const int bn = work.product[kTwo ? at.which : 0].bn, buf = i & 1;
+      const int span = SWIGLU ? bn / 2 : bn;  // output columns of the tile
+      const int64_t row = (int64_t)at.m * kPairM + cta * 128 + quad * 32 + lane;
       // the residual's part of the tile comes into L2 during the products
       if (e.residual && row < e.M) {
         const int size = e.out_bf16 ? 2 : 4;
-        const int c1 = min(span, e.cols - at.y * span) * size;
-        const char* p = static_cast<const char*>(e.residual) + (row * e.cols + (int64_t)at.y * span) * size;
+        const int c1 = min(span, e.cols - at.n * span) * size;
+        const char* p = static_cast<const char*>(e.residual) + (row * e.cols + (int64_t)at.n * span) * size;
         for (int c = half * 128; c < c1; c += 256) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + c));
       }
       int ok = mbar_wait_sleep(&sums_full[buf], (uint32_t)(i >> 1) & 1u, kWaitBudgetCycles);
@@ -233,7 +290,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
               z[x] = __uint_as_float(r[0][q * 8 + x]);
               if constexpr (SWIGLU) u[x] = __uint_as_float(r[1][q * 8 + x]);
             }
-            finish8<SWIGLU>(e, row, at.y * span + c + q * 8, z, u);
+            finish8<SWIGLU>(e, row, at.n * span + c + q * 8, z, u);
           }
         }
       }
@@ -298,22 +355,69 @@ PairChoice choose_pairs(const LinearEpi& e, int pairs, bool b_rows) {
   return best;
 }
 
-template <bool A_ROW, bool B_ROW, bool SWIGLU>
-moe_status_t launch_pairs(const LinearOp& a, const LinearOp& b, int K, const LinearEpi& e,
-                          cudaStream_t st) {
-  constexpr auto kern = linear_pair_kernel<A_ROW, B_ROW, SWIGLU>;
+// One product with tiles of this width; fails only if no map describes an operand.
+bool set_product(PairProduct& q, const LinearOp& a, const LinearOp& b, int K, const LinearEpi& e, int bn) {
+  const int span = e.act == MOE_ACT_SWIGLU ? bn / 2 : bn;
+  q.e = e;
+  q.K = K;
+  q.bn = bn;
+  q.m_tiles = (e.M + kPairM - 1) / kPairM;
+  q.n_tiles = (e.cols + span - 1) / span;
+  q.tiles = q.m_tiles * q.n_tiles;
+  return linear_map(&q.a, a, e.M, K, 128) && linear_map(&q.b, b, e.N, K, bn / 2);
+}
+
+bool too_many(const LinearEpi& e) {
+  return (int64_t)((e.M + kPairM - 1) / kPairM) * ((e.cols + 47) / 48) > INT32_MAX / 4;
+}
+
+template <int A_ORDER, bool B_ROW, bool SWIGLU>
+moe_status_t launch_pairs(const PairWork& w, int pairs, cudaStream_t st) {
+  constexpr auto kern = linear_pair_kernel<A_ORDER, B_ROW, SWIGLU>;
+  return moe_host::launch_clusters(kern, dim3(2 * pairs), kPairThreads, kPairSmem, dim3(2, 1, 1), st, w,
+                                   moe_host::device_error_word());
+}
+
+template <int A_ORDER, bool B_ROW, bool SWIGLU>
+moe_status_t one_product(const LinearOp& a, const LinearOp& b, int K, const LinearEpi& e, cudaStream_t st) {
+  constexpr auto kern = linear_pair_kernel<A_ORDER, B_ROW, SWIGLU>;
+  if (too_many(e)) return MOE_ERR_INVALID_ARG;
   if (const moe_status_t s = moe_host::allow_smem<kern>(kPairSmem)) return s;
   const int most = pairs_resident<kern>(kPairSmem);
-  const int m_tiles = (e.M + kPairM - 1) / kPairM;
-  const int bn = choose_pairs(e, most, B_ROW).bn;
-  const int span = SWIGLU ? bn / 2 : bn, n_tiles = (e.cols + span - 1) / span;
-  if ((int64_t)m_tiles * n_tiles > INT32_MAX / 2) return MOE_ERR_INVALID_ARG;
-  CUtensorMap ta, tb;
-  if (!linear_map(&ta, a, e.M, K, 128) || !linear_map(&tb, b, e.N, K, bn / 2)) return MOE_ERR_CUDA;
-  const int tiles = m_tiles * n_tiles;
-  return moe_host::launch_clusters(kern, dim3(2 * (tiles < most ? tiles : most)), kPairThreads,
-                                   kPairSmem, dim3(2, 1, 1), st, ta, tb, e, K, bn, m_tiles, n_tiles,
-                                   moe_host::device_error_word());
+  PairWork w;
+  memset(&w, 0, sizeof w);
+  if (!set_product(w.product[0], a, b, K, e, choose_pairs(e, most, B_ROW).bn)) return MOE_ERR_CUDA;
+  const int tiles = w.product[0].tiles;
+  return launch_pairs<A_ORDER, B_ROW, SWIGLU>(w, tiles < most ? tiles : most, st);
+}
+
+float block_us(int K, int bn) { return (K + kLinBK - 1) / kLinBK * (bn + 217) * 0.5e-3f; }
+int64_t tiles_at(const LinearEpi& e, int bn) {
+  return (int64_t)((e.M + kPairM - 1) / kPairM) * ((e.cols + bn - 1) / bn);
+}
+
+// How two products are dealt: widths, the turns that the light pairs have for
+// themselves, and the time, by the same estimate as for one.
+struct BothChoice {
+  int bn[2];
+  int extra;
+  float us;
+};
+BothChoice choose_both(const LinearEpi (&e)[2], const int (&K)[2], int pairs) {
+  BothChoice best{{0, 0}, 0, 1e30f};
+  for (int b0 = 128; b0 <= 256; b0 += 128)
+    for (int b1 = 128; b1 <= 256; b1 += 128) {
+      const int64_t t0 = tiles_at(e[0], b0), t1 = tiles_at(e[1], b1);
+      const float c0 = block_us(K[0], b0) + 1.0f, c1 = block_us(K[1], b1) + 1.0f;
+      const int64_t whole = t0 / pairs, heavy = t0 % pairs, light = pairs - heavy;
+      for (int extra = 0; extra <= 64 && extra * light <= t1 && (extra == 0 || heavy); ++extra) {
+        const int64_t rest = (t1 - extra * light + pairs - 1) / pairs;
+        const float busy = (whole + 1) * c0 + rest * c1, idle = whole * c0 + (extra + rest) * c1;
+        const float us = 3.9f + (heavy && busy > idle ? busy : idle);
+        if (us < best.us) best = {{b0, b1}, extra, us};
+      }
+    }
+  return best;
 }
 
 }  // namespace
@@ -322,16 +426,36 @@ moe_status_t launch_pairs(const LinearOp& a, const LinearOp& b, int K, const Lin
 float linear_pairs_us(const LinearEpi& e, int K, bool b_rows) {
   const PairChoice c = choose_pairs(e, moe_host::sm_count() < 2 ? 1 : moe_host::sm_count() / 2, b_rows);
   const float waves = (float)c.waves;
-  return 4.9f + waves * ((K + kLinBK - 1) / kLinBK) * (c.bn + 217) * 0.5e-3f + (waves - 1.0f);
+  return 4.9f + waves * block_us(K, c.bn) + (waves - 1.0f);
 }
 
 moe_status_t linear_pairs(const LinearOp& a, const LinearOp& b, int K, const LinearEpi& e,
                           cudaStream_t st) {
-  if (e.act == MOE_ACT_SWIGLU) return launch_pairs<true, true, true>(a, b, K, e, st);
-  if (a.row_major)
-    return b.row_major ? launch_pairs<true, true, false>(a, b, K, e, st)
-                       : launch_pairs<true, false, false>(a, b, K, e, st);
-  return launch_pairs<false, false, false>(a, b, K, e, st);
+  if (e.act == MOE_ACT_SWIGLU) return one_product<kARows, true, true>(a, b, K, e, st);
+  if (!a.row_major) return one_product<kACols, false, false>(a, b, K, e, st);
+  return b.row_major ? one_product<kARows, true, false>(a, b, K, e, st)
+                     : one_product<kARows, false, false>(a, b, K, e, st);
+}
+
+float linear_pairs_both_us(const LinearEpi (&e)[2], const int (&K)[2]) {
+  return choose_both(e, K, moe_host::sm_count() < 2 ? 1 : moe_host::sm_count() / 2).us;
+}
+
+moe_status_t linear_pairs_both(const LinearOp (&a)[2], const LinearOp (&b)[2], const int (&K)[2],
+                               const LinearEpi (&e)[2], cudaStream_t st) {
+  constexpr auto kern = linear_pair_kernel<kABoth, false, false>;
+  if (too_many(e[0]) || too_many(e[1])) return MOE_ERR_INVALID_ARG;
+  if (const moe_status_t s = moe_host::allow_smem<kern>(kPairSmem)) return s;
+  const int pairs = pairs_resident<kern>(kPairSmem);
+  const BothChoice c = choose_both(e, K, pairs);
+  PairWork w;
+  memset(&w, 0, sizeof w);
+  for (int i = 0; i < 2; ++i)
+    if (!set_product(w.product[i], a[i], b[i], K[i], e[i], c.bn[i])) return MOE_ERR_CUDA;
+  w.heavy = w.product[0].tiles % pairs;
+  w.extra = c.extra;
+  w.rows_first = a[0].row_major ? 0 : 1;
+  return launch_pairs<kABoth, false, false>(w, pairs, st);
 }
 
 }  // namespace moe
