@@ -185,8 +185,11 @@ extern "C" moe_status_t moe_linear_backward(const void* d_out, int d_dtype, int6
   uint16_t* made = direct ? nullptr : d_preact;
   if (made || d_bias) {
     const int run = dz_run(T, cols);
-    DzParams p{d_out, ld_d, preact, made, ld_dp, d_bias ? static_cast<float*>(workspace) : nullptr,
-               T, N, cols, activation, run, 0};
+    // one run of rows: its sums are the bias's gradient
+    const bool whole = dz_runs(T, run) == 1;
+    DzParams p{d_out, ld_d, preact, made, ld_dp,
+               d_bias ? (whole ? d_bias : static_cast<float*>(workspace)) : nullptr, T, N, cols,
+               activation, run, 0};
     p.vec = cols % 8 == 0 && aligned16(d_out) && ld_d % 8 == 0 && aligned16(preact) && N % 8 == 0;
     const dim3 grid((cols + kDzCols - 1) / kDzCols, (unsigned)dz_runs(T, run)), block(32, kDzRows);
     using moe_host::launch;
@@ -196,7 +199,7 @@ extern "C" moe_status_t moe_linear_backward(const void* d_out, int d_dtype, int6
                                   : (db ? launch(linear_dz_kernel<true, false>, grid, block, 0, st, p)
                                         : launch(linear_dz_kernel<false, false>, grid, block, 0, st, p));
     if (r) return r;
-    if (d_bias)
+    if (d_bias && !whole)
       if (const moe_status_t s = moe_host::column_sums(p.part, (int)dz_runs(T, run), N, N, d_bias, nullptr, st))
         return s;
   }

@@ -30,7 +30,9 @@ constexpr int kPairTmem = 512;
 constexpr int kPairN = 256;    // widest tile
 constexpr int kPairStages = 6;
 constexpr int kPairStageBytes = (128 + kPairN / 2) * 128;
-constexpr size_t kPairSmem = (size_t)kPairStages * kPairStageBytes + 1024;
+constexpr int kPairStrip = 32 * 128;  // an epilogue warp's: 32 rows x 128 bytes
+constexpr size_t kPairRing = (size_t)kPairStages * kPairStageBytes;
+constexpr size_t kPairSmem = kPairRing + kPairEpiWarps * kPairStrip + 1024;
 
 // As linear_tma_2d, on a barrier of either CTA of the pair (`bar` as the
 // cluster has it).
@@ -108,6 +110,100 @@ __device__ __forceinline__ PairTile pair_tile(const PairWork& w, int pair, int p
   const int per = kPairGroup * q.n_tiles, g = t / per, r = t - g * per;
   const int rows = min(kPairGroup, q.m_tiles - g * kPairGroup);
   return {which, g * kPairGroup + r % rows, r / rows};
+}
+
+// ---- the epilogue of rows off their 16-byte boundary ----------------------------
+//
+// A lane's sums are a row of the tile.  Rows of whole 16-byte pieces it stores
+// itself; else single values would go to as many lines as there are lanes, so a
+// strip of 32 rows x 128 bytes goes through shared memory and neighbouring lanes
+// take neighbouring columns (335 x 408 x 3468, us: 20.0 without, 12.3; where pieces
+// are whole the detour costs: 4096 x 2048 x 1536 SwiGLU 19.7 without, 20.3).  Piece
+// p (16 bytes) of row r lies at p ^ (r & 7), without bank conflicts.
+
+__device__ __forceinline__ unsigned char* strip_at(unsigned char* strip, int row, int piece) {
+  return strip + row * 128 + ((piece ^ (row & 7)) << 4);
+}
+
+// The strip -> `n` columns at `col` of the warp's rows (of which `rows` are there)
+// of a matrix with rows of `ld` elements, plus what `residual` has there.  By the
+// warp together.
+template <bool BF16>
+__device__ __forceinline__ void strip_store(unsigned char* strip, void* p, const void* residual,
+                                            int64_t row0, int rows, int64_t ld, int64_t col, int n) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 4
+  for (int r = 0; r < rows; ++r)
+    for (int c = lane; c < n; c += 32) {
+      const int64_t at = (row0 + r) * ld + col + c;
+      float f = *reinterpret_cast<float*>(strip_at(strip, r, c / 4) + (c % 4) * 4);
+      if constexpr (BF16) {
+        if (residual) f += bf16_bits_to_f32(static_cast<const uint16_t*>(residual)[at]);
+        static_cast<uint16_t*>(p)[at] = f32_to_bf16_rne(f);
+      } else {
+        if (residual) f += static_cast<const float*>(residual)[at];
+        static_cast<float*>(p)[at] = f;
+      }
+    }
+  __syncwarp();
+}
+
+// Sixteen of a row's sums with their bias; columns past `left` get any.
+__device__ __forceinline__ void strip_sums(float (&z)[16], uint32_t tmem, const float* bias, int left) {
+  uint32_t r[16];
+  tmem_ld16(tmem, r);
+  tmem_ld_wait();
+#pragma unroll
+  for (int x = 0; x < 16; ++x) z[x] = __uint_as_float(r[x]) + (bias && x < left ? bias[x] : 0.0f);
+}
+
+// 32 columns of the tile, from accumulator column `tmem` on, to column `col` of the
+// outputs; `done` is called when nothing reads the sums any more, if `last`.
+template <bool SWIGLU, typename F>
+__device__ __forceinline__ void strip_finish(const LinearEpi& e, unsigned char* strip, uint32_t tmem, int up,
+                                             int64_t row0, int rows, int col, int n, bool last, F&& done) {
+  const int lane = threadIdx.x & 31;
+  auto hold = [&](int c, const float (&z)[16]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<float4*>(strip_at(strip, lane, c / 4 + q)) =
+          make_float4(z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]);
+  };
+  if (e.preact) {
+#pragma unroll 1
+    for (int h = 0; h < (SWIGLU ? 2 : 1); ++h) {
+#pragma unroll 1
+      for (int c = 0; c < n; c += 16) {
+        float z[16];
+        strip_sums(z, tmem + h * up + c, e.bias ? e.bias + h * e.cols + col + c : nullptr, n - c);
+        hold(c, z);
+      }
+      __syncwarp();
+      strip_store<true>(strip, e.preact, nullptr, row0, rows, e.N, h * e.cols + col, n);
+    }
+  }
+#pragma unroll 1
+  for (int c = 0; c < n; c += 16) {
+    float z[16];
+    strip_sums(z, tmem + c, e.bias ? e.bias + col + c : nullptr, n - c);
+    if constexpr (SWIGLU) {
+      float u[16];
+      strip_sums(u, tmem + up + c, e.bias ? e.bias + e.cols + col + c : nullptr, n - c);
+#pragma unroll
+      for (int x = 0; x < 16; ++x) z[x] = swiglu_f32(z[x], u[x]);
+    } else if (e.act == MOE_ACT_SILU) {
+#pragma unroll
+      for (int x = 0; x < 16; ++x) z[x] = silu_f32(z[x]);
+    } else if (e.act == MOE_ACT_GELU) {
+#pragma unroll
+      for (int x = 0; x < 16; ++x) z[x] = gelu_f32(z[x]);
+    }
+    hold(c, z);
+  }
+  if (last) done();
+  __syncwarp();
+  if (e.out_bf16) strip_store<true>(strip, e.out, e.residual, row0, rows, e.cols, col, n);
+  else strip_store<false>(strip, e.out, e.residual, row0, rows, e.cols, col, n);
 }
 
 // A's order.  Of two products one has it in rows of k, the other by columns.
@@ -249,6 +345,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
   } else {
     const int quad = warp & 3, half = (warp - 2) >> 2;
+    unsigned char* strip = smem + kPairRing + (warp - 2) * kPairStrip;
     for (int i = 0;; ++i) {
       const PairTile at = pair_tile<kTwo>(work, pair, pairs, i);
       if (at.which < 0) break;
@@ -270,29 +367,44 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
       tc_fence_after();
       const uint32_t base = tmem + buf * kPairN + ((uint32_t)(quad * 32) << 16);
+      auto done = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) remote_arrive(cluster_addr(&sums_empty[buf], 0));
+      };
+      if (e.vec) {
 #pragma unroll 1
-      for (int c = half * 16; c < span; c += 32) {
-        uint32_t r[2][16];
-        tmem_ld16(base + c, r[0]);
-        if constexpr (SWIGLU) tmem_ld16(base + span + c, r[1]);
-        tmem_ld_wait();
-        if (c + 32 >= span) {  // the sums are in registers
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) remote_arrive(cluster_addr(&sums_empty[buf], 0));
-        }
-        if (row < e.M) {
+        for (int c = half * 16; c < span; c += 32) {
+          uint32_t r[2][16];
+          tmem_ld16(base + c, r[0]);
+          if constexpr (SWIGLU) tmem_ld16(base + span + c, r[1]);
+          tmem_ld_wait();
+          if (c + 32 >= span) done();  // the sums are in registers
+          if (row < e.M) {
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            float z[8], u[8];
+            for (int q = 0; q < 2; ++q) {
+              float z[8], u[8];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-              z[x] = __uint_as_float(r[0][q * 8 + x]);
-              if constexpr (SWIGLU) u[x] = __uint_as_float(r[1][q * 8 + x]);
+              for (int x = 0; x < 8; ++x) {
+                z[x] = __uint_as_float(r[0][q * 8 + x]);
+                if constexpr (SWIGLU) u[x] = __uint_as_float(r[1][q * 8 + x]);
+              }
+              finish8<SWIGLU>(e, row, at.n * span + c + q * 8, z, u);
             }
-            finish8<SWIGLU>(e, row, at.n * span + c + q * 8, z, u);
           }
         }
+      } else {
+        const int64_t row0 = row - lane;
+        const int rows = (int)(e.M - row0 < 32 ? (e.M > row0 ? e.M - row0 : 0) : 32);
+        const int width = min(span, e.cols - at.n * span);  // columns that are there
+        bool left = false;
+        for (int c = half * 32; c < width; c += 64) {
+          const bool last = c + 64 >= width;
+          left |= last;
+          strip_finish<SWIGLU>(e, strip, base + c, span, row0, rows, at.n * span + c, min(32, width - c),
+                               last, done);
+        }
+        if (!left) done();  // no columns of this tile for this warp
       }
     }
   }

@@ -791,7 +791,6 @@ PyObject* linear_backward(Args a) {
   const bool accumulate = a.flag();
   Tensor d_b = a.tensor("d_bias", true), ws = a.tensor("workspace", true), d_z;
   const StreamArg stream(a.next());
-  int64_t features = 0;
   const moe_status_t s = unlocked([&] {
     const int64_t ld_x = mapped_rows(x, "x");
     const c10::Device dev = x.device();
@@ -806,7 +805,6 @@ PyObject* linear_backward(Args a) {
     const int N = as_int(w.defined() ? w.size(0) : d.size(1) * (act == MOE_ACT_SWIGLU ? 2 : 1), "N");
     if (w.defined()) like(w, {N, K}, at::kBFloat16, dev, "w");
     const int64_t cols = act == MOE_ACT_SWIGLU ? N / 2 : N;
-    features = N;
     const int64_t ld_d = rows_like(d, T, cols, dev, "d_out");
     if (preact.defined()) like(preact, {T, N}, at::kBFloat16, dev, "preact");
     else if (act != MOE_ACT_NONE) throw Refused("preact is needed for the activation's gradient");
@@ -836,7 +834,7 @@ PyObject* linear_backward(Args a) {
       d_z = d;
     } else {
       ld_z = ((int64_t)N + 7) / 8 * 8;
-      d_z = make({T, ld_z}, at::kBFloat16, dev);
+      d_z = at::detail::empty_strided_cuda({T, N}, {ld_z, 1}, at::kBFloat16, dev);
     }
     if (!ws.defined() && d_b.defined())
       ws = make({(int64_t)moe_linear_backward_workspace_size(T, N, act)}, at::kByte, dev);
@@ -847,7 +845,6 @@ PyObject* linear_backward(Args a) {
                                ws.defined() ? scratch_bytes(ws, dev) : 0, on.handle);
   });
   if (s) return status(s);
-  if (d_z.size(1) != features) d_z = d_z.narrow(1, 0, features);
   return result({d_x, d_w, d_b, d_z, ws});
 }
 
