@@ -137,23 +137,11 @@ __device__ __forceinline__ void store_bf16x8(uint16_t* p, const float* f) {
 
 // 32 columns of a row at once, of which `left` are there: what the call leaves out
 // costs a branch for all of them, not for eight (4096 x 4096 sums over 512: 24.6 us
-// in eights, 22.4, and 21.7 with a way of its own for `plain` sums).
+// in eights, 22.4; bf16 sums as they are have a loop of their own, 21.7).
 template <bool SWIGLU>
 __device__ __forceinline__ void wide_finish(const LinearEpi& e, int64_t row, int col, int left,
                                             const uint32_t (&r)[SWIGLU ? 4 : 2][16],
-                                            const Residual8 (&res)[4], bool plain) {
-  if (!SWIGLU && plain) {
-    uint16_t* p = static_cast<uint16_t*>(e.out) + row * e.cols + col;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (8 * q >= left) continue;
-      float f[8];
-#pragma unroll
-      for (int x = 0; x < 8; ++x) f[x] = __uint_as_float(r[q >> 1][(q & 1) * 8 + x]);
-      store_bf16x8(p + 8 * q, f);
-    }
-    return;
-  }
+                                            const Residual8 (&res)[4]) {
   float z[32], u[SWIGLU ? 32 : 1];
 #pragma unroll
   for (int x = 0; x < 32; ++x) {
@@ -492,9 +480,33 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         __syncwarp();
         if (lane == 0) remote_arrive(cluster_addr(&sums_empty[buf], 0));
       };
-      if (e.vec) {
+      const bool plain = !SWIGLU && e.out_bf16 && e.act == MOE_ACT_NONE && !e.bias && !e.residual && !e.preact;
+      if (plain && e.vec) {
+        uint16_t* out = static_cast<uint16_t*>(e.out) + row * e.cols + at.n * span;
+        const int width = min(span, e.cols - at.n * span);
+        bool left = false;
+#pragma unroll 1
+        for (int c = half * 32; c < span; c += 64) {
+          uint32_t r[2][16];
+          tmem_ld16(base + c, r[0]);
+          tmem_ld16(base + c + 16, r[1]);
+          tmem_ld_wait();
+          if (c + 64 >= span) {
+            done();
+            left = true;
+          }
+          if (row >= e.M) continue;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float f[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) f[x] = __uint_as_float(r[q >> 1][(q & 1) * 8 + x]);
+            if (c + q * 8 < width) store_bf16x8(out + c + q * 8, f);
+          }
+        }
+        if (!left) done();
+      } else if (e.vec) {
         const int width = min(span, e.cols - at.n * span);  // columns that are there
-        const bool plain = e.out_bf16 && e.act == MOE_ACT_NONE && !e.bias && !e.residual && !e.preact;
         bool left = false;
 #pragma unroll 1
         for (int c = half * 32; c < span; c += 64) {
@@ -515,7 +527,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             done();
             left = true;
           }
-          if (row < e.M) wide_finish<SWIGLU>(e, row, at.n * span + c, width - c, r, res, plain);
+          if (row < e.M) wide_finish<SWIGLU>(e, row, at.n * span + c, width - c, r, res);
         }
         if (!left) done();  // no columns of this tile for this warp
       } else {
