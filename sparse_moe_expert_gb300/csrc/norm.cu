@@ -345,7 +345,13 @@ __device__ __forceinline__ void load2(float2 (&f)[4], const void* p, int bf16, i
 // meanwhile.  Weight and bias lie there as fp32, [H] each, in front of the rows: from
 // global memory they would not stay in the L1 that is left.  One CTA per SM, its
 // warps as many as registers and shared memory allow.
-constexpr size_t kNormRoom = 200 * 1024;
+// Dynamic shared memory of a CTA, at most, and of one of `n` per SM (which has 228 KB
+// and keeps 1 KB for each).
+constexpr size_t kNormRoom = 226 * 1024;
+constexpr int norm_room(int n) {
+  const int share = 228 * 1024 / n - 1536;
+  return share < (int)kNormRoom ? share : (int)kNormRoom;
+}
 // Warps whose rows (4 or 8 registers per vector and lane) the registers hold.
 constexpr int warp_rows_most(bool bf16, int nv) { return nv * (bf16 ? 4 : 8) <= 64 ? 16 : 12; }
 
@@ -485,23 +491,28 @@ __global__ void __launch_bounds__(warp_rows_most(X_BF16, NV) * 32, 1)
 }
 
 // The gradient: bulk copies bring the rows of a CTA's next turns into shared memory
-// while it works on one.  A thread takes eight columns and keeps their weights.
+// while it works on one.  A thread takes NV vectors of eight columns.  One vector
+// leaves registers for its weights and for two CTAs of 512 threads per SM; two of them
+// need twice the registers, and the weights lie in shared memory in front of the rows
+// (bf16 with d_sum, us with one vector and two: 16384 x 4096 98, 123; 4096 x 8192,
+// where one takes CTAs of 1024 threads, 64, 49).
 constexpr int kRingMost = 8;
+constexpr int kRingThreads = 512;
 struct RingPlan {
-  int threads, per_sm, stages;
+  int nv, threads, per_sm, stages;
   int stage_bytes;
 };
 
-template <bool D_BF16, bool X_BF16>
-__global__ void __launch_bounds__(1024)
+template <bool D_BF16, bool X_BF16, int NV>
+__global__ void __launch_bounds__(kRingThreads, NV == 1 ? 2 : 1)
     layer_norm_backward_ring_kernel(NormGradParams p, int stages, int stage_bytes, unsigned int* err) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ __align__(8) uint64_t full[kRingMost];
-  __shared__ float2 part[2][32];
+  __shared__ float2 part[2][kRingThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-  const int col = tid * 8;
-  const bool on = col < p.H;
   const uint32_t d_bytes = p.H * (D_BF16 ? 2 : 4), x_bytes = p.H * (X_BF16 ? 2 : 4);
+  float* w_s = reinterpret_cast<float*>(smem);
+  unsigned char* rows = smem + (NV > 1 && p.weight ? (size_t)p.H * 4 : 0);
   if (tid == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
     fence_barrier_init();
@@ -512,7 +523,7 @@ __global__ void __launch_bounds__(1024)
   const int64_t step = gridDim.x;
   const uint32_t row_bytes = d_bytes + x_bytes + (p.d_sum ? x_bytes : 0);
   auto fetch = [&](int64_t t, int s) {  // by thread 0
-    unsigned char* at = smem + (size_t)s * stage_bytes;
+    unsigned char* at = rows + (size_t)s * stage_bytes;
     mbar_arrive_expect_tx(&full[s], row_bytes);
     bulk_g2s(at, static_cast<const unsigned char*>(p.d_out) + t * p.ldd * (D_BF16 ? 2 : 4), d_bytes, &full[s]);
     bulk_g2s(at + d_bytes, static_cast<const unsigned char*>(p.x) + t * p.ldx * (X_BF16 ? 2 : 4), x_bytes,
@@ -525,13 +536,22 @@ __global__ void __launch_bounds__(1024)
     for (int s = 0; s < stages; ++s)
       if (blockIdx.x + s * step < p.T) fetch(blockIdx.x + s * step, s);
   const float2 zero = make_float2(0.0f, 0.0f);
-  float2 dw[4], db[4], w[4];
+  float2 dw[NV][4], db[NV][4], w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    dw[i] = db[i] = zero;
-    w[i] = both(1.0f);
+  for (int i = 0; i < 4; ++i) w[i] = both(1.0f);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dw[j][i] = db[j][i] = zero;
+    const int col = (j * (int)blockDim.x + tid) * 8;
+    if (!p.weight || col >= p.H) continue;
+    load2(w, p.weight, p.w_bf16, col);
+    if constexpr (NV > 1) {  // read by this thread alone
+      Vec8<false> v;
+      set2(v, w);
+      v.store(w_s, col);
+    }
   }
-  if (on && p.weight) load2(w, p.weight, p.w_bf16, col);
   const float inv_h = 1.0f / (float)p.H;
   // the next row's statistics are on their way during this one
   float mu = 0.0f, rstd = 0.0f;
@@ -548,25 +568,32 @@ __global__ void __launch_bounds__(1024)
       rstd = p.rstd[t + step];
     }
     if (!mbar_wait(&full[s], phase, kWaitBudgetCycles)) bad = 1;
-    const unsigned char* at = smem + (size_t)s * stage_bytes;
-    float2 c[4], xh[4], s0 = zero, s1 = zero;
-    Vec8<X_BF16> ds;
-    if (on) {
+    const unsigned char* at = rows + (size_t)s * stage_bytes;
+    float2 c[NV][4], xh[NV][4], s0 = zero, s1 = zero;
+    Vec8<X_BF16> ds[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int col = (j * (int)blockDim.x + tid) * 8;
+      if (col >= p.H) continue;
       Vec8<D_BF16> dv;
       Vec8<X_BF16> xv;
       dv.load(at, col);
       xv.load(at + d_bytes, col);
-      if (p.d_sum) ds.load(at + d_bytes + x_bytes, col);
-      get2(c, dv);
-      get2(xh, xv);
+      if (p.d_sum) ds[j].load(at + d_bytes + x_bytes, col);
+      get2(c[j], dv);
+      get2(xh[j], xv);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        xh[i] = ffma2(xh[i], both(r), both(shift));
-        db[i] = add2(db[i], c[i]);
-        dw[i] = ffma2(c[i], xh[i], dw[i]);
-        c[i] = mul2(c[i], w[i]);
-        s0 = add2(s0, c[i]);
-        s1 = ffma2(c[i], xh[i], s1);
+        xh[j][i] = ffma2(xh[j][i], both(r), both(shift));
+        db[j][i] = add2(db[j][i], c[j][i]);
+        dw[j][i] = ffma2(c[j][i], xh[j][i], dw[j][i]);
+      }
+      if (NV > 1 && p.weight) load2(w, w_s, 0, col);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c[j][i] = mul2(c[j][i], w[i]);
+        s0 = add2(s0, c[j][i]);
+        s1 = ffma2(c[j][i], xh[j][i], s1);
       }
     }
     float sum[2] = {s0.x + s0.y, s1.x + s1.y};
@@ -579,17 +606,20 @@ __global__ void __launch_bounds__(1024)
     sum[0] = mine.x;
     sum[1] = mine.y;
     warp_sum(sum);
-    if (on) {
-      const float2 m0 = both(p.mean ? -r * (sum[0] * inv_h) : 0.0f), m1 = both(-r * (sum[1] * inv_h));
+    const float2 m0 = both(p.mean ? -r * (sum[0] * inv_h) : 0.0f), m1 = both(-r * (sum[1] * inv_h));
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int col = (j * (int)blockDim.x + tid) * 8;
+      if (col >= p.H) continue;
       float2 g[4];
-      if (p.d_sum) get2(g, ds);
+      if (p.d_sum) get2(g, ds[j]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        c[i] = ffma2(c[i], both(r), ffma2(xh[i], m1, m0));
-        if (p.d_sum) c[i] = add2(c[i], g[i]);
+        c[j][i] = ffma2(c[j][i], both(r), ffma2(xh[j][i], m1, m0));
+        if (p.d_sum) c[j][i] = add2(c[j][i], g[i]);
       }
       Vec8<X_BF16> o;
-      set2(o, c);
+      set2(o, c[j]);
       o.store(p.d_x, t * p.H + col);
     }
     if (++s == stages) {
@@ -604,13 +634,18 @@ __global__ void __launch_bounds__(1024)
     }
     return;
   }
-  if (!p.part || !on) return;
+  if (!p.part) return;
   float* out = p.part + (int64_t)blockIdx.x * 2 * p.H;
-  Vec8<false> o;
-  set2(o, dw);
-  o.store(out, col);
-  set2(o, db);
-  o.store(out, p.H + col);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int col = (j * (int)blockDim.x + tid) * 8;
+    if (col >= p.H) continue;
+    Vec8<false> o;
+    set2(o, dw[j]);
+    o.store(out, col);
+    set2(o, db[j]);
+    o.store(out, p.H + col);
+  }
 }
 
 // ---- column sums ---------------------------------------------------------------
@@ -671,16 +706,17 @@ Shape norm_shape(int H, int want) {
   return {nv, ((vecs + nv - 1) / nv + 31) / 32 * 32, 1};
 }
 
-// A thread for each vector; as many CTAs as make 1024 threads per SM, of narrow
-// rows up to eight; then as many stages as the shared memory holds.
-RingPlan ring_plan(int H, int row_bytes) {
+// CTAs of one vector per thread make 1024 threads per SM, of narrow rows eight CTAs;
+// then as many stages as the shared memory holds.
+RingPlan ring_plan(int H, int row_bytes, int weight_bytes) {
   RingPlan r;
-  r.threads = (H / 8 + 31) / 32 * 32;
-  r.per_sm = 1024 / r.threads < 8 ? 1024 / r.threads : 8;
+  r.nv = H <= kRingThreads * 8 ? 1 : 2;
+  r.threads = ((H / 8 + r.nv - 1) / r.nv + 31) / 32 * 32;
+  r.per_sm = r.nv == 2 ? 1 : 1024 / r.threads < 8 ? 1024 / r.threads : 8;
   r.stage_bytes = row_bytes;
-  while (r.per_sm > 1 && (int)kNormRoom / r.per_sm / row_bytes < 2) --r.per_sm;
-  r.stages = (int)kNormRoom / r.per_sm / row_bytes;
-  if (r.stages > kRingMost) r.stages = kRingMost;
+  auto stages = [&] { return (norm_room(r.per_sm) - weight_bytes) / row_bytes; };
+  while (r.per_sm > 1 && stages() < 2) --r.per_sm;
+  r.stages = stages() < kRingMost ? stages() : kRingMost;
   return r;
 }
 
@@ -705,21 +741,31 @@ moe_status_t launch_norm_grad(const NormGradParams& p, const Shape& s, int grid,
 // CTAs of the gradient, at most: as many as the workspace has room for.
 int norm_grad_ctas(int64_t T, int H) {
   const Shape s = norm_shape(H, 2);
-  const int per_sm = s.rows > 1 ? 4 : ring_plan((H + 7) / 8 * 8, 1).per_sm;
+  const int per_sm = s.rows > 1 ? 4 : ring_plan((H + 7) / 8 * 8, 1, 0).per_sm;
   const int64_t most = (int64_t)moe_host::sm_count() * per_sm;
   const int64_t need = (T + s.rows - 1) / s.rows;
   return (int)(need < most ? need : most);
 }
 
+template <auto Kernel>
+moe_status_t launch_ring(const NormGradParams& p, const RingPlan& r, int weight_bytes, int grid,
+                         cudaStream_t st) {
+  if (const moe_status_t s = moe_host::allow_smem<Kernel>(kNormRoom)) return s;
+  return moe_host::launch(Kernel, dim3(grid), dim3(r.threads),
+                          (size_t)weight_bytes + (size_t)r.stages * r.stage_bytes, st, p, r.stages,
+                          r.stage_bytes, moe_host::device_error_word());
+}
+
 template <bool D_BF16, bool X_BF16>
 moe_status_t norm_grad_ring(const NormGradParams& p, int& grid, cudaStream_t st) {
-  constexpr auto kern = layer_norm_backward_ring_kernel<D_BF16, X_BF16>;
-  const RingPlan r = ring_plan(p.H, p.H * ((D_BF16 ? 2 : 4) + (X_BF16 ? 2 : 4) * (p.d_sum ? 2 : 1)));
+  const int weight = p.weight && p.H > kRingThreads * 8 ? p.H * 4 : 0;
+  const RingPlan r =
+      ring_plan(p.H, p.H * ((D_BF16 ? 2 : 4) + (X_BF16 ? 2 : 4) * (p.d_sum ? 2 : 1)), weight);
   const int most = moe_host::sm_count() * r.per_sm;
   if (grid > most) grid = most;
-  if (const moe_status_t s = moe_host::allow_smem<kern>(kNormRoom)) return s;
-  return moe_host::launch(kern, dim3(grid), dim3(r.threads), (size_t)r.stages * r.stage_bytes, st, p,
-                          r.stages, r.stage_bytes, moe_host::device_error_word());
+  return r.nv == 1
+             ? launch_ring<layer_norm_backward_ring_kernel<D_BF16, X_BF16, 1>>(p, r, weight, grid, st)
+             : launch_ring<layer_norm_backward_ring_kernel<D_BF16, X_BF16, 2>>(p, r, weight, grid, st);
 }
 
 template <bool X_BF16, bool OUT_BF16, int NV>
