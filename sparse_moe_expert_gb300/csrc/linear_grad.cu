@@ -29,17 +29,23 @@ struct DzParams {
 
 // silu(z) and its derivative s (1 + z (1 - s)), s = 1 / (1 + e^-z).
 __device__ __forceinline__ float silu_slope(float z, float& value) {
-  const float s = __fdividef(1.0f, 1.0f + expf(-z));
+  const float s = __fdividef(1.0f, 1.0f + __expf(-z));
   value = z * s;
   return s * fmaf(z, 1.0f - s, 1.0f);
 }
 // Phi(z) + z phi(z).
 __device__ __forceinline__ float gelu_slope(float z) {
-  return fmaf(z * 0.39894228040143268f, expf(-0.5f * z * z), 0.5f * erfcf(z * -0.70710678118654752f));
+  return fmaf(z * 0.39894228040143268f, __expf(-0.5f * z * z),
+              fmaf(0.5f, erff(z * 0.70710678118654752f), 0.5f));
 }
 
-template <bool D_BF16, bool SWIGLU>
-__global__ void __launch_bounds__(256) linear_dz_kernel(DzParams p) {
+// KIND: no activation, SiLU or GELU, SwiGLU.
+enum { kDzNone, kDzOne, kDzGated };
+
+template <bool D_BF16, int KIND>
+__global__ void __launch_bounds__(256, 4) linear_dz_kernel(DzParams p) {
+  constexpr bool SWIGLU = KIND == kDzGated;
+  constexpr int kUnroll = KIND == kDzNone ? 4 : 1;  // rows of a thread at a time
   __shared__ float join[SWIGLU ? 2 : 1][kDzRows][kDzCols];
   pdl_wait();
   pdl_trigger();
@@ -49,14 +55,14 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(DzParams p) {
   float sum[SWIGLU ? 2 : 1][8] = {};
   const int64_t t1 = min((int64_t)(blockIdx.y + 1) * p.run, (int64_t)p.T);
   if (n > 0) {
-#pragma unroll 2
+#pragma unroll kUnroll
     for (int64_t t = (int64_t)blockIdx.y * p.run + threadIdx.y; t < t1; t += kDzRows) {
       Vec8<D_BF16> dv;
       if (vec) dv.load(p.d_out, t * p.ld_d + c);
       else dv.load_some(p.d_out, t * p.ld_d + c, n);
       float d[SWIGLU ? 2 : 1][8];
       dv.get(d[0]);
-      if (p.act != MOE_ACT_NONE) {
+      if constexpr (KIND != kDzNone) {
         Vec8<true> zv;
         float z[8];
         const int64_t at = t * p.N + c;
@@ -194,10 +200,12 @@ extern "C" moe_status_t moe_linear_backward(const void* d_out, int d_dtype, int6
     const dim3 grid((cols + kDzCols - 1) / kDzCols, (unsigned)dz_runs(T, run)), block(32, kDzRows);
     using moe_host::launch;
     const bool db = d_dtype == MOE_DTYPE_BF16;
-    const moe_status_t r = swiglu ? (db ? launch(linear_dz_kernel<true, true>, grid, block, 0, st, p)
-                                        : launch(linear_dz_kernel<false, true>, grid, block, 0, st, p))
-                                  : (db ? launch(linear_dz_kernel<true, false>, grid, block, 0, st, p)
-                                        : launch(linear_dz_kernel<false, false>, grid, block, 0, st, p));
+    auto go = [&](auto kern) { return launch(kern, grid, block, 0, st, p); };
+    const moe_status_t r =
+        swiglu ? (db ? go(linear_dz_kernel<true, kDzGated>) : go(linear_dz_kernel<false, kDzGated>))
+        : activation != MOE_ACT_NONE
+            ? (db ? go(linear_dz_kernel<true, kDzOne>) : go(linear_dz_kernel<false, kDzOne>))
+            : (db ? go(linear_dz_kernel<true, kDzNone>) : go(linear_dz_kernel<false, kDzNone>));
     if (r) return r;
     if (d_bias && !whole)
       if (const moe_status_t s = moe_host::column_sums(p.part, (int)dz_runs(T, run), N, N, d_bias, nullptr, st))
