@@ -18,7 +18,9 @@
  *   [C] "oMLX MoE gate/up 融合优化：qwen35_moe_gate_up 实现剖析" (xdnf.cn/news/169715)
  *
  * Beside these steps: routing by scores with its gradient, the combine's
- * gradient, and low-rank adapters of many requests (the last declarations).
+ * gradient, and low-rank adapters of many requests; the norms around the layer
+ * and a dense product (a shared expert, a projection) with their gradients, and
+ * the AdamW step (the last declarations).
  *
  * Conventions shared by every call
  * --------------------------------
@@ -726,8 +728,9 @@ moe_status_t moe_layer_norm_backward(const void* d_out, int d_dtype, int64_t ld_
  * coded after the step has used m and v; scales are fp32 [ceil(n / 256)].  A
  * value that is not finite makes its block's states NaN.
  *
- * tensors     host array (read before the call returns).  The tensors are
- *             different memory and do not overlap; the same param twice is refused.
+ * tensors     host array (read before the call returns).  The buffers are
+ *             different memory; overlaps within a tensor, and of the tensors'
+ *             params, masters, states or scales among each other, are refused.
  * param_dtype, grad_dtype  fp32 or bf16, for all tensors; masters for all
  *             tensors or none, and only beside bf16 params.
  * lr_dev      device scalar that takes lr's place, or NULL (a captured graph

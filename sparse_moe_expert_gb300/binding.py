@@ -582,8 +582,8 @@ def moe_linear_backward(d_out, x, w, preact=None, activation: int = _lib.ACT_NON
 
     d_out is the residual's gradient as it stands.  d_w is fp32 unless d_w or
     d_w_dtype says bf16; with accumulate d_w is added to.  w may be None where d_x is
-    not wanted.  d_preact is d_out itself
-    where there is no activation and d_out is bf16 with 16-byte aligned rows."""
+    not wanted.  d_preact is d_out itself where there is no activation and d_out is
+    bf16 with 16-byte aligned rows."""
     if d_w_dtype is not None:
         if d_w_dtype not in _DT:
             raise ValueError(f"d_w_dtype must be float32 or bfloat16, got {d_w_dtype}")
@@ -600,7 +600,8 @@ def moe_linear_backward(d_out, x, w, preact=None, activation: int = _lib.ACT_NON
 def moe_adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, beta1: float = 0.9,
                    beta2: float = 0.999, eps: float = 1e-8, weight_decay=0.0, masters=None,
                    exp_avg_scales=None, exp_avg_sq_scales=None, grad_scale=None, stream=None):
-    """One AdamW step over lists of dense tensors, in place.
+    """One AdamW step over lists of dense tensors, in place (no two of one list
+    may overlap).
 
     params: all fp32, or all bf16 (with fp32 ``masters``, of which they are the
     rounding, or without); grads all fp32 or all bf16.  States are fp32, or

@@ -100,7 +100,6 @@ __device__ __forceinline__ int tensor_of(const AdamTable<CAP>& tab, int u) {
   return lo;
 }
 
-// The bytes of w become floats without a conversion, as the end of 2^23's mantissa.
 // Pairs of values: one instruction for both.  Each result is rounded on its own, but
 // a product and a sum that follow each other may be joined.
 __device__ __forceinline__ float2 mul2_rn(float2 a, float2 b) {
@@ -129,7 +128,8 @@ __device__ __forceinline__ float2 decode_r2(float2 c, float s) {
   const float2 a = mul2_rn(c, both((float)(1.0 / 255.0)));
   return mul2_rn(mul2_rn(a, a), both(s));
 }
-// Bytes e and e + 1 of w.
+// Bytes e and e + 1 of w, which become floats without a conversion, as the end of
+// 2^23's mantissa.
 __device__ __forceinline__ float2 byte_floats(uint32_t w, int e) {
   return add2_rn(make_float2(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u | (uint32_t)e)),
                              __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7441u + (uint32_t)e))),
@@ -529,6 +529,32 @@ bool at_least_aligned(const void* p, int bytes) {
   return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0;
 }
 
+struct Span {
+  uintptr_t lo, hi;
+};
+Span span(const void* p, int64_t bytes) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  return {lo, p ? lo + (uintptr_t)bytes : lo};
+}
+// The buffers of one tensor share nothing.
+bool apart(const Span (&s)[7]) {
+  for (int i = 0; i < 7; ++i)
+    for (int j = i + 1; j < 7; ++j)
+      if (s[i].lo < s[j].hi && s[j].lo < s[i].hi) return false;
+  return true;
+}
+// Buffers of one kind share nothing.  Tensors made one after the other are mostly in order.
+bool apart(std::vector<Span>& s) {
+  auto in_order = [&] {
+    for (size_t i = 1; i < s.size(); ++i)
+      if (s[i].lo < s[i - 1].hi) return false;
+    return true;
+  };
+  if (in_order()) return true;
+  std::sort(s.begin(), s.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  return in_order();
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -552,8 +578,10 @@ extern "C" moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int co
   const bool eight = state_bits == 8;
   std::vector<AdamTensor> all;
   all.reserve(count);
-  std::vector<const void*> seen;
-  seen.reserve(count);
+  bool clash = false;
+  // what is written: param, master, states and their scales
+  std::vector<Span> written[6];
+  for (auto& w : written) w.reserve(count);
   int masters = 0;
   for (int i = 0; i < count; ++i) {
     const moe_adamw_tensor_t& t = tensors[i];
@@ -572,12 +600,20 @@ extern "C" moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int co
     const double keep = 1.0 - lr * (double)t.weight_decay;
     all.push_back(AdamTensor{t.param, t.grad, t.master, t.exp_avg, t.exp_avg_sq, t.exp_avg_scale,
                              t.exp_avg_sq_scale, t.n, t.weight_decay, (float)keep});
-    seen.push_back(t.param);
+    const int64_t state = t.n * (eight ? 1 : 4), scales = eight ? (t.n + kAdamBlock - 1) / kAdamBlock * 4 : 0;
+    const Span own[7] = {span(t.param, t.n * psize),       span(t.master, t.n * 4),
+                         span(t.exp_avg, state),           span(t.exp_avg_sq, state),
+                         span(t.exp_avg_scale, scales),    span(t.exp_avg_sq_scale, scales),
+                         span(t.grad, t.n * gsize)};
+    clash |= !apart(own);
+    for (int k = 0; k < 6; ++k)
+      if (own[k].hi > own[k].lo) written[k].push_back(own[k]);
   }
   if (masters != 0 && masters != (int)all.size()) return MOE_ERR_UNSUPPORTED;
-  // a tensor given twice would be stepped by two CTAs at once
-  std::sort(seen.begin(), seen.end());
-  if (std::adjacent_find(seen.begin(), seen.end()) != seen.end()) return MOE_ERR_INVALID_ARG;
+  if (clash) return MOE_ERR_INVALID_ARG;
+  // a buffer given twice would be written by two CTAs at once
+  for (auto& w : written)
+    if (!apart(w)) return MOE_ERR_INVALID_ARG;
   AdamParams p{beta1, beta2, (float)beta1, (float)beta2, (float)(1.0 - beta1), (float)(1.0 - beta2),
                (float)eps, (float)lr, lr_dev, grad_scale, step, 0,
                eps < 1e-15};

@@ -518,6 +518,10 @@ PyObject* layer_norm(Args a) {
     same_or_apart(summed, "summed", x, "x");
     same_or_apart(summed, "summed", residual, "residual");
     apart(out, "out", summed, "summed");
+    for (const Tensor* v : {&w, &bias}) {  // read by every row
+      apart(out, "out", *v, v == &w ? "weight" : "bias");
+      apart(summed, "summed", *v, v == &w ? "weight" : "bias");
+    }
     return moe_layer_norm(x.data_ptr(), dtype_code(x, "x"), ld, ptr<void>(residual), ld_r,
                           ptr<void>(w), ptr<void>(bias), wt, T, H, kind, (float)eps, out_code,
                           out.data_ptr(), ptr<void>(summed), ptr<float>(mean), ptr<float>(rstd),
@@ -564,6 +568,8 @@ PyObject* layer_norm_backward(Args a) {
     same_or_apart(d_x, "d_x", d, "d_out");
     same_or_apart(d_x, "d_x", x, "x");
     same_or_apart(d_x, "d_x", d_sum, "d_sum");
+    apart(d_x, "d_x", w, "weight");
+    apart(d_w, "d_weight", w, "weight");
     if (!ws.defined() && (d_w.defined() || d_b.defined()))
       ws = make({(int64_t)moe_layer_norm_workspace_size(T, H)}, at::kByte, dev);
     return moe_layer_norm_backward(

@@ -15,7 +15,8 @@ import numpy as np
 import torch
 
 from . import binding as B
-from ._lib import (ACT_SWIGLU, NORM_LAYER, NORM_RMS, EPILOGUE_RAW, EPILOGUE_SWIGLU, PATH_AUTO, PATH_FLAG_WEIGHTS_EARLY, PATH_GEMV,
+from ._lib import (ACT_SWIGLU, EPILOGUE_RAW, EPILOGUE_SWIGLU, NORM_LAYER, NORM_RMS, PATH_AUTO,
+                   PATH_FLAG_WEIGHTS_EARLY, PATH_GEMV,
                    PATH_TC, SCORE_SIGMOID, SCORE_SOFTMAX, MoEError, path_k_range)
 
 FUSE_ENV = "MOE_GB300_FUSE_GATE_UP"
@@ -368,11 +369,11 @@ class MoELayer:
         list of (start, end) CUDA events around its launches ("shared" with a
         shared expert).  ``adapter_ids`` (int32 [T], negative: none) names each
         token's adapter."""
-        self._kept = dict(x=x) if self.keep_for_grad else None
+        self._kept = None
         res = self._routed(x, out, inv_temperature, events, adapter_ids)
-        if self._kept is not None:
-            self._kept["inv_temperature"] = (self.inv_temperature if inv_temperature is None
-                                             else float(inv_temperature))
+        if self.keep_for_grad:
+            self._kept = dict(x=x, inv_temperature=(
+                self.inv_temperature if inv_temperature is None else float(inv_temperature)))
         if self.shared is not None and x.shape[0] > 0:
             ev = _Timer(events, "shared")
             b = self.buffers(x.shape[0])

@@ -33,6 +33,8 @@ class AdamW:
             raise ValueError("state_bits must be 8 or 32")
         if not params:
             raise ValueError("no tensors to optimize")
+        if isinstance(weight_decay, dict) and not set(weight_decay) <= set(params):
+            raise ValueError(f"weight_decay names no tensor: {sorted(set(weight_decay) - set(params))}")
         self.lr, self.betas, self.eps, self.state_bits = lr, tuple(betas), float(eps), state_bits
         self._groups = []
         for dtype in (torch.float32, torch.bfloat16):

@@ -131,6 +131,46 @@ def test_adamw(moe):
     assert g((AdamWTensor * 1)(tensor(n=0)), 1, None, None, None) == 0
 
 
+def test_adamw_refuses_buffers_that_share_memory(moe):
+    from sparse_moe_expert_gb300._lib import AdamWTensor
+    f = moe.lib().moe_adamw_step
+    MB = 1 << 20
+    names = ["param", "grad", "master", "exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale"]
+    n = 1000
+    size = dict(param=2 * n, grad=2 * n, master=4 * n, exp_avg=n, exp_avg_sq=n, exp_avg_scale=16,
+                exp_avg_sq_scale=16)
+
+    def tensors(count=3):
+        return [dict({k: MB * (1 + i * 8 + j) for j, k in enumerate(names)}, n=n, weight_decay=0.0)
+                for i in range(count)]
+
+    def call(ts):  # bf16 params with masters, 8-bit states
+        arr = (AdamWTensor * len(ts))(*[AdamWTensor(**t) for t in ts])
+        return f(arr, len(ts), 1, 1, 8, 1e-3, None, 0.9, 0.99, 1e-8, None, vp(MB), None)
+    for k in names:  # within a tensor: by its last bytes, by its first
+        for other in names:
+            if other == k:
+                continue
+            ts = tensors()
+            ts[1][k] = ts[1][other] + (size[other] - 4)
+            assert call(ts) == 1, (k, other)
+    for k in names:
+        if k == "grad":  # only read
+            continue
+        for i, j in ((0, 2), (2, 0)):
+            ts = tensors()
+            ts[i][k] = ts[j][k] + (size[k] - 4)
+            assert call(ts) == 1, (k, i, j)
+            ts = tensors()
+            ts[i][k] = ts[j][k]
+            assert call(ts) == 1, (k, i, j)
+
+
+def test_optimizer_refuses_decay_of_unknown_names(moe):
+    with pytest.raises(ValueError):
+        moe.AdamW({"w": torch.zeros(4)}, weight_decay={"v": 0.1})
+
+
 def test_python_calls_refuse_tensors_of_the_host(moe):
     x, w = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(32, 64, dtype=torch.bfloat16)
     f = torch.zeros(4)
