@@ -29,7 +29,9 @@ namespace {
 //
 // 128 x BN tiles.  A cluster of `splits` CTAs takes a tile, each CTA a run of K;
 // the sums meet in shared memory and are added in rank order, each CTA a share
-// of the rows.
+// of the rows.  64 x 1536 -> 4096 with residual takes 6.5 us (2.0 for its bytes): the
+// launch, a TMA round trip, six blocks of k (0.14 us each), the joint and the store follow
+// each other.
 
 constexpr int kTileThreads = 256;
 constexpr int kTileM = 128;
