@@ -10,14 +10,15 @@
 // variance is summed from the centred values.  All sums are fp32 in an order
 // that the sizes fix.  A thread owns columns, and in the gradient it keeps
 // their d_w and d_b over all rows of its CTA; the CTAs' sums are joined by a
-// second kernel in the CTAs' order.
+// second kernel in the CTAs' order, those of a few rows by their cluster.
 //
 // Bound by the bytes where there are many rows, by launch and latency where there are
 // few.  Measured (device time, share of the copy rate): norm of 1 x 4096 bf16 with
 // residual 2.4 us; of 8192 x 4096 bf16 with weight and bias 27.3, .72; gradient of 64 x
-// 2048 fp32 5.5; of 16384 x 4096 bf16 with d_sum 100, .79.
+// 2048 fp32 6.5; of 16384 x 4096 bf16 with d_sum 100, .79.
 #include "async.cuh"
 #include "dense.cuh"
+#include "lora.cuh"
 
 namespace moe {
 namespace {
@@ -217,7 +218,7 @@ struct NormGradParams {
 // present one is summed.
 template <bool D_BF16, bool X_BF16, int NV, bool VEC>
 __global__ void __launch_bounds__(512) layer_norm_backward_kernel(NormGradParams p) {
-  extern __shared__ float join[];  // [2][H], where a CTA takes several rows
+  extern __shared__ __align__(16) float join[];  // [rows][2][H], where a CTA takes several rows
   __shared__ float part[2][2][32];
   pdl_wait();
   pdl_trigger();
@@ -283,31 +284,22 @@ __global__ void __launch_bounds__(512) layer_norm_backward_kernel(NormGradParams
   }
   if (!p.part) return;
   float* out = p.part + (int64_t)blockIdx.x * 2 * p.H;
-  if (blockDim.y > 1) {  // the warps' sums, one warp after the other
-    for (int w = 0; w < (int)blockDim.y; ++w) {
-      if ((int)threadIdx.y == w) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int col = column<VEC>(j, e);
-            if (col >= p.H) continue;
-            join[col] = w ? join[col] + dw[j][e] : dw[j][e];
-            join[p.H + col] = w ? join[p.H + col] + db[j][e] : db[j][e];
-          }
-      }
-      __syncthreads();
-    }
-    for (int i = threadIdx.y * 32 + threadIdx.x; i < 2 * p.H; i += 32 * blockDim.y) out[i] = join[i];
-    return;
-  }
+  const bool several = blockDim.y > 1;
+  float* mine = several ? join + (int64_t)threadIdx.y * 2 * p.H : out;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     RowVec<false, VEC> o;
     o.v.set(dw[j]);
-    o.store(out, 0, j, p.H);
+    o.store(mine, 0, j, p.H);
     o.v.set(db[j]);
-    o.store(out, p.H, j, p.H);
+    o.store(mine, p.H, j, p.H);
+  }
+  if (!several) return;
+  __syncthreads();
+  for (int i = threadIdx.y * 32 + threadIdx.x; i < 2 * p.H; i += 32 * blockDim.y) {
+    float s = join[i];
+    for (int w = 1; w < (int)blockDim.y; ++w) s += join[w * 2 * p.H + i];
+    out[i] = s;
   }
 }
 
@@ -658,6 +650,125 @@ __global__ void __launch_bounds__(kRingThreads, NV == 1 ? 2 : 1)
   }
 }
 
+// ---- the gradient of a few rows ----------------------------------------------------
+//
+// One launch: groups of threads take a row each, a vector of eight per thread, and the
+// CTAs of one cluster join their sums of d_w and d_b through shared memory, groups and
+// then CTAs in their order.
+constexpr int kFewThreads = 512;
+constexpr int kFewCtas = 16;
+// Rows a group takes, at most.  A call of one launch costs the host less than one of two,
+// while a cluster's joint and 16 SMs cost the device more the wider the rows (us on the
+// device and per call, this form and the others: 64 x 64 3.2, 6.3 and 3.2, 9.7; 64 x 2048
+// fp32, two rows per group, 6.5, 6.9 and 5.8, 9.9; 128 x 2048, four, 9.2, 9.5 and 6.2, 9.8).
+constexpr int kFewTurns = 2;
+
+template <bool D_BF16, bool X_BF16>
+__global__ void __launch_bounds__(kFewThreads, 1)
+    layer_norm_backward_few_kernel(NormGradParams p, int per, float* d_weight, float* d_bias) {
+  extern __shared__ __align__(16) float join[];  // [groups][2][H]
+  __shared__ float2 part[2][kFewThreads / 32];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int group = tid / per, groups = blockDim.x / per, member = tid - group * per;
+  const int col = member * 8, rank = blockIdx.x;
+  const bool on = col < p.H;
+  const float2 zero = make_float2(0.0f, 0.0f);
+  float2 dw[4], db[4], w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    dw[i] = db[i] = zero;
+    w[i] = both(1.0f);
+  }
+  Vec8<D_BF16> d;
+  Vec8<X_BF16> x, s;
+  float mu = 0.0f, rstd = 0.0f;
+  auto fetch = [&](int64_t t) {
+    if (on) {
+      d.load(p.d_out, t * p.ldd + col);
+      x.load(p.x, t * p.ldx + col);
+      if (p.d_sum) s.load(p.d_sum, t * p.lds + col);
+    } else {
+      d.zero();
+      x.zero();
+      s.zero();
+    }
+    if (p.mean) mu = p.mean[t];
+    rstd = p.rstd[t];
+  };
+  const int64_t step = (int64_t)kFewCtas * groups;
+  int64_t t = (int64_t)rank * groups + group;
+  if (t < p.T) fetch(t);
+  if (p.weight && on) load2(w, p.weight, p.w_bf16, col);
+  const float inv_h = 1.0f / (float)p.H;
+  for (int buf = 0; t < p.T; t += step, buf ^= 1) {  // alike for a group
+    const float r = rstd, shift = -mu * rstd;
+    float2 c[4], xh[4], g[4], s0 = zero, s1 = zero;
+    get2(c, d);
+    get2(xh, x);
+    if (p.d_sum) get2(g, s);
+    if (t + step < p.T) fetch(t + step);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      xh[i] = on ? ffma2(xh[i], both(r), both(shift)) : zero;
+      db[i] = add2(db[i], c[i]);
+      dw[i] = ffma2(c[i], xh[i], dw[i]);
+      c[i] = mul2(c[i], w[i]);
+      s0 = add2(s0, c[i]);
+      s1 = ffma2(c[i], xh[i], s1);
+    }
+    float sum[2] = {s0.x + s0.y, s1.x + s1.y};
+    warp_sum(sum);
+    if (per > 32) {
+      if (lane == 0) part[buf][warp] = make_float2(sum[0], sum[1]);
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(per) : "memory");
+      const float2 mine = lane < per / 32 ? part[buf][group * (per / 32) + lane] : zero;
+      sum[0] = mine.x;
+      sum[1] = mine.y;
+      warp_sum(sum);
+    }
+    const float2 m0 = both(p.mean ? -r * (sum[0] * inv_h) : 0.0f), m1 = both(-r * (sum[1] * inv_h));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = ffma2(c[i], both(r), ffma2(xh[i], m1, m0));
+      if (p.d_sum) c[i] = add2(c[i], g[i]);
+    }
+    Vec8<X_BF16> o;
+    set2(o, c);
+    if (on) o.store(p.d_x, t * p.H + col);
+  }
+  if (on) {
+    float* mine = join + group * 2 * p.H + col;
+    Vec8<false> o;
+    set2(o, dw);
+    o.store(mine, 0);
+    set2(o, db);
+    o.store(mine, p.H);
+  }
+  __syncthreads();
+  if (groups > 1) {  // into the first group's place
+    for (int i = tid; i < 2 * p.H; i += blockDim.x) {
+      float v = join[i];
+      for (int k = 1; k < groups; ++k) v += join[k * 2 * p.H + i];
+      join[i] = v;
+    }
+  }
+  cluster_barrier();
+  for (int i = rank * blockDim.x + tid; i < 2 * p.H; i += kFewCtas * blockDim.x) {
+    float* out = i < p.H ? d_weight : d_bias;
+    if (!out) continue;
+    float f[kFewCtas];
+#pragma unroll
+    for (int q = 0; q < kFewCtas; ++q)
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f[q]) : "r"(cluster_addr(join + i, q)));
+#pragma unroll
+    for (int q = 1; q < kFewCtas; ++q) f[0] += f[q];
+    out[i < p.H ? i : i - p.H] = f[0];
+  }
+  cluster_barrier();  // no CTA leaves while its sums are read
+}
+
 // ---- column sums ---------------------------------------------------------------
 
 constexpr int kColThreads = 1024;
@@ -741,7 +852,7 @@ moe_status_t launch_norm(const NormParams& p, const Shape& s, cudaStream_t st) {
 template <bool D_BF16, bool X_BF16, bool VEC>
 moe_status_t launch_norm_grad(const NormGradParams& p, const Shape& s, int grid, cudaStream_t st) {
   const dim3 block(s.threads, s.rows);
-  const size_t smem = s.rows > 1 ? (size_t)p.H * 8 : 0;
+  const size_t smem = s.rows > 1 ? (size_t)s.rows * p.H * 8 : 0;
   using moe_host::launch;
   if (s.nv == 1)
     return launch(layer_norm_backward_kernel<D_BF16, X_BF16, 1, VEC>, grid, block, smem, st, p);
@@ -776,6 +887,51 @@ moe_status_t norm_grad_ring(const NormGradParams& p, int& grid, cudaStream_t st)
   return r.nv == 1
              ? launch_ring<layer_norm_backward_ring_kernel<D_BF16, X_BF16, 1>>(p, r, weight, grid, st)
              : launch_ring<layer_norm_backward_ring_kernel<D_BF16, X_BF16, 2>>(p, r, weight, grid, st);
+}
+
+// Threads for a row of the form for few rows, and the rows that it takes, at most.
+int few_per(int H) { return (H / 8 + 31) / 32 * 32; }
+int few_most(int H) { return kFewTurns * kFewCtas * (kFewThreads / few_per(H)); }
+
+// Whether the device holds clusters of this size for the form for few rows.
+template <auto Kernel>
+bool few_fit() {
+  static std::atomic<int> known[moe_host::kMaxCachedDevices] = {};  // 1 yes, -1 no
+  std::atomic<int>& mine = known[moe_host::device_index()];
+  int n = mine.load(std::memory_order_relaxed);
+  if (n == 0) {
+    n = -1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kFewCtas);
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = kFewThreads * 8 * 8;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kFewCtas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&clusters, Kernel, &cfg) == cudaSuccess && clusters > 0)
+      n = 1;
+    cudaGetLastError();
+    mine.store(n, std::memory_order_relaxed);
+  }
+  return n > 0;
+}
+
+template <bool D_BF16, bool X_BF16>
+bool few_fit_as() {
+  return few_fit<layer_norm_backward_few_kernel<D_BF16, X_BF16>>();
+}
+
+template <bool D_BF16, bool X_BF16>
+moe_status_t norm_grad_few(const NormGradParams& p, float* d_weight, float* d_bias, cudaStream_t st) {
+  const int per = few_per(p.H), groups = kFewThreads / per;
+  return moe_host::launch_clusters(layer_norm_backward_few_kernel<D_BF16, X_BF16>, dim3(kFewCtas),
+                                   groups * per, (size_t)groups * p.H * 8, dim3(kFewCtas, 1, 1), st, p, per,
+                                   d_weight, d_bias);
 }
 
 template <bool X_BF16, bool OUT_BF16, int NV>
@@ -885,6 +1041,15 @@ extern "C" moe_status_t moe_layer_norm_backward(
                      vec_ok(d_sum, x_dtype, ld_sum) && vec_ok(d_x, x_dtype, H) &&
                      vec_ok(weight, weight_dtype, H);
     const bool db = d_dtype == MOE_DTYPE_BF16, xb = x_dtype == MOE_DTYPE_BF16;
+    if (sums && vec && H <= kFewThreads * 8 && T <= few_most(H)) {
+      const bool fits = db ? (xb ? few_fit_as<true, true>() : few_fit_as<true, false>())
+                           : (xb ? few_fit_as<false, true>() : few_fit_as<false, false>());
+      if (fits)
+        return db ? (xb ? norm_grad_few<true, true>(p, d_weight, d_bias, st)
+                        : norm_grad_few<true, false>(p, d_weight, d_bias, st))
+                  : (xb ? norm_grad_few<false, true>(p, d_weight, d_bias, st)
+                        : norm_grad_few<false, false>(p, d_weight, d_bias, st));
+    }
     const Shape run = norm_shape(H, vec ? 2 : 1);
     moe_status_t r;
     if (vec && run.rows == 1)

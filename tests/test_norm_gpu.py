@@ -251,3 +251,84 @@ def test_refusals():
     with pytest.raises(m.MoEError):
         m.moe_layer_norm_backward(o, x, rstd, mean, w,
                                   workspace=torch.empty(16, dtype=torch.uint8, device=dev()))
+
+
+@pytest.mark.parametrize("T,H", [(1, 8), (16, 8), (255, 64), (513, 64), (128, 264), (257, 512),
+                                 (33, 520), (127, 1024), (129, 1024), (32, 2048), (64, 2048),
+                                 (65, 2048), (31, 4096), (33, 4096)])
+@pytest.mark.parametrize("d_dtype,dtype", [(F32, F32), (B16, B16), (B16, F32)])
+def test_backward_around_the_form_for_few_rows(T, H, d_dtype, dtype):
+    """At most 4 rows of a group, 16 groups and 16 CTAs one after the other, or what the
+    other forms add: below the 256 u of the sums' tolerance."""
+    m = moe()
+    x, d, ds = make(T, H, dtype, 11), make(T, H, d_dtype, 12, pad=8), make(T, H, dtype, 13, pad=16)
+    for w in (vec(H, 14, centre=1.0), None):
+        for rms in (False, True):
+            k = m.NORM_RMS if rms else m.NORM_LAYER
+            _, _, mean, rstd = m.moe_layer_norm(x, w, eps=1e-5, kind=k, need_stats=True)
+            args = dict(mean=None if rms else mean, weight=w, d_sum=ds, kind=k)
+            d_x, d_w, d_b = m.moe_layer_norm_backward(d, x, rstd, **args)
+            xd = x.double().cpu()
+            mu = torch.zeros(T, 1, dtype=torch.float64) if rms else xd.mean(1, keepdim=True)
+            r = 1.0 / torch.sqrt(((xd - mu) ** 2).mean(1, keepdim=True) + 1e-5)
+            xh, dd = (xd - mu) * r, d.double().cpu()
+            c = dd if w is None else dd * w.double().cpu()
+            core = c - xh * (c * xh).mean(1, keepdim=True)
+            if not rms:
+                core = core - c.mean(1, keepdim=True)
+            want = r * core + ds.double().cpu()
+            size = r * (c.abs() + 1.0 * xh.abs() * (c * xh).abs().mean(1, keepdim=True)
+                        + c.abs().mean(1, keepdim=True)) + ds.double().cpu().abs()
+            close(d_x, want, TOL + (BF16 if dtype is B16 else 0.0), size)
+            close(d_w, (dd * xh).sum(0), SUM_TOL, (dd * xh).abs().sum(0))
+            close(d_b, dd.sum(0), SUM_TOL, dd.abs().sum(0))
+            # the same bits again, and each output alone
+            again = m.moe_layer_norm_backward(d, x, rstd, **args)
+            assert all(torch.equal(a, b) for a, b in zip(again, (d_x, d_w, d_b)))
+            only = m.moe_layer_norm_backward(d, x, rstd, need_d_weight=False, **args)
+            assert only[1] is None and torch.equal(only[2], d_b) and torch.equal(only[0], d_x)
+            only = m.moe_layer_norm_backward(d, x, rstd, need_d_bias=False, **args)
+            assert only[2] is None and torch.equal(only[1], d_w)
+
+
+@pytest.mark.parametrize("T,H", [(20, 64), (20, 2048), (20, 4096)])
+def test_few_rows_on_streams_at_once_and_captured(T, H):
+    """Calls on two streams and a replayed graph give the bits of a call alone."""
+    m = moe()
+    w = vec(H, 14, centre=1.0)
+    sets = [(make(T, H, B16, 20 + i), make(T, H, B16, 30 + i)) for i in range(4)]
+    rstd, mean = vec(T, 1, centre=1.0), vec(T, 2)
+    want = [m.moe_layer_norm_backward(d, x, rstd, mean, w) for x, d in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for i, (x, d) in enumerate(sets * 8):
+        got.append(m.moe_layer_norm_backward(d, x, rstd, mean, w, stream=streams[i % 2]))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, want[i % 4]))
+    x, d = sets[0][0].clone(), sets[0][1].clone()
+    m.moe_layer_norm_backward(d, x, rstd, mean, w)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = m.moe_layer_norm_backward(d, x, rstd, mean, w)
+    for i in (1, 3):
+        x.copy_(sets[i][0])
+        d.copy_(sets[i][1])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
+
+
+def test_outputs_over_the_weights_are_refused():
+    m = moe()
+    x, w = make(4, 64, F32, 1), vec(64, 2)
+    both = torch.zeros(5, 64, device=dev())
+    for call in (lambda: m.moe_layer_norm(x, both[0], out=both[:4]),
+                 lambda: m.moe_layer_norm(x, w, both[3], out=both[:4]),
+                 lambda: m.moe_layer_norm(x, both[2], residual=x.clone(), summed=both[:4]),
+                 lambda: m.moe_layer_norm_backward(x, x, w[:4], w[:4].clone(), both[1], d_x=both[:4]),
+                 lambda: m.moe_layer_norm_backward(x, x, w[:4], w[:4].clone(), both[1],
+                                                   d_weight=both[1])):
+        with pytest.raises(ValueError):
+            call()
