@@ -8,8 +8,8 @@
 // takes eight columns of every eighth row of its CTA's run of rows, the CTAs'
 // sums are joined in their order.  Without an activation d_out is d_z.  That pass
 // over 4096 rows with bias, us and share of the copy rate: SwiGLU of 11008 40, .83; SiLU
-// 62, .64; GELU 76, .52 (bound by the issue of its two functions; with two CTAs per SM
-// and expf 51, 86 and 134).
+// 61, .65; GELU 66, .60 (bound by the issue of the functions; with two CTAs per SM, expf
+// and erff 51, 86 and 134).
 #include "linear.cuh"
 
 namespace moe {
@@ -36,10 +36,12 @@ __device__ __forceinline__ float silu_slope(float z, float& value) {
   value = z * s;
   return s * fmaf(z, 1.0f - s, 1.0f);
 }
-// Phi(z) + z phi(z); 2^-23 off in absolute terms, which is what a factor of d_out needs.
-__device__ __forceinline__ float gelu_slope(float z) {
-  return fmaf(z * 0.39894228040143268f, __expf(-0.5f * z * z),
-              fmaf(0.5f, erff(z * 0.70710678118654752f), 0.5f));
+// Phi(z) + z phi(z) of two values.
+__device__ __forceinline__ float2 gelu_slope2(float2 z) {
+  float2 bell;
+  const float2 q = normal_tail2(z, bell);
+  return make_float2(fmaf(z.x * 0.39894228f, bell.x, z.x > 0.0f ? 1.0f - q.x : q.x),
+                     fmaf(z.y * 0.39894228f, bell.y, z.y > 0.0f ? 1.0f - q.y : q.y));
 }
 
 // KIND: no activation, SiLU or GELU, SwiGLU.
@@ -86,7 +88,11 @@ __global__ void __launch_bounds__(256, 4) linear_dz_kernel(DzParams p) {
           }
         } else if (p.act == MOE_ACT_GELU) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) d[0][i] *= gelu_slope(z[i]);
+          for (int i = 0; i < 8; i += 2) {
+            const float2 s = gelu_slope2(make_float2(z[i], z[i + 1]));
+            d[0][i] *= s.x;
+            d[0][i + 1] *= s.y;
+          }
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {

@@ -117,57 +117,68 @@ __device__ __forceinline__ PairTile pair_tile(const PairWork& w, int pair, int p
 
 // ---- the epilogue of rows of whole 16-byte pieces --------------------------------
 
-// Eight columns of the residual, asked for ahead.
-struct Residual8 {
-  uint4 q[2];
-  __device__ __forceinline__ void ask(const LinearEpi& e, int64_t row, int col, bool on) {
-    if (!on || row >= e.M) return;
+// The residual of a row's 32 columns, asked for ahead.
+struct Residual32 {
+  uint4 q[8];  // bf16: the first four
+  __device__ __forceinline__ void ask(const LinearEpi& e, int64_t row, int col, int n) {
+    if (row >= e.M) return;
     const int64_t at = row * e.cols + col;
-    if (e.out_bf16) {
-      q[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.residual) + at);
-    } else {
-      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(e.residual) + at);
-      q[0] = p[0];
-      q[1] = p[1];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (e.out_bf16) {
+        if (i < 4 && i * 8 < n)
+          q[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.residual) + at + i * 8);
+      } else if (i * 4 < n) {
+        q[i] = *reinterpret_cast<const uint4*>(static_cast<const float*>(e.residual) + at + i * 4);
+      }
     }
   }
 };
+
+// A warp's strip of 32 rows x 128 bytes in shared memory: piece p (16 bytes) of row r lies
+// at p ^ (r & 7), without bank conflicts.
+__device__ __forceinline__ unsigned char* strip_at(unsigned char* strip, int row, int piece) {
+  return strip + row * 128 + ((piece ^ (row & 7)) << 4);
+}
 
 __device__ __forceinline__ void store_bf16x8(uint16_t* p, const float* f) {
   *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
                                             pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
-// 32 columns of a row at once, of which `left` are there: what the call leaves out
-// costs a branch for all of them, not for eight (4096 x 4096 sums over 512: 24.6 us
-// in eights, 22.4; bf16 sums as they are have a loop of their own, 22.1; 777 x 4096 x
-// 1536, both gradients 23.6, 21.5, 21.0).
-template <bool SWIGLU>
-__device__ __forceinline__ void wide_finish(const LinearEpi& e, int64_t row, int col, int left,
-                                            const uint32_t (&r)[SWIGLU ? 4 : 2][16],
-                                            const Residual8 (&res)[4]) {
-  float z[32], u[SWIGLU ? 32 : 1];
+__device__ __forceinline__ void strip_hold(unsigned char* strip, const uint32_t (&r)[2][16]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    *reinterpret_cast<uint4*>(strip_at(strip, lane, q)) =
+        make_uint4(r[q >> 2][(q & 3) * 4], r[q >> 2][(q & 3) * 4 + 1], r[q >> 2][(q & 3) * 4 + 2],
+                   r[q >> 2][(q & 3) * 4 + 3]);
+}
+
+// SwiGLU's 32 columns of a row, of which `left` are there: a lane has both halves and
+// stores its row itself (4096 x 2048 x 1536 19.7 us, through the strip 20.3).
+__device__ __forceinline__ void gated_finish(const LinearEpi& e, int64_t row, int col, int left,
+                                             const uint32_t (&r)[4][16], const Residual32& res) {
+  float z[32], u[32];
 #pragma unroll
   for (int x = 0; x < 32; ++x) {
     z[x] = __uint_as_float(r[x >> 4][x & 15]);
-    if constexpr (SWIGLU) u[x] = __uint_as_float(r[2 + (x >> 4)][x & 15]);
+    u[x] = __uint_as_float(r[2 + (x >> 4)][x & 15]);
   }
   if (e.bias) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       if (4 * q >= left) continue;
       const float4 b = *reinterpret_cast<const float4*>(e.bias + col + 4 * q);
+      const float4 d = *reinterpret_cast<const float4*>(e.bias + e.cols + col + 4 * q);
       z[4 * q] += b.x;
       z[4 * q + 1] += b.y;
       z[4 * q + 2] += b.z;
       z[4 * q + 3] += b.w;
-      if constexpr (SWIGLU) {
-        const float4 d = *reinterpret_cast<const float4*>(e.bias + e.cols + col + 4 * q);
-        u[4 * q] += d.x;
-        u[4 * q + 1] += d.y;
-        u[4 * q + 2] += d.z;
-        u[4 * q + 3] += d.w;
-      }
+      u[4 * q] += d.x;
+      u[4 * q + 1] += d.y;
+      u[4 * q + 2] += d.z;
+      u[4 * q + 3] += d.w;
     }
   }
   if (e.preact) {
@@ -176,51 +187,158 @@ __device__ __forceinline__ void wide_finish(const LinearEpi& e, int64_t row, int
     for (int q = 0; q < 4; ++q) {
       if (8 * q >= left) continue;
       store_bf16x8(p + 8 * q, z + 8 * q);
-      if constexpr (SWIGLU) store_bf16x8(p + e.cols + 8 * q, u + 8 * q);
+      store_bf16x8(p + e.cols + 8 * q, u + 8 * q);
     }
   }
-  if constexpr (SWIGLU) {
 #pragma unroll
-    for (int x = 0; x < 32; ++x) z[x] = swiglu_f32(z[x], u[x]);
-  } else if (e.act == MOE_ACT_SILU) {
-#pragma unroll
-    for (int x = 0; x < 32; ++x) z[x] = silu_f32(z[x]);
-  } else if (e.act == MOE_ACT_GELU) {
-#pragma unroll
-    for (int x = 0; x < 32; ++x) z[x] = gelu_f32(z[x]);
-  }
-  const int64_t at = row * e.cols + col;
-  if (e.out_bf16) {
-    uint16_t* p = static_cast<uint16_t*>(e.out) + at;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (8 * q >= left) continue;
-      if (e.residual) {
-        const uint32_t w[4] = {res[q].q[0].x, res[q].q[0].y, res[q].q[0].z, res[q].q[0].w};
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float2 f = bf16x2_to_f32x2(w[x]);
-          z[8 * q + 2 * x] += f.x;
-          z[8 * q + 2 * x + 1] += f.y;
-        }
-      }
-      store_bf16x8(p + 8 * q, z + 8 * q);
-    }
-  } else {
-    float* p = static_cast<float*>(e.out) + at;
+  for (int x = 0; x < 32; ++x) z[x] = swiglu_f32(z[x], u[x]);
+  if (!e.out_bf16) {
+    float* p = static_cast<float*>(e.out) + row * e.cols + col;
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       if (4 * q >= left) continue;
       float4 f = make_float4(z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]);
       if (e.residual) {
-        const uint4 w = res[q >> 1].q[q & 1];
-        f.x += __uint_as_float(w.x);
-        f.y += __uint_as_float(w.y);
-        f.z += __uint_as_float(w.z);
-        f.w += __uint_as_float(w.w);
+        f.x += __uint_as_float(res.q[q].x);
+        f.y += __uint_as_float(res.q[q].y);
+        f.z += __uint_as_float(res.q[q].z);
+        f.w += __uint_as_float(res.q[q].w);
       }
       *reinterpret_cast<float4*>(p + 4 * q) = f;
     }
+    return;
+  }
+  uint16_t* p = static_cast<uint16_t*>(e.out) + row * e.cols + col;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (8 * q >= left) continue;
+    if (e.residual) {
+      const uint32_t w[4] = {res.q[q].x, res.q[q].y, res.q[q].z, res.q[q].w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float2 f = bf16x2_to_f32x2(w[x]);
+        z[8 * q + 2 * x] += f.x;
+        z[8 * q + 2 * x + 1] += f.y;
+      }
+    }
+    store_bf16x8(p + 8 * q, z + 8 * q);
+  }
+}
+
+// What four columns of a row are added to, asked for ahead: eight lanes take a row, a lane
+// the rows lane / 8 + 4 i, in two halves of four.
+struct StripAdd {
+  float4 bias;
+  uint4 residual[4];  // of the half to come; bf16: two words of each
+  // `n` columns and `rows` rows are there
+  __device__ __forceinline__ void ask_bias(const LinearEpi& e, int64_t col, int n) {
+    const int c = (threadIdx.x & 7) * 4;
+    bias = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (e.bias && c < n) bias = *reinterpret_cast<const float4*>(e.bias + col + c);
+  }
+  __device__ __forceinline__ void ask(int h, const LinearEpi& e, int64_t row0, int rows, int64_t col, int n) {
+    const int lane = threadIdx.x & 31, c = (lane & 7) * 4;
+    if (!e.residual || c >= n) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = (h * 4 + i) * 4 + (lane >> 3);
+      const int64_t at = (row0 + r) * e.cols + col + c;
+      if (r >= rows) continue;
+      if (e.out_bf16) {
+        const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(e.residual) + at);
+        residual[i].x = v.x;
+        residual[i].y = v.y;
+      } else {
+        residual[i] = *reinterpret_cast<const uint4*>(static_cast<const float*>(e.residual) + at);
+      }
+    }
+  }
+};
+
+// The sums of 32 rows x 32 columns in the warp's strip -> columns col .. col + n of the
+// outputs.  Rows leave as whole 64 or 128 bytes; four of them are read before the first is
+// stored, so that their chains run side by side.  Against lanes that finish and store their
+// own rows, 16 bytes at a time (us, 3001 x 4096 sums over 256, then d_w and both gradients
+// of 512 x 4096 x 4096 in fp32): bias 19.1, 17.6; GELU, bias and residual 46.6, 29.6; fp32
+// 22.2, 17.6; fp32 with residual 35.3, 30.3; SiLU 17.7, 21.8; d_w 35.1, 25.7; both 50.5,
+// 37.3 (with all eight rows at once, or their residuals, registers spill: 65, 91).
+template <int ACT, bool OUT_BF16>
+__device__ __forceinline__ void strip_rows(const LinearEpi& e, unsigned char* strip, int64_t row0, int rows,
+                                           int64_t col, int n, StripAdd& add) {
+  const int lane = threadIdx.x & 31, c = (lane & 7) * 4;
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    const uint4 present[4] = {add.residual[0], add.residual[1], add.residual[2], add.residual[3]};
+    if (h == 0) add.ask(1, e, row0, rows, col, n);
+    if (c >= n) continue;
+    float4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = *reinterpret_cast<const float4*>(strip_at(strip, (h * 4 + i) * 4 + (lane >> 3), lane & 7));
+    const int64_t first = row0 + h * 16 + (lane >> 3);
+    bool on[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) on[i] = h * 16 + i * 4 + (lane >> 3) < rows;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i].x += add.bias.x;
+      v[i].y += add.bias.y;
+      v[i].z += add.bias.z;
+      v[i].w += add.bias.w;
+    }
+    if (e.preact) {
+      uint16_t* p = e.preact + first * e.N + col + c;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (on[i])
+          *reinterpret_cast<uint2*>(p + i * 4 * (int64_t)e.N) =
+              make_uint2(pack_bf16x2(v[i].x, v[i].y), pack_bf16x2(v[i].z, v[i].w));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (ACT == MOE_ACT_SILU) {
+        v[i] = make_float4(silu_f32(v[i].x), silu_f32(v[i].y), silu_f32(v[i].z), silu_f32(v[i].w));
+      } else if constexpr (ACT == MOE_ACT_GELU) {
+        gelu2(v[i].x, v[i].y);
+        gelu2(v[i].z, v[i].w);
+      }
+    }
+    if (e.residual) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 q = present[i];
+        const float2 lo = OUT_BF16 ? bf16x2_to_f32x2(q.x) : make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+        const float2 hi = OUT_BF16 ? bf16x2_to_f32x2(q.y) : make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
+        v[i].x += lo.x;
+        v[i].y += lo.y;
+        v[i].z += hi.x;
+        v[i].w += hi.y;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!on[i]) continue;
+      const int64_t at = (first + i * 4) * e.cols + col + c;
+      if constexpr (OUT_BF16)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(e.out) + at) =
+            make_uint2(pack_bf16x2(v[i].x, v[i].y), pack_bf16x2(v[i].z, v[i].w));
+      else
+        *reinterpret_cast<float4*>(static_cast<float*>(e.out) + at) = v[i];
+    }
+  }
+}
+
+__device__ __forceinline__ void strip_wide(const LinearEpi& e, unsigned char* strip, int64_t row0, int rows,
+                                           int64_t col, int n, StripAdd& add) {
+  if (e.act == MOE_ACT_GELU) {
+    if (e.out_bf16) strip_rows<MOE_ACT_GELU, true>(e, strip, row0, rows, col, n, add);
+    else strip_rows<MOE_ACT_GELU, false>(e, strip, row0, rows, col, n, add);
+  } else if (e.act == MOE_ACT_SILU) {
+    if (e.out_bf16) strip_rows<MOE_ACT_SILU, true>(e, strip, row0, rows, col, n, add);
+    else strip_rows<MOE_ACT_SILU, false>(e, strip, row0, rows, col, n, add);
+  } else {
+    if (e.out_bf16) strip_rows<MOE_ACT_NONE, true>(e, strip, row0, rows, col, n, add);
+    else strip_rows<MOE_ACT_NONE, false>(e, strip, row0, rows, col, n, add);
   }
 }
 
@@ -230,12 +348,7 @@ __device__ __forceinline__ void wide_finish(const LinearEpi& e, int64_t row, int
 // itself; else single values would go to as many lines as there are lanes, so a
 // strip of 32 rows x 128 bytes goes through shared memory and neighbouring lanes
 // take neighbouring columns (335 x 408 x 3468, us: 20.0 without, 12.3; where pieces
-// are whole the detour costs: 4096 x 2048 x 1536 SwiGLU 19.7 without, 20.3).  Piece
-// p (16 bytes) of row r lies at p ^ (r & 7), without bank conflicts.
-
-__device__ __forceinline__ unsigned char* strip_at(unsigned char* strip, int row, int piece) {
-  return strip + row * 128 + ((piece ^ (row & 7)) << 4);
-}
+// of bf16 are whole the detour costs: 4096 x 2048 x 1536 SwiGLU 19.7 without, 20.3).
 
 // The strip -> `n` columns at `col` of the warp's rows (of which `rows` are there)
 // of a matrix with rows of `ld` elements, plus what `residual` has there.  By the
@@ -308,7 +421,7 @@ __device__ __forceinline__ void strip_finish(const LinearEpi& e, unsigned char* 
       for (int x = 0; x < 16; ++x) z[x] = silu_f32(z[x]);
     } else if (e.act == MOE_ACT_GELU) {
 #pragma unroll
-      for (int x = 0; x < 16; ++x) z[x] = gelu_f32(z[x]);
+      for (int x = 0; x < 16; x += 2) gelu2(z[x], z[x + 1]);
     }
     hold(c, z);
   }
@@ -486,6 +599,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         __syncwarp();
         if (lane == 0) remote_arrive(cluster_addr(&sums_empty[buf], 0));
       };
+      const int64_t below = e.M - (row - lane);
+      const int rows = below >= 32 ? 32 : below > 0 ? (int)below : 0;  // of this warp that are there
       const bool plain = !SWIGLU && e.out_bf16 && e.act == MOE_ACT_NONE && !e.bias && !e.residual && !e.preact;
       if (plain && e.vec) {
         uint16_t* out = static_cast<uint16_t*>(e.out) + row * e.cols + at.n * span;
@@ -516,10 +631,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         bool left = false;
 #pragma unroll 1
         for (int c = half * 32; c < span; c += 64) {
-          Residual8 res[4];
-          if (e.residual) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) res[q].ask(e, row, at.n * span + c + q * 8, c + q * 8 < width);
+          Residual32 res;
+          StripAdd add;
+          if constexpr (SWIGLU) {
+            if (e.residual) res.ask(e, row, at.n * span + c, width - c);
+          } else {
+            add.ask_bias(e, at.n * span + c, width - c);
+            add.ask(0, e, row - lane, rows, at.n * span + c, width - c);
           }
           uint32_t r[SWIGLU ? 4 : 2][16];
           tmem_ld16(base + c, r[0]);
@@ -533,12 +651,18 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             done();
             left = true;
           }
-          if (row < e.M) wide_finish<SWIGLU>(e, row, at.n * span + c, width - c, r, res);
+          if constexpr (SWIGLU) {
+            if (lane < rows) gated_finish(e, row, at.n * span + c, width - c, r, res);
+          } else {
+            strip_hold(strip, r);
+            __syncwarp();
+            strip_wide(e, strip, row - lane, rows, at.n * span + c, width - c, add);
+            __syncwarp();
+          }
         }
         if (!left) done();  // no columns of this tile for this warp
       } else {
         const int64_t row0 = row - lane;
-        const int rows = (int)(e.M - row0 < 32 ? (e.M > row0 ? e.M - row0 : 0) : 32);
         const int width = min(span, e.cols - at.n * span);  // columns that are there
         bool left = false;
         for (int c = half * 32; c < width; c += 64) {

@@ -297,3 +297,46 @@ def test_refusals():
             m.moe_linear_backward(*args, **kw)
     with pytest.raises(m.MoEError):
         m.moe_linear_backward(d, x, w, workspace=torch.empty(16, dtype=torch.uint8, device=dev()))
+
+
+@pytest.mark.parametrize("T,N", [(12, 24), (100, 64), (300, 4096), (300, 1001)])
+def test_gelu_keeps_its_digits_in_the_tail(T, N):
+    """z is exact (one product by one).  The tail is 1.2e-6 of itself off, e^(-z^2/2) z^2 2^-23
+    and 2 ulp, so 1.2e-5 at |z| = 9; the slope's terms as much of themselves, below 1e-6 in
+    all, and a rounding to bf16."""
+    m = moe()
+    z = torch.linspace(-9.0, 9.0, T).to(B16)
+    x = torch.zeros(T, 8, dtype=B16)
+    x[:, 0] = z
+    w = torch.zeros(N, 8, dtype=B16)
+    w[:, 0] = 1.0
+    x, w = x.to(dev()), w.to(dev())
+    out, pre = m.moe_linear(x, w, activation=m.ACT_GELU, out_dtype=F32, need_preact=True)
+    zd = z.double()
+    tail = 0.5 * torch.special.erfc(-zd / math.sqrt(2.0))
+    want = (zd * tail)[:, None].expand(T, N)
+    got = out.double().cpu()
+    assert float(((got - want).abs() - 1.2e-5 * want.abs()).max()) <= 1e-30
+    assert torch.equal(pre.cpu(), z[:, None].expand(T, N))
+    d = torch.ones(T, N, dtype=B16, device=dev())
+    dz = m.moe_linear_backward(d, x, w, pre, activation=m.ACT_GELU, need_d_x=False, need_d_w=False)[3]
+    slope = tail + zd * torch.exp(-0.5 * zd * zd) / math.sqrt(2.0 * math.pi)
+    err = (dz.double().cpu() - slope[:, None]).abs()
+    assert float((err - BF16 * slope.abs()[:, None]).max()) <= 1e-6
+
+
+def test_gelu_of_values_that_are_not_ordinary():
+    m = moe()
+    z = torch.tensor([float("inf"), 1e38, 1e20, 14.0, 0.0, -14.0, -1e20, -1e38, float("nan")], dtype=B16)
+    for T, N in ((9, 16), (9 * 20, 512)):
+        x = torch.zeros(T, 8, dtype=B16)
+        x[:, 0] = z.repeat(T // 9)
+        w = torch.zeros(N, 8, dtype=B16)
+        w[:, 0] = 1.0
+        out = m.moe_linear(x.to(dev()), w.to(dev()), activation=m.ACT_GELU, out_dtype=F32)[0].cpu()
+        # the other seven products of a sum are 0 x 0
+        for i in range(4):
+            assert torch.equal(out[i::9], x[i::9, :1].float().expand(T // 9, N)), i
+        assert float(out[4::9].abs().max()) == 0.0
+        assert float(out[5::9].abs().max()) < 1e-37 and float(out[6::9].abs().max()) == 0.0
+        assert float(out[7::9].abs().max()) == 0.0 and bool(torch.isnan(out[8::9]).all())
