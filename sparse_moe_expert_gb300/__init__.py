@@ -5,7 +5,8 @@ include/moe_gb300.h).  This package is its binding: ``binding`` has one
 function per C entry point and ``MoELayer`` composes them.  Importing it
 does not build anything; calling into it without the built library raises.
 """
-from ._lib import (ACT_GELU, ACT_NONE, ACT_SILU, ACT_SWIGLU, ADAMW_BLOCK, NORM_LAYER, NORM_RMS, DEVERR_BAD_ADAPTER, DEVERR_BAD_EXPERT, DEVERR_BAD_INDEX, DEVERR_BAD_SCORE,
+from ._lib import (ACT_GELU, ACT_NONE, ACT_SILU, ACT_SWIGLU, ADAMW_BLOCK, NORM_LAYER, NORM_RMS,
+                   DEVERR_BAD_ADAPTER, DEVERR_BAD_EXPERT, DEVERR_BAD_INDEX, DEVERR_BAD_SCORE,
                    DEVERR_TIMEOUT, DROPPED, DTYPE_BF16, DTYPE_F32, SCORE_SIGMOID, SCORE_SOFTMAX,
                    EPILOGUE_RAW, EPILOGUE_SWIGLU, EXPORTS, PATH_AUTO, PATH_FLAG_K_GATED,
                    PATH_FLAG_WEIGHTS_EARLY, PATH_GEMV, PATH_TC, path_k_range,
@@ -13,7 +14,8 @@ from ._lib import (ACT_GELU, ACT_NONE, ACT_SILU, ACT_SWIGLU, ADAMW_BLOCK, NORM_L
                    lib, lib_path)
 from .binding import (moe_abi_version, moe_adamw_step, moe_adamw_values, moe_layer_norm,
                       moe_layer_norm_backward, moe_layer_norm_workspace_size, moe_linear,
-                      moe_linear_backward, moe_linear_backward_workspace_size, moe_combine, moe_combine_backward, moe_down_qmm, moe_expert_counts_accumulate,
+                      moe_linear_backward, moe_linear_backward_workspace_size, moe_combine,
+                      moe_combine_backward, moe_down_qmm, moe_expert_counts_accumulate,
                       moe_expert_health, moe_gate_up_qmm,
                       moe_get_device_error, moe_pack_gate_up, moe_permute, moe_permute_capped,
                       moe_lora_apply, moe_lora_workspace_size, moe_permute_masked,
@@ -41,6 +43,6 @@ __all__ = [
     "moe_lora_apply", "moe_lora_workspace_size",
     "NORM_LAYER", "NORM_RMS", "ADAMW_BLOCK", "moe_layer_norm", "moe_layer_norm_backward",
     "moe_layer_norm_workspace_size", "moe_adamw_step", "moe_adamw_values",
-    "AdamW", "Norm", "SharedExpert", "ACT_NONE", "ACT_SILU", "ACT_GELU", "ACT_SWIGLU", "moe_linear", "moe_linear_backward",
-    "moe_linear_backward_workspace_size",
+    "AdamW", "Norm", "SharedExpert", "ACT_NONE", "ACT_SILU", "ACT_GELU", "ACT_SWIGLU", "moe_linear",
+    "moe_linear_backward", "moe_linear_backward_workspace_size",
 ]

@@ -14,7 +14,7 @@
 //
 // Bound by the bytes where there are many rows, by launch and latency where there are
 // few.  Measured (device time, share of the copy rate): norm of 1 x 4096 bf16 with
-// residual 2.4 us; of 8192 x 4096 bf16 with weight and bias 27.3, .72; gradient of 64 x
+// residual 2.4 us; of 8192 x 4096 bf16 with weight and bias 26.6, .74; gradient of 64 x
 // 2048 fp32 6.5; of 16384 x 4096 bf16 with d_sum 100, .79.
 #include "async.cuh"
 #include "dense.cuh"
@@ -345,7 +345,7 @@ __device__ __forceinline__ void load2(float2 (&f)[4], const void* p, int bf16, i
 // warp waits for another; a bulk copy brings its next row into shared memory
 // meanwhile.  Weight and bias lie there as fp32, [H] each, in front of the rows: from
 // global memory they would not stay in the L1 that is left.  One CTA per SM, its
-// warps as many as registers and shared memory allow.  8192 x 4096 bf16, us: 27 (a CTA
+// warps as many as registers and shared memory allow.  8192 x 4096 bf16, us: 26.6 (a CTA
 // per row 37, rows in shared memory read three times 40, weights through L1 43 to 56).
 // Dynamic shared memory of a CTA, at most, and of one of `n` per SM (which has 228 KB
 // and keeps 1 KB for each).
@@ -940,7 +940,12 @@ moe_status_t launch_norm_warps(const NormParams& p, cudaStream_t st) {
   const int row_bytes = p.H * (X_BF16 ? 2 : 4) * (p.residual ? 2 : 1);
   const int params = ((p.weight ? 1 : 0) + (p.bias ? 1 : 0)) * p.H * 4;
   const int room = ((int)kNormRoom - params) / row_bytes, most = warp_rows_most(X_BF16, NV);
-  const int warps = room < most ? room : most;
+  int warps = room < most ? room : most;
+  // Warps that all have rows in the last turn too (us, as many as there is room for and
+  // these: 4096 x 4096 fp32 31.7, 26.0; 3001 x 4096 bf16 14.1, 12.7; 8192 27.2, 26.6; 4096
+  // 15.9, 16.4).  A single turn's spare warps help to load weight and bias.
+  const int64_t sms = moe_host::sm_count(), turns = (p.T + sms * warps - 1) / (sms * warps);
+  if (turns > 1) warps = (int)((p.T + sms * turns - 1) / (sms * turns));
   if (const moe_status_t s = moe_host::allow_smem<kern>(kNormRoom)) return s;
   return moe_host::launch(kern, dim3(moe_host::sm_count()), dim3(warps * 32),
                           (size_t)params + (size_t)warps * row_bytes, st, p, row_bytes, moe_host::device_error_word());
