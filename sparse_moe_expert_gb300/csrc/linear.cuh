@@ -197,6 +197,10 @@ float linear_pairs_both_us(const LinearEpi (&e)[2], const int (&K)[2]);
 constexpr int kLinearRowsMost = 32;
 moe_status_t linear_rows(const uint16_t* x, int64_t ldx, const uint16_t* w, int K,
                          const LinearEpi& e, cudaStream_t st);
+// d_w = d_z^T x (+ d_w) of a few rows, where this serves the sizes.
+bool linear_few_serves(int tokens, int N, int K);
+moe_status_t linear_few_dw(const uint16_t* dz, int64_t ld, const uint16_t* x, int64_t ldx, int tokens, int N,
+                           int K, bool add, bool bf16, void* d_w, cudaStream_t st);
 // Which of the forms serves the call.
 moe_status_t linear_product(const LinearOp& a, const LinearOp& b, int K, LinearEpi e, cudaStream_t st);
 // The same for two products with B by columns.

@@ -222,6 +222,12 @@ extern "C" moe_status_t moe_linear_backward(const void* d_out, int d_dtype, int6
   }
   const uint16_t* dz = direct ? static_cast<const uint16_t*>(d_out) : d_preact;
   const int64_t ld = direct ? ld_d : ld_dp;
+  if (d_w && linear_few_serves(T, N, K)) {
+    if (const moe_status_t s = linear_few_dw(dz, ld, x, ld_x, T, N, K, accumulate != 0,
+                                             d_w_dtype == MOE_DTYPE_BF16, d_w, st))
+      return s;
+    d_w = nullptr;
+  }
   const LinearEpi ex{nullptr, nullptr, d_x, nullptr, T, K, K, MOE_ACT_NONE, 1, 0};
   const LinearEpi ew{nullptr, accumulate ? d_w : nullptr, d_w, nullptr, N, K, K, MOE_ACT_NONE,
                      d_w_dtype == MOE_DTYPE_BF16, 0};

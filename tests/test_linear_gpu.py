@@ -340,3 +340,32 @@ def test_gelu_of_values_that_are_not_ordinary():
         assert float(out[4::9].abs().max()) == 0.0
         assert float(out[5::9].abs().max()) < 1e-37 and float(out[6::9].abs().max()) == 0.0
         assert float(out[7::9].abs().max()) == 0.0 and bool(torch.isnan(out[8::9]).all())
+
+
+@pytest.mark.parametrize("T,K,N", [(1, 8, 1), (1, 216, 4770), (2, 264, 77), (3, 2048, 1536), (4, 1032, 999),
+                                   (5, 4096, 2048), (8, 2056, 4097), (9, 2056, 4097), (7, 2048, 1536)])
+def test_d_w_of_a_few_rows(T, K, N):
+    """At most 9 products summed: 9 u of their magnitudes, below TOL; the same bits again;
+    rows of x and d_out of any stride; values that are not finite stay in their columns."""
+    m = moe()
+    g = torch.Generator().manual_seed(T * 7 + K)
+    x = torch.randn(T, K + 24, generator=g).to(B16).to(dev())[:, :K]
+    w = torch.randn(N, K, generator=g).to(B16).to(dev())
+    d = torch.randn(T, N + 5, generator=g).to(B16).to(dev())[:, :N]
+    want = d.double().t() @ x.double()
+    size = float((d.double().abs().t() @ x.double().abs()).norm())
+    for dt, tol in ((F32, TOL), (B16, TOL + BF16)):
+        _, dw, db, _ = m.moe_linear_backward(d, x, w, d_w_dtype=dt)
+        assert dw.dtype == dt and float((dw.double() - want).norm()) <= tol * size
+        again = m.moe_linear_backward(d, x, w, d_w_dtype=dt, need_d_x=False)[1]
+        assert torch.equal(again, dw)
+        start = torch.randn(N, K, generator=g).to(dt).to(dev())
+        more = start.clone()
+        m.moe_linear_backward(d, x, None, d_w=more, accumulate=True, need_d_x=False, need_d_bias=False)
+        close(more, want + start.double(), tol * max(1.0, size / float((want + start.double()).norm())),
+              "accumulated")
+    x2, d2 = x.clone(), d.clone()
+    x2[0, K - 1], d2[T - 1, 0] = float("inf"), float("nan")
+    dw = m.moe_linear_backward(d2, x2, None, need_d_x=False, need_d_bias=False)[1]
+    assert bool(torch.isnan(dw[0]).all())
+    assert bool(torch.isfinite(dw[1:, :K - 1]).all()) and not bool(torch.isfinite(dw[:, K - 1]).any())
