@@ -134,8 +134,8 @@ class MoELayer:
     they need the fused gate_up matrix.  ``shared`` (SharedExpert) is added to
     the routed experts' sum.  ``norm`` and ``out_norm`` (Norm) stand in front of
     and behind the layer in block().  With ``keep_for_grad`` a forward keeps what
-    grads() needs (the input, which must not change until then, and the shared
-    expert's pre-activations).
+    grads() needs (the input, which must not change until then and may not be the
+    memory of the result, and the shared expert's pre-activations).
     """
     scoring: Optional[ScoredRouting] = None
     adapters: Optional[ExpertAdapters] = None
@@ -364,22 +364,31 @@ class MoELayer:
                 inv_temperature: Optional[float] = None, events: Optional[dict] = None,
                 adapter_ids: Optional[torch.Tensor] = None) -> torch.Tensor:
         """x: bf16 [T, H] on the device.  Returns bf16 [T, H] (a reused buffer
-        unless ``out`` is given).  ``events``, if given, receives per kernel
-        ("router", "permute", "permute_rows", "gate_up", "down", "combine") a
-        list of (start, end) CUDA events around its launches ("shared" with a
-        shared expert).  ``adapter_ids`` (int32 [T], negative: none) names each
+        unless ``out`` is given); x may be the result's memory.  ``events``, if
+        given, receives per kernel ("router", "permute", "permute_rows", "gate_up",
+        "down", "combine") a list of (start, end) CUDA events around its launches
+        ("shared" with a shared expert, once for each product).  ``adapter_ids`` (int32 [T], negative: none) names each
         token's adapter."""
         self._kept = None
-        res = self._routed(x, out, inv_temperature, events, adapter_ids)
+        if self.shared is None and not self.keep_for_grad:
+            return self._routed(x, out, inv_temperature, events, adapter_ids)
+        T = x.shape[0]
+        shared, b = self.shared if T > 0 else None, self.buffers(T)
+        res = out if out is not None else b["out"]
+        if self.keep_for_grad and (shared is not None or self.scoring is not None) and _overlap(x, res):
+            raise ValueError("keep_for_grad needs an input apart from the result: grads() reads it again")
+        if shared is not None:  # x may be the result's memory, which the routed experts write
+            ev = _Timer(events, "shared")
+            B.moe_linear(x, shared.gate_up, activation=ACT_SWIGLU, out=b["shared_h"],
+                         preact=b["shared_z"] if self.keep_for_grad else None)
+            ev.stop()
+        self._routed(x, res, inv_temperature, events, adapter_ids)
         if self.keep_for_grad:
             self._kept = dict(x=x, inv_temperature=(
                 self.inv_temperature if inv_temperature is None else float(inv_temperature)))
-        if self.shared is not None and x.shape[0] > 0:
+        if shared is not None:
             ev = _Timer(events, "shared")
-            b = self.buffers(x.shape[0])
-            B.moe_linear(x, self.shared.gate_up, activation=ACT_SWIGLU, out=b["shared_h"],
-                         preact=b["shared_z"] if self.keep_for_grad else None)
-            B.moe_linear(b["shared_h"], self.shared.down, residual=res, out=res)
+            B.moe_linear(b["shared_h"], shared.down, residual=res, out=res)
             ev.stop()
         return res
 
@@ -653,6 +662,18 @@ class MoELayer:
         res = self.forward(b["x_dev"], inv_temperature=inv_temperature, adapter_ids=adapter_ids)
         out_host.copy_(res, non_blocking=True)
         return out_host
+
+
+def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether the memory between the first and last elements of a and b meets."""
+    if a.numel() == 0 or b.numel() == 0:
+        return False
+
+    def span(t):
+        last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+        return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+    (a0, a1), (b0, b1) = span(a), span(b)
+    return a0 < b1 and b0 < a1
 
 
 class _Timer:

@@ -1,0 +1,51 @@
+"""The layer and its block where the input is the memory of the result: the layer's
+own reused buffer given back to it, or out=x."""
+import pytest
+import torch
+
+from _parity import dev
+from test_block_gpu import make, rand
+
+pytestmark = pytest.mark.gpu
+
+
+def test_shared_expert_reads_the_input_before_the_result_is_written():
+    for T in (1, 7, 300):
+        layer, _ = make(T=T)
+        x = rand((T, 256), 7, 0.5)
+        apart = [torch.empty_like(x), torch.empty_like(x)]
+        layer(x, out=apart[0])
+        layer(apart[0], out=apart[1])
+        y = layer(x)
+        assert torch.equal(y, apart[0])
+        again = layer(y)  # the buffer that the call before returned
+        assert again.data_ptr() == y.data_ptr() and torch.equal(again, apart[1])
+        both = x.clone()
+        assert layer(both, out=both) is both and torch.equal(both, apart[0])
+
+
+def test_blocks_without_norms_take_the_buffer_of_their_result():
+    layer, _ = make(out_norm=False)
+    layer.norm = None
+    x = rand((48, 256), 7, 0.5)
+    first = layer.block(x)[0].clone()
+    second = layer.block(first, out=torch.empty_like(x))[0]
+    y, _ = layer.block(x)
+    assert torch.equal(layer.block(y)[0], second)
+
+
+def test_gradients_need_an_input_apart_from_the_result():
+    layer, x = make(out_norm=False)
+    layer.keep_for_grad = True
+    d = rand(x.shape, 3, 0.1)
+    y = layer(x)
+    want = {n: t.clone() for n, t in layer.grads(d)[0].items()}
+    for call in (lambda: layer(y), lambda: layer(x, out=x), lambda: layer(x[1:], out=x[:-1])):
+        with pytest.raises(ValueError):  # grads() would read the result in the input's place
+            call()
+        with pytest.raises(ValueError):
+            layer.grads(d)
+    layer(x)
+    assert all(torch.equal(t, want[n]) for n, t in layer.grads(d)[0].items())
+    layer.keep_for_grad = False
+    layer(x, out=x)  # nothing reads it again
