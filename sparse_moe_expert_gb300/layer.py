@@ -397,25 +397,28 @@ class MoELayer:
         """The layer with its norms, as a block of a model: with s = x + residual
         (x without one), out_norm(layer(norm(s))) -> (out, s), both bf16 [T, H] and
         buffers that the next call of T tokens writes again unless ``out`` is
-        given (s is x itself without a residual).  The next block takes them as x and
-        residual, so the sum is part of its norm's kernel; out + s ends the last."""
+        given (s is x itself without a residual, or a copy where x is the result's
+        memory).  The next block takes them as x and residual, so the sum is part of
+        its norm's kernel; out + s ends the last."""
         if residual is not None and self.norm is None:
             raise ValueError("a residual needs a layer with a norm, whose kernel adds it")
-        T = x.shape[0]
-        b, s, h = self.buffers(T), x, x
+        b = self.buffers(x.shape[0])
+        res = out if out is not None else b["out" if self.out_norm is None else "block_out"]
+        if residual is not None and _overlap(b["summed"], res):
+            raise ValueError("out is the memory of the sum that is returned beside it")
+        s, h = x.clone() if residual is None and _overlap(x, res) else x, x
         if self.norm is not None:
             n = self.norm
-            h, s, _, _ = B.moe_layer_norm(
+            h, summed, _, _ = B.moe_layer_norm(
                 x, n.weight, n.bias, residual=residual, eps=n.eps, kind=n.kind, out=b["normed"],
                 summed=None if residual is None else b["summed"])
-            s = x if residual is None else s
+            s = s if residual is None else summed
         y = self.forward(h, out=out if self.out_norm is None else None, **forward_args)
         if self.out_norm is None:
             return y, s
         n = self.out_norm
-        res, _, mean, rstd = B.moe_layer_norm(
-            y, n.weight, n.bias, eps=n.eps, kind=n.kind, need_stats=self.keep_for_grad,
-            out=out if out is not None else b["block_out"])
+        _, _, mean, rstd = B.moe_layer_norm(y, n.weight, n.bias, eps=n.eps, kind=n.kind,
+                                            need_stats=self.keep_for_grad, out=res)
         if self._kept is not None:
             self._kept.update(y=y, mean=mean, rstd=rstd)
         return res, s

@@ -49,3 +49,30 @@ def test_gradients_need_an_input_apart_from_the_result():
     assert all(torch.equal(t, want[n]) for n, t in layer.grads(d)[0].items())
     layer.keep_for_grad = False
     layer(x, out=x)  # nothing reads it again
+
+
+def test_the_sum_of_a_block_is_not_its_result():
+    for kw in (dict(), dict(out_norm=False)):
+        layer, x = make(**kw)
+        first, s = layer.block(x)
+        assert s is x
+        first = first.clone()
+        second = layer.block(first)[0].clone()
+        both = x.clone()
+        y, s = layer.block(both, out=both)
+        assert y is both and torch.equal(y, first) and torch.equal(s, x)
+        y, _ = layer.block(x)
+        y, s = layer.block(y)  # its own buffer once more
+        assert torch.equal(y, second) and torch.equal(s, first)
+        third, total = layer.block(x, residual=first)
+        third, total = third.clone(), total.clone()
+        _, mine = layer.block(x, residual=first)
+        with pytest.raises(ValueError):
+            layer.block(x, residual=first, out=mine)
+        other = torch.empty_like(x)
+        y, mine = layer.block(x, residual=first, out=other)
+        assert torch.equal(y, third) and torch.equal(mine, total)
+        # the sum may take the place of the one before
+        y, again = layer.block(x, residual=mine)
+        assert again.data_ptr() == mine.data_ptr()
+        assert torch.equal(again, (x.float() + total.float()).to(torch.bfloat16))
