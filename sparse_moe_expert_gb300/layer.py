@@ -406,6 +406,10 @@ class MoELayer:
         res = out if out is not None else b["out" if self.out_norm is None else "block_out"]
         if residual is not None and _overlap(b["summed"], res):
             raise ValueError("out is the memory of the sum that is returned beside it")
+        kept = [x] if self.norm is None and (self.shared or self.scoring) else []
+        if self.keep_for_grad and self.out_norm is not None and any(
+                _overlap(t, res) for t in kept + [b["out"]]):
+            raise ValueError("out is the memory of what grads() reads again")
         s, h = x.clone() if residual is None and _overlap(x, res) else x, x
         if self.norm is not None:
             n = self.norm

@@ -76,3 +76,26 @@ def test_the_sum_of_a_block_is_not_its_result():
         y, again = layer.block(x, residual=mine)
         assert again.data_ptr() == mine.data_ptr()
         assert torch.equal(again, (x.float() + total.float()).to(torch.bfloat16))
+
+
+def test_the_result_of_a_block_is_not_written_over_what_its_gradients_read():
+    layer, x = make()
+    d = rand(x.shape, 3, 0.1)
+    y = layer(x)  # the rows that block() keeps for out_norm's gradient are this buffer
+    layer.keep_for_grad = True
+    layer.block(x)
+    want = {n: t.clone() for n, t in layer.grads(d)[0].items()}
+    with pytest.raises(ValueError):
+        layer.block(x, out=y)
+    same = x.clone()
+    layer.block(same, out=same)  # the norm in front keeps rows of its own
+    assert all(torch.equal(t, want[n]) for n, t in layer.grads(d)[0].items())
+    layer.norm = None
+    with pytest.raises(ValueError):
+        layer.block(same, out=same)
+    result, _ = layer.block(x)
+    with pytest.raises(ValueError):
+        layer.block(result)
+    layer.keep_for_grad = False
+    layer.block(x, out=y)
+    layer.block(result)
