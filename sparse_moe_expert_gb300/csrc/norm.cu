@@ -15,7 +15,7 @@
 // Bound by the bytes where there are many rows, by launch and latency where there are
 // few.  Measured (device time, share of the copy rate): norm of 1 x 4096 bf16 with
 // residual 2.4 us; of 8192 x 4096 bf16 with weight and bias 26.6, .74; gradient of 64 x
-// 2048 fp32 6.5; of 16384 x 4096 bf16 with d_sum 100, .79.
+// 2048 fp32 6.5; of 16384 x 4096 bf16 with d_sum 101, .78.
 #include "async.cuh"
 #include "dense.cuh"
 #include "lora.cuh"
@@ -309,6 +309,12 @@ __global__ void __launch_bounds__(512) layer_norm_backward_kernel(NormGradParams
 __device__ __forceinline__ float2 add2(float2 a, float2 b) { return ffma2(a, make_float2(1.0f, 1.0f), b); }
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return ffma2(a, b, make_float2(0.0f, 0.0f)); }
 __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+// (x - mu) rstd.  The mean goes first: x rstd - mu rstd in one operation less keeps the
+// rounding of mu rstd, the same one for a whole row (xh of rows whose mean is 1e3 of their
+// deviations 2e-5 of itself off, against 3e-8).
+__device__ __forceinline__ float2 centred(float2 x, float mu, float rstd) {
+  return mul2(add2(x, both(-mu)), both(rstd));
+}
 
 template <bool BF16>
 __device__ __forceinline__ void get2(float2 (&f)[4], const Vec8<BF16>& v) {
@@ -564,7 +570,7 @@ __global__ void __launch_bounds__(kRingThreads, NV == 1 ? 2 : 1)
   int s = 0, buf = 0, bad = 0;
   uint32_t phase = 0;
   for (int64_t t = blockIdx.x; t < p.T; t += step, buf ^= 1) {
-    const float r = rstd, shift = -mu * rstd;
+    const float r = rstd, m = mu;
     if (t + step < p.T) {
       if (p.mean) mu = p.mean[t + step];
       rstd = p.rstd[t + step];
@@ -586,7 +592,7 @@ __global__ void __launch_bounds__(kRingThreads, NV == 1 ? 2 : 1)
       get2(xh[j], xv);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        xh[j][i] = ffma2(xh[j][i], both(r), both(shift));
+        xh[j][i] = centred(xh[j][i], m, r);
         db[j][i] = add2(db[j][i], c[j][i]);
         dw[j][i] = ffma2(c[j][i], xh[j][i], dw[j][i]);
       }
@@ -703,7 +709,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   if (p.weight && on) load2(w, p.weight, p.w_bf16, col);
   const float inv_h = 1.0f / (float)p.H;
   for (int buf = 0; t < p.T; t += step, buf ^= 1) {  // alike for a group
-    const float r = rstd, shift = -mu * rstd;
+    const float r = rstd, m = mu;
     float2 c[4], xh[4], g[4], s0 = zero, s1 = zero;
     get2(c, d);
     get2(xh, x);
@@ -711,7 +717,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     if (t + step < p.T) fetch(t + step);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      xh[i] = on ? ffma2(xh[i], both(r), both(shift)) : zero;
+      xh[i] = on ? centred(xh[i], m, r) : zero;
       db[i] = add2(db[i], c[i]);
       dw[i] = ffma2(c[i], xh[i], dw[i]);
       c[i] = mul2(c[i], w[i]);
