@@ -377,8 +377,10 @@ __global__ void __launch_bounds__(kAdamThreads, kAdamCtas)
         const float2 y = mul2_rn(make_float2(sqrt_approx(v[i].x), sqrt_approx(v[i].y)), both(ir));
         code(i, make_float2(sqrt_approx(x.x), sqrt_approx(x.y)), make_float2(sqrt_approx(y.x), sqrt_approx(y.y)));
       }
-      // near a border, or so small that the hardware's roots lose it
-      if (off_m > 0.49996f || off_v > 0.4999f || top < 0x1p-100f) {
+      // Near a border, or so small that the hardware's root loses some: it takes a v below
+      // 2^-126 for zero, whose code becomes 1.  That is the formula's, 255 (v / top)^(1/4) <
+      // 1.5, where top > 2^-126 (255 / 1.5)^4 = 2^-96.4.
+      if (off_m > 0.49996f || off_v > 0.4999f || top < 0x1p-96f) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 x = mul2_rn(make_float2(fabsf(m[i].x), fabsf(m[i].y)), both(im));

@@ -1,0 +1,40 @@
+"""The 8-bit second moments' codes where values come near the smallest that fp32 holds."""
+import numpy as np
+import pytest
+import torch
+
+from _parity import dev
+from test_adamw_gpu import counter, encode, f
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+def test_codes_of_blocks_with_subnormal_second_moments(shift):
+    """From states of zero one step makes v = (1 - beta2) g^2: its largest value of a
+    block runs from 2^-104 to 2^-92, the others down to zero.  The codes are those of the
+    formula with every operation rounded to fp32."""
+    import sparse_moe_expert_gb300 as m
+    b1, b2 = 0.9, 0.5
+    rng = np.random.default_rng(5)
+    tops = np.repeat(np.arange(-104.0, -91.75, 0.25), 8)
+    low = rng.uniform(-150.0, tops[:, None], (len(tops), 256))
+    low[:, 0] = tops
+    low[:, 1:40] = rng.uniform(-127.5, -125.5, (len(tops), 39))  # around the last normal values
+    g = np.exp2((np.concatenate([row[rng.permutation(256)] for row in low]) + 1.0) / 2.0).astype(f)
+    n = g.size
+    v = (g * g) * f(1 - b2)
+    mm = g * f(1 - b1)
+    want = encode(mm, np.sqrt(v), v)
+    assert (want[2][(v > 0) & (v < 2.0 ** -126)] > 1).any()  # such values have codes of their own
+
+    def make(a):
+        return torch.cat([torch.zeros(shift, dtype=a.dtype), a]).to(dev())[shift:]
+    p, grad = make(torch.zeros(n)), make(torch.from_numpy(g))
+    cm, cv = make(torch.zeros(n, dtype=torch.int8)), make(torch.zeros(n, dtype=torch.uint8))
+    sm, sr = torch.zeros(n // 256, device=dev()), torch.zeros(n // 256, device=dev())
+    m.moe_adamw_step([p], [grad], [cm], [cv], counter(0), beta1=b1, beta2=b2, exp_avg_scales=[sm],
+                     exp_avg_sq_scales=[sr])
+    for got, w, what in zip((cm, sm, cv, sr), want, ("m", "m's scale", "v", "v's scale")):
+        got = got.cpu().numpy()
+        assert np.array_equal(got, w), (what, int((got != w).sum()))
