@@ -72,7 +72,7 @@ struct AdamParams {
   const float* grad_scale;
   int32_t* step;  // steps done, CTAs that have read it
   int count_step;
-  int tiny_eps;   // below 1e-15
+  int tiny_eps;   // so small that a root below 2^-63 counts beside it
 };
 
 enum { kParamF32, kParamMaster, kParamBf16 };
@@ -626,9 +626,12 @@ extern "C" moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int co
   // a buffer given twice would be written by two CTAs at once
   for (auto& w : written)
     if (!apart(w)) return MOE_ERR_INVALID_ARG;
+  // The hardware's root takes v below 2^-126 for zero: the divisor loses up to 2^-63 / sqrt(1
+  // - beta2^t), which is 2^-23 of eps or less from here on (2.9e-11 for beta2 = 0.999).
+  const bool tiny_eps = eps < 0x1p-40 / sqrt(1.0 - beta2);
   AdamParams p{beta1, beta2, (float)beta1, (float)beta2, (float)(1.0 - beta1), (float)(1.0 - beta2),
                (float)eps, (float)lr, lr_dev, grad_scale, step, 0,
-               eps < 1e-15};
+               tiny_eps};
   const int param = param_dtype == MOE_DTYPE_F32 ? kParamF32 : masters ? kParamMaster : kParamBf16;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return over_tables(all, [&](const auto& tab, bool last) {

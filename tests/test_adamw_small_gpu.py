@@ -38,3 +38,20 @@ def test_codes_of_blocks_with_subnormal_second_moments(shift):
     for got, w, what in zip((cm, sm, cv, sr), want, ("m", "m's scale", "v", "v's scale")):
         got = got.cpu().numpy()
         assert np.array_equal(got, w), (what, int((got != w).sum()))
+
+
+@pytest.mark.parametrize("eps", [1e-10, 2e-11, 1e-12, 1e-14, 1e-16])
+@pytest.mark.parametrize("b2", [0.5, 0.999, 0.99999])
+def test_steps_of_subnormal_second_moments_beside_a_small_eps(eps, b2):
+    """m is one product (1 u), its correction another; the divisor's terms are 2^-23 of eps
+    and 6 u of the root off: 16 u of the move, with v as fp32 holds it."""
+    import sparse_moe_expert_gb300 as m
+    n, lr, b1 = 2000, 0.5, 0.9
+    g = torch.Generator().manual_seed(3)
+    p, grad = torch.zeros(n, device=dev()), torch.zeros(n, device=dev())
+    avg = (torch.randn(n, generator=g) * eps).to(dev())
+    sq = torch.exp2(-132.0 + 12.0 * torch.rand(n, generator=g)).to(dev())
+    first = avg.double()
+    m.moe_adamw_step([p], [grad], [avg], [sq], counter(0), lr=lr, beta1=b1, beta2=b2, eps=eps)
+    want = -lr * (b1 * first / (1 - b1)) / (torch.sqrt(sq.double() / (1 - b2)) + eps)
+    assert bool(((p.double() - want).abs() <= 16 * 2.0 ** -24 * want.abs()).all())
