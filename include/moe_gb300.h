@@ -782,8 +782,9 @@ moe_status_t moe_adamw_values(const moe_adamw_tensor_t* tensors, int count, floa
  * residual  [T, cols] of out_dtype, or NULL; may be out (in place).
  * out       [T, cols] of out_dtype; cols = N, with SWIGLU N / 2.
  * preact    out: bf16 [T, N], z rounded, for the gradient; or NULL.
- * K % 8 == 0, K >= 8; N >= 1, even with SWIGLU.  Outputs are aligned to their
- * type; cols a multiple of 8 and 16-byte aligned outputs are fastest.
+ * K % 8 == 0, K >= 8; N >= 1, even with SWIGLU; T, K, N <= 2^31 - 4096.  Outputs
+ * are aligned to their type; cols a multiple of 8 and 16-byte aligned outputs are
+ * fastest.
  * ---------------------------------------------------------------------- */
 enum { MOE_ACT_NONE = 0, MOE_ACT_SILU = 1, MOE_ACT_GELU = 2, MOE_ACT_SWIGLU = 3 };
 moe_status_t moe_linear(const uint16_t* x, int64_t ld_x, const uint16_t* w, const float* bias,

@@ -339,6 +339,7 @@ extern "C" moe_status_t moe_linear(const uint16_t* x, int64_t ld_x, const uint16
   using moe_host::aligned16;
   using moe_host::aligned4;
   if (T < 0 || K < 8 || K % 8 != 0 || N < 1) return MOE_ERR_INVALID_ARG;
+  if (T > kLinearMost || K > kLinearMost || N > kLinearMost) return MOE_ERR_INVALID_ARG;
   if (activation < MOE_ACT_NONE || activation > MOE_ACT_SWIGLU) return MOE_ERR_INVALID_ARG;
   if (activation == MOE_ACT_SWIGLU && N % 2 != 0) return MOE_ERR_INVALID_ARG;
   if (out_dtype != MOE_DTYPE_F32 && out_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;

@@ -10,6 +10,9 @@
 
 namespace moe {
 
+// The largest T, K and N: sizes are rounded up to whole tiles and turns in 32 bits.
+constexpr int kLinearMost = INT32_MAX - 4095;
+
 // An operand of D[i, j] = sum_k A[i, k] B[j, k].  `rows` are i or j.
 struct LinearOp {
   const uint16_t* p;

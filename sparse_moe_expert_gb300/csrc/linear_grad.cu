@@ -165,6 +165,7 @@ extern "C" moe_status_t moe_linear_backward(const void* d_out, int d_dtype, int6
   using moe_host::aligned16;
   using moe_host::aligned4;
   if (T < 0 || K < 8 || K % 8 != 0 || N < 1) return MOE_ERR_INVALID_ARG;
+  if (T > kLinearMost || K > kLinearMost || N > kLinearMost) return MOE_ERR_INVALID_ARG;
   if (activation < MOE_ACT_NONE || activation > MOE_ACT_SWIGLU) return MOE_ERR_INVALID_ARG;
   const bool swiglu = activation == MOE_ACT_SWIGLU;
   if (swiglu && N % 2 != 0) return MOE_ERR_INVALID_ARG;
