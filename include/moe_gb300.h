@@ -675,6 +675,7 @@ moe_status_t moe_lora_apply(const uint16_t* x, int x_by_token, const int32_t* ad
  *              residual and untouched without.  Dense rows.  out may be x, and
  *              summed x or residual, where type and rows are the same.
  * mean, rstd   fp32 [T] out, or NULL: what the gradient needs (RMS: mean 0).
+ *              Memory of their own.
  * 1 <= H <= 8192; eps finite and not negative.  Tensors are aligned to their
  * type; rows of whole 16-byte pieces at 16-byte aligned addresses are fastest.
  * ---------------------------------------------------------------------- */
@@ -702,6 +703,7 @@ moe_status_t moe_layer_norm(const void* x, int x_dtype, int64_t ld_x, const void
  * d_x    [T, H] of x_dtype, dense; may be d_out, x or d_sum where type and rows
  *        are the same.
  * d_weight, d_bias  fp32 [H], or NULL.  Written, not added to (zeros for T = 0).
+ *        They and the workspace are memory of their own.
  * workspace   moe_layer_norm_workspace_size(T, H) bytes of device scratch,
  *        16-byte aligned, for d_weight or d_bias.
  * ---------------------------------------------------------------------- */
@@ -807,7 +809,8 @@ moe_status_t moe_linear(const uint16_t* x, int64_t ld_x, const uint16_t* w, cons
  *           NULL if not wanted.  Zeros for T = 0 (d_w with accumulate: as it was).
  * workspace moe_linear_backward_workspace_size(T, N, activation) bytes of
  *           device scratch, 16-byte aligned, for d_bias.
- * No output may overlap an input.  x, w, K, N as in moe_linear.
+ * No output and no workspace may overlap an input or another of them.  x, w, K, N
+ * as in moe_linear.
  * ---------------------------------------------------------------------- */
 size_t moe_linear_backward_workspace_size(int T, int N, int activation);
 

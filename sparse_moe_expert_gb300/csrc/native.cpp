@@ -448,6 +448,16 @@ void apart(const Tensor& out, const char* name, const Tensor& in, const char* ot
   same_or_apart(out, name, in, other);
 }
 
+struct Named {
+  const Tensor& t;
+  const char* name;
+};
+// A caller's buffer that shares memory with none of the others.
+void apart_from(const Tensor& out, const char* name, std::initializer_list<Named> others) {
+  if (!out.defined()) return;
+  for (const Named& o : others) apart(out, name, o.t, o.name);
+}
+
 // x's rows [T, H], of `type` if given; the row stride.
 int64_t rows_like(const Tensor& t, int64_t T, int64_t H, c10::Device dev, const char* name) {
   const int64_t ld = rows2d(t, name);
@@ -522,6 +532,10 @@ PyObject* layer_norm(Args a) {
       apart(out, "out", *v, v == &w ? "weight" : "bias");
       apart(summed, "summed", *v, v == &w ? "weight" : "bias");
     }
+    for (const Tensor* v : {&mean, &rstd})
+      apart_from(*v, v == &mean ? "mean" : "rstd",
+                 {{out, "out"}, {summed, "summed"}, {x, "x"}, {residual, "residual"}, {w, "weight"}, {bias, "bias"}});
+    apart(mean, "mean", rstd, "rstd");
     return moe_layer_norm(x.data_ptr(), dtype_code(x, "x"), ld, ptr<void>(residual), ld_r,
                           ptr<void>(w), ptr<void>(bias), wt, T, H, kind, (float)eps, out_code,
                           out.data_ptr(), ptr<void>(summed), ptr<float>(mean), ptr<float>(rstd),
@@ -569,7 +583,13 @@ PyObject* layer_norm_backward(Args a) {
     same_or_apart(d_x, "d_x", x, "x");
     same_or_apart(d_x, "d_x", d_sum, "d_sum");
     apart(d_x, "d_x", w, "weight");
-    apart(d_w, "d_weight", w, "weight");
+    apart(d_x, "d_x", mean, "mean");
+    apart(d_x, "d_x", rstd, "rstd");
+    for (const Tensor* o : {&d_w, &d_b, &ws})
+      apart_from(*o, o == &d_w ? "d_weight" : o == &d_b ? "d_bias" : "workspace",
+                 {{d_x, "d_x"}, {d, "d_out"}, {x, "x"}, {d_sum, "d_sum"}, {w, "weight"}, {mean, "mean"}, {rstd, "rstd"}});
+    apart(d_w, "d_weight", d_b, "d_bias");
+    apart_from(ws, "workspace", {{d_w, "d_weight"}, {d_b, "d_bias"}});
     if (!ws.defined() && (d_w.defined() || d_b.defined()))
       ws = make({(int64_t)moe_layer_norm_workspace_size(T, H)}, at::kByte, dev);
     return moe_layer_norm_backward(
@@ -832,6 +852,9 @@ PyObject* linear_backward(Args a) {
       apart(*o, name, preact, "preact");
     }
     apart(d_x, "d_x", d_w, "d_w");
+    apart_from(d_b, "d_bias", {{d_x, "d_x"}, {d_w, "d_w"}});
+    apart_from(ws, "workspace",
+               {{d_x, "d_x"}, {d_w, "d_w"}, {d_b, "d_bias"}, {d, "d_out"}, {x, "x"}, {w, "w"}, {preact, "preact"}});
     // d_out is d_preact where it is bf16 with aligned rows and nothing was activated
     const bool direct = act == MOE_ACT_NONE && d.scalar_type() == at::kBFloat16 && ld_d % 8 == 0 &&
                         reinterpret_cast<uintptr_t>(d.data_ptr()) % 16 == 0;
