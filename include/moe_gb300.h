@@ -730,9 +730,9 @@ moe_status_t moe_layer_norm_backward(const void* d_out, int d_dtype, int64_t ld_
  * coded after the step has used m and v; scales are fp32 [ceil(n / 256)].  A
  * value that is not finite makes its block's states NaN.
  *
- * tensors     host array (read before the call returns).  The buffers are
- *             different memory; overlaps within a tensor, and of the tensors'
- *             params, masters, states or scales among each other, are refused.
+ * tensors     host array (read before the call returns).  What is written
+ *             (params, masters, states, scales) is memory of its own: an overlap
+ *             with any other buffer of the table is refused.  Gradients may overlap.
  * param_dtype, grad_dtype  fp32 or bf16, for all tensors; masters for all
  *             tensors or none, and only beside bf16 params.
  * lr_dev      device scalar that takes lr's place, or NULL (a captured graph

@@ -600,8 +600,8 @@ def moe_linear_backward(d_out, x, w, preact=None, activation: int = _lib.ACT_NON
 def moe_adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, beta1: float = 0.9,
                    beta2: float = 0.999, eps: float = 1e-8, weight_decay=0.0, masters=None,
                    exp_avg_scales=None, exp_avg_sq_scales=None, grad_scale=None, stream=None):
-    """One AdamW step over lists of dense tensors, in place (no two of one list
-    may overlap).
+    """One AdamW step over lists of dense tensors, in place (none of what is written
+    may overlap another tensor of the lists; gradients may overlap each other).
 
     params: all fp32, or all bf16 (with fp32 ``masters``, of which they are the
     rounding, or without); grads all fp32 or all bf16.  States are fp32, or

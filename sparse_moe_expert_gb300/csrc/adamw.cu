@@ -544,27 +544,38 @@ bool at_least_aligned(const void* p, int bytes) {
 struct Span {
   uintptr_t lo, hi;
 };
-Span span(const void* p, int64_t bytes) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return {lo, p ? lo + (uintptr_t)bytes : lo};
-}
-// The buffers of one tensor share nothing.
-bool apart(const Span (&s)[7]) {
-  for (int i = 0; i < 7; ++i)
-    for (int j = i + 1; j < 7; ++j)
-      if (s[i].lo < s[j].hi && s[j].lo < s[i].hi) return false;
+// The buffers of one kind, by address.  Tensors made one after the other are mostly in order.
+struct Spans {
+  std::vector<Span> v;
+  uintptr_t top = 0;     // behind the last byte of any
+  bool sorted = true;
+  void add(const void* p, int64_t bytes) {
+    if (!p || bytes == 0) return;
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p), hi = lo + (uintptr_t)bytes;
+    sorted = sorted && (v.empty() || v.back().lo <= lo);
+    top = hi > top ? hi : top;
+    v.push_back({lo, hi});
+  }
+  void order() {
+    if (!sorted) std::sort(v.begin(), v.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  }
+};
+// Ordered buffers of one kind that share nothing.
+bool apart(const Spans& s) {
+  for (size_t i = 1; i < s.v.size(); ++i)
+    if (s.v[i].lo < s.v[i - 1].hi) return false;
   return true;
 }
-// Buffers of one kind share nothing.  Tensors made one after the other are mostly in order.
-bool apart(std::vector<Span>& s) {
-  auto in_order = [&] {
-    for (size_t i = 1; i < s.size(); ++i)
-      if (s[i].lo < s[i - 1].hi) return false;
-    return true;
-  };
-  if (in_order()) return true;
-  std::sort(s.begin(), s.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
-  return in_order();
+// None of b's shares memory with one of a's, which share nothing; both ordered.
+bool apart(const Spans& a, const Spans& b) {
+  if (a.v.empty() || b.v.empty() || a.top <= b.v.front().lo || b.top <= a.v.front().lo) return true;
+  size_t i = 0;
+  for (const Span& s : b.v) {
+    while (i < a.v.size() && a.v[i].hi <= s.lo) ++i;
+    if (i == a.v.size()) return true;
+    if (a.v[i].lo < s.hi) return false;
+  }
+  return true;
 }
 
 }  // namespace
@@ -590,10 +601,10 @@ extern "C" moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int co
   const bool eight = state_bits == 8;
   std::vector<AdamTensor> all;
   all.reserve(count);
-  bool clash = false;
-  // what is written: param, master, states and their scales
-  std::vector<Span> written[6];
-  for (auto& w : written) w.reserve(count);
+  // what is written (param, master, states and their scales), and the gradients
+  constexpr int kWritten = 6;
+  Spans kinds[kWritten + 1];
+  for (auto& k : kinds) k.v.reserve(count);
   int masters = 0;
   for (int i = 0; i < count; ++i) {
     const moe_adamw_tensor_t& t = tensors[i];
@@ -613,19 +624,22 @@ extern "C" moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int co
     all.push_back(AdamTensor{t.param, t.grad, t.master, t.exp_avg, t.exp_avg_sq, t.exp_avg_scale,
                              t.exp_avg_sq_scale, t.n, t.weight_decay, (float)keep});
     const int64_t state = t.n * (eight ? 1 : 4), scales = eight ? (t.n + kAdamBlock - 1) / kAdamBlock * 4 : 0;
-    const Span own[7] = {span(t.param, t.n * psize),       span(t.master, t.n * 4),
-                         span(t.exp_avg, state),           span(t.exp_avg_sq, state),
-                         span(t.exp_avg_scale, scales),    span(t.exp_avg_sq_scale, scales),
-                         span(t.grad, t.n * gsize)};
-    clash |= !apart(own);
-    for (int k = 0; k < 6; ++k)
-      if (own[k].hi > own[k].lo) written[k].push_back(own[k]);
+    kinds[0].add(t.param, t.n * psize);
+    kinds[1].add(t.master, t.n * 4);
+    kinds[2].add(t.exp_avg, state);
+    kinds[3].add(t.exp_avg_sq, state);
+    kinds[4].add(t.exp_avg_scale, scales);
+    kinds[5].add(t.exp_avg_sq_scale, scales);
+    kinds[kWritten].add(t.grad, t.n * gsize);
   }
   if (masters != 0 && masters != (int)all.size()) return MOE_ERR_UNSUPPORTED;
-  if (clash) return MOE_ERR_INVALID_ARG;
-  // a buffer given twice would be written by two CTAs at once
-  for (auto& w : written)
-    if (!apart(w)) return MOE_ERR_INVALID_ARG;
+  // what one CTA writes no other may read or write
+  for (auto& k : kinds) k.order();
+  for (int i = 0; i < kWritten; ++i) {
+    if (!apart(kinds[i])) return MOE_ERR_INVALID_ARG;
+    for (int j = i + 1; j <= kWritten; ++j)
+      if (!apart(kinds[i], kinds[j])) return MOE_ERR_INVALID_ARG;
+  }
   // The hardware's root takes v below 2^-126 for zero: the divisor loses up to 2^-63 / sqrt(1
   // - beta2^t), which is 2^-23 of eps or less from here on (2.9e-11 for beta2 = 0.999).
   const bool tiny_eps = eps < 0x1p-40 / sqrt(1.0 - beta2);

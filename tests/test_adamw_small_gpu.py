@@ -55,3 +55,18 @@ def test_steps_of_subnormal_second_moments_beside_a_small_eps(eps, b2):
     m.moe_adamw_step([p], [grad], [avg], [sq], counter(0), lr=lr, beta1=b1, beta2=b2, eps=eps)
     want = -lr * (b1 * first / (1 - b1)) / (torch.sqrt(sq.double() / (1 - b2)) + eps)
     assert bool(((p.double() - want).abs() <= 16 * 2.0 ** -24 * want.abs()).all())
+
+
+def test_gradients_may_overlap_each_other():
+    import sparse_moe_expert_gb300 as m
+    flat = torch.randn(3000, device=dev())
+    grads = [flat[i:i + 1000] for i in (1000, 0, 500, 1000, 2000)]
+    sets = []
+    for gs in (grads, [g.clone() for g in grads]):
+        p, a, b = ([torch.zeros(1000, device=dev()) for _ in grads] for _ in range(3))
+        m.moe_adamw_step(p, gs, a, b, counter(0))
+        sets.append(p + a + b)
+    assert all(torch.equal(x, y) for x, y in zip(*sets))
+    params = [flat[2000:]] + [torch.zeros(1000, device=dev()) for _ in range(4)]
+    with pytest.raises(m.MoEError):  # the last tensor's gradient
+        m.moe_adamw_step(params, grads, a, b, counter(0))
