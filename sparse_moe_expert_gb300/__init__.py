@@ -5,8 +5,8 @@ include/moe_gb300.h).  This package is its binding: ``binding`` has one
 function per C entry point and ``MoELayer`` composes them.  Importing it
 does not build anything; calling into it without the built library raises.
 """
-from ._lib import (ACT_GELU, ACT_NONE, ACT_SILU, ACT_SWIGLU, ADAMW_BLOCK, NORM_LAYER, NORM_RMS,
-                   DEVERR_BAD_ADAPTER, DEVERR_BAD_EXPERT, DEVERR_BAD_INDEX, DEVERR_BAD_SCORE,
+from ._lib import (ACT_GELU, ACT_NONE, ACT_SILU, ACT_SWIGLU, ADAMW_BLOCK, NORM_LAYER, NORM_MAX_WIDTH,
+                   NORM_RMS, DEVERR_BAD_ADAPTER, DEVERR_BAD_EXPERT, DEVERR_BAD_INDEX, DEVERR_BAD_SCORE,
                    DEVERR_TIMEOUT, DROPPED, DTYPE_BF16, DTYPE_F32, SCORE_SIGMOID, SCORE_SOFTMAX,
                    EPILOGUE_RAW, EPILOGUE_SWIGLU, EXPORTS, PATH_AUTO, PATH_FLAG_K_GATED,
                    PATH_FLAG_WEIGHTS_EARLY, PATH_GEMV, PATH_TC, path_k_range,
@@ -41,7 +41,8 @@ __all__ = [
     "moe_router_logits", "moe_route_scored", "moe_route_scored_backward",
     "moe_route_backward_workspace_size", "moe_permute_masked", "moe_combine_backward",
     "moe_lora_apply", "moe_lora_workspace_size",
-    "NORM_LAYER", "NORM_RMS", "ADAMW_BLOCK", "moe_layer_norm", "moe_layer_norm_backward",
+    "NORM_LAYER", "NORM_MAX_WIDTH", "NORM_RMS", "ADAMW_BLOCK", "moe_layer_norm",
+    "moe_layer_norm_backward",
     "moe_layer_norm_workspace_size", "moe_adamw_step", "moe_adamw_values",
     "AdamW", "Norm", "SharedExpert", "ACT_NONE", "ACT_SILU", "ACT_GELU", "ACT_SWIGLU", "moe_linear",
     "moe_linear_backward", "moe_linear_backward_workspace_size",

@@ -26,6 +26,7 @@ DEVERR_BAD_EXPERT, DEVERR_TIMEOUT, DEVERR_BAD_INDEX = 1, 2, 4
 DEVERR_BAD_SCORE, DEVERR_BAD_ADAPTER = 8, 16
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 NORM_LAYER, NORM_RMS = 0, 1
+NORM_MAX_WIDTH = 8192  # of a row
 ACT_NONE, ACT_SILU, ACT_GELU, ACT_SWIGLU = 0, 1, 2, 3
 ADAMW_BLOCK = 256  # consecutive elements that share a scale of the 8-bit states
 DROPPED = -2  # inv_pos of an assignment dropped by its expert's capacity

@@ -15,9 +15,9 @@ import numpy as np
 import torch
 
 from . import binding as B
-from ._lib import (ACT_SWIGLU, EPILOGUE_RAW, EPILOGUE_SWIGLU, NORM_LAYER, NORM_RMS, PATH_AUTO,
-                   PATH_FLAG_WEIGHTS_EARLY, PATH_GEMV,
-                   PATH_TC, SCORE_SIGMOID, SCORE_SOFTMAX, MoEError, path_k_range)
+from ._lib import (ACT_SWIGLU, EPILOGUE_RAW, EPILOGUE_SWIGLU, NORM_LAYER, NORM_MAX_WIDTH, NORM_RMS,
+                   PATH_AUTO, PATH_FLAG_WEIGHTS_EARLY, PATH_GEMV, PATH_TC, SCORE_SIGMOID,
+                   SCORE_SOFTMAX, MoEError, path_k_range)
 
 FUSE_ENV = "MOE_GB300_FUSE_GATE_UP"
 TC_MIN_TOKENS_PER_EXPERT = 24  # mirrors the library's automatic path choice
@@ -98,7 +98,8 @@ class ExpertAdapters:
 @dataclasses.dataclass
 class Norm:
     """A norm of the block around the layer (moe_layer_norm): weight and bias
-    [H], fp32 or bf16, either may be None; kind NORM_RMS or NORM_LAYER."""
+    [H], fp32 or bf16, either may be None; kind NORM_RMS or NORM_LAYER.  H is at
+    most NORM_MAX_WIDTH."""
     weight: Optional[torch.Tensor] = None
     bias: Optional[torch.Tensor] = None
     kind: int = NORM_RMS
@@ -200,6 +201,15 @@ class MoELayer:
             two_i, h = shared.gate_up.shape
             if h != self.H or two_i % 16 or tuple(shared.down.shape) != (self.H, two_i // 2):
                 raise ValueError("shared needs gate_up [2*I', H] and down [H, I'] with I' a multiple of 8")
+        for name, n in (("norm", norm), ("out_norm", out_norm)):
+            if n is None:
+                continue
+            if self.H > NORM_MAX_WIDTH:
+                raise ValueError(f"{name}: rows of {self.H} are wider than {NORM_MAX_WIDTH}")
+            ts = [t for t in (n.weight, n.bias) if t is not None]
+            if any(tuple(t.shape) != (self.H,) or t.dtype not in (torch.float32, torch.bfloat16)
+                   or t.dtype != ts[0].dtype for t in ts):
+                raise ValueError(f"{name} needs weight and bias {(self.H,)}, both float32 or both bfloat16")
         self.shared, self.norm, self.out_norm = shared, norm, out_norm
         self._kept = None
         self._bufs = {}
