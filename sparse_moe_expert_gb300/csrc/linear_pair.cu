@@ -260,8 +260,8 @@ struct StripAdd {
 // stored, so that their chains run side by side.  Against lanes that finish and store their
 // own rows, 16 bytes at a time (us, 3001 x 4096 sums over 256, then d_w and both gradients
 // of 512 x 4096 x 4096 in fp32): bias 19.1, 17.6; GELU, bias and residual 46.6, 29.6; fp32
-// 22.2, 17.6; fp32 with residual 35.3, 30.3; SiLU 17.7, 21.8; d_w 35.1, 25.7; both 50.5,
-// 37.3 (with all eight rows at once, or their residuals, registers spill: 65, 91).
+// 22.2, 17.6; fp32 with residual 35.3, 30.3; d_w 35.1, 25.7; both 50.5, 37.3; bf16 SiLU
+// alone loses, 17.7, 21.8 (with all eight rows at once, or their residuals, registers spill: 65, 91).
 template <int ACT, bool OUT_BF16>
 __device__ __forceinline__ void strip_rows(const LinearEpi& e, unsigned char* strip, int64_t row0, int rows,
                                            int64_t col, int n, StripAdd& add) {
@@ -344,11 +344,11 @@ __device__ __forceinline__ void strip_wide(const LinearEpi& e, unsigned char* st
 
 // ---- the epilogue of rows off their 16-byte boundary ----------------------------
 //
-// A lane's sums are a row of the tile.  Rows of whole 16-byte pieces it stores
-// itself; else single values would go to as many lines as there are lanes, so a
-// strip of 32 rows x 128 bytes goes through shared memory and neighbouring lanes
-// take neighbouring columns (335 x 408 x 3468, us: 20.0 without, 12.3; where pieces
-// of bf16 are whole the detour costs: 4096 x 2048 x 1536 SwiGLU 19.7 without, 20.3).
+// A lane's sums are a row of the tile.  Stored from there, single values would go to as
+// many lines as there are lanes, so a strip of 32 rows x 128 bytes goes through shared
+// memory and neighbouring lanes take neighbouring columns (335 x 408 x 3468, us: 20.0
+// without, 12.3).  Rows of whole 16-byte pieces have a strip of their own above; bf16 sums
+// as they are and SwiGLU's leave from the lanes.
 
 // The strip -> `n` columns at `col` of the warp's rows (of which `rows` are there)
 // of a matrix with rows of `ld` elements, plus what `residual` has there.  By the
@@ -716,8 +716,9 @@ int pairs_resident(size_t smem) {
 // 288, 266, 249, 228, 208), so a narrower tile pays where it fills the last wave:
 // us at 256 and at the width taken, 3001 x 11008 x 4096 179, 163 (224), 4096 x 2048
 // x 1536 SwiGLU 28.4, 23.6 (192), 4096^3 91, 83 (224).  A B by columns comes in
-// blocks of 64 rows for each CTA, and SwiGLU's halves are whole chunks of the
-// epilogue.
+// blocks of 64 rows for each CTA.  SwiGLU's halves are multiples of 16, so their last
+// chunk of 32 columns may read 16 of what lies behind them (the other half, or TMEM that
+// no tile has); the epilogue's `width` keeps those from being stored.
 struct PairChoice {
   int bn;
   int64_t waves;

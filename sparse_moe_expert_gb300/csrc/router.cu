@@ -530,8 +530,9 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRouterThreads)
     if (threadIdx.x == 0 && ne > 0) {
       const uint32_t wbytes = (uint32_t)ne * p.H * 4u, xbytes = (uint32_t)nt * p.H * 2u;
       mbar_arrive_expect_tx(&stage_bar, wbytes + xbytes);
-      // one copy per weight row (no kernel of this library writes router
-      // weights, so they are read before the wait on the previous kernel)
+      // One copy per weight row, read before the wait on the previous kernel: what
+      // writes router weights (the AdamW step) lets no kernel start before it ends, and
+      // fences its writes before that.
       for (int e = 0; e < ne; ++e)
         bulk_g2s(ws_s + (size_t)e * p.H, p.w + (int64_t)(e_lo + e) * p.H, (uint32_t)p.H * 4u,
                  &stage_bar);
@@ -843,8 +844,9 @@ __global__ void __launch_bounds__(512, 1) router_small_kernel(RouterParams p, in
   }
   __syncthreads();
   if (threadIdx.x == 0 && ne > 0) {
-    // the weight rows: no kernel of this library writes router weights, so
-    // they are read before the wait on the previous kernel
+    // The weight rows, read before the wait on the previous kernel: what writes them
+    // (the AdamW step) lets no kernel start before it ends, and fences its writes
+    // before that.
     mbar_arrive_expect_tx(&wbar, (uint32_t)ne * H * 4u);
     for (int e = 0; e < ne; ++e)
       bulk_g2s(ws_s + (size_t)e * H, p.w + (int64_t)(e_lo + e) * H, (uint32_t)H * 4u, &wbar);
