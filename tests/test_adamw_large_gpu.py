@@ -76,3 +76,35 @@ def test_8_bit_states_of_many_units(param, masters, grad, shift):
             tol = tol + 2.0 ** -8 * w.abs() + 2.0 ** -133
         assert bool(((got - w).abs() <= tol).all()), i
     assert at == flat_m.numel()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_captured_steps_of_many_tensors(bits):
+    """Tables of a few tensors, of hundreds and of more than one launch holds."""
+    import sparse_moe_expert_gb300 as m
+    for count in (3, 60, 500):
+        ns = sizes(count, 5000)
+        sets = []
+        for _ in range(2):
+            s = make(ns, B16, B16, True, seed=8)
+            states = eight(s) if bits == 8 else (s["m"], [], s["v"], [])
+            sets.append((s, states, counter(0)))
+
+        def go(s, c, step):
+            kw = dict(exp_avg_scales=c[1], exp_avg_sq_scales=c[3]) if bits == 8 else {}
+            m.moe_adamw_step(s["params"], s["grads"], c[0], c[2], step, lr=LR, weight_decay=0.1,
+                             masters=s["masters"], **kw)
+        for _ in range(3):
+            go(*sets[0])
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            go(*sets[1])
+        for _ in range(3):
+            graph.replay()
+        torch.cuda.synchronize()
+        (a, ca, sa), (b, cb, sb) = sets
+        assert sa.tolist() == sb.tolist() == [3, 0]
+        for x, y in zip([*a["params"], *a["masters"], *(t for c in ca for t in c)],
+                        [*b["params"], *b["masters"], *(t for c in cb for t in c)]):
+            assert torch.equal(x, y)

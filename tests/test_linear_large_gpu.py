@@ -54,7 +54,7 @@ def test_many_tiles_are_exact_where_the_sums_are():
     def whole(*shape):
         return torch.randint(-3, 4, shape, generator=g, device=dev())
     for T, K, N in ((6000, 136, 3088), (6000, 136, 3082), (5900, 72, 6160), (2300, 2056, 2064),
-                    (6000, 3088, 136), (777, 4104, 1544)):
+                    (6000, 3088, 136), (777, 4104, 1544), (4000, 2056, 3080), (4000, 2056, 3083)):
         x, w, b = whole(T, K).to(B16), whole(N, K).to(B16), whole(N).to(F32)
         sums = (x.double() @ w.double().t()).float()
         assert torch.equal(m.moe_linear(x, w, out_dtype=F32)[0], sums)
@@ -140,3 +140,44 @@ def test_a_few_rows_with_more_columns_than_the_ctas_take_at_once(T, K, N, act):
             close(pre, z, TOL + BF16, "preact")
     whole = [torch.randint(-3, 4, s).to(B16).to(dev()) for s in ((T, K), (N, K))]
     assert torch.equal(m.moe_linear(*whole, out_dtype=F32)[0], (whole[0].double() @ whole[1].double().t()).float())
+
+
+def test_many_tiles_captured_and_on_streams_beside_smaller_products():
+    """A replayed graph and calls on two streams, with other kernels in between, give the bits
+    of a call alone; accumulation adds once per replay."""
+    m = moe()
+    shapes = [(2300, 136, 3088), (64, 1536, 512), (2300, 136, 1541 * 2), (20, 520, 5000)]
+    data = [(rand((T, K), i), rand((N, K), 9 + i, K ** -0.5), rand((T, N // 2), 20 + i))
+            for i, (T, K, N) in enumerate(shapes)]
+
+    def step(stream=None, sums=None):
+        out = []
+        for i, (x, w, d) in enumerate(data):
+            y, pre = m.moe_linear(x, w, activation=m.ACT_SWIGLU, need_preact=True, stream=stream)
+            out += [y, pre, *m.moe_linear_backward(d, x, w, pre, activation=m.ACT_SWIGLU, stream=stream)]
+            if sums is not None:
+                m.moe_linear_backward(d, x, w, pre, activation=m.ACT_SWIGLU, d_w=sums[i], accumulate=True,
+                                      stream=stream)
+        return out
+    want = [t.clone() for t in step()]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    outs = [step(s) for s in streams * 5]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for o in outs for a, b in zip(o, want))
+    once, sums = ([torch.zeros_like(w, dtype=F32) for _, w, _ in data] for _ in range(2))
+    for _ in range(3):
+        step(sums=once)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(sums=sums)
+    assert not any(bool(s.any()) for s in sums)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(torch.equal(a, b) for a, b in zip(sums, once))
+    assert m.moe_get_device_error() == 0
