@@ -719,6 +719,20 @@ PyObject* adamw_step(Args a) {
   return s ? status(s) : result({});
 }
 
+// params, grads: the checks of the gradients that adamw_step makes
+PyObject* adamw_check(Args a) {
+  const std::vector<Tensor> params = tensors(a.next(), "params"), grads = tensors(a.next(), "grads");
+  unlocked([&] {
+    entries(grads, params.size(), "grads");
+    for (size_t i = 0; i < params.size(); ++i) {
+      dtype_code(grads[i], "grads");
+      item(grads[i], params[i].numel(), grads[0].scalar_type(), params[0].device(), "grads");
+    }
+    return MOE_OK;
+  });
+  return result({});
+}
+
 // exp_avg, exp_avg_sq, exp_avg_scales, exp_avg_sq_scales, stream
 PyObject* adamw_values(Args a) {
   const std::vector<Tensor> m = tensors(a.next(), "exp_avg"), v = tensors(a.next(), "exp_avg_sq"),
@@ -916,6 +930,7 @@ PyMethodDef methods[] = {
     {"linear", method<linear>(), METH_FASTCALL, nullptr},
     {"linear_backward", method<linear_backward>(), METH_FASTCALL, nullptr},
     {"adamw_step", method<adamw_step>(), METH_FASTCALL, nullptr},
+    {"adamw_check", method<adamw_check>(), METH_FASTCALL, nullptr},
     {"adamw_values", method<adamw_values>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -65,13 +65,17 @@ class AdamW:
              stream=None) -> None:
         """One step with the gradients by name (all of a type's tensors fp32 or all
         bf16).  grad_scale (fp32, one element on the device) multiplies them; one
-        that is not finite skips the step."""
+        that is not finite skips the step.  Gradients that are refused leave every
+        tensor as it was."""
         names = {n for g in self._groups for n in g["names"]}
         if set(grads) != names:
             raise ValueError(f"gradients must be those of {sorted(names)}, got {sorted(grads)}")
-        for g in self._groups:
+        lists = [[grads[n] for n in g["names"]] for g in self._groups]
+        for g, gs in zip(self._groups[1:], lists[1:]):  # a later launch is not refused behind an earlier one
+            B.native().adamw_check(g["params"], gs)
+        for g, gs in zip(self._groups, lists):
             B.moe_adamw_step(
-                g["params"], [grads[n] for n in g["names"]], g["exp_avg"], g["exp_avg_sq"],
+                g["params"], gs, g["exp_avg"], g["exp_avg_sq"],
                 g["step"], self.lr, self.betas[0], self.betas[1], self.eps, g["decay"],
                 g["masters"], g["exp_avg_scales"], g["exp_avg_sq_scales"], grad_scale, stream)
 

@@ -70,3 +70,30 @@ def test_gradients_may_overlap_each_other():
     params = [flat[2000:]] + [torch.zeros(1000, device=dev()) for _ in range(4)]
     with pytest.raises(m.MoEError):  # the last tensor's gradient
         m.moe_adamw_step(params, grads, a, b, counter(0))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_refused_gradients_leave_every_tensor_as_it_was(bits):
+    """The fp32 and the bf16 tensors are a launch each; neither runs if one is refused."""
+    import sparse_moe_expert_gb300 as m
+
+    def normal(n, dtype=torch.float32):
+        return torch.randn(n, device=dev()).to(dtype)
+    B16 = torch.bfloat16
+    p = {"a": normal(300), "b": normal(77, B16), "c": normal(1000, B16)}
+    opt = m.AdamW(p, lr=0.1, state_bits=bits)
+    good = {n: normal(t.numel()) for n, t in p.items()}
+    opt.step(good)
+    keep = {n: t.clone() for n, t in p.items()}
+    states = {n: {k: t.clone() for k, t in s.items()} for n, s in opt.state_dict().items()}
+    for wrong in (dict(b=normal(76)), dict(c=normal(1000, B16)), dict(c=normal(2000)[::2]), dict(b=normal(77).cpu()),
+                  dict(b=normal(77).half(), c=normal(1000).half()), dict(b=None), dict(a=normal(299)),
+                  dict(a=normal(300).half())):
+        with pytest.raises(ValueError):
+            opt.step(dict(good, **wrong))
+    assert all(torch.equal(t, keep[n]) for n, t in p.items())
+    for n, s in opt.state_dict().items():
+        assert all(torch.equal(t, states[n][k]) for k, t in s.items())
+    opt.step(good)
+    assert all(int(s["step"][0]) == 2 for s in opt.state_dict().values())
+    assert not any(torch.equal(t, keep[n]) for n, t in p.items())
