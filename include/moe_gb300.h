@@ -805,8 +805,8 @@ moe_status_t moe_linear(const uint16_t* x, int64_t ld_x, const uint16_t* w, cons
  * d_preact  out: bf16 [T, N], rows ld_dp apart (a multiple of 8, >= N), 16-byte
  *           aligned.  Not written, and may be NULL, where d_out is d_z as it
  *           stands: MOE_ACT_NONE, bf16, 16-byte aligned, ld_d a multiple of 8.
- * d_x       bf16 [T, K], d_w [N, K] of d_w_dtype, d_bias fp32 [N]: out, each
- *           NULL if not wanted.  Zeros for T = 0 (d_w with accumulate: as it was).
+ * d_x       bf16 [T, K], d_w [N, K] of d_w_dtype, both 16-byte aligned, d_bias
+ *           fp32 [N]: out, each NULL if not wanted.  Zeros for T = 0 (d_w with accumulate: as it was).
  * workspace moe_linear_backward_workspace_size(T, N, activation) bytes of
  *           device scratch, 16-byte aligned, for d_bias.
  * No output and no workspace may overlap an input or another of them.  x, w, K, N

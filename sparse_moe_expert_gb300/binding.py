@@ -581,7 +581,8 @@ def moe_linear_backward(d_out, x, w, preact=None, activation: int = _lib.ACT_NON
     d_preact bf16 [T, N]); what is not wanted is None.
 
     d_out is the residual's gradient as it stands.  d_w is fp32 unless d_w or
-    d_w_dtype says bf16; with accumulate d_w is added to.  w may be None where d_x is
+    d_w_dtype says bf16; with accumulate d_w is added to.  Buffers for d_x and d_w are
+    16-byte aligned, and no two buffers share memory.  w may be None where d_x is
     not wanted.  d_preact is d_out itself where there is no activation and d_out is
     bf16 with 16-byte aligned rows."""
     if d_w_dtype is not None:

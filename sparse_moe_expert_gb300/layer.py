@@ -568,9 +568,9 @@ class MoELayer:
 
     def trainable(self) -> dict:
         """The tensors that grads() gives gradients of, by name: ``router_w`` (with
-        scoring), the shared expert's and out_norm's.  The quantized experts stay as
-        they are, and with them whatever reaches the loss through their input:
-        ``norm`` is not among them."""
+        scoring; ``logit_bias`` stays as it is), the shared expert's and out_norm's.
+        The quantized experts stay as they are, and with them whatever reaches the
+        loss through their input: ``norm`` is not among them."""
         t = {}
         if self.scoring is not None:
             t["router_w"] = self.router_w
