@@ -398,6 +398,8 @@ class MoELayer:
                 self.inv_temperature if inv_temperature is None else float(inv_temperature)))
         if shared is not None:
             ev = _Timer(events, "shared")
+            # the routed sum comes as the layer's result, in bf16: half a bf16 step of it
+            # more than one rounding of the whole
             B.moe_linear(b["shared_h"], shared.down, residual=res, out=res)
             ev.stop()
         return res

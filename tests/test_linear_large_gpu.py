@@ -181,3 +181,23 @@ def test_many_tiles_captured_and_on_streams_beside_smaller_products():
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert all(torch.equal(a, b) for a, b in zip(sums, once))
     assert m.moe_get_device_error() == 0
+
+
+@pytest.mark.parametrize("T,N", [(12, 32), (100, 64), (6000, 3088), (6000, 3082)])
+def test_silu_and_swiglu_keep_their_digits_in_the_tail(T, N):
+    """z is exact (one product by one).  The hardware's exponential is 2 + 1.173 |z| ulp off, the
+    sum 1/2, the quotient 2 ulp: (5 + 1.2 |z|) 2^-23 of the value; SwiGLU's product 2^-24 more."""
+    m = moe()
+    x, w = torch.zeros(T, 8, dtype=B16), torch.zeros(N, 8, dtype=B16)
+    z = torch.linspace(-80.0, 80.0, T).to(B16)
+    x[:, 0] = z
+    x[:, 1] = 3.0
+    w[:, 0] = 1.0
+    zd = z.double()[:, None]
+    silu = zd / (1.0 + torch.exp(-zd))
+    out = m.moe_linear(x.to(dev()), w.to(dev()), activation=m.ACT_SILU, out_dtype=F32)[0].cpu().double()
+    assert bool(((out - silu).abs() <= (5.0 + 1.2 * zd.abs()) * 2.0 ** -23 * silu.abs()).all())
+    w[N // 2:, 0], w[N // 2:, 1] = 0.0, 1.0  # up: 3 everywhere
+    out = m.moe_linear(x.to(dev()), w.to(dev()), activation=m.ACT_SWIGLU, out_dtype=F32)[0].cpu().double()
+    assert out.shape == (T, N // 2)
+    assert bool(((out - 3.0 * silu).abs() <= (5.5 + 1.2 * zd.abs()) * 2.0 ** -23 * 3.0 * silu.abs()).all())
