@@ -394,7 +394,7 @@ class MoELayer:
             ev.stop()
         self._routed(x, res, inv_temperature, events, adapter_ids)
         if self.keep_for_grad:
-            self._kept = dict(x=x, inv_temperature=(
+            self._kept = dict(x=x, shared=_fields(self.shared), scoring=self._scores(), inv_temperature=(
                 self.inv_temperature if inv_temperature is None else float(inv_temperature)))
         if shared is not None:
             ev = _Timer(events, "shared")
@@ -436,7 +436,7 @@ class MoELayer:
         _, _, mean, rstd = B.moe_layer_norm(y, n.weight, n.bias, eps=n.eps, kind=n.kind,
                                             need_stats=self.keep_for_grad, out=res)
         if self._kept is not None:
-            self._kept.update(y=y, mean=mean, rstd=rstd)
+            self._kept.update(y=y, mean=mean, rstd=rstd, out_norm=_fields(n))
         return res, s
 
     def _routed(self, x, out, inv_temperature, events, adapter_ids):
@@ -568,6 +568,10 @@ class MoELayer:
             b["logits"], b["topk_ids"], d_w, counts, s.score, self.k_fixed, self.renormalize,
             s.scale, balance_coef, z_coef)
 
+    def _scores(self) -> tuple:
+        """What the weights of the chosen experts are made with."""
+        return () if self.scoring is None else (self.scoring.score, self.scoring.scale, self.renormalize)
+
     def trainable(self) -> dict:
         """The tensors that grads() gives gradients of, by name: ``router_w`` (with
         scoring; ``logit_bias`` stays as it is), the shared expert's and out_norm's.
@@ -592,6 +596,10 @@ class MoELayer:
         k = self._kept
         if k is None:
             raise ValueError("grads needs a forward with keep_for_grad")
+        norm = self.out_norm if "rstd" in k else None
+        if not (_same(_fields(self.shared), k["shared"]) and _same(_fields(norm), k.get("out_norm", ()))
+                and _same(self._scores(), k["scoring"])):
+            raise ValueError("grads needs a forward with the layer's shared expert, norm and scoring as they are")
         x, g, losses = k["x"], {}, None
         T = x.shape[0]
         if tuple(d_out.shape) != (T, self.H) or d_out.dtype != torch.bfloat16:
@@ -681,6 +689,17 @@ class MoELayer:
         res = self.forward(b["x_dev"], inv_temperature=inv_temperature, adapter_ids=adapter_ids)
         out_host.copy_(res, non_blocking=True)
         return out_host
+
+
+def _fields(part) -> tuple:
+    """The tensors and settings of a SharedExpert or a Norm; none of None."""
+    return () if part is None else tuple(getattr(part, f.name) for f in dataclasses.fields(part))
+
+
+def _same(a: tuple, b: tuple) -> bool:
+    """The same tensors and equal settings."""
+    return len(a) == len(b) and all(
+        x is y or not (torch.is_tensor(x) or torch.is_tensor(y)) and x == y for x, y in zip(a, b))
 
 
 def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:

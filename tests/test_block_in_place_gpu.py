@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from _parity import dev
-from test_block_gpu import make, rand
+from test_block_gpu import m, make, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -99,3 +99,39 @@ def test_the_result_of_a_block_is_not_written_over_what_its_gradients_read():
     layer.keep_for_grad = False
     layer.block(x, out=y)
     layer.block(result)
+
+
+def test_gradients_belong_to_the_parts_of_their_forward():
+    """A shared expert or a norm that came, went or changed after the forward left no rows for
+    its gradient."""
+    layer, x = make()
+    layer.keep_for_grad = True
+    d = rand(x.shape, 3, 0.1)
+    layer.block(x)
+    want = {n: t.clone() for n, t in layer.grads(d)[0].items()}
+    shared, norm = layer.shared, layer.out_norm
+    moe = m()
+    others = [("shared", None), ("shared", moe.SharedExpert(shared.gate_up.clone(), shared.down)),
+              ("shared", moe.SharedExpert(rand((64, 256), 1), rand((256, 32), 2))), ("out_norm", None),
+              ("out_norm", moe.Norm(norm.weight.clone(), norm.bias, norm.kind)),
+              ("out_norm", moe.Norm(norm.weight, norm.bias, moe.NORM_RMS)),
+              ("scoring", moe.ScoredRouting(score=moe.SCORE_SOFTMAX, n_groups=4, topk_groups=2, scale=2.0)),
+              ("scoring", None)]
+    scoring = layer.scoring
+    for name, other in others:
+        setattr(layer, name, other)
+        with pytest.raises(ValueError):
+            layer.grads(d)
+        layer.shared, layer.out_norm, layer.scoring = shared, norm, scoring
+    layer.out_norm = moe.Norm(norm.weight, norm.bias, norm.kind, float(str(norm.eps)))  # equal
+    layer.scoring = moe.ScoredRouting(scoring.score, torch.zeros(layer.E, device=dev()), 4, 2, 2, 2.0)  # of the next call
+    assert all(torch.equal(t, want[n]) for n, t in layer.grads(d)[0].items())
+    layer.shared = None
+    layer.block(x)
+    layer.grads(d)
+    layer.shared = shared  # no forward has passed it
+    with pytest.raises(ValueError):
+        layer.grads(d)
+    layer(x)  # a forward alone leaves the norm out
+    layer.out_norm = None
+    assert "shared.down" in layer.grads(d)[0]
