@@ -201,6 +201,8 @@ class MoELayer:
             two_i, h = shared.gate_up.shape
             if h != self.H or two_i % 16 or tuple(shared.down.shape) != (self.H, two_i // 2):
                 raise ValueError("shared needs gate_up [2*I', H] and down [H, I'] with I' a multiple of 8")
+            if any(t.dtype != torch.bfloat16 or not t.is_contiguous() for t in (shared.gate_up, shared.down)):
+                raise ValueError("shared needs contiguous bfloat16 matrices")
         for name, n in (("norm", norm), ("out_norm", out_norm)):
             if n is None:
                 continue

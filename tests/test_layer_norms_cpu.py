@@ -1,17 +1,18 @@
-"""A layer refuses norms that its rows do not fit when it is made, not at its first block.
+"""A layer refuses norms and shared experts that do not fit it when it is made, not at its
+first block.
 The layer is made of host tensors, without the fused matrix."""
 import pytest
 import torch
 
 import sparse_moe_expert_gb300 as moe
-from sparse_moe_expert_gb300.layer import MoELayer, Norm, QTensor
+from sparse_moe_expert_gb300.layer import MoELayer, Norm, QTensor, SharedExpert
 
 
 def make(H, **kw):
     def q(rows, cols):
-        z = torch.zeros(2, rows, cols // 64, dtype=torch.float16)
-        return QTensor(torch.zeros(2, rows, cols // 8, dtype=torch.int32), z, z, 4)
-    return MoELayer(torch.zeros(2, H), None, q(64, H), q(64, H), q(H, 64), k_fixed=1, fuse_gate_up=False, **kw)
+        z = torch.empty(2, rows, cols // 64, dtype=torch.float16)
+        return QTensor(torch.empty(2, rows, cols // 8, dtype=torch.int32), z, z, 4)
+    return MoELayer(torch.empty(2, H), None, q(64, H), q(64, H), q(H, 64), k_fixed=1, fuse_gate_up=False, **kw)
 
 
 @pytest.mark.parametrize("name", ["norm", "out_norm"])
@@ -35,3 +36,14 @@ def test_norms_are_checked_when_the_layer_is_made(name):
     _build.build()
     assert moe.moe_layer_norm_workspace_size(4, moe.NORM_MAX_WIDTH) > 16
     assert moe.moe_layer_norm_workspace_size(4, moe.NORM_MAX_WIDTH + 1) == 16
+
+
+def test_shared_experts_are_checked_when_the_layer_is_made():
+    H, B16 = 128, torch.bfloat16
+    gate_up, down = torch.zeros(128, H, dtype=B16), torch.zeros(H, 64, dtype=B16)
+    assert make(H, shared=SharedExpert(gate_up, down)).shared.down is down
+    for a, b in ((gate_up.float(), down), (gate_up, down.float()), (gate_up, down.half()),
+                 (torch.zeros(H, 128, dtype=B16).t(), down), (gate_up, torch.zeros(64, H, dtype=B16).t()),
+                 (gate_up[:96], down), (gate_up[:, :64], down), (torch.zeros(24, H, dtype=B16), down[:, :12])):
+        with pytest.raises(ValueError):
+            make(H, shared=SharedExpert(a, b))
