@@ -379,8 +379,8 @@ class MoELayer:
         unless ``out`` is given); x may be the result's memory.  ``events``, if
         given, receives per kernel ("router", "permute", "permute_rows", "gate_up",
         "down", "combine") a list of (start, end) CUDA events around its launches
-        ("shared" with a shared expert, once for each product).  ``adapter_ids`` (int32 [T], negative: none) names each
-        token's adapter."""
+        ("shared" with a shared expert, once for each product).  ``adapter_ids``
+        (int32 [T], negative: none) names each token's adapter."""
         self._kept = None
         if self.shared is None and not self.keep_for_grad:
             return self._routed(x, out, inv_temperature, events, adapter_ids)
@@ -411,8 +411,8 @@ class MoELayer:
         """The layer with its norms, as a block of a model: with s = x + residual
         (x without one), out_norm(layer(norm(s))) -> (out, s), both bf16 [T, H] and
         buffers that the next call of T tokens writes again unless ``out`` is
-        given (s is x itself without a residual, or a copy where x is the result's
-        memory).  The next block takes them as x and residual, so the sum is part of
+        given (s is x itself without a residual, or a copy where x is memory that the
+        block writes).  The next block takes them as x and residual, so the sum is part of
         its norm's kernel; out + s ends the last."""
         if residual is not None and self.norm is None:
             raise ValueError("a residual needs a layer with a norm, whose kernel adds it")
@@ -420,11 +420,15 @@ class MoELayer:
         res = out if out is not None else b["out" if self.out_norm is None else "block_out"]
         if residual is not None and _overlap(b["summed"], res):
             raise ValueError("out is the memory of the sum that is returned beside it")
-        kept = [x] if self.norm is None and (self.shared or self.scoring) else []
-        if self.keep_for_grad and self.out_norm is not None and any(
-                _overlap(t, res) for t in kept + [b["out"]]):
-            raise ValueError("out is the memory of what grads() reads again")
-        s, h = x.clone() if residual is None and _overlap(x, res) else x, x
+        if self.keep_for_grad and self.out_norm is not None:
+            kept = [b["out"]]
+            if self.shared is not None or self.scoring is not None:
+                kept.append(x if self.norm is None else b["normed"])
+            if _overlap(res, *kept):
+                raise ValueError("out is the memory of what grads() reads again")
+        # what is written on the way to the result, and the result
+        written = (res, b["out"]) if self.norm is None else (res, b["out"], b["normed"])
+        s, h = x.clone() if residual is None and _overlap(x, *written) else x, x
         if self.norm is not None:
             n = self.norm
             h, summed, _, _ = B.moe_layer_norm(
@@ -704,16 +708,21 @@ def _same(a: tuple, b: tuple) -> bool:
         x is y or not (torch.is_tensor(x) or torch.is_tensor(y)) and x == y for x, y in zip(a, b))
 
 
-def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
-    """Whether the memory between the first and last elements of a and b meets."""
-    if a.numel() == 0 or b.numel() == 0:
-        return False
-
+def _overlap(t: torch.Tensor, *others: torch.Tensor) -> bool:
+    """Whether the memory between t's first and last elements meets that of one of the others."""
     def span(t):
-        last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
-        return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
-    (a0, a1), (b0, b1) = span(a), span(b)
-    return a0 < b1 and b0 < a1
+        p = t.data_ptr()
+        if t.is_contiguous():
+            return p, p + t.nbytes
+        return p, p + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
+    if t.numel() == 0:
+        return False
+    lo, hi = span(t)
+    for o in others:
+        p, q = span(o)
+        if lo < q and p < hi:
+            return True
+    return False
 
 
 class _Timer:

@@ -135,3 +135,26 @@ def test_gradients_belong_to_the_parts_of_their_forward():
     layer(x)  # a forward alone leaves the norm out
     layer.out_norm = None
     assert "shared.down" in layer.grads(d)[0]
+
+
+def test_the_sum_of_a_block_is_kept_from_every_buffer_that_the_block_writes():
+    """A block's input may be what the layer alone returned before, in the buffer that stands
+    between the layer and the norm behind it."""
+    for norm in (True, False):
+        layer, x = make()
+        if not norm:
+            layer.norm = None
+        y = layer(x)
+        first = y.clone()
+        want = layer.block(first, out=torch.empty_like(x))[0]
+        y = layer(x)
+        got, s = layer.block(y)
+        assert torch.equal(got, want) and torch.equal(s, first)
+        normed = layer.buffers(x.shape[0]).get("normed")
+        if normed is not None:
+            normed.copy_(first)
+            got, s = layer.block(normed)
+            assert torch.equal(got, want) and torch.equal(s, first)
+            layer.keep_for_grad = True
+            with pytest.raises(ValueError):  # grads() reads the normed rows
+                layer.block(first, out=normed)
