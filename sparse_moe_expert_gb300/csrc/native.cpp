@@ -519,6 +519,10 @@ PyObject* layer_norm(Args a) {
     else out = make({T, H}, ot, dev);
     const int out_code = dtype_code(out, "out");
     const bool layer = kind == MOE_NORM_LAYER;
+    for (const Tensor* v : {&mean, &rstd})  // the caller's
+      apart_from(*v, v == &mean ? "mean" : "rstd",
+                 {{out, "out"}, {summed, "summed"}, {x, "x"}, {residual, "residual"}, {w, "weight"}, {bias, "bias"}});
+    apart(mean, "mean", rstd, "rstd");
     if (mean.defined()) like(mean, {T}, at::kFloat, dev, "mean");
     else if (need_stats && layer) mean = make({T}, at::kFloat, dev);
     if (rstd.defined()) like(rstd, {T}, at::kFloat, dev, "rstd");
@@ -532,10 +536,6 @@ PyObject* layer_norm(Args a) {
       apart(out, "out", *v, v == &w ? "weight" : "bias");
       apart(summed, "summed", *v, v == &w ? "weight" : "bias");
     }
-    for (const Tensor* v : {&mean, &rstd})
-      apart_from(*v, v == &mean ? "mean" : "rstd",
-                 {{out, "out"}, {summed, "summed"}, {x, "x"}, {residual, "residual"}, {w, "weight"}, {bias, "bias"}});
-    apart(mean, "mean", rstd, "rstd");
     return moe_layer_norm(x.data_ptr(), dtype_code(x, "x"), ld, ptr<void>(residual), ld_r,
                           ptr<void>(w), ptr<void>(bias), wt, T, H, kind, (float)eps, out_code,
                           out.data_ptr(), ptr<void>(summed), ptr<float>(mean), ptr<float>(rstd),
@@ -575,6 +575,11 @@ PyObject* layer_norm_backward(Args a) {
     }
     if (d_x.defined()) like(d_x, {T, H}, xt, dev, "d_x");
     else d_x = make({T, H}, xt, dev);
+    for (const Tensor* o : {&d_w, &d_b, &ws})  // the caller's
+      apart_from(*o, o == &d_w ? "d_weight" : o == &d_b ? "d_bias" : "workspace",
+                 {{d_x, "d_x"}, {d, "d_out"}, {x, "x"}, {d_sum, "d_sum"}, {w, "weight"}, {mean, "mean"}, {rstd, "rstd"}});
+    apart(d_w, "d_weight", d_b, "d_bias");
+    apart_from(ws, "workspace", {{d_w, "d_weight"}, {d_b, "d_bias"}});
     if (d_w.defined()) like(d_w, {H}, at::kFloat, dev, "d_weight");
     else if (need_w) d_w = make({H}, at::kFloat, dev);
     if (d_b.defined()) like(d_b, {H}, at::kFloat, dev, "d_bias");
@@ -585,11 +590,6 @@ PyObject* layer_norm_backward(Args a) {
     apart(d_x, "d_x", w, "weight");
     apart(d_x, "d_x", mean, "mean");
     apart(d_x, "d_x", rstd, "rstd");
-    for (const Tensor* o : {&d_w, &d_b, &ws})
-      apart_from(*o, o == &d_w ? "d_weight" : o == &d_b ? "d_bias" : "workspace",
-                 {{d_x, "d_x"}, {d, "d_out"}, {x, "x"}, {d_sum, "d_sum"}, {w, "weight"}, {mean, "mean"}, {rstd, "rstd"}});
-    apart(d_w, "d_weight", d_b, "d_bias");
-    apart_from(ws, "workspace", {{d_w, "d_weight"}, {d_b, "d_bias"}});
     if (!ws.defined() && (d_w.defined() || d_b.defined()))
       ws = make({(int64_t)moe_layer_norm_workspace_size(T, H)}, at::kByte, dev);
     return moe_layer_norm_backward(
